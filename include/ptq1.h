@@ -370,6 +370,158 @@ size_t ptq1_gemm_w2a8_workspace_bytes(int64_t m, int64_t n, int64_t k);
 ptq1_status ptq1_gemm_w2a8(const uint8_t *tiled, int64_t n, int64_t k, const float *x, int64_t m, float *y, void *ws,
                            size_t ws_bytes, hipStream_t stream);
 
+/* ---- Attention: the other half of a layer ("Why I Am Building Another
+ * Inference Engine", Level 4: a layer's projections, rotary positions,
+ * attention and output projection; "Speed, and where it goes": the key-value
+ * cache is what long contexts cost).  The calls below take the fp32 rows that
+ * the projections above produce (or 16-bit rows), keep keys and values in a
+ * paged cache, and return rows for the output projection.
+ *
+ * The cache is a set of pages that the caller owns; a page holds page_size
+ * consecutive tokens of one sequence for every key-value head:
+ *   k_pages  [n_pages][n_kv_heads][page_size][head_dim]
+ *   v_pages  [n_pages][n_kv_heads][head_dim][page_size]   (dimension-major)
+ * in binary16, bfloat16 or int8.  An int8 cache has one fp32 step for every
+ * token and head, k_steps and v_steps [n_pages][n_kv_heads][page_size]: the
+ * value is step * code (step = max|x| / 127 over the head's row, code =
+ * rint(x * float(127 / max|x|)), ties to even, as in ptq1_matvec_w2a8; a row
+ * below 2^-119 in magnitude is stored as zeros; a row that holds a NaN or an
+ * infinity reads back as NaN).  V is dimension-major because the attention
+ * over one token multiplies whole runs of tokens of one dimension: both
+ * operands of both products are then 16 contiguous bytes per lane.  A token's
+ * slot is page * page_size + its place in the page.  Cache memory needs no
+ * initial contents: what no token was written to is never used. */
+typedef enum ptq1_dtype {
+    PTQ1_F32 = 0,  /* IEEE binary32 */
+    PTQ1_F16 = 1,  /* IEEE binary16 */
+    PTQ1_BF16 = 2, /* bfloat16 */
+    PTQ1_I8 = 3    /* int8 codes with fp32 steps (cache only) */
+} ptq1_dtype;
+
+typedef struct ptq1_kv_cache {
+    void *k_pages;       /* device pointers, 16-byte aligned */
+    void *v_pages;
+    float *k_steps;      /* PTQ1_I8 only, else NULL */
+    float *v_steps;
+    int64_t n_pages;     /* 1 .. 2^31 - 1 */
+    int32_t page_size;   /* 16, 32, 64, 128 or 256 tokens */
+    int32_t n_kv_heads;  /* 1 .. 1024 */
+    int32_t head_dim;    /* 64, 128 or 256 */
+    int32_t dtype;       /* PTQ1_F16, PTQ1_BF16 or PTQ1_I8 */
+} ptq1_kv_cache;
+
+/* Writes n_tokens fresh tokens into the cache, with rotary positions on
+ * their keys and queries, in one launch.
+ *   q, k, v    rows [n_tokens] of n_q_heads, n_kv_heads and n_kv_heads heads
+ *              of head_dim elements of src_dtype (F32, F16 or BF16; heads
+ *              contiguous, rows q_stride, k_stride, v_stride elements apart,
+ *              so they may be parts of one stacked projection's rows).  16-byte
+ *              aligned, strides multiples of 16 bytes, at least a row (or
+ *              anything when n_tokens <= 1).  n_q_heads = 0: no queries
+ *              (q and q_out unused).
+ *   cos_sin    fp32 [n_positions][rot_dim]: rot_dim / 2 cosines, then
+ *              rot_dim / 2 sines; rot_dim a multiple of 8, <= head_dim; 0 (and
+ *              cos_sin NULL): no rotation.  Elements i and i + rot_dim / 2 of
+ *              a head turn together: (a cos - b sin, b cos + a sin), each
+ *              product and sum rounded to fp32; elements from rot_dim on
+ *              stay.
+ *   positions  int32 [n_tokens], the row of cos_sin for each token (unused
+ *              without rotation).  A position outside [0, n_positions) makes
+ *              the token's q_out NaN and its key read back as NaN.
+ *   slots      int64 [n_tokens].  A slot outside [0, n_pages * page_size)
+ *              writes nothing to the cache (padding: -1); q_out is written
+ *              all the same.  The slots in the cache must differ: of two
+ *              tokens with one slot, either may end up there, or parts of
+ *              both.
+ *   q_out      [n_tokens][n_q_heads][head_dim] of q_dtype (F32, F16, BF16),
+ *              16-byte aligned, overlapping neither inputs nor the cache.
+ * Values are rounded once, to nearest even, to the cache's and q_out's types.
+ * Errors: NULL, SHAPE, ALIGN, ALIAS, OVERFLOW, UNSUPPORTED (types, head_dim,
+ * page_size, more than 2^24 tokens or 2^31 rows). */
+ptq1_status ptq1_kv_write(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                          int64_t v_stride, int32_t src_dtype, int64_t n_tokens, int32_t n_q_heads,
+                          const int32_t *positions, const float *cos_sin, int64_t n_positions, int32_t rot_dim,
+                          const int64_t *slots, void *q_out, int32_t q_dtype, const ptq1_kv_cache *cache,
+                          hipStream_t stream);
+
+/* Reads whole sequences back, packed: rows cu_seqlens[b] .. cu_seqlens[b + 1]
+ * of k_out and v_out [n_rows][n_kv_heads][head_dim] (out_dtype F32, F16 or
+ * BF16) get the first cu_seqlens[b + 1] - cu_seqlens[b] tokens of sequence b,
+ * whose pages are block_table[b][0..max_pages) (int32, device).  cu_seqlens
+ * int32 [batch + 1], device, not decreasing.  Rows that belong to no sequence
+ * are left as they were, and no row from n_rows on is written.  A token whose
+ * page is outside [0, n_pages), or past max_pages, reads as NaN.  An int8
+ * value is step * code, rounded once to out_dtype.
+ * Errors: NULL, SHAPE, ALIGN, ALIAS, OVERFLOW, UNSUPPORTED (types, head_dim,
+ * page_size, batch * n_kv_heads > 65535, n_rows > 2^31 - 1). */
+ptq1_status ptq1_kv_read(const ptq1_kv_cache *cache, const int32_t *block_table, int64_t max_pages,
+                         const int32_t *cu_seqlens, int64_t batch, int64_t n_rows, void *k_out, void *v_out,
+                         int32_t out_dtype, hipStream_t stream);
+
+/* Attention of one new token of each of `batch` sequences over the paged
+ * cache:
+ *   out[b][h] = sum_j p_j V[j],  p = softmax over j < seq_lens[b] of
+ *               scale * (q[b][h] . K[j]),
+ * query head h reading key-value head h / (n_q_heads / n_kv_heads).
+ *   q, out     [batch][n_q_heads][head_dim], q_dtype F32, the cache's own
+ *              16-bit type, or any of F32, F16, BF16 over an int8 cache; out
+ *              has q's type and must not overlap q.
+ *   block_table int32 [batch][max_pages], seq_lens int32 [batch] (device):
+ *              sequence b's tokens are 0 .. seq_lens[b], the new token's own
+ *              key among them if it is to be seen.  Length 0 gives zeros.  A
+ *              length outside [0, max_len], or a page outside [0, n_pages)
+ *              among those the length covers, makes the sequence's rows NaN.
+ *   max_len    a bound on the lengths that the caller knows (at most
+ *              max_pages * page_size); the work is laid out for it.
+ *   scale      positive and finite.
+ * The products run on the matrix cores with 16-bit operands: K and V enter
+ * exactly; fp32 queries enter as three 16-bit terms, weights as two or three,
+ * so that nothing is rounded to 16 bits but the stored cache; sums, maxima and
+ * accumulators are fp32.  A NaN or an infinity in a query or in a key or value
+ * that is read makes the entries of out that it enters NaN or infinite.  Long sequences are cut into chunks that run side by
+ * side and are joined by a second launch, in a fixed order.
+ * Errors: NULL, SHAPE (n_q_heads not a multiple of n_kv_heads, max_len, scale),
+ * ALIGN, ALIAS, OVERFLOW, WORKSPACE, UNSUPPORTED (types, head_dim, page_size,
+ * batch > 65535, more than 65535 groups of 16 query heads per sequence,
+ * max_len > 2^22). */
+size_t ptq1_attn_decode_workspace_bytes(int64_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                        int64_t max_len);
+ptq1_status ptq1_attn_decode(const void *q, int32_t q_dtype, int64_t batch, int32_t n_q_heads,
+                             const ptq1_kv_cache *cache, const int32_t *block_table, int64_t max_pages,
+                             const int32_t *seq_lens, int64_t max_len, float scale, void *out, void *ws,
+                             size_t ws_bytes, hipStream_t stream);
+
+/* Attention over whole prompts, packed without padding: sequence b's queries
+ * are rows cu_q[b] .. cu_q[b + 1] of q [n_q_rows][n_q_heads][head_dim], its
+ * keys and values rows cu_k[b] .. cu_k[b + 1] of k and v
+ * [n_k_rows][n_kv_heads][head_dim] (heads contiguous, rows q_stride,
+ * k_stride, v_stride elements apart; 16-byte aligned, strides multiples of 16
+ * bytes), all of dtype F16 or BF16; cu_q, cu_k int32 [batch + 1], device, not
+ * decreasing.
+ *   out  [n_q_rows][n_q_heads][head_dim] contiguous, of dtype; must overlap
+ *        no input.  Rows that belong to no sequence are left as they were.
+ *   causal != 0: query i of n_q sees the keys j <= i + n_k - n_q (the last
+ *        query sees the last key, as when the first n_k - n_q keys come from
+ *        a cache: ptq1_kv_read); else every key.  A query that sees no key
+ *        gets zeros.  Keys and values that a query does not see do not enter
+ *        its row, whatever they hold.
+ *   max_q, max_k  bounds on the sequences' query and key counts that the
+ *        caller knows; the work is laid out for them.  A sequence that
+ *        exceeds one gets NaN rows, as does one whose rows lie outside
+ *        [0, n_q_rows) or [0, n_k_rows) (those inside q's range).
+ *   scale  positive and finite.
+ * bf16 or fp16 matrix cores, fp32 scores, maxima, sums and accumulators; the
+ * weights enter the second product rounded to dtype, the sum is over fp32.
+ * Errors: NULL, SHAPE, ALIGN, ALIAS, OVERFLOW, WORKSPACE, UNSUPPORTED (types,
+ * head_dim, sizes past 2^31 - 1 rows of one kv head). */
+size_t ptq1_attn_prompt_workspace_bytes(int64_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                        int64_t max_q, int64_t max_k);
+ptq1_status ptq1_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                             int64_t v_stride, int32_t dtype, const int32_t *cu_q, const int32_t *cu_k,
+                             int64_t batch, int64_t n_q_rows, int64_t n_k_rows, int64_t max_q, int64_t max_k,
+                             int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t causal, float scale,
+                             void *out, void *ws, size_t ws_bytes, hipStream_t stream);
+
 /* Profiling: attaches start[i] / stop[i] to the dispatch of the i-th of the
  * next `count` launches of one kernel family (hipExtLaunchKernel: they take
  * the kernel's own start and end times on its stream), so a caller can time

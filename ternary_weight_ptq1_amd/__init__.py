@@ -82,6 +82,14 @@ _SIGS = {
     "ptq1_ffn_workspace_offsets": ([i64, i64, i64, p], C.c_int),
     "ptq1_ffn_block_noalloc": ([p, p, i64, i64, i64, p, p, p, p, C.c_float, p, p], C.c_int),
     "pq2_ffn_workspace_offsets": ([i64, i64, i64, p], C.c_int),
+    "ptq1_kv_write": ([p, i64, p, i64, p, i64, C.c_int32, i64, C.c_int32, p, p, i64, C.c_int32, p, p, C.c_int32, p, p],
+                      C.c_int),
+    "ptq1_kv_read": ([p, p, i64, p, i64, i64, p, p, C.c_int32, p], C.c_int),
+    "ptq1_attn_decode_workspace_bytes": ([i64, C.c_int32, C.c_int32, C.c_int32, i64], sz),
+    "ptq1_attn_decode": ([p, C.c_int32, i64, C.c_int32, p, p, i64, p, i64, C.c_float, p, p, sz, p], C.c_int),
+    "ptq1_attn_prompt_workspace_bytes": ([i64, C.c_int32, C.c_int32, C.c_int32, i64, i64], sz),
+    "ptq1_attn_prompt": ([p, i64, p, i64, p, i64, C.c_int32, p, p, i64, i64, i64, i64, i64, C.c_int32, C.c_int32,
+                          C.c_int32, C.c_int32, C.c_float, p, p, sz, p], C.c_int),
     "ptq1_profile_arm": ([C.c_char_p, p, p, C.c_int32], C.c_int),
     "ptq1_profile_count": ([C.c_char_p], C.c_int32),
 }
@@ -518,6 +526,292 @@ def ptq1_gemm_w2a8(tiled: torch.Tensor, n: int, k: int, x: torch.Tensor, out: to
     return out
 
 
+# -------------------------------------------------------------- attention ----
+
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}
+_FLOATS = (torch.float32, torch.float16, torch.bfloat16)
+_CACHE_TYPES = (torch.float16, torch.bfloat16, torch.int8)
+
+
+class _CacheStruct(C.Structure):
+    _fields_ = [("k_pages", p), ("v_pages", p), ("k_steps", p), ("v_steps", p), ("n_pages", i64),
+                ("page_size", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("dtype", C.c_int32)]
+
+
+class KvCache:
+    """A paged key-value cache over tensors that it keeps: k_pages [n_pages, n_kv_heads, page_size, head_dim],
+    v_pages [n_pages, n_kv_heads, head_dim, page_size] (fp16, bf16 or int8) and, for int8, k_steps and v_steps
+    [n_pages, n_kv_heads, page_size] fp32."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, k_steps: torch.Tensor | None = None,
+                 v_steps: torch.Tensor | None = None):
+        _dev(k_pages, "k_pages", _CACHE_TYPES)
+        if k_pages.dim() != 4:
+            raise ValueError("k_pages must be [n_pages, n_kv_heads, page_size, head_dim]")
+        n, h, page, d = k_pages.shape
+        _dev(v_pages, "v_pages", k_pages.dtype, device=k_pages.device)
+        if tuple(v_pages.shape) != (n, h, d, page):
+            raise ValueError(f"v_pages must be [n_pages, n_kv_heads, head_dim, page_size] = {[n, h, d, page]}")
+        if k_pages.dtype == torch.int8:
+            for name, s in (("k_steps", k_steps), ("v_steps", v_steps)):
+                _dev(s, name, torch.float32, device=k_pages.device)
+                if tuple(s.shape) != (n, h, page):
+                    raise ValueError(f"{name} must be [n_pages, n_kv_heads, page_size] = {[n, h, page]}")
+        elif k_steps is not None or v_steps is not None:
+            raise ValueError("k_steps and v_steps belong to an int8 cache")
+        self.k_pages, self.v_pages, self.k_steps, self.v_steps = k_pages, v_pages, k_steps, v_steps
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = n, h, page, d
+        self.dtype, self.device = k_pages.dtype, k_pages.device
+        self._struct = _CacheStruct(*(None if t is None else t.data_ptr()
+                                      for t in (k_pages, v_pages, k_steps, v_steps)),
+                                    n, page, h, d, _DTYPES[k_pages.dtype])
+        self._ref = C.byref(self._struct)
+
+
+def ptq1_kv_cache(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, dtype=torch.bfloat16,
+                  device="cuda") -> KvCache:
+    """A cache of its own memory (uninitialised: only what was written is ever used)."""
+    if dtype not in _CACHE_TYPES:
+        raise ValueError(f"dtype must be one of {_CACHE_TYPES}, got {dtype}")
+    k = torch.empty((n_pages, n_kv_heads, page_size, head_dim), dtype=dtype, device=device)
+    v = torch.empty((n_pages, n_kv_heads, head_dim, page_size), dtype=dtype, device=device)
+    steps = [torch.empty((n_pages, n_kv_heads, page_size), dtype=torch.float32, device=device) for _ in range(2)] \
+        if dtype == torch.int8 else (None, None)
+    return KvCache(k, v, *steps)
+
+
+class _On:
+    """The launch's device and stream: makes the operands' device current where it is not, and ties tensors
+    allocated for the call to a stream that is not the allocator's current one."""
+
+    def __init__(self, device, stream):
+        self.device = device
+        self.other = device.index is not None and device.index != torch.cuda.current_device()
+        self.guard = torch.cuda.device(device) if self.other else None
+        if self.guard is not None:
+            self.guard.__enter__()
+        current = torch.cuda.current_stream(device)
+        self.stream = current if stream is None else stream
+        self.foreign = self.stream != current
+        self.handle = C.c_void_p(self.stream.cuda_stream)
+
+    def keep(self, *tensors):
+        if self.foreign:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+    def done(self):
+        if self.guard is not None:
+            self.guard.__exit__(None, None, None)
+
+
+def _rows3(t: torch.Tensor, name: str, dtype, device) -> tuple[int, int, int, int]:
+    """(rows, heads, head_dim, row stride) of a [rows, heads, head_dim] tensor whose rows may lie apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not _on_device(t):
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows, heads, head_dim]")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
+    rows, heads, d = t.shape
+    sr, sh, sd = t.stride()
+    if t.numel() > 0 and ((d > 1 and sd != 1) or (heads > 1 and sh != d)):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    if rows > 1 and heads > 0 and sr < heads * d:
+        raise ValueError(f"{name}: rows overlap one another (stride {sr})")
+    return rows, heads, d, sr if rows > 1 else heads * d
+
+
+def _kv(cache) -> KvCache:
+    if not isinstance(cache, KvCache):
+        raise TypeError("cache must be a KvCache")
+    return cache
+
+
+def _table(block_table, batch, device):
+    _dev(block_table, "block_table", torch.int32, device=device)
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError(f"block_table must be [{batch}, max_pages]")
+    return block_table.shape[1]
+
+
+def ptq1_kv_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: KvCache,
+                  positions: torch.Tensor | None = None, cos_sin: torch.Tensor | None = None, q_dtype=None,
+                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Writes fresh tokens k, v [n, n_kv_heads, head_dim] into the cache at slots (int64 [n]; page * page_size +
+    place, -1: not written), turning k and q [n, n_q_heads, head_dim] by the rows positions (int32 [n]) of
+    cos_sin [n_positions, rot_dim] (rot_dim / 2 cosines, then sines) if it is given.  q, k and v may be parts of
+    the rows of one stacked projection.  Returns the turned queries in q_dtype (q's own by default), or None
+    without q."""
+    kv = _kv(cache)
+    dv = kv.device
+    n, h, d, ks = _rows3(k, "k", _FLOATS, dv)
+    if (h, d) != (kv.n_kv_heads, kv.head_dim):
+        raise ValueError(f"k has {h} heads of {d}, the cache {kv.n_kv_heads} of {kv.head_dim}")
+    nv, hv, d2, vs = _rows3(v, "v", k.dtype, dv)
+    if (nv, hv, d2) != (n, h, d):
+        raise ValueError(f"v must be {[n, h, d]}")
+    hq = qs = 0
+    if q is not None:
+        nq, hq, d3, qs = _rows3(q, "q", k.dtype, dv)
+        if (nq, d3) != (n, d):
+            raise ValueError(f"q must be [{n}, n_q_heads, {d}]")
+        q_dtype = q.dtype if q_dtype is None else q_dtype
+        if q_dtype not in _FLOATS:
+            raise ValueError(f"q_dtype must be one of {_FLOATS}, got {q_dtype}")
+    elif out is not None:
+        raise ValueError("out needs q")
+    _dev(slots, "slots", torch.int64, numel=n, device=dv)
+    rot = n_pos = 0
+    if cos_sin is not None:
+        _dev(cos_sin, "cos_sin", torch.float32, device=dv)
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [n_positions, rot_dim]")
+        n_pos, rot = cos_sin.shape
+        if positions is None:
+            raise ValueError("cos_sin needs positions")
+    if positions is not None:
+        _dev(positions, "positions", torch.int32, numel=n, device=dv)
+    on = _On(dv, stream)
+    try:
+        fresh = None
+        if q is not None:
+            if out is None:
+                out = fresh = torch.empty((n, hq, d), dtype=q_dtype, device=dv)
+            else:
+                _dev(out, "out", q_dtype, numel=n * hq * d, device=dv)
+        on.keep(fresh)
+        _check("ptq1_kv_write",
+               lib().ptq1_kv_write(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _DTYPES[k.dtype], n, hq,
+                                   _ptr(positions) if rot else None, _ptr(cos_sin) if rot else None, n_pos, rot,
+                                   _ptr(slots), _ptr(out), _DTYPES[q_dtype] if q is not None else 0, kv._ref,
+                                   on.handle))
+    finally:
+        on.done()
+    return out
+
+
+def ptq1_kv_read(cache: KvCache, block_table: torch.Tensor, cu_seqlens: torch.Tensor, n_rows: int,
+                 dtype=torch.bfloat16, out: tuple[torch.Tensor, torch.Tensor] | None = None, stream=None):
+    """The first cu_seqlens[b + 1] - cu_seqlens[b] tokens of every sequence b (pages block_table[b], int32),
+    packed: k and v [n_rows, n_kv_heads, head_dim] of dtype.  cu_seqlens int32 [batch + 1]."""
+    kv = _kv(cache)
+    dv = kv.device
+    _dev(cu_seqlens, "cu_seqlens", torch.int32, device=dv)
+    batch = cu_seqlens.numel() - 1
+    if batch < 0:
+        raise ValueError("cu_seqlens must hold batch + 1 offsets")
+    max_pages = _table(block_table, batch, dv)
+    if dtype not in _FLOATS:
+        raise ValueError(f"dtype must be one of {_FLOATS}, got {dtype}")
+    if n_rows < 0:
+        raise ValueError(f"n_rows = {n_rows} is negative")
+    shape = (n_rows, kv.n_kv_heads, kv.head_dim)
+    count = n_rows * kv.n_kv_heads * kv.head_dim
+    on = _On(dv, stream)
+    try:
+        if out is None:
+            k = torch.empty(shape, dtype=dtype, device=dv)
+            v = torch.empty(shape, dtype=dtype, device=dv)
+            on.keep(k, v)
+        else:
+            k, v = out
+            _dev(k, "k_out", dtype, numel=count, device=dv)
+            _dev(v, "v_out", dtype, numel=count, device=dv)
+        _check("ptq1_kv_read",
+               lib().ptq1_kv_read(kv._ref, _ptr(block_table), max_pages, _ptr(cu_seqlens), batch, n_rows, _ptr(k),
+                                  _ptr(v), _DTYPES[dtype], on.handle))
+    finally:
+        on.done()
+    return k, v
+
+
+def ptq1_attn_decode(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                     scale: float | None = None, max_len: int | None = None, out: torch.Tensor | None = None,
+                     ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence, q [batch, n_q_heads, head_dim], over the first seq_lens[b] (int32)
+    tokens of its pages block_table[b] (int32 [batch, max_pages]).  scale: 1 / sqrt(head_dim) by default; max_len: a
+    bound on seq_lens (the table's by default).  ws: optional scratch of at least workspace_bytes("attn_decode",
+    batch, n_q_heads, n_kv_heads, head_dim, max_len) bytes."""
+    kv = _kv(cache)
+    dv = kv.device
+    _dev(q, "q", _FLOATS, device=dv)
+    if q.dim() != 3 or q.shape[2] != kv.head_dim:
+        raise ValueError(f"q must be [batch, n_q_heads, {kv.head_dim}]")
+    batch, hq, d = q.shape
+    max_pages = _table(block_table, batch, dv)
+    _dev(seq_lens, "seq_lens", torch.int32, numel=batch, device=dv)
+    if max_len is None:
+        max_len = max_pages * kv.page_size
+    on = _On(dv, stream)
+    try:
+        need = lib().ptq1_attn_decode_workspace_bytes(batch, hq, kv.n_kv_heads, d, max_len)
+        mine = ws is None and need > 0
+        ws, wsb = _ws(need, dv, ws)
+        fresh = None
+        if out is None:
+            out = fresh = torch.empty((batch, hq, d), dtype=q.dtype, device=dv)
+        else:
+            _dev(out, "out", q.dtype, numel=q.numel(), device=dv)
+        on.keep(fresh, ws if mine else None)
+        _check("ptq1_attn_decode",
+               lib().ptq1_attn_decode(_ptr(q), _DTYPES[q.dtype], batch, hq, kv._ref, _ptr(block_table), max_pages,
+                                      _ptr(seq_lens), max_len, d ** -0.5 if scale is None else scale, _ptr(out),
+                                      _ptr(ws), wsb, on.handle))
+    finally:
+        on.done()
+    return out
+
+
+def ptq1_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
+                     max_q: int | None = None, max_k: int | None = None, causal: bool = True,
+                     scale: float | None = None, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Attention over packed prompts: q [n_q_rows, n_q_heads, head_dim], k and v [n_k_rows, n_kv_heads, head_dim]
+    (fp16 or bf16; rows may lie apart), sequence b's rows cu_q[b] .. cu_q[b + 1] and cu_k[b] .. cu_k[b + 1] (int32
+    [batch + 1]).  causal: the last query of a sequence sees its last key.  max_q, max_k: bounds on the sequences'
+    query and key counts (all rows by default).  scale: 1 / sqrt(head_dim) by default.  ws: optional scratch of at
+    least workspace_bytes("attn_prompt", batch, n_q_heads, n_kv_heads, head_dim, max_q, max_k) bytes."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    dv = q.device
+    nq, hq, d, qs = _rows3(q, "q", (torch.float16, torch.bfloat16), dv)
+    nk, hkv, dk, ks = _rows3(k, "k", q.dtype, dv)
+    nv, hv, d2, vs = _rows3(v, "v", q.dtype, dv)
+    if dk != d or (nv, hv, d2) != (nk, hkv, dk):
+        raise ValueError(f"k and v must both be [n_k_rows, n_kv_heads, {d}]")
+    _dev(cu_q, "cu_q", torch.int32, device=dv)
+    batch = cu_q.numel() - 1
+    if batch < 0:
+        raise ValueError("cu_q must hold batch + 1 offsets")
+    _dev(cu_k, "cu_k", torch.int32, numel=batch + 1, device=dv)
+    max_q = nq if max_q is None else min(max_q, nq)
+    max_k = nk if max_k is None else min(max_k, nk)
+    on = _On(dv, stream)
+    try:
+        need = lib().ptq1_attn_prompt_workspace_bytes(batch, hq, hkv, d, max_q, max_k)
+        mine = ws is None and need > 0
+        ws, wsb = _ws(need, dv, ws)
+        fresh = None
+        if out is None:
+            out = fresh = torch.empty((nq, hq, d), dtype=q.dtype, device=dv)
+        else:
+            _dev(out, "out", q.dtype, numel=nq * hq * d, device=dv)
+        on.keep(fresh, ws if mine else None)
+        _check("ptq1_attn_prompt",
+               lib().ptq1_attn_prompt(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _DTYPES[q.dtype], _ptr(cu_q), _ptr(cu_k),
+                                      batch, nq, nk, max_q, max_k, hq, hkv, d, 1 if causal else 0,
+                                      d ** -0.5 if scale is None else scale, _ptr(out), _ptr(ws), wsb, on.handle))
+    finally:
+        on.done()
+    return out
+
+
 def ffn_workspace_offsets(m: int, d: int, f: int, fmt: str = "ptq1") -> tuple[int, int, int]:
     """Byte offsets of (g, u, h) in an FFN block's workspace (-1: not stored on that path)."""
     out = (C.c_int64 * 3)()
@@ -529,7 +823,9 @@ def ffn_workspace_offsets(m: int, d: int, f: int, fmt: str = "ptq1") -> tuple[in
 def workspace_bytes(kind: str, *shape) -> int:
     fn = {"matvec": "ptq1_matvec_workspace_bytes", "gate_up": "ptq1_gate_up_workspace_bytes",
           "gemm": "ptq1_gemm_workspace_bytes", "ffn": "ptq1_ffn_workspace_bytes",
-          "pq2_matvec": "pq2_matvec_workspace_bytes", "pq2_gemm": "pq2_gemm_workspace_bytes"}[kind]
+          "pq2_matvec": "pq2_matvec_workspace_bytes", "pq2_gemm": "pq2_gemm_workspace_bytes",
+          "attn_decode": "ptq1_attn_decode_workspace_bytes",
+          "attn_prompt": "ptq1_attn_prompt_workspace_bytes"}[kind]
     return int(getattr(lib(), fn)(*shape))
 
 

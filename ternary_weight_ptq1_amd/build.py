@@ -22,11 +22,15 @@ ARCH = "gfx950"
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    # MFMA results in VGPRs: the GEMM scales every block's partial with VALU
-    # FMAs, which cannot read accumulation registers directly.
-    "-mllvm", "-amdgpu-mfma-vgpr-form",
     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
 ]
+
+# MFMA results in VGPRs: the GEMM scales every block's partial with VALU
+# FMAs, which cannot read accumulation registers directly.  The decode
+# attention is compiled without it (the pass that backs the option crashes on
+# its 256-wide kernels) and gets the same registers by the allocator's choice.
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+NO_VGPR_FORM = ("attn_decode.hip",)
 
 
 def hipcc() -> str:
@@ -42,7 +46,8 @@ def sources() -> list[str]:
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
-    cmd = [hipcc(), *HIPCC_FLAGS, "-c", src, "-o", obj]
+    form = [] if os.path.basename(src) in NO_VGPR_FORM else VGPR_FORM
+    cmd = [hipcc(), *HIPCC_FLAGS, *form, "-c", src, "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{res.stdout}\n{res.stderr}")

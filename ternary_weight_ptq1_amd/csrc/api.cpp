@@ -74,6 +74,8 @@ constexpr int64_t kMaxGridY = 65535;
 // Decode calls: rows per matrix (keeps the matvec grid's second dimension,
 // chunks of 32-row groups, far below its limit).
 constexpr int64_t kMaxLutRows = int64_t{1} << 20;
+// Decode attention: tokens of one sequence (1024 chunks of 4096).
+constexpr int64_t kMaxDecodeLen = int64_t{1} << 22;
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -1048,6 +1050,334 @@ ptq1_status pq2_ffn_block(const float *x, float *x_out, int64_t m, int64_t d, in
             });
     }
     return hip_status(e, "pq2_ffn_block");
+}
+
+// ---- attention ---------------------------------------------------------------
+
+}  // extern "C"
+
+namespace {
+
+bool is_pow2_in(int32_t v, int32_t lo, int32_t hi) { return v >= lo && v <= hi && (v & (v - 1)) == 0; }
+
+bool float_type(int32_t t) { return t == PTQ1_F32 || t == PTQ1_F16 || t == PTQ1_BF16; }
+
+int64_t type_bytes(int32_t t) { return t == PTQ1_F32 ? 4 : t == PTQ1_I8 ? 1 : 2; }
+
+const char *type_name(int32_t t)
+{
+    return t == PTQ1_F32 ? "F32" : t == PTQ1_F16 ? "F16" : t == PTQ1_BF16 ? "BF16" : t == PTQ1_I8 ? "I8" : "unknown";
+}
+
+ptq1_status check_head_dim(int32_t d)
+{
+    if (d != 64 && d != 128 && d != 256)
+        return fail(PTQ1_ERR_UNSUPPORTED, "head_dim = %d (64, 128 or 256)", d);
+    return PTQ1_OK;
+}
+
+ptq1_status check_device_array(const void *p, const char *name, int64_t bytes, uintptr_t align)
+{
+    if (bytes > 0 && p == nullptr) return fail(PTQ1_ERR_NULL, "%s is NULL", name);
+    if (bytes > 0 && !aligned(p, align))
+        return fail(PTQ1_ERR_ALIGN, "%s is not %d-byte aligned", name, static_cast<int>(align));
+    return PTQ1_OK;
+}
+
+constexpr int64_t kMaxRows32 = 2147483647;
+constexpr int32_t kMaxHeads = 65536;
+
+// The byte sizes of a cache's arrays, after every check of it.
+struct KvBytes {
+    int64_t pages = 0, steps = 0;  // of k_pages (v_pages alike), of k_steps
+};
+
+ptq1_status check_cache(const ptq1_kv_cache *c, KvBytes *out)
+{
+    if (c == nullptr) return fail(PTQ1_ERR_NULL, "cache is NULL");
+    if (c->dtype != PTQ1_F16 && c->dtype != PTQ1_BF16 && c->dtype != PTQ1_I8)
+        return fail(PTQ1_ERR_UNSUPPORTED, "cache dtype %d (F16, BF16 or I8)", c->dtype);
+    PTQ1_TRY(check_head_dim(c->head_dim));
+    if (!is_pow2_in(c->page_size, 16, 256))
+        return fail(PTQ1_ERR_UNSUPPORTED, "page_size = %d (16, 32, 64, 128 or 256)", c->page_size);
+    if (c->n_kv_heads < 1 || c->n_kv_heads > 1024)
+        return fail(PTQ1_ERR_SHAPE, "n_kv_heads = %d (1 to 1024)", c->n_kv_heads);
+    if (c->n_pages < 1 || c->n_pages > kMaxRows32)
+        return fail(PTQ1_ERR_SHAPE, "n_pages = %lld (1 to 2^31 - 1)", (long long)c->n_pages);
+    const int64_t cells = c->n_pages * c->n_kv_heads * c->page_size;  // below 2^49
+    out->pages = cells * c->head_dim * type_bytes(c->dtype);
+    PTQ1_TRY(check_device_array(c->k_pages, "k_pages", out->pages, kAlign));
+    PTQ1_TRY(check_device_array(c->v_pages, "v_pages", out->pages, kAlign));
+    if (c->dtype == PTQ1_I8) {
+        out->steps = cells * 4;
+        PTQ1_TRY(check_device_array(c->k_steps, "k_steps", out->steps, kAlign));
+        PTQ1_TRY(check_device_array(c->v_steps, "v_steps", out->steps, kAlign));
+    }
+    return PTQ1_OK;
+}
+
+// [p, p + bytes) overlaps one of the cache's arrays
+bool overlaps_cache(const void *p, int64_t bytes, const ptq1_kv_cache *c, const KvBytes &kb)
+{
+    return overlaps(p, bytes, c->k_pages, kb.pages) || overlaps(p, bytes, c->v_pages, kb.pages) ||
+           (c->dtype == PTQ1_I8 && (overlaps(p, bytes, c->k_steps, kb.steps) || overlaps(p, bytes, c->v_steps, kb.steps)));
+}
+
+// The cache's own arrays do not overlap one another (checked where they are written).
+bool cache_disjoint(const ptq1_kv_cache *c, const KvBytes &kb)
+{
+    if (overlaps(c->k_pages, kb.pages, c->v_pages, kb.pages)) return false;
+    if (c->dtype != PTQ1_I8) return true;
+    return !overlaps(c->k_steps, kb.steps, c->v_steps, kb.steps) && !overlaps(c->k_steps, kb.steps, c->k_pages, kb.pages) &&
+           !overlaps(c->k_steps, kb.steps, c->v_pages, kb.pages) && !overlaps(c->v_steps, kb.steps, c->k_pages, kb.pages) &&
+           !overlaps(c->v_steps, kb.steps, c->v_pages, kb.pages);
+}
+
+// Rows of `width` elements, `stride` apart; *bytes: from the first element to the last.
+ptq1_status check_strided(const void *p, const char *name, int64_t rows, int64_t width, int64_t stride, int64_t esize,
+                          int64_t *bytes)
+{
+    *bytes = 0;
+    if (rows == 0 || width == 0) return PTQ1_OK;
+    if (rows > 1 && stride < width)
+        return fail(PTQ1_ERR_SHAPE, "%s: row stride %lld is below a row's %lld elements", name, (long long)stride,
+                    (long long)width);
+    int64_t span = 0;
+    if (rows > 1 && !mul_ok(rows - 1, stride, &span)) return fail(PTQ1_ERR_OVERFLOW, "%s: size overflows", name);
+    if (__builtin_add_overflow(span, width, &span) || !mul_ok(span, esize, &span))
+        return fail(PTQ1_ERR_OVERFLOW, "%s: size overflows", name);
+    if (p == nullptr) return fail(PTQ1_ERR_NULL, "%s is NULL", name);
+    if (!aligned(p, kAlign)) return fail(PTQ1_ERR_ALIGN, "%s is not 16-byte aligned", name);
+    if (rows > 1 && (stride * esize) % static_cast<int64_t>(kAlign) != 0)
+        return fail(PTQ1_ERR_ALIGN, "%s: row stride %lld is not a multiple of 16 bytes", name, (long long)stride);
+    *bytes = span;
+    return PTQ1_OK;
+}
+
+ptq1_status check_heads(int32_t hq, int32_t hkv)
+{
+    if (hkv < 1 || hkv > 1024) return fail(PTQ1_ERR_SHAPE, "n_kv_heads = %d (1 to 1024)", hkv);
+    if (hq < 1 || hq > kMaxHeads) return fail(PTQ1_ERR_SHAPE, "n_q_heads = %d (1 to %d)", hq, kMaxHeads);
+    if (hq % hkv != 0)
+        return fail(PTQ1_ERR_SHAPE, "n_q_heads = %d is not a multiple of n_kv_heads = %d", hq, hkv);
+    return PTQ1_OK;
+}
+
+ptq1_status check_scale(float scale)
+{
+    if (!(scale > 0.0f) || scale > 3.0e38f) return fail(PTQ1_ERR_SHAPE, "scale must be positive and finite");
+    return PTQ1_OK;
+}
+
+bool decode_sizes_ok(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_t max_len)
+{
+    return batch >= 0 && batch <= kMaxGridY && hkv >= 1 && hkv <= 1024 && hq >= 1 && hq <= kMaxHeads && hq % hkv == 0 &&
+           (d == 64 || d == 128 || d == 256) && max_len >= 0 && max_len <= kMaxDecodeLen &&
+           static_cast<int64_t>(hkv) * ((hq / hkv + 15) / 16) <= kMaxGridY;
+}
+
+}  // namespace
+
+extern "C" {
+
+ptq1_status ptq1_kv_write(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                          int64_t v_stride, int32_t src_dtype, int64_t n_tokens, int32_t n_q_heads,
+                          const int32_t *positions, const float *cos_sin, int64_t n_positions, int32_t rot_dim,
+                          const int64_t *slots, void *q_out, int32_t q_dtype, const ptq1_kv_cache *cache,
+                          hipStream_t stream)
+{
+    KvBytes kb;
+    PTQ1_TRY(check_cache(cache, &kb));
+    if (!cache_disjoint(cache, kb)) return fail(PTQ1_ERR_ALIAS, "the cache's arrays overlap one another");
+    if (n_tokens < 0) return fail(PTQ1_ERR_SHAPE, "n_tokens = %lld is negative", (long long)n_tokens);
+    if (n_tokens > int64_t{1} << 24)
+        return fail(PTQ1_ERR_UNSUPPORTED, "n_tokens = %lld > 2^24", (long long)n_tokens);
+    if (n_q_heads < 0 || n_q_heads > kMaxHeads)
+        return fail(PTQ1_ERR_SHAPE, "n_q_heads = %d (0 to %d)", n_q_heads, kMaxHeads);
+    if (n_tokens * (n_q_heads + 2 * static_cast<int64_t>(cache->n_kv_heads)) > kMaxRows32)
+        return fail(PTQ1_ERR_UNSUPPORTED, "n_tokens * heads above 2^31 - 1");
+    if (!float_type(src_dtype)) return fail(PTQ1_ERR_UNSUPPORTED, "src_dtype %d (F32, F16 or BF16)", src_dtype);
+    if (!float_type(q_dtype)) return fail(PTQ1_ERR_UNSUPPORTED, "q_dtype %d (F32, F16 or BF16)", q_dtype);
+    if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 8 != 0)
+        return fail(PTQ1_ERR_SHAPE, "rot_dim = %d (a multiple of 8 up to head_dim)", rot_dim);
+    if (n_tokens == 0) return ok();
+    const int64_t d = cache->head_dim, es = type_bytes(src_dtype);
+    int64_t qb, kbytes, vbytes, tb = 0;
+    PTQ1_TRY(check_strided(q, "q", n_tokens, n_q_heads * d, q_stride, es, &qb));
+    PTQ1_TRY(check_strided(k, "k", n_tokens, cache->n_kv_heads * d, k_stride, es, &kbytes));
+    PTQ1_TRY(check_strided(v, "v", n_tokens, cache->n_kv_heads * d, v_stride, es, &vbytes));
+    if (rot_dim > 0) {
+        if (n_positions < 0) return fail(PTQ1_ERR_SHAPE, "n_positions = %lld is negative", (long long)n_positions);
+        if (!mul_ok(n_positions, 4 * rot_dim, &tb)) return fail(PTQ1_ERR_OVERFLOW, "cos_sin: size overflows");
+        PTQ1_TRY(check_device_array(cos_sin, "cos_sin", tb, kAlign));
+        PTQ1_TRY(check_device_array(positions, "positions", n_tokens * 4, 4));
+    }
+    PTQ1_TRY(check_device_array(slots, "slots", n_tokens * 8, 8));
+    const int64_t ob = n_tokens * n_q_heads * d * type_bytes(q_dtype);
+    PTQ1_TRY(check_device_array(q_out, "q_out", ob, kAlign));
+    if (overlaps(q_out, ob, q, qb) || overlaps(q_out, ob, k, kbytes) || overlaps(q_out, ob, v, vbytes))
+        return fail(PTQ1_ERR_ALIAS, "q_out overlaps q, k or v");
+    if (overlaps_cache(q_out, ob, cache, kb)) return fail(PTQ1_ERR_ALIAS, "q_out overlaps the cache");
+    if (overlaps(q_out, ob, slots, n_tokens * 8)) return fail(PTQ1_ERR_ALIAS, "q_out overlaps slots");
+    if (overlaps_cache(q, qb, cache, kb) || overlaps_cache(k, kbytes, cache, kb) || overlaps_cache(v, vbytes, cache, kb))
+        return fail(PTQ1_ERR_ALIAS, "the cache overlaps q, k or v");
+    if (overlaps_cache(slots, n_tokens * 8, cache, kb)) return fail(PTQ1_ERR_ALIAS, "the cache overlaps slots");
+    if (rot_dim > 0) {
+        if (overlaps(q_out, ob, cos_sin, tb) || overlaps_cache(cos_sin, tb, cache, kb))
+            return fail(PTQ1_ERR_ALIAS, "q_out or the cache overlaps cos_sin");
+        if (overlaps(q_out, ob, positions, n_tokens * 4) || overlaps_cache(positions, n_tokens * 4, cache, kb))
+            return fail(PTQ1_ERR_ALIAS, "q_out or the cache overlaps positions");
+    }
+    return hip_status(ptq1::launch_kv_write(q, q_stride, k, k_stride, v, v_stride, src_dtype, n_tokens, n_q_heads,
+                                            positions, cos_sin, n_positions, rot_dim, slots, q_out, q_dtype, *cache,
+                                            stream),
+                      "ptq1_kv_write");
+}
+
+ptq1_status ptq1_kv_read(const ptq1_kv_cache *cache, const int32_t *block_table, int64_t max_pages,
+                         const int32_t *cu_seqlens, int64_t batch, int64_t n_rows, void *k_out, void *v_out,
+                         int32_t out_dtype, hipStream_t stream)
+{
+    KvBytes kb;
+    PTQ1_TRY(check_cache(cache, &kb));
+    if (batch < 0) return fail(PTQ1_ERR_SHAPE, "batch = %lld is negative", (long long)batch);
+    if (max_pages < 0) return fail(PTQ1_ERR_SHAPE, "max_pages = %lld is negative", (long long)max_pages);
+    if (n_rows < 0) return fail(PTQ1_ERR_SHAPE, "n_rows = %lld is negative", (long long)n_rows);
+    if (n_rows > kMaxRows32) return fail(PTQ1_ERR_UNSUPPORTED, "n_rows = %lld > 2^31 - 1", (long long)n_rows);
+    if (batch > kMaxGridY || batch * cache->n_kv_heads > kMaxGridY)
+        return fail(PTQ1_ERR_UNSUPPORTED, "batch * n_kv_heads > %lld", (long long)kMaxGridY);
+    if (!float_type(out_dtype)) return fail(PTQ1_ERR_UNSUPPORTED, "out_dtype %d (F32, F16 or BF16)", out_dtype);
+    if (batch == 0 || n_rows == 0) return ok();
+    int64_t table = 0;
+    if (max_pages > kMaxRows32 || !mul_ok(batch, max_pages * 4, &table))
+        return fail(PTQ1_ERR_OVERFLOW, "block_table: size overflows");
+    PTQ1_TRY(check_device_array(block_table, "block_table", table, 4));
+    PTQ1_TRY(check_device_array(cu_seqlens, "cu_seqlens", (batch + 1) * 4, 4));
+    const int64_t ob = n_rows * cache->n_kv_heads * cache->head_dim * type_bytes(out_dtype);
+    PTQ1_TRY(check_device_array(k_out, "k_out", ob, kAlign));
+    PTQ1_TRY(check_device_array(v_out, "v_out", ob, kAlign));
+    if (overlaps(k_out, ob, v_out, ob)) return fail(PTQ1_ERR_ALIAS, "k_out overlaps v_out");
+    for (const void *o : {static_cast<const void *>(k_out), static_cast<const void *>(v_out)}) {
+        if (overlaps_cache(o, ob, cache, kb)) return fail(PTQ1_ERR_ALIAS, "k_out or v_out overlaps the cache");
+        if (overlaps(o, ob, block_table, table) || overlaps(o, ob, cu_seqlens, (batch + 1) * 4))
+            return fail(PTQ1_ERR_ALIAS, "k_out or v_out overlaps block_table or cu_seqlens");
+    }
+    return hip_status(ptq1::launch_kv_read(*cache, block_table, max_pages, cu_seqlens, batch, n_rows, k_out, v_out,
+                                           out_dtype, stream),
+                      "ptq1_kv_read");
+}
+
+size_t ptq1_attn_decode_workspace_bytes(int64_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                        int64_t max_len)
+{
+    if (!decode_sizes_ok(batch, n_q_heads, n_kv_heads, head_dim, max_len)) return 0;
+    return round_up(ptq1::decode_plan(batch, n_q_heads, n_kv_heads, head_dim, max_len).part_floats * 4, kWsAlign);
+}
+
+ptq1_status ptq1_attn_decode(const void *q, int32_t q_dtype, int64_t batch, int32_t n_q_heads,
+                             const ptq1_kv_cache *cache, const int32_t *block_table, int64_t max_pages,
+                             const int32_t *seq_lens, int64_t max_len, float scale, void *out, void *ws,
+                             size_t ws_bytes, hipStream_t stream)
+{
+    KvBytes kb;
+    PTQ1_TRY(check_cache(cache, &kb));
+    if (batch < 0) return fail(PTQ1_ERR_SHAPE, "batch = %lld is negative", (long long)batch);
+    if (batch > kMaxGridY) return fail(PTQ1_ERR_UNSUPPORTED, "batch = %lld > %lld", (long long)batch, (long long)kMaxGridY);
+    PTQ1_TRY(check_heads(n_q_heads, cache->n_kv_heads));
+    PTQ1_TRY(check_scale(scale));
+    if (max_pages < 0 || max_pages > kMaxRows32)
+        return fail(PTQ1_ERR_SHAPE, "max_pages = %lld", (long long)max_pages);
+    if (max_len < 0 || max_len > max_pages * cache->page_size)
+        return fail(PTQ1_ERR_SHAPE, "max_len = %lld (0 to max_pages * page_size = %lld)", (long long)max_len,
+                    (long long)(max_pages * cache->page_size));
+    if (!float_type(q_dtype)) return fail(PTQ1_ERR_UNSUPPORTED, "q_dtype %d (F32, F16 or BF16)", q_dtype);
+    if (cache->dtype != PTQ1_I8 && q_dtype != PTQ1_F32 && q_dtype != cache->dtype)
+        return fail(PTQ1_ERR_UNSUPPORTED, "q_dtype %s over a %s cache (F32 or the cache's own type)", type_name(q_dtype),
+                    type_name(cache->dtype));
+    if (max_len > kMaxDecodeLen)
+        return fail(PTQ1_ERR_UNSUPPORTED, "max_len = %lld > %lld", (long long)max_len, (long long)kMaxDecodeLen);
+    if (!decode_sizes_ok(batch, n_q_heads, cache->n_kv_heads, cache->head_dim, max_len))
+        return fail(PTQ1_ERR_UNSUPPORTED, "more than %lld groups of 16 query heads", (long long)kMaxGridY);
+    if (batch == 0) return ok();
+    const int64_t qb = batch * n_q_heads * cache->head_dim * type_bytes(q_dtype);
+    PTQ1_TRY(check_device_array(q, "q", qb, kAlign));
+    PTQ1_TRY(check_device_array(out, "out", qb, kAlign));
+    int64_t table = 0;
+    if (!mul_ok(batch, max_pages * 4, &table)) return fail(PTQ1_ERR_OVERFLOW, "block_table: size overflows");
+    PTQ1_TRY(check_device_array(block_table, "block_table", table, 4));
+    PTQ1_TRY(check_device_array(seq_lens, "seq_lens", batch * 4, 4));
+    const ptq1::DecodePlan plan = ptq1::decode_plan(batch, n_q_heads, cache->n_kv_heads, cache->head_dim, max_len);
+    const size_t need = round_up(plan.part_floats * 4, kWsAlign);
+    PTQ1_TRY(check_ws(ws, ws_bytes, need, "ptq1_attn_decode"));
+    if (overlaps(out, qb, q, qb)) return fail(PTQ1_ERR_ALIAS, "out overlaps q");
+    if (overlaps_cache(out, qb, cache, kb)) return fail(PTQ1_ERR_ALIAS, "out overlaps the cache");
+    if (overlaps(out, qb, block_table, table) || overlaps(out, qb, seq_lens, batch * 4))
+        return fail(PTQ1_ERR_ALIAS, "out overlaps block_table or seq_lens");
+    const int64_t wn = static_cast<int64_t>(need);
+    if (overlaps(ws, wn, q, qb) || overlaps(ws, wn, out, qb) || overlaps_cache(ws, wn, cache, kb) ||
+        overlaps(ws, wn, block_table, table) || overlaps(ws, wn, seq_lens, batch * 4))
+        return fail(PTQ1_ERR_ALIAS, "ws overlaps an argument");
+    return hip_status(ptq1::launch_attn_decode(plan, q, q_dtype, batch, n_q_heads, *cache, block_table, max_pages,
+                                               seq_lens, max_len, scale, out, static_cast<float *>(ws), stream),
+                      "ptq1_attn_decode");
+}
+
+size_t ptq1_attn_prompt_workspace_bytes(int64_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                        int64_t max_q, int64_t max_k)
+{
+    if (batch < 0 || batch > kMaxRows32 || n_kv_heads < 1 || n_kv_heads > 1024 || n_q_heads < 1 ||
+        n_q_heads > kMaxHeads || n_q_heads % n_kv_heads != 0 || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+        max_q < 0 || max_k < 0 || max_q > kMaxRows32 || max_k > kMaxRows32)
+        return 0;
+    return round_up(ptq1::prompt_part_floats(batch, n_q_heads, n_kv_heads, head_dim, max_q, max_k) * 4, kWsAlign);
+}
+
+ptq1_status ptq1_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                             int64_t v_stride, int32_t dtype, const int32_t *cu_q, const int32_t *cu_k,
+                             int64_t batch, int64_t n_q_rows, int64_t n_k_rows, int64_t max_q, int64_t max_k,
+                             int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t causal, float scale,
+                             void *out, void *ws, size_t ws_bytes, hipStream_t stream)
+{
+    if (dtype != PTQ1_F16 && dtype != PTQ1_BF16) return fail(PTQ1_ERR_UNSUPPORTED, "dtype %d (F16 or BF16)", dtype);
+    PTQ1_TRY(check_head_dim(head_dim));
+    PTQ1_TRY(check_heads(n_q_heads, n_kv_heads));
+    PTQ1_TRY(check_scale(scale));
+    if (batch < 0) return fail(PTQ1_ERR_SHAPE, "batch = %lld is negative", (long long)batch);
+    if (n_q_rows < 0 || n_k_rows < 0) return fail(PTQ1_ERR_SHAPE, "n_q_rows or n_k_rows is negative");
+    if (max_q < 0 || max_k < 0) return fail(PTQ1_ERR_SHAPE, "max_q or max_k is negative");
+    if (max_q > n_q_rows) max_q = n_q_rows;  // no sequence can be longer
+    if (max_k > n_k_rows) max_k = n_k_rows;
+    const int64_t group = n_q_heads / n_kv_heads;
+    if (batch > kMaxRows32 || n_q_rows > kMaxRows32 || n_k_rows > kMaxRows32 - 1024 ||
+        max_q * group > kMaxRows32 - 1024)
+        return fail(PTQ1_ERR_UNSUPPORTED, "more than 2^31 - 1025 rows of one kv head");
+    int64_t blocks;
+    if (!mul_ok((max_q * group + 127) / 128, batch * n_kv_heads, &blocks) || blocks > kMaxGridX)
+        return fail(PTQ1_ERR_UNSUPPORTED, "max_q * batch * heads too large");
+    if (batch == 0 || n_q_rows == 0 || max_q == 0) return ok();
+    int64_t qb, kbytes, vbytes;
+    const int64_t d = head_dim;
+    PTQ1_TRY(check_strided(q, "q", n_q_rows, n_q_heads * d, q_stride, 2, &qb));
+    PTQ1_TRY(check_strided(k, "k", n_k_rows, n_kv_heads * d, k_stride, 2, &kbytes));
+    PTQ1_TRY(check_strided(v, "v", n_k_rows, n_kv_heads * d, v_stride, 2, &vbytes));
+    PTQ1_TRY(check_device_array(cu_q, "cu_q", (batch + 1) * 4, 4));
+    PTQ1_TRY(check_device_array(cu_k, "cu_k", (batch + 1) * 4, 4));
+    const int64_t ob = n_q_rows * n_q_heads * d * 2;
+    PTQ1_TRY(check_device_array(out, "out", ob, kAlign));
+    if (overlaps(out, ob, q, qb) || overlaps(out, ob, k, kbytes) || overlaps(out, ob, v, vbytes))
+        return fail(PTQ1_ERR_ALIAS, "out overlaps q, k or v");
+    if (overlaps(out, ob, cu_q, (batch + 1) * 4) || overlaps(out, ob, cu_k, (batch + 1) * 4))
+        return fail(PTQ1_ERR_ALIAS, "out overlaps cu_q or cu_k");
+    const size_t need =
+        round_up(ptq1::prompt_part_floats(batch, n_q_heads, n_kv_heads, head_dim, max_q, max_k) * 4, kWsAlign);
+    PTQ1_TRY(check_ws(ws, ws_bytes, need, "ptq1_attn_prompt"));
+    const int64_t wn = static_cast<int64_t>(need);
+    if (overlaps(ws, wn, q, qb) || overlaps(ws, wn, k, kbytes) || overlaps(ws, wn, v, vbytes) ||
+        overlaps(ws, wn, out, ob) || overlaps(ws, wn, cu_q, (batch + 1) * 4) || overlaps(ws, wn, cu_k, (batch + 1) * 4))
+        return fail(PTQ1_ERR_ALIAS, "ws overlaps an argument");
+    const ptq1::PromptArgs a{q,      k,        v,        q_stride, k_stride, v_stride, cu_q,       cu_k,   batch,
+                             n_q_rows, n_k_rows, max_q,  max_k,    n_q_heads, n_kv_heads, causal != 0, scale, out};
+    return hip_status(ptq1::launch_attn_prompt(a, dtype, head_dim, static_cast<float *>(ws), stream), "ptq1_attn_prompt");
 }
 
 }  // extern "C"

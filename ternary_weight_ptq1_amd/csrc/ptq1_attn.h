@@ -1,0 +1,104 @@
+// ptq1_attn.h -- device helpers shared by the cache and attention kernels
+// (kv_cache.hip, attn_decode.hip, attn_prompt.hip).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <cstdint>
+
+#include "ptq1_device.h"
+
+namespace ptq1 {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float at_f32x4 __attribute__((ext_vector_type(4)));
+typedef float at_f32x8 __attribute__((ext_vector_type(8)));
+typedef float at_f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t at_u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t at_u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// The 16-bit operand types of the matrix instructions.
+template <typename T>
+struct Op16;
+
+template <>
+struct Op16<__bf16> {
+    typedef bf16x4 x4;
+    typedef bf16x8 x8;
+    static __device__ __forceinline__ at_f32x4 mfma16(x8 a, x8 b, at_f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ at_f32x16 mfma32(x8 a, x8 b, at_f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
+
+template <>
+struct Op16<_Float16> {
+    typedef f16x4 x4;
+    typedef f16x8 x8;
+    static __device__ __forceinline__ at_f32x4 mfma16(x8 a, x8 b, at_f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ at_f32x16 mfma32(x8 a, x8 b, at_f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+};
+
+// max of two values, NaN when either is: a row with a NaN must not end as a
+// finite maximum.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    return a != a || b != b ? __builtin_nanf("") : fmaxf(a, b);
+}
+
+// The larger of lane l's and lane l ^ H's value, in both lanes (H = 16, 32).
+template <int H>
+__device__ __forceinline__ float lane_pair_max(float v)
+{
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    uint32_t lo, hi;
+    if constexpr (H == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        lo = r[0];
+        hi = r[1];
+    } else {
+        const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        lo = r[0];
+        hi = r[1];
+    }
+    return fmaxf(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi));
+}
+
+// 4 contiguous elements of a source row, as fp32.
+__device__ __forceinline__ at_f32x4 load4(const float *p) { return *reinterpret_cast<const at_f32x4 *>(p); }
+__device__ __forceinline__ at_f32x4 load4(const __bf16 *p)
+{
+    return __builtin_convertvector(*reinterpret_cast<const bf16x4 *>(p), at_f32x4);
+}
+__device__ __forceinline__ at_f32x4 load4(const _Float16 *p)
+{
+    return __builtin_convertvector(*reinterpret_cast<const f16x4 *>(p), at_f32x4);
+}
+
+// 4 fp32 values to 4 contiguous elements, rounded to nearest even.
+__device__ __forceinline__ void store4(float *p, at_f32x4 v) { *reinterpret_cast<at_f32x4 *>(p) = v; }
+__device__ __forceinline__ void store4(__bf16 *p, at_f32x4 v)
+{
+    *reinterpret_cast<bf16x4 *>(p) = __builtin_convertvector(v, bf16x4);
+}
+__device__ __forceinline__ void store4(_Float16 *p, at_f32x4 v)
+{
+    *reinterpret_cast<f16x4 *>(p) = __builtin_convertvector(v, f16x4);
+}
+
+}  // namespace ptq1

@@ -7,6 +7,8 @@
 #include <atomic>
 #include <cstdint>
 
+#include "../../include/ptq1.h"
+
 namespace ptq1 {
 
 // Events for the next profiled launch (set by the C ABI's profiling hook,
@@ -140,5 +142,40 @@ hipError_t launch_prep_frag_pq2(const float *x, const float *g, const float *u, 
 hipError_t launch_gemm_pq2(const GemmPlan &p, const uint16_t *xf, int64_t m, const uint8_t *w0, int64_t n0,
                            const uint8_t *w1, int64_t n1, float *y0, float *y1, const float *residual, float *part,
                            hipStream_t s, bool fix = true);
+
+// ---- attention ---------------------------------------------------------------
+hipError_t launch_kv_write(const void *q, int64_t qs, const void *k, int64_t ks, const void *v, int64_t vs, int src,
+                           int64_t tokens, int32_t hq, const int32_t *positions, const float *cos_sin,
+                           int64_t n_positions, int32_t rot, const int64_t *slots, void *q_out, int q_type,
+                           const ptq1_kv_cache &c, hipStream_t s);
+hipError_t launch_kv_read(const ptq1_kv_cache &c, const int32_t *table, int64_t max_pages, const int32_t *cu,
+                          int64_t batch, int64_t rows, void *k_out, void *v_out, int out_type, hipStream_t s);
+
+// Decode attention: every sequence is cut into chunks of `chunk` tokens (a
+// multiple of 256), one workgroup per chunk, kv head and 16 query heads.
+// part: the chunks' unnormalised rows [batch][hq][chunks][d], then their
+// (maximum, sum) pairs; unused when chunks == 1.
+struct DecodePlan {
+    int64_t chunk = 0, chunks = 0;
+    size_t rows_floats = 0, part_floats = 0;
+};
+DecodePlan decode_plan(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_t max_len);
+hipError_t launch_attn_decode(const DecodePlan &p, const void *q, int q_type, int64_t batch, int32_t hq,
+                              const ptq1_kv_cache &c, const int32_t *table, int64_t max_pages, const int32_t *lens,
+                              int64_t max_len, float scale, void *out, float *part, hipStream_t s);
+
+// Prompt attention.  part: unused (splits == 1) or the splits' unnormalised
+// rows and their (maximum, sum) pairs.
+struct PromptArgs {
+    const void *q, *k, *v;
+    int64_t qs, ks, vs;  // row strides in elements
+    const int32_t *cu_q, *cu_k;
+    int64_t batch, q_rows, k_rows, max_q, max_k;
+    int32_t hq, hkv, causal;
+    float scale;
+    void *out;
+};
+hipError_t launch_attn_prompt(const PromptArgs &a, int dtype, int32_t d, float *part, hipStream_t s);
+size_t prompt_part_floats(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_t max_q, int64_t max_k);
 
 }  // namespace ptq1

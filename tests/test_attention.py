@@ -1,0 +1,617 @@
+"""The cache and attention calls against plain 64-bit implementations.
+
+Tolerances are bounds, computed from each case's own numbers:
+  - rounding to a type t is off by at most finfo(t).eps / 2 of the value (plus half the smallest step near zero);
+  - a dot product of d fp32 products is off by at most d 2^-24 sum |a b| (each product and sum rounded once);
+  - a weight exp2(x) with x off by e is off by ln(2) e of itself, and the hardware's exp2 by 2^-22;
+  - a weight that enters a product as two bf16 terms is off by 2^-17 of itself at most, as one 16-bit term by eps / 2;
+  - the weighted mean of v is then off by at most (twice the weights' relative error + n 2^-24) sum p |v|: once in
+    the sum of products, once in the sum of weights; sums of n fp32 terms add n 2^-24.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import synth
+import ternary_weight_ptq1_amd as P
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+F32, F16, BF16, I8 = torch.float32, torch.float16, torch.bfloat16, torch.int8
+U = 2.0 ** -24
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, *shape):
+    return torch.randn(shape, generator=g, device=DEV, dtype=F32)
+
+
+def half_step(y, t):
+    """The largest rounding error of values y (fp64) in type t."""
+    info = torch.finfo(t)
+    return y.abs() * (info.eps / 2) + info.smallest_normal * info.eps / 2
+
+
+# --------------------------------------------------------------- the cache ----
+
+def rope_table(n, rot):
+    half = rot // 2
+    a = torch.arange(n, dtype=torch.float64, device=DEV)[:, None] * 10000.0 ** (
+        -torch.arange(half, dtype=torch.float64, device=DEV) / half)
+    return torch.cat([a.cos(), a.sin()], 1).float()
+
+
+def turned(x, pos, table):
+    """(rotated rows in fp64, a bound on the fp32 rotation's error)."""
+    x = x.double()
+    if table is None:
+        return x, torch.zeros_like(x)
+    half = table.shape[1] // 2
+    row = table[pos.long()].double()[:, None]
+    c, s = row[..., :half], row[..., half:]
+    a, b, rest = x[..., :half], x[..., half:2 * half], x[..., 2 * half:]
+    y = torch.cat([a * c - b * s, b * c + a * s, rest], -1)
+    e = torch.cat([(a * c).abs() + (b * s).abs(), (b * c).abs() + (a * s).abs(), 0 * rest], -1) * (2 * U)
+    return y, e
+
+
+def cache_values(c):
+    """K and V [pages, heads, slots, d] in fp64 of a cache (NaN steps included)."""
+    k, v = c.k_pages.double(), c.v_pages.double().transpose(-1, -2)
+    if c.k_steps is not None:
+        k, v = k * c.k_steps.double()[..., None], v * c.v_steps.double()[..., None]
+    return k, v
+
+
+def check_rows(got, want, slack, t, amax=None):
+    """got against want (fp64) with `slack` of fp32 error and one rounding to t (int8: half a step of the row)."""
+    if t == I8:
+        top = want.abs().amax(-1, keepdim=True)
+        tol = (top / 127) * 0.5 * (1 + 2.0 ** -15) + slack.amax(-1, keepdim=True) * 2
+    else:
+        tol = half_step(want.abs() + slack, t) + slack
+    err = (got.double() - want).abs()
+    assert bool((err <= tol).all()), f"worst error over its bound: {(err / tol.clamp_min(1e-300)).max().item():.3f}"
+
+
+@pytest.mark.parametrize("src", [F32, F16, BF16])
+@pytest.mark.parametrize("ctype", [F16, BF16, I8])
+@pytest.mark.parametrize("n,hq,hkv,d,page,rot", [
+    (1, 5, 1, 64, 16, 64),
+    (3, 0, 2, 128, 32, 32),
+    (33, 6, 3, 64, 64, 8),
+    (70, 8, 2, 256, 16, 64),
+    (129, 4, 4, 128, 256, 128),
+    (40, 3, 1, 128, 128, 0),
+])
+def test_kv_write(src, ctype, n, hq, hkv, d, page, rot):
+    g = gen(n + d + rot)
+    pages = -(-2 * n // page) + 2
+    qt = {F16: F16, BF16: BF16, I8: F32}[ctype]
+    x = randn(g, n, hq + 2 * hkv + 1, d).to(src)  # one head more: the rows lie apart
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:hq + 2 * hkv]
+    slots = torch.randperm(pages * page, generator=g, device=DEV)[:n]
+    slots[n // 2] = -1
+    if n > 8:  # a run of neighbours and one past the end
+        slots[:8] = pages * page - 8 + torch.arange(8, device=DEV)
+        slots[8:] = torch.randperm(pages * page - 8, generator=g, device=DEV)[:n - 8]
+        slots[9], slots[10] = -5, pages * page
+    pos = torch.randint(0, 50, (n,), generator=g, device=DEV, dtype=torch.int32)
+    table = rope_table(50, rot) if rot else None
+    c = P.ptq1_kv_cache(pages, page, hkv, d, ctype, DEV)
+    for t in (c.k_pages, c.v_pages):
+        t.fill_(3)
+    if ctype == I8:
+        c.k_steps.fill_(0.5), c.v_steps.fill_(0.5)
+    out = P.ptq1_kv_write(q if hq else None, k, v, slots, c, positions=pos, cos_sin=table, q_dtype=qt if hq else None)
+    torch.cuda.synchronize()
+    if hq:
+        y, e = turned(q, pos, table)
+        assert out.dtype == qt and out.shape == (n, hq, d)
+        check_rows(out, y, e, qt)
+    else:
+        assert out is None
+    kc, vc = cache_values(c)
+    ok = (slots >= 0) & (slots < pages * page)
+    at, off = slots[ok] // page, slots[ok] % page
+    y, e = turned(k, pos, table)
+    check_rows(kc[at, :, off], y[ok], e[ok], ctype)
+    check_rows(vc[at, :, off], v[ok].double(), torch.zeros_like(y[ok]), ctype)
+    kept = torch.ones(pages * page, dtype=torch.bool, device=DEV)
+    kept[slots[ok]] = False
+    other = 1.5 if ctype == I8 else 3.0
+    for t in (kc, vc):  # everything else as it was
+        assert bool((t.transpose(1, 2).reshape(pages * page, hkv, d)[kept] == other).all())
+
+
+def test_kv_write_awkward_rows():
+    """Zeros, tiny rows, a NaN, an infinity and a position outside the table."""
+    d, page = 128, 16
+    for ctype in (I8, BF16):
+        c = P.ptq1_kv_cache(2, page, 1, d, ctype, DEV)
+        k = torch.ones((6, 1, d), device=DEV)
+        k[0] = 0.0
+        k[1] = 2.0 ** -120
+        k[2, 0, 5] = float("nan")
+        k[3, 0, 7] = float("inf")
+        k[4] = 3e38
+        pos = torch.zeros(6, dtype=torch.int32, device=DEV)
+        pos[5] = 9
+        table = rope_table(9, 64)
+        slots = torch.arange(6, device=DEV)
+        q = P.ptq1_kv_write(k, k, k, slots, c, positions=pos, cos_sin=table)
+        kc, vc = cache_values(c)
+        kc, vc = kc[0, 0], vc[0, 0]
+        assert bool((kc[0] == 0).all()) and bool((vc[0] == 0).all())
+        assert bool((vc[1] == (0.0 if ctype == I8 else 2.0 ** -120)).all())
+        if ctype == I8:
+            assert bool(vc[2].isnan().all()) and bool(vc[3].isnan().all())
+            assert bool(kc[5].isnan().all())
+        else:
+            assert bool(vc[2, 5].isnan()) and vc[3, 7].item() == float("inf") and int(vc[2:4].isnan().sum()) == 1
+            assert bool(kc[5, :64].isnan().all()) and bool((kc[5, 64:] == 1).all())
+        assert bool(((vc[4] - 3e38).abs() <= 3e38 * 2.0 ** -8).all())
+        # int8: 127 times fl(1 / 127), whose relative error is at most half a step of fp32
+        assert bool(((vc[5] - 1).abs() <= (U if ctype == I8 else 0.0)).all())
+        assert bool(q[5, 0, :64].isnan().all()) and bool((q[5, 0, 64:] == 1).all())
+
+
+def filled_cache(g, pages, page, hkv, d, ctype):
+    c = P.ptq1_kv_cache(pages, page, hkv, d, ctype, DEV)
+    if ctype == I8:
+        c.k_pages.copy_(torch.randint(-127, 128, c.k_pages.shape, generator=g, device=DEV))
+        c.v_pages.copy_(torch.randint(-127, 128, c.v_pages.shape, generator=g, device=DEV))
+        c.k_steps.copy_(0.01 + 0.02 * torch.rand(c.k_steps.shape, generator=g, device=DEV))
+        c.v_steps.copy_(0.01 + 0.02 * torch.rand(c.v_steps.shape, generator=g, device=DEV))
+    else:
+        c.k_pages.copy_(randn(g, *c.k_pages.shape))
+        c.v_pages.copy_(randn(g, *c.v_pages.shape))
+    return c
+
+
+def tables(g, lens, page, width=None):
+    need = [-(-n // page) for n in lens]
+    pages = sum(need) + 1
+    order = torch.randperm(pages, generator=g, device=DEV).to(torch.int32)
+    t = torch.full((len(lens), max(1, *need) if width is None else width), -7, dtype=torch.int32, device=DEV)
+    at = 0
+    for i, n in enumerate(need):
+        t[i, :n] = order[at:at + n]
+        at += n
+    return t, pages
+
+
+def poison_unused(c, table, lens):
+    """Everything in the pages that no sequence's length covers: NaN (int8: NaN steps)."""
+    page = c.page_size
+    used = torch.zeros((c.n_pages, page), dtype=torch.bool, device=DEV)
+    for i, n in enumerate(lens):
+        for j in range(-(-n // page)):
+            used[table[i, j].item(), :min(page, n - j * page)] = True
+    hid = ~used[:, None, :].expand(-1, c.n_kv_heads, -1)
+    if c.k_steps is not None:
+        c.k_steps[hid] = float("nan")
+        c.v_steps[hid] = float("nan")
+    else:
+        c.k_pages[hid] = float("nan")
+        c.v_pages[hid[:, :, None, :].expand_as(c.v_pages)] = float("inf")
+
+
+def sequence(c, values, table, b, n):
+    """K or V [heads, n, d] of sequence b in fp64."""
+    page = c.page_size
+    rows = table[b, :-(-n // page)].long()
+    return values[rows].transpose(0, 1).reshape(c.n_kv_heads, -1, c.head_dim)[:, :n]
+
+
+@pytest.mark.parametrize("ctype,out", [(F16, F16), (BF16, BF16), (BF16, F32), (I8, BF16), (I8, F32), (I8, F16)])
+@pytest.mark.parametrize("hkv,d,page,lens", [
+    (1, 64, 16, [1]),
+    (3, 128, 32, [5, 0, 64, 130]),
+    (2, 256, 64, [63, 200, 1]),
+    (8, 128, 256, [300, 17]),
+])
+def test_kv_read(ctype, out, hkv, d, page, lens):
+    g = gen(sum(lens) + d)
+    table, pages = tables(g, lens, page)
+    c = filled_cache(g, pages, page, hkv, d, ctype)
+    poison_unused(c, table, lens)
+    cu = torch.tensor(np.cumsum([2] + lens), dtype=torch.int32, device=DEV)  # two rows ahead of the first sequence
+    total = int(cu[-1]) + 3                                                  # and three behind the last
+    ko = torch.full((total, hkv, d), 9.0, dtype=out, device=DEV)
+    vo = torch.full((total, hkv, d), 9.0, dtype=out, device=DEV)
+    P.ptq1_kv_read(c, table, cu, total, dtype=out, out=(ko, vo))
+    kc, vc = cache_values(c)
+    for got, val in ((ko, kc), (vo, vc)):
+        want = torch.full((total, hkv, d), 9.0, dtype=torch.float64, device=DEV)
+        for b, n in enumerate(lens):
+            want[int(cu[b]):int(cu[b]) + n] = sequence(c, val, table, b, n).transpose(0, 1)
+        # step * code is one fp32 product, then one rounding
+        tol = half_step(want, out) + want.abs() * (U if ctype == I8 else 0.0)
+        tol[got.double() == want] = 0
+        assert bool(((got.double() - want).abs() <= tol).all())
+        assert bool((got[:2] == 9).all()) and bool((got[int(cu[-1]):] == 9).all())
+
+
+def test_kv_read_bad_pages_and_short_output():
+    g = gen(5)
+    c = filled_cache(g, 4, 16, 2, 64, BF16)
+    table = torch.tensor([[1, 99], [-1, 2]], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, 40, 60], dtype=torch.int32, device=DEV)  # 40 tokens: page 99 is bad, tokens 32.. have none
+    k, v = P.ptq1_kv_read(c, table, cu, 50, dtype=F32)             # the last ten rows do not fit
+    kc, vc = cache_values(c)
+    for got, val in ((k, kc), (v, vc)):
+        assert bool((got[:16].double() == val[1].transpose(0, 1)).all())
+        assert bool(got[16:50].isnan().all())
+
+
+# ------------------------------------------------------------------ decode ----
+
+def attention_bounds(q, k, v, scale, wterm, mask=None):
+    """(rows, bound on the kernels' error before the rounding of the result) of one kv head in fp64: q [n, d],
+    k, v [m, d]; wterm: relative error of a weight as it enters the second product; mask [n, m] (True: seen)."""
+    d = q.shape[1]
+    logits = scale * (q @ k.T.contiguous())
+    size = scale * (q.abs() @ k.abs().T.contiguous())
+    if mask is not None:
+        logits = logits.masked_fill(~mask, -math.inf)
+        size = size.masked_fill(~mask, 0.0)
+    top = logits.amax(1, keepdim=True)
+    w = torch.exp(logits - torch.where(top == -math.inf, 0.0, top))
+    total = w.sum(1, keepdim=True)
+    p = torch.where(total > 0, w / total, 0.0)
+    # scores: d products and sums, then a few more roundings of the score and its maximum
+    score = (d + 8) * U * size.amax(1, keepdim=True) + 4 * U * torch.where(top == -math.inf, 0.0, top.abs())
+    weight = score + 2.0 ** -22
+    n = (p > 0).sum(1, keepdim=True).double()
+    return p @ v, (2 * weight + wterm + 2 * n * U) * (p @ v.abs())
+
+
+WEIGHT_TERM = {(F32, BF16): 2.0 ** -24, (BF16, BF16): 2.0 ** -17, (F32, F16): 2.0 ** -21, (F16, F16): 2.0 ** -21,
+               (F32, I8): 2.0 ** -24, (BF16, I8): 2.0 ** -17, (F16, I8): 2.0 ** -17}
+
+
+def check_decode(q, c, table, lens, got, scale=None):
+    hq, d = q.shape[1:]
+    group = hq // c.n_kv_heads
+    scale = d ** -0.5 if scale is None else scale
+    kc, vc = cache_values(c)
+    term = WEIGHT_TERM[(q.dtype, c.dtype)]
+    for b, n in enumerate(lens):
+        if n == 0:
+            assert bool((got[b] == 0).all())
+            continue
+        k, v = sequence(c, kc, table, b, n), sequence(c, vc, table, b, n)
+        for h in range(c.n_kv_heads):
+            rows = slice(h * group, (h + 1) * group)
+            want, tol = attention_bounds(q[b, rows].double(), k[h], v[h], scale, term)
+            tol = tol + half_step(want.abs() + tol, q.dtype)
+            err = (got[b, rows].double() - want).abs()
+            assert bool((err <= tol).all()), f"b={b} h={h}: {(err / tol).max().item():.3f} of the bound"
+
+
+PAIRS = [(F32, BF16), (BF16, BF16), (F32, F16), (F16, F16), (F32, I8), (BF16, I8), (F16, I8)]
+
+
+@pytest.mark.parametrize("qt,ctype", PAIRS)
+@pytest.mark.parametrize("hq,hkv,d,page,lens", [
+    (1, 1, 64, 16, [1]),
+    (5, 1, 128, 16, [31, 0, 33, 64, 7]),
+    (6, 2, 256, 32, [129, 1, 255]),
+    (32, 8, 128, 64, [257, 511, 512, 1030]),
+    (20, 1, 64, 256, [300, 0, 2]),      # more than 16 query heads of one kv head
+    (33, 1, 128, 128, [700, 128]),
+    (7, 7, 128, 16, [100, 2049]),
+])
+def test_attn_decode(qt, ctype, hq, hkv, d, page, lens):
+    g = gen(hq * d + sum(lens))
+    table, pages = tables(g, lens, page)
+    c = filled_cache(g, pages, page, hkv, d, ctype)
+    poison_unused(c, table, lens)
+    q = randn(g, len(lens), hq, d).to(qt)
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    got = P.ptq1_attn_decode(q, c, table, sl)
+    assert got.dtype == qt and got.shape == q.shape
+    check_decode(q, c, table, lens, got)
+    # a bound on the lengths changes the split, not what is computed
+    check_decode(q, c, table, lens, P.ptq1_attn_decode(q, c, table, sl, max_len=max(lens)))
+    # the same call gives the same bits
+    assert torch.equal(got, P.ptq1_attn_decode(q, c, table, sl))
+
+
+@pytest.mark.parametrize("ctype", [BF16, I8])
+def test_attn_decode_long(ctype):
+    """Long enough for many chunks, larger scores than the softmax's first ones, and a scale of the caller's."""
+    g = gen(11)
+    lens = [40000, 3]
+    table, pages = tables(g, lens, 64)
+    c = filled_cache(g, pages, 64, 2, 128, ctype)
+    q = randn(g, 2, 8, 128) * 3
+    got = P.ptq1_attn_decode(q, c, table, torch.tensor(lens, dtype=torch.int32, device=DEV), scale=0.3)
+    check_decode(q, c, table, lens, got, scale=0.3)
+
+
+def test_attn_decode_large_and_small_queries():
+    """fp32 queries outside fp16's range over an fp16 cache, and zeros."""
+    g = gen(12)
+    lens = [70, 70, 70]
+    table, pages = tables(g, lens, 32)
+    c = filled_cache(g, pages, 32, 1, 64, F16)
+    q = randn(g, 3, 4, 64)
+    q[0] *= 1e7
+    q[1] *= 1e-9
+    q[2] = 0
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    for scale in (1e-7, 1e-2):
+        check_decode(q[1:], c, table[1:], lens[1:], P.ptq1_attn_decode(q[1:].contiguous(), c, table[1:], sl[1:],
+                                                                        scale=scale), scale)
+    check_decode(q[:1], c, table[:1], lens[:1], P.ptq1_attn_decode(q[:1].contiguous(), c, table[:1], sl[:1],
+                                                                    scale=1e-8), 1e-8)
+
+
+def test_attn_decode_refused_sequences():
+    """Bad lengths and pages make their own sequence NaN and no other."""
+    g = gen(13)
+    lens = [100, 100, 100, 100, 100]
+    table, pages = tables(g, lens, 16, width=20)
+    c = filled_cache(g, pages, 16, 2, 64, BF16)
+    good = table.clone()
+    table[1, 6] = pages      # the last page of its length
+    table[2, 0] = -1
+    table[3, 7] = -1         # not covered by the length: never read
+    sl = torch.tensor([100, 100, 100, 100, -3], dtype=torch.int32, device=DEV)
+    q = randn(g, 5, 4, 64).to(BF16)
+    for max_len in (100, 320):
+        got = P.ptq1_attn_decode(q, c, table, sl, max_len=max_len)
+        assert bool(got[[1, 2, 4]].isnan().all())
+        check_decode(q[[0, 3]], c, good[[0, 3]], [100, 100], got[[0, 3]])
+    got = P.ptq1_attn_decode(q, c, good, torch.tensor([100, 101, 0, 99, 400], dtype=torch.int32, device=DEV), max_len=100)
+    assert bool(got[[1, 4]].isnan().all())
+    check_decode(q[[0, 2, 3]], c, good[[0, 2, 3]], [100, 0, 99], got[[0, 2, 3]])
+
+
+def test_attn_decode_non_finite_values():
+    """A NaN key makes the rows of its heads NaN; an infinite value reaches only its dimension (as an infinity or, where
+    a weight's second 16-bit term is zero or negative, as a NaN: the header promises either)."""
+    g = gen(14)
+    lens = [50, 50]
+    table, pages = tables(g, lens, 16)
+    c = filled_cache(g, pages, 16, 2, 64, BF16)
+    c.k_pages[table[0, 1].item(), 1, 3, 5] = float("nan")
+    c.v_pages[table[1, 2].item(), 0, 9, 4] = float("inf")
+    q = randn(g, 2, 4, 64)
+    got = P.ptq1_attn_decode(q, c, table, torch.tensor(lens, dtype=torch.int32, device=DEV))
+    assert bool(got[0, 2:].isnan().all()) and bool(got[0, :2].isfinite().all())
+    assert not bool(got[1, :2, 9].isfinite().any()) and int((~got[1].isfinite()).sum()) == 2
+
+
+# ------------------------------------------------------------------ prompt ----
+
+def check_prompt(q, k, v, lq, lk, got, causal, scale=None, at_q=0, at_k=0):
+    hq, d = q.shape[1:]
+    hkv = k.shape[1]
+    group = hq // hkv
+    scale = d ** -0.5 if scale is None else scale
+    term = torch.finfo(q.dtype).eps / 2
+    for nq, nk in zip(lq, lk):
+        mask = None
+        if causal:
+            mask = torch.arange(nk, device=DEV)[None] <= torch.arange(nq, device=DEV)[:, None] + (nk - nq)
+        for h in range(hq):
+            qq = q[at_q:at_q + nq, h].double()
+            kk, vv = (t[at_k:at_k + nk, h // group].double() for t in (k, v))
+            if nk == 0:
+                assert bool((got[at_q:at_q + nq, h] == 0).all())
+                continue
+            want, tol = attention_bounds(qq, kk, vv, scale, term, mask)
+            tol = tol + half_step(want.abs() + tol, q.dtype)
+            err = (got[at_q:at_q + nq, h].double() - want).abs()
+            assert bool((err <= tol).all()), f"head {h} of {nq} x {nk}: {(err / tol).nan_to_num(9e9).max().item():.3f}"
+            if causal and nq > nk:
+                assert bool((got[at_q:at_q + nq - nk, h] == 0).all())
+        at_q += nq
+        at_k += nk
+
+
+def cumulated(lens, first=0):
+    return torch.tensor(np.cumsum([first] + list(lens)), dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,d,lq,lk", [
+    (1, 1, 64, [1], [1]),
+    (5, 1, 128, [1, 33, 0, 64], [1, 33, 5, 64]),
+    (4, 2, 256, [40, 31], [40, 95]),
+    (8, 8, 128, [129, 3], [129, 700]),
+    (7, 1, 64, [200, 10, 9], [200, 3, 0]),     # queries that see no key
+    (32, 8, 128, [65, 127, 66], [65, 256, 1025]),
+    (3, 3, 256, [150], [333]),
+    (40, 1, 64, [7, 20], [64, 20]),            # a large group
+])
+def test_attn_prompt(dtype, causal, hq, hkv, d, lq, lk):
+    g = gen(hq + d + sum(lq))
+    q, k, v = randn(g, sum(lq), hq, d).to(dtype), randn(g, sum(lk), hkv, d).to(dtype), randn(g, sum(lk), hkv, d).to(dtype)
+    got = P.ptq1_attn_prompt(q, k, v, cumulated(lq), cumulated(lk), max_q=max(lq), max_k=max(lk), causal=causal)
+    assert got.dtype == dtype and got.shape == q.shape
+    check_prompt(q, k, v, lq, lk, got, causal)
+    # without the bounds, and the same bits again
+    assert torch.equal(got, P.ptq1_attn_prompt(q, k, v, cumulated(lq), cumulated(lk), max_q=max(lq), max_k=max(lk),
+                                               causal=causal))
+    check_prompt(q, k, v, lq, lk, P.ptq1_attn_prompt(q, k, v, cumulated(lq), cumulated(lk), causal=causal), causal)
+
+
+def test_attn_prompt_stacked_rows_and_gaps():
+    """q, k and v as parts of one stacked projection; rows ahead of the first sequence and behind the last stay."""
+    g = gen(21)
+    lens = [70, 45]
+    x = randn(g, 120, 4 + 2 * 2, 128).to(BF16)
+    q, k, v = x[:, :4], x[:, 4:6], x[:, 6:]
+    out = torch.full((120, 4, 128), 7.0, dtype=BF16, device=DEV)
+    cu = cumulated(lens, 3)
+    P.ptq1_attn_prompt(q, k, v, cu, cu, max_q=70, max_k=70, out=out)
+    check_prompt(q, k, v, lens, lens, out, True, at_q=3, at_k=3)
+    assert bool((out[:3] == 7).all()) and bool((out[118:] == 7).all())
+
+
+def test_attn_prompt_bounds_and_ranges():
+    """A sequence past its bound, or with rows out of range, gets NaN rows; the others are right."""
+    g = gen(22)
+    lens = [30, 200, 17]
+    q, k, v = (randn(g, 247, 2, 64).to(F16) for _ in range(3))
+    cu = cumulated(lens)
+    got = P.ptq1_attn_prompt(q, k, v, cu, cu, max_q=100, max_k=247)
+    assert bool(got[30:230].isnan().all())
+    check_prompt(q, k, v, [30], [30], got[:30], True)
+    check_prompt(q[230:], k[230:], v[230:], [17], [17], got[230:], True)
+    far = cumulated([30, 200, 18])  # the last one's keys end behind the last row
+    got = P.ptq1_attn_prompt(q, k, v, cu, far, max_q=247, max_k=247)
+    assert bool(got[230:].isnan().all()) and bool(got[:230].isfinite().all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attn_prompt_large_scores(d):
+    """Scores whose maximum grows along the keys by more than fp16 or bf16 weights span."""
+    g = gen(23)
+    n = 300
+    q, k, v = (randn(g, n, 1, d).to(BF16) for _ in range(3))
+    k = (k.float() * torch.linspace(0.1, 8, n, device=DEV)[:, None, None]).to(BF16)
+    for scale in (d ** -0.5, 1.0):
+        got = P.ptq1_attn_prompt(q, k, v, cumulated([n]), cumulated([n]), scale=scale)
+        check_prompt(q, k, v, [n], [n], got, True, scale)
+
+
+# ---------------------------------------------------------------- together ----
+
+def folded(seed, n, k):
+    t = synth.trits(seed, synth.S_GATE_TRITS, n, k)
+    s = synth.scales(seed, synth.S_GATE_SCALES, n, k // 128)
+    blocks = oracle.pack(t, s)
+    return P.ptq1_tile(torch.from_numpy(blocks).to(DEV), n, k), \
+        torch.from_numpy(oracle.dequant(blocks, n, k).astype(np.float64)).to(DEV)
+
+
+def test_layer_half_prompt_then_token():
+    """A layer's attention half as a program runs it: stacked q, k, v projection of a prompt (ptq1_gemm), rotary
+    positions and the cache write, the sequence read back, prompt attention, output projection; then one more token
+    through the decode calls over the same cache.  Each stage against fp64 from that stage's own inputs."""
+    dm, hq, hkv, d, n, page = 1024, 8, 2, 128, 77, 32
+    wqkv, dense_qkv = folded(1, (hq + 2 * hkv) * d, dm)
+    wo, dense_o = folded(2, dm, hq * d)
+    signs = torch.from_numpy(synth.signs(3)).to(DEV)
+    x = torch.from_numpy(synth.activations(4, n + 1, dm)).to(DEV)
+    rope = rope_table(200, d)
+    c = P.ptq1_kv_cache(5, page, hkv, d, BF16, DEV)
+    table = torch.tensor([[3, 0, 4]], dtype=torch.int32, device=DEV)
+    place = torch.arange(n + 1, device=DEV)
+    slots = table[0, place // page].long() * page + place % page
+    pos = place.to(torch.int32)
+    # prompt
+    qkv = P.ptq1_gemm(wqkv, (hq + 2 * hkv) * d, dm, x[:n].contiguous(), signs).view(n, hq + 2 * hkv, d)
+    rot = P.hadamard_rotate(x, signs).double()
+    want = rot[:n] @ dense_qkv.T.contiguous()
+    assert (qkv.double().view(n, -1) - want).norm() <= 3e-3 * want.norm()
+    q = P.ptq1_kv_write(qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], slots[:n], c, positions=pos[:n],
+                        cos_sin=rope, q_dtype=BF16)
+    y, e = turned(qkv[:, :hq], pos[:n], rope)
+    check_rows(q, y, e, BF16)
+    cu = cumulated([n])
+    k, v = P.ptq1_kv_read(c, table, cu, n, dtype=BF16)
+    y, e = turned(qkv[:, hq:hq + hkv], pos[:n], rope)
+    check_rows(k, y, e, BF16)
+    assert torch.equal(v, qkv[:, hq + hkv:].to(BF16))
+    o = P.ptq1_attn_prompt(q, k, v, cu, cu)
+    check_prompt(q, k, v, [n], [n], o, True)
+    P.ptq1_gemm(wo, dm, hq * d, o.float().view(n, hq * d), signs)
+    # one more token
+    qkv1 = P.ptq1_matvec(wqkv, (hq + 2 * hkv) * d, dm, x[n].contiguous(), signs).view(1, hq + 2 * hkv, d)
+    q1 = P.ptq1_kv_write(qkv1[:, :hq], qkv1[:, hq:hq + hkv], qkv1[:, hq + hkv:], slots[n:], c, positions=pos[n:],
+                         cos_sin=rope)
+    assert q1.dtype == F32
+    o1 = P.ptq1_attn_decode(q1, c, table, torch.tensor([n + 1], dtype=torch.int32, device=DEV))
+    check_decode(q1, c, table, [n + 1], o1)
+    out = P.ptq1_matvec(wo, dm, hq * d, o1.view(-1), signs, residual=x[n].contiguous())
+    want = x[n].double() + dense_o @ P.hadamard_rotate(o1.view(1, -1), signs).double()[0]
+    assert (out.double() - want).norm() <= 1e-5 * want.norm()
+    # the decode call on the prompt's last position agrees with the prompt call (16-bit weights there)
+    last = P.ptq1_attn_decode(q[-1:].contiguous(), c, table, torch.tensor([n], dtype=torch.int32, device=DEV))
+    # both are within their own bounds of the same exact rows
+    check_decode(q[-1:], c, table, [n], last)
+
+
+def decode_state(seed, lens, ctype=BF16, qt=F32):
+    g = gen(seed)
+    table, pages = tables(g, lens, 32)
+    c = filled_cache(g, pages, 32, 2, 128, ctype)
+    return randn(g, len(lens), 8, 128).to(qt), c, table, torch.tensor(lens, dtype=torch.int32, device=DEV)
+
+
+def test_captured_step_replays_with_new_contents():
+    """The token step (write, attend) captured once and replayed with the lengths, slots and rows that the program
+    puts into the same buffers, its own eager work in between."""
+    lens = [300, 700]
+    q, c, table, sl = decode_state(31, [n + 8 for n in lens], BF16)
+    sl.copy_(torch.tensor(lens, dtype=torch.int32))
+    g = gen(32)
+    rows = randn(g, 2, 12, 128)
+    rope = rope_table(1000, 128)
+    slots = torch.zeros(2, dtype=torch.int64, device=DEV)
+    ws = torch.empty(P.workspace_bytes("attn_decode", 2, 8, 2, 128, 736), dtype=torch.uint8, device=DEV)
+    q_out, out = torch.empty(2, 8, 128, device=DEV), torch.empty(2, 8, 128, device=DEV)
+
+    def step():
+        P.ptq1_kv_write(rows[:, :8], rows[:, 8:10], rows[:, 10:], slots, c, positions=sl, cos_sin=rope, out=q_out)
+        P.ptq1_attn_decode(q_out, c, table, sl, max_len=736, out=out, ws=ws)
+
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for i in range(4):
+        rows.copy_(randn(g, 2, 12, 128))
+        sl.add_(1)
+        place = (sl - 1).long()
+        slots.copy_(table[torch.arange(2, device=DEV), place // 32].long() * 32 + place % 32)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        step()
+        assert torch.equal(got, out)
+        check_decode(q_out, c, table, [n + i + 1 for n in lens], out)
+
+
+def test_other_stream():
+    """Calls on a stream of the caller's, with workspaces and results of their own allocated meanwhile."""
+    q, c, table, sl = decode_state(33, [2000, 900], I8)
+    want = P.ptq1_attn_decode(q, c, table, sl)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        got = P.ptq1_attn_decode(q, c, table, sl, stream=side)
+        torch.empty(1 << 20, device=DEV).fill_(float("nan"))  # the allocator may hand out a freed workspace
+        side.synchronize()
+        assert torch.equal(got, want)
+
+
+def test_two_streams_with_a_workspace_each():
+    states = [decode_state(40 + i, [1500 + 100 * i, 64]) for i in range(2)]
+    want = [P.ptq1_attn_decode(q, c, t, sl) for q, c, t, sl in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in states]
+    got = [[], []]
+    for _ in range(6):
+        for i, (q, c, t, sl) in enumerate(states):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(P.ptq1_attn_decode(q, c, t, sl))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
