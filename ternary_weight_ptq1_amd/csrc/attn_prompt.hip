@@ -22,6 +22,8 @@
 // two transposing LDS reads of four keys each.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "ptq1_attn.h"
 #include "ptq1_launch.h"
 
@@ -31,41 +33,76 @@ namespace {
 constexpr int kPrWaves = 4;
 constexpr int kPrThreads = 64 * kPrWaves;
 constexpr int kPrRows = 32 * kPrWaves;  // query rows of a workgroup
+constexpr int kAhead = 4;               // K reads ahead of their products
 
 typedef short at_s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) at_s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) void lds_void;
+constexpr int kBufferFlags = 0x00027000;  // raw buffer of bytes
 
-// Place (in elements) of the 16-byte piece p of key row r in a K or V tile of
-// rows of D elements.  K is read 16 rows at one piece at a time, V 4 rows at
-// four pieces; the exclusive-or spreads either over the 64 banks.
+constexpr int prompt_keys(int d) { return d == 256 ? 32 : 64; }
+
+// The 16-byte piece p of key row r of a K or V tile lies at piece p ^ swizzle
+// of that row.  K is read 16 rows at one piece at a time, V 4 rows at four
+// pieces; the exclusive-or spreads either over the 64 banks.
+template <int D>
+__device__ __forceinline__ int k_swizzle(int r)
+{
+    return D >= 128 ? r & 15 : (r >> 1) & 7;
+}
+template <int D>
+__device__ __forceinline__ int v_swizzle(int r)
+{
+    return D >= 128 ? (r & 3) << 2 : ((r >> 1) & 1) << 2;
+}
 template <int D>
 __device__ __forceinline__ int k_place(int r, int p)
 {
-    constexpr int P = D / 8;  // pieces of a row
-    const int x = P >= 16 ? r & 15 : (r >> 1) & 7;
-    return r * D + ((p ^ x) << 3);
+    return r * D + ((p ^ k_swizzle<D>(r)) << 3);
 }
 template <int D>
 __device__ __forceinline__ int v_place(int r, int p)
 {
-    const int x = D >= 128 ? (r & 3) << 2 : ((r >> 1) & 1) << 2;
-    return r * D + ((p ^ x) << 3);
+    return r * D + ((p ^ v_swizzle<D>(r)) << 3);
+}
+
+// 16 bytes per lane from base + off to 1024 consecutive bytes of LDS; bytes
+// from `bytes` on are not read.
+__device__ __forceinline__ void copy_to_lds(const char *base, uint32_t bytes, uint32_t off, void *dst)
+{
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(base), 0, static_cast<int>(bytes), kBufferFlags);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)dst, 16, static_cast<int>(off), 0, 0, 0);
+}
+
+// One of the eight values has an exponent of all ones.
+template <typename T>
+__device__ __forceinline__ bool has_non_finite(at_u32x4 w)
+{
+    constexpr uint32_t E = std::is_same<T, __bf16>::value ? 0x7f807f80u : 0x7c007c00u;
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = (w[i] & E) ^ E;  // a zero half: all ones
+        any |= (x - 0x00010001u) & ~x & 0x80008000u;
+    }
+    return any != 0;
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(PromptArgs a, int32_t tiles)
+__global__ void __launch_bounds__(kPrThreads, 2) k_attn_prompt(PromptArgs a, int32_t tiles)
 {
     typedef typename Op16<T>::x8 x8;
-    constexpr int BN = D == 256 ? 32 : 64;  // keys of a tile
+    constexpr int BN = prompt_keys(D);      // keys of a tile
     constexpr int KT = BN / 32;             // score tiles
     constexpr int DT = D / 32;              // output tiles
     constexpr int KK = D / 16;              // MFMA steps over the head dimension
     constexpr int P = D / 8;                // 16-byte pieces of a row
     constexpr int NLD = BN * P / kPrThreads;  // pieces a thread stages, of K and of V
 
-    extern __shared__ __attribute__((aligned(16))) char lds[];
-    T *kt = reinterpret_cast<T *>(lds);            // [2][BN * D]
-    T *vt = kt + 2 * BN * D;                       // [2][BN * D]
+    // Two tiles each: separate objects, so that the copies into one need not
+    // have ended before the other is read.
+    __shared__ __attribute__((aligned(16))) T kt0[BN * D], kt1[BN * D], vt0[BN * D], vt1[BN * D];
+    __shared__ int odd_values;  // a NaN or an infinity was met in a V tile on the causal border
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = lane & 31, half = lane >> 5;
@@ -120,28 +157,28 @@ __global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(Pr
         for (int kk = 0; kk < KK; ++kk) qf[kk] = *reinterpret_cast<const x8 *>(qp + 16 * kk + 8 * half);
     }
 
-    // ---- staging: thread -> pieces (row i * RS + threadIdx.x / P, piece threadIdx.x % P)
-    constexpr int RS = kPrThreads / P;
-    const int sr = threadIdx.x / P, sp = threadIdx.x % P;
-    const T *kp = static_cast<const T *>(a.k) + (k0 + sr) * a.ks + static_cast<int64_t>(kh) * D + 8 * sp;
-    const T *vp = static_cast<const T *>(a.v) + (k0 + sr) * a.vs + static_cast<int64_t>(kh) * D + 8 * sp;
-    at_u32x4 kr[NLD], vr[NLD];
-    const at_u32x4 zero = {0u, 0u, 0u, 0u};
-    auto load_tile = [&](int n0) {
+    // ---- staging: straight from memory into LDS, 64 pieces of 16 bytes per
+    // wave instruction at consecutive places; the lane picks the piece that
+    // belongs there.  The tile's address is in the (scalar) buffer
+    // descriptor, the lane's part a 32-bit offset that stays.  The
+    // descriptor ends with the last visible key's row: nothing behind it is read.
+    const char *kbase = reinterpret_cast<const char *>(static_cast<const T *>(a.k) + k0 * a.ks + static_cast<int64_t>(kh) * D);
+    const char *vbase = reinterpret_cast<const char *>(static_cast<const T *>(a.v) + k0 * a.vs + static_cast<int64_t>(kh) * D);
+    const uint32_t kstep = static_cast<uint32_t>(a.ks) * 2, vstep = static_cast<uint32_t>(a.vs) * 2;
+    uint32_t koff[NLD], voff[NLD];
+#pragma unroll
+    for (int i = 0; i < NLD; ++i) {
+        const uint32_t slot = (i * kPrWaves + wave) * 64 + lane, r = slot / P, p = slot % P;
+        koff[i] = r * kstep + 16 * (p ^ k_swizzle<D>(r));
+        voff[i] = r * vstep + 16 * (p ^ v_swizzle<D>(r));
+    }
+    auto stage = [&](T *kd, T *vd, int n0) {
+        const uint32_t more = any - 1 - n0 < BN - 1 ? any - 1 - n0 : BN - 1;  // rows behind the first
+        const char *kt = kbase + n0 * (a.ks * 2), *vt = vbase + n0 * (a.vs * 2);
 #pragma unroll
         for (int i = 0; i < NLD; ++i) {
-            const int r = n0 + i * RS;
-            const bool in = r + sr < any;  // past the last visible key: zeros
-            kr[i] = in ? *reinterpret_cast<const at_u32x4 *>(kp + r * a.ks) : zero;
-            vr[i] = in ? *reinterpret_cast<const at_u32x4 *>(vp + r * a.vs) : zero;
-        }
-    };
-    auto store_tile = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < NLD; ++i) {
-            const int r = i * RS + sr;
-            *reinterpret_cast<at_u32x4 *>(kt + buf * BN * D + k_place<D>(r, sp)) = kr[i];
-            *reinterpret_cast<at_u32x4 *>(vt + buf * BN * D + v_place<D>(r, sp)) = vr[i];
+            copy_to_lds(kt, more * kstep + 2 * D, koff[i], kd + (i * kPrWaves + wave) * 512);
+            copy_to_lds(vt, more * vstep + 2 * D, voff[i], vd + (i * kPrWaves + wave) * 512);
         }
     };
 
@@ -153,16 +190,11 @@ __global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(Pr
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
     float m = -__builtin_inff(), l = 0.0f;  // m: in units of log2
 
-    if (any > 0) {
-        load_tile(0);
-        store_tile(0);
-    }
-    __syncthreads();
-    int buf = 0;
-    for (int n0 = 0; n0 < any; n0 += BN, buf ^= 1) {
-        const bool more = n0 + BN < any;
-        if (more) load_tile(n0 + BN);
-        const T *kb = kt + buf * BN * D, *vb = vt + buf * BN * D;
+    // One tile: its keys' scores, weights and products, while the next one
+    // arrives.
+    auto step = [&](auto border, const T *kb, const T *vb, T *vmend, T *kn, T *vn, int n0) {
+        constexpr bool BORDER = decltype(border)::value;  // some row does not see some key of the tile
+        if (n0 + BN < any) stage(kn, vn, n0 + BN);
         // ---- S^T
         at_f32x16 s[KT];
 #pragma unroll
@@ -175,7 +207,15 @@ __global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(Pr
                 s[t] = Op16<T>::mfma32(kf, qf[kk], s[t]);
             }
         }
-        if (n0 + BN > all) {
+        // the K reads run ahead of the products
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+        for (int i = 0; i < KT * KK - kAhead; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x8, kAhead, 0);
+        if constexpr (BORDER) {
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -189,9 +229,11 @@ __global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(Pr
 #pragma unroll
             for (int j = 0; j < 16; ++j) top = fmaxf(top, s[t][j]);
         top = lane_pair_max<32>(top) * c;
-        if (__ballot(top > m) != 0) {
+        // The maximum in use may lag by 8 (weights up to 2^8 lose nothing in
+        // either type): few tiles after the first rescale.
+        if (__ballot(top > m + 8.0f) != 0) {
             const float mn = fmaxf(m, top);
-            const float f = m == mn ? 1.0f : exp2f(m - mn);
+            const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
             l *= f;
 #pragma unroll
             for (int i = 0; i < DT; ++i) o[i] *= f;
@@ -207,6 +249,31 @@ __global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(Pr
                 l += e;
                 pf[2 * t + (j >> 3)][j & 7] = static_cast<T>(e);
             }
+        if constexpr (BORDER) {
+            // Keys hidden from some rows: their zero weights would not keep a
+            // NaN or an infinity out of those rows.
+            bool odd = false;
+            for (int i = threadIdx.x; i < BN * P; i += kPrThreads)
+                odd |= has_non_finite<T>(*reinterpret_cast<const at_u32x4 *>(vb + 8 * i));
+            if (odd) odd_values = 1;
+            __syncthreads();
+            if (odd_values != 0) {
+                // such values go to the rows that see them one by one, and zeros into the tile
+                for (int r = 0; r < BN; ++r)
+#pragma unroll
+                    for (int i = 0; i < DT; ++i)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const int d = 32 * i + 8 * (j >> 2) + 4 * half + (j & 3);
+                            const float x = static_cast<float>(vb[v_place<D>(r, d >> 3) + (d & 7)]);
+                            if (n0 + r < seen && !(fabsf(x) <= 3.4028235e38f)) o[i][j] += x;
+                        }
+                __syncthreads();
+                for (int i = threadIdx.x; i < BN * D; i += kPrThreads)
+                    if (!(fabsf(static_cast<float>(vb[i])) <= 3.4028235e38f)) vmend[i] = static_cast<T>(0.0f);
+                __syncthreads();
+            }
+        }
         // ---- O^T += V^T P^T
 #pragma unroll
         for (int u = 0; u < 2 * KT; ++u) {
@@ -223,8 +290,21 @@ __global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(Pr
                 o[i] = Op16<T>::mfma32(__builtin_bit_cast(x8, w), pf[u], o[i]);
             }
         }
-        if (more) store_tile(buf ^ 1);
         __syncthreads();
+    };
+
+    if (threadIdx.x == 0) odd_values = 0;
+    if (any > 0) stage(kt0, vt0, 0);
+    __syncthreads();
+    int n0 = 0;
+    for (; n0 + 2 * BN <= all; n0 += 2 * BN) {
+        step(std::false_type{}, kt0, vt0, vt0, kt1, vt1, n0);
+        step(std::false_type{}, kt1, vt1, vt1, kt0, vt0, n0 + BN);
+    }
+    for (; n0 < any; n0 += 2 * BN) {
+        step(std::true_type{}, kt0, vt0, vt0, kt1, vt1, n0);
+        if (n0 + BN >= any) break;
+        step(std::true_type{}, kt1, vt1, vt1, kt0, vt0, n0 + BN);
     }
     l = lane_pair_sum<32>(l);
     if (row < rows) {
@@ -242,15 +322,9 @@ __global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(Pr
 template <typename T, int D>
 hipError_t prompt_launch(const PromptArgs &a, hipStream_t s)
 {
-    static std::atomic<uint64_t> lds_done{0};
-    constexpr int BN = D == 256 ? 32 : 64;
-    constexpr int lds = 4 * BN * D * 2;
-    const auto kernel = k_attn_prompt<T, D>;
-    const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(kernel), lds, lds_done);
-    if (e != hipSuccess) return e;
     const int64_t tiles = (a.max_q * (a.hq / a.hkv) + kPrRows - 1) / kPrRows;
-    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(tiles * a.batch * a.hkv)), dim3(kPrThreads), lds, s, a,
-                       static_cast<int32_t>(tiles));
+    hipLaunchKernelGGL((k_attn_prompt<T, D>), dim3(static_cast<uint32_t>(tiles * a.batch * a.hkv)), dim3(kPrThreads), 0, s,
+                       a, static_cast<int32_t>(tiles));
     return hipGetLastError();
 }
 
