@@ -437,7 +437,7 @@ typedef struct ptq1_kv_cache {
  *              16-byte aligned, overlapping neither inputs nor the cache.
  * Values are rounded once, to nearest even, to the cache's and q_out's types.
  * Errors: NULL, SHAPE, ALIGN, ALIAS, OVERFLOW, UNSUPPORTED (types, head_dim,
- * page_size, more than 2^24 tokens or 2^31 rows). */
+ * page_size, more than 2^24 tokens or 2^25 rows of heads). */
 ptq1_status ptq1_kv_write(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                           int64_t v_stride, int32_t src_dtype, int64_t n_tokens, int32_t n_q_heads,
                           const int32_t *positions, const float *cos_sin, int64_t n_positions, int32_t rot_dim,
@@ -513,7 +513,8 @@ ptq1_status ptq1_attn_decode(const void *q, int32_t q_dtype, int64_t batch, int3
  * bf16 or fp16 matrix cores, fp32 scores, maxima, sums and accumulators; the
  * weights enter the second product rounded to dtype, the sum is over fp32.
  * Errors: NULL, SHAPE, ALIGN, ALIAS, OVERFLOW, WORKSPACE, UNSUPPORTED (types,
- * head_dim, sizes past 2^31 - 1 rows of one kv head). */
+ * head_dim, more than 2^31 - 1025 rows of one kv head or 2^24 - 1 tiles of 128
+ * query rows, k_stride or v_stride above 2^24). */
 size_t ptq1_attn_prompt_workspace_bytes(int64_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                                         int64_t max_q, int64_t max_k);
 ptq1_status ptq1_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,

@@ -1086,6 +1086,9 @@ ptq1_status check_device_array(const void *p, const char *name, int64_t bytes, u
 
 constexpr int64_t kMaxRows32 = 2147483647;
 constexpr int32_t kMaxHeads = 65536;
+constexpr int64_t kMaxWriteRows = int64_t{1} << 25;      // four rows of 256 elements a workgroup
+constexpr int64_t kMaxStride = int64_t{1} << 24;         // 64 rows of K or V within 32-bit offsets
+constexpr int64_t kMaxBlocks256 = (int64_t{1} << 24) - 1;  // a grid's threads fit 32 bits
 
 // The byte sizes of a cache's arrays, after every check of it.
 struct KvBytes {
@@ -1194,8 +1197,8 @@ ptq1_status ptq1_kv_write(const void *q, int64_t q_stride, const void *k, int64_
         return fail(PTQ1_ERR_UNSUPPORTED, "n_tokens = %lld > 2^24", (long long)n_tokens);
     if (n_q_heads < 0 || n_q_heads > kMaxHeads)
         return fail(PTQ1_ERR_SHAPE, "n_q_heads = %d (0 to %d)", n_q_heads, kMaxHeads);
-    if (n_tokens * (n_q_heads + 2 * static_cast<int64_t>(cache->n_kv_heads)) > kMaxRows32)
-        return fail(PTQ1_ERR_UNSUPPORTED, "n_tokens * heads above 2^31 - 1");
+    if (n_tokens * (n_q_heads + 2 * static_cast<int64_t>(cache->n_kv_heads)) > kMaxWriteRows)
+        return fail(PTQ1_ERR_UNSUPPORTED, "n_tokens * heads above 2^25");
     if (!float_type(src_dtype)) return fail(PTQ1_ERR_UNSUPPORTED, "src_dtype %d (F32, F16 or BF16)", src_dtype);
     if (!float_type(q_dtype)) return fail(PTQ1_ERR_UNSUPPORTED, "q_dtype %d (F32, F16 or BF16)", q_dtype);
     if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 8 != 0)
@@ -1244,6 +1247,8 @@ ptq1_status ptq1_kv_read(const ptq1_kv_cache *cache, const int32_t *block_table,
     if (max_pages < 0) return fail(PTQ1_ERR_SHAPE, "max_pages = %lld is negative", (long long)max_pages);
     if (n_rows < 0) return fail(PTQ1_ERR_SHAPE, "n_rows = %lld is negative", (long long)n_rows);
     if (n_rows > kMaxRows32) return fail(PTQ1_ERR_UNSUPPORTED, "n_rows = %lld > 2^31 - 1", (long long)n_rows);
+    if (n_rows > kMaxBlocks256 * 32)
+        return fail(PTQ1_ERR_UNSUPPORTED, "n_rows = %lld too large", (long long)n_rows);
     if (batch > kMaxGridY || batch * cache->n_kv_heads > kMaxGridY)
         return fail(PTQ1_ERR_UNSUPPORTED, "batch * n_kv_heads > %lld", (long long)kMaxGridY);
     if (!float_type(out_dtype)) return fail(PTQ1_ERR_UNSUPPORTED, "out_dtype %d (F32, F16 or BF16)", out_dtype);
@@ -1349,11 +1354,12 @@ ptq1_status ptq1_attn_prompt(const void *q, int64_t q_stride, const void *k, int
     if (max_k > n_k_rows) max_k = n_k_rows;
     const int64_t group = n_q_heads / n_kv_heads;
     if (batch > kMaxRows32 || n_q_rows > kMaxRows32 || n_k_rows > kMaxRows32 - 1024 ||
-        max_q * group > kMaxRows32 - 1024)
+        n_q_rows * group > kMaxRows32 - 1024)
         return fail(PTQ1_ERR_UNSUPPORTED, "more than 2^31 - 1025 rows of one kv head");
-    int64_t blocks;
-    if (!mul_ok((max_q * group + 127) / 128, batch * n_kv_heads, &blocks) || blocks > kMaxGridX)
-        return fail(PTQ1_ERR_UNSUPPORTED, "max_q * batch * heads too large");
+    if (k_stride > kMaxStride || v_stride > kMaxStride)
+        return fail(PTQ1_ERR_UNSUPPORTED, "k_stride or v_stride above 2^24 elements");
+    if (ptq1::prompt_tiles(batch, n_q_rows, n_q_heads, n_kv_heads) * n_kv_heads > kMaxBlocks256)
+        return fail(PTQ1_ERR_UNSUPPORTED, "more than 2^24 - 1 tiles of 128 query rows");
     if (batch == 0 || n_q_rows == 0 || max_q == 0) return ok();
     int64_t qb, kbytes, vbytes;
     const int64_t d = head_dim;

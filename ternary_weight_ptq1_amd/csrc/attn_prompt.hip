@@ -74,22 +74,24 @@ __device__ __forceinline__ void copy_to_lds(const char *base, uint32_t bytes, ui
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)dst, 16, static_cast<int>(off), 0, 0, 0);
 }
 
-// One of the eight values has an exponent of all ones.
+// Zeros in the place of NaNs and infinities (an exponent of all ones) among
+// eight values; true if there was one.
 template <typename T>
-__device__ __forceinline__ bool has_non_finite(at_u32x4 w)
+__device__ __forceinline__ bool clear_non_finite(at_u32x4 &w)
 {
-    constexpr uint32_t E = std::is_same<T, __bf16>::value ? 0x7f807f80u : 0x7c007c00u;
-    uint32_t any = 0;
+    constexpr uint32_t E = std::is_same<T, __bf16>::value ? 0x7f80u : 0x7c00u;
+    bool found = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t x = (w[i] & E) ^ E;  // a zero half: all ones
-        any |= (x - 0x00010001u) & ~x & 0x80008000u;
+        const bool lo = (w[i] & E) == E, hi = (w[i] & (E << 16)) == (E << 16);
+        w[i] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
+        found |= lo || hi;
     }
-    return any != 0;
+    return found;
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kPrThreads, 2) k_attn_prompt(PromptArgs a, int32_t tiles)
+__global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(PromptArgs a)
 {
     typedef typename Op16<T>::x8 x8;
     constexpr int BN = prompt_keys(D);      // keys of a tile
@@ -107,23 +109,27 @@ __global__ void __launch_bounds__(kPrThreads, 2) k_attn_prompt(PromptArgs a, int
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = lane & 31, half = lane >> 5;
 
-    const int64_t pairs = a.batch * a.hkv;
-    const int64_t pair = static_cast<int64_t>(blockIdx.x) % pairs;
-    const int64_t b = pair / a.hkv;
-    const int kh = static_cast<int>(pair % a.hkv);
+    // Workgroups go to the eight XCDs in turn, each with an L2 of its own.
+    // Heads vary fastest, so that a head's tiles meet on as few XCDs as its
+    // number allows (eight heads: one each).
     const int group = a.hq / a.hkv;
+    const int kh = static_cast<int>(blockIdx.x % static_cast<uint32_t>(a.hkv));
+    int64_t b, at;
+    if (!find_tile(blockIdx.x / static_cast<uint32_t>(a.hkv), a.batch,
+                   [&](int64_t i) {
+                       // the sequence's rows that exist
+                       const int64_t first = a.cu_q[i], end = a.cu_q[i + 1];
+                       const int64_t n = (end < a.q_rows ? end : a.q_rows) - (first > 0 ? first : 0);
+                       return n > 0 ? (n * group + kPrRows - 1) / kPrRows : 0;
+                   },
+                   b, at))
+        return;
     const int64_t q0 = a.cu_q[b], k0 = a.cu_k[b];
     const int64_t lq = a.cu_q[b + 1] - q0, lk = a.cu_k[b + 1] - k0;
-    if (lq <= 0) return;
     const int64_t rows = lq * group;
-    const bool bad = q0 < 0 || k0 < 0 || q0 + lq > a.q_rows || lk < 0 || k0 + lk > a.k_rows || lq > a.max_q ||
-                     lk > a.max_k;
-    if (bad) {
-        for (int64_t r = static_cast<int64_t>(blockIdx.x) / pairs * kPrRows + threadIdx.x; r < rows;
-             r += static_cast<int64_t>(tiles) * kPrRows) {
-            if (threadIdx.x >= kPrRows) break;
-            const int64_t tok = q0 + r / group;
-            if (tok < 0 || tok >= a.q_rows) continue;
+    if (q0 < 0 || k0 < 0 || q0 + lq > a.q_rows || lk < 0 || k0 + lk > a.k_rows || lq > a.max_q || lk > a.max_k) {
+        const int64_t r = (q0 < 0 ? -q0 * group : 0) + at * kPrRows + threadIdx.x, tok = q0 + r / group;
+        if (threadIdx.x < kPrRows && r < rows && tok < a.q_rows) {
             T *dst = static_cast<T *>(a.out) + (tok * a.hq + kh * group + r % group) * D;
             const float n = __builtin_nanf("");
             for (int e = 0; e < D; e += 4) store4(dst + e, at_f32x4{n, n, n, n});
@@ -131,9 +137,7 @@ __global__ void __launch_bounds__(kPrThreads, 2) k_attn_prompt(PromptArgs a, int
         return;
     }
     // the last rows see the most keys: they start first
-    const int64_t nt = (rows + kPrRows - 1) / kPrRows;
-    const int64_t tile = nt - 1 - static_cast<int64_t>(blockIdx.x) / pairs;
-    if (tile < 0) return;
+    const int64_t tile = (rows + kPrRows - 1) / kPrRows - 1 - at;
 
     const int64_t row = tile * kPrRows + 32 * wave + col;
     const int64_t rowc = row < rows ? row : rows - 1;
@@ -165,21 +169,29 @@ __global__ void __launch_bounds__(kPrThreads, 2) k_attn_prompt(PromptArgs a, int
     const char *kbase = reinterpret_cast<const char *>(static_cast<const T *>(a.k) + k0 * a.ks + static_cast<int64_t>(kh) * D);
     const char *vbase = reinterpret_cast<const char *>(static_cast<const T *>(a.v) + k0 * a.vs + static_cast<int64_t>(kh) * D);
     const uint32_t kstep = static_cast<uint32_t>(a.ks) * 2, vstep = static_cast<uint32_t>(a.vs) * 2;
-    uint32_t koff[NLD], voff[NLD];
+    // piece i of a lane: rows i * RS further on, where the swizzle is the
+    // same again after KC pieces
+    constexpr int RS = kPrThreads / P, KC = D == 256 ? 2 : 1;
+    uint32_t koff[KC], voff;
 #pragma unroll
-    for (int i = 0; i < NLD; ++i) {
-        const uint32_t slot = (i * kPrWaves + wave) * 64 + lane, r = slot / P, p = slot % P;
+    for (int i = 0; i < KC; ++i) {
+        const uint32_t r = i * RS + threadIdx.x / P, p = threadIdx.x % P;
         koff[i] = r * kstep + 16 * (p ^ k_swizzle<D>(r));
-        voff[i] = r * vstep + 16 * (p ^ v_swizzle<D>(r));
+        if (i == 0) voff = r * vstep + 16 * (p ^ v_swizzle<D>(r));
     }
-    auto stage = [&](T *kd, T *vd, int n0) {
+    auto stage_k = [&](T *dst, int n0) {
         const uint32_t more = any - 1 - n0 < BN - 1 ? any - 1 - n0 : BN - 1;  // rows behind the first
-        const char *kt = kbase + n0 * (a.ks * 2), *vt = vbase + n0 * (a.vs * 2);
+        const char *src = kbase + n0 * (a.ks * 2);
 #pragma unroll
-        for (int i = 0; i < NLD; ++i) {
-            copy_to_lds(kt, more * kstep + 2 * D, koff[i], kd + (i * kPrWaves + wave) * 512);
-            copy_to_lds(vt, more * vstep + 2 * D, voff[i], vd + (i * kPrWaves + wave) * 512);
-        }
+        for (int i = 0; i < NLD; ++i)
+            copy_to_lds(src, more * kstep + 2 * D, koff[i % KC] + (i / KC * KC * RS) * kstep, dst + (i * kPrWaves + wave) * 512);
+    };
+    auto stage_v = [&](T *dst, int n0) {
+        const uint32_t more = any - 1 - n0 < BN - 1 ? any - 1 - n0 : BN - 1;
+        const char *src = vbase + n0 * (a.vs * 2);
+#pragma unroll
+        for (int i = 0; i < NLD; ++i)
+            copy_to_lds(src, more * vstep + 2 * D, voff + (i * RS) * vstep, dst + (i * kPrWaves + wave) * 512);
     };
 
     const float c = a.scale * kLog2e;
@@ -190,13 +202,8 @@ __global__ void __launch_bounds__(kPrThreads, 2) k_attn_prompt(PromptArgs a, int
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
     float m = -__builtin_inff(), l = 0.0f;  // m: in units of log2
 
-    // One tile: its keys' scores, weights and products, while the next one
-    // arrives.
-    auto step = [&](auto border, const T *kb, const T *vb, T *vmend, T *kn, T *vn, int n0) {
-        constexpr bool BORDER = decltype(border)::value;  // some row does not see some key of the tile
-        if (n0 + BN < any) stage(kn, vn, n0 + BN);
-        // ---- S^T
-        at_f32x16 s[KT];
+    // S^T of the tile in kb
+    auto scores = [&](at_f32x16 (&s)[KT], const T *kb) {
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
 #pragma unroll
@@ -207,30 +214,25 @@ __global__ void __launch_bounds__(kPrThreads, 2) k_attn_prompt(PromptArgs a, int
                 s[t] = Op16<T>::mfma32(kf, qf[kk], s[t]);
             }
         }
-        // the K reads run ahead of the products
-        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+    };
+    auto hide = [&](at_f32x16 (&s)[KT], int n0) {
 #pragma unroll
-        for (int i = 0; i < KT * KK - kAhead; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x8, kAhead, 0);
-        if constexpr (BORDER) {
+        for (int t = 0; t < KT; ++t)
 #pragma unroll
-            for (int t = 0; t < KT; ++t)
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (n0 + 32 * t + 8 * (j >> 2) + 4 * half + (j & 3) >= seen) s[t][j] = -__builtin_inff();
-        }
-        // ---- softmax
+            for (int j = 0; j < 16; ++j)
+                if (n0 + 32 * t + 8 * (j >> 2) + 4 * half + (j & 3) >= seen) s[t][j] = -__builtin_inff();
+    };
+    auto largest = [&](const at_f32x16 (&s)[KT]) {
         float top = s[0][0];
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int j = 0; j < 16; ++j) top = fmaxf(top, s[t][j]);
-        top = lane_pair_max<32>(top) * c;
-        // The maximum in use may lag by 8 (weights up to 2^8 lose nothing in
-        // either type): few tiles after the first rescale.
+        return lane_pair_max<32>(top) * c;
+    };
+    // The maximum in use may lag by 8 (weights up to 2^8 lose nothing in
+    // either type): few tiles after the first rescale.
+    auto raise = [&](float top) {
         if (__ballot(top > m + 8.0f) != 0) {
             const float mn = fmaxf(m, top);
             const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
@@ -239,6 +241,28 @@ __global__ void __launch_bounds__(kPrThreads, 2) k_attn_prompt(PromptArgs a, int
             for (int i = 0; i < DT; ++i) o[i] *= f;
             m = mn;
         }
+    };
+
+    // One tile: its scores, weights and products, while the next one arrives
+    // in the other buffers.
+    auto step = [&](auto border, const T *kb, T *vb, T *kn, T *vn, int n0) {
+        constexpr bool BORDER = decltype(border)::value;  // some row may not see some key of the tile
+        if (n0 + BN < any) {
+            stage_k(kn, n0 + BN);
+            stage_v(vn, n0 + BN);
+        }
+        at_f32x16 s[KT];
+        scores(s, kb);
+        // the K reads run ahead of the products
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+        for (int i = 0; i < KT * KK - kAhead; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x8, kAhead, 0);
+        if constexpr (BORDER) hide(s, n0);
+        raise(largest(s));
         const float ms = m == -__builtin_inff() ? 0.0f : m;
         x8 pf[2 * KT];
 #pragma unroll
@@ -250,29 +274,19 @@ __global__ void __launch_bounds__(kPrThreads, 2) k_attn_prompt(PromptArgs a, int
                 pf[2 * t + (j >> 3)][j & 7] = static_cast<T>(e);
             }
         if constexpr (BORDER) {
-            // Keys hidden from some rows: their zero weights would not keep a
-            // NaN or an infinity out of those rows.
+            // Some rows do not see some of these keys, and a zero weight would
+            // not keep a NaN or an infinity out of them: such values leave the
+            // tile and are given to the rows that see them at the end.
             bool odd = false;
-            for (int i = threadIdx.x; i < BN * P; i += kPrThreads)
-                odd |= has_non_finite<T>(*reinterpret_cast<const at_u32x4 *>(vb + 8 * i));
+            for (int i = threadIdx.x; i < BN * P; i += kPrThreads) {
+                at_u32x4 w = *reinterpret_cast<const at_u32x4 *>(vb + 8 * i);
+                if (clear_non_finite<T>(w)) {
+                    *reinterpret_cast<at_u32x4 *>(vb + 8 * i) = w;
+                    odd = true;
+                }
+            }
             if (odd) odd_values = 1;
             __syncthreads();
-            if (odd_values != 0) {
-                // such values go to the rows that see them one by one, and zeros into the tile
-                for (int r = 0; r < BN; ++r)
-#pragma unroll
-                    for (int i = 0; i < DT; ++i)
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const int d = 32 * i + 8 * (j >> 2) + 4 * half + (j & 3);
-                            const float x = static_cast<float>(vb[v_place<D>(r, d >> 3) + (d & 7)]);
-                            if (n0 + r < seen && !(fabsf(x) <= 3.4028235e38f)) o[i][j] += x;
-                        }
-                __syncthreads();
-                for (int i = threadIdx.x; i < BN * D; i += kPrThreads)
-                    if (!(fabsf(static_cast<float>(vb[i])) <= 3.4028235e38f)) vmend[i] = static_cast<T>(0.0f);
-                __syncthreads();
-            }
         }
         // ---- O^T += V^T P^T
 #pragma unroll
@@ -282,10 +296,10 @@ __global__ void __launch_bounds__(kPrThreads, 2) k_attn_prompt(PromptArgs a, int
                 // lane: key 16 u + 4 half + (lane % 16) / 4 (then + 8), dimensions 32 i + 16 ((lane / 16) % 2) + 4 (lane % 4)
                 const int r = 16 * u + 4 * half + ((lane & 15) >> 2);
                 const int d = 32 * i + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-                const at_s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (lds_s16x4 *)(vb + v_place<D>(r, d >> 3) + (d & 7)));
-                const at_s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (lds_s16x4 *)(vb + v_place<D>(r + 8, d >> 3) + (d & 7)));
+                const at_s16x4 lo =
+                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + v_place<D>(r, d >> 3) + (d & 7)));
+                const at_s16x4 hi =
+                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + v_place<D>(r + 8, d >> 3) + (d & 7)));
                 const auto w = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
                 o[i] = Op16<T>::mfma32(__builtin_bit_cast(x8, w), pf[u], o[i]);
             }
@@ -294,37 +308,56 @@ __global__ void __launch_bounds__(kPrThreads, 2) k_attn_prompt(PromptArgs a, int
     };
 
     if (threadIdx.x == 0) odd_values = 0;
-    if (any > 0) stage(kt0, vt0, 0);
+    if (any > 0) {
+        stage_k(kt0, 0);
+        stage_v(vt0, 0);
+    }
     __syncthreads();
     int n0 = 0;
     for (; n0 + 2 * BN <= all; n0 += 2 * BN) {
-        step(std::false_type{}, kt0, vt0, vt0, kt1, vt1, n0);
-        step(std::false_type{}, kt1, vt1, vt1, kt0, vt0, n0 + BN);
+        step(std::false_type{}, kt0, vt0, kt1, vt1, n0);
+        step(std::false_type{}, kt1, vt1, kt0, vt0, n0 + BN);
     }
+    const int border = n0;
     for (; n0 < any; n0 += 2 * BN) {
-        step(std::true_type{}, kt0, vt0, vt0, kt1, vt1, n0);
+        step(std::true_type{}, kt0, vt0, kt1, vt1, n0);
         if (n0 + BN >= any) break;
-        step(std::true_type{}, kt1, vt1, vt1, kt0, vt0, n0 + BN);
+        step(std::true_type{}, kt1, vt1, kt0, vt0, n0 + BN);
     }
     l = lane_pair_sum<32>(l);
+    const float f = seen == 0 ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int i = 0; i < DT; ++i) o[i] *= f;
+    if (any > 0 && odd_values != 0) {
+        for (int r = border; r < any; ++r) {
+            const T *src = static_cast<const T *>(a.v) + (k0 + r) * a.vs + static_cast<int64_t>(kh) * D + 4 * half;
+#pragma unroll
+            for (int i = 0; i < DT; ++i)
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const at_f32x4 x = load4(src + 32 * i + 2 * j);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (r < seen && !(fabsf(x[e]) <= 3.4028235e38f)) o[i][j + e] += x[e];
+                }
+        }
+    }
     if (row < rows) {
-        const float f = seen == 0 ? 0.0f : 1.0f / l;
         T *dst = static_cast<T *>(a.out) + ((q0 + tok) * a.hq + kh * group + head) * D;
 #pragma unroll
         for (int i = 0; i < DT; ++i)
 #pragma unroll
             for (int j = 0; j < 16; j += 4)
                 store4(dst + 32 * i + 2 * j + 4 * half,
-                       at_f32x4{o[i][j] * f, o[i][j + 1] * f, o[i][j + 2] * f, o[i][j + 3] * f});
+                       at_f32x4{o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]});
     }
 }
 
 template <typename T, int D>
 hipError_t prompt_launch(const PromptArgs &a, hipStream_t s)
 {
-    const int64_t tiles = (a.max_q * (a.hq / a.hkv) + kPrRows - 1) / kPrRows;
-    hipLaunchKernelGGL((k_attn_prompt<T, D>), dim3(static_cast<uint32_t>(tiles * a.batch * a.hkv)), dim3(kPrThreads), 0, s,
-                       a, static_cast<int32_t>(tiles));
+    hipLaunchKernelGGL((k_attn_prompt<T, D>), dim3(static_cast<uint32_t>(prompt_tiles(a.batch, a.q_rows, a.hq, a.hkv) * a.hkv)),
+                       dim3(kPrThreads), 0, s, a);
     return hipGetLastError();
 }
 
@@ -335,6 +368,12 @@ hipError_t prompt_d(const PromptArgs &a, int d, hipStream_t s)
 }
 
 }  // namespace
+
+// Whole tiles of all rows, and a part of one for every sequence.
+int64_t prompt_tiles(int64_t batch, int64_t q_rows, int32_t hq, int32_t hkv)
+{
+    return q_rows * (hq / hkv) / kPrRows + batch;
+}
 
 size_t prompt_part_floats(int64_t, int32_t, int32_t, int32_t, int64_t, int64_t) { return 0; }
 

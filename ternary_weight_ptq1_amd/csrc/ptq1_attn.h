@@ -101,4 +101,37 @@ __device__ __forceinline__ void store4(_Float16 *p, at_f32x4 v)
     *reinterpret_cast<f16x4 *>(p) = __builtin_convertvector(v, f16x4);
 }
 
+// The place of flat tile `flat` among the tiles of `batch` sequences, of which
+// sequence i has tiles_of(i): dense, 64 sequences at a time with the longest
+// of them first (the most expensive tiles start earliest, and none of the
+// workgroups that share the engines in turn is empty).  Every lane of a wave
+// takes part and gets the answer; false: there are fewer tiles.
+template <class F>
+__device__ __forceinline__ bool find_tile(int64_t flat, int64_t batch, F tiles_of, int64_t &seq, int64_t &tile)
+{
+    const int lane = threadIdx.x & 63;
+    for (int64_t base = 0; base < batch; base += 64) {
+        const int n = static_cast<int>(batch - base < 64 ? batch - base : 64);
+        // at most 2^31 - 1 tiles in all (the grid's limit)
+        const int mine = lane < n ? static_cast<int>(tiles_of(base + lane)) : 0;
+        int before = 0, total = 0;
+        for (int j = 0; j < n; ++j) {
+            const int other = __builtin_amdgcn_readlane(mine, j);
+            total += other;
+            if (other > mine || (other == mine && j < lane)) before += other;
+        }
+        if (flat >= total) {
+            flat -= total;
+            continue;
+        }
+        const int at = static_cast<int>(flat);
+        const uint64_t hit = __ballot(lane < n && at >= before && at - before < mine);
+        const int who = __builtin_ctzll(hit);
+        seq = base + who;
+        tile = at - __builtin_amdgcn_readlane(before, who);
+        return true;
+    }
+    return false;
+}
+
 }  // namespace ptq1

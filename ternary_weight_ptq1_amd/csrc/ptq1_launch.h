@@ -176,6 +176,8 @@ struct PromptArgs {
     void *out;
 };
 hipError_t launch_attn_prompt(const PromptArgs &a, int dtype, int32_t d, float *part, hipStream_t s);
+// tiles of 128 query rows that one kv head's rows may make up
+int64_t prompt_tiles(int64_t batch, int64_t q_rows, int32_t hq, int32_t hkv);
 size_t prompt_part_floats(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_t max_q, int64_t max_k);
 
 }  // namespace ptq1
