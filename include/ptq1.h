@@ -512,11 +512,15 @@ ptq1_status ptq1_attn_decode(const void *q, int32_t q_dtype, int64_t batch, int3
  *   scale  positive and finite.
  * bf16 or fp16 matrix cores, fp32 scores, maxima, sums and accumulators; the
  * weights enter the second product rounded to dtype, the sum is over fp32.
+ * Where the query rows alone would not fill the GPU, the keys are cut into
+ * chunks that run side by side and are joined by a second launch, in a fixed
+ * order; the workspace (for max_k as given, or n_k_rows if that is less) holds
+ * their parts.
  * Errors: NULL, SHAPE, ALIGN, ALIAS, OVERFLOW, WORKSPACE, UNSUPPORTED (types,
  * head_dim, more than 2^31 - 1025 rows of one kv head or 2^24 - 1 tiles of 128
  * query rows, k_stride or v_stride above 2^24). */
-size_t ptq1_attn_prompt_workspace_bytes(int64_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
-                                        int64_t max_q, int64_t max_k);
+size_t ptq1_attn_prompt_workspace_bytes(int64_t batch, int64_t n_q_rows, int64_t max_k, int32_t n_q_heads,
+                                        int32_t n_kv_heads, int32_t head_dim);
 ptq1_status ptq1_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                              int64_t v_stride, int32_t dtype, const int32_t *cu_q, const int32_t *cu_k,
                              int64_t batch, int64_t n_q_rows, int64_t n_k_rows, int64_t max_q, int64_t max_k,

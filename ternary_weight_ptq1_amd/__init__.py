@@ -87,7 +87,7 @@ _SIGS = {
     "ptq1_kv_read": ([p, p, i64, p, i64, i64, p, p, C.c_int32, p], C.c_int),
     "ptq1_attn_decode_workspace_bytes": ([i64, C.c_int32, C.c_int32, C.c_int32, i64], sz),
     "ptq1_attn_decode": ([p, C.c_int32, i64, C.c_int32, p, p, i64, p, i64, C.c_float, p, p, sz, p], C.c_int),
-    "ptq1_attn_prompt_workspace_bytes": ([i64, C.c_int32, C.c_int32, C.c_int32, i64, i64], sz),
+    "ptq1_attn_prompt_workspace_bytes": ([i64, i64, i64, C.c_int32, C.c_int32, C.c_int32], sz),
     "ptq1_attn_prompt": ([p, i64, p, i64, p, i64, C.c_int32, p, p, i64, i64, i64, i64, i64, C.c_int32, C.c_int32,
                           C.c_int32, C.c_int32, C.c_float, p, p, sz, p], C.c_int),
     "ptq1_profile_arm": ([C.c_char_p, p, p, C.c_int32], C.c_int),
@@ -776,7 +776,8 @@ def ptq1_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     (fp16 or bf16; rows may lie apart), sequence b's rows cu_q[b] .. cu_q[b + 1] and cu_k[b] .. cu_k[b + 1] (int32
     [batch + 1]).  causal: the last query of a sequence sees its last key.  max_q, max_k: bounds on the sequences'
     query and key counts (all rows by default).  scale: 1 / sqrt(head_dim) by default.  ws: optional scratch of at
-    least workspace_bytes("attn_prompt", batch, n_q_heads, n_kv_heads, head_dim, max_q, max_k) bytes."""
+    least workspace_bytes("attn_prompt", batch, n_q_rows, min(max_k, n_k_rows), n_q_heads, n_kv_heads, head_dim)
+    bytes."""
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     dv = q.device
@@ -794,7 +795,7 @@ def ptq1_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     max_k = nk if max_k is None else min(max_k, nk)
     on = _On(dv, stream)
     try:
-        need = lib().ptq1_attn_prompt_workspace_bytes(batch, hq, hkv, d, max_q, max_k)
+        need = lib().ptq1_attn_prompt_workspace_bytes(batch, nq, max_k, hq, hkv, d)
         mine = ws is None and need > 0
         ws, wsb = _ws(need, dv, ws)
         fresh = None

@@ -1327,14 +1327,14 @@ ptq1_status ptq1_attn_decode(const void *q, int32_t q_dtype, int64_t batch, int3
                       "ptq1_attn_decode");
 }
 
-size_t ptq1_attn_prompt_workspace_bytes(int64_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
-                                        int64_t max_q, int64_t max_k)
+size_t ptq1_attn_prompt_workspace_bytes(int64_t batch, int64_t n_q_rows, int64_t max_k, int32_t n_q_heads,
+                                        int32_t n_kv_heads, int32_t head_dim)
 {
     if (batch < 0 || batch > kMaxRows32 || n_kv_heads < 1 || n_kv_heads > 1024 || n_q_heads < 1 ||
         n_q_heads > kMaxHeads || n_q_heads % n_kv_heads != 0 || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
-        max_q < 0 || max_k < 0 || max_q > kMaxRows32 || max_k > kMaxRows32)
+        n_q_rows < 0 || max_k < 0 || n_q_rows > kMaxRows32 || max_k > kMaxRows32)
         return 0;
-    return round_up(ptq1::prompt_part_floats(batch, n_q_heads, n_kv_heads, head_dim, max_q, max_k) * 4, kWsAlign);
+    return round_up(ptq1::prompt_plan(batch, n_q_rows, max_k, n_q_heads, n_kv_heads, head_dim).part_floats * 4, kWsAlign);
 }
 
 ptq1_status ptq1_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -1374,8 +1374,8 @@ ptq1_status ptq1_attn_prompt(const void *q, int64_t q_stride, const void *k, int
         return fail(PTQ1_ERR_ALIAS, "out overlaps q, k or v");
     if (overlaps(out, ob, cu_q, (batch + 1) * 4) || overlaps(out, ob, cu_k, (batch + 1) * 4))
         return fail(PTQ1_ERR_ALIAS, "out overlaps cu_q or cu_k");
-    const size_t need =
-        round_up(ptq1::prompt_part_floats(batch, n_q_heads, n_kv_heads, head_dim, max_q, max_k) * 4, kWsAlign);
+    const ptq1::PromptPlan plan = ptq1::prompt_plan(batch, n_q_rows, max_k, n_q_heads, n_kv_heads, head_dim);
+    const size_t need = round_up(plan.part_floats * 4, kWsAlign);
     PTQ1_TRY(check_ws(ws, ws_bytes, need, "ptq1_attn_prompt"));
     const int64_t wn = static_cast<int64_t>(need);
     if (overlaps(ws, wn, q, qb) || overlaps(ws, wn, k, kbytes) || overlaps(ws, wn, v, vbytes) ||
@@ -1383,7 +1383,7 @@ ptq1_status ptq1_attn_prompt(const void *q, int64_t q_stride, const void *k, int
         return fail(PTQ1_ERR_ALIAS, "ws overlaps an argument");
     const ptq1::PromptArgs a{q,      k,        v,        q_stride, k_stride, v_stride, cu_q,       cu_k,   batch,
                              n_q_rows, n_k_rows, max_q,  max_k,    n_q_heads, n_kv_heads, causal != 0, scale, out};
-    return hip_status(ptq1::launch_attn_prompt(a, dtype, head_dim, static_cast<float *>(ws), stream), "ptq1_attn_prompt");
+    return hip_status(ptq1::launch_attn_prompt(a, dtype, head_dim, plan, static_cast<float *>(ws), stream), "ptq1_attn_prompt");
 }
 
 }  // extern "C"

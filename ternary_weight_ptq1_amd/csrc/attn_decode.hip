@@ -39,8 +39,8 @@ namespace {
 constexpr int kDecWaves = 4;
 constexpr int kDecThreads = 64 * kDecWaves;
 constexpr int kDecHeads = 16;       // query heads per workgroup (MFMA columns)
-constexpr int kMaxChunks = 1024;    // chunks of one sequence (the join's LDS)
-constexpr int64_t kMaxChunk = 4096; // tokens (page indices of a chunk in LDS: 256 pages of 16)
+constexpr int kStep = 256;          // tokens of one step of the work split (one page or several)
+constexpr int kMaxShares = 512;     // a sequence's pieces are twice that at most (the join's LDS)
 
 struct DecodeArgs {
     const void *q;
@@ -52,11 +52,42 @@ struct DecodeArgs {
     const int32_t *table;
     int64_t max_pages;
     const int32_t *lens;
-    int64_t max_len, chunk, chunks;
+    int64_t batch, max_len;
+    int32_t shares;  // workgroups that the GPU holds for one kv head (for 16 query heads of it)
+    int32_t cut;     // some sequence may have more than one step
     float scale;
     void *out;
     float *part_rows, *part_ml;
 };
+
+// Steps of a sequence: one at least (an empty or refused one has its rows
+// written too).  All sequences' together are below 2^30 (2^16 times 2^14).
+__device__ __forceinline__ int decode_steps(const DecodeArgs &a, int64_t b)
+{
+    const int len = a.lens[b];
+    return len <= 0 || len > a.max_len ? 1 : (len + kStep - 1) / kStep;
+}
+
+// Steps of the sequences before `end`.
+__device__ __forceinline__ int steps_before(const DecodeArgs &a, int64_t end)
+{
+    int sum = 0;
+    for (int64_t i = threadIdx.x & 63; i < end; i += 64) sum += decode_steps(a, i);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
+    return __builtin_amdgcn_readfirstlane(sum);
+}
+
+// Steps of one workgroup's piece of a sequence.  Few sequences: pieces that
+// fill the GPU once.  Many: half of that, since their ends leave the pieces
+// unequal (64 sequences of 3 to 8190 tokens: 62 us with 512 tokens a piece,
+// 71 with 256, 75 with 2048; one of 131071 over int8: 64 us in one round of
+// 2048, 75 in two).
+__device__ __forceinline__ int steps_per_piece(const DecodeArgs &a, int total)
+{
+    const int want = a.batch * 2 <= a.shares ? a.shares : 2 * a.shares;
+    return (total + want - 1) / want;
+}
 
 // MFMA operand type of a cache type
 template <typename C>
@@ -65,7 +96,7 @@ struct OpOf {
 };
 template <>
 struct OpOf<int8_t> {
-    typedef __bf16 type;
+    typedef _Float16 type;
 };
 
 // The n-th 16-bit term of x: x = hi + mid + lo with each term the rounding
@@ -88,20 +119,34 @@ __device__ __forceinline__ void split_terms(const float (&x)[8], typename Op16<T
     }
 }
 
-// 8 int8 codes (two dwords) as bf16: exact.
-__device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t a, uint32_t b)
+// 8 int8 codes (two dwords) as fp16, exact: the byte code + 128 put into the
+// mantissa of 1024 is 1152 + code.
+__device__ __forceinline__ f16x8 codes_to_f16(uint32_t a, uint32_t b)
 {
-    bf16x8 o;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        o[j] = static_cast<__bf16>(static_cast<float>(static_cast<int8_t>(a >> (8 * j))));
-        o[4 + j] = static_cast<__bf16>(static_cast<float>(static_cast<int8_t>(b >> (8 * j))));
-    }
-    return o;
+    a ^= 0x80808080u;
+    b ^= 0x80808080u;
+    at_u32x4 w;
+    w[0] = __builtin_amdgcn_perm(0x64646464u, a, 0x04010400u);
+    w[1] = __builtin_amdgcn_perm(0x64646464u, a, 0x04030402u);
+    w[2] = __builtin_amdgcn_perm(0x64646464u, b, 0x04010400u);
+    w[3] = __builtin_amdgcn_perm(0x64646464u, b, 0x04030402u);
+    return __builtin_bit_cast(f16x8, w) - static_cast<_Float16>(1152.0f);
 }
 
-// C: cache element, QT: type of q and out, D: head_dim, NQ / NP: 16-bit terms
-// of the queries and the weights.
+// 2^e for e in [-126, 127]
+__device__ __forceinline__ float pow2(int e) { return __builtin_bit_cast(float, static_cast<uint32_t>(127 + e) << 23); }
+
+// C: cache element, QT: type of q and out, D: head_dim, NQ: 16-bit terms of
+// the queries (int8 caches: 8-bit digits), NP: 16-bit terms of the weights.
+//
+// int8 caches: K's codes are operands as they are, of the int8 MFMA; the
+// queries are fixed-point numbers of NQ signed 8-bit digits, scaled by a
+// power of two to the head's largest magnitude, and the digits' exact int32
+// products are joined in fp32.  V's codes become fp16 (exactly), the token's
+// step goes into its weight, relative to a running power of two that no step
+// exceeds.  Converting both to bf16 and taking the steps' whole range
+// there spent 1300 vector instructions on 64 tokens instead of about 560: 93
+// us for 131071 tokens of 8 heads of 128 where 61 are enough now.
 template <typename C, typename QT, int D, int NQ, int NP>
 __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(DecodeArgs a)
 {
@@ -116,185 +161,272 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
     constexpr int LPT = NL / NT;            // K loads per score tile
 
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    __shared__ int32_t pages[kMaxChunk / 16];
     __shared__ float wm[kDecWaves][kDecHeads], wl[kDecWaves][kDecHeads];
-    __shared__ int bad_page;
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = lane & 15, grp = lane >> 4;
-    const int64_t b = blockIdx.z;
-    const int kh = static_cast<int>(blockIdx.y) / a.hblocks, hb = static_cast<int>(blockIdx.y) % a.hblocks;
+    const int page_shift = a.page_shift, page_mask = (1 << page_shift) - 1;
+    // heads vary fastest: the same number of chunks for each of the eight XCDs
+    const uint32_t hgroups = static_cast<uint32_t>(a.hkv * a.hblocks);
+    const int hg = static_cast<int>(blockIdx.x % hgroups);
+    const int kh = hg / a.hblocks, hb = hg % a.hblocks;
     const int group = a.hq / a.hkv;
     const int h0 = kh * group + hb * kDecHeads;                                  // first query head
     const int nh = group - hb * kDecHeads < kDecHeads ? group - hb * kDecHeads : kDecHeads;
-    const int64_t len = a.lens[b];
-    const bool bad_len = len < 0 || len > a.max_len;
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
-    const int64_t c1 = bad_len ? c0 : (c0 + a.chunk < len ? c0 + a.chunk : len);
-    if (c0 >= c1 && blockIdx.x != 0) return;  // the join reads the first chunk and those below the length
-    const int ntok = static_cast<int>(c1 > c0 ? c1 - c0 : 0);
-    const int page_mask = (1 << a.page_shift) - 1;
-
-    // ---- the chunk's pages (a bad one: page 0 is read, and the rows end NaN)
-    if (threadIdx.x == 0) bad_page = bad_len ? 1 : 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < (ntok + page_mask) >> a.page_shift; i += kDecThreads) {
-        int32_t pg = a.table[b * a.max_pages + (c0 >> a.page_shift) + i];
-        if (pg < 0 || pg >= a.n_pages) {
-            bad_page = 1;
-            pg = 0;
-        }
-        pages[i] = pg;
+    // ---- this workgroup's piece: up to `per` steps of one sequence
+    const int64_t piece = blockIdx.x / hgroups;
+    int per = 1, b = static_cast<int>(piece), first = 0;
+    if (a.cut) {
+        per = steps_per_piece(a, steps_before(a, a.batch));
+        int64_t seq, tile;
+        if (!find_tile<false>(piece, a.batch, [&](int64_t i) { return (decode_steps(a, i) + per - 1) / per; }, seq, tile))
+            return;
+        b = __builtin_amdgcn_readfirstlane(static_cast<int>(seq));
+        first = __builtin_amdgcn_readfirstlane(static_cast<int>(tile));
     }
+    const int len = a.lens[b];
+    const bool bad_len = len < 0 || len > a.max_len;
+    const bool whole = decode_steps(a, b) <= per;
+    const int begin = first * per * kStep;
+    const int end = bad_len ? begin : (begin + per * kStep < len ? begin + per * kStep : len);
 
     // ---- queries: B operand, column = head, k = 8 consecutive dimensions
     // (int8: dimension 64 p + 16 grp + 8 s of steps 2 p + s, the bytes a lane
     // loads at once; else 32 kk + 8 grp)
     float c = a.scale * kLog2e;  // scores in units of log2
-    x8 qf[KK][NQ];
+    constexpr int QK = I8 ? D / 64 : KK;
+    x8 qf[I8 ? 1 : QK][NQ];  // (int8: the digits stay in LDS)
     {
-        const QT *qp = static_cast<const QT *>(a.q) + (b * a.hq + h0 + (col < nh ? col : 0)) * D;
+        const QT *qp = static_cast<const QT *>(a.q) + (static_cast<int64_t>(b) * a.hq + h0 + (col < nh ? col : 0)) * D;
         float mul = 1.0f;
-        if constexpr (std::is_same<T, _Float16>::value && std::is_same<QT, float>::value) {
-            // fp16 terms: bring the head's largest magnitude to [1, 2)
-            float m = 0.0f;
+        if constexpr (I8 || (std::is_same<T, _Float16>::value && std::is_same<QT, float>::value)) {
+            // the head's largest magnitude, brought to [1, 2) (fp16 terms) or
+            // below 2^(8 NQ - 2) (digits)
+            uint32_t mx = 0;  // of the bit patterns: NaN and infinity last
             for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(static_cast<float>(qp[32 * kk + 8 * grp + j])));
-            m = lane_pair_max<32>(lane_pair_max<16>(m));
-            if (m > 0x1p-120f && m < 0x1p120f) {
-                const int e = static_cast<int>((__builtin_bit_cast(uint32_t, m) >> 23) & 255u) - 127;
-                mul = __builtin_bit_cast(float, static_cast<uint32_t>(127 - e) << 23);
-                c *= __builtin_bit_cast(float, static_cast<uint32_t>(127 + e) << 23);
+                for (int j = 0; j < 8; ++j) {
+                    const float x = static_cast<float>(qp[32 * kk + 8 * grp + j]);
+                    const uint32_t u = __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
+                    mx = mx > u ? mx : u;
+                }
+            mx = max(mx, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mx), 16, 64)));
+            mx = max(mx, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mx), 32, 64)));
+            constexpr int BITS = I8 ? 8 * NQ - 3 : 0;
+            const int e = static_cast<int>(mx >> 23) - 127;
+            if (e == 128) {
+                c = __builtin_nanf("");  // a NaN or an infinity in the query
+                if (I8) mul = 0.0f;
+            } else if (e > -90 && e < 96) {
+                mul = pow2(BITS - e);
+                c *= pow2(e - BITS);
+            } else if (e >= 96) {
+                mul = pow2(BITS - 96) * pow2(96 - e);  // two factors, each in range
+                c = c * pow2(96 - BITS) * pow2(e - 96);
+            } else if (I8) {
+                mul = pow2(BITS + 90);  // all below 2^-90: fixed point to that
+                c *= pow2(-90 - BITS);
             }
         }
+        if constexpr (I8) {
+            // the waves share the work: operand kk by wave kk, through LDS
+            static_assert(QK <= kDecWaves, "an operand for each wave at most");
+            at_i32x4 *shared = reinterpret_cast<at_i32x4 *>(lds);
+            if (wave < QK) {
+                at_i32x4 dig[NQ];
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-            const int d0 = I8 ? 64 * (kk >> 1) + 16 * grp + 8 * (kk & 1) : 32 * kk + 8 * grp;
-            float x[8];
+                for (int n = 0; n < NQ; ++n) dig[n] = at_i32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = static_cast<float>(qp[d0 + j]) * mul;
-            split_terms<T, NQ>(x, qf[kk]);
+                for (int j = 0; j < 16; ++j) {
+                    int v = static_cast<int>(rintf(static_cast<float>(qp[64 * wave + 16 * grp + j]) * mul));
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        dig[n][j >> 2] |= (v & 255) << (8 * (j & 3));
+                        v = (v - static_cast<int8_t>(v)) >> 8;
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) shared[(wave * NQ + n) * 64 + lane] = dig[n];
+            }
+            __syncthreads();
+        } else {
+#pragma unroll
+            for (int kk = 0; kk < QK; ++kk) {
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = static_cast<float>(qp[32 * kk + 8 * grp + j]) * mul;
+                split_terms<T, NQ>(x, qf[kk]);
+            }
         }
     }
-    __syncthreads();
+    const at_f32x4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
+    at_f32x4 o[D / 16];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) o[i] = zero4;
+    float m = -__builtin_inff(), l = 0.0f;
+    // int8: weights times steps in units of vunit / 2^14, so below 2^14 in fp16
+    float vunit = pow2(-112), vinv = pow2(112 + 14);
 
-    // ---- one step's loads.  Tokens past the chunk's end are read from its
-    // last token (K) or last run (V), and masked below.
-    const int last = ntok - 1;
+    // ---- one step's loads.  Tokens past the end are read from the last token
+    // (K) or the last run (V), and masked below.  The pages of a lane's runs are
+    // looked up a step ahead: K's run is that of its row, V's that of its
+    // slots.  A page that does not exist: page 0 is read, and the rows end NaN.
+    const int last = end - 1, last_run = last & ~(RUN - 1);
+    const int32_t *table = a.table + static_cast<int64_t>(b) * a.max_pages;
+    bool bad = bad_len;
+    auto page_of = [&](int tok) {
+        const int32_t pg = table[(tok < last ? tok : last) >> page_shift];
+        return pg;
+    };
+    auto checked = [&](int32_t pg) {
+        const bool is = pg >= 0 && pg < a.n_pages;
+        bad |= !is;
+        return is ? pg : 0;
+    };
     const char *kp = static_cast<const char *>(a.k_pages), *vp = static_cast<const char *>(a.v_pages);
-    auto load_k = [&](int base, at_u32x4 (&r)[NL]) {
+    auto load_k = [&](int base, int32_t pg, at_u32x4 (&r)[NL]) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             int tok = base + RUN * (col >> 2) + 4 * t + (col & 3);
             tok = tok < last ? tok : last;
-            const int64_t cell = ((static_cast<int64_t>(pages[tok >> a.page_shift]) * a.hkv + kh) << a.page_shift) +
-                                 (tok & page_mask);
+            const int64_t cell = ((static_cast<int64_t>(pg) * a.hkv + kh) << page_shift) + (tok & page_mask);
             const char *src = kp + cell * (D * static_cast<int64_t>(sizeof(C))) + 16 * grp;
 #pragma unroll
             for (int i = 0; i < LPT; ++i) r[t * LPT + i] = *reinterpret_cast<const at_u32x4 *>(src + 64 * i);
         }
     };
     auto run_of = [&](int base) {
-        const int tok = base + RUN * grp, lr = last & ~(RUN - 1);
-        return tok < lr ? tok : lr;
+        const int tok = base + RUN * grp;
+        return tok < last_run ? tok : last_run;
     };
-    auto load_v = [&](int base, at_u32x4 (&r)[NL]) {
-        const int tok = run_of(base);
-        const int64_t pgh = static_cast<int64_t>(pages[tok >> a.page_shift]) * a.hkv + kh;
-        const char *src = vp + (((pgh * D + col) << a.page_shift) + (tok & page_mask)) * static_cast<int64_t>(sizeof(C));
-        const int64_t stride = (static_cast<int64_t>(16) << a.page_shift) * sizeof(C);
+    auto load_v = [&](int base, int32_t pg, at_u32x4 (&r)[NL]) {
+        const int64_t pgh = static_cast<int64_t>(pg) * a.hkv + kh;
+        const char *src = vp + (((pgh * D + col) << page_shift) + (run_of(base) & page_mask)) * static_cast<int64_t>(sizeof(C));
+        const int64_t stride = (static_cast<int64_t>(16) << page_shift) * sizeof(C);
 #pragma unroll
         for (int i = 0; i < NL; ++i) r[i] = *reinterpret_cast<const at_u32x4 *>(src + i * stride);
     };
-    auto load_steps = [&](int base, at_f32x4 (&ks)[NT], at_f32x4 (&vs)[NT]) {
-        const int tok = run_of(base);
-        const int64_t cell = ((static_cast<int64_t>(pages[tok >> a.page_shift]) * a.hkv + kh) << a.page_shift) +
-                             (tok & page_mask);
+    auto load_steps = [&](const float *steps, int base, int32_t pg, at_f32x4 (&r)[NT]) {
+        const int64_t cell = ((static_cast<int64_t>(pg) * a.hkv + kh) << page_shift) + (run_of(base) & page_mask);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            ks[t] = *reinterpret_cast<const at_f32x4 *>(a.k_steps + cell + 4 * t);
-            vs[t] = *reinterpret_cast<const at_f32x4 *>(a.v_steps + cell + 4 * t);
-        }
+        for (int t = 0; t < NT; ++t) r[t] = *reinterpret_cast<const at_f32x4 *>(steps + cell + 4 * t);
     };
-
-    const at_f32x4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
-    at_f32x4 o[D / 16];
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) o[i] = zero4;
-    float m = -__builtin_inff(), l = 0.0f;
 
     at_u32x4 kr[NL], vr[NL];
     at_f32x4 ks[NT], vs[NT];
-    int base = wave * TS;
-    if (base < ntok) {
-        load_k(base, kr);
-        if constexpr (I8) load_steps(base, ks, vs);
-        load_v(base, vr);
+    int base = begin + wave * TS;
+    int32_t kpage = 0, vpage = 0;
+    if (base < end) {
+        kpage = page_of(base + RUN * (col >> 2));
+        vpage = page_of(base + RUN * grp);
+        const int32_t k0 = checked(kpage), v0 = checked(vpage);
+        load_k(base, k0, kr);
+        if constexpr (I8) load_steps(a.k_steps, base, v0, ks);
+        if constexpr (I8) load_steps(a.v_steps, base, v0, vs);
+        load_v(base, v0, vr);
+        kpage = page_of(base + kDecWaves * TS + RUN * (col >> 2));
+        vpage = page_of(base + kDecWaves * TS + RUN * grp);
     }
-    for (; base < ntok; base += kDecWaves * TS) {
+    for (; base < end; base += kDecWaves * TS) {
         const int next = base + kDecWaves * TS;
         // ---- scores: tile t, register i of lane: token base + RUN grp + 4 t + i, head col
         at_f32x4 s[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            s[t] = zero4;
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                x8 kf;
-                if constexpr (I8) {
-                    at_u32x4 w = kr[t * LPT + (kk >> 1)];
-                    asm volatile("" : "+v"(w));  // keeps the codes packed up to here
-                    kf = kk & 1 ? codes_to_bf16(w[2], w[3]) : codes_to_bf16(w[0], w[1]);
-                } else {
-                    kf = __builtin_bit_cast(x8, kr[t * LPT + kk]);
-                }
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) s[t] = Op16<T>::mfma16(kf, qf[kk][n], s[t]);
-            }
-            if constexpr (I8) __builtin_amdgcn_sched_barrier(0);  // or every code is converted up front, into spills
-        }
-        at_f32x4 vsc[NT];
         if constexpr (I8) {
+            // digit by digit from the highest, each read from LDS anew: kept
+            // in registers they make the kernel spill
+            uint32_t place = lane;
+            asm volatile("" : "+v"(place));
+            const at_i32x4 *digits = reinterpret_cast<const at_i32x4 *>(lds) + place;
+#pragma unroll
+            for (int n = NQ - 1; n >= 0; --n) {
+                at_i32x4 dig[QK];
+#pragma unroll
+                for (int kk = 0; kk < QK; ++kk) dig[kk] = digits[(kk * NQ + n) * 64];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    at_i32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+                    for (int kk = 0; kk < QK; ++kk)
+                        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(at_i32x4, kr[t * LPT + kk]), dig[kk],
+                                                                    acc, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = static_cast<float>(acc[i]);
+                        s[t][i] = n == NQ - 1 ? x : fmaf(s[t][i], 256.0f, x);
+                    }
+                }
+            }
+        } else {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                s[t] *= ks[t];
-                vsc[t] = vs[t];
+                s[t] = zero4;
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+                        s[t] = Op16<T>::mfma16(__builtin_bit_cast(x8, kr[t * LPT + kk]), qf[kk][n], s[t]);
             }
         }
-        if (next < ntok) {
-            load_k(next, kr);
-            if constexpr (I8) load_steps(next, ks, vs);
+        if constexpr (I8) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) s[t] *= ks[t];
         }
-        const bool tail = base + TS > ntok;
+        const int32_t kn = checked(kpage), vn = checked(vpage);
+        if (next < end) {
+            load_k(next, kn, kr);
+            if constexpr (I8) load_steps(a.k_steps, next, vn, ks);
+            kpage = page_of(next + kDecWaves * TS + RUN * (col >> 2));
+            vpage = page_of(next + kDecWaves * TS + RUN * grp);
+        }
+        const bool tail = base + TS > end;
         float top = -__builtin_inff();
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 s[t][i] *= c;
-                if (tail && base + RUN * grp + 4 * t + i >= ntok) s[t][i] = -__builtin_inff();
+                if (tail && base + RUN * grp + 4 * t + i >= end) s[t][i] = -__builtin_inff();
                 top = fmaxf(top, s[t][i]);
             }
         top = lane_pair_max<32>(lane_pair_max<16>(top));
         // a larger maximum rescales what is there (all lanes of a head alike)
         if (__ballot(top > m) != 0) {
             const float mn = fmaxf(m, top);
-            const float f = m == mn ? 1.0f : exp2f(m - mn);
+            const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
             l *= f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) o[i] *= f;
             m = mn;
         }
         const float ms = m == -__builtin_inff() ? 0.0f : m;
+        if constexpr (I8) {
+            // the steps' running power of two
+            float vtop = 0.0f;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (tail && base + RUN * grp + 4 * t + i >= end) vs[t][i] = 0.0f;
+                    vtop = fmaxf(vtop, vs[t][i]);
+                }
+            vtop = lane_pair_max<32>(lane_pair_max<16>(vtop));
+            if (vtop > vunit) {
+                const int e = static_cast<int>(__builtin_bit_cast(uint32_t, vtop) >> 23) - 126;  // 2^e > vtop
+                const float f = vunit * pow2(-e);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) o[i] *= f;
+                vunit = pow2(e);
+                vinv = pow2(14 - e);
+            }
+        }
         float p[TS / 4];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float e = exp2f(s[t][i] - ms);
+                float e = __builtin_amdgcn_exp2f(s[t][i] - ms);
                 l += e;
-                if constexpr (I8) e = tail && base + RUN * grp + 4 * t + i >= ntok ? 0.0f : e * vsc[t][i];
+                if constexpr (I8) e *= vs[t][i] * vinv;
                 p[4 * t + i] = e;
             }
         // ---- O^T += V^T P^T, slot j of step u: token base + RUN grp + 8 u + j
@@ -305,7 +437,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
                 constexpr int PER = 4 / sizeof(C);  // tokens per dword
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    const int left = ntok - (base + RUN * grp + PER * w);
+                    const int left = end - (base + RUN * grp + PER * w);
                     const uint32_t keep = left >= PER ? 0xffffffffu
                                           : left <= 0 ? 0u
                                                       : (1u << (8 * static_cast<int>(sizeof(C)) * left)) - 1u;
@@ -325,22 +457,31 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
                 x8 vf;
                 if constexpr (I8) {
                     at_u32x2 w = {vr[i][2 * u], vr[i][2 * u + 1]};
-                    asm volatile("" : "+v"(w));
-                    vf = codes_to_bf16(w[0], w[1]);
+                    asm volatile("" : "+v"(w));  // keeps the codes packed up to here
+                    vf = codes_to_f16(w[0], w[1]);
                 } else
                     vf = __builtin_bit_cast(x8, vr[i]);
 #pragma unroll
                 for (int n = 0; n < NP; ++n) o[i] = Op16<T>::mfma16(vf, pf[n], o[i]);
                 if constexpr (I8)
-                    if ((i & 1) == 1) __builtin_amdgcn_sched_barrier(0);
+                    if ((i & 1) == 1) __builtin_amdgcn_sched_barrier(0);  // or every code is converted up front
             }
         }
-        if (next < ntok) load_v(next, vr);
+        if (next < end) {
+            if constexpr (I8) load_steps(a.v_steps, next, vn, vs);
+            load_v(next, vn, vr);
+        }
     }
     l = lane_pair_sum<32>(lane_pair_sum<16>(l));
+    if constexpr (I8) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) o[i] *= vunit * pow2(-14);
+    }
 
     // ---- join the four waves: rows in LDS [wave][head][D + 4]
+    if constexpr (I8) __syncthreads();  // where the digits were
     float *rows = reinterpret_cast<float *>(lds);
+    if (__ballot(bad) != 0) l = __builtin_nanf("");
     if (grp == 0) {
         wm[wave][col] = m;
         wl[wave][col] = l;
@@ -351,7 +492,6 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
             *reinterpret_cast<at_f32x4 *>(rows + (wave * nh + col) * (D + 4) + 16 * i + 4 * grp) = o[i];
     }
     __syncthreads();
-    const bool bad = bad_page != 0;
     for (int i = threadIdx.x; i < nh * (D / 4); i += kDecThreads) {
         const int h = i / (D / 4), e = (i % (D / 4)) * 4;
         float M = wm[0][h];
@@ -362,42 +502,45 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
         at_f32x4 r = zero4;
 #pragma unroll
         for (int w = 0; w < kDecWaves; ++w) {
-            const float f = exp2f(wm[w][h] - Ms);
+            const float f = __builtin_amdgcn_exp2f(wm[w][h] - Ms);
             L += f * wl[w][h];
             r += f * *reinterpret_cast<const at_f32x4 *>(rows + (w * nh + h) * (D + 4) + e);
         }
-        if (bad) L = __builtin_nanf("");
-        const int64_t row = b * a.hq + h0 + h;
-        if (a.chunks == 1) {
-            const float f = ntok == 0 && !bad ? 0.0f : 1.0f / L;
-            store4(static_cast<QT *>(a.out) + row * D + e, r * f);
+        if (whole) {
+            const float f = len == 0 ? 0.0f : 1.0f / L;
+            store4(static_cast<QT *>(a.out) + (static_cast<int64_t>(b) * a.hq + h0 + h) * D + e, r * f);
         } else {
-            *reinterpret_cast<at_f32x4 *>(a.part_rows + (row * a.chunks + blockIdx.x) * D + e) = r;
+            const int64_t slot = piece * a.hq + h0 + h;
+            *reinterpret_cast<at_f32x4 *>(a.part_rows + slot * D + e) = r;
             if (e == 0) {
-                a.part_ml[(row * a.chunks + blockIdx.x) * 2] = M;
-                a.part_ml[(row * a.chunks + blockIdx.x) * 2 + 1] = L;
+                a.part_ml[slot * 2] = M;
+                a.part_ml[slot * 2 + 1] = L;
             }
         }
     }
 }
 
-// Joins a row's chunks: one workgroup per (query head, sequence), its D / 4
-// lanes wide groups taking every n-th chunk, then a sum over the groups in
-// LDS.
+// Joins the pieces of a sequence that was cut: one workgroup
+// per (query head, sequence), its D / 4 lanes wide groups taking every n-th
+// piece, then a sum over the groups in LDS.
 template <typename QT, int D>
 __global__ void __launch_bounds__(256) k_attn_join(DecodeArgs a)
 {
     constexpr int LPR = D / 4, G = 256 / LPR;
-    __shared__ float wgt[kMaxChunks];
+    __shared__ float wgt[2 * kMaxShares];
     __shared__ float red[4];
     __shared__ at_f32x4 sums[G][LPR];
-    const int64_t b = blockIdx.y;
-    const int64_t row = b * a.hq + blockIdx.x;
-    const int64_t len = a.lens[b];
-    const int n = len <= 0 || len > a.max_len ? 1 : static_cast<int>((len + a.chunk - 1) / a.chunk);
-    const float *ml = a.part_ml + row * a.chunks * 2;
+    const int64_t b = blockIdx.y, h = blockIdx.x;
+    const int per = steps_per_piece(a, steps_before(a, a.batch));
+    const int n = (decode_steps(a, b) + per - 1) / per;
+    if (n == 1) return;
+    int64_t before = 0;  // pieces of the sequences before
+    for (int64_t i = threadIdx.x & 63; i < b; i += 64) before += (decode_steps(a, i) + per - 1) / per;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) before += __shfl_xor(before, o, 64);
+    auto slot = [&](int i) { return (before + i) * a.hq + h; };
     float M = -__builtin_inff();
-    for (int i = threadIdx.x; i < n; i += 256) M = fmaxf(M, ml[2 * i]);
+    for (int i = threadIdx.x; i < n; i += 256) M = fmaxf(M, a.part_ml[slot(i) * 2]);
     M = wave_max(M);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = M;
     __syncthreads();
@@ -406,9 +549,9 @@ __global__ void __launch_bounds__(256) k_attn_join(DecodeArgs a)
     __syncthreads();
     float L = 0.0f;
     for (int i = threadIdx.x; i < n; i += 256) {
-        const float w = exp2f(ml[2 * i] - M);
+        const float w = __builtin_amdgcn_exp2f(a.part_ml[slot(i) * 2] - M);
         wgt[i] = w;
-        L += w * ml[2 * i + 1];
+        L += w * a.part_ml[slot(i) * 2 + 1];
     }
     L = wave_sum(L);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = L;
@@ -416,15 +559,14 @@ __global__ void __launch_bounds__(256) k_attn_join(DecodeArgs a)
     L = (red[0] + red[1]) + (red[2] + red[3]);
     const int g = threadIdx.x / LPR, x = threadIdx.x % LPR;
     at_f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
-    const float *pr = a.part_rows + row * a.chunks * D + 4 * x;
 #pragma unroll 8
-    for (int i = g; i < n; i += G) r += wgt[i] * *reinterpret_cast<const at_f32x4 *>(pr + static_cast<int64_t>(i) * D);
+    for (int i = g; i < n; i += G) r += wgt[i] * *reinterpret_cast<const at_f32x4 *>(a.part_rows + slot(i) * D + 4 * x);
     sums[g][x] = r;
     __syncthreads();
     if (g == 0) {
 #pragma unroll
         for (int i = 1; i < G; ++i) r += sums[i][x];
-        store4(static_cast<QT *>(a.out) + row * D + 4 * x, r * (len == 0 ? 0.0f : 1.0f / L));
+        store4(static_cast<QT *>(a.out) + (b * a.hq + h) * D + 4 * x, r * (1.0f / L));
     }
 }
 
@@ -433,16 +575,18 @@ hipError_t decode_launch(const DecodePlan &p, const DecodeArgs &a, int64_t batch
 {
     static std::atomic<uint64_t> lds_done{0};
     const auto kernel = k_attn_decode<C, QT, D, NQ, NP>;
+    // the waves' rows at the end; int8: the queries' digits before
     constexpr int kMaxLds = kDecWaves * kDecHeads * (D + 4) * 4;
+    constexpr int kDigits = std::is_same<C, int8_t>::value ? D / 64 * NQ * 1024 : 0;
+    static_assert(kDigits <= kMaxLds, "the digits fit");
     const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void *>(kernel), kMaxLds, lds_done);
     if (e != hipSuccess) return e;
     const int group = a.hq / a.hkv;
-    const int lds = kDecWaves * (group < kDecHeads ? group : kDecHeads) * (D + 4) * 4;
+    const int rows = kDecWaves * (group < kDecHeads ? group : kDecHeads) * (D + 4) * 4;
+    const int lds = rows > kDigits ? rows : kDigits;
     hipLaunchKernelGGL(kernel,
-                       dim3(static_cast<uint32_t>(p.chunks), static_cast<uint32_t>(a.hkv * a.hblocks),
-                            static_cast<uint32_t>(batch)),
-                       dim3(kDecThreads), lds, s, a);
-    if (p.chunks > 1)
+                       dim3(static_cast<uint32_t>(p.pieces * a.hkv * a.hblocks)), dim3(kDecThreads), lds, s, a);
+    if (p.join)
         hipLaunchKernelGGL((k_attn_join<QT, D>), dim3(static_cast<uint32_t>(a.hq), static_cast<uint32_t>(batch)),
                            dim3(256), 0, s, a);
     return hipGetLastError();
@@ -461,20 +605,19 @@ hipError_t decode_d(const DecodePlan &p, const DecodeArgs &a, int64_t batch, int
 DecodePlan decode_plan(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_t max_len)
 {
     DecodePlan p;
-    const int64_t group = hq / hkv, hblocks = (group + kDecHeads - 1) / kDecHeads;
-    const int64_t per = batch * hkv * hblocks;
-    // about four workgroups per CU when every sequence is at its bound
-    int64_t chunk = (max_len * per + 1023) / 1024;
-    chunk = (chunk + 255) / 256 * 256;
-    const int64_t least = ((max_len + kMaxChunks - 1) / kMaxChunks + 255) / 256 * 256;
-    if (chunk > 1024) chunk = 1024;
-    if (chunk < least) chunk = least;
-    if (chunk < 256) chunk = 256;
-    p.chunk = chunk;
-    p.chunks = max_len > 0 ? (max_len + chunk - 1) / chunk : 1;
-    if (p.chunks > 1) {
-        p.rows_floats = static_cast<size_t>(batch) * hq * p.chunks * d;
-        p.part_floats = p.rows_floats + static_cast<size_t>(batch) * hq * p.chunks * 2;
+    const int64_t group = hq / hkv, hgroups = hkv * ((group + kDecHeads - 1) / kDecHeads);
+    const int64_t each = max_len > 0 ? (max_len + kStep - 1) / kStep : 1;  // steps of a sequence at its bound
+    // two workgroups of four waves a CU; of 256-wide heads' registers, one
+    int64_t shares = (d == 256 ? 256 : 512) / hgroups;
+    if (shares < 1) shares = 1;
+    if (shares > kMaxShares) shares = kMaxShares;
+    p.shares = static_cast<int32_t>(shares);
+    p.pieces = batch * 2 <= shares ? shares + batch : 2 * shares + batch;
+    if (p.pieces > each * batch) p.pieces = each * batch;
+    p.join = each > 1;
+    if (p.join) {
+        p.rows_floats = static_cast<size_t>(p.pieces) * hq * d;
+        p.part_floats = p.rows_floats + static_cast<size_t>(p.pieces) * hq * 2;
     }
     return p;
 }
@@ -486,7 +629,7 @@ hipError_t launch_attn_decode(const DecodePlan &p, const void *q, int q_type, in
     const int32_t group = hq / c.n_kv_heads;
     const DecodeArgs a{q, hq, c.n_kv_heads, (group + kDecHeads - 1) / kDecHeads, c.k_pages, c.v_pages, c.k_steps,
                        c.v_steps, c.n_pages, __builtin_ctz(static_cast<unsigned>(c.page_size)), table, max_pages, lens,
-                       max_len, p.chunk, p.chunks, scale, out, part, part + p.rows_floats};
+                       batch, max_len, p.shares, p.join, scale, out, part, part + p.rows_floats};
     const int d = c.head_dim;
     if (c.dtype == PTQ1_BF16)
         return q_type == PTQ1_F32 ? decode_d<__bf16, float, 3, 3>(p, a, batch, d, s)
@@ -494,9 +637,9 @@ hipError_t launch_attn_decode(const DecodePlan &p, const void *q, int q_type, in
     if (c.dtype == PTQ1_F16)
         return q_type == PTQ1_F32 ? decode_d<_Float16, float, 3, 2>(p, a, batch, d, s)
                                   : decode_d<_Float16, _Float16, 1, 2>(p, a, batch, d, s);
-    return q_type == PTQ1_F32 ? decode_d<int8_t, float, 3, 3>(p, a, batch, d, s)
-           : q_type == PTQ1_F16 ? decode_d<int8_t, _Float16, 2, 2>(p, a, batch, d, s)
-                                : decode_d<int8_t, __bf16, 1, 2>(p, a, batch, d, s);
+    return q_type == PTQ1_F32 ? decode_d<int8_t, float, 4, 3>(p, a, batch, d, s)
+           : q_type == PTQ1_F16 ? decode_d<int8_t, _Float16, 3, 2>(p, a, batch, d, s)
+                                : decode_d<int8_t, __bf16, 3, 2>(p, a, batch, d, s);
 }
 
 }  // namespace ptq1

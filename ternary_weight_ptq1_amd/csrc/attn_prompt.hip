@@ -33,6 +33,7 @@ namespace {
 constexpr int kPrWaves = 4;
 constexpr int kPrThreads = 64 * kPrWaves;
 constexpr int kPrRows = 32 * kPrWaves;  // query rows of a workgroup
+constexpr int kJoinParts = 4;           // workgroups that join one tile
 constexpr int kAhead = 4;               // K reads ahead of their products
 
 typedef short at_s16x4 __attribute__((ext_vector_type(4)));
@@ -90,8 +91,35 @@ __device__ __forceinline__ bool clear_non_finite(at_u32x4 &w)
     return found;
 }
 
+// The flat tile's sequence and its place there, counted from the end; only
+// rows that exist count.
+__device__ __forceinline__ bool prompt_tile(const PromptArgs &a, int64_t flat, int64_t &b, int64_t &at)
+{
+    return find_tile<true>(
+        flat, a.batch,
+        [&](int64_t i) {
+            const int64_t first = a.cu_q[i], end = a.cu_q[i + 1];
+            const int64_t n = (end < a.q_rows ? end : a.q_rows) - (first > 0 ? first : 0);
+            return n > 0 ? (n * (a.hq / a.hkv) + kPrRows - 1) / kPrRows : 0;
+        },
+        b, at);
+}
+
+// A sequence past its bounds, or with rows that are not there: its rows are NaN.
+__device__ __forceinline__ bool prompt_refused(const PromptArgs &a, int64_t q0, int64_t lq, int64_t k0, int64_t lk)
+{
+    return q0 < 0 || k0 < 0 || q0 + lq > a.q_rows || lk < 0 || k0 + lk > a.k_rows || lq > a.max_q || lk > a.max_k;
+}
+
+// Keys that query `tok` of a sequence sees: the first so many.
+__device__ __forceinline__ int visible(const PromptArgs &a, int64_t tok, int64_t off, int64_t lk)
+{
+    const int64_t n = a.causal ? tok + off + 1 : lk;
+    return static_cast<int>(n > 0 ? n : 0);
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(PromptArgs a)
+__global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(PromptArgs a, PromptPlan plan, float *part)
 {
     typedef typename Op16<T>::x8 x8;
     constexpr int BN = prompt_keys(D);      // keys of a tile
@@ -114,22 +142,15 @@ __global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(Pr
     // number allows (eight heads: one each).
     const int group = a.hq / a.hkv;
     const int kh = static_cast<int>(blockIdx.x % static_cast<uint32_t>(a.hkv));
+    const int64_t flat = blockIdx.x / static_cast<uint32_t>(a.hkv);
     int64_t b, at;
-    if (!find_tile(blockIdx.x / static_cast<uint32_t>(a.hkv), a.batch,
-                   [&](int64_t i) {
-                       // the sequence's rows that exist
-                       const int64_t first = a.cu_q[i], end = a.cu_q[i + 1];
-                       const int64_t n = (end < a.q_rows ? end : a.q_rows) - (first > 0 ? first : 0);
-                       return n > 0 ? (n * group + kPrRows - 1) / kPrRows : 0;
-                   },
-                   b, at))
-        return;
+    if (!prompt_tile(a, flat, b, at)) return;
     const int64_t q0 = a.cu_q[b], k0 = a.cu_k[b];
     const int64_t lq = a.cu_q[b + 1] - q0, lk = a.cu_k[b + 1] - k0;
     const int64_t rows = lq * group;
-    if (q0 < 0 || k0 < 0 || q0 + lq > a.q_rows || lk < 0 || k0 + lk > a.k_rows || lq > a.max_q || lk > a.max_k) {
+    if (prompt_refused(a, q0, lq, k0, lk)) {
         const int64_t r = (q0 < 0 ? -q0 * group : 0) + at * kPrRows + threadIdx.x, tok = q0 + r / group;
-        if (threadIdx.x < kPrRows && r < rows && tok < a.q_rows) {
+        if (blockIdx.y == 0 && threadIdx.x < kPrRows && r < rows && tok < a.q_rows) {
             T *dst = static_cast<T *>(a.out) + (tok * a.hq + kh * group + r % group) * D;
             const float n = __builtin_nanf("");
             for (int e = 0; e < D; e += 4) store4(dst + e, at_f32x4{n, n, n, n});
@@ -142,16 +163,19 @@ __global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(Pr
     const int64_t row = tile * kPrRows + 32 * wave + col;
     const int64_t rowc = row < rows ? row : rows - 1;
     const int32_t tok = static_cast<int32_t>(rowc / group), head = static_cast<int32_t>(rowc % group);
-    // keys below `seen` are visible to this lane's row
     const int64_t off = lk - lq;
-    int64_t seen64 = a.causal ? tok + off + 1 : lk;
-    if (seen64 < 0) seen64 = 0;
-    const int seen = static_cast<int>(seen64);
+    // keys below `seen` are visible to this lane's row
+    const int seen = visible(a, tok, off, lk);
     const int64_t tok_first = tile * kPrRows / group;
     const int64_t row_last = (tile + 1) * kPrRows < rows ? (tile + 1) * kPrRows - 1 : rows - 1;
-    int64_t all64 = a.causal ? tok_first + off + 1 : lk;                 // keys that every row of the tile sees
-    int64_t any64 = a.causal ? row_last / group + off + 1 : lk;         // keys that some row sees
-    const int all = static_cast<int>(all64 < 0 ? 0 : all64), any = static_cast<int>(any64 < 0 ? 0 : any64);
+    // keys that some row of the tile sees; of them, this workgroup's
+    const int reach = visible(a, row_last / group, off, lk);
+    const int first = static_cast<int>(blockIdx.y * plan.chunk);
+    if (first >= reach && blockIdx.y > 0) return;
+    const bool split = reach > plan.chunk;
+    const int any = split && reach - first > plan.chunk ? first + static_cast<int>(plan.chunk) : reach;
+    // keys that every row sees
+    const int every = visible(a, tok_first, off, lk), all = every < any ? every : any;
 
     // ---- queries: B operand, column = row, k = 16 kk + 8 half + j
     x8 qf[KK];
@@ -308,12 +332,12 @@ __global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(Pr
     };
 
     if (threadIdx.x == 0) odd_values = 0;
-    if (any > 0) {
-        stage_k(kt0, 0);
-        stage_v(vt0, 0);
+    if (first < any) {
+        stage_k(kt0, first);
+        stage_v(vt0, first);
     }
     __syncthreads();
-    int n0 = 0;
+    int n0 = first;
     for (; n0 + 2 * BN <= all; n0 += 2 * BN) {
         step(std::false_type{}, kt0, vt0, kt1, vt1, n0);
         step(std::false_type{}, kt1, vt1, kt0, vt0, n0 + BN);
@@ -325,10 +349,10 @@ __global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(Pr
         step(std::true_type{}, kt1, vt1, kt0, vt0, n0 + BN);
     }
     l = lane_pair_sum<32>(l);
-    const float f = seen == 0 ? 0.0f : 1.0f / l;
+    const float f = split ? 1.0f : seen == 0 ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[i] *= f;
-    if (any > 0 && odd_values != 0) {
+    if (first < any && odd_values != 0) {
         for (int r = border; r < any; ++r) {
             const T *src = static_cast<const T *>(a.v) + (k0 + r) * a.vs + static_cast<int64_t>(kh) * D + 4 * half;
 #pragma unroll
@@ -342,29 +366,83 @@ __global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(Pr
                 }
         }
     }
-    if (row < rows) {
+    if (row >= rows) return;
+    if (!split) {
         T *dst = static_cast<T *>(a.out) + ((q0 + tok) * a.hq + kh * group + head) * D;
 #pragma unroll
         for (int i = 0; i < DT; ++i)
 #pragma unroll
             for (int j = 0; j < 16; j += 4)
-                store4(dst + 32 * i + 2 * j + 4 * half,
-                       at_f32x4{o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]});
+                store4(dst + 32 * i + 2 * j + 4 * half, at_f32x4{o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]});
+    } else {
+        const int64_t slot = ((q0 + tok) * a.hq + kh * group + head) * plan.splits + blockIdx.y;
+        float *dst = part + slot * D;
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+                store4(dst + 32 * i + 2 * j + 4 * half, at_f32x4{o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]});
+        if (half == 0) {
+            part[plan.rows_floats + slot * 2] = m;
+            part[plan.rows_floats + slot * 2 + 1] = l;
+        }
+    }
+}
+
+// Joins the chunks of the tiles that were split: D / 4 lanes per row.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) k_prompt_join(PromptArgs a, PromptPlan plan, const float *part)
+{
+    constexpr int LPR = D / 4;
+    const int group = a.hq / a.hkv;
+    const int kh = static_cast<int>(blockIdx.x % static_cast<uint32_t>(a.hkv));
+    int64_t b, at;
+    if (!prompt_tile(a, blockIdx.x / static_cast<uint32_t>(a.hkv), b, at)) return;
+    const int64_t q0 = a.cu_q[b], k0 = a.cu_k[b];
+    const int64_t lq = a.cu_q[b + 1] - q0, lk = a.cu_k[b + 1] - k0, rows = lq * group;
+    if (prompt_refused(a, q0, lq, k0, lk)) return;
+    const int64_t tile = (rows + kPrRows - 1) / kPrRows - 1 - at;
+    const int64_t end = (tile + 1) * kPrRows < rows ? (tile + 1) * kPrRows : rows;
+    const int reach = visible(a, (end - 1) / group, lk - lq, lk);
+    if (reach <= plan.chunk) return;
+    const int n = static_cast<int>((reach + plan.chunk - 1) / plan.chunk);
+    const int e = (threadIdx.x % LPR) * 4;
+    // blockIdx.y: a quarter of the tile's rows
+    const int64_t r0 = tile * kPrRows + blockIdx.y * (kPrRows / kJoinParts);
+    for (int64_t r = r0 + threadIdx.x / LPR; r < r0 + kPrRows / kJoinParts && r < end; r += 256 / LPR) {
+        const int64_t tok = r / group, at_out = (q0 + tok) * a.hq + kh * group + r % group;
+        const float *ml = part + plan.rows_floats + at_out * plan.splits * 2, *src = part + at_out * plan.splits * D + e;
+        float M = -__builtin_inff();
+        for (int i = 0; i < n; ++i) M = fmaxf(M, ml[2 * i]);
+        if (M == -__builtin_inff()) M = 0.0f;
+        float L = 0.0f;
+        at_f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < n; ++i) {
+            const float w = __builtin_amdgcn_exp2f(ml[2 * i] - M);
+            L += w * ml[2 * i + 1];
+            o += w * *reinterpret_cast<const at_f32x4 *>(src + static_cast<int64_t>(i) * D);
+        }
+        const float f = visible(a, tok, lk - lq, lk) == 0 ? 0.0f : 1.0f / L;
+        store4(static_cast<T *>(a.out) + at_out * D + e, o * f);
     }
 }
 
 template <typename T, int D>
-hipError_t prompt_launch(const PromptArgs &a, hipStream_t s)
+hipError_t prompt_launch(const PromptArgs &a, const PromptPlan &plan, float *part, hipStream_t s)
 {
-    hipLaunchKernelGGL((k_attn_prompt<T, D>), dim3(static_cast<uint32_t>(prompt_tiles(a.batch, a.q_rows, a.hq, a.hkv) * a.hkv)),
-                       dim3(kPrThreads), 0, s, a);
+    const uint32_t tiles = static_cast<uint32_t>(prompt_tiles(a.batch, a.q_rows, a.hq, a.hkv) * a.hkv);
+    hipLaunchKernelGGL((k_attn_prompt<T, D>), dim3(tiles, static_cast<uint32_t>(plan.splits)), dim3(kPrThreads), 0, s, a,
+                       plan, part);
+    if (plan.splits > 1)
+        hipLaunchKernelGGL((k_prompt_join<T, D>), dim3(tiles, kJoinParts), dim3(256), 0, s, a, plan, part);
     return hipGetLastError();
 }
 
 template <typename T>
-hipError_t prompt_d(const PromptArgs &a, int d, hipStream_t s)
+hipError_t prompt_d(const PromptArgs &a, int d, const PromptPlan &plan, float *part, hipStream_t s)
 {
-    return d == 64 ? prompt_launch<T, 64>(a, s) : d == 128 ? prompt_launch<T, 128>(a, s) : prompt_launch<T, 256>(a, s);
+    return d == 64 ? prompt_launch<T, 64>(a, plan, part, s)
+                   : d == 128 ? prompt_launch<T, 128>(a, plan, part, s) : prompt_launch<T, 256>(a, plan, part, s);
 }
 
 }  // namespace
@@ -375,11 +453,34 @@ int64_t prompt_tiles(int64_t batch, int64_t q_rows, int32_t hq, int32_t hkv)
     return q_rows * (hq / hkv) / kPrRows + batch;
 }
 
-size_t prompt_part_floats(int64_t, int32_t, int32_t, int32_t, int64_t, int64_t) { return 0; }
-
-hipError_t launch_attn_prompt(const PromptArgs &a, int dtype, int32_t d, float *, hipStream_t s)
+PromptPlan prompt_plan(int64_t batch, int64_t q_rows, int64_t max_k, int32_t hq, int32_t hkv, int32_t d)
 {
-    return dtype == PTQ1_BF16 ? prompt_d<__bf16>(a, d, s) : prompt_d<_Float16>(a, d, s);
+    PromptPlan p;
+    p.chunk = max_k > 0 ? (max_k + 127) / 128 * 128 : 128;
+    const int64_t slots = d == 256 ? 256 : 512;  // workgroups the GPU holds
+    const int64_t tiles = prompt_tiles(batch, q_rows, hq, hkv) * hkv;
+    // Chunks that fill the GPU about once (half of max_k: a causal tile's
+    // reach on average), of 512 keys at least: a chunk costs its rows in fp32,
+    // written and read.  Cut three times finer: 0.34 ms for 0.28 at 1657
+    // queries of 24 heads of 256 over 4000 keys and more, and with many tiles
+    // cutting costs more than the last workgroups' wait: 1272 tiles of
+    // up to 2500 keys of 128 in two took 115 us for 88.
+    if (tiles < 4 * slots) {
+        int64_t chunk = (tiles * (max_k / 2) / slots + 127) / 128 * 128;
+        if (chunk < 512) chunk = 512;
+        if (chunk < max_k) {
+            p.chunk = chunk;
+            p.splits = (max_k + chunk - 1) / chunk;
+            p.rows_floats = static_cast<size_t>(q_rows) * hq * p.splits * d;
+            p.part_floats = p.rows_floats + static_cast<size_t>(q_rows) * hq * p.splits * 2;
+        }
+    }
+    return p;
+}
+
+hipError_t launch_attn_prompt(const PromptArgs &a, int dtype, int32_t d, const PromptPlan &plan, float *part, hipStream_t s)
+{
+    return dtype == PTQ1_BF16 ? prompt_d<__bf16>(a, d, plan, part, s) : prompt_d<_Float16>(a, d, plan, part, s);
 }
 
 }  // namespace ptq1

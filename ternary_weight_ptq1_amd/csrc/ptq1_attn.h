@@ -17,6 +17,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float at_f32x4 __attribute__((ext_vector_type(4)));
 typedef float at_f32x8 __attribute__((ext_vector_type(8)));
 typedef float at_f32x16 __attribute__((ext_vector_type(16)));
+typedef int at_i32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t at_u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t at_u32x4 __attribute__((ext_vector_type(4)));
 
@@ -102,11 +103,12 @@ __device__ __forceinline__ void store4(_Float16 *p, at_f32x4 v)
 }
 
 // The place of flat tile `flat` among the tiles of `batch` sequences, of which
-// sequence i has tiles_of(i): dense, 64 sequences at a time with the longest
-// of them first (the most expensive tiles start earliest, and none of the
-// workgroups that share the engines in turn is empty).  Every lane of a wave
-// takes part and gets the answer; false: there are fewer tiles.
-template <class F>
+// sequence i has tiles_of(i): dense, so that none of the workgroups that the
+// engines take in turn is empty (with one tile index for all sequences, short
+// sequences left whole engines idle).  SORTED: the longest of each 64
+// sequences come first, for tiles of unlike cost.  Every lane of a wave takes
+// part and gets the answer; false: there are fewer tiles.
+template <bool SORTED, class F>
 __device__ __forceinline__ bool find_tile(int64_t flat, int64_t batch, F tiles_of, int64_t &seq, int64_t &tile)
 {
     const int lane = threadIdx.x & 63;
@@ -115,17 +117,28 @@ __device__ __forceinline__ bool find_tile(int64_t flat, int64_t batch, F tiles_o
         // at most 2^31 - 1 tiles in all (the grid's limit)
         const int mine = lane < n ? static_cast<int>(tiles_of(base + lane)) : 0;
         int before = 0, total = 0;
-        for (int j = 0; j < n; ++j) {
-            const int other = __builtin_amdgcn_readlane(mine, j);
-            total += other;
-            if (other > mine || (other == mine && j < lane)) before += other;
+        if constexpr (SORTED) {
+            for (int j = 0; j < n; ++j) {
+                const int other = __builtin_amdgcn_readlane(mine, j);
+                total += other;
+                if (other > mine || (other == mine && j < lane)) before += other;
+            }
+        } else {
+            int sum = mine;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int up = __shfl_up(sum, o, 64);
+                if (lane >= o) sum += up;
+            }
+            before = sum - mine;
+            total = __builtin_amdgcn_readlane(sum, 63);
         }
         if (flat >= total) {
             flat -= total;
             continue;
         }
         const int at = static_cast<int>(flat);
-        const uint64_t hit = __ballot(lane < n && at >= before && at - before < mine);
+        const uint64_t hit = __ballot(at >= before && at - before < mine);
         const int who = __builtin_ctzll(hit);
         seq = base + who;
         tile = at - __builtin_amdgcn_readlane(before, who);

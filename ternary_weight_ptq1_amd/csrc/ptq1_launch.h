@@ -151,12 +151,15 @@ hipError_t launch_kv_write(const void *q, int64_t qs, const void *k, int64_t ks,
 hipError_t launch_kv_read(const ptq1_kv_cache &c, const int32_t *table, int64_t max_pages, const int32_t *cu,
                           int64_t batch, int64_t rows, void *k_out, void *v_out, int out_type, hipStream_t s);
 
-// Decode attention: every sequence is cut into chunks of `chunk` tokens (a
-// multiple of 256), one workgroup per chunk, kv head and 16 query heads.
-// part: the chunks' unnormalised rows [batch][hq][chunks][d], then their
-// (maximum, sum) pairs; unused when chunks == 1.
+// Decode attention: the kernel cuts every sequence into pieces of equally
+// many steps of 256 tokens, so many that all sequences' pieces fill the GPU
+// (`shares` workgroups for one kv head); `pieces` bounds their number.  part:
+// the pieces' unnormalised rows [piece][hq][d], then their (maximum, sum)
+// pairs; unused without join (no sequence can be cut).
 struct DecodePlan {
-    int64_t chunk = 0, chunks = 0;
+    int32_t shares = 1;
+    int64_t pieces = 1;
+    bool join = false;
     size_t rows_floats = 0, part_floats = 0;
 };
 DecodePlan decode_plan(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_t max_len);
@@ -164,8 +167,7 @@ hipError_t launch_attn_decode(const DecodePlan &p, const void *q, int q_type, in
                               const ptq1_kv_cache &c, const int32_t *table, int64_t max_pages, const int32_t *lens,
                               int64_t max_len, float scale, void *out, float *part, hipStream_t s);
 
-// Prompt attention.  part: unused (splits == 1) or the splits' unnormalised
-// rows and their (maximum, sum) pairs.
+// Prompt attention.
 struct PromptArgs {
     const void *q, *k, *v;
     int64_t qs, ks, vs;  // row strides in elements
@@ -175,9 +177,18 @@ struct PromptArgs {
     float scale;
     void *out;
 };
-hipError_t launch_attn_prompt(const PromptArgs &a, int dtype, int32_t d, float *part, hipStream_t s);
+// The keys are cut into chunks of `chunk` (a multiple of 128): a tile of query
+// rows that reaches further than one is worked on by several workgroups.
+struct PromptPlan {
+    int64_t chunk = 0, splits = 1;
+    size_t rows_floats = 0, part_floats = 0;
+};
+PromptPlan prompt_plan(int64_t batch, int64_t q_rows, int64_t max_k, int32_t hq, int32_t hkv, int32_t d);
 // tiles of 128 query rows that one kv head's rows may make up
 int64_t prompt_tiles(int64_t batch, int64_t q_rows, int32_t hq, int32_t hkv);
-size_t prompt_part_floats(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_t max_q, int64_t max_k);
+// part: unused (splits == 1), or the chunks' unnormalised rows [row][head]
+// [splits][d], then their (maximum, sum) pairs.
+hipError_t launch_attn_prompt(const PromptArgs &a, int dtype, int32_t d, const PromptPlan &plan, float *part,
+                              hipStream_t s);
 
 }  // namespace ptq1
