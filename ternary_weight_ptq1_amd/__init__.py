@@ -531,6 +531,7 @@ def ptq1_gemm_w2a8(tiled: torch.Tensor, n: int, k: int, x: torch.Tensor, out: to
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}
 _FLOATS = (torch.float32, torch.float16, torch.bfloat16)
 _CACHE_TYPES = (torch.float16, torch.bfloat16, torch.int8)
+_SIXTEEN = (torch.float16, torch.bfloat16)
 
 
 class _CacheStruct(C.Structure):
@@ -580,30 +581,32 @@ def ptq1_kv_cache(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, 
     return KvCache(k, v, *steps)
 
 
-class _On:
-    """The launch's device and stream: makes the operands' device current where it is not, and ties tensors
-    allocated for the call to a stream that is not the allocator's current one."""
+def _elsewhere(device) -> bool:
+    """The operands' device is not the current one (the call is then made under it)."""
+    return device.index is not None and device.index != torch.cuda.current_device()
 
-    def __init__(self, device, stream):
-        self.device = device
-        self.other = device.index is not None and device.index != torch.cuda.current_device()
-        self.guard = torch.cuda.device(device) if self.other else None
-        if self.guard is not None:
-            self.guard.__enter__()
-        current = torch.cuda.current_stream(device)
-        self.stream = current if stream is None else stream
-        self.foreign = self.stream != current
-        self.handle = C.c_void_p(self.stream.cuda_stream)
 
-    def keep(self, *tensors):
-        if self.foreign:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
+def _launch_stream(device, stream):
+    """(handle, stream): the stream to launch on, and the stream itself if it is not the allocator's current one, so
+    that memory allocated for the call can be tied to it (_tie)."""
+    if stream is None:
+        if device.index is None:
+            return None, None
+        return torch._C._cuda_getCurrentRawStream(device.index), None
+    return stream.cuda_stream, stream if stream != torch.cuda.current_stream(device) else None
 
-    def done(self):
-        if self.guard is not None:
-            self.guard.__exit__(None, None, None)
+
+def _tie(stream, *tensors):
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _plain(t, dtype, numel: int, device) -> bool:
+    """A contiguous tensor of exactly this type, size and device (_dev says what is wrong with any other)."""
+    return type(t) is torch.Tensor and t.dtype is dtype and t.numel() == numel and t.device == device \
+        and t.is_contiguous() and t.is_cuda
 
 
 def _rows3(t: torch.Tensor, name: str, dtype, device) -> tuple[int, int, int, int]:
@@ -614,17 +617,19 @@ def _rows3(t: torch.Tensor, name: str, dtype, device) -> tuple[int, int, int, in
         raise ValueError(f"{name} must be a device tensor")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [rows, heads, head_dim]")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if t.dtype not in dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
     rows, heads, d = t.shape
     sr, sh, sd = t.stride()
-    if t.numel() > 0 and ((d > 1 and sd != 1) or (heads > 1 and sh != d)):
+    if ((d > 1 and sd != 1) or (heads > 1 and sh != d)) and rows > 0 and heads > 0 and d > 0:
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    if rows > 1 and heads > 0 and sr < heads * d:
-        raise ValueError(f"{name}: rows overlap one another (stride {sr})")
-    return rows, heads, d, sr if rows > 1 else heads * d
+    if rows > 1:
+        if sr < heads * d:
+            raise ValueError(f"{name}: rows overlap one another (stride {sr})")
+        return rows, heads, d, sr
+    return rows, heads, d, heads * d
 
 
 def _kv(cache) -> KvCache:
@@ -650,23 +655,29 @@ def ptq1_kv_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, slot
     without q."""
     kv = _kv(cache)
     dv = kv.device
+    if _elsewhere(dv):
+        with torch.cuda.device(dv):
+            return ptq1_kv_write(q, k, v, slots, cache, positions, cos_sin, q_dtype, out, stream)
     n, h, d, ks = _rows3(k, "k", _FLOATS, dv)
-    if (h, d) != (kv.n_kv_heads, kv.head_dim):
+    if h != kv.n_kv_heads or d != kv.head_dim:
         raise ValueError(f"k has {h} heads of {d}, the cache {kv.n_kv_heads} of {kv.head_dim}")
-    nv, hv, d2, vs = _rows3(v, "v", k.dtype, dv)
-    if (nv, hv, d2) != (n, h, d):
+    src = k.dtype
+    nv, hv, d2, vs = _rows3(v, "v", (src,), dv)
+    if nv != n or hv != h or d2 != d:
         raise ValueError(f"v must be {[n, h, d]}")
     hq = qs = 0
     if q is not None:
-        nq, hq, d3, qs = _rows3(q, "q", k.dtype, dv)
-        if (nq, d3) != (n, d):
+        nq, hq, d3, qs = _rows3(q, "q", (src,), dv)
+        if nq != n or d3 != d:
             raise ValueError(f"q must be [{n}, n_q_heads, {d}]")
-        q_dtype = q.dtype if q_dtype is None else q_dtype
-        if q_dtype not in _FLOATS:
+        if q_dtype is None:
+            q_dtype = src
+        elif q_dtype not in _FLOATS:
             raise ValueError(f"q_dtype must be one of {_FLOATS}, got {q_dtype}")
     elif out is not None:
         raise ValueError("out needs q")
-    _dev(slots, "slots", torch.int64, numel=n, device=dv)
+    if not _plain(slots, torch.int64, n, dv):
+        _dev(slots, "slots", torch.int64, numel=n, device=dv)
     rot = n_pos = 0
     if cos_sin is not None:
         _dev(cos_sin, "cos_sin", torch.float32, device=dv)
@@ -675,24 +686,21 @@ def ptq1_kv_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, slot
         n_pos, rot = cos_sin.shape
         if positions is None:
             raise ValueError("cos_sin needs positions")
-    if positions is not None:
+    if positions is not None and not _plain(positions, torch.int32, n, dv):
         _dev(positions, "positions", torch.int32, numel=n, device=dv)
-    on = _On(dv, stream)
-    try:
-        fresh = None
-        if q is not None:
-            if out is None:
-                out = fresh = torch.empty((n, hq, d), dtype=q_dtype, device=dv)
-            else:
-                _dev(out, "out", q_dtype, numel=n * hq * d, device=dv)
-        on.keep(fresh)
-        _check("ptq1_kv_write",
-               lib().ptq1_kv_write(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _DTYPES[k.dtype], n, hq,
-                                   _ptr(positions) if rot else None, _ptr(cos_sin) if rot else None, n_pos, rot,
-                                   _ptr(slots), _ptr(out), _DTYPES[q_dtype] if q is not None else 0, kv._ref,
-                                   on.handle))
-    finally:
-        on.done()
+    handle, other = _launch_stream(dv, stream)
+    if q is not None:
+        if out is None:
+            out = torch.empty((n, hq, d), dtype=q_dtype, device=dv)
+            _tie(other, out)
+        else:
+            _dev(out, "out", q_dtype, numel=n * hq * d, device=dv)
+    status = lib().ptq1_kv_write(0 if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPES[src],
+                                 n, hq, positions.data_ptr() if rot else 0, cos_sin.data_ptr() if rot else 0, n_pos, rot,
+                                 slots.data_ptr(), 0 if out is None else out.data_ptr(),
+                                 _DTYPES[src if q is None else q_dtype], kv._ref, handle)
+    if status:
+        _check("ptq1_kv_write", status)
     return out
 
 
@@ -702,6 +710,9 @@ def ptq1_kv_read(cache: KvCache, block_table: torch.Tensor, cu_seqlens: torch.Te
     packed: k and v [n_rows, n_kv_heads, head_dim] of dtype.  cu_seqlens int32 [batch + 1]."""
     kv = _kv(cache)
     dv = kv.device
+    if _elsewhere(dv):
+        with torch.cuda.device(dv):
+            return ptq1_kv_read(cache, block_table, cu_seqlens, n_rows, dtype, out, stream)
     _dev(cu_seqlens, "cu_seqlens", torch.int32, device=dv)
     batch = cu_seqlens.numel() - 1
     if batch < 0:
@@ -711,23 +722,19 @@ def ptq1_kv_read(cache: KvCache, block_table: torch.Tensor, cu_seqlens: torch.Te
         raise ValueError(f"dtype must be one of {_FLOATS}, got {dtype}")
     if n_rows < 0:
         raise ValueError(f"n_rows = {n_rows} is negative")
-    shape = (n_rows, kv.n_kv_heads, kv.head_dim)
-    count = n_rows * kv.n_kv_heads * kv.head_dim
-    on = _On(dv, stream)
-    try:
-        if out is None:
-            k = torch.empty(shape, dtype=dtype, device=dv)
-            v = torch.empty(shape, dtype=dtype, device=dv)
-            on.keep(k, v)
-        else:
-            k, v = out
-            _dev(k, "k_out", dtype, numel=count, device=dv)
-            _dev(v, "v_out", dtype, numel=count, device=dv)
-        _check("ptq1_kv_read",
-               lib().ptq1_kv_read(kv._ref, _ptr(block_table), max_pages, _ptr(cu_seqlens), batch, n_rows, _ptr(k),
-                                  _ptr(v), _DTYPES[dtype], on.handle))
-    finally:
-        on.done()
+    handle, other = _launch_stream(dv, stream)
+    if out is None:
+        k, v = torch.empty((2, n_rows, kv.n_kv_heads, kv.head_dim), dtype=dtype, device=dv).unbind(0)
+        _tie(other, k)
+    else:
+        k, v = out
+        count = n_rows * kv.n_kv_heads * kv.head_dim
+        _dev(k, "k_out", dtype, numel=count, device=dv)
+        _dev(v, "v_out", dtype, numel=count, device=dv)
+    status = lib().ptq1_kv_read(kv._ref, block_table.data_ptr(), max_pages, cu_seqlens.data_ptr(), batch, n_rows,
+                                k.data_ptr(), v.data_ptr(), _DTYPES[dtype], handle)
+    if status:
+        _check("ptq1_kv_read", status)
     return k, v
 
 
@@ -740,31 +747,36 @@ def ptq1_attn_decode(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor,
     batch, n_q_heads, n_kv_heads, head_dim, max_len) bytes."""
     kv = _kv(cache)
     dv = kv.device
+    if _elsewhere(dv):
+        with torch.cuda.device(dv):
+            return ptq1_attn_decode(q, cache, block_table, seq_lens, scale, max_len, out, ws, stream)
     _dev(q, "q", _FLOATS, device=dv)
     if q.dim() != 3 or q.shape[2] != kv.head_dim:
         raise ValueError(f"q must be [batch, n_q_heads, {kv.head_dim}]")
     batch, hq, d = q.shape
     max_pages = _table(block_table, batch, dv)
-    _dev(seq_lens, "seq_lens", torch.int32, numel=batch, device=dv)
+    if not _plain(seq_lens, torch.int32, batch, dv):
+        _dev(seq_lens, "seq_lens", torch.int32, numel=batch, device=dv)
     if max_len is None:
         max_len = max_pages * kv.page_size
-    on = _On(dv, stream)
-    try:
-        need = lib().ptq1_attn_decode_workspace_bytes(batch, hq, kv.n_kv_heads, d, max_len)
-        mine = ws is None and need > 0
-        ws, wsb = _ws(need, dv, ws)
-        fresh = None
-        if out is None:
-            out = fresh = torch.empty((batch, hq, d), dtype=q.dtype, device=dv)
-        else:
-            _dev(out, "out", q.dtype, numel=q.numel(), device=dv)
-        on.keep(fresh, ws if mine else None)
-        _check("ptq1_attn_decode",
-               lib().ptq1_attn_decode(_ptr(q), _DTYPES[q.dtype], batch, hq, kv._ref, _ptr(block_table), max_pages,
-                                      _ptr(seq_lens), max_len, d ** -0.5 if scale is None else scale, _ptr(out),
-                                      _ptr(ws), wsb, on.handle))
-    finally:
-        on.done()
+    handle, other = _launch_stream(dv, stream)
+    wsb = lib().ptq1_attn_decode_workspace_bytes(batch, hq, kv.n_kv_heads, d, max_len)
+    if ws is None:
+        if wsb:
+            ws = torch.empty(wsb, dtype=torch.uint8, device=dv)
+            _tie(other, ws)
+    else:
+        ws, wsb = _ws(wsb, dv, ws)
+    if out is None:
+        out = torch.empty((batch, hq, d), dtype=q.dtype, device=dv)
+        _tie(other, out)
+    else:
+        _dev(out, "out", q.dtype, numel=q.numel(), device=dv)
+    status = lib().ptq1_attn_decode(q.data_ptr(), _DTYPES[q.dtype], batch, hq, kv._ref, block_table.data_ptr(), max_pages,
+                                    seq_lens.data_ptr(), max_len, d ** -0.5 if scale is None else scale, out.data_ptr(),
+                                    0 if ws is None else ws.data_ptr(), wsb, handle)
+    if status:
+        _check("ptq1_attn_decode", status)
     return out
 
 
@@ -781,35 +793,42 @@ def ptq1_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     dv = q.device
-    nq, hq, d, qs = _rows3(q, "q", (torch.float16, torch.bfloat16), dv)
-    nk, hkv, dk, ks = _rows3(k, "k", q.dtype, dv)
-    nv, hv, d2, vs = _rows3(v, "v", q.dtype, dv)
-    if dk != d or (nv, hv, d2) != (nk, hkv, dk):
+    if _elsewhere(dv):
+        with torch.cuda.device(dv):
+            return ptq1_attn_prompt(q, k, v, cu_q, cu_k, max_q, max_k, causal, scale, out, ws, stream)
+    nq, hq, d, qs = _rows3(q, "q", _SIXTEEN, dv)
+    kind = q.dtype
+    nk, hkv, dk, ks = _rows3(k, "k", (kind,), dv)
+    nv, hv, d2, vs = _rows3(v, "v", (kind,), dv)
+    if dk != d or nv != nk or hv != hkv or d2 != d:
         raise ValueError(f"k and v must both be [n_k_rows, n_kv_heads, {d}]")
     _dev(cu_q, "cu_q", torch.int32, device=dv)
     batch = cu_q.numel() - 1
     if batch < 0:
         raise ValueError("cu_q must hold batch + 1 offsets")
-    _dev(cu_k, "cu_k", torch.int32, numel=batch + 1, device=dv)
+    if not _plain(cu_k, torch.int32, batch + 1, dv):
+        _dev(cu_k, "cu_k", torch.int32, numel=batch + 1, device=dv)
     max_q = nq if max_q is None else min(max_q, nq)
     max_k = nk if max_k is None else min(max_k, nk)
-    on = _On(dv, stream)
-    try:
-        need = lib().ptq1_attn_prompt_workspace_bytes(batch, nq, max_k, hq, hkv, d)
-        mine = ws is None and need > 0
-        ws, wsb = _ws(need, dv, ws)
-        fresh = None
-        if out is None:
-            out = fresh = torch.empty((nq, hq, d), dtype=q.dtype, device=dv)
-        else:
-            _dev(out, "out", q.dtype, numel=nq * hq * d, device=dv)
-        on.keep(fresh, ws if mine else None)
-        _check("ptq1_attn_prompt",
-               lib().ptq1_attn_prompt(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _DTYPES[q.dtype], _ptr(cu_q), _ptr(cu_k),
-                                      batch, nq, nk, max_q, max_k, hq, hkv, d, 1 if causal else 0,
-                                      d ** -0.5 if scale is None else scale, _ptr(out), _ptr(ws), wsb, on.handle))
-    finally:
-        on.done()
+    handle, other = _launch_stream(dv, stream)
+    wsb = lib().ptq1_attn_prompt_workspace_bytes(batch, nq, max_k, hq, hkv, d)
+    if ws is None:
+        if wsb:
+            ws = torch.empty(wsb, dtype=torch.uint8, device=dv)
+            _tie(other, ws)
+    else:
+        ws, wsb = _ws(wsb, dv, ws)
+    if out is None:
+        out = torch.empty((nq, hq, d), dtype=kind, device=dv)
+        _tie(other, out)
+    else:
+        _dev(out, "out", kind, numel=nq * hq * d, device=dv)
+    status = lib().ptq1_attn_prompt(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPES[kind], cu_q.data_ptr(),
+                                    cu_k.data_ptr(), batch, nq, nk, max_q, max_k, hq, hkv, d, 1 if causal else 0,
+                                    d ** -0.5 if scale is None else scale, out.data_ptr(),
+                                    0 if ws is None else ws.data_ptr(), wsb, handle)
+    if status:
+        _check("ptq1_attn_prompt", status)
     return out
 
 
