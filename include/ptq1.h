@@ -453,7 +453,8 @@ ptq1_status ptq1_kv_write(const void *q, int64_t q_stride, const void *k, int64_
  * page is outside [0, n_pages), or past max_pages, reads as NaN.  An int8
  * value is step * code, rounded once to out_dtype.
  * Errors: NULL, SHAPE, ALIGN, ALIAS, OVERFLOW, UNSUPPORTED (types, head_dim,
- * page_size, batch * n_kv_heads > 65535, n_rows > 2^31 - 1). */
+ * page_size, more than 2^24 - 1 tiles of 64 tokens of a head, n_rows >
+ * 2^31 - 1). */
 ptq1_status ptq1_kv_read(const ptq1_kv_cache *cache, const int32_t *block_table, int64_t max_pages,
                          const int32_t *cu_seqlens, int64_t batch, int64_t n_rows, void *k_out, void *v_out,
                          int32_t out_dtype, hipStream_t stream);

@@ -1247,10 +1247,8 @@ ptq1_status ptq1_kv_read(const ptq1_kv_cache *cache, const int32_t *block_table,
     if (max_pages < 0) return fail(PTQ1_ERR_SHAPE, "max_pages = %lld is negative", (long long)max_pages);
     if (n_rows < 0) return fail(PTQ1_ERR_SHAPE, "n_rows = %lld is negative", (long long)n_rows);
     if (n_rows > kMaxRows32) return fail(PTQ1_ERR_UNSUPPORTED, "n_rows = %lld > 2^31 - 1", (long long)n_rows);
-    if (n_rows > kMaxBlocks256 * 32)
-        return fail(PTQ1_ERR_UNSUPPORTED, "n_rows = %lld too large", (long long)n_rows);
-    if (batch > kMaxGridY || batch * cache->n_kv_heads > kMaxGridY)
-        return fail(PTQ1_ERR_UNSUPPORTED, "batch * n_kv_heads > %lld", (long long)kMaxGridY);
+    if (batch > kMaxRows32 || (n_rows / 64 + batch) * cache->n_kv_heads > kMaxBlocks256)
+        return fail(PTQ1_ERR_UNSUPPORTED, "more than 2^24 - 1 tiles of 64 tokens of a head");
     if (!float_type(out_dtype)) return fail(PTQ1_ERR_UNSUPPORTED, "out_dtype %d (F32, F16 or BF16)", out_dtype);
     if (batch == 0 || n_rows == 0) return ok();
     int64_t table = 0;
