@@ -518,7 +518,7 @@ ptq1_status ptq1_attn_decode(const void *q, int32_t q_dtype, int64_t batch, int3
  * order; the workspace (for max_k as given, or n_k_rows if that is less) holds
  * their parts.
  * Errors: NULL, SHAPE, ALIGN, ALIAS, OVERFLOW, WORKSPACE, UNSUPPORTED (types,
- * head_dim, more than 2^31 - 1025 rows of one kv head or 2^24 - 1 tiles of 128
+ * head_dim, more than 2^31 - 1025 rows of one kv head or 2^23 tiles of 128
  * query rows, k_stride or v_stride above 2^24). */
 size_t ptq1_attn_prompt_workspace_bytes(int64_t batch, int64_t n_q_rows, int64_t max_k, int32_t n_q_heads,
                                         int32_t n_kv_heads, int32_t head_dim);

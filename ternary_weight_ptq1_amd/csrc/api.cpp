@@ -1356,8 +1356,8 @@ ptq1_status ptq1_attn_prompt(const void *q, int64_t q_stride, const void *k, int
         return fail(PTQ1_ERR_UNSUPPORTED, "more than 2^31 - 1025 rows of one kv head");
     if (k_stride > kMaxStride || v_stride > kMaxStride)
         return fail(PTQ1_ERR_UNSUPPORTED, "k_stride or v_stride above 2^24 elements");
-    if (ptq1::prompt_tiles(batch, n_q_rows, n_q_heads, n_kv_heads) * n_kv_heads > kMaxBlocks256)
-        return fail(PTQ1_ERR_UNSUPPORTED, "more than 2^24 - 1 tiles of 128 query rows");
+    if (ptq1::prompt_tiles(batch, n_q_rows, n_q_heads, n_kv_heads) * n_kv_heads >= kMaxBlocks256 / 2)
+        return fail(PTQ1_ERR_UNSUPPORTED, "more than 2^23 tiles of 128 query rows");
     if (batch == 0 || n_q_rows == 0 || max_q == 0) return ok();
     int64_t qb, kbytes, vbytes;
     const int64_t d = head_dim;

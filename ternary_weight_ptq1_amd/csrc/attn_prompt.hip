@@ -30,10 +30,6 @@
 namespace ptq1 {
 namespace {
 
-constexpr int kPrWaves = 4;
-constexpr int kPrThreads = 64 * kPrWaves;
-constexpr int kPrRows = 32 * kPrWaves;  // query rows of a workgroup
-constexpr int kJoinParts = 4;           // workgroups that join one tile
 constexpr int kAhead = 4;               // K reads ahead of their products
 
 typedef short at_s16x4 __attribute__((ext_vector_type(4)));
@@ -41,7 +37,12 @@ typedef __attribute__((address_space(3))) at_s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) void lds_void;
 constexpr int kBufferFlags = 0x00027000;  // raw buffer of bytes
 
-constexpr int prompt_keys(int d) { return d == 256 ? 32 : 64; }
+constexpr int kKeys = 64;  // keys of a tile
+
+// Query rows of a workgroup: 32 a wave, or a pair of waves (256-wide heads).
+constexpr int kPrRows = 128;
+// Waves of a workgroup.
+constexpr int prompt_waves(int d) { return d == 256 ? 8 : 4; }
 
 // The 16-byte piece p of key row r of a K or V tile lies at piece p ^ swizzle
 // of that row.  K is read 16 rows at one piece at a time, V 4 rows at four
@@ -91,43 +92,215 @@ __device__ __forceinline__ bool clear_non_finite(at_u32x4 &w)
     return found;
 }
 
-// The flat tile's sequence and its place there, counted from the end; only
-// rows that exist count.
-__device__ __forceinline__ bool prompt_tile(const PromptArgs &a, int64_t flat, int64_t &b, int64_t &at)
+// Keys that query `tok` of a sequence sees, with `off` keys before its first
+// query and `lk` in all: the first so many.
+__device__ __forceinline__ int visible(const PromptArgs &a, int tok, int off, int lk)
 {
-    return find_tile<true>(
-        flat, a.batch,
-        [&](int64_t i) {
-            const int64_t first = a.cu_q[i], end = a.cu_q[i + 1];
-            const int64_t n = (end < a.q_rows ? end : a.q_rows) - (first > 0 ? first : 0);
-            return n > 0 ? (n * (a.hq / a.hkv) + kPrRows - 1) / kPrRows : 0;
-        },
-        b, at);
+    const int n = a.causal ? tok + off + 1 : lk;
+    return n > 0 ? n : 0;
 }
 
-// A sequence past its bounds, or with rows that are not there: its rows are NaN.
-__device__ __forceinline__ bool prompt_refused(const PromptArgs &a, int64_t q0, int64_t lq, int64_t k0, int64_t lk)
+// One tile of R query rows of one kv head, and the keys of one workgroup (all
+// below 2^31: the host has seen to it).
+struct PromptTile {
+    int q0, k0, lk, off;    // the sequence: its first rows, its keys, keys before its first query
+    int rows, row0, end;    // its rows; this tile's first one and the one behind its last
+    int group, kh;
+    int reach;              // keys that some row of the tile sees; of them, this workgroup's:
+    int first, any, all;    // the first one, the one behind the last, and where the first comes that not every row sees
+    bool split;             // there are several workgroups
+};
+
+// Workgroups go to the eight XCDs in turn, each with an L2 of its own: heads
+// vary fastest, so that a head's tiles meet on as few XCDs as its number
+// allows (eight heads: one each).  False: nothing (more) to do.  The rows of
+// a sequence past its bounds, or with rows that are not there, become NaN.
+template <typename T, int D>
+__device__ __forceinline__ bool prompt_tile(const PromptArgs &a, const PromptPlan &plan, int part, bool join, PromptTile &t)
 {
-    return q0 < 0 || k0 < 0 || q0 + lq > a.q_rows || lk < 0 || k0 + lk > a.k_rows || lq > a.max_q || lk > a.max_k;
+    constexpr int R = kPrRows;
+    t.group = a.hq / a.hkv;
+    t.kh = static_cast<int>(blockIdx.x % static_cast<uint32_t>(a.hkv));
+    int64_t b, at;
+    if (!find_tile<true>(
+            blockIdx.x / static_cast<uint32_t>(a.hkv), a.batch,
+            [&](int64_t i) {
+                // only rows that exist count
+                const int64_t first = a.cu_q[i], end = a.cu_q[i + 1];
+                const int64_t n = (end < a.q_rows ? end : a.q_rows) - (first > 0 ? first : 0);
+                return n > 0 ? (n * t.group + R - 1) / R : 0;
+            },
+            b, at))
+        return false;
+    const int64_t q0 = a.cu_q[b], lq = a.cu_q[b + 1] - q0, k0 = a.cu_k[b], lk = a.cu_k[b + 1] - k0;
+    if (q0 < 0 || k0 < 0 || q0 + lq > a.q_rows || lk < 0 || k0 + lk > a.k_rows || lq > a.max_q || lk > a.max_k) {
+        const int64_t r = (q0 < 0 ? -q0 * t.group : 0) + at * R + threadIdx.x, tok = q0 + r / t.group;
+        if (!join && part == 0 && threadIdx.x < R && tok < q0 + lq && tok < a.q_rows) {
+            T *dst = static_cast<T *>(a.out) + (tok * a.hq + t.kh * t.group + r % t.group) * D;
+            const float n = __builtin_nanf("");
+            for (int e = 0; e < D; e += 4) store4(dst + e, at_f32x4{n, n, n, n});
+        }
+        return false;
+    }
+    t.q0 = static_cast<int>(q0);
+    t.k0 = static_cast<int>(k0);
+    t.lk = static_cast<int>(lk);
+    t.off = static_cast<int>(lk - lq);
+    t.rows = static_cast<int>(lq) * t.group;
+    // the last rows see the most keys: they start first
+    t.row0 = ((t.rows + R - 1) / R - 1 - static_cast<int>(at)) * R;
+    t.end = t.row0 + R < t.rows ? t.row0 + R : t.rows;
+    t.reach = visible(a, (t.end - 1) / t.group, t.off, t.lk);
+    t.split = t.reach > plan.chunk;
+    t.first = part * plan.chunk;
+    if (t.first >= t.reach && part > 0) return false;
+    t.any = t.split && t.reach - t.first > plan.chunk ? t.first + plan.chunk : t.reach;
+    const int every = visible(a, t.row0 / t.group, t.off, t.lk);
+    t.all = every < t.any ? every : t.any;
+    return true;
 }
 
-// Keys that query `tok` of a sequence sees: the first so many.
-__device__ __forceinline__ int visible(const PromptArgs &a, int64_t tok, int64_t off, int64_t lk)
+// One lane's query row (column lane % 32 of its tile of 32).
+struct PromptRow {
+    bool is;
+    int tok, head;
+    int seen;  // keys that it sees
+};
+__device__ __forceinline__ PromptRow prompt_row(const PromptArgs &a, const PromptTile &t, int row)
 {
-    const int64_t n = a.causal ? tok + off + 1 : lk;
-    return static_cast<int>(n > 0 ? n : 0);
+    PromptRow r;
+    r.is = row < t.rows;
+    const int at = r.is ? row : t.rows - 1;
+    r.tok = at / t.group;
+    r.head = t.kh * t.group + at % t.group;
+    r.seen = visible(a, r.tok, t.off, t.lk);
+    return r;
+}
+
+// Adds to O^T, dimensions d0 + 32 i + ..., the NaNs and infinities among the
+// values from key `border` on that the row sees (they were left out of the
+// products, or a zero weight would have carried them to rows that do not).
+template <typename T, int N>
+__device__ __forceinline__ void add_non_finite(const PromptArgs &a, const PromptTile &t, const PromptRow &row, int border,
+                                               int d, int d0, int half, at_f32x16 (&o)[N])
+{
+    for (int r = border; r < t.any; ++r) {
+        const T *src = static_cast<const T *>(a.v) + static_cast<int64_t>(t.k0 + r) * a.vs + static_cast<int64_t>(t.kh) * d + d0 + 4 * half;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+                const at_f32x4 x = load4(src + 32 * i + 2 * j);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (r < row.seen && !(fabsf(x[e]) <= 3.4028235e38f)) o[i][j + e] += x[e];
+            }
+    }
+}
+
+// The row's dimensions d0 + 32 i + 8 b + 4 half + e, finished, or as one part of several.
+template <typename T, int N>
+__device__ __forceinline__ void store_rows(const PromptArgs &a, const PromptPlan &plan, const PromptTile &t, const PromptRow &row,
+                                           int part, int d, int d0, int half, const at_f32x16 (&o)[N], float m, float l,
+                                           float *parts)
+{
+    const int64_t at = static_cast<int64_t>(t.q0 + row.tok) * a.hq + row.head;
+    if (!t.split) {
+        T *dst = static_cast<T *>(a.out) + at * d + d0 + 4 * half;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+                store4(dst + 32 * i + 2 * j, at_f32x4{o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]});
+        return;
+    }
+    const int64_t slot = at * plan.splits + part;
+    float *dst = parts + slot * d + d0 + 4 * half;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+            store4(dst + 32 * i + 2 * j, at_f32x4{o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]});
+    if (half == 0 && d0 == 0) {
+        parts[plan.rows_floats + slot * 2] = m;
+        parts[plan.rows_floats + slot * 2 + 1] = l;
+    }
+}
+
+// A NaN or an infinity leaves a V tile in LDS (zeros in its place); true if there was one.
+template <typename T, int D>
+__device__ __forceinline__ bool clean_tile(T *vb)
+{
+    bool odd = false;
+    for (int i = threadIdx.x; i < kKeys * (D / 8); i += 64 * prompt_waves(D)) {
+        at_u32x4 w = *reinterpret_cast<const at_u32x4 *>(vb + 8 * i);
+        if (clear_non_finite<T>(w)) {
+            *reinterpret_cast<at_u32x4 *>(vb + 8 * i) = w;
+            odd = true;
+        }
+    }
+    return odd;
+}
+
+// A lane's share of copying tiles of 64 rows straight from memory into LDS:
+// 64 pieces of 16 bytes per wave instruction at consecutive places; the lane
+// picks the piece that belongs there.  The tile's address is in the (scalar)
+// buffer descriptor, the lane's part a 32-bit offset that stays: piece i is
+// i * RS rows further on, where the swizzle is the same again after KC
+// pieces.  The descriptor ends with row `rows` - 1: nothing behind it is read.
+template <typename T, int D, bool V>
+struct Staging {
+    static constexpr int W = prompt_waves(D), P = D / 8, RS = 64 * W / P, N = kKeys / RS;
+    static constexpr int KC = 1;
+    static_assert(RS % 16 == 0 || (V && RS % 4 == 0), "the swizzle is the same RS rows further on");
+    const char *base;
+    int64_t stride;  // bytes
+    uint32_t off[KC];
+    __device__ __forceinline__ Staging(const void *src, int64_t row, int64_t row_stride, int kh)
+        : base(reinterpret_cast<const char *>(static_cast<const T *>(src) + row * row_stride + static_cast<int64_t>(kh) * D)),
+          stride(row_stride * 2)
+    {
+#pragma unroll
+        for (int i = 0; i < KC; ++i) {
+            const uint32_t r = i * RS + threadIdx.x / P, p = threadIdx.x % P;
+            off[i] = r * static_cast<uint32_t>(stride) + 16 * (p ^ (V ? v_swizzle<D>(r) : k_swizzle<D>(r)));
+        }
+    }
+    // rows n0 .. n0 + 63, of `rows`
+    __device__ __forceinline__ void copy(T *dst, int n0, int rows) const
+    {
+        const uint32_t step = static_cast<uint32_t>(stride);
+        const uint32_t more = rows - 1 - n0 < kKeys - 1 ? rows - 1 - n0 : kKeys - 1;  // rows behind the first
+        const char *src = base + n0 * stride;
+        const int wave = threadIdx.x >> 6;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            copy_to_lds(src, more * step + 2 * D, off[i % KC] + (i / KC * KC * RS) * step, dst + (i * W + wave) * 512);
+    }
+};
+
+// The V operand of keys 16 u .. + 15, dimensions 32 i .. + 31: lane: key 16 u
+// + 4 half + (lane % 16) / 4 (then + 8), dimensions 32 i + 16 ((lane / 16) %
+// 2) + 4 (lane % 4) of two transposing reads.
+template <typename T, int D>
+__device__ __forceinline__ typename Op16<T>::x8 read_v(const T *vb, int u, int i)
+{
+    const int lane = threadIdx.x & 63;
+    const int r = 16 * u + 4 * (lane >> 5) + ((lane & 15) >> 2);
+    const int d = 32 * i + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    const at_s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + v_place<D>(r, d >> 3) + (d & 7)));
+    const at_s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + v_place<D>(r + 8, d >> 3) + (d & 7)));
+    return __builtin_bit_cast(typename Op16<T>::x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(PromptArgs a, PromptPlan plan, float *part)
+__global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptArgs a, PromptPlan plan, float *parts)
 {
     typedef typename Op16<T>::x8 x8;
-    constexpr int BN = prompt_keys(D);      // keys of a tile
+    constexpr int BN = kKeys;
     constexpr int KT = BN / 32;             // score tiles
     constexpr int DT = D / 32;              // output tiles
     constexpr int KK = D / 16;              // MFMA steps over the head dimension
-    constexpr int P = D / 8;                // 16-byte pieces of a row
-    constexpr int NLD = BN * P / kPrThreads;  // pieces a thread stages, of K and of V
 
     // Two tiles each: separate objects, so that the copies into one need not
     // have ended before the other is read.
@@ -136,87 +309,22 @@ __global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(Pr
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = lane & 31, half = lane >> 5;
-
-    // Workgroups go to the eight XCDs in turn, each with an L2 of its own.
-    // Heads vary fastest, so that a head's tiles meet on as few XCDs as its
-    // number allows (eight heads: one each).
-    const int group = a.hq / a.hkv;
-    const int kh = static_cast<int>(blockIdx.x % static_cast<uint32_t>(a.hkv));
-    const int64_t flat = blockIdx.x / static_cast<uint32_t>(a.hkv);
-    int64_t b, at;
-    if (!prompt_tile(a, flat, b, at)) return;
-    const int64_t q0 = a.cu_q[b], k0 = a.cu_k[b];
-    const int64_t lq = a.cu_q[b + 1] - q0, lk = a.cu_k[b + 1] - k0;
-    const int64_t rows = lq * group;
-    if (prompt_refused(a, q0, lq, k0, lk)) {
-        const int64_t r = (q0 < 0 ? -q0 * group : 0) + at * kPrRows + threadIdx.x, tok = q0 + r / group;
-        if (blockIdx.y == 0 && threadIdx.x < kPrRows && r < rows && tok < a.q_rows) {
-            T *dst = static_cast<T *>(a.out) + (tok * a.hq + kh * group + r % group) * D;
-            const float n = __builtin_nanf("");
-            for (int e = 0; e < D; e += 4) store4(dst + e, at_f32x4{n, n, n, n});
-        }
-        return;
-    }
-    // the last rows see the most keys: they start first
-    const int64_t tile = (rows + kPrRows - 1) / kPrRows - 1 - at;
-
-    const int64_t row = tile * kPrRows + 32 * wave + col;
-    const int64_t rowc = row < rows ? row : rows - 1;
-    const int32_t tok = static_cast<int32_t>(rowc / group), head = static_cast<int32_t>(rowc % group);
-    const int64_t off = lk - lq;
-    // keys below `seen` are visible to this lane's row
-    const int seen = visible(a, tok, off, lk);
-    const int64_t tok_first = tile * kPrRows / group;
-    const int64_t row_last = (tile + 1) * kPrRows < rows ? (tile + 1) * kPrRows - 1 : rows - 1;
-    // keys that some row of the tile sees; of them, this workgroup's
-    const int reach = visible(a, row_last / group, off, lk);
-    const int first = static_cast<int>(blockIdx.y * plan.chunk);
-    if (first >= reach && blockIdx.y > 0) return;
-    const bool split = reach > plan.chunk;
-    const int any = split && reach - first > plan.chunk ? first + static_cast<int>(plan.chunk) : reach;
-    // keys that every row sees
-    const int every = visible(a, tok_first, off, lk), all = every < any ? every : any;
+    const int piece = static_cast<int>(blockIdx.y);
+    PromptTile t;
+    if (!prompt_tile<T, D>(a, plan, piece, false, t)) return;
+    const int any = t.any, all = t.all;
+    int seen = 0;  // (set for the border tiles; the others use every key)
 
     // ---- queries: B operand, column = row, k = 16 kk + 8 half + j
     x8 qf[KK];
     {
-        const T *qp = static_cast<const T *>(a.q) + (q0 + tok) * a.qs + static_cast<int64_t>(kh * group + head) * D;
+        const PromptRow row = prompt_row(a, t, t.row0 + 32 * wave + col);
+        const T *qp = static_cast<const T *>(a.q) + static_cast<int64_t>(t.q0 + row.tok) * a.qs + static_cast<int64_t>(row.head) * D;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) qf[kk] = *reinterpret_cast<const x8 *>(qp + 16 * kk + 8 * half);
     }
-
-    // ---- staging: straight from memory into LDS, 64 pieces of 16 bytes per
-    // wave instruction at consecutive places; the lane picks the piece that
-    // belongs there.  The tile's address is in the (scalar) buffer
-    // descriptor, the lane's part a 32-bit offset that stays.  The
-    // descriptor ends with the last visible key's row: nothing behind it is read.
-    const char *kbase = reinterpret_cast<const char *>(static_cast<const T *>(a.k) + k0 * a.ks + static_cast<int64_t>(kh) * D);
-    const char *vbase = reinterpret_cast<const char *>(static_cast<const T *>(a.v) + k0 * a.vs + static_cast<int64_t>(kh) * D);
-    const uint32_t kstep = static_cast<uint32_t>(a.ks) * 2, vstep = static_cast<uint32_t>(a.vs) * 2;
-    // piece i of a lane: rows i * RS further on, where the swizzle is the
-    // same again after KC pieces
-    constexpr int RS = kPrThreads / P, KC = D == 256 ? 2 : 1;
-    uint32_t koff[KC], voff;
-#pragma unroll
-    for (int i = 0; i < KC; ++i) {
-        const uint32_t r = i * RS + threadIdx.x / P, p = threadIdx.x % P;
-        koff[i] = r * kstep + 16 * (p ^ k_swizzle<D>(r));
-        if (i == 0) voff = r * vstep + 16 * (p ^ v_swizzle<D>(r));
-    }
-    auto stage_k = [&](T *dst, int n0) {
-        const uint32_t more = any - 1 - n0 < BN - 1 ? any - 1 - n0 : BN - 1;  // rows behind the first
-        const char *src = kbase + n0 * (a.ks * 2);
-#pragma unroll
-        for (int i = 0; i < NLD; ++i)
-            copy_to_lds(src, more * kstep + 2 * D, koff[i % KC] + (i / KC * KC * RS) * kstep, dst + (i * kPrWaves + wave) * 512);
-    };
-    auto stage_v = [&](T *dst, int n0) {
-        const uint32_t more = any - 1 - n0 < BN - 1 ? any - 1 - n0 : BN - 1;
-        const char *src = vbase + n0 * (a.vs * 2);
-#pragma unroll
-        for (int i = 0; i < NLD; ++i)
-            copy_to_lds(src, more * vstep + 2 * D, voff + (i * RS) * vstep, dst + (i * kPrWaves + wave) * 512);
-    };
+    const Staging<T, D, false> keys(a.k, t.k0, a.ks, t.kh);
+    const Staging<T, D, true> values(a.v, t.k0, a.vs, t.kh);
 
     const float c = a.scale * kLog2e;
     at_f32x16 o[DT];
@@ -272,8 +380,8 @@ __global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(Pr
     auto step = [&](auto border, const T *kb, T *vb, T *kn, T *vn, int n0) {
         constexpr bool BORDER = decltype(border)::value;  // some row may not see some key of the tile
         if (n0 + BN < any) {
-            stage_k(kn, n0 + BN);
-            stage_v(vn, n0 + BN);
+            keys.copy(kn, n0 + BN, any);
+            values.copy(vn, n0 + BN, any);
         }
         at_f32x16 s[KT];
         scores(s, kb);
@@ -301,43 +409,172 @@ __global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(Pr
             // Some rows do not see some of these keys, and a zero weight would
             // not keep a NaN or an infinity out of them: such values leave the
             // tile and are given to the rows that see them at the end.
-            bool odd = false;
-            for (int i = threadIdx.x; i < BN * P; i += kPrThreads) {
-                at_u32x4 w = *reinterpret_cast<const at_u32x4 *>(vb + 8 * i);
-                if (clear_non_finite<T>(w)) {
-                    *reinterpret_cast<at_u32x4 *>(vb + 8 * i) = w;
-                    odd = true;
-                }
-            }
-            if (odd) odd_values = 1;
+            if (clean_tile<T, D>(vb)) odd_values = 1;
             __syncthreads();
         }
         // ---- O^T += V^T P^T
 #pragma unroll
         for (int u = 0; u < 2 * KT; ++u) {
 #pragma unroll
-            for (int i = 0; i < DT; ++i) {
-                // lane: key 16 u + 4 half + (lane % 16) / 4 (then + 8), dimensions 32 i + 16 ((lane / 16) % 2) + 4 (lane % 4)
-                const int r = 16 * u + 4 * half + ((lane & 15) >> 2);
-                const int d = 32 * i + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-                const at_s16x4 lo =
-                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + v_place<D>(r, d >> 3) + (d & 7)));
-                const at_s16x4 hi =
-                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(vb + v_place<D>(r + 8, d >> 3) + (d & 7)));
-                const auto w = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                o[i] = Op16<T>::mfma32(__builtin_bit_cast(x8, w), pf[u], o[i]);
-            }
+            for (int i = 0; i < DT; ++i) o[i] = Op16<T>::mfma32(read_v<T, D>(vb, u, i), pf[u], o[i]);
         }
         __syncthreads();
     };
 
     if (threadIdx.x == 0) odd_values = 0;
-    if (first < any) {
-        stage_k(kt0, first);
-        stage_v(vt0, first);
+    if (t.first < any) {
+        keys.copy(kt0, t.first, any);
+        values.copy(vt0, t.first, any);
     }
     __syncthreads();
-    int n0 = first;
+    int n0 = t.first;
+    for (; n0 + 2 * BN <= all; n0 += 2 * BN) {
+        step(std::false_type{}, kt0, vt0, kt1, vt1, n0);
+        step(std::false_type{}, kt1, vt1, kt0, vt0, n0 + BN);
+    }
+    const int border = n0;
+    // the row anew: kept through the loop it takes registers that the V reads run ahead in
+    int again = col;
+    asm volatile("" : "+v"(again));
+    const PromptRow row = prompt_row(a, t, t.row0 + 32 * wave + again);
+    seen = row.seen;
+    for (; n0 < any; n0 += 2 * BN) {
+        step(std::true_type{}, kt0, vt0, kt1, vt1, n0);
+        if (n0 + BN >= any) break;
+        step(std::true_type{}, kt1, vt1, kt0, vt0, n0 + BN);
+    }
+    l = lane_pair_sum<32>(l);
+    const float f = t.split ? 1.0f : seen == 0 ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int i = 0; i < DT; ++i) o[i] *= f;
+    if (t.first < any && odd_values != 0) add_non_finite<T, DT>(a, t, row, border, D, 0, half, o);
+    if (row.is) store_rows<T, DT>(a, plan, t, row, piece, D, 0, half, o, m, l, parts);
+}
+
+// The same for 256-wide heads, whose O^T and queries for 32 rows take 192
+// registers of a lane: a pair of waves shares 32 rows.  Each makes the scores
+// of one half of a tile's 64 keys and forms their weights, the pair exchanges
+// maxima and weights through LDS, and each multiplies all 64 keys' weights
+// with one half of the dimensions.  Eight waves, 128 rows, share the tiles: one
+// workgroup a CU, two waves a SIMD.  1657 queries of 24 heads over 4000 keys
+// and more: 273 us with one wave for 32 rows (one a SIMD), 285 with pairs in
+// workgroups of four waves and one buffer each for K and V (two a CU; the
+// copies had half a tile's time), 280 this way; 4000 queries: 286, 251, 250.
+//
+// Barriers with explicit waits: those of __syncthreads would wait for the
+// copies that have just been issued.
+__device__ __forceinline__ void barrier_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+__device__ __forceinline__ void barrier_copies()
+{
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+template <typename T>
+__global__ void __launch_bounds__(64 * prompt_waves(256), 2) k_attn_prompt_wide(PromptArgs a, PromptPlan plan, float *parts)
+{
+    typedef typename Op16<T>::x8 x8;
+    constexpr int D = 256, BN = kKeys, DT = 4, KK = D / 16;
+    __shared__ __attribute__((aligned(16))) T kt0[BN * D], kt1[BN * D], vt0[BN * D], vt1[BN * D];
+    __shared__ x8 weights[4][4][64];   // [pair][k-step of 16 keys][lane]
+    __shared__ float tops[4][2][32];   // [pair][key half][row]
+    __shared__ int odd_values;
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int col = lane & 31, half = lane >> 5;
+    const int pair = wave >> 1, part = wave & 1;
+    const int piece = static_cast<int>(blockIdx.y);
+    PromptTile t;
+    if (!prompt_tile<T, D>(a, plan, piece, false, t)) return;
+    const PromptRow row = prompt_row(a, t, t.row0 + 32 * pair + col);
+    const int seen = row.seen, any = t.any, all = t.all;
+
+    x8 qf[KK];
+    {
+        const T *qp = static_cast<const T *>(a.q) + static_cast<int64_t>(t.q0 + row.tok) * a.qs + static_cast<int64_t>(row.head) * D;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) qf[kk] = *reinterpret_cast<const x8 *>(qp + 16 * kk + 8 * half);
+    }
+    const Staging<T, D, false> keys(a.k, t.k0, a.ks, t.kh);
+    const Staging<T, D, true> values(a.v, t.k0, a.vs, t.kh);
+    const float c = a.scale * kLog2e;
+    at_f32x16 o[DT];  // dimensions 128 part + 32 i + ...
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
+    float m = -__builtin_inff(), l = 0.0f;  // l: of this wave's keys
+
+    auto step = [&](auto border, const T *kb, T *vb, T *kn, T *vn, int n0) {
+        constexpr bool BORDER = decltype(border)::value;
+        if (n0 + BN < any) {
+            keys.copy(kn, n0 + BN, any);
+            values.copy(vn, n0 + BN, any);
+        }
+        // ---- S^T of keys 32 part ..
+        at_f32x16 s;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s[j] = 0.0f;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+            s = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(kb + k_place<D>(32 * part + col, 2 * kk + half)), qf[kk], s);
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+        for (int i = 0; i < KK - kAhead; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x8, kAhead, 0);
+        if constexpr (BORDER) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (n0 + 32 * part + 8 * (j >> 2) + 4 * half + (j & 3) >= seen) s[j] = -__builtin_inff();
+        }
+        float top = s[0];
+#pragma unroll
+        for (int j = 1; j < 16; ++j) top = fmaxf(top, s[j]);
+        top = lane_pair_max<32>(top) * c;
+        if (half == 0) tops[pair][part][col] = top;
+        barrier_lds();
+        top = fmaxf(top, tops[pair][part ^ 1][col]);
+        if (__ballot(top > m + 8.0f) != 0) {  // the same in both waves
+            const float mn = fmaxf(m, top);
+            const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < DT; ++i) o[i] *= f;
+            m = mn;
+        }
+        const float ms = m == -__builtin_inff() ? 0.0f : m;
+        x8 pf[2];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float e = __builtin_amdgcn_exp2f(fmaf(s[j], c, -ms));
+            l += e;
+            pf[j >> 3][j & 7] = static_cast<T>(e);
+        }
+        weights[pair][2 * part][lane] = pf[0];
+        weights[pair][2 * part + 1][lane] = pf[1];
+        if constexpr (BORDER) {
+            if (clean_tile<T, D>(vb)) odd_values = 1;
+        }
+        barrier_lds();
+        // ---- O^T of dimensions 128 part ..
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const x8 w = weights[pair][u][lane];
+#pragma unroll
+            for (int i = 0; i < DT; ++i) o[i] = Op16<T>::mfma32(read_v<T, D>(vb, u, DT * part + i), w, o[i]);
+        }
+        barrier_copies();  // all have read, the next tile is there
+    };
+
+    if (threadIdx.x == 0) odd_values = 0;
+    if (t.first < any) {
+        keys.copy(kt0, t.first, any);
+        values.copy(vt0, t.first, any);
+    }
+    barrier_copies();
+    int n0 = t.first;
     for (; n0 + 2 * BN <= all; n0 += 2 * BN) {
         step(std::false_type{}, kt0, vt0, kt1, vt1, n0);
         step(std::false_type{}, kt1, vt1, kt0, vt0, n0 + BN);
@@ -348,93 +585,64 @@ __global__ void __launch_bounds__(kPrThreads, D == 256 ? 1 : 2) k_attn_prompt(Pr
         if (n0 + BN >= any) break;
         step(std::true_type{}, kt1, vt1, kt0, vt0, n0 + BN);
     }
+
+    // the pair's sums
     l = lane_pair_sum<32>(l);
-    const float f = split ? 1.0f : seen == 0 ? 0.0f : 1.0f / l;
+    __syncthreads();
+    if (half == 0) tops[pair][part][col] = l;
+    __syncthreads();
+    l = tops[pair][0][col] + tops[pair][1][col];
+    const float f = t.split ? 1.0f : seen == 0 ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[i] *= f;
-    if (first < any && odd_values != 0) {
-        for (int r = border; r < any; ++r) {
-            const T *src = static_cast<const T *>(a.v) + (k0 + r) * a.vs + static_cast<int64_t>(kh) * D + 4 * half;
-#pragma unroll
-            for (int i = 0; i < DT; ++i)
-#pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const at_f32x4 x = load4(src + 32 * i + 2 * j);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (r < seen && !(fabsf(x[e]) <= 3.4028235e38f)) o[i][j + e] += x[e];
-                }
-        }
-    }
-    if (row >= rows) return;
-    if (!split) {
-        T *dst = static_cast<T *>(a.out) + ((q0 + tok) * a.hq + kh * group + head) * D;
-#pragma unroll
-        for (int i = 0; i < DT; ++i)
-#pragma unroll
-            for (int j = 0; j < 16; j += 4)
-                store4(dst + 32 * i + 2 * j + 4 * half, at_f32x4{o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]});
-    } else {
-        const int64_t slot = ((q0 + tok) * a.hq + kh * group + head) * plan.splits + blockIdx.y;
-        float *dst = part + slot * D;
-#pragma unroll
-        for (int i = 0; i < DT; ++i)
-#pragma unroll
-            for (int j = 0; j < 16; j += 4)
-                store4(dst + 32 * i + 2 * j + 4 * half, at_f32x4{o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]});
-        if (half == 0) {
-            part[plan.rows_floats + slot * 2] = m;
-            part[plan.rows_floats + slot * 2 + 1] = l;
-        }
-    }
+    if (t.first < any && odd_values != 0) add_non_finite<T, DT>(a, t, row, border, D, 128 * part, half, o);
+    if (row.is) store_rows<T, DT>(a, plan, t, row, piece, D, 128 * part, half, o, m, l, parts);
 }
 
-// Joins the chunks of the tiles that were split: D / 4 lanes per row.
+// Joins the chunks of the tiles that were split: D / 4 lanes per row, one row
+// each (blockIdx.y: the part of a tile's rows).
+constexpr int join_rows(int d) { return 256 / (d / 4); }
+
 template <typename T, int D>
 __global__ void __launch_bounds__(256) k_prompt_join(PromptArgs a, PromptPlan plan, const float *part)
 {
     constexpr int LPR = D / 4;
-    const int group = a.hq / a.hkv;
-    const int kh = static_cast<int>(blockIdx.x % static_cast<uint32_t>(a.hkv));
-    int64_t b, at;
-    if (!prompt_tile(a, blockIdx.x / static_cast<uint32_t>(a.hkv), b, at)) return;
-    const int64_t q0 = a.cu_q[b], k0 = a.cu_k[b];
-    const int64_t lq = a.cu_q[b + 1] - q0, lk = a.cu_k[b + 1] - k0, rows = lq * group;
-    if (prompt_refused(a, q0, lq, k0, lk)) return;
-    const int64_t tile = (rows + kPrRows - 1) / kPrRows - 1 - at;
-    const int64_t end = (tile + 1) * kPrRows < rows ? (tile + 1) * kPrRows : rows;
-    const int reach = visible(a, (end - 1) / group, lk - lq, lk);
-    if (reach <= plan.chunk) return;
-    const int n = static_cast<int>((reach + plan.chunk - 1) / plan.chunk);
-    const int e = (threadIdx.x % LPR) * 4;
-    // blockIdx.y: a quarter of the tile's rows
-    const int64_t r0 = tile * kPrRows + blockIdx.y * (kPrRows / kJoinParts);
-    for (int64_t r = r0 + threadIdx.x / LPR; r < r0 + kPrRows / kJoinParts && r < end; r += 256 / LPR) {
-        const int64_t tok = r / group, at_out = (q0 + tok) * a.hq + kh * group + r % group;
-        const float *ml = part + plan.rows_floats + at_out * plan.splits * 2, *src = part + at_out * plan.splits * D + e;
-        float M = -__builtin_inff();
-        for (int i = 0; i < n; ++i) M = fmaxf(M, ml[2 * i]);
-        if (M == -__builtin_inff()) M = 0.0f;
-        float L = 0.0f;
-        at_f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int i = 0; i < n; ++i) {
-            const float w = __builtin_amdgcn_exp2f(ml[2 * i] - M);
-            L += w * ml[2 * i + 1];
-            o += w * *reinterpret_cast<const at_f32x4 *>(src + static_cast<int64_t>(i) * D);
-        }
-        const float f = visible(a, tok, lk - lq, lk) == 0 ? 0.0f : 1.0f / L;
-        store4(static_cast<T *>(a.out) + at_out * D + e, o * f);
+    PromptTile t;
+    if (!prompt_tile<T, D>(a, plan, 0, true, t) || !t.split) return;
+    const int n = (t.reach + plan.chunk - 1) / plan.chunk;
+    const int x = threadIdx.x % LPR;
+    const int r = t.row0 + static_cast<int>(blockIdx.y * join_rows(D) + threadIdx.x / LPR);
+    if (r >= t.end) return;
+    const PromptRow row = prompt_row(a, t, r);
+    const int64_t at = static_cast<int64_t>(t.q0 + row.tok) * a.hq + row.head;
+    const float *ml = part + plan.rows_floats + at * plan.splits * 2, *src = part + at * plan.splits * D + 4 * x;
+    float M = -__builtin_inff();
+    for (int i = x; i < n; i += LPR) M = fmaxf(M, ml[2 * i]);
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) M = fmaxf(M, __shfl_xor(M, o, 64));
+    if (M == -__builtin_inff()) M = 0.0f;
+    float L = 0.0f;
+    at_f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float w = __builtin_amdgcn_exp2f(ml[2 * i] - M);
+        L += w * ml[2 * i + 1];
+        o += w * *reinterpret_cast<const at_f32x4 *>(src + static_cast<int64_t>(i) * D);
     }
+    store4(static_cast<T *>(a.out) + at * D + 4 * x, o * (row.seen == 0 ? 0.0f : 1.0f / L));
 }
 
 template <typename T, int D>
 hipError_t prompt_launch(const PromptArgs &a, const PromptPlan &plan, float *part, hipStream_t s)
 {
     const uint32_t tiles = static_cast<uint32_t>(prompt_tiles(a.batch, a.q_rows, a.hq, a.hkv) * a.hkv);
-    hipLaunchKernelGGL((k_attn_prompt<T, D>), dim3(tiles, static_cast<uint32_t>(plan.splits)), dim3(kPrThreads), 0, s, a,
-                       plan, part);
+    const dim3 grid(tiles, static_cast<uint32_t>(plan.splits));
+    if constexpr (D == 256)
+        hipLaunchKernelGGL((k_attn_prompt_wide<T>), grid, dim3(64 * prompt_waves(D)), 0, s, a, plan, part);
+    else
+        hipLaunchKernelGGL((k_attn_prompt<T, D>), grid, dim3(64 * prompt_waves(D)), 0, s, a, plan, part);
     if (plan.splits > 1)
-        hipLaunchKernelGGL((k_prompt_join<T, D>), dim3(tiles, kJoinParts), dim3(256), 0, s, a, plan, part);
+        hipLaunchKernelGGL((k_prompt_join<T, D>), dim3(tiles, kPrRows / join_rows(D)), dim3(256), 0, s, a, plan, part);
     return hipGetLastError();
 }
 
@@ -455,25 +663,34 @@ int64_t prompt_tiles(int64_t batch, int64_t q_rows, int32_t hq, int32_t hkv)
 
 PromptPlan prompt_plan(int64_t batch, int64_t q_rows, int64_t max_k, int32_t hq, int32_t hkv, int32_t d)
 {
+    // The time with the keys of every tile cut in n, in us: rounds of workgroups,
+    // each of a key's time as measured with the GPU full, and from n = 2 on
+    // the parts' rows in fp32 (written and read, at half of HBM's rate: they
+    // come in bursts) and the join.  Causal tiles reach half as far on
+    // average, and ragged batches less: this cuts rather too little, which
+    // costs less than too much (1272 tiles of up to 2500 keys of 128, 89 us,
+    // took 115 in two).  16 queries over 8016 keys: 146 us uncut, 20 in
+    // chunks of 512; 1657 queries of 24 heads of 256 over 4000 and more: 307
+    // uncut, 274 in two.
     PromptPlan p;
-    p.chunk = max_k > 0 ? (max_k + 127) / 128 * 128 : 128;
-    const int64_t slots = d == 256 ? 256 : 512;  // workgroups the GPU holds
-    const int64_t tiles = prompt_tiles(batch, q_rows, hq, hkv) * hkv;
-    // Chunks that fill the GPU about once (half of max_k: a causal tile's
-    // reach on average), of 512 keys at least: a chunk costs its rows in fp32,
-    // written and read.  Cut three times finer: 0.34 ms for 0.28 at 1657
-    // queries of 24 heads of 256 over 4000 keys and more, and with many tiles
-    // cutting costs more than the last workgroups' wait: 1272 tiles of
-    // up to 2500 keys of 128 in two took 115 us for 88.
-    if (tiles < 4 * slots) {
-        int64_t chunk = (tiles * (max_k / 2) / slots + 127) / 128 * 128;
-        if (chunk < 512) chunk = 512;
-        if (chunk < max_k) {
-            p.chunk = chunk;
-            p.splits = (max_k + chunk - 1) / chunk;
-            p.rows_floats = static_cast<size_t>(q_rows) * hq * p.splits * d;
-            p.part_floats = p.rows_floats + static_cast<size_t>(q_rows) * hq * p.splits * 2;
+    const double slots = d == 256 ? 256 : 512, key = d == 256 ? 0.04 : 0.029;  // workgroups the GPU holds
+    const double tiles = static_cast<double>(prompt_tiles(batch, q_rows, hq, hkv) * hkv);
+    double best = 0.0;
+    int n = 1;
+    for (int i = 1; i <= 64 && max_k / i >= 256; ++i) {
+        double us = __builtin_ceil(tiles * i / slots) * static_cast<double>(max_k) / i * key;
+        if (i > 1) us += 6.0 + tiles * i * kPrRows * d * 4 * 2 / 2.5e6;
+        if (i == 1 || us < best * 0.95) {
+            best = us;
+            n = i;
         }
+    }
+    p.chunk = static_cast<int32_t>(((max_k + n - 1) / n + 127) / 128 * 128);
+    if (p.chunk == 0) p.chunk = 128;
+    p.splits = static_cast<int32_t>(max_k > 0 ? (max_k + p.chunk - 1) / p.chunk : 1);
+    if (p.splits > 1) {
+        p.rows_floats = static_cast<size_t>(q_rows) * hq * p.splits * d;
+        p.part_floats = p.rows_floats + static_cast<size_t>(q_rows) * hq * p.splits * 2;
     }
     return p;
 }
