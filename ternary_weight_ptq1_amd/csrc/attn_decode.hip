@@ -107,7 +107,13 @@ __device__ __forceinline__ void split_terms(const float (&x)[8], typename Op16<T
 {
     float r[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = x[j];
+    for (int j = 0; j < 8; ++j) {
+        r[j] = x[j];
+        // one rounding of x for all its uses: the product behind x, fused into
+        // the first term alone, rounds the other way now and then, and the
+        // second term then lacks 2^-11 of x
+        if (N > 1) asm volatile("" : "+v"(r[j]));
+    }
 #pragma unroll
     for (int n = 0; n < N; ++n) {
 #pragma unroll

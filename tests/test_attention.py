@@ -339,6 +339,37 @@ def test_attn_decode_long(ctype):
     check_decode(q, c, table, lens, got, scale=0.3)
 
 
+def test_attn_decode_every_weight_is_exact_to_its_terms():
+    """fp32 queries over an int8 cache: no single token's weight may be off by a rounding of its first 16-bit term
+    (2^-11).  The tolerance of a whole row hides one such token among a thousand; here each token has a dimension
+    of its own, 128 at a time, with steps that are no powers of two."""
+    g = gen(15)
+    n, d = 1024, 128
+    table, pages = tables(g, [n], 64)
+    c = filled_cache(g, pages, 64, 1, d, I8)
+    c.k_pages.copy_((randn(g, *c.k_pages.shape) * 40).clamp(-127, 127).round())
+    q = randn(g, 1, 16, d)
+    sl = torch.tensor([n], dtype=torch.int32, device=DEV)
+    rows = table[0].long()
+    k = sequence(c, cache_values(c)[0], table, 0, n)[0]
+    steps = c.v_steps[rows, 0].reshape(-1).double()
+    logits = q[0].double() @ k.T.contiguous() * d ** -0.5
+    size = q[0].double().abs() @ k.T.contiguous().abs() * d ** -0.5
+    w = torch.softmax(logits, 1)
+    for first in range(0, n, 128):
+        v = torch.zeros((n, d), dtype=I8, device=DEV)
+        v[torch.arange(first, first + 128, device=DEV), torch.arange(128, device=DEV)] = 127
+        c.v_pages[rows, 0] = v.view(-1, 64, d).transpose(1, 2)
+        got = P.ptq1_attn_decode(q, c, table, sl)[0].double()
+        want = w[:, first:first + 128] * 127 * steps[first:first + 128]
+        # score and exp2 as in attention_bounds (d + 8 roundings, twice: weight and sum), the sum of n weights, the
+        # product with the step and the last division
+        tol = (2 * (d + 8) * U * size.amax(1, keepdim=True) + 8 * U * logits.abs().amax(1, keepdim=True) + 2 * 2.0 ** -22
+               + n * U + 8 * U) * want
+        assert bool(((got - want).abs() <= tol).all()), ((got - want).abs() / want).max().item()
+        assert bool((((got - want).abs() / want) < 2.0 ** -13).all())
+
+
 def test_attn_decode_large_and_small_queries():
     """fp32 queries outside fp16's range over an fp16 cache, and zeros."""
     g = gen(12)
