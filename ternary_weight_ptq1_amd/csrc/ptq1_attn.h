@@ -55,13 +55,6 @@ struct Op16<_Float16> {
     }
 };
 
-// max of two values, NaN when either is: a row with a NaN must not end as a
-// finite maximum.
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    return a != a || b != b ? __builtin_nanf("") : fmaxf(a, b);
-}
-
 // The larger of lane l's and lane l ^ H's value, in both lanes (H = 16, 32).
 template <int H>
 __device__ __forceinline__ float lane_pair_max(float v)

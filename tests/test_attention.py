@@ -646,3 +646,276 @@ def test_two_streams_with_a_workspace_each():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+# -------------------------------------------------- masks, splits, many sequences ----
+
+def prompt_state(g, lq, lk, hq, hkv, d, dtype=BF16):
+    return (randn(g, sum(lq), hq, d).to(dtype), randn(g, sum(lk), hkv, d).to(dtype), randn(g, sum(lk), hkv, d).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("hq,hkv,d,lq,lk", [
+    (4, 2, 64, [200, 60], [200, 150]),
+    (4, 1, 128, [70, 5, 33], [200, 5, 64]),
+    (2, 2, 256, [130, 9], [190, 40]),
+    (4, 2, 128, [3, 2], [9000, 700]),      # few rows over many keys: the keys are cut into parts
+    (2, 1, 256, [2], [6000]),
+    (2, 1, 64, [5], [8100]),
+])
+def test_attn_prompt_non_finite_hidden(dtype, hq, hkv, d, lq, lk):
+    """NaN and infinities in keys and values that a row does not see leave that row as it is: later positions,
+    other sequences, rows between sequences."""
+    g = gen(sum(lk) + d)
+    q, k, v = prompt_state(g, lq, lk, hq, hkv, d, dtype)
+    args = dict(max_q=max(lq), max_k=max(lk))
+    cq, ck = cumulated(lq), cumulated(lk)
+    want = P.ptq1_attn_prompt(q, k, v, cq, ck, **args)
+    check_prompt(q, k, v, lq, lk, want, True)
+    k2, v2 = k.clone(), v.clone()
+    spoiled = torch.zeros(sum(lq), dtype=torch.bool, device=DEV)
+    at_q = at_k = 0
+    for i, (nq, nk) in enumerate(zip(lq, lk)):
+        if nq > 1:  # the last two keys: seen by the last two rows, one of them by the last alone
+            v2[at_k + nk - 1, :, 3] = float("inf")
+            k2[at_k + nk - 1, :, 1] = float("nan")
+            v2[at_k + nk - 1, :, 7] = float("nan")
+            spoiled[at_q + nq - 1] = True
+        if i == 1:  # one whole sequence of NaN
+            k2[at_k:at_k + nk], v2[at_k:at_k + nk] = float("nan"), float("-inf")
+            spoiled[at_q:at_q + nq] = True
+        at_q, at_k = at_q + nq, at_k + nk
+    got = P.ptq1_attn_prompt(q, k2, v2, cq, ck, **args)
+    assert torch.equal(got[~spoiled], want[~spoiled])
+    # a NaN key makes the whole row NaN
+    assert bool(got[spoiled].isnan().all())
+    # the rows of one sequence between two others are hidden from both
+    gap_q, gap_k = torch.cat([q, q, q]), torch.cat([k, k2, k])
+    gap_v = torch.cat([v, torch.full_like(v, float("nan")), v])
+    nq, nk = sum(lq), sum(lk)
+    if len(lq) == 1:
+        cu_q = torch.tensor([0, nq], dtype=torch.int32, device=DEV)
+        cu_k = torch.tensor([2 * nk, 3 * nk], dtype=torch.int32, device=DEV)
+        got = P.ptq1_attn_prompt(gap_q, gap_k, gap_v, cu_q, cu_k, **args)
+        assert torch.equal(got[:nq], want)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attn_prompt_hidden_infinity_of_a_visible_key(d):
+    """An infinite value that a row sees reaches that row's dimension alone."""
+    g = gen(50 + d)
+    n = 150
+    q, k, v = prompt_state(g, [n], [n], 2, 1, d)
+    want = P.ptq1_attn_prompt(q, k, v, cumulated([n]), cumulated([n]))
+    v2 = v.clone()
+    v2[77, 0, 5] = float("inf")
+    got = P.ptq1_attn_prompt(q, k, v2, cumulated([n]), cumulated([n]))
+    seen = torch.arange(n, device=DEV) >= 77
+    assert not bool(got[seen][:, :, 5].isfinite().any())
+    hit = torch.zeros_like(got, dtype=torch.bool)
+    hit[77:, :, 5] = True
+    assert torch.equal(got[~hit], want[~hit])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,d,lq,lk", [
+    (4, 2, 64, [1], [20000]),
+    (8, 2, 128, [16, 3], [12345, 1]),
+    (2, 2, 256, [5], [9001]),
+    (6, 1, 128, [20, 4, 0, 9], [7000, 2, 50, 0]),   # queries that see nothing beside a cut sequence
+    (16, 1, 256, [33, 1], [4100, 4096]),
+])
+def test_attn_prompt_cut_along_the_keys(dtype, causal, hq, hkv, d, lq, lk):
+    g = gen(hq + d + sum(lk))
+    q, k, v = prompt_state(g, lq, lk, hq, hkv, d, dtype)
+    assert P.workspace_bytes("attn_prompt", len(lq), sum(lq), max(lk), hq, hkv, d) > 0
+    out = torch.full((sum(lq) + 2, hq, d), 7.0, dtype=dtype, device=DEV)
+    qq = torch.cat([q, q[:1], q[:1]])
+    P.ptq1_attn_prompt(qq, k, v, cumulated(lq), cumulated(lk), max_q=max(lq), max_k=max(lk), causal=causal, out=out)
+    check_prompt(q, k, v, lq, lk, out, causal)
+    assert bool((out[sum(lq):] == 7).all())   # rows behind the last sequence
+    again = P.ptq1_attn_prompt(qq, k, v, cumulated(lq), cumulated(lk), max_q=max(lq), max_k=max(lk), causal=causal)
+    assert torch.equal(out[:sum(lq)], again[:sum(lq)])
+    # a refused sequence beside them
+    bad = cumulated(lk)
+    bad[-1] = sum(lk) + 1
+    got = P.ptq1_attn_prompt(q, k, v, cumulated(lq), bad, max_q=max(lq), max_k=max(lk) + 1, causal=causal)
+    first = sum(lq[:-1])
+    check_prompt(q, k, v, lq[:-1], lk[:-1], got, causal)
+    assert bool(got[first:].isnan().all())
+
+
+@pytest.mark.parametrize("batch", [65, 200, 1000])
+def test_many_sequences(batch):
+    """More sequences than lanes, with empty ones among them, through read-back, prompt and decode."""
+    g = gen(batch)
+    lens = [int(n) for n in np.random.default_rng(batch).integers(0, 40, batch)]
+    lens[0], lens[64], lens[-1] = 0, 100, 0
+    table, pages = tables(g, lens, 16)
+    c = filled_cache(g, pages, 16, 2, 64, BF16)
+    poison_unused(c, table, lens)
+    cu = cumulated(lens)
+    k, v = P.ptq1_kv_read(c, table, cu, sum(lens), dtype=BF16)
+    kc, vc = cache_values(c)
+    order = [sequence(c, kc, table, b, n).transpose(0, 1) for b, n in enumerate(lens) if n]
+    assert torch.equal(k.double(), torch.cat(order))
+    order = [sequence(c, vc, table, b, n).transpose(0, 1) for b, n in enumerate(lens) if n]
+    assert torch.equal(v.double(), torch.cat(order))
+    q = randn(g, sum(lens), 4, 64).to(BF16)
+    o = P.ptq1_attn_prompt(q, k, v, cu, cu, max_q=100, max_k=100)
+    some = [b for b in range(batch) if b < 3 or b in (63, 64, 65, batch - 2) or b % 50 == 7]
+    for b in some:
+        a, z = int(cu[b]), int(cu[b + 1])
+        check_prompt(q[a:z], k[a:z], v[a:z], [z - a], [z - a], o[a:z], True)
+    last = torch.stack([q[int(cu[b + 1]) - 1] if n else q[0] for b, n in enumerate(lens)])
+    got = P.ptq1_attn_decode(last, c, table, torch.tensor(lens, dtype=torch.int32, device=DEV))
+    check_decode(last, c, table, lens, got)
+
+
+@pytest.mark.parametrize("ctype", [F16, BF16, I8])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_kv_write_runs_across_pages(ctype, d):
+    """A prompt's neighbouring slots from an odd place on, over pages that lie apart, with holes; the same in one call
+    or in two."""
+    g = gen(60 + d)
+    n, page, hkv = 203, 32, 2
+    order = torch.randperm(9, generator=g, device=DEV)
+    place = torch.arange(5, 5 + n, device=DEV)
+    slots = order[place // page] * page + place % page
+    slots[torch.tensor([17, 90, 91, 92], device=DEV)] = -1
+    k, v = randn(g, n, hkv, d).to(BF16), randn(g, n, hkv, d).to(BF16)
+    caches = [P.ptq1_kv_cache(9, page, hkv, d, ctype, DEV) for _ in range(2)]
+    for c in caches:
+        for t in (c.k_pages, c.v_pages, c.k_steps, c.v_steps):
+            if t is not None:
+                t.fill_(1)
+    P.ptq1_kv_write(None, k, v, slots, caches[0])
+    P.ptq1_kv_write(None, k[:101], v[:101], slots[:101], caches[1])
+    P.ptq1_kv_write(None, k[101:], v[101:], slots[101:], caches[1])
+    for name in ("k_pages", "v_pages", "k_steps", "v_steps"):
+        a, b = (getattr(c, name) for c in caches)
+        assert a is None or torch.equal(a, b)
+    kc, vc = cache_values(caches[0])
+    ok = slots >= 0
+    at, off = slots[ok] // page, slots[ok] % page
+    zero = torch.zeros((int(ok.sum()), hkv, d), dtype=torch.float64, device=DEV)
+    check_rows(kc[at, :, off], k[ok].double(), zero, ctype)
+    check_rows(vc[at, :, off], v[ok].double(), zero, ctype)
+    kept = torch.ones(9 * page, dtype=torch.bool, device=DEV)
+    kept[slots[ok]] = False
+    for t in (kc, vc):
+        assert bool((t.transpose(1, 2).reshape(9 * page, hkv, d)[kept] == 1).all())
+
+
+def test_nothing_to_do():
+    c = P.ptq1_kv_cache(2, 16, 2, 64, I8, DEV)
+    k = torch.empty((0, 2, 64), device=DEV)
+    i64, i32 = torch.empty(0, dtype=torch.int64, device=DEV), torch.empty(0, dtype=torch.int32, device=DEV)
+    assert P.ptq1_kv_write(None, k, k, i64, c) is None
+    assert P.ptq1_kv_write(k, k, k, i64, c, q_dtype=BF16).shape == (0, 2, 64)
+    cu0 = torch.zeros(1, dtype=torch.int32, device=DEV)
+    table = torch.empty((0, 3), dtype=torch.int32, device=DEV)
+    kr, vr = P.ptq1_kv_read(c, table, cu0, 0, dtype=BF16)
+    assert kr.shape == vr.shape == (0, 2, 64)
+    q = torch.empty((0, 4, 64), dtype=BF16, device=DEV)
+    assert P.ptq1_attn_decode(q, c, table, i32).shape == (0, 4, 64)
+    kb = k.to(BF16)
+    assert P.ptq1_attn_prompt(q, kb, kb, cu0, cu0).shape == (0, 4, 64)
+    # sequences without a token, and a table without columns
+    q = torch.ones((3, 4, 64), dtype=BF16, device=DEV)
+    zero = torch.zeros(3, dtype=torch.int32, device=DEV)
+    assert bool((P.ptq1_attn_decode(q, c, torch.empty((3, 0), dtype=torch.int32, device=DEV), zero) == 0).all())
+    cu = torch.zeros(4, dtype=torch.int32, device=DEV)
+    kr, vr = P.ptq1_kv_read(c, torch.zeros((3, 1), dtype=torch.int32, device=DEV), cu, 5, dtype=BF16)
+    assert kr.shape == (5, 2, 64)
+    o = P.ptq1_attn_prompt(q, kb, kb, torch.tensor([0, 1, 1, 3], dtype=torch.int32, device=DEV), cu)
+    assert bool((o == 0).all())
+    torch.cuda.synchronize()
+
+
+def test_captured_prompt_and_read_back():
+    """Two graphs, a workspace each, replayed in turn and together with eager calls between them."""
+    g = gen(70)
+    page, lens, new = 32, [5000, 900], [6, 11]
+    table, pages = tables(g, lens, page)
+    c = filled_cache(g, pages, page, 2, 128, BF16)
+    cu_k, cu_q = cumulated(lens), cumulated(new)
+    need = P.workspace_bytes("attn_prompt", 2, sum(new), max(lens), 8, 2, 128)
+    assert need > 0
+    parts = []
+    for _ in range(2):
+        kv = [torch.empty((sum(lens), 2, 128), dtype=BF16, device=DEV) for _ in range(2)]
+        parts.append((randn(g, sum(new), 8, 128).to(BF16), kv, torch.empty((sum(new), 8, 128), dtype=BF16, device=DEV),
+                      torch.empty(need, dtype=torch.uint8, device=DEV)))
+
+    def step(q, kv, out, ws):
+        P.ptq1_kv_read(c, table, cu_k, sum(lens), dtype=BF16, out=kv)
+        P.ptq1_attn_prompt(q, *kv, cu_q, cu_k, max_q=max(new), max_k=max(lens), out=out, ws=ws)
+
+    torch.cuda.synchronize()
+    streams, graphs = [torch.cuda.Stream() for _ in parts], []
+    for part, s in zip(parts, streams):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            step(*part)
+        graphs.append(graph)
+    for i in range(3):
+        for q, _, out, _ in parts:
+            q.copy_(randn(g, *q.shape))
+            out.fill_(float("nan"))
+        c.k_pages.mul_(0.9)
+        torch.cuda.synchronize()
+        for s, graph in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for q, kv, out, ws in parts:
+            got = out.clone()
+            check_prompt(q, *kv, new, lens, got, True)
+            step(q, kv, out, ws)
+            assert torch.equal(out, got)
+
+
+@pytest.mark.parametrize("ctype", [BF16, I8])
+def test_cache_past_32_bit_offsets(ctype):
+    """Pages whose elements lie past 2^32."""
+    g = gen(80)
+    page, hkv, d, pages = 256, 8, 128, 16400
+    assert pages * page * hkv * d > 1 << 32
+    c = P.ptq1_kv_cache(pages, page, hkv, d, ctype, DEV)
+    table = torch.tensor([[16399, 3, 16397], [16398, 8200, 0]], dtype=torch.int32, device=DEV)
+    lens = [600, 515]
+    cu = cumulated(lens)
+    k, v = (randn(g, sum(lens), hkv, d).to(BF16) for _ in range(2))
+    place = torch.cat([torch.arange(n, device=DEV) for n in lens])
+    seq = torch.repeat_interleave(torch.arange(2, device=DEV), torch.tensor(lens, device=DEV))
+    slots = table[seq, place // page].long() * page + place % page
+    P.ptq1_kv_write(None, k, v, slots, c)
+    kr, vr = P.ptq1_kv_read(c, table, cu, sum(lens), dtype=F32)
+    zero = torch.zeros(kr.shape, dtype=torch.float64, device=DEV)
+    check_rows(kr, k.double(), zero + (half_step(k.double(), F32) if ctype == I8 else 0), ctype)
+    check_rows(vr, v.double(), zero + (half_step(v.double(), F32) if ctype == I8 else 0), ctype)
+    q = randn(g, 2, 16, d)
+    got = P.ptq1_attn_decode(q, c, table, torch.tensor(lens, dtype=torch.int32, device=DEV))
+    kr, vr = kr.double(), vr.double()
+    for b in range(2):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        for h in range(hkv):
+            want, tol = attention_bounds(q[b, 2 * h:2 * h + 2].double(), kr[rows, h], vr[rows, h], d ** -0.5,
+                                         WEIGHT_TERM[(F32, ctype)])
+            tol = tol + 4 * U * want.abs() + 4 * U  # kr and vr are rounded products of code and step
+            assert bool(((got[b, 2 * h:2 * h + 2].double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attn_prompt_rows_far_apart(d):
+    """Rows at the largest stride, their offsets past 2^32 bytes."""
+    g = gen(81)
+    n, stride = 200, 1 << 24
+    room = torch.empty((n, stride), dtype=BF16, device=DEV)
+    q, k, v = (room.as_strided((n, h, d), (stride, d, 1), i * 4096) for i, h in enumerate((4, 2, 2)))
+    for t in (q, k, v):
+        t.copy_(randn(g, *t.shape))
+    got = P.ptq1_attn_prompt(q, k, v, cumulated([n]), cumulated([n]))
+    check_prompt(q, k, v, [n], [n], got, True)
