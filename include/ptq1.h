@@ -448,7 +448,7 @@ ptq1_status ptq1_kv_write(const void *q, int64_t q_stride, const void *k, int64_
  * of k_out and v_out [n_rows][n_kv_heads][head_dim] (out_dtype F32, F16 or
  * BF16) get the first cu_seqlens[b + 1] - cu_seqlens[b] tokens of sequence b,
  * whose pages are block_table[b][0..max_pages) (int32, device).  cu_seqlens
- * int32 [batch + 1], device, not decreasing.  Rows that belong to no sequence
+ * int32 [batch + 1], device, not negative, not decreasing.  Rows that belong to no sequence
  * are left as they were, and no row from n_rows on is written.  A token whose
  * page is outside [0, n_pages), or past max_pages, reads as NaN.  An int8
  * value is step * code, rounded once to out_dtype.
@@ -468,19 +468,24 @@ ptq1_status ptq1_kv_read(const ptq1_kv_cache *cache, const int32_t *block_table,
  *              16-bit type, or any of F32, F16, BF16 over an int8 cache; out
  *              has q's type and must not overlap q.
  *   block_table int32 [batch][max_pages], seq_lens int32 [batch] (device):
- *              sequence b's tokens are 0 .. seq_lens[b], the new token's own
+ *              sequence b's tokens are 0 .. seq_lens[b] - 1, the new token's own
  *              key among them if it is to be seen.  Length 0 gives zeros.  A
  *              length outside [0, max_len], or a page outside [0, n_pages)
  *              among those the length covers, makes the sequence's rows NaN.
  *   max_len    a bound on the lengths that the caller knows (at most
  *              max_pages * page_size); the work is laid out for it.
  *   scale      positive and finite.
- * The products run on the matrix cores with 16-bit operands: K and V enter
- * exactly; fp32 queries enter as three 16-bit terms, weights as two or three,
- * so that nothing is rounded to 16 bits but the stored cache; sums, maxima and
+ * The products run on the matrix cores.  Over 16-bit caches K and V enter
+ * exactly, fp32 queries as three 16-bit terms and weights as two or three
+ * (bf16 queries: two, 16 bits of a weight; fp16: down to 2^-38 of the row's
+ * largest).  Over int8 caches the codes enter exactly; the queries are fixed-point
+ * numbers, multiples of 2^-29 (fp32 queries) or 2^-21 of a power of two not
+ * above the head's largest magnitude; weight times step enters as three fp16
+ * terms (16-bit queries: two), down to 2^-38 of the largest.  Sums, maxima and
  * accumulators are fp32.  A NaN or an infinity in a query or in a key or value
- * that is read makes the entries of out that it enters NaN or infinite.  Long sequences are cut into chunks that run side by
- * side and are joined by a second launch, in a fixed order.
+ * that is read makes the entries of out that it enters NaN or infinite.  Long
+ * sequences are cut into pieces that run side by side and are joined by a
+ * second launch, in a fixed order.
  * Errors: NULL, SHAPE (n_q_heads not a multiple of n_kv_heads, max_len, scale),
  * ALIGN, ALIAS, OVERFLOW, WORKSPACE, UNSUPPORTED (types, head_dim, page_size,
  * batch > 65535, more than 65535 groups of 16 query heads per sequence,
@@ -512,7 +517,8 @@ ptq1_status ptq1_attn_decode(const void *q, int32_t q_dtype, int64_t batch, int3
  *        [0, n_q_rows) or [0, n_k_rows) (those inside q's range).
  *   scale  positive and finite.
  * bf16 or fp16 matrix cores, fp32 scores, maxima, sums and accumulators; the
- * weights enter the second product rounded to dtype, the sum is over fp32.
+ * weights enter the second product rounded to dtype (fp16: to 11 bits, down to
+ * 2^-32 of the row's largest), the sum is over fp32.
  * Where the query rows alone would not fill the GPU, the keys are cut into
  * chunks that run side by side and are joined by a second launch, in a fixed
  * order; the workspace (for max_k as given, or n_k_rows if that is less) holds

@@ -542,7 +542,7 @@ class _CacheStruct(C.Structure):
 class KvCache:
     """A paged key-value cache over tensors that it keeps: k_pages [n_pages, n_kv_heads, page_size, head_dim],
     v_pages [n_pages, n_kv_heads, head_dim, page_size] (fp16, bf16 or int8) and, for int8, k_steps and v_steps
-    [n_pages, n_kv_heads, page_size] fp32."""
+    [n_pages, n_kv_heads, page_size] fp32.  Its attributes cannot be set: the calls use the tensors it was made of."""
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, k_steps: torch.Tensor | None = None,
                  v_steps: torch.Tensor | None = None):
@@ -567,6 +567,11 @@ class KvCache:
                                       for t in (k_pages, v_pages, k_steps, v_steps)),
                                     n, page, h, d, _DTYPES[k_pages.dtype])
         self._ref = C.byref(self._struct)
+
+    def __setattr__(self, name, value):
+        if "_ref" in self.__dict__:
+            raise AttributeError(f"a KvCache's {name} cannot be set: make a new one over other tensors")
+        object.__setattr__(self, name, value)
 
 
 def ptq1_kv_cache(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, dtype=torch.bfloat16,

@@ -74,7 +74,7 @@ constexpr int64_t kMaxGridY = 65535;
 // Decode calls: rows per matrix (keeps the matvec grid's second dimension,
 // chunks of 32-row groups, far below its limit).
 constexpr int64_t kMaxLutRows = int64_t{1} << 20;
-// Decode attention: tokens of one sequence (1024 chunks of 4096).
+// Decode attention: tokens of one sequence (the steps of all fit 30 bits).
 constexpr int64_t kMaxDecodeLen = int64_t{1} << 22;
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -1358,7 +1358,7 @@ ptq1_status ptq1_attn_prompt(const void *q, int64_t q_stride, const void *k, int
         return fail(PTQ1_ERR_UNSUPPORTED, "k_stride or v_stride above 2^24 elements");
     if (ptq1::prompt_tiles(batch, n_q_rows, n_q_heads, n_kv_heads) * n_kv_heads >= kMaxBlocks256 / 2)
         return fail(PTQ1_ERR_UNSUPPORTED, "more than 2^23 tiles of 128 query rows");
-    if (batch == 0 || n_q_rows == 0 || max_q == 0) return ok();
+    if (batch == 0 || n_q_rows == 0) return ok();
     int64_t qb, kbytes, vbytes;
     const int64_t d = head_dim;
     PTQ1_TRY(check_strided(q, "q", n_q_rows, n_q_heads * d, q_stride, 2, &qb));

@@ -149,8 +149,8 @@ __device__ __forceinline__ float pow2(int e) { return __builtin_bit_cast(float, 
 // queries are fixed-point numbers of NQ signed 8-bit digits, scaled by a
 // power of two to the head's largest magnitude, and the digits' exact int32
 // products are joined in fp32.  V's codes become fp16 (exactly), the token's
-// step goes into its weight, relative to a running power of two that no step
-// exceeds.  Converting both to bf16 and taking the steps' whole range
+// step goes into its weight, relative to a running power of two that no such
+// product exceeds.  Converting both to bf16 and taking the steps' whole range
 // there spent 1300 vector instructions on 64 tokens instead of about 560: 93
 // us for 131071 tokens of 8 heads of 128 where 61 are enough now.
 template <typename C, typename QT, int D, int NQ, int NP>
@@ -206,8 +206,9 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
         const QT *qp = static_cast<const QT *>(a.q) + (static_cast<int64_t>(b) * a.hq + h0 + (col < nh ? col : 0)) * D;
         float mul = 1.0f;
         if constexpr (I8 || (std::is_same<T, _Float16>::value && std::is_same<QT, float>::value)) {
-            // the head's largest magnitude, brought to [1, 2) (fp16 terms) or
-            // below 2^(8 NQ - 2) (digits)
+            // the head's largest magnitude, brought to [2^14, 2^15) (fp16 terms:
+            // what the third leaves is then 2^-39 of it) or below 2^(8 NQ - 2)
+            // (digits)
             uint32_t mx = 0;  // of the bit patterns: NaN and infinity last
             for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
                 }
             mx = max(mx, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mx), 16, 64)));
             mx = max(mx, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mx), 32, 64)));
-            constexpr int BITS = I8 ? 8 * NQ - 3 : 0;
+            constexpr int BITS = I8 ? 8 * NQ - 3 : 14;
             const int e = static_cast<int>(mx >> 23) - 127;
             if (e == 128) {
                 c = __builtin_nanf("");  // a NaN or an infinity in the query
@@ -265,13 +266,18 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
             }
         }
     }
+    // fp16 weights as multiples of 2^-14 of themselves, sums too: small ones
+    // (many tokens beside one that takes nearly all) would fall below fp16's
+    // smallest step, 2^-24, otherwise
+    constexpr float kLift = std::is_same<C, _Float16>::value ? 14.0f : 0.0f;
     const at_f32x4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
     at_f32x4 o[D / 16];
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) o[i] = zero4;
     float m = -__builtin_inff(), l = 0.0f;
-    // int8: weights times steps in units of vunit / 2^14, so below 2^14 in fp16
-    float vunit = pow2(-112), vinv = pow2(112 + 14);
+    // int8: weights times steps enter in units of 2^(wexp - 14), wexp such that
+    // they are below 2^14 in fp16; o is in these units
+    int wexp = -112;
 
     // ---- one step's loads.  Tokens past the end are read from the last token
     // (K) or the last run (V), and masked below.  The pages of a lane's runs are
@@ -398,33 +404,21 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
         // a larger maximum rescales what is there (all lanes of a head alike)
         if (__ballot(top > m) != 0) {
             const float mn = fmaxf(m, top);
-            const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+            float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
             l *= f;
+            if constexpr (I8) {
+                // the units come down with the weights, or a large step whose
+                // weight has become nothing would keep the resolution coarse
+                int down = static_cast<int>(__builtin_bit_cast(uint32_t, f) >> 23) - 126;  // f < 2^down
+                down = down > 0 ? 0 : down < -112 - wexp ? -112 - wexp : down;
+                f *= pow2(-down);
+                wexp += down;
+            }
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) o[i] *= f;
             m = mn;
         }
-        const float ms = m == -__builtin_inff() ? 0.0f : m;
-        if constexpr (I8) {
-            // the steps' running power of two
-            float vtop = 0.0f;
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (tail && base + RUN * grp + 4 * t + i >= end) vs[t][i] = 0.0f;
-                    vtop = fmaxf(vtop, vs[t][i]);
-                }
-            vtop = lane_pair_max<32>(lane_pair_max<16>(vtop));
-            if (vtop > vunit) {
-                const int e = static_cast<int>(__builtin_bit_cast(uint32_t, vtop) >> 23) - 126;  // 2^e > vtop
-                const float f = vunit * pow2(-e);
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) o[i] *= f;
-                vunit = pow2(e);
-                vinv = pow2(14 - e);
-            }
-        }
+        const float ms = m == -__builtin_inff() ? 0.0f : m - kLift;
         float p[TS / 4];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -432,9 +426,26 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
             for (int i = 0; i < 4; ++i) {
                 float e = __builtin_amdgcn_exp2f(s[t][i] - ms);
                 l += e;
-                if constexpr (I8) e *= vs[t][i] * vinv;
+                if constexpr (I8) e *= tail && base + RUN * grp + 4 * t + i >= end ? 0.0f : vs[t][i];
                 p[4 * t + i] = e;
             }
+        if constexpr (I8) {
+            float top = 0.0f;
+#pragma unroll
+            for (int j = 0; j < TS / 4; ++j) top = fmaxf(top, p[j]);
+            top = lane_pair_max<32>(lane_pair_max<16>(top));
+            int e = static_cast<int>(__builtin_bit_cast(uint32_t, top) >> 23) - 126;  // 2^e > top
+            e = e > 126 ? 126 : e;
+            if (e > wexp) {
+                const float f = pow2(wexp - e > -126 ? wexp - e : -126);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) o[i] *= f;
+                wexp = e;
+            }
+            const float unit = pow2(14 - wexp);
+#pragma unroll
+            for (int j = 0; j < TS / 4; ++j) p[j] *= unit;
+        }
         // ---- O^T += V^T P^T, slot j of step u: token base + RUN grp + 8 u + j
         if (tail) {
             // what lies past the end may hold anything; zero weights do not silence a NaN
@@ -481,7 +492,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
     l = lane_pair_sum<32>(lane_pair_sum<16>(l));
     if constexpr (I8) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) o[i] *= vunit * pow2(-14);
+        for (int i = 0; i < D / 16; ++i) o[i] *= pow2(wexp - 14);
     }
 
     // ---- join the four waves: rows in LDS [wave][head][D + 4]

@@ -39,6 +39,13 @@ constexpr int kBufferFlags = 0x00027000;  // raw buffer of bytes
 
 constexpr int kKeys = 64;  // keys of a tile
 
+// fp16 weights are 2^7 times themselves (at most 2^15 with the maximum's lag,
+// below), and the sums with them: fp16's smallest step, 2^-24, is then 2^-31
+// of the largest weight at most, so that many small weights beside one large
+// one do not vanish.
+template <typename T>
+constexpr float kWeightLift = std::is_same<T, _Float16>::value ? 7.0f : 0.0f;
+
 // Query rows of a workgroup: 32 a wave, or a pair of waves (256-wide heads).
 constexpr int kPrRows = 128;
 // Waves of a workgroup.
@@ -246,25 +253,20 @@ __device__ __forceinline__ bool clean_tile(T *vb)
 // 64 pieces of 16 bytes per wave instruction at consecutive places; the lane
 // picks the piece that belongs there.  The tile's address is in the (scalar)
 // buffer descriptor, the lane's part a 32-bit offset that stays: piece i is
-// i * RS rows further on, where the swizzle is the same again after KC
-// pieces.  The descriptor ends with row `rows` - 1: nothing behind it is read.
+// i * RS rows further on, where the swizzle is the same.  The descriptor ends with row `rows` - 1: nothing behind it is read.
 template <typename T, int D, bool V>
 struct Staging {
     static constexpr int W = prompt_waves(D), P = D / 8, RS = 64 * W / P, N = kKeys / RS;
-    static constexpr int KC = 1;
     static_assert(RS % 16 == 0 || (V && RS % 4 == 0), "the swizzle is the same RS rows further on");
     const char *base;
     int64_t stride;  // bytes
-    uint32_t off[KC];
+    uint32_t off;
     __device__ __forceinline__ Staging(const void *src, int64_t row, int64_t row_stride, int kh)
         : base(reinterpret_cast<const char *>(static_cast<const T *>(src) + row * row_stride + static_cast<int64_t>(kh) * D)),
           stride(row_stride * 2)
     {
-#pragma unroll
-        for (int i = 0; i < KC; ++i) {
-            const uint32_t r = i * RS + threadIdx.x / P, p = threadIdx.x % P;
-            off[i] = r * static_cast<uint32_t>(stride) + 16 * (p ^ (V ? v_swizzle<D>(r) : k_swizzle<D>(r)));
-        }
+        const uint32_t r = threadIdx.x / P, p = threadIdx.x % P;
+        off = r * static_cast<uint32_t>(stride) + 16 * (p ^ (V ? v_swizzle<D>(r) : k_swizzle<D>(r)));
     }
     // rows n0 .. n0 + 63, of `rows`
     __device__ __forceinline__ void copy(T *dst, int n0, int rows) const
@@ -275,7 +277,7 @@ struct Staging {
         const int wave = threadIdx.x >> 6;
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            copy_to_lds(src, more * step + 2 * D, off[i % KC] + (i / KC * KC * RS) * step, dst + (i * W + wave) * 512);
+            copy_to_lds(src, more * step + 2 * D, off + i * RS * step, dst + (i * W + wave) * 512);
     }
 };
 
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptA
         __builtin_amdgcn_sched_group_barrier(0x8, kAhead, 0);
         if constexpr (BORDER) hide(s, n0);
         raise(largest(s));
-        const float ms = m == -__builtin_inff() ? 0.0f : m;
+        const float ms = m == -__builtin_inff() ? 0.0f : m - kWeightLift<T>;
         x8 pf[2 * KT];
 #pragma unroll
         for (int t = 0; t < KT; ++t)
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(64 * prompt_waves(256), 2) k_attn_prompt_wide(
             for (int i = 0; i < DT; ++i) o[i] *= f;
             m = mn;
         }
-        const float ms = m == -__builtin_inff() ? 0.0f : m;
+        const float ms = m == -__builtin_inff() ? 0.0f : m - kWeightLift<T>;
         x8 pf[2];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {

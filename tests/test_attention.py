@@ -503,6 +503,8 @@ def test_attn_prompt_bounds_and_ranges():
     assert bool(got[30:230].isnan().all())
     check_prompt(q, k, v, [30], [30], got[:30], True)
     check_prompt(q[230:], k[230:], v[230:], [17], [17], got[230:], True)
+    for bound in (dict(max_q=0), dict(max_k=0)):  # exceeded by all
+        assert bool(P.ptq1_attn_prompt(q, k, v, cu, cu, **bound).isnan().all())
     far = cumulated([30, 200, 18])  # the last one's keys end behind the last row
     got = P.ptq1_attn_prompt(q, k, v, cu, far, max_q=247, max_k=247)
     assert bool(got[230:].isnan().all()) and bool(got[:230].isfinite().all())
@@ -919,3 +921,104 @@ def test_attn_prompt_rows_far_apart(d):
         t.copy_(randn(g, *t.shape))
     got = P.ptq1_attn_prompt(q, k, v, cumulated([n]), cumulated([n]))
     check_prompt(q, k, v, [n], [n], got, True)
+
+
+# --------------------------------------------- weights far below the largest ----
+
+def ramp_sequence(kind, n):
+    """Scores in units of log2: one token that takes nearly everything, first or last, or a ramp up or down."""
+    s = torch.full((n,), -27.3, dtype=torch.float64, device=DEV)
+    if kind in ("first", "last"):
+        s[0 if kind == "first" else n - 1] = 0
+        return s
+    s = torch.linspace(-60, 0, n, dtype=torch.float64, device=DEV)
+    return s if kind == "up" else s.flip(0)
+
+
+@pytest.mark.parametrize("qt,ctype", PAIRS)
+@pytest.mark.parametrize("kind", ["first", "last", "up", "down"])
+def test_attn_decode_many_small_weights(qt, ctype, kind):
+    """A token that takes nearly the whole weight and has no value, beside thousands that have: what they add must not
+    vanish.  int8: that token's step is 2^20 times the others'.  A weight (int8: weight times step) enters as 16-bit
+    terms down to 2^-24 of a unit of which the largest has 2^13 at least, so it is off by its relative error or by
+    2^-38 of the largest, whichever is more."""
+    g = gen(90)
+    n, d = 3000, 64
+    table, pages = tables(g, [n], 64)
+    c = filled_cache(g, pages, 64, 1, d, ctype)
+    s = ramp_sequence(kind, n)
+    heavy = {"first": 0, "last": n - 1, "up": 0, "down": n - 1}[kind]  # ramps: the token that weighs least
+    rows = table[0].long()
+    place = torch.arange(n, device=DEV)
+    at, off = rows[place // 64], place % 64
+    # score = scale q0 k0 in log2 units: q0 = 1, scale ln 2, k0 = s (16-bit types round it: the stored value counts)
+    k0 = s.clone()
+    c.k_pages.zero_()
+    if ctype == I8:
+        c.k_steps.fill_(0.5)
+        k0 = (k0 * 2).round().clamp(-127, 127)
+    c.k_pages[at, 0, off, 0] = k0.to(c.dtype)
+    if ctype == I8:
+        c.v_steps.fill_(2.0 ** -7)
+        c.v_steps[at[heavy], 0, off[heavy]] = 2.0 ** 13
+    if kind in ("first", "last"):
+        c.v_pages[at[heavy], 0, :, off[heavy]] = 0
+    q = torch.zeros((1, 2, d), device=DEV, dtype=qt)
+    q[0, :, 0] = 1
+    scale = math.log(2.0)
+    got = P.ptq1_attn_decode(q, c, table, torch.tensor([n], dtype=torch.int32, device=DEV), scale=scale)[0].double()
+    kc, vc = cache_values(c)
+    k, v = sequence(c, kc, table, 0, n)[0], sequence(c, vc, table, 0, n)[0]
+    want, tol = attention_bounds(q[0].double(), k, v, scale, WEIGHT_TERM[(qt, ctype)])
+    p = torch.softmax(scale * (q[0].double() @ k.T.contiguous()), 1)
+    if ctype != BF16:
+        step = c.v_steps[at, 0, off].double()[None] if ctype == I8 else torch.ones_like(p)
+        floor = 2.0 ** -38 * (p * step).amax(1, keepdim=True)
+        tol = tol + floor * (v / step[0][:, None]).abs().sum(0)
+    tol = tol + half_step(want.abs() + tol, qt)
+    err = (got - want).abs()
+    assert bool((err <= tol).all()), f"{(err / tol).max().item():.3f} of the bound, {(err / want.abs()).max().item()}"
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["first", "last", "up", "down"])
+@pytest.mark.parametrize("rows", [2, 300])
+def test_attn_prompt_many_small_weights(dtype, d, kind, rows):
+    """The same through the prompt call, cut along the keys (few rows) or not.  fp16 weights have 11 bits, down to
+    2^-24 of a unit of which the largest weight has 2^7 at least: off by 2^-32 of it at most."""
+    g = gen(91)
+    n = 3000
+    s = ramp_sequence(kind, n)
+    q = torch.zeros((rows, 8, d), device=DEV, dtype=dtype)
+    q[:, :, 0] = 1
+    k = torch.zeros((n, 8, d), device=DEV, dtype=dtype)
+    k[:, :, 0] = s[:, None].to(dtype)
+    v = (randn(g, n, 8, d) + 2).to(dtype)  # (a mean that is not zero: the small weights add up)
+    if kind in ("first", "last"):
+        v[0 if kind == "first" else n - 1] = 0
+    scale = math.log(2.0)
+    got = P.ptq1_attn_prompt(q, k, v, cumulated([rows]), cumulated([n]), causal=False, scale=scale)
+    for h in (0, 7):
+        qq, kk, vv = (t[:, h].double() for t in (q, k, v))
+        want, tol = attention_bounds(qq, kk, vv, scale, torch.finfo(dtype).eps / 2)
+        if dtype == F16:
+            p = torch.softmax(scale * (qq @ kk.T.contiguous()), 1)
+            tol = tol + 2.0 ** -32 * p.amax(1, keepdim=True) * vv.abs().sum(0)
+        tol = tol + half_step(want.abs() + tol, dtype)
+        err = (got[:, h].double() - want).abs()
+        assert bool((err <= tol).all()), f"{(err / tol).max().item():.3f} of the bound"
+
+
+def test_attn_decode_small_queries_beside_a_large_one():
+    """fp32 queries over fp16: a large element that meets keys of zero takes no precision from the others that the
+    bound does not allow (three terms down to 2^-24 of a unit of which the head's largest has 2^14 at least)."""
+    g = gen(92)
+    n, d = 300, 128
+    table, pages = tables(g, [n], 16)
+    c = filled_cache(g, pages, 16, 1, d, F16)
+    c.k_pages[..., 5] = 0
+    q = randn(g, 1, 4, d)
+    q[..., 5] = 4096.0
+    got = P.ptq1_attn_decode(q, c, table, torch.tensor([n], dtype=torch.int32, device=DEV))
+    check_decode(q, c, table, [n], got)

@@ -246,7 +246,7 @@ def test_prompt_workspace():
     assert prompt(**few, ws=at(20))[0] == ALIAS
     for bad in ((-1, 16, 100, 8, 2, 128), (1, 16, 100, 8, 3, 128), (1, 16, 100, 8, 2, 100), (1, -1, 100, 8, 2, 128)):
         assert size(*bad) == 0
-    assert prompt(batch=0)[0] == 0 and prompt(nq=0)[0] == 0 and prompt(max_q=0)[0] == 0
+    assert prompt(batch=0)[0] == 0 and prompt(nq=0)[0] == 0
 
 
 # ------------------------------------------------------------- the binding ----
@@ -304,6 +304,9 @@ def test_binding_cache(host_ok):
         P.KvCache(z(4, 2, 16, 128), z(4, 2, 128, 16), z(4, 2, 16, dtype=torch.float32))
     with pytest.raises(ValueError, match="dtype"):
         P.ptq1_kv_cache(4, 16, 2, 128, torch.float32, "cpu")
+    c = kv()
+    with pytest.raises(AttributeError, match="k_pages cannot be set"):
+        c.k_pages = c.k_pages.clone()
 
 
 def test_binding_write(host_ok):
