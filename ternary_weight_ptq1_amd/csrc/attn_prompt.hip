@@ -458,17 +458,22 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptA
 // of one half of a tile's 64 keys and forms their weights, the pair exchanges
 // maxima and weights through LDS, and each multiplies all 64 keys' weights
 // with one half of the dimensions.  Eight waves, 128 rows, share the tiles: one
-// workgroup a CU, two waves a SIMD.  1657 queries of 24 heads over 4000 keys
-// and more: 273 us with one wave for 32 rows (one a SIMD), 285 with pairs in
-// workgroups of four waves and one buffer each for K and V (two a CU; the
-// copies had half a tile's time), 280 this way; 4000 queries: 286, 251, 250.
+// workgroup a CU, two waves a SIMD.  4000 queries of 24 heads over as many
+// keys: 238 us (826 TFLOP/s of visible pairs); one wave for 32 rows (one a
+// SIMD) took 286, pairs in workgroups of four waves with one buffer each for K
+// and V (two a CU; the copies have half a tile's time) 251, the next tile's
+// scores taken beside this one's weights 266 (the matrix cores and the vector
+// units then overlap in a wave, but the registers leave no reads ahead).
 //
-// Barriers with explicit waits: those of __syncthreads would wait for the
-// copies that have just been issued.
+// Barriers with waits of their own: __syncthreads would wait for the copies
+// that have just been issued.  The wait for the copies is the builtin, so that
+// the compiler knows of it; with one that it could not see it waited itself,
+// for the newest copies too, where the weights are read (238 us: 250).
 __device__ __forceinline__ void barrier_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 __device__ __forceinline__ void barrier_copies()
 {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 template <typename T>
@@ -673,7 +678,7 @@ PromptPlan prompt_plan(int64_t batch, int64_t q_rows, int64_t max_k, int32_t hq,
     // costs less than too much (1272 tiles of up to 2500 keys of 128, 89 us,
     // took 115 in two).  16 queries over 8016 keys: 146 us uncut, 20 in
     // chunks of 512; 1657 queries of 24 heads of 256 over 4000 and more: 307
-    // uncut, 274 in two.
+    // uncut, 270 in two.
     PromptPlan p;
     const double slots = d == 256 ? 256 : 512, key = d == 256 ? 0.04 : 0.029;  // workgroups the GPU holds
     const double tiles = static_cast<double>(prompt_tiles(batch, q_rows, hq, hkv) * hkv);
