@@ -26,6 +26,11 @@
 //     the matrix cores are nearly idle, so fp32 queries and the weights enter
 //     as two or three 16-bit terms: K and V are exact, so the result is that
 //     of fp32 products.
+//
+// Measured: 64 sequences of 3 to 8190 tokens, 32 heads over 8 of 128, bf16:
+// 55 us and 5 for the join (261 MB: 4.8 TB/s; a copy 5.4); 16 sequences of
+// 900 to 5000 tokens, 24 heads over 4 of 256, fp16: 34 and 4.  77 tokens of
+// one sequence: 4.9 us in one launch.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

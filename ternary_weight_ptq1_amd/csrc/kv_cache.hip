@@ -3,7 +3,10 @@
 // semantics: include/ptq1.h.
 //
 // Both are one pass over their data, bounded by HBM for many tokens and by
-// one launch's latency for a few.
+// one launch's latency for a few.  Measured: 8191 tokens of 24 + 4 + 4 heads
+// of 256, fp32 to bf16, written in 87 us (4.65 TB/s; a copy 5.4), one token
+// of 40 + 8 + 8 heads of 128 in 3.0; 96 thousand tokens of 8 heads of 128
+// read back from int8 to bf16 in 88 (4.5 TB/s, two thirds of it written).
 #include <hip/hip_runtime.h>
 
 #include "ptq1_attn.h"
