@@ -67,21 +67,37 @@ struct DecodeArgs {
 
 // Steps of a sequence: one at least (an empty or refused one has its rows
 // written too).  All sequences' together are below 2^30 (2^16 times 2^14).
-__device__ __forceinline__ int decode_steps(const DecodeArgs &a, int64_t b)
+__device__ __forceinline__ int decode_steps(const DecodeArgs &a, int len)
 {
-    const int len = a.lens[b];
     return len <= 0 || len > a.max_len ? 1 : (len + kStep - 1) / kStep;
 }
 
-// Steps of the sequences before `end`.
-__device__ __forceinline__ int steps_before(const DecodeArgs &a, int64_t end)
+__device__ __forceinline__ int wave_total(int v)
 {
-    int sum = 0;
-    for (int64_t i = threadIdx.x & 63; i < end; i += 64) sum += decode_steps(a, i);
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
-    return __builtin_amdgcn_readfirstlane(sum);
+    for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+    return __builtin_amdgcn_readfirstlane(v);
 }
+
+// The lengths of sequences lane, lane + 64 ..., of which the first stays in a
+// register: a batch of 64 makes one trip to memory for them.
+struct LaneLens {
+    int first;
+    __device__ __forceinline__ LaneLens(const DecodeArgs &a)
+    {
+        const int64_t lane = threadIdx.x & 63;
+        first = lane < a.batch ? a.lens[lane] : 0;
+    }
+    __device__ __forceinline__ int operator()(const DecodeArgs &a, int64_t i) const { return i < 64 ? first : a.lens[i]; }
+    // the sum of f(length) over the sequences before `end`
+    template <class F>
+    __device__ __forceinline__ int sum(const DecodeArgs &a, int64_t end, F f) const
+    {
+        int v = 0;
+        for (int64_t i = threadIdx.x & 63; i < end; i += 64) v += f((*this)(a, i));
+        return wave_total(v);
+    }
+};
 
 // Steps of one workgroup's piece of a sequence.  Few sequences: pieces that
 // fill the GPU once.  Many: half of that, since their ends leave the pieces
@@ -186,103 +202,48 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
     const int nh = group - hb * kDecHeads < kDecHeads ? group - hb * kDecHeads : kDecHeads;
     // ---- this workgroup's piece: up to `per` steps of one sequence
     const int64_t piece = blockIdx.x / hgroups;
-    int per = 1, b = static_cast<int>(piece), first = 0;
+    // (every argument in one trip to memory: the branch would take more)
+    asm volatile("" ::"s"(a.q), "s"(a.k_pages), "s"(a.v_pages), "s"(a.k_steps), "s"(a.v_steps), "s"(a.n_pages),
+                 "s"(a.page_shift), "s"(a.table), "s"(a.max_pages), "s"(a.lens), "s"(a.batch), "s"(a.max_len),
+                 "s"(a.shares), "s"(a.scale));
+    int per = 1, b = static_cast<int>(piece), first = 0, len;
     if (a.cut) {
-        per = steps_per_piece(a, steps_before(a, a.batch));
+        const LaneLens lens(a);
+        per = steps_per_piece(a, lens.sum(a, a.batch, [&](int n) { return decode_steps(a, n); }));
         int64_t seq, tile;
-        if (!find_tile<false>(piece, a.batch, [&](int64_t i) { return (decode_steps(a, i) + per - 1) / per; }, seq, tile))
+        int mine = 0;
+        if (!find_tile<false>(
+                piece, a.batch,
+                [&](int64_t i) {
+                    mine = lens(a, i);
+                    return (decode_steps(a, mine) + per - 1) / per;
+                },
+                seq, tile))
             return;
         b = __builtin_amdgcn_readfirstlane(static_cast<int>(seq));
         first = __builtin_amdgcn_readfirstlane(static_cast<int>(tile));
-    }
-    const int len = a.lens[b];
+        len = __builtin_amdgcn_readlane(mine, b & 63);
+    } else
+        len = a.lens[b];
     const bool bad_len = len < 0 || len > a.max_len;
-    const bool whole = decode_steps(a, b) <= per;
+    const bool whole = decode_steps(a, len) <= per;
     const int begin = first * per * kStep;
     const int end = bad_len ? begin : (begin + per * kStep < len ? begin + per * kStep : len);
 
-    // ---- queries: B operand, column = head, k = 8 consecutive dimensions
-    // (int8: dimension 64 p + 16 grp + 8 s of steps 2 p + s, the bytes a lane
-    // loads at once; else 32 kk + 8 grp)
-    float c = a.scale * kLog2e;  // scores in units of log2
+    // ---- the queries' own loads, first of all: of column = head, dimensions
+    // 32 kk + 8 grp .. (int8: for the magnitude; and of wave kk operand kk's
+    // 64 kk + 16 grp ..)
+    typedef QT q8 __attribute__((ext_vector_type(8)));
     constexpr int QK = I8 ? D / 64 : KK;
-    x8 qf[I8 ? 1 : QK][NQ];  // (int8: the digits stay in LDS)
-    {
-        const QT *qp = static_cast<const QT *>(a.q) + (static_cast<int64_t>(b) * a.hq + h0 + (col < nh ? col : 0)) * D;
-        float mul = 1.0f;
-        if constexpr (I8 || (std::is_same<T, _Float16>::value && std::is_same<QT, float>::value)) {
-            // the head's largest magnitude, brought to [2^14, 2^15) (fp16 terms:
-            // what the third leaves is then 2^-39 of it) or below 2^(8 NQ - 2)
-            // (digits)
-            uint32_t mx = 0;  // of the bit patterns: NaN and infinity last
-            for (int kk = 0; kk < KK; ++kk)
+    const QT *qp = static_cast<const QT *>(a.q) + (static_cast<int64_t>(b) * a.hq + h0 + (col < nh ? col : 0)) * D;
+    q8 raw[KK], own[2];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float x = static_cast<float>(qp[32 * kk + 8 * grp + j]);
-                    const uint32_t u = __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
-                    mx = mx > u ? mx : u;
-                }
-            mx = max(mx, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mx), 16, 64)));
-            mx = max(mx, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mx), 32, 64)));
-            constexpr int BITS = I8 ? 8 * NQ - 3 : 14;
-            const int e = static_cast<int>(mx >> 23) - 127;
-            if (e == 128) {
-                c = __builtin_nanf("");  // a NaN or an infinity in the query
-                if (I8) mul = 0.0f;
-            } else if (e > -90 && e < 96) {
-                mul = pow2(BITS - e);
-                c *= pow2(e - BITS);
-            } else if (e >= 96) {
-                mul = pow2(BITS - 96) * pow2(96 - e);  // two factors, each in range
-                c = c * pow2(96 - BITS) * pow2(e - 96);
-            } else if (I8) {
-                mul = pow2(BITS + 90);  // all below 2^-90: fixed point to that
-                c *= pow2(-90 - BITS);
-            }
-        }
-        if constexpr (I8) {
-            // the waves share the work: operand kk by wave kk, through LDS
-            static_assert(QK <= kDecWaves, "an operand for each wave at most");
-            at_i32x4 *shared = reinterpret_cast<at_i32x4 *>(lds);
-            if (wave < QK) {
-                at_i32x4 dig[NQ];
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) dig[n] = at_i32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    int v = static_cast<int>(rintf(static_cast<float>(qp[64 * wave + 16 * grp + j]) * mul));
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-                        dig[n][j >> 2] |= (v & 255) << (8 * (j & 3));
-                        v = (v - static_cast<int8_t>(v)) >> 8;
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) shared[(wave * NQ + n) * 64 + lane] = dig[n];
-            }
-            __syncthreads();
-        } else {
-#pragma unroll
-            for (int kk = 0; kk < QK; ++kk) {
-                float x[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = static_cast<float>(qp[32 * kk + 8 * grp + j]) * mul;
-                split_terms<T, NQ>(x, qf[kk]);
-            }
-        }
+    for (int kk = 0; kk < KK; ++kk) raw[kk] = *reinterpret_cast<const q8 *>(qp + 32 * kk + 8 * grp);
+    if constexpr (I8) {
+        const int at = 64 * (wave < QK ? wave : 0) + 16 * grp;
+        own[0] = *reinterpret_cast<const q8 *>(qp + at);
+        own[1] = *reinterpret_cast<const q8 *>(qp + at + 8);
     }
-    // fp16 weights as multiples of 2^-14 of themselves, sums too: small ones
-    // (many tokens beside one that takes nearly all) would fall below fp16's
-    // smallest step, 2^-24, otherwise
-    constexpr float kLift = std::is_same<C, _Float16>::value ? 14.0f : 0.0f;
-    const at_f32x4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
-    at_f32x4 o[D / 16];
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) o[i] = zero4;
-    float m = -__builtin_inff(), l = 0.0f;
-    // int8: weights times steps enter in units of 2^(wexp - 14), wexp such that
-    // they are below 2^14 in fp16; o is in these units
-    int wexp = -112;
 
     // ---- one step's loads.  Tokens past the end are read from the last token
     // (K) or the last run (V), and masked below.  The pages of a lane's runs are
@@ -329,6 +290,77 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
         for (int t = 0; t < NT; ++t) r[t] = *reinterpret_cast<const at_f32x4 *>(steps + cell + 4 * t);
     };
 
+    // ---- queries: B operand, column = head, k = 8 consecutive dimensions
+    // (int8: dimension 64 p + 16 grp + 8 s of steps 2 p + s, the bytes a lane
+    // loads at once; else 32 kk + 8 grp)
+    float c = a.scale * kLog2e;  // scores in units of log2
+    x8 qf[I8 ? 1 : QK][NQ];  // (int8: the digits stay in LDS)
+    auto make_queries = [&] {
+        float mul = 1.0f;
+        if constexpr (I8 || (std::is_same<T, _Float16>::value && std::is_same<QT, float>::value)) {
+            // the head's largest magnitude, brought to [2^14, 2^15) (fp16 terms:
+            // what the third leaves is then 2^-39 of it) or below 2^(8 NQ - 2)
+            // (digits)
+            uint32_t mx = 0;  // of the bit patterns: NaN and infinity last
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float x = static_cast<float>(raw[kk][j]);
+                    const uint32_t u = __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
+                    mx = mx > u ? mx : u;
+                }
+            mx = max(mx, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mx), 16, 64)));
+            mx = max(mx, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mx), 32, 64)));
+            constexpr int BITS = I8 ? 8 * NQ - 3 : 14;
+            const int e = static_cast<int>(mx >> 23) - 127;
+            if (e == 128) {
+                c = __builtin_nanf("");  // a NaN or an infinity in the query
+                if (I8) mul = 0.0f;
+            } else if (e > -90 && e < 96) {
+                mul = pow2(BITS - e);
+                c *= pow2(e - BITS);
+            } else if (e >= 96) {
+                mul = pow2(BITS - 96) * pow2(96 - e);  // two factors, each in range
+                c = c * pow2(96 - BITS) * pow2(e - 96);
+            } else if (I8) {
+                mul = pow2(BITS + 90);  // all below 2^-90: fixed point to that
+                c *= pow2(-90 - BITS);
+            }
+        }
+        if constexpr (I8) {
+            // the waves share the work: operand kk by wave kk, through LDS
+            static_assert(QK <= kDecWaves, "an operand for each wave at most");
+            at_i32x4 *shared = reinterpret_cast<at_i32x4 *>(lds);
+            if (wave < QK) {
+                at_i32x4 dig[NQ];
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) dig[n] = at_i32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    int v = static_cast<int>(rintf(static_cast<float>(own[j >> 3][j & 7]) * mul));
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        dig[n][j >> 2] |= (v & 255) << (8 * (j & 3));
+                        v = (v - static_cast<int8_t>(v)) >> 8;
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) shared[(wave * NQ + n) * 64 + lane] = dig[n];
+            }
+        } else {
+#pragma unroll
+            for (int kk = 0; kk < QK; ++kk) {
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = static_cast<float>(raw[kk][j]) * mul;
+                split_terms<T, NQ>(x, qf[kk]);
+            }
+        }
+    };
+
+    // ---- the first step's loads, ahead of the queries' conversion (in the same
+    // branch: behind it the compiler would wait for these loads as well)
     at_u32x4 kr[NL], vr[NL];
     at_f32x4 ks[NT], vs[NT];
     int base = begin + wave * TS;
@@ -343,7 +375,24 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
         load_v(base, v0, vr);
         kpage = page_of(base + kDecWaves * TS + RUN * (col >> 2));
         vpage = page_of(base + kDecWaves * TS + RUN * grp);
-    }
+        make_queries();
+    } else if (I8)
+        make_queries();
+    // not __syncthreads: it would wait for the first K and V
+    if constexpr (I8) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    // fp16 weights as multiples of 2^-14 of themselves, sums too: small ones
+    // (many tokens beside one that takes nearly all) would fall below fp16's
+    // smallest step, 2^-24, otherwise
+    constexpr float kLift = std::is_same<C, _Float16>::value ? 14.0f : 0.0f;
+    const at_f32x4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
+    at_f32x4 o[D / 16];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) o[i] = zero4;
+    float m = -__builtin_inff(), l = 0.0f;
+    // int8: weights times steps enter in units of 2^(wexp - 14), wexp such that
+    // they are below 2^14 in fp16; o is in these units
+    int wexp = -112;
+
     for (; base < end; base += kDecWaves * TS) {
         const int next = base + kDecWaves * TS;
         // ---- scores: tile t, register i of lane: token base + RUN grp + 4 t + i, head col
@@ -553,13 +602,12 @@ __global__ void __launch_bounds__(256) k_attn_join(DecodeArgs a)
     __shared__ float red[4];
     __shared__ at_f32x4 sums[G][LPR];
     const int64_t b = blockIdx.y, h = blockIdx.x;
-    const int per = steps_per_piece(a, steps_before(a, a.batch));
-    const int n = (decode_steps(a, b) + per - 1) / per;
+    const LaneLens lens(a);
+    const int per = steps_per_piece(a, lens.sum(a, a.batch, [&](int n) { return decode_steps(a, n); }));
+    const auto pieces = [&](int len) { return (decode_steps(a, len) + per - 1) / per; };
+    const int n = pieces(b < 64 ? __builtin_amdgcn_readlane(lens.first, static_cast<int>(b)) : a.lens[b]);
     if (n == 1) return;
-    int64_t before = 0;  // pieces of the sequences before
-    for (int64_t i = threadIdx.x & 63; i < b; i += 64) before += (decode_steps(a, i) + per - 1) / per;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) before += __shfl_xor(before, o, 64);
+    const int64_t before = lens.sum(a, b, pieces);
     auto slot = [&](int i) { return (before + i) * a.hq + h; };
     float M = -__builtin_inff();
     for (int i = threadIdx.x; i < n; i += 256) M = fmaxf(M, a.part_ml[slot(i) * 2]);

@@ -111,7 +111,8 @@ __device__ __forceinline__ int visible(const PromptArgs &a, int tok, int off, in
 }
 
 // One tile of R query rows of one kv head, and the keys of one workgroup (all
-// below 2^31: the host has seen to it).
+// below 2^31: the host has seen to it).  The tiles of a kv head are numbered
+// densely; those from plan.whole on have plan.splits workgroups each.
 struct PromptTile {
     int q0, k0, lk, off;    // the sequence: its first rows, its keys, keys before its first query
     int rows, row0, end;    // its rows; this tile's first one and the one behind its last
@@ -126,15 +127,27 @@ struct PromptTile {
 // allows (eight heads: one each).  False: nothing (more) to do.  The rows of
 // a sequence past its bounds, or with rows that are not there, become NaN.
 template <typename T, int D>
-__device__ __forceinline__ bool prompt_tile(const PromptArgs &a, const PromptPlan &plan, int part, bool join, PromptTile &t)
+__device__ __forceinline__ bool prompt_tile(const PromptArgs &a, const PromptPlan &plan, bool join, int &part, PromptTile &t)
 {
     constexpr int R = kPrRows;
     t.group = a.hq / a.hkv;
     t.kh = static_cast<int>(blockIdx.x % static_cast<uint32_t>(a.hkv));
+    int number = static_cast<int>(blockIdx.x / static_cast<uint32_t>(a.hkv));
+    // all first parts of the tiles that are cut, then all second ones ...; no
+    // branch, which would take another trip to the arguments (0.4 us of a
+    // short prompt's 9); exact below 2^20 workgroups of a kv head
+    part = 0;
+    if (join)
+        number += plan.whole;
+    else {
+        part = static_cast<int>(fmaxf((static_cast<float>(number - plan.whole) + 0.5f) * plan.per_cut, 0.0f));
+        part = __builtin_amdgcn_readfirstlane(part);
+        number -= part * (plan.tiles - plan.whole);
+    }
     int64_t b, at;
     int qf = 0, qe = 0, kf = 0, ke = 0;  // the lane's sequence (all four at once: one trip to memory)
     if (!find_tile<true>(
-            blockIdx.x / static_cast<uint32_t>(a.hkv), a.batch,
+            number, a.batch,
             [&](int64_t i) {
                 qf = a.cu_q[i];
                 qe = a.cu_q[i + 1];
@@ -168,7 +181,7 @@ __device__ __forceinline__ bool prompt_tile(const PromptArgs &a, const PromptPla
     t.row0 = ((t.rows + R - 1) / R - 1 - static_cast<int>(at)) * R;
     t.end = t.row0 + R < t.rows ? t.row0 + R : t.rows;
     t.reach = visible(a, (t.end - 1) / t.group, t.off, t.lk);
-    t.split = t.reach > plan.chunk;
+    t.split = number >= plan.whole && t.reach > plan.chunk;
     t.first = part * plan.chunk;
     if (t.first >= t.reach && part > 0) return false;
     t.any = t.split && t.reach - t.first > plan.chunk ? t.first + plan.chunk : t.reach;
@@ -321,9 +334,9 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptA
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = lane & 31, half = lane >> 5;
-    const int piece = static_cast<int>(blockIdx.y);
+    int piece;
     PromptTile t;
-    if (!prompt_tile<T, D>(a, plan, piece, false, t)) return;
+    if (!prompt_tile<T, D>(a, plan, false, piece, t)) return;
     const int any = t.any, all = t.all;
     int seen = 0;  // (set for the border tiles; the others use every key)
 
@@ -499,9 +512,9 @@ __global__ void __launch_bounds__(64 * prompt_waves(256), 2) k_attn_prompt_wide(
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = lane & 31, half = lane >> 5;
     const int pair = wave >> 1, part = wave & 1;
-    const int piece = static_cast<int>(blockIdx.y);
+    int piece;
     PromptTile t;
-    if (!prompt_tile<T, D>(a, plan, piece, false, t)) return;
+    if (!prompt_tile<T, D>(a, plan, false, piece, t)) return;
     const PromptRow row = prompt_row(a, t, t.row0 + 32 * pair + col);
     const int seen = row.seen, any = t.any, all = t.all;
 
@@ -624,8 +637,9 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256) k_prompt_join(PromptArgs a, PromptPlan plan, const float *part)
 {
     constexpr int LPR = D / 4;
+    int piece;
     PromptTile t;
-    if (!prompt_tile<T, D>(a, plan, 0, true, t) || !t.split) return;
+    if (!prompt_tile<T, D>(a, plan, true, piece, t) || !t.split) return;
     const int n = (t.reach + plan.chunk - 1) / plan.chunk;
     const int x = threadIdx.x % LPR;
     const int r = t.row0 + static_cast<int>(blockIdx.y * join_rows(D) + threadIdx.x / LPR);
@@ -652,14 +666,14 @@ __global__ void __launch_bounds__(256) k_prompt_join(PromptArgs a, PromptPlan pl
 template <typename T, int D>
 hipError_t prompt_launch(const PromptArgs &a, const PromptPlan &plan, float *part, hipStream_t s)
 {
-    const uint32_t tiles = static_cast<uint32_t>(prompt_tiles(a.batch, a.q_rows, a.hq, a.hkv) * a.hkv);
-    const dim3 grid(tiles, static_cast<uint32_t>(plan.splits));
+    const int cut = plan.tiles - plan.whole;
+    const dim3 grid(static_cast<uint32_t>((plan.whole + cut * plan.splits) * a.hkv));
     if constexpr (D == 256)
         hipLaunchKernelGGL((k_attn_prompt_wide<T>), grid, dim3(64 * prompt_waves(D)), 0, s, a, plan, part);
     else
         hipLaunchKernelGGL((k_attn_prompt<T, D>), grid, dim3(64 * prompt_waves(D)), 0, s, a, plan, part);
     if (plan.splits > 1)
-        hipLaunchKernelGGL((k_prompt_join<T, D>), dim3(tiles, kPrRows / join_rows(D)), dim3(256), 0, s, a, plan, part);
+        hipLaunchKernelGGL((k_prompt_join<T, D>), dim3(static_cast<uint32_t>(cut * a.hkv), kPrRows / join_rows(D)), dim3(256), 0, s, a, plan, part);
     return hipGetLastError();
 }
 
@@ -680,32 +694,44 @@ int64_t prompt_tiles(int64_t batch, int64_t q_rows, int32_t hq, int32_t hkv)
 
 PromptPlan prompt_plan(int64_t batch, int64_t q_rows, int64_t max_k, int32_t hq, int32_t hkv, int32_t d)
 {
-    // The time with the keys of every tile cut in n, in us: rounds of workgroups,
-    // each of a key's time as measured with the GPU full, and from n = 2 on
-    // the parts' rows in fp32 (written and read, at half of HBM's rate: they
-    // come in bursts) and the join.  Causal tiles reach half as far on
-    // average, and ragged batches less: this cuts rather too little, which
-    // costs less than too much (1272 tiles of up to 2500 keys of 128, 89 us,
-    // took 115 in two).  16 queries over 8016 keys: 146 us uncut, 20 in
-    // chunks of 512; 1657 queries of 24 heads of 256 over 4000 and more: 307
-    // uncut, 270 in two.
+    // The time with tiles cut in n along their keys, in us: rounds of
+    // workgroups, each of a key's time as measured with the GPU full, and from
+    // n = 2 on the parts' rows in fp32 (written and read, at half of HBM's rate:
+    // they come in bursts) and the join.  Either all tiles are cut, or only
+    // those behind the last full round of whole ones, if the tiles reach about
+    // equally far (few queries behind many keys): of whole prompts' tiles the
+    // last ones are the shortest, which fill the gaps as they are (1272 tiles of
+    // up to 2500 keys of 128, 89 us, took 115 cut in two).  16 queries over 8016
+    // keys: 146 us uncut, 20 in chunks of 512; 1657 queries of 24 heads of 256 over 4000 and more, 320 tiles: 307
+    // uncut, 266 all cut in two, 229 the last 64 in three.
     PromptPlan p;
     const double slots = d == 256 ? 256 : 512, key = d == 256 ? 0.04 : 0.029;  // workgroups the GPU holds
-    const double tiles = static_cast<double>(prompt_tiles(batch, q_rows, hq, hkv) * hkv);
+    const int64_t tiles = prompt_tiles(batch, q_rows, hq, hkv);
+    p.tiles = static_cast<int32_t>(tiles);
+    const bool alike = batch > 0 && max_k >= 4 * (q_rows / batch);
+    const int64_t full = alike ? static_cast<int64_t>(static_cast<double>(tiles * hkv) / slots) * static_cast<int64_t>(slots) / hkv : 0;
     double best = 0.0;
     int n = 1;
-    for (int i = 1; i <= 64 && max_k / i >= 256; ++i) {
-        double us = __builtin_ceil(tiles * i / slots) * static_cast<double>(max_k) / i * key;
-        if (i > 1) us += 6.0 + tiles * i * kPrRows * d * 4 * 2 / 2.5e6;
-        if (i == 1 || us < best * 0.95) {
-            best = us;
-            n = i;
+    for (const int64_t whole : {int64_t{0}, full}) {
+        if (whole == 0 && best > 0.0) break;  // the same again
+        const double rest = static_cast<double>((tiles - whole) * hkv);
+        const double before = __builtin_ceil(static_cast<double>(whole * hkv) / slots) * static_cast<double>(max_k) * key;
+        for (int i = whole > 0 ? 2 : 1; i <= 64 && max_k / i >= 256; ++i) {
+            double us = before + __builtin_ceil(rest * i / slots) * static_cast<double>(max_k) / i * key;
+            if (i > 1) us += 6.0 + rest * i * kPrRows * d * 4 * 2 / 2.5e6;
+            if (i == 1 || us < best * 0.95) {
+                best = us;
+                n = i;
+                p.whole = static_cast<int32_t>(whole);
+            }
         }
     }
     p.chunk = static_cast<int32_t>(((max_k + n - 1) / n + 127) / 128 * 128);
     if (p.chunk == 0) p.chunk = 128;
     p.splits = static_cast<int32_t>(max_k > 0 ? (max_k + p.chunk - 1) / p.chunk : 1);
+    if (p.splits == 1) p.whole = 0;
     if (p.splits > 1) {
+        p.per_cut = 1.0f / static_cast<float>(tiles - p.whole);
         p.rows_floats = static_cast<size_t>(q_rows) * hq * p.splits * d;
         p.part_floats = p.rows_floats + static_cast<size_t>(q_rows) * hq * p.splits * 2;
     }

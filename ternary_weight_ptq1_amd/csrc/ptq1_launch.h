@@ -178,9 +178,11 @@ struct PromptArgs {
     void *out;
 };
 // The keys are cut into chunks of `chunk` (a multiple of 128): a tile of query
-// rows that reaches further than one is worked on by several workgroups.
+// rows (of at most `tiles` for one kv head) from number `whole` on that
+// reaches further than one is worked on by several workgroups.
 struct PromptPlan {
-    int32_t chunk = 0, splits = 1;
+    int32_t chunk = 0, splits = 1, whole = 0, tiles = 0;
+    float per_cut = 0.0f;  // 1 / (tiles - whole), 0 with splits = 1
     size_t rows_floats = 0, part_floats = 0;
 };
 PromptPlan prompt_plan(int64_t batch, int64_t q_rows, int64_t max_k, int32_t hq, int32_t hkv, int32_t d);

@@ -1022,3 +1022,29 @@ def test_attn_decode_small_queries_beside_a_large_one():
     q[..., 5] = 4096.0
     got = P.ptq1_attn_decode(q, c, table, torch.tensor([n], dtype=torch.int32, device=DEV))
     check_decode(q, c, table, [n], got)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,d,lq,lk", [
+    (128, 16, 256, [150, 126], [2400, 2300]),
+    (128, 16, 128, [300, 40, 196], [3000, 2900, 1000]),
+    (64, 32, 64, [400, 1, 666], [2700, 2800, 2600]),
+])
+def test_attn_prompt_last_tiles_cut(dtype, causal, hq, hkv, d, lq, lk):
+    """More tiles than the GPU holds at once: those behind the last full round are cut along the keys."""
+    g = gen(hq + d + sum(lk))
+    assert P.workspace_bytes("attn_prompt", len(lq), sum(lq), max(lk), hq, hkv, d) > 0
+    q, k, v = prompt_state(g, lq, lk, hq, hkv, d, dtype)
+    args = dict(max_q=max(lq), max_k=max(lk), causal=causal)
+    got = P.ptq1_attn_prompt(q, k, v, cumulated(lq), cumulated(lk), **args)
+    check_prompt(q, k, v, lq, lk, got, causal)
+    assert torch.equal(got, P.ptq1_attn_prompt(q, k, v, cumulated(lq), cumulated(lk), **args))
+    # one sequence refused: the others as they were within their bounds
+    bad = cumulated(lk)
+    bad[-1] += 1
+    args["max_k"] += 1
+    got = P.ptq1_attn_prompt(q, k, v, cumulated(lq), bad, **args)
+    first = sum(lq[:-1])
+    assert bool(got[first:].isnan().all())
+    check_prompt(q, k, v, lq[:-1], lk[:-1], got, causal)
