@@ -19,6 +19,7 @@
 //     registers of a lane are 8 (int8 caches: 16) consecutive tokens of its
 //     head: exactly the k-slots of the lane's V operand, so P goes from the
 //     softmax into the second product without leaving its lane.
+//   - The first K and V are requested before the queries are converted.
 //   - A wave's next K is requested as soon as the first product has consumed
 //     the current one, its next V after the second: one of the two is always
 //     in flight.
@@ -28,9 +29,9 @@
 //     of fp32 products.
 //
 // Measured: 64 sequences of 3 to 8190 tokens, 32 heads over 8 of 128, bf16:
-// 55 us and 5 for the join (261 MB: 4.8 TB/s; a copy 5.4); 16 sequences of
-// 900 to 5000 tokens, 24 heads over 4 of 256, fp16: 34 and 4.  77 tokens of
-// one sequence: 4.9 us in one launch.
+// 55 us and 5 for the join (261 MB: 4.7 TB/s; a copy 5.4); 16 sequences of
+// 900 to 5000 tokens, 24 heads over 4 of 256, fp16: 31 and 5.  77 tokens of
+// one sequence: 4.7 us in one launch.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

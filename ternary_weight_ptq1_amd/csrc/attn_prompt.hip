@@ -7,7 +7,7 @@
 // matrix cores: 2 d multiply-adds for every visible pair, against 2 bytes of
 // each operand.  Measured: 16384 tokens, 40 heads over 8 of 128, causal:
 // 2.5 ms (1090 TFLOP/s of visible pairs; a library matrix product 1180 to
-// 1350), matrix cores busy 58% of the cycles and vector units 51%, at a clock
+// 1350), matrix cores busy 60% of the cycles and vector units 52%, at a clock
 // of 1.75 GHz; 9 prompts of 5 to 2500 tokens 87 us; 33 tokens 8.6 us.
 //
 // Rows.  The query rows of a kv head are its group's heads of every token
