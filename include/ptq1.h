@@ -386,7 +386,8 @@ ptq1_status ptq1_gemm_w2a8(const uint8_t *tiled, int64_t n, int64_t k, const flo
  * value is step * code (step = max|x| / 127 over the head's row, code =
  * rint(x * float(127 / max|x|)), ties to even, as in ptq1_matvec_w2a8; a row
  * below 2^-119 in magnitude is stored as zeros; a row that holds a NaN or an
- * infinity reads back as NaN).  V is dimension-major because the attention
+ * infinity reads back as NaN; steps that a program writes itself are not
+ * negative and below 2^122, or NaN).  V is dimension-major because the attention
  * over one token multiplies whole runs of tokens of one dimension: both
  * operands of both products are then 16 contiguous bytes per lane.  A token's
  * slot is page * page_size + its place in the page.  Cache memory needs no
@@ -474,7 +475,7 @@ ptq1_status ptq1_kv_read(const ptq1_kv_cache *cache, const int32_t *block_table,
  *              among those the length covers, makes the sequence's rows NaN.
  *   max_len    a bound on the lengths that the caller knows (at most
  *              max_pages * page_size); the work is laid out for it.
- *   scale      positive and finite.
+ *   scale      positive, 2^126 at most.
  * The products run on the matrix cores.  Over 16-bit caches K and V enter
  * exactly, fp32 queries as three 16-bit terms and weights as two or three
  * (bf16 queries: two, 16 bits of a weight; fp16: down to 2^-38 of the row's
@@ -515,7 +516,7 @@ ptq1_status ptq1_attn_decode(const void *q, int32_t q_dtype, int64_t batch, int3
  *        caller knows; the work is laid out for them.  A sequence that
  *        exceeds one gets NaN rows, as does one whose rows lie outside
  *        [0, n_q_rows) or [0, n_k_rows) (those inside q's range).
- *   scale  positive and finite.
+ *   scale  positive, 2^126 at most.
  * bf16 or fp16 matrix cores, fp32 scores, maxima, sums and accumulators; the
  * weights enter the second product rounded to dtype (fp16: to 11 bits, down to
  * 2^-32 of the row's largest), the sum is over fp32.

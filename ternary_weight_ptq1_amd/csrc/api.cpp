@@ -1168,7 +1168,8 @@ ptq1_status check_heads(int32_t hq, int32_t hkv)
 
 ptq1_status check_scale(float scale)
 {
-    if (!(scale > 0.0f) || scale > 3.0e38f) return fail(PTQ1_ERR_SHAPE, "scale must be positive and finite");
+    // (times log2 e it is finite)
+    if (!(scale > 0.0f) || scale > 0x1p126f) return fail(PTQ1_ERR_SHAPE, "scale must be positive, 2^126 at most");
     return PTQ1_OK;
 }
 

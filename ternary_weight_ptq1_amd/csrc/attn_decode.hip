@@ -102,7 +102,7 @@ struct LaneLens {
 
 // Steps of one workgroup's piece of a sequence.  Few sequences: pieces that
 // fill the GPU once.  Many: half of that, since their ends leave the pieces
-// unequal (64 sequences of 3 to 8190 tokens: 62 us with 512 tokens a piece,
+// unequal (64 sequences of 3 to 8190 tokens: 61 us with 512 tokens a piece,
 // 71 with 256, 75 with 2048; one of 131071 over int8: 64 us in one round of
 // 2048, 75 in two).
 __device__ __forceinline__ int steps_per_piece(const DecodeArgs &a, int total)

@@ -160,6 +160,7 @@ def test_read_nothing():
     (dict(scale=-1.0), SHAPE, "scale"),
     (dict(scale=float("nan")), SHAPE, "scale"),
     (dict(scale=float("inf")), SHAPE, "scale"),
+    (dict(scale=1e38), SHAPE, "scale"),
     (dict(max_len=6401), SHAPE, "max_len"),
     (dict(max_len=-1), SHAPE, "max_len"),
     (dict(max_pages=1 << 20, max_len=(1 << 22) + 1), UNSUPPORTED, "max_len"),
