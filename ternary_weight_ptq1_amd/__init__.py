@@ -588,7 +588,8 @@ def ptq1_kv_cache(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, 
 
 def _elsewhere(device) -> bool:
     """The operands' device is not the current one (the call is then made under it)."""
-    return device.index is not None and device.index != torch.cuda.current_device()
+    index = device.index
+    return index is not None and index != torch._C._cuda_getDevice()
 
 
 def _launch_stream(device, stream):
@@ -616,6 +617,11 @@ def _plain(t, dtype, numel: int, device) -> bool:
 
 def _rows3(t: torch.Tensor, name: str, dtype, device) -> tuple[int, int, int, int]:
     """(rows, heads, head_dim, row stride) of a [rows, heads, head_dim] tensor whose rows may lie apart."""
+    if type(t) is torch.Tensor and t.is_cuda and t.dtype in dtype and t.device == device and t.dim() == 3:
+        rows, heads, d = t.shape
+        sr, sh, sd = t.stride()
+        if sd == 1 and sh == d and (sr >= heads * d or rows < 2):
+            return rows, heads, d, sr if rows > 1 else heads * d
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not _on_device(t):
@@ -644,6 +650,11 @@ def _kv(cache) -> KvCache:
 
 
 def _table(block_table, batch, device):
+    if type(block_table) is torch.Tensor and block_table.dtype is torch.int32 and block_table.is_cuda \
+            and block_table.device == device and block_table.dim() == 2 and block_table.is_contiguous():
+        rows, width = block_table.shape
+        if rows == batch:
+            return width
     _dev(block_table, "block_table", torch.int32, device=device)
     if block_table.dim() != 2 or block_table.shape[0] != batch:
         raise ValueError(f"block_table must be [{batch}, max_pages]")
@@ -696,7 +707,7 @@ def ptq1_kv_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, slot
     handle, other = _launch_stream(dv, stream)
     if q is not None:
         if out is None:
-            out = torch.empty((n, hq, d), dtype=q_dtype, device=dv)
+            out = torch.empty_like(q, dtype=q_dtype, memory_format=torch.contiguous_format)
             _tie(other, out)
         else:
             _dev(out, "out", q_dtype, numel=n * hq * d, device=dv)
@@ -729,7 +740,8 @@ def ptq1_kv_read(cache: KvCache, block_table: torch.Tensor, cu_seqlens: torch.Te
         raise ValueError(f"n_rows = {n_rows} is negative")
     handle, other = _launch_stream(dv, stream)
     if out is None:
-        k, v = torch.empty((2, n_rows, kv.n_kv_heads, kv.head_dim), dtype=dtype, device=dv).unbind(0)
+        h, d = kv.n_kv_heads, kv.head_dim
+        k, v = torch.empty_strided((2, n_rows, h, d), (n_rows * h * d, h * d, d, 1), dtype=dtype, device=dv).unbind(0)
         _tie(other, k)
     else:
         k, v = out
@@ -768,12 +780,12 @@ def ptq1_attn_decode(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor,
     wsb = lib().ptq1_attn_decode_workspace_bytes(batch, hq, kv.n_kv_heads, d, max_len)
     if ws is None:
         if wsb:
-            ws = torch.empty(wsb, dtype=torch.uint8, device=dv)
+            ws = torch.empty_strided((wsb,), (1,), dtype=torch.uint8, device=dv)
             _tie(other, ws)
     else:
         ws, wsb = _ws(wsb, dv, ws)
     if out is None:
-        out = torch.empty((batch, hq, d), dtype=q.dtype, device=dv)
+        out = torch.empty_like(q)
         _tie(other, out)
     else:
         _dev(out, "out", q.dtype, numel=q.numel(), device=dv)
@@ -819,12 +831,12 @@ def ptq1_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     wsb = lib().ptq1_attn_prompt_workspace_bytes(batch, nq, max_k, hq, hkv, d)
     if ws is None:
         if wsb:
-            ws = torch.empty(wsb, dtype=torch.uint8, device=dv)
+            ws = torch.empty_strided((wsb,), (1,), dtype=torch.uint8, device=dv)
             _tie(other, ws)
     else:
         ws, wsb = _ws(wsb, dv, ws)
     if out is None:
-        out = torch.empty((nq, hq, d), dtype=kind, device=dv)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         _tie(other, out)
     else:
         _dev(out, "out", kind, numel=nq * hq * d, device=dv)
