@@ -60,7 +60,7 @@ struct DecodeArgs {
     const int32_t *lens;
     int64_t batch, max_len;
     int32_t shares;  // workgroups that the GPU holds for one kv head (for 16 query heads of it)
-    int32_t cut;     // some sequence may have more than one step
+    int32_t cut;     // some sequence may be cut
     float scale;
     void *out;
     float *part_rows, *part_ml;
@@ -89,13 +89,12 @@ struct LaneLens {
         const int64_t lane = threadIdx.x & 63;
         first = lane < a.batch ? a.lens[lane] : 0;
     }
-    __device__ __forceinline__ int operator()(const DecodeArgs &a, int64_t i) const { return i < 64 ? first : a.lens[i]; }
     // the sum of f(length) over the sequences before `end`
     template <class F>
     __device__ __forceinline__ int sum(const DecodeArgs &a, int64_t end, F f) const
     {
         int v = 0;
-        for (int64_t i = threadIdx.x & 63; i < end; i += 64) v += f((*this)(a, i));
+        for (int64_t i = threadIdx.x & 63; i < end; i += 64) v += f(i < 64 ? first : a.lens[i]);
         return wave_total(v);
     }
 };
@@ -105,9 +104,13 @@ struct LaneLens {
 // unequal (64 sequences of 3 to 8190 tokens: 61 us with 512 tokens a piece,
 // 71 with 256, 75 with 2048; one of 131071 over int8: 64 us in one round of
 // 2048, 75 in two).
+__host__ __device__ __forceinline__ int64_t wanted_pieces(int64_t batch, int64_t shares)
+{
+    return batch * 2 <= shares ? shares : 2 * shares;
+}
 __device__ __forceinline__ int steps_per_piece(const DecodeArgs &a, int total)
 {
-    const int want = a.batch * 2 <= a.shares ? a.shares : 2 * a.shares;
+    const int want = static_cast<int>(wanted_pieces(a.batch, a.shares));
     return (total + want - 1) / want;
 }
 
@@ -207,23 +210,21 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
     asm volatile("" ::"s"(a.q), "s"(a.k_pages), "s"(a.v_pages), "s"(a.k_steps), "s"(a.v_steps), "s"(a.n_pages),
                  "s"(a.page_shift), "s"(a.table), "s"(a.max_pages), "s"(a.lens), "s"(a.batch), "s"(a.max_len),
                  "s"(a.shares), "s"(a.scale));
-    int per = 1, b = static_cast<int>(piece), first = 0, len;
+    int per = 1 << 14, b = static_cast<int>(piece), first = 0, len;
     if (a.cut) {
         const LaneLens lens(a);
         per = steps_per_piece(a, lens.sum(a, a.batch, [&](int n) { return decode_steps(a, n); }));
         int64_t seq, tile;
         int mine = 0;
-        if (!find_tile<false>(
-                piece, a.batch,
-                [&](int64_t i) {
-                    mine = lens(a, i);
-                    return (decode_steps(a, mine) + per - 1) / per;
-                },
-                seq, tile))
+        const auto pieces = [&](int n) { return (decode_steps(a, n) + per - 1) / per; };
+        const auto of_lane = [&](int64_t) { return pieces(mine = lens.first); };
+        const auto of_any = [&](int64_t i) { return pieces(a.lens[i]); };
+        if (!(a.batch <= 64 ? find_tile<false>(piece, a.batch, of_lane, seq, tile)
+                            : find_tile_in_runs(piece, a.batch, of_any, seq, tile)))
             return;
         b = __builtin_amdgcn_readfirstlane(static_cast<int>(seq));
         first = __builtin_amdgcn_readfirstlane(static_cast<int>(tile));
-        len = __builtin_amdgcn_readlane(mine, b & 63);
+        len = a.batch <= 64 ? __builtin_amdgcn_readlane(mine, b & 63) : a.lens[b];
     } else
         len = a.lens[b];
     const bool bad_len = len < 0 || len > a.max_len;
@@ -683,9 +684,12 @@ DecodePlan decode_plan(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_
     if (shares < 1) shares = 1;
     if (shares > kMaxShares) shares = kMaxShares;
     p.shares = static_cast<int32_t>(shares);
-    p.pieces = batch * 2 <= shares ? shares + batch : 2 * shares + batch;
-    if (p.pieces > each * batch) p.pieces = each * batch;
-    p.join = each > 1;
+    const int64_t want = wanted_pieces(batch, shares);
+    // every sequence has a step, so a piece has at least so many: large
+    // batches of short sequences are not cut (1024 of 512 tokens: 455 us with
+    // the search for their pieces and the join's launch, 364 without)
+    p.join = each > (batch + want - 1) / want;
+    p.pieces = p.join && want + batch < each * batch ? want + batch : p.join ? each * batch : batch;
     if (p.join) {
         p.rows_floats = static_cast<size_t>(p.pieces) * hq * d;
         p.part_floats = p.rows_floats + static_cast<size_t>(p.pieces) * hq * 2;

@@ -144,25 +144,41 @@ __device__ __forceinline__ bool prompt_tile(const PromptArgs &a, const PromptPla
         part = __builtin_amdgcn_readfirstlane(part);
         number -= part * (plan.tiles - plan.whole);
     }
-    int64_t b, at;
-    int qf = 0, qe = 0, kf = 0, ke = 0;  // the lane's sequence (all four at once: one trip to memory)
-    if (!find_tile<true>(
-            number, a.batch,
-            [&](int64_t i) {
-                qf = a.cu_q[i];
-                qe = a.cu_q[i + 1];
-                kf = a.cu_k[i];
-                ke = a.cu_k[i + 1];
-                // only rows that exist count
-                const int64_t first = qf, end = qe;
-                const int64_t n = (end < a.q_rows ? end : a.q_rows) - (first > 0 ? first : 0);
-                return n > 0 ? (n * t.group + R - 1) / R : 0;
-            },
-            b, at))
-        return false;
-    const int who = static_cast<int>(b & 63);
-    const int64_t q0 = __builtin_amdgcn_readlane(qf, who), lq = __builtin_amdgcn_readlane(qe, who) - q0;
-    const int64_t k0 = __builtin_amdgcn_readlane(kf, who), lk = __builtin_amdgcn_readlane(ke, who) - k0;
+    int64_t b, at, q0, k0, lq, lk;
+    if (a.batch <= 64) {
+        int qf = 0, qe = 0, kf = 0, ke = 0;  // the lane's sequence (all four at once: one trip to memory)
+        if (!find_tile<true>(
+                number, a.batch,
+                [&](int64_t i) {
+                    qf = a.cu_q[i];
+                    qe = a.cu_q[i + 1];
+                    kf = a.cu_k[i];
+                    ke = a.cu_k[i + 1];
+                    // only rows that exist count
+                    const int64_t first = qf, end = qe;
+                    const int64_t n = (end < a.q_rows ? end : a.q_rows) - (first > 0 ? first : 0);
+                    return n > 0 ? (n * t.group + R - 1) / R : 0;
+                },
+                b, at))
+            return false;
+        const int who = static_cast<int>(b);
+        q0 = __builtin_amdgcn_readlane(qf, who);
+        lq = __builtin_amdgcn_readlane(qe, who) - q0;
+        k0 = __builtin_amdgcn_readlane(kf, who);
+        lk = __builtin_amdgcn_readlane(ke, who) - k0;
+    } else {
+        // Large batches in the order they come, without counting through all
+        // sequences: 128 prompts of 512 tokens 592 us (801 counted, the longest
+        // first), 4096 of 16 tokens 640 us (18400).  9 prompts of 5 to 2500
+        // tokens: 92 to 95 us with the longest first, 94 to 100 as they come.
+        if (!find_rows<R>(number, a.cu_q, a.batch, a.q_rows, t.group, b, at)) return false;
+        b = __builtin_amdgcn_readfirstlane(static_cast<int>(b));
+        at = __builtin_amdgcn_readfirstlane(static_cast<int>(at));
+        q0 = a.cu_q[b];
+        lq = a.cu_q[b + 1] - q0;
+        k0 = a.cu_k[b];
+        lk = a.cu_k[b + 1] - k0;
+    }
     if (q0 < 0 || k0 < 0 || q0 + lq > a.q_rows || lk < 0 || k0 + lk > a.k_rows || lq > a.max_q || lk > a.max_k) {
         const int64_t r = (q0 < 0 ? -q0 * t.group : 0) + at * R + threadIdx.x, tok = q0 + r / t.group;
         if (!join && part == 0 && threadIdx.x < R && tok < q0 + lq && tok < a.q_rows) {

@@ -312,13 +312,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_read(KvReadArgs a)
     typedef C c8 __attribute__((ext_vector_type(8)));
     const int kh = static_cast<int>(blockIdx.x % static_cast<uint32_t>(a.hkv));
     int64_t b, at;
-    if (!find_tile<false>(blockIdx.x / static_cast<uint32_t>(a.hkv), a.batch,
-                          [&](int64_t i) {
-                              // the sequence's rows that exist, from its start
-                              const int64_t first = a.cu[i], end = a.cu[i + 1] < a.rows ? a.cu[i + 1] : a.rows;
-                              return first >= 0 && end > first ? (end - first + kReadTok - 1) / kReadTok : 0;
-                          },
-                          b, at))
+    if (!find_rows<kReadTok>(blockIdx.x / static_cast<uint32_t>(a.hkv), a.cu, a.batch, a.rows, 1, b, at) || a.cu[b] < 0)
         return;
     const int64_t first = a.cu[b], end = a.cu[b + 1] < a.rows ? a.cu[b + 1] : a.rows;
     const int64_t t0 = at * kReadTok, out0 = first + t0;

@@ -140,4 +140,53 @@ __device__ __forceinline__ bool find_tile(int64_t flat, int64_t batch, F tiles_o
     return false;
 }
 
+// find_tile<false> for large batches: a lane counts the tiles of a run of
+// sequences, and only the run that holds the tile is searched.
+template <class F>
+__device__ __forceinline__ bool find_tile_in_runs(int64_t flat, int64_t batch, F tiles_of, int64_t &seq, int64_t &tile)
+{
+    const int64_t run = (batch + 63) / 64, from = (threadIdx.x & 63) * run;
+    const int64_t to = from + run < batch ? from + run : batch;
+    int mine = 0;
+#pragma unroll 4
+    for (int64_t i = from; i < to; ++i) mine += static_cast<int>(tiles_of(i));
+    int64_t lane, rest;
+    if (!find_tile<false>(flat, 64, [&](int64_t) { return mine; }, lane, rest)) return false;
+    const int64_t first = __builtin_amdgcn_readfirstlane(static_cast<int>(lane)) * run;
+    const int64_t n = first + run < batch ? run : batch - first;
+    if (!find_tile<false>(rest, n, [&](int64_t i) { return tiles_of(first + i); }, seq, tile)) return false;
+    seq += first;
+    return true;
+}
+
+// The same for sequences that are consecutive rows cu[i] .. cu[i + 1] of
+// `rows` (what lies outside does not count), `group` of a tile's R each, in
+// any batch with one trip to memory for a factor of 64: sequence i's tiles
+// are numbered from (rows before it) / R + i on, which leaves room for all of
+// them and at most one number unused; the numbers end below rows * group / R
+// + batch.
+template <int R>
+__device__ __forceinline__ bool find_rows(int64_t flat, const int32_t *cu, int64_t batch, int64_t rows, int64_t group,
+                                          int64_t &seq, int64_t &tile)
+{
+    const auto row = [&](int64_t i) {
+        const int64_t r = cu[i];
+        return r < 0 ? 0 : r < rows ? r : rows;
+    };
+    int64_t lo = 0, n = batch;
+    for (;;) {
+        const int64_t step = (n + 63) / 64, at = (threadIdx.x & 63) * step;
+        const uint64_t below = __ballot(at < n && row(lo + at) * group / R + lo + at <= flat);
+        if (below == 0) return false;
+        const int64_t skip = (63 - __builtin_clzll(below)) * step;
+        lo += skip;
+        n = n - skip < step ? n - skip : step;
+        if (step == 1) break;
+    }
+    const int64_t first = row(lo), count = row(lo + 1) - first;
+    seq = lo;
+    tile = flat - (first * group / R + lo);
+    return tile * R < count * group;
+}
+
 }  // namespace ptq1

@@ -1048,3 +1048,44 @@ def test_attn_prompt_last_tiles_cut(dtype, causal, hq, hkv, d, lq, lk):
     first = sum(lq[:-1])
     assert bool(got[first:].isnan().all())
     check_prompt(q, k, v, lq[:-1], lk[:-1], got, causal)
+
+
+@pytest.mark.parametrize("batch", [65, 130, 1000, 5000])
+def test_many_sequences_of_unlike_lengths(batch):
+    """Large batches with a few long sequences: tiles and pieces of one sequence among those of many."""
+    g = gen(100 + batch)
+    rng = np.random.default_rng(batch)
+    lens = [int(n) for n in rng.integers(0, 9, batch)]
+    long = [0, batch // 3, 63, 64, batch - 1]
+    for b in long:
+        lens[b] = int(rng.integers(700, 3000))
+    table, pages = tables(g, lens, 16)
+    c = filled_cache(g, pages, 16, 2, 64, BF16)
+    cu = cumulated(lens, 5)  # five rows ahead of the first sequence
+    total = sum(lens) + 9
+    k, v = P.ptq1_kv_read(c, table, cu, total, dtype=BF16)
+    kc, vc = cache_values(c)
+    some = sorted(set(long + [1, 2, batch // 2, 62, batch - 2]))
+    q = randn(g, total, 4, 64).to(BF16)
+    o = P.ptq1_attn_prompt(q, k, v, cu, cu, max_q=3000, max_k=3000)
+    last = q[:batch].contiguous() if total >= batch else randn(g, batch, 4, 64).to(BF16)
+    got = P.ptq1_attn_decode(last, c, table, torch.tensor(lens, dtype=torch.int32, device=DEV))
+    for b in some:
+        a, z = int(cu[b]), int(cu[b + 1])
+        for have, val in ((k, kc), (v, vc)):
+            assert torch.equal(have[a:z].double(), sequence(c, val, table, b, lens[b]).transpose(0, 1))
+        check_prompt(q[a:z], k[a:z], v[a:z], [z - a], [z - a], o[a:z], True)
+        check_decode(last[b:b + 1], c, table[b:b + 1], [lens[b]], got[b:b + 1])
+    # every row of every sequence was written, with the same numbers as alone
+    assert bool(o[5:5 + sum(lens)].isfinite().all()) and bool(got.isfinite().all())
+    few = [i for i in range(batch) if lens[i] > 0][:40]
+    alone = P.ptq1_attn_decode(last[few].contiguous(), c, table[few].contiguous(),
+                               torch.tensor([lens[i] for i in few], dtype=torch.int32, device=DEV))
+    small = [j for j, i in enumerate(few) if lens[i] < 256]  # (one piece in either call)
+    assert torch.equal(alone[small], got[[few[j] for j in small]])
+    # a sequence out of bounds and one of a bad length leave the others as they were
+    bad = cu.clone()
+    bad[-1] += 100
+    o2 = P.ptq1_attn_prompt(q, k, v, cu, bad, max_q=3000, max_k=3100)
+    edge = int(cu[batch - 1])
+    assert torch.equal(o2[5:edge], o[5:edge]) and bool(o2[edge:5 + sum(lens)].isnan().all())
