@@ -120,7 +120,17 @@ struct PromptTile {
     int reach;              // keys that some row of the tile sees; of them, this workgroup's:
     int first, any, all;    // the first one, the one behind the last, and where the first comes that not every row sees
     bool split;             // there are several workgroups
+    int cut;                // its number among the tiles that may be cut, of all kv heads
 };
+
+// The place of a row's parts: by tile where only the last tiles are cut, else
+// by row and head (tiles of few rows would leave much of theirs unused).
+__device__ __forceinline__ int64_t part_row(const PromptArgs &a, const PromptPlan &plan, const PromptTile &t, int tok,
+                                            int head, int row)
+{
+    return plan.whole > 0 ? static_cast<int64_t>(t.cut) * kPrRows + (row - t.row0)
+                          : static_cast<int64_t>(t.q0 + tok) * a.hq + head;
+}
 
 // Workgroups go to the eight XCDs in turn, each with an L2 of its own: heads
 // vary fastest, so that a head's tiles meet on as few XCDs as its number
@@ -198,6 +208,7 @@ __device__ __forceinline__ bool prompt_tile(const PromptArgs &a, const PromptPla
     t.end = t.row0 + R < t.rows ? t.row0 + R : t.rows;
     t.reach = visible(a, (t.end - 1) / t.group, t.off, t.lk);
     t.split = number >= plan.whole && t.reach > plan.chunk;
+    t.cut = (number - plan.whole) * a.hkv + t.kh;
     t.first = part * plan.chunk;
     if (t.first >= t.reach && part > 0) return false;
     t.any = t.split && t.reach - t.first > plan.chunk ? t.first + plan.chunk : t.reach;
@@ -209,7 +220,7 @@ __device__ __forceinline__ bool prompt_tile(const PromptArgs &a, const PromptPla
 // One lane's query row (column lane % 32 of its tile of 32).
 struct PromptRow {
     bool is;
-    int tok, head;
+    int at, tok, head;
     int seen;  // keys that it sees
 };
 __device__ __forceinline__ PromptRow prompt_row(const PromptArgs &a, const PromptTile &t, int row)
@@ -217,6 +228,7 @@ __device__ __forceinline__ PromptRow prompt_row(const PromptArgs &a, const Promp
     PromptRow r;
     r.is = row < t.rows;
     const int at = r.is ? row : t.rows - 1;
+    r.at = at;
     r.tok = at / t.group;
     r.head = t.kh * t.group + at % t.group;
     r.seen = visible(a, r.tok, t.off, t.lk);
@@ -260,7 +272,7 @@ __device__ __forceinline__ void store_rows(const PromptArgs &a, const PromptPlan
                 store4(dst + 32 * i + 2 * j, at_f32x4{o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]});
         return;
     }
-    const int64_t slot = at * plan.splits + part;
+    const int64_t slot = part_row(a, plan, t, row.tok, row.head, row.at) * plan.splits + part;
     float *dst = parts + slot * d + d0 + 4 * half;
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -662,7 +674,8 @@ __global__ void __launch_bounds__(256) k_prompt_join(PromptArgs a, PromptPlan pl
     if (r >= t.end) return;
     const PromptRow row = prompt_row(a, t, r);
     const int64_t at = static_cast<int64_t>(t.q0 + row.tok) * a.hq + row.head;
-    const float *ml = part + plan.rows_floats + at * plan.splits * 2, *src = part + at * plan.splits * D + 4 * x;
+    const int64_t place = part_row(a, plan, t, row.tok, row.head, r) * plan.splits;
+    const float *ml = part + plan.rows_floats + place * 2, *src = part + place * D + 4 * x;
     float M = -__builtin_inff();
     for (int i = x; i < n; i += LPR) M = fmaxf(M, ml[2 * i]);
 #pragma unroll
@@ -708,6 +721,10 @@ int64_t prompt_tiles(int64_t batch, int64_t q_rows, int32_t hq, int32_t hkv)
     return q_rows * (hq / hkv) / kPrRows + batch;
 }
 
+// Bytes of parts above which nothing is cut: max_k may be a bound that no
+// sequence comes near.
+constexpr double kMaxParts = 1 << 28;
+
 PromptPlan prompt_plan(int64_t batch, int64_t q_rows, int64_t max_k, int32_t hq, int32_t hkv, int32_t d)
 {
     // The time with tiles cut in n along their keys, in us: rounds of
@@ -732,7 +749,9 @@ PromptPlan prompt_plan(int64_t batch, int64_t q_rows, int64_t max_k, int32_t hq,
         if (whole == 0 && best > 0.0) break;  // the same again
         const double rest = static_cast<double>((tiles - whole) * hkv);
         const double before = __builtin_ceil(static_cast<double>(whole * hkv) / slots) * static_cast<double>(max_k) * key;
+        const double rows = whole > 0 ? rest * kPrRows : static_cast<double>(q_rows) * hq;
         for (int i = whole > 0 ? 2 : 1; i <= 64 && max_k / i >= 256; ++i) {
+            if (i > 1 && rows * i * (d + 2) * 4 > kMaxParts) break;
             double us = before + __builtin_ceil(rest * i / slots) * static_cast<double>(max_k) / i * key;
             if (i > 1) us += 6.0 + rest * i * kPrRows * d * 4 * 2 / 2.5e6;
             if (i == 1 || us < best * 0.95) {
@@ -748,8 +767,9 @@ PromptPlan prompt_plan(int64_t batch, int64_t q_rows, int64_t max_k, int32_t hq,
     if (p.splits == 1) p.whole = 0;
     if (p.splits > 1) {
         p.per_cut = 1.0f / static_cast<float>(tiles - p.whole);
-        p.rows_floats = static_cast<size_t>(q_rows) * hq * p.splits * d;
-        p.part_floats = p.rows_floats + static_cast<size_t>(q_rows) * hq * p.splits * 2;
+        const size_t rows = p.whole > 0 ? static_cast<size_t>(tiles - p.whole) * hkv * kPrRows : static_cast<size_t>(q_rows) * hq;
+        p.rows_floats = rows * p.splits * d;
+        p.part_floats = p.rows_floats + rows * p.splits * 2;
     }
     return p;
 }

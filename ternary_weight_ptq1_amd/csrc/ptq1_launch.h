@@ -189,7 +189,8 @@ PromptPlan prompt_plan(int64_t batch, int64_t q_rows, int64_t max_k, int32_t hq,
 // tiles of 128 query rows that one kv head's rows may make up
 int64_t prompt_tiles(int64_t batch, int64_t q_rows, int32_t hq, int32_t hkv);
 // part: unused (splits == 1), or the chunks' unnormalised rows [row][head]
-// [splits][d], then their (maximum, sum) pairs.
+// [splits][d] (whole > 0: [tile that is cut][row of the tile][splits][d]), then
+// their (maximum, sum) pairs.
 hipError_t launch_attn_prompt(const PromptArgs &a, int dtype, int32_t d, const PromptPlan &plan, float *part,
                               hipStream_t s);
 

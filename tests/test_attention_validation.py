@@ -380,3 +380,13 @@ def test_binding_prompt(host_ok):
             P.ptq1_attn_prompt(*bad)
     with pytest.raises(ValueError, match="out has"):
         P.ptq1_attn_prompt(q, k, k, cu, cu, out=z(8, 8, 128))
+
+
+def test_prompt_workspace_stays_bounded():
+    """A loose bound on the keys must not ask for more than 256 MB."""
+    size = P.lib().ptq1_attn_prompt_workspace_bytes
+    for batch in (1, 3, 64, 500, 4096):
+        for rows in (1, 70, 1000, 20000, 300000):
+            for max_k in (300, 5000, 100000, 1 << 24):
+                for hq, hkv, d in ((8, 8, 64), (40, 8, 128), (64, 1, 256)):
+                    assert size(batch, rows, max_k, hq, hkv, d) <= (1 << 28) + 256
