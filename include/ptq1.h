@@ -477,7 +477,8 @@ ptq1_status ptq1_kv_read(const ptq1_kv_cache *cache, const int32_t *block_table,
  *              max_pages * page_size); the work is laid out for it.
  *   scale      positive, 2^126 at most.
  * The products run on the matrix cores.  Over 16-bit caches K and V enter
- * exactly, fp32 queries as three 16-bit terms and weights as two or three
+ * exactly, fp32 queries as three 16-bit terms (over bf16 down to 2^-133, over
+ * fp16 down to 2^-38 of the head's largest magnitude) and weights as two or three
  * (bf16 queries: two, 16 bits of a weight; fp16: down to 2^-38 of the row's
  * largest).  Over int8 caches the codes enter exactly; the queries are fixed-point
  * numbers, multiples of 2^-29 (fp32 queries) or 2^-21 of a power of two not

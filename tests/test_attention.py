@@ -1089,3 +1089,34 @@ def test_many_sequences_of_unlike_lengths(batch):
     o2 = P.ptq1_attn_prompt(q, k, v, cu, bad, max_q=3000, max_k=3100)
     edge = int(cu[batch - 1])
     assert torch.equal(o2[5:edge], o[5:edge]) and bool(o2[edge:5 + sum(lens)].isnan().all())
+
+
+# -------------------------------------------------- magnitudes at the limits ----
+
+@pytest.mark.parametrize("ctype", [F16, BF16, I8])
+@pytest.mark.parametrize("size,scale", [(1e-28, 1e28), (1e-30, 2e29), (2.0 ** -118, 2.0 ** 116), (2.0 ** -124, 2.0 ** 123),
+                                        (2.0 ** -131, 2.0 ** 126)])
+def test_attn_decode_tiny_queries(ctype, size, scale):
+    """fp32 queries near the smallest fp32 values, under a scale that makes ordinary scores of them: their fp16 terms
+    (int8: digits) follow the head's magnitude, bf16 terms go down to 2^-133 (half a step of that, times the keys and
+    the scale, is what a score may be off by then; twice, since the weights' sum has it too)."""
+    g = gen(111)
+    lens = [90, 33]
+    table, pages = tables(g, lens, 16)
+    c = filled_cache(g, pages, 16, 2, 64, ctype)
+    q = randn(g, 2, 6, 64) * size
+    got = P.ptq1_attn_decode(q, c, table, torch.tensor(lens, dtype=torch.int32, device=DEV), scale=scale)
+    if ctype != BF16:
+        check_decode(q, c, table, lens, got, scale)
+        return
+    kc, vc = cache_values(c)
+    for b, n in enumerate(lens):
+        k, v = sequence(c, kc, table, b, n), sequence(c, vc, table, b, n)
+        for h in range(2):
+            qq = q[b, 3 * h:3 * h + 3].double()
+            want, tol = attention_bounds(qq, k[h], v[h], scale, WEIGHT_TERM[(F32, BF16)])
+            p = torch.softmax(scale * (qq @ k[h].T.contiguous()), 1)
+            off = scale * 2.0 ** -134 * k[h].abs().sum(1).max()
+            tol = tol + 2 * off * (p @ v[h].abs()) + half_step(want.abs() + tol, F32)
+            err = (got[b, 3 * h:3 * h + 3].double() - want).abs()
+            assert bool((err <= tol).all()), f"b={b} h={h}: {(err / tol).max().item():.3f} of the bound"
