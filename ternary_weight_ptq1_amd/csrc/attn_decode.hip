@@ -316,7 +316,10 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
             mx = max(mx, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mx), 32, 64)));
             const int e = __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, mx)) - 1;
             shift = (I8 ? 8 * NQ - 3 : 14) - e;
-            c = mx < 0x7f800000u ? ldexpf(c, -shift) : __builtin_nanf("");  // a NaN or an infinity in the query
+            // finite, or it would make a NaN of a key of zeros: scores that are
+            // not zero are then past 2^79 either way
+            c = fminf(ldexpf(c, -shift), 3.4028235e38f);
+            if (mx >= 0x7f800000u) c = __builtin_nanf("");  // a NaN or an infinity in the query
         }
         // (bf16 terms have fp32's exponents and are taken as they are, down to
         // 2^-133: to look for heads near that and scale them took 0.13 us of the

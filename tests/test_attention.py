@@ -1120,3 +1120,16 @@ def test_attn_decode_tiny_queries(ctype, size, scale):
             tol = tol + 2 * off * (p @ v[h].abs()) + half_step(want.abs() + tol, F32)
             err = (got[b, 3 * h:3 * h + 3].double() - want).abs()
             assert bool((err <= tol).all()), f"b={b} h={h}: {(err / tol).max().item():.3f} of the bound"
+
+
+@pytest.mark.parametrize("ctype", [F16, BF16, I8])
+def test_attn_decode_large_queries_over_zero_keys(ctype):
+    """Keys of zero give scores of zero, and the mean of the values, whatever the query and the scale are."""
+    g = gen(112)
+    lens = [70, 5]
+    table, pages = tables(g, lens, 16)
+    c = filled_cache(g, pages, 16, 1, 64, ctype)
+    c.k_pages.zero_()
+    q = randn(g, 2, 4, 64) * 2.0 ** 110
+    got = P.ptq1_attn_decode(q, c, table, torch.tensor(lens, dtype=torch.int32, device=DEV), scale=2.0 ** 126)
+    check_decode(q, c, table, lens, got, 2.0 ** 126)
