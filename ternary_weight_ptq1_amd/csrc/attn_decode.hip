@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
     // ---- queries: B operand, column = head, k = 8 consecutive dimensions
     // (int8: dimension 64 p + 16 grp + 8 s of steps 2 p + s, the bytes a lane
     // loads at once; else 32 kk + 8 grp)
-    float c = a.scale * kLog2e;  // scores in units of log2
+    float c = a.scale * kLog2e, far = 1.0f;  // scores in units of log2
     x8 qf[I8 ? 1 : QK][NQ];  // (int8: the digits stay in LDS)
     auto make_queries = [&] {
         int shift = 0;  // the queries enter times 2^shift
@@ -316,9 +316,19 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
             mx = max(mx, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mx), 32, 64)));
             const int e = __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, mx)) - 1;
             shift = (I8 ? 8 * NQ - 3 : 14) - e;
-            // finite, or it would make a NaN of a key of zeros: scores that are
-            // not zero are then past 2^79 either way
-            c = fminf(ldexpf(c, -shift), 3.4028235e38f);
+            if constexpr (I8) {
+                // Products of digits and codes are whole numbers below 2^45.  c
+                // comes first and a step (below 2^122) second, so c keeps what
+                // makes the first factor neither overflow nor lose bits, and
+                // `far` the rest of a power of two beyond that (none for scales
+                // and queries of ordinary size).
+                const int all = __builtin_amdgcn_frexp_expf(c) - shift, here = min(max(all, -125), 80);
+                c = ldexpf(__builtin_amdgcn_frexp_mantf(c), here);
+                far = ldexpf(1.0f, min(max(all - here, -126), 127));
+            } else
+                // finite, or it would make a NaN of a key of zeros: scores that
+                // are not zero are then past 2^79 either way
+                c = fminf(ldexpf(c, -shift), 3.4028235e38f);
             if (mx >= 0x7f800000u) c = __builtin_nanf("");  // a NaN or an infinity in the query
         }
         // (bf16 terms have fp32's exponents and are taken as they are, down to
@@ -379,6 +389,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
         make_queries();
     // not __syncthreads: it would wait for the first K and V
     if constexpr (I8) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const bool any_far = I8 && __ballot(far != 1.0f) != 0;
     // fp16 weights as multiples of 2^-14 of themselves, sums too: small ones
     // (many tokens beside one that takes nearly all) would fall below fp16's
     // smallest step, 2^-24, otherwise
@@ -434,7 +445,11 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
         }
         if constexpr (I8) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) s[t] *= ks[t];
+            for (int t = 0; t < NT; ++t) s[t] = s[t] * c * ks[t];
+            if (any_far) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) s[t] *= far;
+            }
         }
         const int32_t kn = checked(kpage), vn = checked(vpage);
         if (next < end) {
@@ -449,7 +464,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                s[t][i] *= c;
+                if constexpr (!I8) s[t][i] *= c;
                 if (tail && base + RUN * grp + 4 * t + i >= end) s[t][i] = -__builtin_inff();
                 top = fmaxf(top, s[t][i]);
             }

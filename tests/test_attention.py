@@ -1133,3 +1133,27 @@ def test_attn_decode_large_queries_over_zero_keys(ctype):
     q = randn(g, 2, 4, 64) * 2.0 ** 110
     got = P.ptq1_attn_decode(q, c, table, torch.tensor(lens, dtype=torch.int32, device=DEV), scale=2.0 ** 126)
     check_decode(q, c, table, lens, got, 2.0 ** 126)
+
+
+@pytest.mark.parametrize("qt", [F32, BF16])
+@pytest.mark.parametrize("size,step,scale", [
+    (2.0 ** -90, 2.0 ** 90, 0.1),
+    (2.0 ** -121, 2.0 ** 121, 0.125),         # the largest steps
+    (2.0 ** -60, 2.0 ** 121, 2.0 ** -60),
+    (2.0 ** -20, 2.0 ** 121, 2.0 ** -100),
+    (2.0 ** 121, 2.0 ** -126, 1.0),           # the smallest steps that ptq1_kv_write makes
+    (2.0 ** 100, 2.0 ** -45, 2.0 ** -57),
+    (2.0 ** -115, 2.0 ** -2, 2.0 ** 116),
+])
+def test_attn_decode_large_and_small_steps(qt, size, step, scale):
+    """int8 keys of any step that a cache may hold, with queries and scales that make ordinary scores of them: no
+    product on the way may leave fp32's range."""
+    g = gen(110)
+    lens = [300, 70, 1]
+    table, pages = tables(g, lens, 32)
+    c = filled_cache(g, pages, 32, 2, 128, I8)
+    c.k_steps.mul_(50).clamp_(0.5, 1.0).mul_(step / 127)
+    c.k_pages[table[1, 1].item(), :, 3] = 0   # a key of zeros among them
+    q = (randn(g, 3, 8, 128) * size).to(qt)
+    got = P.ptq1_attn_decode(q, c, table, torch.tensor(lens, dtype=torch.int32, device=DEV), scale=scale)
+    check_decode(q, c, table, lens, got, scale)
