@@ -61,6 +61,7 @@ struct DecodeArgs {
     int64_t batch, max_len;
     int32_t shares;  // workgroups that the GPU holds for one kv head (for 16 query heads of it)
     int32_t cut;     // some sequence may be cut
+    int32_t lowered;  // the parts' rows are 2^sum_exponent of their sum of weights times lower (int8 caches)
     float scale;
     void *out;
     float *part_rows, *part_ml;
@@ -163,6 +164,9 @@ __device__ __forceinline__ f16x8 codes_to_f16(uint32_t a, uint32_t b)
     w[3] = __builtin_amdgcn_perm(0x64646464u, b, 0x04030402u);
     return __builtin_bit_cast(f16x8, w) - static_cast<_Float16>(1152.0f);
 }
+
+// The e of the power of two 2^e above a sum of weights (0 for 0, NaN and infinity).
+__device__ __forceinline__ int sum_exponent(float l) { return __builtin_amdgcn_frexp_expf(l); }
 
 // 2^e for e in [-126, 127]
 __device__ __forceinline__ float pow2(int e) { return __builtin_bit_cast(float, static_cast<uint32_t>(127 + e) << 23); }
@@ -559,8 +563,14 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
     }
     l = lane_pair_sum<32>(lane_pair_sum<16>(l));
     if constexpr (I8) {
+        // out of the units, and divided by a power of two next to the weights'
+        // sum: with the largest steps a sum may be past fp32's range when no
+        // mean is
+        const int down = wexp - 14 - sum_exponent(l);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) o[i] *= pow2(wexp - 14);
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = ldexpf(o[i][j], down);
     }
 
     // ---- join the four waves: rows in LDS [wave][head][D + 4]
@@ -583,17 +593,21 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
 #pragma unroll
         for (int w = 1; w < kDecWaves; ++w) M = fmaxf(M, wm[w][h]);
         const float Ms = M == -__builtin_inff() ? 0.0f : M;
-        float L = 0.0f;
-        at_f32x4 r = zero4;
+        // (int8: the rows are below the waves' sums by a power of two)
+        float L = 0.0f, f[kDecWaves];
 #pragma unroll
         for (int w = 0; w < kDecWaves; ++w) {
-            const float f = __builtin_amdgcn_exp2f(wm[w][h] - Ms);
-            L += f * wl[w][h];
-            r += f * *reinterpret_cast<const at_f32x4 *>(rows + (w * nh + h) * (D + 4) + e);
+            f[w] = __builtin_amdgcn_exp2f(wm[w][h] - Ms);
+            L += f[w] * wl[w][h];
         }
+        const float inv = whole ? 1.0f / L : I8 ? ldexpf(1.0f, -sum_exponent(L)) : 1.0f;
+        at_f32x4 r = zero4;
+#pragma unroll
+        for (int w = 0; w < kDecWaves; ++w)
+            r += (I8 ? ldexpf(f[w], sum_exponent(wl[w][h])) * inv : f[w] * inv) * *reinterpret_cast<const at_f32x4 *>(rows + (w * nh + h) * (D + 4) + e);
         if (whole) {
-            const float f = len == 0 ? 0.0f : 1.0f / L;
-            store4(static_cast<QT *>(a.out) + (static_cast<int64_t>(b) * a.hq + h0 + h) * D + e, r * f);
+            if (len == 0) r = zero4;
+            store4(static_cast<QT *>(a.out) + (static_cast<int64_t>(b) * a.hq + h0 + h) * D + e, r);
         } else {
             const int64_t slot = piece * a.hq + h0 + h;
             *reinterpret_cast<at_f32x4 *>(a.part_rows + slot * D + e) = r;
@@ -634,23 +648,24 @@ __global__ void __launch_bounds__(256) k_attn_join(DecodeArgs a)
     float L = 0.0f;
     for (int i = threadIdx.x; i < n; i += 256) {
         const float w = __builtin_amdgcn_exp2f(a.part_ml[slot(i) * 2] - M);
-        wgt[i] = w;
-        L += w * a.part_ml[slot(i) * 2 + 1];
+        const float l = w * a.part_ml[slot(i) * 2 + 1];
+        wgt[i] = a.lowered ? ldexpf(w, sum_exponent(a.part_ml[slot(i) * 2 + 1])) : w;
+        L += l;
     }
     L = wave_sum(L);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = L;
     __syncthreads();
-    L = (red[0] + red[1]) + (red[2] + red[3]);
+    const float inv = 1.0f / ((red[0] + red[1]) + (red[2] + red[3]));
     const int g = threadIdx.x / LPR, x = threadIdx.x % LPR;
     at_f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
-    for (int i = g; i < n; i += G) r += wgt[i] * *reinterpret_cast<const at_f32x4 *>(a.part_rows + slot(i) * D + 4 * x);
+    for (int i = g; i < n; i += G) r += wgt[i] * inv * *reinterpret_cast<const at_f32x4 *>(a.part_rows + slot(i) * D + 4 * x);
     sums[g][x] = r;
     __syncthreads();
     if (g == 0) {
 #pragma unroll
         for (int i = 1; i < G; ++i) r += sums[i][x];
-        store4(static_cast<QT *>(a.out) + (b * a.hq + h) * D + 4 * x, r * (1.0f / L));
+        store4(static_cast<QT *>(a.out) + (b * a.hq + h) * D + 4 * x, r);
     }
 }
 
@@ -716,7 +731,7 @@ hipError_t launch_attn_decode(const DecodePlan &p, const void *q, int q_type, in
     const int32_t group = hq / c.n_kv_heads;
     const DecodeArgs a{q, hq, c.n_kv_heads, (group + kDecHeads - 1) / kDecHeads, c.k_pages, c.v_pages, c.k_steps,
                        c.v_steps, c.n_pages, __builtin_ctz(static_cast<unsigned>(c.page_size)), table, max_pages, lens,
-                       batch, max_len, p.shares, p.join, scale, out, part, part + p.rows_floats};
+                       batch, max_len, p.shares, p.join, c.dtype == PTQ1_I8, scale, out, part, part + p.rows_floats};
     const int d = c.head_dim;
     if (c.dtype == PTQ1_BF16)
         return q_type == PTQ1_F32 ? decode_d<__bf16, float, 3, 3>(p, a, batch, d, s)

@@ -154,8 +154,9 @@ hipError_t launch_kv_read(const ptq1_kv_cache &c, const int32_t *table, int64_t 
 // Decode attention: the kernel cuts every sequence into pieces of equally
 // many steps of 256 tokens, so many that all sequences' pieces fill the GPU
 // (`shares` workgroups for one kv head); `pieces` bounds their number.  part:
-// the pieces' unnormalised rows [piece][hq][d], then their (maximum, sum)
-// pairs; unused without join (no sequence can be cut).
+// the pieces' unnormalised rows [piece][hq][d] (int8 caches: lower by a power
+// of two), then their (maximum, sum) pairs; unused without join (no sequence
+// can be cut).
 struct DecodePlan {
     int32_t shares = 1;
     int64_t pieces = 1;

@@ -1157,3 +1157,19 @@ def test_attn_decode_large_and_small_steps(qt, size, step, scale):
     q = (randn(g, 3, 8, 128) * size).to(qt)
     got = P.ptq1_attn_decode(q, c, table, torch.tensor(lens, dtype=torch.int32, device=DEV), scale=scale)
     check_decode(q, c, table, lens, got, scale)
+
+
+@pytest.mark.parametrize("qt", [F32, BF16])
+@pytest.mark.parametrize("step", [2.0 ** 121, 2.0 ** 60, 2.0 ** -60, 2.0 ** -110])
+def test_attn_decode_large_and_small_value_steps(qt, step):
+    """int8 values of any step, ordinary keys; one token's step is 2^10 times smaller than the others'."""
+    g = gen(113)
+    lens = [300, 70]
+    table, pages = tables(g, lens, 32)
+    c = filled_cache(g, pages, 32, 2, 128, I8)
+    c.v_pages.copy_((c.v_pages.float() / 2).round())   # (the largest step's results stay below 2^128)
+    c.v_steps.mul_(50).clamp_(0.5, 1.0).mul_(step)
+    c.v_steps[table[0, 2].item(), :, 5] *= 2.0 ** -10
+    q = randn(g, 2, 8, 128).to(qt)
+    got = P.ptq1_attn_decode(q, c, table, torch.tensor(lens, dtype=torch.int32, device=DEV))
+    check_decode(q, c, table, lens, got)
