@@ -396,8 +396,10 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
     const bool any_far = I8 && __ballot(far != 1.0f) != 0;
     // fp16 weights as multiples of 2^-14 of themselves, sums too: small ones
     // (many tokens beside one that takes nearly all) would fall below fp16's
-    // smallest step, 2^-24, otherwise
-    constexpr float kLift = std::is_same<C, _Float16>::value ? 14.0f : 0.0f;
+    // smallest step, 2^-24, otherwise.  bf16 weights, which have fp32's
+    // exponents, 2^-22 times themselves: the sum over the 2^22 tokens that a
+    // sequence may have is then in fp32's range whenever the values are.
+    constexpr float kLift = std::is_same<C, _Float16>::value ? 14.0f : I8 ? 0.0f : -22.0f;
     const at_f32x4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
     at_f32x4 o[D / 16];
 #pragma unroll

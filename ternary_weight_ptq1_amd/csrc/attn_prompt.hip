@@ -45,9 +45,11 @@ constexpr int kKeys = 64;  // keys of a tile
 // fp16 weights are 2^7 times themselves (at most 2^15 with the maximum's lag,
 // below), and the sums with them: fp16's smallest step, 2^-24, is then 2^-31
 // of the largest weight at most, so that many small weights beside one large
-// one do not vanish.
+// one do not vanish.  bf16 weights, which have fp32's exponents, are 2^-40
+// times themselves: the sum over 2^31 keys is then in fp32's range whenever the
+// values are.
 template <typename T>
-constexpr float kWeightLift = std::is_same<T, _Float16>::value ? 7.0f : 0.0f;
+constexpr float kWeightLift = std::is_same<T, _Float16>::value ? 7.0f : -40.0f;
 
 // Query rows of a workgroup: 32 a wave, or a pair of waves (256-wide heads).
 constexpr int kPrRows = 128;

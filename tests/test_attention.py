@@ -1173,3 +1173,33 @@ def test_attn_decode_large_and_small_value_steps(qt, step):
     q = randn(g, 2, 8, 128).to(qt)
     got = P.ptq1_attn_decode(q, c, table, torch.tensor(lens, dtype=torch.int32, device=DEV))
     check_decode(q, c, table, lens, got)
+
+
+# ------------------------------------------------------ values near fp32's end ----
+
+def largest_values(g, *shape):
+    """bf16 values up to 2^127.98, all of them large: sums of a few are past fp32's range."""
+    return ((0.9 + 0.09 * torch.rand(shape, generator=g, device=DEV)) * 3.4e38).to(BF16)
+
+
+@pytest.mark.parametrize("qt", [F32, BF16])
+@pytest.mark.parametrize("lens", [[300, 5], [9000, 700]])
+def test_attn_decode_largest_values(qt, lens):
+    """bf16 values whose mean is in fp32's range and whose sum is not."""
+    g = gen(120)
+    table, pages = tables(g, lens, 32)
+    c = filled_cache(g, pages, 32, 2, 128, BF16)
+    c.v_pages.copy_(largest_values(g, *c.v_pages.shape))
+    q = randn(g, 2, 8, 128).to(qt)
+    got = P.ptq1_attn_decode(q, c, table, torch.tensor(lens, dtype=torch.int32, device=DEV))
+    check_decode(q, c, table, lens, got)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lq,lk", [([300], [300]), ([3, 2], [9000, 700])])
+def test_attn_prompt_largest_values(d, lq, lk):
+    g = gen(121)
+    q, k, _ = prompt_state(g, lq, lk, 4, 2, d)
+    v = largest_values(g, *k.shape)
+    got = P.ptq1_attn_prompt(q, k, v, cumulated(lq), cumulated(lk), max_q=max(lq), max_k=max(lk))
+    check_prompt(q, k, v, lq, lk, got, True)
