@@ -490,8 +490,8 @@ ptq1_status ptq1_kv_read(const ptq1_kv_cache *cache, const int32_t *block_table,
  * second launch, in a fixed order.
  * Errors: NULL, SHAPE (n_q_heads not a multiple of n_kv_heads, max_len, scale),
  * ALIGN, ALIAS, OVERFLOW, WORKSPACE, UNSUPPORTED (types, head_dim, page_size,
- * batch > 65535, more than 65535 groups of 16 query heads per sequence,
- * max_len > 2^22). */
+ * batch > 65535, more than 2^24 - 2^14 groups of 16 query heads of a kv head in
+ * all sequences together, max_len > 2^22). */
 size_t ptq1_attn_decode_workspace_bytes(int64_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                                         int64_t max_len);
 ptq1_status ptq1_attn_decode(const void *q, int32_t q_dtype, int64_t batch, int32_t n_q_heads,

@@ -1089,6 +1089,10 @@ constexpr int32_t kMaxHeads = 65536;
 constexpr int64_t kMaxWriteRows = int64_t{1} << 25;      // four rows of 256 elements a workgroup
 constexpr int64_t kMaxStride = int64_t{1} << 24;         // 64 rows of K or V within 32-bit offsets
 constexpr int64_t kMaxBlocks256 = (int64_t{1} << 24) - 1;  // a grid's threads fit 32 bits
+// Decode attention: a workgroup for each group of query heads of a sequence,
+// and where sequences are cut at most 2 * max(512, groups of one sequence)
+// more (decode_plan), of which there are 5120 at most.
+constexpr int64_t kMaxDecodeGroups = (int64_t{1} << 24) - (int64_t{1} << 14);
 
 // The byte sizes of a cache's arrays, after every check of it.
 struct KvBytes {
@@ -1177,7 +1181,7 @@ bool decode_sizes_ok(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_t 
 {
     return batch >= 0 && batch <= kMaxGridY && hkv >= 1 && hkv <= 1024 && hq >= 1 && hq <= kMaxHeads && hq % hkv == 0 &&
            (d == 64 || d == 128 || d == 256) && max_len >= 0 && max_len <= kMaxDecodeLen &&
-           static_cast<int64_t>(hkv) * ((hq / hkv + 15) / 16) <= kMaxGridY;
+           batch * hkv * ((hq / hkv + 15) / 16) <= kMaxDecodeGroups;
 }
 
 }  // namespace
@@ -1301,7 +1305,7 @@ ptq1_status ptq1_attn_decode(const void *q, int32_t q_dtype, int64_t batch, int3
     if (max_len > kMaxDecodeLen)
         return fail(PTQ1_ERR_UNSUPPORTED, "max_len = %lld > %lld", (long long)max_len, (long long)kMaxDecodeLen);
     if (!decode_sizes_ok(batch, n_q_heads, cache->n_kv_heads, cache->head_dim, max_len))
-        return fail(PTQ1_ERR_UNSUPPORTED, "more than %lld groups of 16 query heads", (long long)kMaxGridY);
+        return fail(PTQ1_ERR_UNSUPPORTED, "more than %lld groups of 16 query heads of a kv head", (long long)kMaxDecodeGroups);
     if (batch == 0) return ok();
     const int64_t qb = batch * n_q_heads * cache->head_dim * type_bytes(q_dtype);
     PTQ1_TRY(check_device_array(q, "q", qb, kAlign));

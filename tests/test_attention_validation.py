@@ -194,6 +194,24 @@ def test_decode_types_over_each_cache():
     assert decode(batch=0)[0] == 0
 
 
+def test_decode_grid_limit():
+    """Every launch that is accepted has fewer than 2^24 workgroups of 256 threads (a grid's threads fit 32 bits)."""
+    size = P.lib().ptq1_attn_decode_workspace_bytes
+    # (out = q: what passes the sizes' checks is refused before a launch)
+    for heads, hq, d, batch in ((1024, 1024, 64, 16384), (1, 65536, 64, 4096), (1000, 64000, 128, 65535), (257, 257, 64, 65281)):
+        rc, msg = decode(cache(heads=heads, d=d), hq=hq, batch=batch, out=at(0))
+        assert rc == UNSUPPORTED and "groups of 16 query heads" in msg, msg
+        assert size(batch, hq, heads, d, 6400) == 0
+    for heads, hq, d, batch in ((1024, 1024, 64, 16368), (1, 65536, 64, 4092), (256, 256, 64, 65472)):
+        rc, msg = decode(cache(heads=heads, d=d), hq=hq, batch=batch, out=at(0))
+        assert rc == ALIAS, msg
+    # what a refused size would be launched with is what the limit is for: pieces of the plan, as the workspace tells
+    for heads, hq, d, batch in ((1024, 1024, 64, 1), (5, 65535, 64, 3), (1, 16, 128, 60000), (1024, 65536, 256, 100)):
+        groups = heads * -(-(hq // heads) // 16)
+        pieces = size(batch, hq, heads, d, 1 << 22) // (hq * (d + 2) * 4)
+        assert pieces * groups <= batch * groups + (1 << 14)
+
+
 def test_decode_workspace():
     size = P.lib().ptq1_attn_decode_workspace_bytes
     assert size(1, 8, 2, 128, 256) == 0          # one step: nothing to join
