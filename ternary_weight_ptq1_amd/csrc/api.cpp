@@ -19,6 +19,7 @@
 #include "../../include/ptq1.h"
 #include "ptq1_geometry.h"
 #include "ptq1_launch.h"
+#include "ptq1_split.h"
 
 static_assert(PTQ1_BLOCK_WEIGHTS == ptq1::kBlockWeights, "public header and geometry agree");
 static_assert(PTQ1_TRIT_BYTES == ptq1::kTritBytes, "public header and geometry agree");
@@ -74,8 +75,8 @@ constexpr int64_t kMaxGridY = 65535;
 // Decode calls: rows per matrix (keeps the matvec grid's second dimension,
 // chunks of 32-row groups, far below its limit).
 constexpr int64_t kMaxLutRows = int64_t{1} << 20;
-// Decode attention: tokens of one sequence (the steps of all fit 30 bits).
-constexpr int64_t kMaxDecodeLen = int64_t{1} << 22;
+// Decode attention: tokens of one sequence.
+constexpr int64_t kMaxDecodeLen = int64_t{ptq1::kMaxSteps} * ptq1::kStep;
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 

@@ -38,6 +38,7 @@
 
 #include "ptq1_attn.h"
 #include "ptq1_launch.h"
+#include "ptq1_split.h"
 
 namespace ptq1 {
 namespace {
@@ -45,7 +46,6 @@ namespace {
 constexpr int kDecWaves = 4;
 constexpr int kDecThreads = 64 * kDecWaves;
 constexpr int kDecHeads = 16;       // query heads per workgroup (MFMA columns)
-constexpr int kStep = 256;          // tokens of one step of the work split (one page or several)
 constexpr int kMaxShares = 512;     // a sequence's pieces are twice that at most (the join's LDS)
 
 struct DecodeArgs {
@@ -66,13 +66,6 @@ struct DecodeArgs {
     void *out;
     float *part_rows, *part_ml;
 };
-
-// Steps of a sequence: one at least (an empty or refused one has its rows
-// written too).  All sequences' together are below 2^30 (2^16 times 2^14).
-__device__ __forceinline__ int decode_steps(const DecodeArgs &a, int len)
-{
-    return len <= 0 || len > a.max_len ? 1 : (len + kStep - 1) / kStep;
-}
 
 __device__ __forceinline__ int wave_total(int v)
 {
@@ -100,19 +93,11 @@ struct LaneLens {
     }
 };
 
-// Steps of one workgroup's piece of a sequence.  Few sequences: pieces that
-// fill the GPU once.  Many: half of that, since their ends leave the pieces
-// unequal (64 sequences of 3 to 8190 tokens: 61 us with 512 tokens a piece,
-// 71 with 256, 75 with 2048; one of 131071 over int8: 64 us in one round of
-// 2048, 75 in two).
-__host__ __device__ __forceinline__ int64_t wanted_pieces(int64_t batch, int64_t shares)
+// Steps of one workgroup's piece of a sequence.
+__device__ __forceinline__ int piece_steps(const DecodeArgs &a, const LaneLens &lens)
 {
-    return batch * 2 <= shares ? shares : 2 * shares;
-}
-__device__ __forceinline__ int steps_per_piece(const DecodeArgs &a, int total)
-{
-    const int want = static_cast<int>(wanted_pieces(a.batch, a.shares));
-    return (total + want - 1) / want;
+    const int total = lens.sum(a, a.batch, [&](int n) { return decode_steps(n, a.max_len); });
+    return steps_per_piece(total, wanted_pieces(a.batch, a.shares));
 }
 
 // MFMA operand type of a cache type
@@ -214,13 +199,13 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
     asm volatile("" ::"s"(a.q), "s"(a.k_pages), "s"(a.v_pages), "s"(a.k_steps), "s"(a.v_steps), "s"(a.n_pages),
                  "s"(a.page_shift), "s"(a.table), "s"(a.max_pages), "s"(a.lens), "s"(a.batch), "s"(a.max_len),
                  "s"(a.shares), "s"(a.scale));
-    int per = 1 << 14, b = static_cast<int>(piece), first = 0, len;
+    int per = kMaxSteps, b = static_cast<int>(piece), first = 0, len;
     if (a.cut) {
         const LaneLens lens(a);
-        per = steps_per_piece(a, lens.sum(a, a.batch, [&](int n) { return decode_steps(a, n); }));
+        per = piece_steps(a, lens);
         int64_t seq, tile;
         int mine = 0;
-        const auto pieces = [&](int n) { return (decode_steps(a, n) + per - 1) / per; };
+        const auto pieces = [&](int n) { return pieces_of(decode_steps(n, a.max_len), per); };
         const auto of_lane = [&](int64_t) { return pieces(mine = lens.first); };
         const auto of_any = [&](int64_t i) { return pieces(a.lens[i]); };
         if (!(a.batch <= 64 ? find_tile<false>(piece, a.batch, of_lane, seq, tile)
@@ -232,9 +217,9 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
     } else
         len = a.lens[b];
     const bool bad_len = len < 0 || len > a.max_len;
-    const bool whole = decode_steps(a, len) <= per;
-    const int begin = first * per * kStep;
-    const int end = bad_len ? begin : (begin + per * kStep < len ? begin + per * kStep : len);
+    const bool whole = decode_steps(len, a.max_len) <= per;
+    const PieceTokens tokens = piece_tokens(first, per, len);
+    const int begin = tokens.begin, end = bad_len ? begin : tokens.end;
 
     // ---- the queries' own loads, first of all: of column = head, dimensions
     // 32 kk + 8 grp .. (int8: for the magnitude; and of wave kk operand kk's
@@ -633,8 +618,8 @@ __global__ void __launch_bounds__(256) k_attn_join(DecodeArgs a)
     __shared__ at_f32x4 sums[G][LPR];
     const int64_t b = blockIdx.y, h = blockIdx.x;
     const LaneLens lens(a);
-    const int per = steps_per_piece(a, lens.sum(a, a.batch, [&](int n) { return decode_steps(a, n); }));
-    const auto pieces = [&](int len) { return (decode_steps(a, len) + per - 1) / per; };
+    const int per = piece_steps(a, lens);
+    const auto pieces = [&](int len) { return pieces_of(decode_steps(len, a.max_len), per); };
     const int n = pieces(b < 64 ? __builtin_amdgcn_readlane(lens.first, static_cast<int>(b)) : a.lens[b]);
     if (n == 1) return;
     const int64_t before = lens.sum(a, b, pieces);

@@ -1,6 +1,8 @@
 """Host-only checks of the cache and attention calls: sizes, refusals of the C entry points before anything is
 enqueued (fake device addresses, never dereferenced), and of the binding before the C call."""
 import ctypes as C
+import os
+import subprocess
 
 import pytest
 import torch
@@ -408,3 +410,51 @@ def test_prompt_workspace_stays_bounded():
             for max_k in (300, 5000, 100000, 1 << 24):
                 for hq, hkv, d in ((8, 8, 64), (40, 8, 128), (64, 1, 256)):
                     assert size(batch, rows, max_k, hq, hkv, d) <= (1 << 28) + 256
+
+
+def test_decode_pieces_cover_every_sequence(tmp_path):
+    """The split's arithmetic as the kernels have it, at its limits (up to 65535 sequences of 2^22 tokens, two pieces
+    wanted, where steps times tokens of a piece would pass 32 bits): the pieces are as many as the host has room for,
+    and lie end to end."""
+    source = tmp_path / "split.cpp"
+    source.write_text(r"""
+#include <cstdio>
+#include "ptq1_split.h"
+int main()
+{
+    const int64_t batches[] = {1, 2, 3, 64, 257, 1024, 16384, 65535}, shares[] = {1, 2, 13, 64, 512};
+    const int lens[] = {-1, 0, 1, 255, 256, 257, 5000, 131071, (1 << 22) - 1, 1 << 22, (1 << 22) + 1};
+    const int64_t max_len = 1 << 22;
+    for (int64_t batch : batches)
+        for (int64_t share : shares)
+            for (int most : lens) {      // every sequence but two has this length
+                int64_t total = 0;
+                for (int64_t i = 0; i < batch; ++i) total += ptq1::decode_steps(i < 2 ? lens[3 + i] : most, max_len);
+                const int64_t want = ptq1::wanted_pieces(batch, share);
+                const int per = ptq1::steps_per_piece(static_cast<int>(total), want);
+                if (per < 1 || per > ptq1::kMaxSteps) return 1;
+                int64_t pieces = 0;
+                for (int64_t i = 0; i < batch; ++i) {
+                    const int len = i < 2 ? lens[3 + i] : most, steps = ptq1::decode_steps(len, max_len);
+                    const int n = ptq1::pieces_of(steps, per);
+                    pieces += n;
+                    int at = 0;
+                    for (int k = 0; k < n; ++k) {
+                        const ptq1::PieceTokens p = ptq1::piece_tokens(k, per, len);
+                        if (p.begin != at) return 2;
+                        at = p.end;
+                        if (len >= 1 && len <= max_len && p.end <= p.begin) return 3;
+                    }
+                    if (len >= 0 && len <= max_len && at != len) return 4;
+                }
+                if (pieces > want + batch) return 5;
+            }
+    std::puts("covered");
+    return 0;
+}
+""")
+    program = tmp_path / "split"
+    csrc = os.path.join(os.path.dirname(P.__file__), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fwrapv", "-I", csrc, str(source), "-o", str(program)], check=True)
+    done = subprocess.run([str(program)], capture_output=True, text=True)
+    assert done.returncode == 0 and done.stdout == "covered\n", done.returncode
