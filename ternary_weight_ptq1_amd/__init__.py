@@ -592,21 +592,31 @@ def _elsewhere(device) -> bool:
     return index is not None and index != torch._C._cuda_getDevice()
 
 
-def _launch_stream(device, stream):
-    """(handle, stream): the stream to launch on, and the stream itself if it is not the allocator's current one, so
-    that memory allocated for the call can be tied to it (_tie)."""
+def _beside(device, stream) -> bool:
+    """A stream is given that is not the operands' device's current one (the call is then made under it, _under)."""
     if stream is None:
-        if device.index is None:
-            return None, None
-        return torch._C._cuda_getCurrentRawStream(device.index), None
-    return stream.cuda_stream, stream if stream != torch.cuda.current_stream(device) else None
+        return False
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the call runs on {device}")
+    return stream != torch.cuda.current_stream(device)
 
 
-def _tie(stream, *tensors):
-    if stream is not None:
-        for t in tensors:
+def _under(stream, device, fresh: bool, call, *args):
+    """call(*args) with `stream` as the current one, so that what it allocates comes from that stream's memory: a block
+    that the caller's stream has freed may still have work of that stream pending on it.  fresh: the results are new
+    tensors, whose memory may go back to that stream only behind what the caller's does with them."""
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        result = call(*args)
+    if fresh:
+        for t in result if isinstance(result, tuple) else (result,):
             if t is not None:
-                t.record_stream(stream)
+                t.record_stream(here)
+    return result
+
+
+def _current_handle(device):
+    return None if device.index is None else torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _plain(t, dtype, numel: int, device) -> bool:
@@ -674,6 +684,8 @@ def ptq1_kv_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, slot
     if _elsewhere(dv):
         with torch.cuda.device(dv):
             return ptq1_kv_write(q, k, v, slots, cache, positions, cos_sin, q_dtype, out, stream)
+    if _beside(dv, stream):
+        return _under(stream, dv, out is None, ptq1_kv_write, q, k, v, slots, cache, positions, cos_sin, q_dtype, out)
     n, h, d, ks = _rows3(k, "k", _FLOATS, dv)
     if h != kv.n_kv_heads or d != kv.head_dim:
         raise ValueError(f"k has {h} heads of {d}, the cache {kv.n_kv_heads} of {kv.head_dim}")
@@ -704,11 +716,10 @@ def ptq1_kv_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, slot
             raise ValueError("cos_sin needs positions")
     if positions is not None and not _plain(positions, torch.int32, n, dv):
         _dev(positions, "positions", torch.int32, numel=n, device=dv)
-    handle, other = _launch_stream(dv, stream)
+    handle = _current_handle(dv)
     if q is not None:
         if out is None:
             out = torch.empty_like(q, dtype=q_dtype, memory_format=torch.contiguous_format)
-            _tie(other, out)
         else:
             _dev(out, "out", q_dtype, numel=n * hq * d, device=dv)
     status = lib().ptq1_kv_write(0 if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPES[src],
@@ -729,6 +740,8 @@ def ptq1_kv_read(cache: KvCache, block_table: torch.Tensor, cu_seqlens: torch.Te
     if _elsewhere(dv):
         with torch.cuda.device(dv):
             return ptq1_kv_read(cache, block_table, cu_seqlens, n_rows, dtype, out, stream)
+    if _beside(dv, stream):
+        return _under(stream, dv, out is None, ptq1_kv_read, cache, block_table, cu_seqlens, n_rows, dtype, out)
     _dev(cu_seqlens, "cu_seqlens", torch.int32, device=dv)
     batch = cu_seqlens.numel() - 1
     if batch < 0:
@@ -738,11 +751,10 @@ def ptq1_kv_read(cache: KvCache, block_table: torch.Tensor, cu_seqlens: torch.Te
         raise ValueError(f"dtype must be one of {_FLOATS}, got {dtype}")
     if n_rows < 0:
         raise ValueError(f"n_rows = {n_rows} is negative")
-    handle, other = _launch_stream(dv, stream)
+    handle = _current_handle(dv)
     if out is None:
         h, d = kv.n_kv_heads, kv.head_dim
         k, v = torch.empty_strided((2, n_rows, h, d), (n_rows * h * d, h * d, d, 1), dtype=dtype, device=dv).unbind(0)
-        _tie(other, k)
     else:
         k, v = out
         count = n_rows * kv.n_kv_heads * kv.head_dim
@@ -767,6 +779,8 @@ def ptq1_attn_decode(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor,
     if _elsewhere(dv):
         with torch.cuda.device(dv):
             return ptq1_attn_decode(q, cache, block_table, seq_lens, scale, max_len, out, ws, stream)
+    if _beside(dv, stream):
+        return _under(stream, dv, out is None, ptq1_attn_decode, q, cache, block_table, seq_lens, scale, max_len, out, ws)
     _dev(q, "q", _FLOATS, device=dv)
     if q.dim() != 3 or q.shape[2] != kv.head_dim:
         raise ValueError(f"q must be [batch, n_q_heads, {kv.head_dim}]")
@@ -776,17 +790,15 @@ def ptq1_attn_decode(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor,
         _dev(seq_lens, "seq_lens", torch.int32, numel=batch, device=dv)
     if max_len is None:
         max_len = max_pages * kv.page_size
-    handle, other = _launch_stream(dv, stream)
+    handle = _current_handle(dv)
     wsb = lib().ptq1_attn_decode_workspace_bytes(batch, hq, kv.n_kv_heads, d, max_len)
     if ws is None:
         if wsb:
             ws = torch.empty_strided((wsb,), (1,), dtype=torch.uint8, device=dv)
-            _tie(other, ws)
     else:
         ws, wsb = _ws(wsb, dv, ws)
     if out is None:
         out = torch.empty_like(q)
-        _tie(other, out)
     else:
         _dev(out, "out", q.dtype, numel=q.numel(), device=dv)
     status = lib().ptq1_attn_decode(q.data_ptr(), _DTYPES[q.dtype], batch, hq, kv._ref, block_table.data_ptr(), max_pages,
@@ -813,6 +825,8 @@ def ptq1_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     if _elsewhere(dv):
         with torch.cuda.device(dv):
             return ptq1_attn_prompt(q, k, v, cu_q, cu_k, max_q, max_k, causal, scale, out, ws, stream)
+    if _beside(dv, stream):
+        return _under(stream, dv, out is None, ptq1_attn_prompt, q, k, v, cu_q, cu_k, max_q, max_k, causal, scale, out, ws)
     nq, hq, d, qs = _rows3(q, "q", _SIXTEEN, dv)
     kind = q.dtype
     nk, hkv, dk, ks = _rows3(k, "k", (kind,), dv)
@@ -827,17 +841,15 @@ def ptq1_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
         _dev(cu_k, "cu_k", torch.int32, numel=batch + 1, device=dv)
     max_q = nq if max_q is None else min(max_q, nq)
     max_k = nk if max_k is None else min(max_k, nk)
-    handle, other = _launch_stream(dv, stream)
+    handle = _current_handle(dv)
     wsb = lib().ptq1_attn_prompt_workspace_bytes(batch, nq, max_k, hq, hkv, d)
     if ws is None:
         if wsb:
             ws = torch.empty_strided((wsb,), (1,), dtype=torch.uint8, device=dv)
-            _tie(other, ws)
     else:
         ws, wsb = _ws(wsb, dv, ws)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        _tie(other, out)
     else:
         _dev(out, "out", kind, numel=nq * hq * d, device=dv)
     status = lib().ptq1_attn_prompt(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPES[kind], cu_q.data_ptr(),

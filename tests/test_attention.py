@@ -1203,3 +1203,82 @@ def test_attn_prompt_largest_values(d, lq, lk):
     v = largest_values(g, *k.shape)
     got = P.ptq1_attn_prompt(q, k, v, cumulated(lq), cumulated(lk), max_q=max(lq), max_k=max(lk))
     check_prompt(q, k, v, lq, lk, got, True)
+
+
+# ------------------------------------------------------------ memory of two streams ----
+
+def busy(x):
+    """Some milliseconds of ordinary work on the current stream."""
+    for _ in range(20):
+        x = torch.mm(x, x).mul_(1e-3)
+    return x
+
+
+def side_state(seed):
+    q, c, table, sl = decode_state(seed, [2000, 900], I8)
+    need = P.workspace_bytes("attn_decode", 2, 8, 2, 128, table.shape[1] * 32)
+    assert 0 < need < 1 << 20    # (a block of the allocator's small pool)
+    want = P.ptq1_attn_decode(q, c, table, sl)
+    return q, c, table, sl, need, want, torch.full((4096, 4096), 1e-3, device=DEV)
+
+
+def test_side_stream_while_its_work_is_pending():
+    """The scratch of a call that waits on a side stream is not handed to the current stream's next tensors of that
+    size, nor is its result's memory when the caller drops it."""
+    q, c, table, sl, need, want, x = side_state(130)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            busy(x)
+        got = P.ptq1_attn_decode(q, c, table, sl, stream=side)
+        P.ptq1_attn_decode(q, c, table, sl, stream=side)                     # dropped at once
+        taken = [torch.empty(n, dtype=torch.uint8, device=DEV).fill_(255)    # NaN in fp32
+                 for n in (need, want.numel() * 4) for _ in range(6)]
+        torch.cuda.current_stream().synchronize()
+        side.synchronize()
+        assert torch.equal(got, want)
+        assert all(bool((t == 255).all()) for t in taken)
+
+
+def test_side_stream_beside_pending_work_of_the_current_stream():
+    """Blocks that the current stream has freed, with its own writes still pending on them, do not become the scratch
+    or the result of a call on a side stream."""
+    q, c, table, sl, need, want, x = side_state(131)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        blocks = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in (need, want.numel() * 4) for _ in range(6)]
+        torch.cuda.synchronize()
+        busy(x)
+        for b in blocks:
+            b.fill_(255)
+        del blocks, b
+        got = P.ptq1_attn_decode(q, c, table, sl, stream=side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
+def test_side_stream_every_call():
+    """The four calls, one behind the other on a side stream, give what they give on the current one."""
+    g = gen(132)
+    page, n = 32, 150
+    rows, rope = randn(g, n, 12, 128), rope_table(200, 128)
+    table = torch.arange(5, dtype=torch.int32, device=DEV).view(1, 5)
+    slots, pos = torch.arange(n, device=DEV), torch.arange(n, dtype=torch.int32, device=DEV)
+    cu, sl = cumulated([n]), torch.tensor([n], dtype=torch.int32, device=DEV)
+
+    def chain(stream):
+        c = P.ptq1_kv_cache(5, page, 2, 128, BF16, DEV)
+        torch.cuda.synchronize()
+        q = P.ptq1_kv_write(rows[:, :8], rows[:, 8:10], rows[:, 10:], slots, c, positions=pos, cos_sin=rope, q_dtype=BF16,
+                            stream=stream)
+        k, v = P.ptq1_kv_read(c, table, cu, n, dtype=BF16, stream=stream)
+        o = P.ptq1_attn_prompt(q, k, v, cu, cu, stream=stream)
+        d = P.ptq1_attn_decode(q[-1:], c, table, sl, stream=stream)
+        torch.cuda.synchronize()
+        return q, k, v, o, d
+
+    for a, b in zip(chain(None), chain(torch.cuda.Stream())):
+        assert torch.equal(a, b)

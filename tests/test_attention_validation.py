@@ -458,3 +458,80 @@ int main()
     subprocess.run(["g++", "-std=c++17", "-O1", "-fwrapv", "-I", csrc, str(source), "-o", str(program)], check=True)
     done = subprocess.run([str(program)], capture_output=True, text=True)
     assert done.returncode == 0 and done.stdout == "covered\n", done.returncode
+
+
+class Streams:
+    """A stand-in for torch's current stream: which stream's memory every allocation of a call comes from, and which
+    streams its results are tied to."""
+
+    class Stream:
+        def __init__(self, name, handle):
+            self.name, self.cuda_stream, self.device = name, handle, torch.device("cpu")
+
+    def __init__(self, monkeypatch):
+        import contextlib
+
+        self.main, self.side = self.Stream("main", 1), self.Stream("side", 2)
+        self.current, self.allocated, self.tied = self.main, [], []
+
+        @contextlib.contextmanager
+        def under(s):
+            before, self.current = self.current, s
+            yield
+            self.current = before
+
+        for name in ("empty", "empty_like", "empty_strided"):
+            real = getattr(torch, name)
+
+            def make(*a, _real=real, **kw):
+                self.allocated.append(self.current.name)
+                return _real(*a, **kw)
+
+            monkeypatch.setattr(torch, name, make)
+        monkeypatch.setattr(torch.cuda, "stream", under)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self.current)
+        monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: self.tied.append(s.name))
+        monkeypatch.setattr(P, "_on_device", lambda t: True)
+        real = P.lib()
+
+        class Launched:
+            def __getattr__(_, name):
+                return getattr(real, name) if name.endswith("_bytes") else lambda *a: 0
+
+        monkeypatch.setattr(P, "lib", lambda: Launched())
+
+
+def side_calls():
+    """(call, whether it allocates without out) of each cache and attention call, over host tensors."""
+    c, t = kv(), torch.zeros((2, 400), dtype=torch.int32)
+    q, k, s = z(3, 8, 128), z(3, 2, 128), torch.zeros(3, dtype=torch.int64)
+    return {"kv_write": lambda **o: P.ptq1_kv_write(q, k, k, s, c, **o),
+            "kv_read": lambda **o: P.ptq1_kv_read(c, t, i32(0, 2, 4), 4, **o),
+            "attn_decode": lambda **o: P.ptq1_attn_decode(q[:2], c, t, i32(1, 2), **o),
+            "attn_prompt": lambda **o: P.ptq1_attn_prompt(z(16, 8, 128), z(9000, 2, 128), z(9000, 2, 128), i32(0, 16),
+                                                          i32(0, 9000), **o)}
+
+
+@pytest.mark.parametrize("name", ["kv_write", "kv_read", "attn_decode", "attn_prompt"])
+def test_side_stream_allocates_its_own_memory(monkeypatch, name):
+    """Scratch and results of a call on a stream of the caller's come from that stream's memory (the current stream's
+    freed blocks may have pending work of its own), and the results are tied to the current stream, which uses them."""
+    streams = Streams(monkeypatch)
+    call = side_calls()[name]
+    streams.allocated.clear()
+    call(stream=streams.side)
+    assert streams.allocated and set(streams.allocated) == {"side"}
+    assert streams.tied and set(streams.tied) == {"main"} and streams.current is streams.main
+    # on the current stream, given or not: its own memory, nothing to tie
+    for stream in (None, streams.main):
+        streams.allocated.clear(), streams.tied.clear()
+        call(stream=stream)
+        assert set(streams.allocated) == {"main"} and not streams.tied
+
+
+def test_stream_of_another_device_refused(monkeypatch):
+    streams = Streams(monkeypatch)
+    streams.side.device = torch.device("cuda:1")
+    for call in side_calls().values():
+        with pytest.raises(ValueError, match="the stream is on cuda:1"):
+            call(stream=streams.side)
