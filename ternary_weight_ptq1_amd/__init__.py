@@ -10,6 +10,8 @@ functions raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
+import inspect
 import os
 import re
 
@@ -204,6 +206,32 @@ def _out(out, name, shape, device, dtype=torch.float32):
     return _dev(out, name, dtype, numel=count, device=device)
 
 
+def _tied(result, stream):
+    """result, its tensors' memory kept from other uses until what `stream` does with them is done."""
+    for t in result if isinstance(result, tuple) else (result,):
+        if t is not None:
+            t.record_stream(stream)
+    return result
+
+
+def _on_its_stream(call):
+    """A call whose stream= is not the current one is made with that stream as the current one, so that its scratch and
+    results come from that stream's memory: a block that the current stream has freed may still have work of that
+    stream pending on it."""
+    at = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def run(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None or stream == torch.cuda.current_stream():
+            return call(*args, **kw)
+        here = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            return _tied(call(*args, **kw), here)
+
+    return run
+
+
 # ------------------------------------------------------------------ codec ----
 
 def ptq1_geometry() -> tuple[int, int, int, int, int, int]:
@@ -229,6 +257,7 @@ def _trits_scales(trits, scales_f16):
     return n, k
 
 
+@_on_its_stream
 def ptq1_pack(trits: torch.Tensor, scales_f16: torch.Tensor, out: torch.Tensor | None = None,
               stream=None) -> torch.Tensor:
     """int8 trits [n, k] + binary16 bit patterns [n, k/128] (int16 or float16) -> uint8 [n, k/128*28]."""
@@ -242,6 +271,7 @@ def ptq1_tiled_bytes(n: int, k: int) -> int:
     return lib().ptq1_tiled_bytes(n, k)
 
 
+@_on_its_stream
 def ptq1_tile(blocks: torch.Tensor, n: int, k: int, out: torch.Tensor | None = None,
               stream=None) -> torch.Tensor:
     """Packed [n, k/128*28] uint8 -> the tiled device layout (flat uint8) the
@@ -255,6 +285,7 @@ def ptq1_tile(blocks: torch.Tensor, n: int, k: int, out: torch.Tensor | None = N
     return out
 
 
+@_on_its_stream
 def ptq1_dequant(blocks: torch.Tensor, n: int, k: int, out: torch.Tensor | None = None,
                  stream=None) -> torch.Tensor:
     _mat(blocks, "blocks", ptq1_packed_bytes(n, k), None)
@@ -265,6 +296,7 @@ def ptq1_dequant(blocks: torch.Tensor, n: int, k: int, out: torch.Tensor | None 
 
 # --------------------------------------------------------------- rotation ----
 
+@_on_its_stream
 def hadamard_rotate(x: torch.Tensor, signs1024: torch.Tensor, out: torch.Tensor | None = None,
                     stream=None) -> torch.Tensor:
     """Rotate the rows of x [m, k] (or [k]); out may be x."""
@@ -280,6 +312,7 @@ def hadamard_rotate(x: torch.Tensor, signs1024: torch.Tensor, out: torch.Tensor 
     return out
 
 
+@_on_its_stream
 def hadamard_unrotate_rows(table: torch.Tensor, signs1024: torch.Tensor, ids: torch.Tensor | None = None,
                            n_rows: int | None = None, out: torch.Tensor | None = None,
                            stream=None) -> torch.Tensor:
@@ -302,6 +335,7 @@ def hadamard_unrotate_rows(table: torch.Tensor, signs1024: torch.Tensor, ids: to
 
 # ----------------------------------------------------------------- decode ----
 
+@_on_its_stream
 def ptq1_matvec(blocks: torch.Tensor, n: int, k: int, x: torch.Tensor, signs1024: torch.Tensor | None,
                 residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
                 ws: torch.Tensor | None = None, stream=None, fn: str = "ptq1_matvec") -> torch.Tensor:
@@ -319,11 +353,13 @@ def ptq1_matvec(blocks: torch.Tensor, n: int, k: int, x: torch.Tensor, signs1024
     return out
 
 
+@_on_its_stream
 def ptq1_matvec_float_peel(blocks, n, k, x, signs1024, residual=None, out=None, ws=None, stream=None):
     """The same matvec with every trit peeled on the float pipeline, eight lanes per block (tiled layout)."""
     return ptq1_matvec(blocks, n, k, x, signs1024, residual, out, ws, stream, fn="ptq1_matvec_float_peel")
 
 
+@_on_its_stream
 def ptq1_gate_up(w_gate: torch.Tensor, w_up: torch.Tensor, f: int, d: int, x: torch.Tensor,
                  signs1024: torch.Tensor | None, g: torch.Tensor | None = None,
                  u: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
@@ -341,6 +377,7 @@ def ptq1_gate_up(w_gate: torch.Tensor, w_up: torch.Tensor, f: int, d: int, x: to
     return g, u
 
 
+@_on_its_stream
 def ptq1_swiglu(g: torch.Tensor, u: torch.Tensor, out: torch.Tensor | None = None, stream=None):
     _dev(g, "g", torch.float32)
     _dev(u, "u", torch.float32, numel=g.numel(), device=g.device)
@@ -353,6 +390,7 @@ def ptq1_swiglu(g: torch.Tensor, u: torch.Tensor, out: torch.Tensor | None = Non
 
 # ---------------------------------------------------------------- prefill ----
 
+@_on_its_stream
 def ptq1_gemm(blocks: torch.Tensor, n: int, k: int, x: torch.Tensor, signs1024: torch.Tensor | None,
               out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     _dev(x, "x", torch.float32)
@@ -367,6 +405,7 @@ def ptq1_gemm(blocks: torch.Tensor, n: int, k: int, x: torch.Tensor, signs1024: 
     return out
 
 
+@_on_its_stream
 def ptq1_ffn_block(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
                    signs1024: torch.Tensor, d: int, f: int, rms_eps: float = 0.0,
                    out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
@@ -394,6 +433,7 @@ def ptq1_ffn_block(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_
     return out
 
 
+@_on_its_stream
 def ptq1_ffn_block_noalloc(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
                            signs1024: torch.Tensor, d: int, f: int, rms_eps: float = 0.0,
                            out: torch.Tensor | None = None, stream=None,
@@ -418,6 +458,7 @@ def ptq1_ffn_block_noalloc(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Te
     return out
 
 
+@_on_its_stream
 def pq2_ffn_block(x, w_gate, w_up, w_down, signs1024, d, f, rms_eps=0.0, out=None, ws=None, stream=None,
                   rms_gain=None):
     """ptq1_ffn_block over PQ2_0 tiled matrices."""
@@ -434,6 +475,7 @@ def pq2_packed_bytes(n: int, k: int) -> int:
     return lib().pq2_packed_bytes(n, k)
 
 
+@_on_its_stream
 def pq2_pack(trits: torch.Tensor, scales_f16: torch.Tensor, out: torch.Tensor | None = None,
              stream=None) -> torch.Tensor:
     """int8 trits [n, k] + binary16 bit patterns [n, k/128] -> uint8 [n, k/128*34]."""
@@ -443,6 +485,7 @@ def pq2_pack(trits: torch.Tensor, scales_f16: torch.Tensor, out: torch.Tensor | 
     return out
 
 
+@_on_its_stream
 def pq2_dequant(blocks: torch.Tensor, n: int, k: int, out: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
     _mat(blocks, "blocks", pq2_packed_bytes(n, k), None)
@@ -455,6 +498,7 @@ def pq2_tiled_bytes(n: int, k: int) -> int:
     return lib().pq2_tiled_bytes(n, k)
 
 
+@_on_its_stream
 def pq2_tile(blocks: torch.Tensor, n: int, k: int, out: torch.Tensor | None = None,
              stream=None) -> torch.Tensor:
     """Packed PQ2_0 [n, k/128*34] uint8 -> the tiled layout pq2_matvec reads (flat uint8)."""
@@ -467,6 +511,7 @@ def pq2_tile(blocks: torch.Tensor, n: int, k: int, out: torch.Tensor | None = No
     return out
 
 
+@_on_its_stream
 def pq2_matvec(tiled: torch.Tensor, n: int, k: int, x: torch.Tensor, signs1024: torch.Tensor | None,
                residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
                ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -483,6 +528,7 @@ def pq2_matvec(tiled: torch.Tensor, n: int, k: int, x: torch.Tensor, signs1024: 
     return out
 
 
+@_on_its_stream
 def pq2_gemm(tiled: torch.Tensor, n: int, k: int, x: torch.Tensor, signs1024: torch.Tensor | None,
              out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y [m, n] = bf16(R X) . W^T over a PQ2_0 tiled matrix (pq2_tile)."""
@@ -498,6 +544,7 @@ def pq2_gemm(tiled: torch.Tensor, n: int, k: int, x: torch.Tensor, signs1024: to
     return out
 
 
+@_on_its_stream
 def ptq1_matvec_w2a8(tiled: torch.Tensor, n: int, k: int, x: torch.Tensor, residual: torch.Tensor | None = None,
                      out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y = residual + W q * step with x quantised to 8-bit integers (per call, absmax)."""
@@ -512,6 +559,7 @@ def ptq1_matvec_w2a8(tiled: torch.Tensor, n: int, k: int, x: torch.Tensor, resid
     return out
 
 
+@_on_its_stream
 def ptq1_gemm_w2a8(tiled: torch.Tensor, n: int, k: int, x: torch.Tensor, out: torch.Tensor | None = None,
                    ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y [m, n] with each row of x quantised to 8-bit integers (its own absmax)."""
@@ -602,17 +650,11 @@ def _beside(device, stream) -> bool:
 
 
 def _under(stream, device, fresh: bool, call, *args):
-    """call(*args) with `stream` as the current one, so that what it allocates comes from that stream's memory: a block
-    that the caller's stream has freed may still have work of that stream pending on it.  fresh: the results are new
-    tensors, whose memory may go back to that stream only behind what the caller's does with them."""
+    """call(*args) with `stream` as the current one (as _on_its_stream does); fresh: the results are new tensors."""
     here = torch.cuda.current_stream(device)
     with torch.cuda.stream(stream):
         result = call(*args)
-    if fresh:
-        for t in result if isinstance(result, tuple) else (result,):
-            if t is not None:
-                t.record_stream(here)
-    return result
+    return _tied(result, here) if fresh else result
 
 
 def _current_handle(device):

@@ -1282,3 +1282,26 @@ def test_side_stream_every_call():
 
     for a, b in zip(chain(None), chain(torch.cuda.Stream())):
         assert torch.equal(a, b)
+
+
+def test_projections_on_a_side_stream_beside_pending_work():
+    """The same for a projection: its scratch and result are none of the current stream's freed blocks."""
+    n, k = 1024, 1024
+    w, _ = folded(3, n, k)
+    signs = torch.from_numpy(synth.signs(3)).to(DEV)
+    x = torch.from_numpy(synth.activations(5, 64, k)).to(DEV)
+    want = P.ptq1_gemm(w, n, k, x, signs)
+    sizes = [P.workspace_bytes("gemm", 64, n, k), want.numel() * 4]
+    side, work = torch.cuda.Stream(), torch.full((4096, 4096), 1e-3, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        blocks = [torch.empty(size, dtype=torch.uint8, device=DEV) for size in sizes if size for _ in range(6)]
+        torch.cuda.synchronize()
+        busy(work)
+        for b in blocks:
+            b.fill_(255)
+        del blocks, b
+        got = P.ptq1_gemm(w, n, k, x, signs, stream=side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)

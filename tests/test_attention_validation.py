@@ -535,3 +535,30 @@ def test_stream_of_another_device_refused(monkeypatch):
     for call in side_calls().values():
         with pytest.raises(ValueError, match="the stream is on cuda:1"):
             call(stream=streams.side)
+
+
+def test_side_stream_of_the_projections(monkeypatch):
+    """The calls around the attention (codec, rotation, projections, feed-forward block) alike."""
+    streams = Streams(monkeypatch)
+    n = k = 1024
+    f32 = dict(dtype=torch.float32)
+    x, row, signs = z(2, k, **f32), z(k, **f32), z(1024, **f32)
+    w, w2 = (torch.zeros(size(n, k), dtype=torch.uint8) for size in (P.ptq1_tiled_bytes, P.pq2_tiled_bytes))
+    blocks, blocks2 = (torch.zeros(size(n, k), dtype=torch.uint8) for size in (P.ptq1_packed_bytes, P.pq2_packed_bytes))
+    trits, scales = torch.zeros((n, k), dtype=torch.int8), torch.zeros((n, k // 128), dtype=torch.int16)
+    calls = [(P.ptq1_pack, trits, scales), (P.ptq1_tile, blocks, n, k), (P.ptq1_dequant, blocks, n, k),
+             (P.pq2_pack, trits, scales), (P.pq2_tile, blocks2, n, k), (P.pq2_dequant, blocks2, n, k),
+             (P.hadamard_rotate, x, signs), (P.hadamard_unrotate_rows, x, signs), (P.ptq1_swiglu, row, row),
+             (P.ptq1_matvec, w, n, k, row, signs), (P.ptq1_matvec_float_peel, w, n, k, row, signs),
+             (P.pq2_matvec, w2, n, k, row, signs), (P.ptq1_matvec_w2a8, w, n, k, row),
+             (P.ptq1_gate_up, w, w, n, k, row, signs), (P.ptq1_gemm, w, n, k, x, signs), (P.pq2_gemm, w2, n, k, x, signs),
+             (P.ptq1_gemm_w2a8, w, n, k, x), (P.ptq1_ffn_block, x, w, w, w, signs, k, n),
+             (P.pq2_ffn_block, x, w2, w2, w2, signs, k, n), (P.ptq1_ffn_block_noalloc, x, w, w, w, signs, k, n)]
+    for call, *args in calls:
+        streams.allocated.clear(), streams.tied.clear()
+        call(*args, stream=streams.side)
+        assert streams.allocated and set(streams.allocated) == {"side"}, call.__name__
+        assert streams.tied and set(streams.tied) == {"main"} and streams.current is streams.main, call.__name__
+        streams.allocated.clear(), streams.tied.clear()
+        call(*args)
+        assert set(streams.allocated) == {"main"} and not streams.tied, call.__name__
