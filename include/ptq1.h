@@ -428,7 +428,8 @@ typedef struct ptq1_kv_cache {
  *              stay.
  *   positions  int32 [n_tokens], the row of cos_sin for each token (unused
  *              without rotation).  A position outside [0, n_positions) makes
- *              the token's q_out NaN and its key read back as NaN.
+ *              the elements that would turn NaN, the first rot_dim of the
+ *              token's q_out and key (in an int8 cache its whole key).
  *   slots      int64 [n_tokens].  A slot outside [0, n_pages * page_size)
  *              writes nothing to the cache (padding: -1); q_out is written
  *              all the same.  The slots in the cache must differ: of two

@@ -1305,3 +1305,25 @@ def test_projections_on_a_side_stream_beside_pending_work():
         side.synchronize()
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("ctype", [BF16, I8])
+def test_kv_write_position_outside_the_table(ctype):
+    """Only the elements that would turn are NaN; an int8 row, which has one step, is NaN throughout."""
+    g = gen(141)
+    n, d, rot = 5, 128, 32
+    c = P.ptq1_kv_cache(1, 16, 1, d, ctype, DEV)
+    x = randn(g, n, 4, d)
+    pos = torch.tensor([0, -1, 3, 8, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
+    out = P.ptq1_kv_write(x[:, :2], x[:, 2:3], x[:, 3:], torch.arange(n, device=DEV), c, positions=pos,
+                          cos_sin=rope_table(8, rot))
+    kc, vc = cache_values(c)
+    for t in range(n):
+        outside = not 0 <= pos[t].item() < 8
+        assert bool(out[t, :, :rot].isnan().all()) == outside and torch.equal(out[t, :, rot:], x[t, :2, rot:])
+        key = kc[0, 0, t]
+        if ctype == I8:
+            assert bool(key.isnan().all()) == outside and bool(key.isnan().any()) == outside
+        else:
+            assert bool(key[:rot].isnan().all()) == outside and torch.equal(key[rot:], x[t, 2, rot:].to(BF16).double())
+        assert bool(vc[0, 0, t].isfinite().all())
