@@ -486,7 +486,9 @@ ptq1_status ptq1_kv_read(const ptq1_kv_cache *cache, const int32_t *block_table,
  * above the head's largest magnitude; weight times step enters as three fp16
  * terms (16-bit queries: two), down to 2^-38 of the largest.  Sums, maxima and
  * accumulators are fp32.  A NaN or an infinity in a query or in a key or value
- * that is read makes the entries of out that it enters NaN or infinite.  Long
+ * that is read makes the entries of out that it enters NaN or infinite; an
+ * infinite key that meets a 16-bit query at a score of -infinity has weight zero
+ * instead, as if it were not there (fp32 queries: that or NaN).  Long
  * sequences are cut into pieces that run side by side and are joined by a
  * second launch, in a fixed order.
  * Errors: NULL, SHAPE (n_q_heads not a multiple of n_kv_heads, max_len, scale),

@@ -1327,3 +1327,28 @@ def test_kv_write_position_outside_the_table(ctype):
         else:
             assert bool(key[:rot].isnan().all()) == outside and torch.equal(key[rot:], x[t, 2, rot:].to(BF16).double())
         assert bool(vc[0, 0, t].isfinite().all())
+
+
+@pytest.mark.parametrize("qt,ctype", [(BF16, BF16), (F32, BF16), (F16, F16), (F32, F16)])
+def test_attn_decode_infinite_key(qt, ctype):
+    """An infinite element of a key: rows whose score of it is +infinity are NaN; at -infinity the key has weight
+    zero (fp32 queries, which meet it as several terms: that, or NaN); the other head's rows are as they were."""
+    g = gen(140)
+    n = 50
+    table, pages = tables(g, [n], 16)
+    c = filled_cache(g, pages, 16, 2, 64, ctype)
+    sl = torch.tensor([n], dtype=torch.int32, device=DEV)
+    q = randn(g, 1, 8, 64).to(qt)
+    q[0, :, 5] = torch.tensor([1.3, -0.7, 2.1, -1.9] * 2, device=DEV).to(qt)
+    want = P.ptq1_attn_decode(q, c, table, sl)
+    c.k_pages[table[0, 1].item(), 1, 3, 5] = float("inf")    # token 19 of head 1
+    got = P.ptq1_attn_decode(q, c, table, sl)
+    assert torch.equal(got[0, :4], want[0, :4])
+    assert bool(got[0, [4, 6]].isnan().all())
+    kc, vc = cache_values(c)
+    kept = torch.arange(n, device=DEV) != 19
+    k, v = sequence(c, kc, table, 0, n)[1][kept], sequence(c, vc, table, 0, n)[1][kept]
+    exact, tol = attention_bounds(q[0, [5, 7]].double(), k, v, 64 ** -0.5, WEIGHT_TERM[(qt, ctype)])
+    tol = tol + half_step(exact.abs() + tol, qt)
+    without = ((got[0, [5, 7]].double() - exact).abs() <= tol).all(1)
+    assert bool((without | (got[0, [5, 7]].isnan().all(1) if qt == F32 else without)).all())
