@@ -1352,3 +1352,38 @@ def test_attn_decode_infinite_key(qt, ctype):
     tol = tol + half_step(exact.abs() + tol, qt)
     without = ((got[0, [5, 7]].double() - exact).abs() <= tol).all(1)
     assert bool((without | (got[0, [5, 7]].isnan().all(1) if qt == F32 else without)).all())
+
+
+def test_layer_half_output_projection_and_both_paths():
+    """What test_layer_half_prompt_then_token leaves out: the prompt's output projection (ptq1_gemm) against 64 bits
+    from its own input, and the decode call at the prompt's last position against the prompt call: both are within
+    their bounds of the same rows, so they differ by the sum of the bounds at most."""
+    g = gen(150)
+    dm, hq, hkv, d, n, page = 1024, 8, 2, 128, 77, 32
+    wo, dense = folded(2, dm, hq * d)
+    signs = torch.from_numpy(synth.signs(3)).to(DEV)
+    x = randn(g, n, hq + 2 * hkv, d)
+    c = P.ptq1_kv_cache(3, page, hkv, d, BF16, DEV)
+    table, place = torch.tensor([[2, 0, 1]], dtype=torch.int32, device=DEV), torch.arange(n, device=DEV)
+    slots = table[0, place // page].long() * page + place % page
+    q = P.ptq1_kv_write(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], slots, c, positions=place.to(torch.int32),
+                        cos_sin=rope_table(n, d), q_dtype=BF16)
+    cu = cumulated([n])
+    k, v = P.ptq1_kv_read(c, table, cu, n, dtype=BF16)
+    o = P.ptq1_attn_prompt(q, k, v, cu, cu)
+    check_prompt(q, k, v, [n], [n], o, True)
+    rows = o.float().view(n, hq * d)
+    y = P.ptq1_gemm(wo, dm, hq * d, rows, signs)
+    rot = P.hadamard_rotate(rows, signs).double()
+    want = rot @ dense.T.contiguous()
+    # bf16 rounds every rotated element by 2^-8 of itself at most, the weights are exact, the sums fp32
+    tol = (2.0 ** -8 + hq * d * U) * (rot.abs() @ dense.abs().T.contiguous())
+    assert bool(((y.double() - want).abs() <= tol).all())
+    last = P.ptq1_attn_decode(q[-1:].contiguous(), c, table, torch.tensor([n], dtype=torch.int32, device=DEV))[0]
+    for h in range(hkv):
+        heads = slice(h * hq // hkv, (h + 1) * hq // hkv)
+        args = (q[-1, heads].double(), k[:, h].double(), v[:, h].double(), d ** -0.5)
+        exact, one = attention_bounds(*args, WEIGHT_TERM[(BF16, BF16)])
+        _, other = attention_bounds(*args, torch.finfo(BF16).eps / 2)
+        tol = one + other + half_step(exact.abs() + one, BF16) + half_step(exact.abs() + other, BF16)
+        assert bool(((last[heads].double() - o[-1, heads].double()).abs() <= tol).all())
