@@ -527,7 +527,7 @@ ptq1_status ptq1_attn_decode(const void *q, int32_t q_dtype, int64_t batch, int3
  * Where the query rows alone would not fill the GPU, the keys are cut into
  * chunks that run side by side and are joined by a second launch, in a fixed
  * order; the workspace (for max_k as given, or n_k_rows if that is less) holds
- * their parts.
+ * their parts (the size covers every n_k_rows; a call may need less).
  * Errors: NULL, SHAPE, ALIGN, ALIAS, OVERFLOW, WORKSPACE, UNSUPPORTED (types,
  * head_dim, more than 2^31 - 1025 rows of one kv head or 2^23 tiles of 128
  * query rows, k_stride or v_stride above 2^24). */

@@ -1338,7 +1338,10 @@ size_t ptq1_attn_prompt_workspace_bytes(int64_t batch, int64_t n_q_rows, int64_t
         n_q_heads > kMaxHeads || n_q_heads % n_kv_heads != 0 || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
         n_q_rows < 0 || max_k < 0 || n_q_rows > kMaxRows32 || max_k > kMaxRows32)
         return 0;
-    return round_up(ptq1::prompt_plan(batch, n_q_rows, max_k, n_q_heads, n_kv_heads, head_dim).part_floats * 4, kWsAlign);
+    // the plan also goes by the keys' number, few or all that there may be
+    const size_t few = ptq1::prompt_plan(batch, n_q_rows, max_k, n_q_heads, n_kv_heads, head_dim, 0).part_floats;
+    const size_t all = ptq1::prompt_plan(batch, n_q_rows, max_k, n_q_heads, n_kv_heads, head_dim, batch * max_k).part_floats;
+    return round_up((few > all ? few : all) * 4, kWsAlign);
 }
 
 ptq1_status ptq1_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -1378,7 +1381,7 @@ ptq1_status ptq1_attn_prompt(const void *q, int64_t q_stride, const void *k, int
         return fail(PTQ1_ERR_ALIAS, "out overlaps q, k or v");
     if (overlaps(out, ob, cu_q, (batch + 1) * 4) || overlaps(out, ob, cu_k, (batch + 1) * 4))
         return fail(PTQ1_ERR_ALIAS, "out overlaps cu_q or cu_k");
-    const ptq1::PromptPlan plan = ptq1::prompt_plan(batch, n_q_rows, max_k, n_q_heads, n_kv_heads, head_dim);
+    const ptq1::PromptPlan plan = ptq1::prompt_plan(batch, n_q_rows, max_k, n_q_heads, n_kv_heads, head_dim, n_k_rows);
     const size_t need = round_up(plan.part_floats * 4, kWsAlign);
     PTQ1_TRY(check_ws(ws, ws_bytes, need, "ptq1_attn_prompt"));
     const int64_t wn = static_cast<int64_t>(need);

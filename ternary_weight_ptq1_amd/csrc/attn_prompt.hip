@@ -727,24 +727,33 @@ int64_t prompt_tiles(int64_t batch, int64_t q_rows, int32_t hq, int32_t hkv)
 // sequence comes near.
 constexpr double kMaxParts = 1 << 28;
 
-PromptPlan prompt_plan(int64_t batch, int64_t q_rows, int64_t max_k, int32_t hq, int32_t hkv, int32_t d)
+PromptPlan prompt_plan(int64_t batch, int64_t q_rows, int64_t max_k, int32_t hq, int32_t hkv, int32_t d, int64_t k_rows)
 {
     // The time with tiles cut in n along their keys, in us: rounds of
     // workgroups, each of a key's time as measured with the GPU full, and from
     // n = 2 on the parts' rows in fp32 (written and read, at half of HBM's rate:
     // they come in bursts) and the join.  Either all tiles are cut, or only
     // those behind the last full round of whole ones, if the tiles reach about
-    // equally far (few queries behind many keys): of whole prompts' tiles the
-    // last ones are the shortest, which fill the gaps as they are (1272 tiles of
-    // up to 2500 keys of 128, 89 us, took 115 cut in two).  16 queries over 8016
-    // keys: 146 us uncut, 20 in chunks of 512; 1657 queries of 24 heads of 256 over 4000 and more, 320 tiles: 307
-    // uncut, 266 all cut in two, 229 the last 64 in three.
+    // equally far: few queries behind many keys, and these at least 0.6 of the
+    // longest sequence's on average (`even`).  16 queries over 8016 keys: 146 us
+    // uncut, 20 in chunks of 512; 1657 queries of 24 heads of 256 over 4000 and
+    // more, 320 tiles: 307 uncut, 266 all cut in two, 229 the last 64 in three;
+    // 40 batches of 1 to 16 chunks behind contexts 0.93 of the time uncut (0.81
+    // to 1.03), at an evenness of 0.5 1.01 to 1.05 times it.
+    // A ragged batch of whole prompts has few queries by their mean as well, but
+    // not as many keys.  Its last tiles are the shortest and fill the gaps as
+    // they are, so where its tiles fill the GPU none is cut: 40 batches of 5 to
+    // 33 prompts of 840 to 7800 tokens and less 0.96 of the time with the last
+    // tiles cut (0.83 to 1.00); 1272 tiles of up to 2500 keys of 128, 89 us, took
+    // 115 all cut in two.
     PromptPlan p;
     const double slots = d == 256 ? 256 : 512, key = d == 256 ? 0.04 : 0.029;  // workgroups the GPU holds
     const int64_t tiles = prompt_tiles(batch, q_rows, hq, hkv);
     p.tiles = static_cast<int32_t>(tiles);
-    const bool alike = batch > 0 && max_k >= 4 * (q_rows / batch);
-    const int64_t full = alike ? static_cast<int64_t>(static_cast<double>(tiles * hkv) / slots) * static_cast<int64_t>(slots) / hkv : 0;
+    const bool few = batch > 0 && max_k >= 4 * (q_rows / batch);
+    const bool even = static_cast<double>(k_rows) >= 0.6 * static_cast<double>(batch) * static_cast<double>(max_k);
+    const int64_t full = few && even ? static_cast<int64_t>(static_cast<double>(tiles * hkv) / slots) * static_cast<int64_t>(slots) / hkv : 0;
+    const int most = few && !even && static_cast<double>(tiles * hkv) > slots ? 1 : 64;
     double best = 0.0;
     int n = 1;
     for (const int64_t whole : {int64_t{0}, full}) {
@@ -752,7 +761,7 @@ PromptPlan prompt_plan(int64_t batch, int64_t q_rows, int64_t max_k, int32_t hq,
         const double rest = static_cast<double>((tiles - whole) * hkv);
         const double before = __builtin_ceil(static_cast<double>(whole * hkv) / slots) * static_cast<double>(max_k) * key;
         const double rows = whole > 0 ? rest * kPrRows : static_cast<double>(q_rows) * hq;
-        for (int i = whole > 0 ? 2 : 1; i <= 64 && max_k / i >= 256; ++i) {
+        for (int i = whole > 0 ? 2 : 1; i <= most && max_k / i >= 256; ++i) {
             if (i > 1 && rows * i * (d + 2) * 4 > kMaxParts) break;
             double us = before + __builtin_ceil(rest * i / slots) * static_cast<double>(max_k) / i * key;
             if (i > 1) us += 6.0 + rest * i * kPrRows * d * 4 * 2 / 2.5e6;

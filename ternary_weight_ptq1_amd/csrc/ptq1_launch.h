@@ -186,7 +186,7 @@ struct PromptPlan {
     float per_cut = 0.0f;  // 1 / (tiles - whole), 0 with splits = 1
     size_t rows_floats = 0, part_floats = 0;
 };
-PromptPlan prompt_plan(int64_t batch, int64_t q_rows, int64_t max_k, int32_t hq, int32_t hkv, int32_t d);
+PromptPlan prompt_plan(int64_t batch, int64_t q_rows, int64_t max_k, int32_t hq, int32_t hkv, int32_t d, int64_t k_rows);
 // tiles of 128 query rows that one kv head's rows may make up
 int64_t prompt_tiles(int64_t batch, int64_t q_rows, int32_t hq, int32_t hkv);
 // part: unused (splits == 1), or the chunks' unnormalised rows [row][head]

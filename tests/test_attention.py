@@ -1387,3 +1387,30 @@ def test_layer_half_output_projection_and_both_paths():
         _, other = attention_bounds(*args, torch.finfo(BF16).eps / 2)
         tol = one + other + half_step(exact.abs() + one, BF16) + half_step(exact.abs() + other, BF16)
         assert bool(((last[heads].double() - o[-1, heads].double()).abs() <= tol).all())
+
+
+def test_attn_prompt_ragged_prompts_are_not_cut():
+    """Whole prompts of unlike lengths in more tiles than the GPU holds: the last tiles are the shortest and stay whole,
+    so the call needs no scratch; chunks behind contexts of about one length, as many tiles, are cut and need it."""
+    g = gen(160)
+    hq, hkv, d = 20, 4, 64
+    lens = [1235, 43, 45, 70, 37, 208, 392, 229, 366, 62, 56, 233, 790, 133, 26, 28]
+    chunks, context = [245] * 16, 4000
+
+    def call(lq, lk, ws):
+        q, k, v = prompt_state(g, lq, lk, hq, hkv, d)
+        cq, ck, out = cumulated(lq), cumulated(lk), torch.empty_like(q)
+        size = 0 if ws is None else ws.numel()
+        status = P.lib().ptq1_attn_prompt(q.data_ptr(), hq * d, k.data_ptr(), hkv * d, v.data_ptr(), hkv * d, 2,
+                                          cq.data_ptr(), ck.data_ptr(), len(lq), sum(lq), sum(lk), max(lq), max(lk), hq,
+                                          hkv, d, 1, d ** -0.5, out.data_ptr(), 0 if ws is None else ws.data_ptr(), size,
+                                          torch.cuda.current_stream().cuda_stream)
+        if status == 0:
+            check_prompt(q, k, v, lq, lk, out, True)
+        return status
+
+    assert call(lens, lens, None) == 0
+    behind = [n + context for n in chunks]
+    assert call(chunks, behind, None) == 6
+    need = P.workspace_bytes("attn_prompt", 16, sum(chunks), max(behind), hq, hkv, d)
+    assert call(chunks, behind, torch.empty(need, dtype=torch.uint8, device=DEV)) == 0
