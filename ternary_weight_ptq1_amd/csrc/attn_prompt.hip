@@ -7,8 +7,18 @@
 // matrix cores: 2 d multiply-adds for every visible pair, against 2 bytes of
 // each operand.  Measured: 16384 tokens, 40 heads over 8 of 128, causal:
 // 2.5 ms (1090 TFLOP/s of visible pairs; a library matrix product 1180 to
-// 1350), matrix cores busy 60% of the cycles and vector units 52%, at a clock
-// of 1.75 GHz; 9 prompts of 5 to 2500 tokens 87 us; 33 tokens 8.6 us.
+// 1350), matrix cores busy 60% of the cycles and vector units 53%, at a clock
+// of 1.75 GHz; 9 prompts of 5 to 2500 tokens 87 us; 33 tokens 8.7 us.  64-wide
+// heads have twice the exponentials for a product: 8192 tokens of 32 heads over
+// 8 reach 900 TFLOP/s with the vector units 79% busy and the matrix cores 50%.
+//
+// The weights enter the second product as one 16-bit term, rounded once, while
+// their sum is taken in fp32.  A second term costs half of the matrix work
+// again and more registers: 16384 tokens 2640 -> 3670 us, 9 prompts 98 -> 125,
+// 33 tokens 8.8 -> 9.3 (one box), for an error against 64 bits, relative to the
+// rows' norm, of 1.64e-3 instead of 2.17e-3 in bf16 (1.64e-3 is the rounding of
+// the result alone) and 2.0e-4 instead of 2.6e-4 in fp16; and of 256-wide heads
+// the pairs' weights would not fit into LDS beside the tiles.
 //
 // Rows.  The query rows of a kv head are its group's heads of every token
 // (row r = token r / group, head r % group): a tile of 128 rows then shares
@@ -516,7 +526,11 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptA
 // SIMD) took 286, pairs in workgroups of four waves with one buffer each for K
 // and V (two a CU; the copies have half a tile's time) 251, the next tile's
 // scores taken beside this one's weights 266 (the matrix cores and the vector
-// units then overlap in a wave, but the registers leave no reads ahead).
+// units then overlap in a wave, but the registers leave no reads ahead).  At
+// 8192 tokens the matrix cores are 44% busy and the vector units 28%: the eight
+// waves run in step, by three barriers a tile.  16 registers of a lane are
+// spilled around the main loop (by the set-up, the border tiles and the end),
+// none in it.
 //
 // Barriers with waits of their own: __syncthreads would wait for the copies
 // that have just been issued.  The wait for the copies is the builtin, so that
