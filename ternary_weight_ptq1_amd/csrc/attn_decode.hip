@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
     at_f32x4 o[D / 16];
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) o[i] = zero4;
-    float m = -__builtin_inff(), l = 0.0f;
+    float m = -__builtin_inff(), l = 0.0f;  // m: the largest score, lifted: the weights are powers relative to it
     // int8: weights times steps enter in units of 2^(wexp - 14), wexp such that
     // they are below 2^14 in fp16; o is in these units
     int wexp = -112;
@@ -463,6 +463,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
             }
         top = lane_pair_max<32>(lane_pair_max<16>(top));
         // a larger maximum rescales what is there (all lanes of a head alike)
+        if constexpr (kLift != 0.0f) top = lifted(top, kLift);
         if (__ballot(top > m) != 0) {
             const float mn = fmaxf(m, top);
             float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
             for (int i = 0; i < D / 16; ++i) o[i] *= f;
             m = mn;
         }
-        const float ms = m == -__builtin_inff() ? 0.0f : m - kLift;
+        const float ms = m == -__builtin_inff() ? 0.0f : m;
         float p[TS / 4];
 #pragma unroll
         for (int t = 0; t < NT; ++t)

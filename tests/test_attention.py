@@ -1414,3 +1414,46 @@ def test_attn_prompt_ragged_prompts_are_not_cut():
     assert call(chunks, behind, None) == 6
     need = P.workspace_bytes("attn_prompt", 16, sum(chunks), max(behind), hq, hkv, d)
     assert call(chunks, behind, torch.empty(need, dtype=torch.uint8, device=DEV)) == 0
+
+
+# ------------------------------------------------------------------ large scores ----
+
+def winners(q, k, v, scale, mask=None):
+    """(rows, which of them count) of one kv head where a row's largest score is so far ahead that its value is the
+    result: by more than 100 and four times what fp32 scores of this size can be off by."""
+    logits = scale * (q @ k.T.contiguous())
+    size = (scale * (q.abs() @ k.abs().T.contiguous())).amax(1)
+    if mask is not None:
+        logits = logits.masked_fill(~mask, -math.inf)
+    best = logits.topk(min(2, logits.shape[1]), 1)
+    ahead = best.values[:, 0] - (best.values[:, -1] if logits.shape[1] > 1 else -math.inf)
+    return v[best.indices[:, 0]], ahead > 100 + 4 * (q.shape[1] + 8) * U * size
+
+
+@pytest.mark.parametrize("qt,ctype", PAIRS)
+@pytest.mark.parametrize("size", [1e4, 1e6, 1e8, 1e12])
+def test_attn_decode_large_scores(qt, ctype, size):
+    """Scores of 10^4 to 10^12 and above: a softmax that picks one token, and no NaN or infinity from what the
+    weights are lifted or lowered by."""
+    g = gen(170)
+    lens = [700, 40, 2]
+    table, pages = tables(g, lens, 32)
+    c = filled_cache(g, pages, 32, 2, 128, ctype)
+    q = randn(g, 3, 8, 128)
+    scale = 128 ** -0.5
+    if qt == F16:   # the rest of the size in the scale
+        q, scale = (q * min(size, 1e3)).to(qt), scale * size / min(size, 1e3)
+    else:
+        q = (q * size).to(qt)
+    got = P.ptq1_attn_decode(q, c, table, torch.tensor(lens, dtype=torch.int32, device=DEV), scale=scale).double()
+    kc, vc = cache_values(c)
+    counted = 0
+    for b, n in enumerate(lens):
+        k, v = sequence(c, kc, table, b, n), sequence(c, vc, table, b, n)
+        assert bool((got[b].abs() <= v.abs().max() * 1.01).all())       # (a NaN fails too)
+        for h in range(2):
+            want, ok = winners(q[b, 4 * h:4 * h + 4].double(), k[h], v[h], scale)
+            counted += int(ok.sum())
+            off = (got[b, 4 * h:4 * h + 4] - want).abs()[ok]
+            assert bool((off <= half_step(want[ok], qt) + 4 * U * want[ok].abs()).all())
+    assert counted >= 12
