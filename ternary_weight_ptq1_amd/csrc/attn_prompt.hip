@@ -57,9 +57,22 @@ constexpr int kKeys = 64;  // keys of a tile
 // of the largest weight at most, so that many small weights beside one large
 // one do not vanish.  bf16 weights, which have fp32's exponents, are 2^-40
 // times themselves: the sum over 2^31 keys is then in fp32's range whenever the
-// values are.
+// values are.  A row's reference, of which its weights are powers, is its
+// largest score less the lift.
 template <typename T>
-constexpr float kWeightLift = std::is_same<T, _Float16>::value ? 7.0f : -40.0f;
+__device__ __forceinline__ float reference(float top)
+{
+    return lifted(top, std::is_same<T, _Float16>::value ? 7.0f : -40.0f);
+}
+
+// Scores so large (2^20 in units of log2) that a product rounded and one fused
+// into the exponent's sum differ by too much of a weight, in some row: the
+// products are then rounded first.
+__device__ __forceinline__ bool large_scores(float top)
+{
+    constexpr uint32_t kFrom = 0x49800000u, kInf = 0x7f800000u;
+    return __ballot((__builtin_bit_cast(uint32_t, top) & 0x7fffffffu) - kFrom < kInf - kFrom) != 0;
+}
 
 // Query rows of a workgroup: 32 a wave, or a pair of waves (256-wide heads).
 constexpr int kPrRows = 128;
@@ -397,7 +410,7 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptA
     for (int i = 0; i < DT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
-    float m = -__builtin_inff(), l = 0.0f;  // m: in units of log2
+    float m = -__builtin_inff(), l = 0.0f;  // m: the reference, in units of log2
 
     // S^T of the tile in kb
     auto scores = [&](at_f32x16 (&s)[KT], const T *kb) {
@@ -427,11 +440,12 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptA
             for (int j = 0; j < 16; ++j) top = fmaxf(top, s[t][j]);
         return lane_pair_max<32>(top) * c;
     };
-    // The maximum in use may lag by 8 (weights up to 2^8 lose nothing in
+    // The reference in use may lag by 8 (weights up to 2^8 lose nothing in
     // either type): few tiles after the first rescale.
     auto raise = [&](float top) {
-        if (__ballot(top > m + 8.0f) != 0) {
-            const float mn = fmaxf(m, top);
+        const float mt = reference<T>(top);
+        if (__ballot(mt > m + 8.0f) != 0) {
+            const float mn = fmaxf(m, mt);
             const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
             l *= f;
 #pragma unroll
@@ -459,14 +473,23 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptA
         }
         __builtin_amdgcn_sched_group_barrier(0x8, kAhead, 0);
         if constexpr (BORDER) hide(s, n0);
-        raise(largest(s));
-        const float ms = m == -__builtin_inff() ? 0.0f : m - kWeightLift<T>;
+        const float top = largest(s);
+        raise(top);
+        const float ms = m == -__builtin_inff() ? 0.0f : m;
+        float mul = c;
+        if (large_scores(top)) {
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[t][j] *= c;
+            mul = 1.0f;
+        }
         x8 pf[2 * KT];
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const float e = __builtin_amdgcn_exp2f(fmaf(s[t][j], c, -ms));
+                const float e = __builtin_amdgcn_exp2f(fmaf(s[t][j], mul, -ms));
                 l += e;
                 pf[2 * t + (j >> 3)][j & 7] = static_cast<T>(e);
             }
@@ -528,7 +551,7 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptA
 // scores taken beside this one's weights 266 (the matrix cores and the vector
 // units then overlap in a wave, but the registers leave no reads ahead).  At
 // 8192 tokens the matrix cores are 44% busy and the vector units 28%: the eight
-// waves run in step, by three barriers a tile.  16 registers of a lane are
+// waves run in step, by three barriers a tile.  15 registers of a lane are
 // spilled around the main loop (by the set-up, the border tiles and the end),
 // none in it.
 //
@@ -610,19 +633,26 @@ __global__ void __launch_bounds__(64 * prompt_waves(256), 2) k_attn_prompt_wide(
         if (half == 0) tops[pair][part][col] = top;
         barrier_lds();
         top = fmaxf(top, tops[pair][part ^ 1][col]);
-        if (__ballot(top > m + 8.0f) != 0) {  // the same in both waves
-            const float mn = fmaxf(m, top);
+        const float mt = reference<T>(top);
+        if (__ballot(mt > m + 8.0f) != 0) {  // the same in both waves
+            const float mn = fmaxf(m, mt);
             const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
             l *= f;
 #pragma unroll
             for (int i = 0; i < DT; ++i) o[i] *= f;
             m = mn;
         }
-        const float ms = m == -__builtin_inff() ? 0.0f : m - kWeightLift<T>;
+        const float ms = m == -__builtin_inff() ? 0.0f : m;
+        float mul = c;
+        if (large_scores(top)) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s[j] *= c;
+            mul = 1.0f;
+        }
         x8 pf[2];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            const float e = __builtin_amdgcn_exp2f(fmaf(s[j], c, -ms));
+            const float e = __builtin_amdgcn_exp2f(fmaf(s[j], mul, -ms));
             l += e;
             pf[j >> 3][j & 7] = static_cast<T>(e);
         }

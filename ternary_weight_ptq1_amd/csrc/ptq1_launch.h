@@ -155,7 +155,7 @@ hipError_t launch_kv_read(const ptq1_kv_cache &c, const int32_t *table, int64_t 
 // many steps of 256 tokens, so many that all sequences' pieces fill the GPU
 // (`shares` workgroups for one kv head); `pieces` bounds their number.  part:
 // the pieces' unnormalised rows [piece][hq][d] (int8 caches: lower by a power
-// of two), then their (maximum, sum) pairs; unused without join (no sequence
+// of two), then their (reference, sum) pairs; unused without join (no sequence
 // can be cut).
 struct DecodePlan {
     int32_t shares = 1;
@@ -191,7 +191,7 @@ PromptPlan prompt_plan(int64_t batch, int64_t q_rows, int64_t max_k, int32_t hq,
 int64_t prompt_tiles(int64_t batch, int64_t q_rows, int32_t hq, int32_t hkv);
 // part: unused (splits == 1), or the chunks' unnormalised rows [row][head]
 // [splits][d] (whole > 0: [tile that is cut][row of the tile][splits][d]), then
-// their (maximum, sum) pairs.
+// their (reference, sum) pairs.
 hipError_t launch_attn_prompt(const PromptArgs &a, int dtype, int32_t d, const PromptPlan &plan, float *part,
                               hipStream_t s);
 

@@ -1457,3 +1457,26 @@ def test_attn_decode_large_scores(qt, ctype, size):
             off = (got[b, 4 * h:4 * h + 4] - want).abs()[ok]
             assert bool((off <= half_step(want[ok], qt) + 4 * U * want[ok].abs()).all())
     assert counted >= 12
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lq,lk", [([150], [150]), ([3], [9000])])
+@pytest.mark.parametrize("size", [1e4, 1e6, 1e8, 1e12])
+def test_attn_prompt_large_scores_pick_one(dtype, d, lq, lk, size):
+    g = gen(171)
+    q, k, v = prompt_state(g, lq, lk, 4, 2, d, dtype)
+    some = min(size, 1e3)
+    q, scale = (q.float() * some).to(dtype), d ** -0.5 * size / some
+    got = P.ptq1_attn_prompt(q, k, v, cumulated(lq), cumulated(lk), scale=scale).double()
+    assert bool((got.abs() <= v.abs().max().double() * 1.01).all())
+    mask = torch.arange(lk[0], device=DEV)[None] <= torch.arange(lq[0], device=DEV)[:, None] + (lk[0] - lq[0])
+    counted = 0
+    for h in range(4):
+        vv = v[:, h // 2].double()
+        want, ok = winners(q[:, h].double(), k[:, h // 2].double(), vv, scale, mask)
+        counted += int(ok.sum())
+        # (its weight is rounded to dtype, their sum is not)
+        off, tol = (got[:, h] - want).abs()[ok], half_step(want[ok], dtype) * 2 + 4 * U * want[ok].abs()
+        assert bool((off <= tol).all())
+    assert counted >= 4
