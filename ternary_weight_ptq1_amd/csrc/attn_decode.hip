@@ -381,17 +381,19 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
     // not __syncthreads: it would wait for the first K and V
     if constexpr (I8) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     const bool any_far = I8 && __ballot(far != 1.0f) != 0;
-    // fp16 weights as multiples of 2^-14 of themselves, sums too: small ones
-    // (many tokens beside one that takes nearly all) would fall below fp16's
-    // smallest step, 2^-24, otherwise.  bf16 weights, which have fp32's
-    // exponents, 2^-22 times themselves: the sum over the 2^22 tokens that a
-    // sequence may have is then in fp32's range whenever the values are.
-    constexpr float kLift = std::is_same<C, _Float16>::value ? 14.0f : I8 ? 0.0f : -22.0f;
+    // fp16 weights, and sums, are 2^14 times themselves: small ones (many tokens
+    // beside one that takes nearly all) would fall below fp16's smallest step,
+    // 2^-24, otherwise.  bf16 weights, which have fp32's exponents, 2^-22 times
+    // themselves: the sum over the 2^22 tokens that a sequence may have is then
+    // in fp32's range whenever the values are.  (A product of its own: in the
+    // exponent it costs the weights the low bits of the sum there: fp32
+    // queries over 77 tokens are off by 4.9e-7 of the result then, 3.0e-7 so.)
+    constexpr float kLift = I8 ? 1.0f : std::is_same<C, _Float16>::value ? 0x1p14f : 0x1p-22f;
     const at_f32x4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
     at_f32x4 o[D / 16];
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) o[i] = zero4;
-    float m = -__builtin_inff(), l = 0.0f;  // m: the largest score, lifted: the weights are powers relative to it
+    float m = -__builtin_inff(), l = 0.0f;
     // int8: weights times steps enter in units of 2^(wexp - 14), wexp such that
     // they are below 2^14 in fp16; o is in these units
     int wexp = -112;
@@ -463,7 +465,6 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
             }
         top = lane_pair_max<32>(lane_pair_max<16>(top));
         // a larger maximum rescales what is there (all lanes of a head alike)
-        if constexpr (kLift != 0.0f) top = lifted(top, kLift);
         if (__ballot(top > m) != 0) {
             const float mn = fmaxf(m, top);
             float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
@@ -486,7 +487,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float e = __builtin_amdgcn_exp2f(s[t][i] - ms);
+                float e = __builtin_amdgcn_exp2f(s[t][i] - ms) * kLift;
                 l += e;
                 if constexpr (I8) e *= tail && base + RUN * grp + 4 * t + i >= end ? 0.0f : vs[t][i];
                 p[4 * t + i] = e;

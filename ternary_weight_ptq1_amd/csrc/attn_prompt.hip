@@ -57,12 +57,16 @@ constexpr int kKeys = 64;  // keys of a tile
 // of the largest weight at most, so that many small weights beside one large
 // one do not vanish.  bf16 weights, which have fp32's exponents, are 2^-40
 // times themselves: the sum over 2^31 keys is then in fp32's range whenever the
-// values are.  A row's reference, of which its weights are powers, is its
-// largest score less the lift.
+// values are.
+//
+// A row's reference, the number that its weights are powers relative to, is its
+// largest score less that.  It is what the kernels keep and join by, so its
+// rounding is no error; but where that could move a weight by more than a
+// factor of 2 (scores from 2^24 on) it is the largest score itself.
 template <typename T>
 __device__ __forceinline__ float reference(float top)
 {
-    return lifted(top, std::is_same<T, _Float16>::value ? 7.0f : -40.0f);
+    return fabsf(top) < 0x1p24f ? top - (std::is_same<T, _Float16>::value ? 7.0f : -40.0f) : top;
 }
 
 // Scores so large (2^20 in units of log2) that a product rounded and one fused

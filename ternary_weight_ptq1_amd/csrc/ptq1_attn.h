@@ -73,13 +73,6 @@ __device__ __forceinline__ float lane_pair_max(float v)
     return fmaxf(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi));
 }
 
-// The number that a row's weights are powers relative to, with a largest score
-// of `top`: top - lift, so that the largest weight is 2^lift.  What is used is
-// what the kernels keep and join by, so its rounding is no error; but where it
-// could move a weight by more than a factor of 2 (scores from 2^24 on) the
-// largest weight is 1.
-__device__ __forceinline__ float lifted(float top, float lift) { return fabsf(top) < 0x1p24f ? top - lift : top; }
-
 // 4 contiguous elements of a source row, as fp32.
 __device__ __forceinline__ at_f32x4 load4(const float *p) { return *reinterpret_cast<const at_f32x4 *>(p); }
 __device__ __forceinline__ at_f32x4 load4(const __bf16 *p)
