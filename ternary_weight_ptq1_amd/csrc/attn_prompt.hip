@@ -61,12 +61,13 @@ constexpr int kKeys = 64;  // keys of a tile
 //
 // A row's reference, the number that its weights are powers relative to, is its
 // largest score less that.  It is what the kernels keep and join by, so its
-// rounding is no error; but where that could move a weight by more than a
-// factor of 2 (scores from 2^24 on) it is the largest score itself.
+// rounding is no error; but from 2^23 on, where that could make a weight larger
+// by more than 2^0.5 (and with the lag more than fp16 holds), it is the largest
+// score itself.
 template <typename T>
 __device__ __forceinline__ float reference(float top)
 {
-    return fabsf(top) < 0x1p24f ? top - (std::is_same<T, _Float16>::value ? 7.0f : -40.0f) : top;
+    return fabsf(top) < 0x1p23f ? top - (std::is_same<T, _Float16>::value ? 7.0f : -40.0f) : top;
 }
 
 // Scores so large (2^20 in units of log2) that a product rounded and one fused

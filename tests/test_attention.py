@@ -1480,3 +1480,26 @@ def test_attn_prompt_large_scores_pick_one(dtype, d, lq, lk, size):
         off, tol = (got[:, h] - want).abs()[ok], half_step(want[ok], dtype) * 2 + 4 * U * want[ok].abs()
         assert bool((off <= tol).all())
     assert counted >= 4
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("power", [20, 23, 24, 25, 31])
+def test_attn_prompt_scores_around_powers_of_two(dtype, d, power):
+    """Exact scores that grow along the keys from just below to just above (minus) a power of two, where the size of
+    the last place changes: no weight may leave the type's range, a row's mean stays within its values."""
+    g = gen(172 + power)
+    n = 200
+    v = randn(g, n, 2, d).to(dtype)
+    for sign in (1, -1):
+        # score in log2 units: sign 2^power + rising small terms, as two exact products
+        q = torch.zeros((3, 2, d), device=DEV, dtype=dtype)
+        k = torch.zeros((n, 2, d), device=DEV, dtype=dtype)
+        half = 2.0 ** min(power // 2, 10)
+        q[..., 0], q[..., 1] = half, 1
+        k[..., 0] = sign * 2.0 ** min(power - math.log2(half), 15)
+        k[..., 1] = torch.arange(-n // 2, n // 2, device=DEV)[:, None] % 64 - 32 + torch.arange(n, device=DEV)[:, None] // 40 * 8
+        scale = math.log(2.0) * 2.0 ** (power - math.log2(half) - min(power - math.log2(half), 15))
+        for lq in (1, 3):
+            got = P.ptq1_attn_prompt(q[:lq], k, v, cumulated([lq]), cumulated([n]), scale=scale, causal=False).double()
+            assert bool(got.isfinite().all()) and bool((got.abs() <= 1.02 * v.abs().amax(0).double()).all())
