@@ -75,7 +75,7 @@ __device__ __forceinline__ void row_quantiser(float top, float &step, float &mul
         step = 0.0f;
         mul = 0.0f;
     } else {
-        step = top / 127.0f;
+        step = fminf(top / 127.0f, 0x1.020406p121f);  // (times 127 it is finite)
         mul = 127.0f / top;
     }
 }

@@ -1503,3 +1503,19 @@ def test_attn_prompt_scores_around_powers_of_two(dtype, d, power):
         for lq in (1, 3):
             got = P.ptq1_attn_prompt(q[:lq], k, v, cumulated([lq]), cumulated([n]), scale=scale, causal=False).double()
             assert bool(got.isfinite().all()) and bool((got.abs() <= 1.02 * v.abs().amax(0).double()).all())
+
+
+def test_kv_write_largest_rows():
+    """int8 rows up to the largest finite value read back finite, within the step's bound."""
+    d = 64
+    c = P.ptq1_kv_cache(1, 16, 1, d, I8, DEV)
+    top = torch.finfo(F32).max
+    x = torch.full((16, 1, d), top, device=DEV)
+    for i in range(1, 16):
+        x[i] = torch.nextafter(x[i - 1], torch.zeros_like(x[i]))
+    x[:, :, 1::2] *= -0.5
+    P.ptq1_kv_write(None, x, x, torch.arange(16, device=DEV), c)
+    table, cu = torch.zeros((1, 1), dtype=torch.int32, device=DEV), cumulated([16])
+    for got in P.ptq1_kv_read(c, table, cu, 16, dtype=F32):
+        assert bool(got.isfinite().all())
+        check_rows(got, x.double(), x.double().abs() * U, I8)
