@@ -484,8 +484,9 @@ ptq1_status ptq1_kv_read(const ptq1_kv_cache *cache, const int32_t *block_table,
  * largest).  Over int8 caches the codes enter exactly; the queries are fixed-point
  * numbers, multiples of 2^-29 (fp32 queries) or 2^-21 of a power of two not
  * above the head's largest magnitude; weight times step enters as three fp16
- * terms (16-bit queries: two), down to 2^-38 of the largest.  Sums, maxima and
- * accumulators are fp32.  A NaN or an infinity in a query or in a key or value
+ * terms (16-bit queries: two), down to 2^-38 of the largest or to 2^-149.  Sums,
+ * maxima and accumulators are fp32; values up to fp32's largest, or steps up to
+ * the bound above, do not overflow on the way to a row that is in range.  A NaN or an infinity in a query or in a key or value
  * that is read makes the entries of out that it enters NaN or infinite; an
  * infinite key that meets a 16-bit query at a score of -infinity has weight zero
  * instead, as if it were not there (fp32 queries: that or NaN).  Long
