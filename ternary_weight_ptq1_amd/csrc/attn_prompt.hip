@@ -70,13 +70,13 @@ __device__ __forceinline__ float reference(float top)
     return fabsf(top) < 0x1p23f ? top - (std::is_same<T, _Float16>::value ? 7.0f : -40.0f) : top;
 }
 
-// Scores so large (2^20 in units of log2) that a product rounded and one fused
-// into the exponent's sum differ by too much of a weight, in some row: the
-// products are then rounded first.
-__device__ __forceinline__ bool large_scores(float top)
+// Some row's reference is so large (2^20 in units of log2) that a product
+// rounded and one fused into the exponent's sum would differ by too much of a
+// weight: the products are then rounded first.
+__device__ __forceinline__ bool large_scores(float m)
 {
     constexpr uint32_t kFrom = 0x49800000u, kInf = 0x7f800000u;
-    return __ballot((__builtin_bit_cast(uint32_t, top) & 0x7fffffffu) - kFrom < kInf - kFrom) != 0;
+    return __ballot((__builtin_bit_cast(uint32_t, m) & 0x7fffffffu) - kFrom < kInf - kFrom) != 0;
 }
 
 // Query rows of a workgroup: 32 a wave, or a pair of waves (256-wide heads).
@@ -416,6 +416,7 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptA
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
     float m = -__builtin_inff(), l = 0.0f;  // m: the reference, in units of log2
+    bool large = false;
 
     // S^T of the tile in kb
     auto scores = [&](at_f32x16 (&s)[KT], const T *kb) {
@@ -456,6 +457,7 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptA
 #pragma unroll
             for (int i = 0; i < DT; ++i) o[i] *= f;
             m = mn;
+            large = large_scores(m);
         }
     };
 
@@ -478,11 +480,10 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptA
         }
         __builtin_amdgcn_sched_group_barrier(0x8, kAhead, 0);
         if constexpr (BORDER) hide(s, n0);
-        const float top = largest(s);
-        raise(top);
+        raise(largest(s));
         const float ms = m == -__builtin_inff() ? 0.0f : m;
         float mul = c;
-        if (large_scores(top)) {
+        if (large) {
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -605,6 +606,7 @@ __global__ void __launch_bounds__(64 * prompt_waves(256), 2) k_attn_prompt_wide(
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
     float m = -__builtin_inff(), l = 0.0f;  // l: of this wave's keys
+    bool large = false;
 
     auto step = [&](auto border, const T *kb, T *vb, T *kn, T *vn, int n0) {
         constexpr bool BORDER = decltype(border)::value;
@@ -646,10 +648,11 @@ __global__ void __launch_bounds__(64 * prompt_waves(256), 2) k_attn_prompt_wide(
 #pragma unroll
             for (int i = 0; i < DT; ++i) o[i] *= f;
             m = mn;
+            large = large_scores(m);
         }
         const float ms = m == -__builtin_inff() ? 0.0f : m;
         float mul = c;
-        if (large_scores(top)) {
+        if (large) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) s[j] *= c;
             mul = 1.0f;
