@@ -486,12 +486,12 @@ ptq1_status ptq1_kv_read(const ptq1_kv_cache *cache, const int32_t *block_table,
  * above the head's largest magnitude; weight times step enters as three fp16
  * terms (16-bit queries: two), down to 2^-38 of the largest or to 2^-149.  Sums,
  * maxima and accumulators are fp32; values up to fp32's largest, or steps up to
- * the bound above, do not overflow on the way to a row that is in range.  A NaN or an infinity in a query or in a key or value
- * that is read makes the entries of out that it enters NaN or infinite; an
- * infinite key that meets a 16-bit query at a score of -infinity has weight zero
- * instead, as if it were not there (fp32 queries: that or NaN).  Long
- * sequences are cut into pieces that run side by side and are joined by a
- * second launch, in a fixed order.
+ * the bound above, do not overflow on the way to a row that is in range.  A NaN
+ * or an infinity in a query or in a key or value that is read makes the entries
+ * of out that it enters NaN or infinite; an infinite key that meets a 16-bit
+ * query at a score of -infinity has weight zero instead, as if it were not there
+ * (fp32 queries: that or NaN).  Long sequences are cut into pieces that run side
+ * by side and are joined by a second launch, in a fixed order.
  * Errors: NULL, SHAPE (n_q_heads not a multiple of n_kv_heads, max_len, scale),
  * ALIGN, ALIAS, OVERFLOW, WORKSPACE, UNSUPPORTED (types, head_dim, page_size,
  * batch > 65535, more than 2^24 - 2^14 groups of 16 query heads of a kv head in
