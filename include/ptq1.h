@@ -524,7 +524,7 @@ ptq1_status ptq1_attn_decode(const void *q, int32_t q_dtype, int64_t batch, int3
  *   scale  positive, 2^126 at most.
  * bf16 or fp16 matrix cores, fp32 scores, maxima, sums and accumulators; the
  * weights enter the second product rounded to dtype (fp16: to 11 bits, down to
- * 2^-32 of the row's largest), the sum is over fp32.
+ * 2^-32 of the row's largest), and their sum, in fp32, is that of the rounded ones.
  * Where the query rows alone would not fill the GPU, the keys are cut into
  * chunks that run side by side and are joined by a second launch, in a fixed
  * order; the workspace (for max_k as given, or n_k_rows if that is less) holds

@@ -12,13 +12,16 @@
 // heads have twice the exponentials for a product: 8192 tokens of 32 heads over
 // 8 reach 900 TFLOP/s with the vector units 79% busy and the matrix cores 50%.
 //
-// The weights enter the second product as one 16-bit term, rounded once, while
-// their sum is taken in fp32.  A second term costs half of the matrix work
-// again and more registers: 16384 tokens 2640 -> 3670 us, 9 prompts 98 -> 125,
-// 33 tokens 8.8 -> 9.3 (one box), for an error against 64 bits, relative to the
-// rows' norm, of 1.64e-3 instead of 2.17e-3 in bf16 (1.64e-3 is the rounding of
-// the result alone) and 2.0e-4 instead of 2.6e-4 in fp16; and of 256-wide heads
-// the pairs' weights would not fit into LDS beside the tiles.
+// The weights enter the second product as one 16-bit term, rounded once, and
+// the rounded ones are summed, in fp32.  Values without a mean under many alike
+// weights show it most: the rows' error against 64 bits, relative to their
+// norm, is 2.15e-3 in bf16 for 16384 tokens (1.64e-3 the rounding of the result
+// alone) and 2.6e-4 in fp16 (2.0e-4); with sharper weights or a mean of the
+// values, 3 times their spread, it is that rounding's plus 1% (summed unrounded
+// plus 9%).  A second term for the rest costs half of the matrix work again and
+// more registers: 16384 tokens 2640 -> 3670 us, 9 prompts 98 -> 125, 33 tokens
+// 8.8 -> 9.3 (one card); and of 256-wide heads the pairs' weights would not fit
+// into LDS beside the tiles.
 //
 // Rows.  The query rows of a kv head are its group's heads of every token
 // (row r = token r / group, head r % group): a tile of 128 rows then shares
@@ -77,6 +80,23 @@ __device__ __forceinline__ bool large_scores(float m)
 {
     constexpr uint32_t kFrom = 0x49800000u, kInf = 0x7f800000u;
     return __ballot((__builtin_bit_cast(uint32_t, m) & 0x7fffffffu) - kFrom < kInf - kFrom) != 0;
+}
+
+// l + the sum, in fp32, of eight weights as they enter the second product,
+// rounded to T: a row's weights then make up one, and what a rounding adds to
+// one value it takes from the others (with the sum over unrounded weights a row
+// that sees one key only was off by that key's rounding).
+template <typename T>
+__device__ __forceinline__ float add_weights(typename Op16<T>::x8 p, float l)
+{
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        if constexpr (std::is_same<T, _Float16>::value)
+            l = __builtin_amdgcn_fdot2(f16x2{p[i], p[i + 1]}, f16x2{1.0f, 1.0f}, l, false);
+        else
+            l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{p[i], p[i + 1]}, bf16x2{1.0f, 1.0f}, l, false);
+    }
+    return l;
 }
 
 // Query rows of a workgroup: 32 a wave, or a pair of waves (256-wide heads).
@@ -415,7 +435,7 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptA
     for (int i = 0; i < DT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
-    float m = -__builtin_inff(), l = 0.0f;  // m: the reference, in units of log2
+    float m = -__builtin_inff(), l = 0.0f, l2 = 0.0f;  // m: the reference, in units of log2
     bool large = false;
 
     // S^T of the tile in kb
@@ -454,6 +474,7 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptA
             const float mn = fmaxf(m, mt);
             const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
             l *= f;
+            l2 *= f;
 #pragma unroll
             for (int i = 0; i < DT; ++i) o[i] *= f;
             m = mn;
@@ -495,10 +516,13 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptA
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const float e = __builtin_amdgcn_exp2f(fmaf(s[t][j], mul, -ms));
-                l += e;
-                pf[2 * t + (j >> 3)][j & 7] = static_cast<T>(e);
+                pf[2 * t + (j >> 3)][j & 7] = static_cast<T>(__builtin_amdgcn_exp2f(fmaf(s[t][j], mul, -ms)));
             }
+#pragma unroll
+        for (int u = 0; u < 2 * KT; u += 2) {
+            l = add_weights<T>(pf[u], l);
+            l2 = add_weights<T>(pf[u + 1], l2);
+        }
         if constexpr (BORDER) {
             // Some rows do not see some of these keys, and a zero weight would
             // not keep a NaN or an infinity out of them: such values leave the
@@ -537,7 +561,7 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptA
         if (n0 + BN >= any) break;
         step(std::true_type{}, kt1, vt1, kt0, vt0, n0 + BN);
     }
-    l = lane_pair_sum<32>(l);
+    l = lane_pair_sum<32>(l + l2);
     const float f = t.split ? 1.0f : seen == 0 ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[i] *= f;
@@ -605,7 +629,7 @@ __global__ void __launch_bounds__(64 * prompt_waves(256), 2) k_attn_prompt_wide(
     for (int i = 0; i < DT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
-    float m = -__builtin_inff(), l = 0.0f;  // l: of this wave's keys
+    float m = -__builtin_inff(), l = 0.0f, l2 = 0.0f;  // l: of this wave's keys
     bool large = false;
 
     auto step = [&](auto border, const T *kb, T *vb, T *kn, T *vn, int n0) {
@@ -645,6 +669,7 @@ __global__ void __launch_bounds__(64 * prompt_waves(256), 2) k_attn_prompt_wide(
             const float mn = fmaxf(m, mt);
             const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
             l *= f;
+            l2 *= f;
 #pragma unroll
             for (int i = 0; i < DT; ++i) o[i] *= f;
             m = mn;
@@ -660,10 +685,10 @@ __global__ void __launch_bounds__(64 * prompt_waves(256), 2) k_attn_prompt_wide(
         x8 pf[2];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            const float e = __builtin_amdgcn_exp2f(fmaf(s[j], mul, -ms));
-            l += e;
-            pf[j >> 3][j & 7] = static_cast<T>(e);
+            pf[j >> 3][j & 7] = static_cast<T>(__builtin_amdgcn_exp2f(fmaf(s[j], mul, -ms)));
         }
+        l = add_weights<T>(pf[0], l);
+        l2 = add_weights<T>(pf[1], l2);
         weights[pair][2 * part][lane] = pf[0];
         weights[pair][2 * part + 1][lane] = pf[1];
         if constexpr (BORDER) {
@@ -699,7 +724,7 @@ __global__ void __launch_bounds__(64 * prompt_waves(256), 2) k_attn_prompt_wide(
     }
 
     // the pair's sums
-    l = lane_pair_sum<32>(l);
+    l = lane_pair_sum<32>(l + l2);
     __syncthreads();
     if (half == 0) tops[pair][part][col] = l;
     __syncthreads();

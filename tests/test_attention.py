@@ -1519,3 +1519,27 @@ def test_kv_write_largest_rows():
     for got in P.ptq1_kv_read(c, table, cu, 16, dtype=F32):
         assert bool(got.isfinite().all())
         check_rows(got, x.double(), x.double().abs() * U, I8)
+
+
+# ------------------------------------------------- weights that make up one ----
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rows", [3, 700])
+def test_attn_prompt_rounded_weights_make_up_one(dtype, d, rows):
+    """Each weight is rounded to 16 bits, and the rounded ones are summed.  One key of score 0 and value 0 comes first,
+    then 500 of score 5 + x (in log2) and one value: the reference stays at the first, and each of the 500 is 2^x
+    times a power of two, which is rounded by 0.45 of a step.  Summed unrounded, that would take the row a step away from
+    its value (1.98, where half a step is 2^-9 of it, fp16 2^-12); so only what the first key weighs is off, 2^-8 / 16000
+    and the fp32 sums, 2 * 600 * 2^-24: neither moves the rounding of the result."""
+    n, step = 564, torch.finfo(dtype).eps
+    q, k, v = (torch.zeros((m, 4, d), device=DEV, dtype=dtype) for m in (rows, n, n))
+    q[..., 0], q[..., 1] = 1, 1
+    k[1:64, :, 0] = -100
+    k[64:, :, 0], k[64:, :, 1] = 5, math.log2(1 + 0.45 * step)
+    v[64:] = 1.98
+    got = P.ptq1_attn_prompt(q, k, v, cumulated([rows]), cumulated([n]), causal=False, scale=math.log(2.0))
+    w = torch.exp(math.log(2.0) * (q[0, 0].double() @ k[:, 0].double().T.contiguous()))
+    exact = (w / w.sum()) @ v[:, 0].double()
+    assert bool((exact - exact.to(dtype).double()).abs().max() < 0.4 * step)    # (far from a border of the rounding)
+    assert torch.equal(got, exact.to(dtype).expand(rows, 4, d))
