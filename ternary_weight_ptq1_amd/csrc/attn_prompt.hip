@@ -6,11 +6,11 @@
 // in one pass over the keys with a running maximum m_i.  Bounded by the
 // matrix cores: 2 d multiply-adds for every visible pair, against 2 bytes of
 // each operand.  Measured: 16384 tokens, 40 heads over 8 of 128, causal:
-// 2.5 ms (1090 TFLOP/s of visible pairs; a library matrix product 1180 to
-// 1350), matrix cores busy 60% of the cycles and vector units 53%, at a clock
+// 2.5 ms (1100 TFLOP/s of visible pairs; a library matrix product 1180 to
+// 1350), matrix cores busy 60% of the cycles and vector units 49%, at a clock
 // of 1.75 GHz; 9 prompts of 5 to 2500 tokens 87 us; 33 tokens 8.7 us.  64-wide
 // heads have twice the exponentials for a product: 8192 tokens of 32 heads over
-// 8 reach 900 TFLOP/s with the vector units 79% busy and the matrix cores 50%.
+// 8 reach 920 TFLOP/s with the vector units 72% busy and the matrix cores 48%.
 //
 // The weights enter the second product as one 16-bit term, rounded once, and
 // the rounded ones are summed, in fp32.  Values without a mean under many alike
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(64 * prompt_waves(D), 2) k_attn_prompt(PromptA
 // and V (two a CU; the copies have half a tile's time) 251, the next tile's
 // scores taken beside this one's weights 266 (the matrix cores and the vector
 // units then overlap in a wave, but the registers leave no reads ahead).  At
-// 8192 tokens the matrix cores are 44% busy and the vector units 28%: the eight
+// 8192 tokens the matrix cores are 44% busy and the vector units 26%: the eight
 // waves run in step, by three barriers a tile.  15 registers of a lane are
 // spilled around the main loop (by the set-up, the border tiles and the end),
 // none in it.
