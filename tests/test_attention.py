@@ -1543,3 +1543,21 @@ def test_attn_prompt_rounded_weights_make_up_one(dtype, d, rows):
     exact = (w / w.sum()) @ v[:, 0].double()
     assert bool((exact - exact.to(dtype).double()).abs().max() < 0.4 * step)    # (far from a border of the rounding)
     assert torch.equal(got, exact.to(dtype).expand(rows, 4, d))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rows", [2, 300])
+@pytest.mark.parametrize("below", [22, 26, 30])
+def test_attn_prompt_small_weights_count_in_the_sum(dtype, d, rows, below):
+    """One key of score 0 and value 0, then 65536 of weight 2^-22 to 2^-30 and one value: fp16's subnormal weights are
+    multiplied and summed alike.  (They are exact: powers of two, down to 2^-31 of the largest in fp16.)"""
+    n = 65537
+    q, k, v = (torch.zeros((m, 2, d), device=DEV, dtype=dtype) for m in (rows, n, n))
+    q[..., 0], k[1:, :, 0], v[1:] = 1, -below, 1000
+    got = P.ptq1_attn_prompt(q, k, v, cumulated([rows]), cumulated([n]), causal=False, scale=math.log(2.0)).double()
+    total = 65536 * 2.0 ** -below
+    want = torch.tensor(1000 * total / (1 + total), dtype=torch.float64)
+    # scale log2(e) is off by 2^-24 of itself, twice: the scores by that times `below`; the sums by 2^-24 for each term
+    tol = want * (below * 2.0 ** -22 + 65536 * U)
+    assert bool(((got - want).abs() <= tol + half_step(want + tol, dtype)).all()), (got.flatten()[0].item(), want.item())
