@@ -446,6 +446,25 @@ ptq1_status ptq1_kv_write(const void *q, int64_t q_stride, const void *k, int64_
                           const int64_t *slots, void *q_out, int32_t q_dtype, const ptq1_kv_cache *cache,
                           hipStream_t stream);
 
+/* ptq1_kv_write with norms of the query and key heads ahead of the rotation
+ * (layers that norm each head of q and k):
+ *   x' = a * gain * x,  a = (mean(x^2) + eps)^(-1/2) over the head's
+ *   head_dim elements, in fp32;
+ * values go into the cache as they are.
+ *   q_gain, k_gain  fp32 [head_dim], 16-byte aligned, one for all heads; NULL:
+ *        ones.
+ *   eps  2^-100 to 2^100.
+ * Everything else as in ptq1_kv_write.  Finite rows of any magnitude are
+ * normed (where the squares leave fp32's range, eps, which is then nothing
+ * beside them, is left out).  A NaN in a head makes all of it NaN, an infinity
+ * its own element NaN and the others, before the rotation, zero.
+ * Errors: as ptq1_kv_write; SHAPE (eps). */
+ptq1_status ptq1_kv_write_norm(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                               int64_t v_stride, int32_t src_dtype, int64_t n_tokens, int32_t n_q_heads,
+                               const float *q_gain, const float *k_gain, float eps, const int32_t *positions,
+                               const float *cos_sin, int64_t n_positions, int32_t rot_dim, const int64_t *slots,
+                               void *q_out, int32_t q_dtype, const ptq1_kv_cache *cache, hipStream_t stream);
+
 /* Reads whole sequences back, packed: rows cu_seqlens[b] .. cu_seqlens[b + 1]
  * of k_out and v_out [n_rows][n_kv_heads][head_dim] (out_dtype F32, F16 or
  * BF16) get the first cu_seqlens[b + 1] - cu_seqlens[b] tokens of sequence b,
@@ -502,6 +521,23 @@ ptq1_status ptq1_attn_decode(const void *q, int32_t q_dtype, int64_t batch, int3
                              const ptq1_kv_cache *cache, const int32_t *block_table, int64_t max_pages,
                              const int32_t *seq_lens, int64_t max_len, float scale, void *out, void *ws,
                              size_t ws_bytes, hipStream_t stream);
+
+/* ptq1_attn_decode for layers with a sliding window: of a sequence's n =
+ * seq_lens[b] tokens the last `window` (the new one among them) and the first
+ * `sinks` are seen,
+ *   j >= n - window  or  j < sinks.
+ * Pages that hold no such token are not read, and their entries of block_table
+ * may be anything: a program may give them back.  Everything else as in
+ * ptq1_attn_decode (a page outside [0, n_pages) matters among those that hold a
+ * token that is seen); the work is laid out for the tokens that are read.
+ *   window  1 or more (more than max_len: every token is seen); sinks 0 or more.
+ * Errors: as ptq1_attn_decode; SHAPE (window, sinks). */
+size_t ptq1_attn_decode_window_workspace_bytes(int64_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                               int64_t max_len, int64_t window, int64_t sinks);
+ptq1_status ptq1_attn_decode_window(const void *q, int32_t q_dtype, int64_t batch, int32_t n_q_heads,
+                                    const ptq1_kv_cache *cache, const int32_t *block_table, int64_t max_pages,
+                                    const int32_t *seq_lens, int64_t max_len, int64_t window, int64_t sinks, float scale,
+                                    void *out, void *ws, size_t ws_bytes, hipStream_t stream);
 
 /* Attention over whole prompts, packed without padding: sequence b's queries
  * are rows cu_q[b] .. cu_q[b + 1] of q [n_q_rows][n_q_heads][head_dim], its

@@ -86,9 +86,14 @@ _SIGS = {
     "pq2_ffn_workspace_offsets": ([i64, i64, i64, p], C.c_int),
     "ptq1_kv_write": ([p, i64, p, i64, p, i64, C.c_int32, i64, C.c_int32, p, p, i64, C.c_int32, p, p, C.c_int32, p, p],
                       C.c_int),
+    "ptq1_kv_write_norm": ([p, i64, p, i64, p, i64, C.c_int32, i64, C.c_int32, p, p, C.c_float, p, p, i64, C.c_int32, p, p,
+                            C.c_int32, p, p], C.c_int),
     "ptq1_kv_read": ([p, p, i64, p, i64, i64, p, p, C.c_int32, p], C.c_int),
     "ptq1_attn_decode_workspace_bytes": ([i64, C.c_int32, C.c_int32, C.c_int32, i64], sz),
     "ptq1_attn_decode": ([p, C.c_int32, i64, C.c_int32, p, p, i64, p, i64, C.c_float, p, p, sz, p], C.c_int),
+    "ptq1_attn_decode_window_workspace_bytes": ([i64, C.c_int32, C.c_int32, C.c_int32, i64, i64, i64], sz),
+    "ptq1_attn_decode_window": ([p, C.c_int32, i64, C.c_int32, p, p, i64, p, i64, i64, i64, C.c_float, p, p, sz, p],
+                                C.c_int),
     "ptq1_attn_prompt_workspace_bytes": ([i64, i64, i64, C.c_int32, C.c_int32, C.c_int32], sz),
     "ptq1_attn_prompt": ([p, i64, p, i64, p, i64, C.c_int32, p, p, i64, i64, i64, i64, i64, C.c_int32, C.c_int32,
                           C.c_int32, C.c_int32, C.c_float, p, p, sz, p], C.c_int),
@@ -713,21 +718,15 @@ def _table(block_table, batch, device):
     return block_table.shape[1]
 
 
-def ptq1_kv_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: KvCache,
-                  positions: torch.Tensor | None = None, cos_sin: torch.Tensor | None = None, q_dtype=None,
-                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
-    """Writes fresh tokens k, v [n, n_kv_heads, head_dim] into the cache at slots (int64 [n]; page * page_size +
-    place, -1: not written), turning k and q [n, n_q_heads, head_dim] by the rows positions (int32 [n]) of
-    cos_sin [n_positions, rot_dim] (rot_dim / 2 cosines, then sines) if it is given.  q, k and v may be parts of
-    the rows of one stacked projection.  Returns the turned queries in q_dtype (q's own by default), or None
-    without q."""
+def _kv_write(q, k, v, slots, cache, positions, cos_sin, q_dtype, out, stream, norm):
+    """Both writes; norm: None or (q_gain, k_gain, eps)."""
     kv = _kv(cache)
     dv = kv.device
     if _elsewhere(dv):
         with torch.cuda.device(dv):
-            return ptq1_kv_write(q, k, v, slots, cache, positions, cos_sin, q_dtype, out, stream)
+            return _kv_write(q, k, v, slots, cache, positions, cos_sin, q_dtype, out, stream, norm)
     if _beside(dv, stream):
-        return _under(stream, dv, out is None, ptq1_kv_write, q, k, v, slots, cache, positions, cos_sin, q_dtype, out)
+        return _under(stream, dv, out is None, _kv_write, q, k, v, slots, cache, positions, cos_sin, q_dtype, out, None, norm)
     n, h, d, ks = _rows3(k, "k", _FLOATS, dv)
     if h != kv.n_kv_heads or d != kv.head_dim:
         raise ValueError(f"k has {h} heads of {d}, the cache {kv.n_kv_heads} of {kv.head_dim}")
@@ -758,19 +757,48 @@ def ptq1_kv_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, slot
             raise ValueError("cos_sin needs positions")
     if positions is not None and not _plain(positions, torch.int32, n, dv):
         _dev(positions, "positions", torch.int32, numel=n, device=dv)
+    if norm is not None:
+        for name, gain in (("q_gain", norm[0]), ("k_gain", norm[1])):
+            if gain is not None and not _plain(gain, torch.float32, d, dv):
+                _dev(gain, name, torch.float32, numel=d, device=dv)
     handle = _current_handle(dv)
     if q is not None:
         if out is None:
             out = torch.empty_like(q, dtype=q_dtype, memory_format=torch.contiguous_format)
         else:
             _dev(out, "out", q_dtype, numel=n * hq * d, device=dv)
-    status = lib().ptq1_kv_write(0 if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPES[src],
-                                 n, hq, positions.data_ptr() if rot else 0, cos_sin.data_ptr() if rot else 0, n_pos, rot,
-                                 slots.data_ptr(), 0 if out is None else out.data_ptr(),
-                                 _DTYPES[src if q is None else q_dtype], kv._ref, handle)
+    rows = 0 if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPES[src], n, hq
+    rest = (positions.data_ptr() if rot else 0, cos_sin.data_ptr() if rot else 0, n_pos, rot, slots.data_ptr(),
+            0 if out is None else out.data_ptr(), _DTYPES[src if q is None else q_dtype], kv._ref, handle)
+    if norm is None:
+        status = lib().ptq1_kv_write(*rows, *rest)
+    else:
+        q_gain, k_gain, eps = norm
+        status = lib().ptq1_kv_write_norm(*rows, 0 if q_gain is None else q_gain.data_ptr(),
+                                          0 if k_gain is None else k_gain.data_ptr(), eps, *rest)
     if status:
-        _check("ptq1_kv_write", status)
+        _check("ptq1_kv_write" if norm is None else "ptq1_kv_write_norm", status)
     return out
+
+
+def ptq1_kv_write(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: KvCache,
+                  positions: torch.Tensor | None = None, cos_sin: torch.Tensor | None = None, q_dtype=None,
+                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Writes fresh tokens k, v [n, n_kv_heads, head_dim] into the cache at slots (int64 [n]; page * page_size +
+    place, -1: not written), turning k and q [n, n_q_heads, head_dim] by the rows positions (int32 [n]) of
+    cos_sin [n_positions, rot_dim] (rot_dim / 2 cosines, then sines) if it is given.  q, k and v may be parts of
+    the rows of one stacked projection.  Returns the turned queries in q_dtype (q's own by default), or None
+    without q."""
+    return _kv_write(q, k, v, slots, cache, positions, cos_sin, q_dtype, out, stream, None)
+
+
+def ptq1_kv_write_norm(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: KvCache,
+                       q_gain: torch.Tensor | None = None, k_gain: torch.Tensor | None = None, eps: float = 1e-6,
+                       positions: torch.Tensor | None = None, cos_sin: torch.Tensor | None = None, q_dtype=None,
+                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """ptq1_kv_write with an RMS norm of every head of q and k ahead of the rotation: (mean(x^2) + eps)^(-1/2) * gain *
+    x, gains fp32 [head_dim] (None: ones).  The other arguments and the result are ptq1_kv_write's."""
+    return _kv_write(q, k, v, slots, cache, positions, cos_sin, q_dtype, out, stream, (q_gain, k_gain, eps))
 
 
 def ptq1_kv_read(cache: KvCache, block_table: torch.Tensor, cu_seqlens: torch.Tensor, n_rows: int,
@@ -809,20 +837,16 @@ def ptq1_kv_read(cache: KvCache, block_table: torch.Tensor, cu_seqlens: torch.Te
     return k, v
 
 
-def ptq1_attn_decode(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, seq_lens: torch.Tensor,
-                     scale: float | None = None, max_len: int | None = None, out: torch.Tensor | None = None,
-                     ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """Attention of one new token per sequence, q [batch, n_q_heads, head_dim], over the first seq_lens[b] (int32)
-    tokens of its pages block_table[b] (int32 [batch, max_pages]).  scale: 1 / sqrt(head_dim) by default; max_len: a
-    bound on seq_lens (the table's by default).  ws: optional scratch of at least workspace_bytes("attn_decode",
-    batch, n_q_heads, n_kv_heads, head_dim, max_len) bytes."""
+def _attn_decode(q, cache, block_table, seq_lens, scale, max_len, out, ws, stream, seen):
+    """Both calls of single tokens; seen: () or (window, sinks)."""
     kv = _kv(cache)
     dv = kv.device
     if _elsewhere(dv):
         with torch.cuda.device(dv):
-            return ptq1_attn_decode(q, cache, block_table, seq_lens, scale, max_len, out, ws, stream)
+            return _attn_decode(q, cache, block_table, seq_lens, scale, max_len, out, ws, stream, seen)
     if _beside(dv, stream):
-        return _under(stream, dv, out is None, ptq1_attn_decode, q, cache, block_table, seq_lens, scale, max_len, out, ws)
+        return _under(stream, dv, out is None, _attn_decode, q, cache, block_table, seq_lens, scale, max_len, out, ws, None,
+                      seen)
     _dev(q, "q", _FLOATS, device=dv)
     if q.dim() != 3 or q.shape[2] != kv.head_dim:
         raise ValueError(f"q must be [batch, n_q_heads, {kv.head_dim}]")
@@ -833,7 +857,11 @@ def ptq1_attn_decode(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor,
     if max_len is None:
         max_len = max_pages * kv.page_size
     handle = _current_handle(dv)
-    wsb = lib().ptq1_attn_decode_workspace_bytes(batch, hq, kv.n_kv_heads, d, max_len)
+    if seen:
+        name, call, size = "ptq1_attn_decode_window", lib().ptq1_attn_decode_window, lib().ptq1_attn_decode_window_workspace_bytes
+    else:
+        name, call, size = "ptq1_attn_decode", lib().ptq1_attn_decode, lib().ptq1_attn_decode_workspace_bytes
+    wsb = size(batch, hq, kv.n_kv_heads, d, max_len, *seen)
     if ws is None:
         if wsb:
             ws = torch.empty_strided((wsb,), (1,), dtype=torch.uint8, device=dv)
@@ -843,12 +871,33 @@ def ptq1_attn_decode(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor,
         out = torch.empty_like(q)
     else:
         _dev(out, "out", q.dtype, numel=q.numel(), device=dv)
-    status = lib().ptq1_attn_decode(q.data_ptr(), _DTYPES[q.dtype], batch, hq, kv._ref, block_table.data_ptr(), max_pages,
-                                    seq_lens.data_ptr(), max_len, d ** -0.5 if scale is None else scale, out.data_ptr(),
-                                    0 if ws is None else ws.data_ptr(), wsb, handle)
+    status = call(q.data_ptr(), _DTYPES[q.dtype], batch, hq, kv._ref, block_table.data_ptr(), max_pages,
+                  seq_lens.data_ptr(), max_len, *seen, d ** -0.5 if scale is None else scale, out.data_ptr(),
+                  0 if ws is None else ws.data_ptr(), wsb, handle)
     if status:
-        _check("ptq1_attn_decode", status)
+        _check(name, status)
     return out
+
+
+def ptq1_attn_decode(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                     scale: float | None = None, max_len: int | None = None, out: torch.Tensor | None = None,
+                     ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence, q [batch, n_q_heads, head_dim], over the first seq_lens[b] (int32)
+    tokens of its pages block_table[b] (int32 [batch, max_pages]).  scale: 1 / sqrt(head_dim) by default; max_len: a
+    bound on seq_lens (the table's by default).  ws: optional scratch of at least workspace_bytes("attn_decode",
+    batch, n_q_heads, n_kv_heads, head_dim, max_len) bytes."""
+    return _attn_decode(q, cache, block_table, seq_lens, scale, max_len, out, ws, stream, ())
+
+
+def ptq1_attn_decode_window(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                            window: int, sinks: int = 0, scale: float | None = None, max_len: int | None = None,
+                            out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                            stream=None) -> torch.Tensor:
+    """ptq1_attn_decode over the last `window` tokens of every sequence (the new one among them) and its first `sinks`
+    alone.  Pages that hold neither are not read: their entries of block_table may be anything.  ws: optional scratch of
+    at least workspace_bytes("attn_decode_window", batch, n_q_heads, n_kv_heads, head_dim, max_len, window, sinks)
+    bytes."""
+    return _attn_decode(q, cache, block_table, seq_lens, scale, max_len, out, ws, stream, (window, sinks))
 
 
 def ptq1_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
@@ -916,6 +965,7 @@ def workspace_bytes(kind: str, *shape) -> int:
           "gemm": "ptq1_gemm_workspace_bytes", "ffn": "ptq1_ffn_workspace_bytes",
           "pq2_matvec": "pq2_matvec_workspace_bytes", "pq2_gemm": "pq2_gemm_workspace_bytes",
           "attn_decode": "ptq1_attn_decode_workspace_bytes",
+          "attn_decode_window": "ptq1_attn_decode_window_workspace_bytes",
           "attn_prompt": "ptq1_attn_prompt_workspace_bytes"}[kind]
     return int(getattr(lib(), fn)(*shape))
 

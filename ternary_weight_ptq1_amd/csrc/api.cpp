@@ -1185,16 +1185,14 @@ bool decode_sizes_ok(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_t 
            batch * hkv * ((hq / hkv + 15) / 16) <= kMaxDecodeGroups;
 }
 
-}  // namespace
-
-extern "C" {
-
-ptq1_status ptq1_kv_write(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
-                          int64_t v_stride, int32_t src_dtype, int64_t n_tokens, int32_t n_q_heads,
-                          const int32_t *positions, const float *cos_sin, int64_t n_positions, int32_t rot_dim,
-                          const int64_t *slots, void *q_out, int32_t q_dtype, const ptq1_kv_cache *cache,
-                          hipStream_t stream)
+// Every check of a write, its norms' gains among them (null without).  *nothing: there are no tokens.
+ptq1_status check_kv_write(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                           int64_t v_stride, int32_t src_dtype, int64_t n_tokens, int32_t n_q_heads,
+                           const float *q_gain, const float *k_gain, const int32_t *positions, const float *cos_sin,
+                           int64_t n_positions, int32_t rot_dim, const int64_t *slots, const void *q_out, int32_t q_dtype,
+                           const ptq1_kv_cache *cache, bool *nothing)
 {
+    *nothing = false;
     KvBytes kb;
     PTQ1_TRY(check_cache(cache, &kb));
     if (!cache_disjoint(cache, kb)) return fail(PTQ1_ERR_ALIAS, "the cache's arrays overlap one another");
@@ -1209,7 +1207,8 @@ ptq1_status ptq1_kv_write(const void *q, int64_t q_stride, const void *k, int64_
     if (!float_type(q_dtype)) return fail(PTQ1_ERR_UNSUPPORTED, "q_dtype %d (F32, F16 or BF16)", q_dtype);
     if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 8 != 0)
         return fail(PTQ1_ERR_SHAPE, "rot_dim = %d (a multiple of 8 up to head_dim)", rot_dim);
-    if (n_tokens == 0) return ok();
+    *nothing = n_tokens == 0;
+    if (*nothing) return ok();
     const int64_t d = cache->head_dim, es = type_bytes(src_dtype);
     int64_t qb, kbytes, vbytes, tb = 0;
     PTQ1_TRY(check_strided(q, "q", n_tokens, n_q_heads * d, q_stride, es, &qb));
@@ -1237,10 +1236,105 @@ ptq1_status ptq1_kv_write(const void *q, int64_t q_stride, const void *k, int64_
         if (overlaps(q_out, ob, positions, n_tokens * 4) || overlaps_cache(positions, n_tokens * 4, cache, kb))
             return fail(PTQ1_ERR_ALIAS, "q_out or the cache overlaps positions");
     }
+    for (const float *gain : {q_gain, k_gain}) {
+        if (gain == nullptr) continue;
+        PTQ1_TRY(check_device_array(gain, gain == q_gain ? "q_gain" : "k_gain", d * 4, kAlign));
+        if (overlaps(q_out, ob, gain, d * 4) || overlaps_cache(gain, d * 4, cache, kb))
+            return fail(PTQ1_ERR_ALIAS, "q_out or the cache overlaps %s", gain == q_gain ? "q_gain" : "k_gain");
+    }
+    return ok();
+}
+
+// Both calls of single tokens (window = 0: every token is seen).
+ptq1_status attn_decode(const char *name, const void *q, int32_t q_dtype, int64_t batch, int32_t n_q_heads,
+                        const ptq1_kv_cache *cache, const int32_t *block_table, int64_t max_pages,
+                        const int32_t *seq_lens, int64_t max_len, int64_t window, int64_t sinks, float scale, void *out,
+                        void *ws, size_t ws_bytes, hipStream_t stream)
+{
+    KvBytes kb;
+    PTQ1_TRY(check_cache(cache, &kb));
+    if (batch < 0) return fail(PTQ1_ERR_SHAPE, "batch = %lld is negative", (long long)batch);
+    if (batch > kMaxGridY) return fail(PTQ1_ERR_UNSUPPORTED, "batch = %lld > %lld", (long long)batch, (long long)kMaxGridY);
+    PTQ1_TRY(check_heads(n_q_heads, cache->n_kv_heads));
+    PTQ1_TRY(check_scale(scale));
+    if (max_pages < 0 || max_pages > kMaxRows32)
+        return fail(PTQ1_ERR_SHAPE, "max_pages = %lld", (long long)max_pages);
+    if (max_len < 0 || max_len > max_pages * cache->page_size)
+        return fail(PTQ1_ERR_SHAPE, "max_len = %lld (0 to max_pages * page_size = %lld)", (long long)max_len,
+                    (long long)(max_pages * cache->page_size));
+    if (!float_type(q_dtype)) return fail(PTQ1_ERR_UNSUPPORTED, "q_dtype %d (F32, F16 or BF16)", q_dtype);
+    if (cache->dtype != PTQ1_I8 && q_dtype != PTQ1_F32 && q_dtype != cache->dtype)
+        return fail(PTQ1_ERR_UNSUPPORTED, "q_dtype %s over a %s cache (F32 or the cache's own type)", type_name(q_dtype),
+                    type_name(cache->dtype));
+    if (max_len > kMaxDecodeLen)
+        return fail(PTQ1_ERR_UNSUPPORTED, "max_len = %lld > %lld", (long long)max_len, (long long)kMaxDecodeLen);
+    if (!decode_sizes_ok(batch, n_q_heads, cache->n_kv_heads, cache->head_dim, max_len))
+        return fail(PTQ1_ERR_UNSUPPORTED, "more than %lld groups of 16 query heads of a kv head", (long long)kMaxDecodeGroups);
+    if (batch == 0) return ok();
+    const int64_t qb = batch * n_q_heads * cache->head_dim * type_bytes(q_dtype);
+    PTQ1_TRY(check_device_array(q, "q", qb, kAlign));
+    PTQ1_TRY(check_device_array(out, "out", qb, kAlign));
+    int64_t table = 0;
+    if (!mul_ok(batch, max_pages * 4, &table)) return fail(PTQ1_ERR_OVERFLOW, "block_table: size overflows");
+    PTQ1_TRY(check_device_array(block_table, "block_table", table, 4));
+    PTQ1_TRY(check_device_array(seq_lens, "seq_lens", batch * 4, 4));
+    if (window > max_len) window = max_len + 1;  // (all of them)
+    if (sinks > max_len) sinks = max_len;
+    const ptq1::DecodePlan plan = ptq1::decode_plan(batch, n_q_heads, cache->n_kv_heads, cache->head_dim,
+                                                    window > 0 ? ptq1::window_bound(max_len, window, sinks) : max_len);
+    const size_t need = round_up(plan.part_floats * 4, kWsAlign);
+    PTQ1_TRY(check_ws(ws, ws_bytes, need, name));
+    if (overlaps(out, qb, q, qb)) return fail(PTQ1_ERR_ALIAS, "out overlaps q");
+    if (overlaps_cache(out, qb, cache, kb)) return fail(PTQ1_ERR_ALIAS, "out overlaps the cache");
+    if (overlaps(out, qb, block_table, table) || overlaps(out, qb, seq_lens, batch * 4))
+        return fail(PTQ1_ERR_ALIAS, "out overlaps block_table or seq_lens");
+    const int64_t wn = static_cast<int64_t>(need);
+    if (overlaps(ws, wn, q, qb) || overlaps(ws, wn, out, qb) || overlaps_cache(ws, wn, cache, kb) ||
+        overlaps(ws, wn, block_table, table) || overlaps(ws, wn, seq_lens, batch * 4))
+        return fail(PTQ1_ERR_ALIAS, "ws overlaps an argument");
+    return hip_status(ptq1::launch_attn_decode(plan, q, q_dtype, batch, n_q_heads, *cache, block_table, max_pages,
+                                               seq_lens, max_len, static_cast<int32_t>(window),
+                                               static_cast<int32_t>(sinks), scale, out, static_cast<float *>(ws), stream),
+                      name);
+}
+
+}  // namespace
+
+extern "C" {
+
+ptq1_status ptq1_kv_write(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                          int64_t v_stride, int32_t src_dtype, int64_t n_tokens, int32_t n_q_heads,
+                          const int32_t *positions, const float *cos_sin, int64_t n_positions, int32_t rot_dim,
+                          const int64_t *slots, void *q_out, int32_t q_dtype, const ptq1_kv_cache *cache,
+                          hipStream_t stream)
+{
+    bool nothing;
+    PTQ1_TRY(check_kv_write(q, q_stride, k, k_stride, v, v_stride, src_dtype, n_tokens, n_q_heads, nullptr, nullptr,
+                            positions, cos_sin, n_positions, rot_dim, slots, q_out, q_dtype, cache, &nothing));
+    if (nothing) return ok();
     return hip_status(ptq1::launch_kv_write(q, q_stride, k, k_stride, v, v_stride, src_dtype, n_tokens, n_q_heads,
                                             positions, cos_sin, n_positions, rot_dim, slots, q_out, q_dtype, *cache,
                                             stream),
                       "ptq1_kv_write");
+}
+
+ptq1_status ptq1_kv_write_norm(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                               int64_t v_stride, int32_t src_dtype, int64_t n_tokens, int32_t n_q_heads,
+                               const float *q_gain, const float *k_gain, float eps, const int32_t *positions,
+                               const float *cos_sin, int64_t n_positions, int32_t rot_dim, const int64_t *slots,
+                               void *q_out, int32_t q_dtype, const ptq1_kv_cache *cache, hipStream_t stream)
+{
+    // (the square root of a smaller one would be that of a number below fp32's normal ones)
+    if (!(eps >= 0x1p-100f) || eps > 0x1p100f) return fail(PTQ1_ERR_SHAPE, "eps must be in [2^-100, 2^100]");
+    bool nothing;
+    PTQ1_TRY(check_kv_write(q, q_stride, k, k_stride, v, v_stride, src_dtype, n_tokens, n_q_heads,
+                            n_q_heads > 0 ? q_gain : nullptr, k_gain, positions, cos_sin, n_positions, rot_dim, slots,
+                            q_out, q_dtype, cache, &nothing));
+    if (nothing) return ok();
+    return hip_status(ptq1::launch_kv_write_norm(q, q_stride, k, k_stride, v, v_stride, src_dtype, n_tokens, n_q_heads,
+                                                 q_gain, k_gain, eps, positions, cos_sin, n_positions, rot_dim, slots,
+                                                 q_out, q_dtype, *cache, stream),
+                      "ptq1_kv_write_norm");
 }
 
 ptq1_status ptq1_kv_read(const ptq1_kv_cache *cache, const int32_t *block_table, int64_t max_pages,
@@ -1288,47 +1382,29 @@ ptq1_status ptq1_attn_decode(const void *q, int32_t q_dtype, int64_t batch, int3
                              const int32_t *seq_lens, int64_t max_len, float scale, void *out, void *ws,
                              size_t ws_bytes, hipStream_t stream)
 {
-    KvBytes kb;
-    PTQ1_TRY(check_cache(cache, &kb));
-    if (batch < 0) return fail(PTQ1_ERR_SHAPE, "batch = %lld is negative", (long long)batch);
-    if (batch > kMaxGridY) return fail(PTQ1_ERR_UNSUPPORTED, "batch = %lld > %lld", (long long)batch, (long long)kMaxGridY);
-    PTQ1_TRY(check_heads(n_q_heads, cache->n_kv_heads));
-    PTQ1_TRY(check_scale(scale));
-    if (max_pages < 0 || max_pages > kMaxRows32)
-        return fail(PTQ1_ERR_SHAPE, "max_pages = %lld", (long long)max_pages);
-    if (max_len < 0 || max_len > max_pages * cache->page_size)
-        return fail(PTQ1_ERR_SHAPE, "max_len = %lld (0 to max_pages * page_size = %lld)", (long long)max_len,
-                    (long long)(max_pages * cache->page_size));
-    if (!float_type(q_dtype)) return fail(PTQ1_ERR_UNSUPPORTED, "q_dtype %d (F32, F16 or BF16)", q_dtype);
-    if (cache->dtype != PTQ1_I8 && q_dtype != PTQ1_F32 && q_dtype != cache->dtype)
-        return fail(PTQ1_ERR_UNSUPPORTED, "q_dtype %s over a %s cache (F32 or the cache's own type)", type_name(q_dtype),
-                    type_name(cache->dtype));
-    if (max_len > kMaxDecodeLen)
-        return fail(PTQ1_ERR_UNSUPPORTED, "max_len = %lld > %lld", (long long)max_len, (long long)kMaxDecodeLen);
-    if (!decode_sizes_ok(batch, n_q_heads, cache->n_kv_heads, cache->head_dim, max_len))
-        return fail(PTQ1_ERR_UNSUPPORTED, "more than %lld groups of 16 query heads of a kv head", (long long)kMaxDecodeGroups);
-    if (batch == 0) return ok();
-    const int64_t qb = batch * n_q_heads * cache->head_dim * type_bytes(q_dtype);
-    PTQ1_TRY(check_device_array(q, "q", qb, kAlign));
-    PTQ1_TRY(check_device_array(out, "out", qb, kAlign));
-    int64_t table = 0;
-    if (!mul_ok(batch, max_pages * 4, &table)) return fail(PTQ1_ERR_OVERFLOW, "block_table: size overflows");
-    PTQ1_TRY(check_device_array(block_table, "block_table", table, 4));
-    PTQ1_TRY(check_device_array(seq_lens, "seq_lens", batch * 4, 4));
-    const ptq1::DecodePlan plan = ptq1::decode_plan(batch, n_q_heads, cache->n_kv_heads, cache->head_dim, max_len);
-    const size_t need = round_up(plan.part_floats * 4, kWsAlign);
-    PTQ1_TRY(check_ws(ws, ws_bytes, need, "ptq1_attn_decode"));
-    if (overlaps(out, qb, q, qb)) return fail(PTQ1_ERR_ALIAS, "out overlaps q");
-    if (overlaps_cache(out, qb, cache, kb)) return fail(PTQ1_ERR_ALIAS, "out overlaps the cache");
-    if (overlaps(out, qb, block_table, table) || overlaps(out, qb, seq_lens, batch * 4))
-        return fail(PTQ1_ERR_ALIAS, "out overlaps block_table or seq_lens");
-    const int64_t wn = static_cast<int64_t>(need);
-    if (overlaps(ws, wn, q, qb) || overlaps(ws, wn, out, qb) || overlaps_cache(ws, wn, cache, kb) ||
-        overlaps(ws, wn, block_table, table) || overlaps(ws, wn, seq_lens, batch * 4))
-        return fail(PTQ1_ERR_ALIAS, "ws overlaps an argument");
-    return hip_status(ptq1::launch_attn_decode(plan, q, q_dtype, batch, n_q_heads, *cache, block_table, max_pages,
-                                               seq_lens, max_len, scale, out, static_cast<float *>(ws), stream),
-                      "ptq1_attn_decode");
+    return attn_decode("ptq1_attn_decode", q, q_dtype, batch, n_q_heads, cache, block_table, max_pages, seq_lens, max_len, 0,
+                       0, scale, out, ws, ws_bytes, stream);
+}
+
+size_t ptq1_attn_decode_window_workspace_bytes(int64_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                               int64_t max_len, int64_t window, int64_t sinks)
+{
+    if (window < 1 || sinks < 0 || !decode_sizes_ok(batch, n_q_heads, n_kv_heads, head_dim, max_len)) return 0;
+    if (window > max_len) window = max_len + 1;
+    if (sinks > max_len) sinks = max_len;
+    return ptq1_attn_decode_workspace_bytes(batch, n_q_heads, n_kv_heads, head_dim,
+                                            ptq1::window_bound(max_len, window, sinks));
+}
+
+ptq1_status ptq1_attn_decode_window(const void *q, int32_t q_dtype, int64_t batch, int32_t n_q_heads,
+                                    const ptq1_kv_cache *cache, const int32_t *block_table, int64_t max_pages,
+                                    const int32_t *seq_lens, int64_t max_len, int64_t window, int64_t sinks, float scale,
+                                    void *out, void *ws, size_t ws_bytes, hipStream_t stream)
+{
+    if (window < 1) return fail(PTQ1_ERR_SHAPE, "window = %lld (1 token or more)", (long long)window);
+    if (sinks < 0) return fail(PTQ1_ERR_SHAPE, "sinks = %lld is negative", (long long)sinks);
+    return attn_decode("ptq1_attn_decode_window", q, q_dtype, batch, n_q_heads, cache, block_table, max_pages, seq_lens,
+                       max_len, window, sinks, scale, out, ws, ws_bytes, stream);
 }
 
 size_t ptq1_attn_prompt_workspace_bytes(int64_t batch, int64_t n_q_rows, int64_t max_k, int32_t n_q_heads,

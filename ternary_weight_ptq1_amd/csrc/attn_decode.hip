@@ -1,5 +1,5 @@
 // attn_decode.hip -- attention of one new token per sequence over the paged
-// cache (ptq1_attn_decode).
+// cache (ptq1_attn_decode), or over a window of it (ptq1_attn_decode_window).
 //
 //   out = sum_j p_j V[j] / sum_j p_j,  p_j = exp2(t_j - M),
 //   t_j = scale log2(e) (q . K[j]),    M = max_j t_j
@@ -67,6 +67,7 @@ struct DecodeArgs {
     float scale;
     void *out;
     float *part_rows, *part_ml;
+    int32_t window, sinks;  // of the windowed calls
 };
 
 __device__ __forceinline__ int wave_total(int v)
@@ -95,10 +96,21 @@ struct LaneLens {
     }
 };
 
+// Tokens of a sequence of `len` that are read (of one that is refused: what it
+// is refused for).
+template <bool WIN>
+__device__ __forceinline__ int tokens_read(const DecodeArgs &a, int len)
+{
+    if constexpr (WIN)
+        if (len > 0 && len <= a.max_len) return window_of(len, a.window, a.sinks).tokens;
+    return len;
+}
+
 // Steps of one workgroup's piece of a sequence.
+template <bool WIN>
 __device__ __forceinline__ int piece_steps(const DecodeArgs &a, const LaneLens &lens)
 {
-    const int total = lens.sum(a, a.batch, [&](int n) { return decode_steps(n, a.max_len); });
+    const int total = lens.sum(a, a.batch, [&](int n) { return decode_steps(tokens_read<WIN>(a, n), a.max_len); });
     return steps_per_piece(total, wanted_pieces(a.batch, a.shares));
 }
 
@@ -169,7 +181,13 @@ __device__ __forceinline__ float pow2(int e) { return __builtin_bit_cast(float, 
 // product exceeds.  Converting both to bf16 and taking the steps' whole range
 // there spent 1300 vector instructions on 64 tokens instead of about 560: 93
 // us for 131071 tokens of 8 heads of 128 where 60 are enough now.
-template <typename C, typename QT, int D, int NQ, int NP>
+//
+// WIN: a sliding window and first tokens that stay visible.  The tokens that
+// are read are numbered without the gap between them (WindowTokens): all of
+// the above then works on these numbers, and a token's real number is needed
+// for its page and its place in it alone.  What is read beside the tokens that
+// are seen (the rest of two runs of 16) is masked like what lies past the end.
+template <typename C, typename QT, int D, int NQ, int NP, bool WIN>
 __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(DecodeArgs a)
 {
     constexpr bool I8 = std::is_same<C, int8_t>::value;
@@ -204,10 +222,10 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
     int per = kMaxSteps, b = static_cast<int>(piece), first = 0, len;
     if (a.cut) {
         const LaneLens lens(a);
-        per = piece_steps(a, lens);
+        per = piece_steps<WIN>(a, lens);
         int64_t seq, tile;
         int mine = 0;
-        const auto pieces = [&](int n) { return pieces_of(decode_steps(n, a.max_len), per); };
+        const auto pieces = [&](int n) { return pieces_of(decode_steps(tokens_read<WIN>(a, n), a.max_len), per); };
         const auto of_lane = [&](int64_t) { return pieces(mine = lens.first); };
         const auto of_any = [&](int64_t i) { return pieces(a.lens[i]); };
         if (!(a.batch <= 64 ? find_tile<false>(piece, a.batch, of_lane, seq, tile)
@@ -219,8 +237,10 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
     } else
         len = a.lens[b];
     const bool bad_len = len < 0 || len > a.max_len;
-    const bool whole = decode_steps(len, a.max_len) <= per;
-    const PieceTokens tokens = piece_tokens(first, per, len);
+    const WindowTokens win = WIN ? window_of(len, a.window, a.sinks) : WindowTokens{};
+    const int read = tokens_read<WIN>(a, len);
+    const bool whole = decode_steps(read, a.max_len) <= per;
+    const PieceTokens tokens = piece_tokens(first, per, read);
     const int begin = tokens.begin, end = bad_len ? begin : tokens.end;
 
     // ---- the queries' own loads, first of all: of column = head, dimensions
@@ -243,10 +263,20 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
     // looked up a step ahead: K's run is that of its row, V's that of its
     // slots.  A page that does not exist: page 0 is read, and the rows end NaN.
     const int last = end - 1, last_run = last & ~(RUN - 1);
+    const auto real = [&](int tok) { return WIN && tok >= win.sunk ? tok + win.gap : tok; };
+    // (WIN: without branches; of those that && makes here, the compiler lost the
+    // selected value)
+    const uint32_t hole_size = win.hole_end > win.hole ? win.hole_end - win.hole : 0;
+    const auto hidden = [&](bool tail, int tok) -> bool {
+        if constexpr (WIN)
+            return tail & ((tok >= end) | (static_cast<uint32_t>(tok - win.hole) < hole_size));
+        else
+            return tail && tok >= end;
+    };
     const int32_t *table = a.table + static_cast<int64_t>(b) * a.max_pages;
     bool bad = bad_len;
     auto page_of = [&](int tok) {
-        const int32_t pg = table[(tok < last ? tok : last) >> page_shift];
+        const int32_t pg = table[real(tok < last ? tok : last) >> page_shift];
         return pg;
     };
     auto checked = [&](int32_t pg) {
@@ -260,7 +290,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
         for (int t = 0; t < NT; ++t) {
             int tok = base + RUN * (col >> 2) + 4 * t + (col & 3);
             tok = tok < last ? tok : last;
-            const int64_t cell = ((static_cast<int64_t>(pg) * a.hkv + kh) << page_shift) + (tok & page_mask);
+            const int64_t cell = ((static_cast<int64_t>(pg) * a.hkv + kh) << page_shift) + (real(tok) & page_mask);
             const char *src = kp + cell * (D * static_cast<int64_t>(sizeof(C))) + 16 * grp;
 #pragma unroll
             for (int i = 0; i < LPT; ++i) r[t * LPT + i] = *reinterpret_cast<const at_u32x4 *>(src + 64 * i);
@@ -268,7 +298,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
     };
     auto run_of = [&](int base) {
         const int tok = base + RUN * grp;
-        return tok < last_run ? tok : last_run;
+        return real(tok < last_run ? tok : last_run);
     };
     auto load_v = [&](int base, int32_t pg, at_u32x4 (&r)[NL]) {
         const int64_t pgh = static_cast<int64_t>(pg) * a.hkv + kh;
@@ -453,14 +483,15 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
             kpage = page_of(next + kDecWaves * TS + RUN * (col >> 2));
             vpage = page_of(next + kDecWaves * TS + RUN * grp);
         }
-        const bool tail = base + TS > end;
+        bool tail = base + TS > end;  // something is masked
+        if constexpr (WIN) tail |= (base < win.hole_end) & (base + TS > win.hole);
         float top = -__builtin_inff();
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if constexpr (!I8) s[t][i] *= c;
-                if (tail && base + RUN * grp + 4 * t + i >= end) s[t][i] = -__builtin_inff();
+                if (hidden(tail, base + RUN * grp + 4 * t + i)) s[t][i] = -__builtin_inff();
                 top = fmaxf(top, s[t][i]);
             }
         top = lane_pair_max<32>(lane_pair_max<16>(top));
@@ -489,7 +520,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
             for (int i = 0; i < 4; ++i) {
                 float e = __builtin_amdgcn_exp2f(s[t][i] - ms) * kLift;
                 l += e;
-                if constexpr (I8) e *= tail && base + RUN * grp + 4 * t + i >= end ? 0.0f : vs[t][i];
+                if constexpr (I8) e *= hidden(tail, base + RUN * grp + 4 * t + i) ? 0.0f : vs[t][i];
                 p[4 * t + i] = e;
             }
         if constexpr (I8) {
@@ -518,9 +549,15 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const int left = end - (base + RUN * grp + PER * w);
-                    const uint32_t keep = left >= PER ? 0xffffffffu
-                                          : left <= 0 ? 0u
-                                                      : (1u << (8 * static_cast<int>(sizeof(C)) * left)) - 1u;
+                    uint32_t keep = left >= PER ? 0xffffffffu
+                                    : left <= 0 ? 0u
+                                                : (1u << (8 * static_cast<int>(sizeof(C)) * left)) - 1u;
+                    if constexpr (WIN) {
+                        constexpr uint32_t kOne = (1ull << (8 * sizeof(C))) - 1;
+#pragma unroll
+                        for (int t = 0; t < PER; ++t)
+                            keep &= hidden(true, base + RUN * grp + PER * w + t) ? ~(kOne << (8 * static_cast<int>(sizeof(C)) * t)) : ~0u;
+                    }
                     vr[i][w] &= keep;
                 }
             }
@@ -613,7 +650,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(D
 // Joins the pieces of a sequence that was cut: one workgroup
 // per (query head, sequence), its D / 4 lanes wide groups taking every n-th
 // piece, then a sum over the groups in LDS.
-template <typename QT, int D>
+template <typename QT, int D, bool WIN>
 __global__ void __launch_bounds__(256) k_attn_join(DecodeArgs a)
 {
     constexpr int LPR = D / 4, G = 256 / LPR;
@@ -622,8 +659,8 @@ __global__ void __launch_bounds__(256) k_attn_join(DecodeArgs a)
     __shared__ at_f32x4 sums[G][LPR];
     const int64_t b = blockIdx.y, h = blockIdx.x;
     const LaneLens lens(a);
-    const int per = piece_steps(a, lens);
-    const auto pieces = [&](int len) { return pieces_of(decode_steps(len, a.max_len), per); };
+    const int per = piece_steps<WIN>(a, lens);
+    const auto pieces = [&](int len) { return pieces_of(decode_steps(tokens_read<WIN>(a, len), a.max_len), per); };
     const int n = pieces(b < 64 ? __builtin_amdgcn_readlane(lens.first, static_cast<int>(b)) : a.lens[b]);
     if (n == 1) return;
     const int64_t before = lens.sum(a, b, pieces);
@@ -660,11 +697,11 @@ __global__ void __launch_bounds__(256) k_attn_join(DecodeArgs a)
     }
 }
 
-template <typename C, typename QT, int D, int NQ, int NP>
+template <bool WIN, typename C, typename QT, int D, int NQ, int NP>
 hipError_t decode_launch(const DecodePlan &p, const DecodeArgs &a, int64_t batch, hipStream_t s)
 {
     static std::atomic<uint64_t> lds_done{0};
-    const auto kernel = k_attn_decode<C, QT, D, NQ, NP>;
+    const auto kernel = k_attn_decode<C, QT, D, NQ, NP, WIN>;
     // the waves' rows at the end; int8: the queries' digits before
     constexpr int kMaxLds = kDecWaves * kDecHeads * (D + 4) * 4;
     constexpr int kDigits = std::is_same<C, int8_t>::value ? D / 64 * NQ * 1024 : 0;
@@ -677,17 +714,31 @@ hipError_t decode_launch(const DecodePlan &p, const DecodeArgs &a, int64_t batch
     hipLaunchKernelGGL(kernel,
                        dim3(static_cast<uint32_t>(p.pieces * a.hkv * a.hblocks)), dim3(kDecThreads), lds, s, a);
     if (p.join)
-        hipLaunchKernelGGL((k_attn_join<QT, D>), dim3(static_cast<uint32_t>(a.hq), static_cast<uint32_t>(batch)),
+        hipLaunchKernelGGL((k_attn_join<QT, D, WIN>), dim3(static_cast<uint32_t>(a.hq), static_cast<uint32_t>(batch)),
                            dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
-template <typename C, typename QT, int NQ, int NP>
+template <bool WIN, typename C, typename QT, int NQ, int NP>
 hipError_t decode_d(const DecodePlan &p, const DecodeArgs &a, int64_t batch, int d, hipStream_t s)
 {
-    return d == 64 ? decode_launch<C, QT, 64, NQ, NP>(p, a, batch, s)
-                   : d == 128 ? decode_launch<C, QT, 128, NQ, NP>(p, a, batch, s)
-                              : decode_launch<C, QT, 256, NQ, NP>(p, a, batch, s);
+    return d == 64 ? decode_launch<WIN, C, QT, 64, NQ, NP>(p, a, batch, s)
+                   : d == 128 ? decode_launch<WIN, C, QT, 128, NQ, NP>(p, a, batch, s)
+                              : decode_launch<WIN, C, QT, 256, NQ, NP>(p, a, batch, s);
+}
+
+template <bool WIN>
+hipError_t decode_types(const DecodePlan &p, const DecodeArgs &a, int q_type, int cache_type, int d, hipStream_t s)
+{
+    if (cache_type == PTQ1_BF16)
+        return q_type == PTQ1_F32 ? decode_d<WIN, __bf16, float, 3, 3>(p, a, a.batch, d, s)
+                                  : decode_d<WIN, __bf16, __bf16, 1, 2>(p, a, a.batch, d, s);
+    if (cache_type == PTQ1_F16)
+        return q_type == PTQ1_F32 ? decode_d<WIN, _Float16, float, 3, 2>(p, a, a.batch, d, s)
+                                  : decode_d<WIN, _Float16, _Float16, 1, 2>(p, a, a.batch, d, s);
+    return q_type == PTQ1_F32 ? decode_d<WIN, int8_t, float, 4, 3>(p, a, a.batch, d, s)
+           : q_type == PTQ1_F16 ? decode_d<WIN, int8_t, _Float16, 3, 2>(p, a, a.batch, d, s)
+                                : decode_d<WIN, int8_t, __bf16, 3, 2>(p, a, a.batch, d, s);
 }
 
 }  // namespace
@@ -717,22 +768,16 @@ DecodePlan decode_plan(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_
 
 hipError_t launch_attn_decode(const DecodePlan &p, const void *q, int q_type, int64_t batch, int32_t hq,
                               const ptq1_kv_cache &c, const int32_t *table, int64_t max_pages, const int32_t *lens,
-                              int64_t max_len, float scale, void *out, float *part, hipStream_t s)
+                              int64_t max_len, int32_t window, int32_t sinks, float scale, void *out, float *part,
+                              hipStream_t s)
 {
     const int32_t group = hq / c.n_kv_heads;
     const DecodeArgs a{q, hq, c.n_kv_heads, (group + kDecHeads - 1) / kDecHeads, c.k_pages, c.v_pages, c.k_steps,
                        c.v_steps, c.n_pages, __builtin_ctz(static_cast<unsigned>(c.page_size)), table, max_pages, lens,
-                       batch, max_len, p.shares, p.join, c.dtype == PTQ1_I8, scale, out, part, part + p.rows_floats};
-    const int d = c.head_dim;
-    if (c.dtype == PTQ1_BF16)
-        return q_type == PTQ1_F32 ? decode_d<__bf16, float, 3, 3>(p, a, batch, d, s)
-                                  : decode_d<__bf16, __bf16, 1, 2>(p, a, batch, d, s);
-    if (c.dtype == PTQ1_F16)
-        return q_type == PTQ1_F32 ? decode_d<_Float16, float, 3, 2>(p, a, batch, d, s)
-                                  : decode_d<_Float16, _Float16, 1, 2>(p, a, batch, d, s);
-    return q_type == PTQ1_F32 ? decode_d<int8_t, float, 4, 3>(p, a, batch, d, s)
-           : q_type == PTQ1_F16 ? decode_d<int8_t, _Float16, 3, 2>(p, a, batch, d, s)
-                                : decode_d<int8_t, __bf16, 3, 2>(p, a, batch, d, s);
+                       batch, max_len, p.shares, p.join, c.dtype == PTQ1_I8, scale, out, part, part + p.rows_floats,
+                       window, sinks};
+    return window > 0 ? decode_types<true>(p, a, q_type, c.dtype, c.head_dim, s)
+                      : decode_types<false>(p, a, q_type, c.dtype, c.head_dim, s);
 }
 
 }  // namespace ptq1

@@ -148,6 +148,10 @@ hipError_t launch_kv_write(const void *q, int64_t qs, const void *k, int64_t ks,
                            int64_t tokens, int32_t hq, const int32_t *positions, const float *cos_sin,
                            int64_t n_positions, int32_t rot, const int64_t *slots, void *q_out, int q_type,
                            const ptq1_kv_cache &c, hipStream_t s);
+hipError_t launch_kv_write_norm(const void *q, int64_t qs, const void *k, int64_t ks, const void *v, int64_t vs, int src,
+                                int64_t tokens, int32_t hq, const float *q_gain, const float *k_gain, float eps,
+                                const int32_t *positions, const float *cos_sin, int64_t n_positions, int32_t rot,
+                                const int64_t *slots, void *q_out, int q_type, const ptq1_kv_cache &c, hipStream_t s);
 hipError_t launch_kv_read(const ptq1_kv_cache &c, const int32_t *table, int64_t max_pages, const int32_t *cu,
                           int64_t batch, int64_t rows, void *k_out, void *v_out, int out_type, hipStream_t s);
 
@@ -156,7 +160,8 @@ hipError_t launch_kv_read(const ptq1_kv_cache &c, const int32_t *table, int64_t 
 // (`shares` workgroups for one kv head); `pieces` bounds their number.  part:
 // the pieces' unnormalised rows [piece][hq][d] (int8 caches: lower by a power
 // of two), then their (reference, sum) pairs; unused without join (no sequence
-// can be cut).
+// can be cut).  window > 0: the windowed call (the plan is made for the tokens
+// that it reads, window_bound).
 struct DecodePlan {
     int32_t shares = 1;
     int64_t pieces = 1;
@@ -166,7 +171,8 @@ struct DecodePlan {
 DecodePlan decode_plan(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_t max_len);
 hipError_t launch_attn_decode(const DecodePlan &p, const void *q, int q_type, int64_t batch, int32_t hq,
                               const ptq1_kv_cache &c, const int32_t *table, int64_t max_pages, const int32_t *lens,
-                              int64_t max_len, float scale, void *out, float *part, hipStream_t s);
+                              int64_t max_len, int32_t window, int32_t sinks, float scale, void *out, float *part,
+                              hipStream_t s);
 
 // Prompt attention.
 struct PromptArgs {

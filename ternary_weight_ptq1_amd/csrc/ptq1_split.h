@@ -33,6 +33,33 @@ constexpr int steps_per_piece(int total, int64_t wanted)
     return per < kMaxSteps ? per : kMaxSteps;
 }
 
+// What the windowed calls read of a sequence of `len` tokens, of which the last
+// `window` and the first `sinks` are seen: the runs of 16 tokens that hold one
+// of them (a page holds whole runs), numbered without the gap between them.
+struct WindowTokens {
+    int tokens = 0;           // so many
+    int sunk = 0, gap = 0;    // from number `sunk` on a token's real number is larger by `gap` (both multiples of 16)
+    int hole = 0, hole_end = 0;  // the numbers in [hole, hole_end) are not seen
+};
+constexpr WindowTokens window_of(int len, int window, int sinks)
+{
+    WindowTokens w;
+    const int lo = len > window ? len - window : 0;  // the window's first token
+    const int kept = sinks < lo ? sinks : lo;
+    const int up = (kept + 15) & ~15, down = lo & ~15;
+    w.sunk = up;
+    w.gap = down > up ? down - up : 0;
+    w.hole = kept;
+    w.hole_end = lo - w.gap;
+    w.tokens = len - w.gap;
+    return w;
+}
+// No sequence has more numbers than this (at most max_len).
+constexpr int64_t window_bound(int64_t max_len, int64_t window, int64_t sinks)
+{
+    return max_len < window + sinks + 30 ? max_len : window + sinks + 30;
+}
+
 constexpr int pieces_of(int steps, int per) { return (steps + per - 1) / per; }
 
 // The tokens begin .. end of a sequence's `first`-th piece.
