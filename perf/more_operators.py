@@ -365,7 +365,8 @@ def run(state):
             return q, s["cache"]["k"], s["cache"]["v"]
         if op == "chunk":
             return P.ptq1_attn_chunk(s["q"], s["kv"], s["table"], s["cu"], s["seq_lens"], window=case["window"],
-                                     sinks=case["sinks"], max_q=case["new"], max_len=case["new"] + case["context"])
+                                     sinks=case["sinks"], max_q=case["new"],
+                                     max_len=min(case["new"] + case["context"], s["table"].shape[1] * case["page"]))
         return P.ptq1_attn_decode_window(s["q"], s["kv"], s["table"], s["seq_lens"], window=case["window"],
                                          sinks=case["sinks"], max_len=case["high"])
     if op == "norm_write":
