@@ -539,6 +539,55 @@ ptq1_status ptq1_attn_decode_window(const void *q, int32_t q_dtype, int64_t batc
                                     const int32_t *seq_lens, int64_t max_len, int64_t window, int64_t sinks, float scale,
                                     void *out, void *ws, size_t ws_bytes, hipStream_t stream);
 
+/* Attention of the last tokens of every sequence over the paged cache that
+ * holds them already (ptq1_kv_write first): proposed tokens to be verified,
+ * prompts that arrive in pieces, and batches of both.  Sequence b's queries are
+ * rows cu_q[b] .. cu_q[b + 1] of q; with m of them and n = seq_lens[b] tokens,
+ * query i stands at position p = n - m + i and sees the tokens
+ *   j <= p  with  window = 0  or  j > p - window  or  j < sinks
+ * (window counts the query's own token; sinks: first tokens that stay visible).
+ * A query at a negative position sees none and gets zeros.
+ *   q    [n_q_rows][n_q_heads][head_dim] (heads contiguous, rows q_stride
+ *        elements apart, 16-byte aligned, a multiple of 16 bytes), q_dtype the
+ *        cache's own 16-bit type, F16 or BF16 over an int8 cache;
+ *   out  [n_q_rows][n_q_heads][head_dim] contiguous, of q's type; must not
+ *        overlap q.  Rows that belong to no sequence are left as they were.
+ *   cu_q, seq_lens, block_table  int32, device: [batch + 1] (not negative, not
+ *        decreasing), [batch], [batch][max_pages].
+ *   max_q, max_len  bounds on the sequences' queries and tokens that the caller
+ *        knows (max_len at most max_pages * page_size); the work is laid out for
+ *        them.  A sequence that exceeds one, or whose length is negative, gets
+ *        NaN rows, as does one whose rows lie outside [0, n_q_rows) (those
+ *        inside).  A row that sees a token whose page is outside [0, n_pages) is
+ *        NaN.
+ *   scale  positive, 2^126 at most.
+ * What a query does not see does not enter its row, whatever it holds, and pages
+ * that hold nothing that a query of their sequence sees are not read: their
+ * entries of block_table may be anything.
+ * bf16 or fp16 matrix cores, fp32 scores, maxima, sums and accumulators.  Over
+ * 16-bit caches the weights enter the second product rounded to their type
+ * (fp16: to 11 bits, down to 2^-32 of the row's largest), and their sum, in fp32, is that
+ * of the rounded ones, as in ptq1_attn_prompt.  Over int8 caches the codes enter
+ * exactly, as fp16, the queries as fp16 times a power of two of their head (bf16:
+ * exact down to 2^-21 of the head's largest magnitude, then down to 2^-39 of
+ * it), and weight times step rounded to fp16 (11 bits, down to 2^-28 of the
+ * row's largest).  A NaN or an infinity in a query, or in a key or value that it
+ * sees, makes the entries of out that it enters NaN or infinite.
+ * Where the tiles of query rows alone would not fill the GPU, the keys are cut
+ * into pieces that run side by side and are joined by a second launch, in a
+ * fixed order, by the lengths on the device.
+ * Errors: NULL, SHAPE, ALIGN, ALIAS, OVERFLOW, WORKSPACE, UNSUPPORTED (types,
+ * head_dim, page_size, max_len > 2^22, more than 2^31 - 1025 rows of one kv head
+ * or 2^23 tiles of 128 query rows). */
+size_t ptq1_attn_chunk_workspace_bytes(int64_t batch, int64_t n_q_rows, int64_t max_q, int32_t n_q_heads,
+                                       int32_t n_kv_heads, int32_t head_dim, int64_t max_len, int64_t window,
+                                       int64_t sinks);
+ptq1_status ptq1_attn_chunk(const void *q, int64_t q_stride, int32_t q_dtype, const int32_t *cu_q, int64_t batch,
+                            int64_t n_q_rows, int64_t max_q, int32_t n_q_heads, const ptq1_kv_cache *cache,
+                            const int32_t *block_table, int64_t max_pages, const int32_t *seq_lens, int64_t max_len,
+                            int64_t window, int64_t sinks, float scale, void *out, void *ws, size_t ws_bytes,
+                            hipStream_t stream);
+
 /* Attention over whole prompts, packed without padding: sequence b's queries
  * are rows cu_q[b] .. cu_q[b + 1] of q [n_q_rows][n_q_heads][head_dim], its
  * keys and values rows cu_k[b] .. cu_k[b + 1] of k and v

@@ -94,6 +94,9 @@ _SIGS = {
     "ptq1_attn_decode_window_workspace_bytes": ([i64, C.c_int32, C.c_int32, C.c_int32, i64, i64, i64], sz),
     "ptq1_attn_decode_window": ([p, C.c_int32, i64, C.c_int32, p, p, i64, p, i64, i64, i64, C.c_float, p, p, sz, p],
                                 C.c_int),
+    "ptq1_attn_chunk_workspace_bytes": ([i64, i64, i64, C.c_int32, C.c_int32, C.c_int32, i64, i64, i64], sz),
+    "ptq1_attn_chunk": ([p, i64, C.c_int32, p, i64, i64, i64, C.c_int32, p, p, i64, p, i64, i64, i64, C.c_float, p, p, sz,
+                         p], C.c_int),
     "ptq1_attn_prompt_workspace_bytes": ([i64, i64, i64, C.c_int32, C.c_int32, C.c_int32], sz),
     "ptq1_attn_prompt": ([p, i64, p, i64, p, i64, C.c_int32, p, p, i64, i64, i64, i64, i64, C.c_int32, C.c_int32,
                           C.c_int32, C.c_int32, C.c_float, p, p, sz, p], C.c_int),
@@ -900,6 +903,61 @@ def ptq1_attn_decode_window(q: torch.Tensor, cache: KvCache, block_table: torch.
     return _attn_decode(q, cache, block_table, seq_lens, scale, max_len, out, ws, stream, (window, sinks))
 
 
+def ptq1_attn_chunk(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, cu_q: torch.Tensor,
+                    seq_lens: torch.Tensor, window: int = 0, sinks: int = 0, scale: float | None = None,
+                    max_q: int | None = None, max_len: int | None = None, out: torch.Tensor | None = None,
+                    ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of the last tokens of every sequence over the cache that holds them already (ptq1_kv_write first): rows
+    cu_q[b] .. cu_q[b + 1] (int32 [batch + 1]) of q [n_q_rows, n_q_heads, head_dim] (the cache's own 16-bit type, fp16 or
+    bf16 over an int8 cache; rows may lie apart) are the last of sequence b's seq_lens[b] (int32) tokens, whose pages are
+    block_table[b] (int32 [batch, max_pages]).  Causal; window > 0: over the last `window` tokens (the query's own among
+    them) and the first `sinks` alone; pages that no query sees are not read.  scale: 1 / sqrt(head_dim) by default;
+    max_q, max_len: bounds on the sequences' queries and tokens (all rows, the table's by default).  ws: optional scratch
+    of at least workspace_bytes("attn_chunk", batch, n_q_rows, max_q, n_q_heads, n_kv_heads, head_dim, max_len, window,
+    sinks) bytes."""
+    kv = _kv(cache)
+    dv = kv.device
+    if _elsewhere(dv):
+        with torch.cuda.device(dv):
+            return ptq1_attn_chunk(q, cache, block_table, cu_q, seq_lens, window, sinks, scale, max_q, max_len, out, ws,
+                                   stream)
+    if _beside(dv, stream):
+        return _under(stream, dv, out is None, ptq1_attn_chunk, q, cache, block_table, cu_q, seq_lens, window, sinks, scale,
+                      max_q, max_len, out, ws)
+    rows, hq, d, qs = _rows3(q, "q", _SIXTEEN, dv)
+    if d != kv.head_dim:
+        raise ValueError(f"q must be [n_q_rows, n_q_heads, {kv.head_dim}]")
+    _dev(cu_q, "cu_q", torch.int32, device=dv)
+    batch = cu_q.numel() - 1
+    if batch < 0:
+        raise ValueError("cu_q must hold batch + 1 offsets")
+    max_pages = _table(block_table, batch, dv)
+    if not _plain(seq_lens, torch.int32, batch, dv):
+        _dev(seq_lens, "seq_lens", torch.int32, numel=batch, device=dv)
+    if max_q is None:
+        max_q = rows
+    if max_len is None:
+        max_len = max_pages * kv.page_size
+    handle = _current_handle(dv)
+    wsb = lib().ptq1_attn_chunk_workspace_bytes(batch, rows, max_q, hq, kv.n_kv_heads, d, max_len, window, sinks)
+    if ws is None:
+        if wsb:
+            ws = torch.empty_strided((wsb,), (1,), dtype=torch.uint8, device=dv)
+    else:
+        ws, wsb = _ws(wsb, dv, ws)
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _dev(out, "out", q.dtype, numel=rows * hq * d, device=dv)
+    status = lib().ptq1_attn_chunk(q.data_ptr(), qs, _DTYPES[q.dtype], cu_q.data_ptr(), batch, rows, max_q, hq, kv._ref,
+                                   block_table.data_ptr(), max_pages, seq_lens.data_ptr(), max_len, window, sinks,
+                                   d ** -0.5 if scale is None else scale, out.data_ptr(),
+                                   0 if ws is None else ws.data_ptr(), wsb, handle)
+    if status:
+        _check("ptq1_attn_chunk", status)
+    return out
+
+
 def ptq1_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
                      max_q: int | None = None, max_k: int | None = None, causal: bool = True,
                      scale: float | None = None, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
@@ -966,6 +1024,7 @@ def workspace_bytes(kind: str, *shape) -> int:
           "pq2_matvec": "pq2_matvec_workspace_bytes", "pq2_gemm": "pq2_gemm_workspace_bytes",
           "attn_decode": "ptq1_attn_decode_workspace_bytes",
           "attn_decode_window": "ptq1_attn_decode_window_workspace_bytes",
+          "attn_chunk": "ptq1_attn_chunk_workspace_bytes",
           "attn_prompt": "ptq1_attn_prompt_workspace_bytes"}[kind]
     return int(getattr(lib(), fn)(*shape))
 

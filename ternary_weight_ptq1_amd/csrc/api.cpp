@@ -18,6 +18,7 @@
 
 #include "../../include/ptq1.h"
 #include "ptq1_geometry.h"
+#include "ptq1_chunk.h"
 #include "ptq1_launch.h"
 #include "ptq1_split.h"
 
@@ -1178,6 +1179,34 @@ ptq1_status check_scale(float scale)
     return PTQ1_OK;
 }
 
+ptq1_status check_lengths(int64_t max_pages, int64_t max_len, int32_t page_size)
+{
+    if (max_pages < 0 || max_pages > kMaxRows32)
+        return fail(PTQ1_ERR_SHAPE, "max_pages = %lld", (long long)max_pages);
+    if (max_len < 0 || max_len > max_pages * page_size)
+        return fail(PTQ1_ERR_SHAPE, "max_len = %lld (0 to max_pages * page_size = %lld)", (long long)max_len,
+                    (long long)(max_pages * page_size));
+    return ok();
+}
+
+// Rows and tiles of the chunk attention, with a piece more for each of 512
+// workgroups where tiles are cut.
+bool chunk_sizes_ok(int64_t batch, int64_t q_rows, int32_t hq, int32_t hkv)
+{
+    if (batch < 0 || batch > kMaxRows32 || hkv < 1 || hkv > 1024 || hq < 1 || hq > kMaxHeads) return false;
+    const int64_t group = hq / hkv;
+    return q_rows >= 0 && q_rows <= kMaxRows32 && q_rows * group <= kMaxRows32 - 1024 &&
+           (q_rows * group / ptq1::kChunkRows + batch) * hkv < kMaxBlocks256 / 2;
+}
+
+// Bounds that no sequence exceeds, brought to what can matter (window 0: one that no sequence fills).
+void clip_chunk(int64_t q_rows, int64_t max_len, int64_t *max_q, int64_t *window, int64_t *sinks)
+{
+    if (*max_q > q_rows) *max_q = q_rows;
+    if (*window == 0 || *window > max_len) *window = max_len + 1;
+    if (*sinks > max_len) *sinks = max_len;
+}
+
 bool decode_sizes_ok(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_t max_len)
 {
     return batch >= 0 && batch <= kMaxGridY && hkv >= 1 && hkv <= 1024 && hq >= 1 && hq <= kMaxHeads && hq % hkv == 0 &&
@@ -1257,11 +1286,7 @@ ptq1_status attn_decode(const char *name, const void *q, int32_t q_dtype, int64_
     if (batch > kMaxGridY) return fail(PTQ1_ERR_UNSUPPORTED, "batch = %lld > %lld", (long long)batch, (long long)kMaxGridY);
     PTQ1_TRY(check_heads(n_q_heads, cache->n_kv_heads));
     PTQ1_TRY(check_scale(scale));
-    if (max_pages < 0 || max_pages > kMaxRows32)
-        return fail(PTQ1_ERR_SHAPE, "max_pages = %lld", (long long)max_pages);
-    if (max_len < 0 || max_len > max_pages * cache->page_size)
-        return fail(PTQ1_ERR_SHAPE, "max_len = %lld (0 to max_pages * page_size = %lld)", (long long)max_len,
-                    (long long)(max_pages * cache->page_size));
+    PTQ1_TRY(check_lengths(max_pages, max_len, cache->page_size));
     if (!float_type(q_dtype)) return fail(PTQ1_ERR_UNSUPPORTED, "q_dtype %d (F32, F16 or BF16)", q_dtype);
     if (cache->dtype != PTQ1_I8 && q_dtype != PTQ1_F32 && q_dtype != cache->dtype)
         return fail(PTQ1_ERR_UNSUPPORTED, "q_dtype %s over a %s cache (F32 or the cache's own type)", type_name(q_dtype),
@@ -1405,6 +1430,78 @@ ptq1_status ptq1_attn_decode_window(const void *q, int32_t q_dtype, int64_t batc
     if (sinks < 0) return fail(PTQ1_ERR_SHAPE, "sinks = %lld is negative", (long long)sinks);
     return attn_decode("ptq1_attn_decode_window", q, q_dtype, batch, n_q_heads, cache, block_table, max_pages, seq_lens,
                        max_len, window, sinks, scale, out, ws, ws_bytes, stream);
+}
+
+size_t ptq1_attn_chunk_workspace_bytes(int64_t batch, int64_t n_q_rows, int64_t max_q, int32_t n_q_heads,
+                                       int32_t n_kv_heads, int32_t head_dim, int64_t max_len, int64_t window,
+                                       int64_t sinks)
+{
+    if (!chunk_sizes_ok(batch, n_q_rows, n_q_heads, n_kv_heads) || n_q_heads % n_kv_heads != 0 ||
+        (head_dim != 64 && head_dim != 128 && head_dim != 256) || max_q < 0 || max_len < 0 || max_len > kMaxDecodeLen ||
+        window < 0 || sinks < 0)
+        return 0;
+    clip_chunk(n_q_rows, max_len, &max_q, &window, &sinks);
+    return round_up(ptq1::chunk_plan(batch, n_q_rows, max_q, n_q_heads, n_kv_heads, head_dim, max_len, window, sinks).part_floats * 4,
+                    kWsAlign);
+}
+
+ptq1_status ptq1_attn_chunk(const void *q, int64_t q_stride, int32_t q_dtype, const int32_t *cu_q, int64_t batch,
+                            int64_t n_q_rows, int64_t max_q, int32_t n_q_heads, const ptq1_kv_cache *cache,
+                            const int32_t *block_table, int64_t max_pages, const int32_t *seq_lens, int64_t max_len,
+                            int64_t window, int64_t sinks, float scale, void *out, void *ws, size_t ws_bytes,
+                            hipStream_t stream)
+{
+    KvBytes kb;
+    PTQ1_TRY(check_cache(cache, &kb));
+    if (batch < 0) return fail(PTQ1_ERR_SHAPE, "batch = %lld is negative", (long long)batch);
+    if (n_q_rows < 0) return fail(PTQ1_ERR_SHAPE, "n_q_rows = %lld is negative", (long long)n_q_rows);
+    if (max_q < 0) return fail(PTQ1_ERR_SHAPE, "max_q = %lld is negative", (long long)max_q);
+    PTQ1_TRY(check_heads(n_q_heads, cache->n_kv_heads));
+    PTQ1_TRY(check_scale(scale));
+    PTQ1_TRY(check_lengths(max_pages, max_len, cache->page_size));
+    if (window < 0) return fail(PTQ1_ERR_SHAPE, "window = %lld is negative", (long long)window);
+    if (sinks < 0) return fail(PTQ1_ERR_SHAPE, "sinks = %lld is negative", (long long)sinks);
+    if (q_dtype != PTQ1_F16 && q_dtype != PTQ1_BF16)
+        return fail(PTQ1_ERR_UNSUPPORTED, "q_dtype %d (F16 or BF16)", q_dtype);
+    if (cache->dtype != PTQ1_I8 && q_dtype != cache->dtype)
+        return fail(PTQ1_ERR_UNSUPPORTED, "q_dtype %s over a %s cache (the cache's own type)", type_name(q_dtype),
+                    type_name(cache->dtype));
+    if (max_len > kMaxDecodeLen)
+        return fail(PTQ1_ERR_UNSUPPORTED, "max_len = %lld > %lld", (long long)max_len, (long long)kMaxDecodeLen);
+    if (!chunk_sizes_ok(batch, n_q_rows, n_q_heads, cache->n_kv_heads))
+        return fail(PTQ1_ERR_UNSUPPORTED, "more than 2^31 - 1025 rows of one kv head or 2^23 tiles of 128 query rows");
+    if (batch == 0 || n_q_rows == 0) return ok();
+    const int64_t d = cache->head_dim;
+    int64_t qb, table = 0;
+    PTQ1_TRY(check_strided(q, "q", n_q_rows, n_q_heads * d, q_stride, 2, &qb));
+    PTQ1_TRY(check_device_array(cu_q, "cu_q", (batch + 1) * 4, 4));
+    if (!mul_ok(batch, max_pages * 4, &table)) return fail(PTQ1_ERR_OVERFLOW, "block_table: size overflows");
+    PTQ1_TRY(check_device_array(block_table, "block_table", table, 4));
+    PTQ1_TRY(check_device_array(seq_lens, "seq_lens", batch * 4, 4));
+    const int64_t ob = n_q_rows * n_q_heads * d * 2;
+    PTQ1_TRY(check_device_array(out, "out", ob, kAlign));
+    clip_chunk(n_q_rows, max_len, &max_q, &window, &sinks);
+    const ptq1::ChunkPlan plan = ptq1::chunk_plan(batch, n_q_rows, max_q, n_q_heads, cache->n_kv_heads, cache->head_dim, max_len,
+                                                  window, sinks);
+    const size_t need = round_up(plan.part_floats * 4, kWsAlign);
+    PTQ1_TRY(check_ws(ws, ws_bytes, need, "ptq1_attn_chunk"));
+    const int64_t wn = static_cast<int64_t>(need);
+    if (overlaps(out, ob, q, qb)) return fail(PTQ1_ERR_ALIAS, "out overlaps q");
+    if (overlaps_cache(out, ob, cache, kb)) return fail(PTQ1_ERR_ALIAS, "out overlaps the cache");
+    if (overlaps(ws, wn, q, qb) || overlaps(ws, wn, out, ob) || overlaps_cache(ws, wn, cache, kb))
+        return fail(PTQ1_ERR_ALIAS, "ws overlaps an argument");
+    const struct {
+        const void *p;
+        int64_t bytes;
+    } indexes[] = {{block_table, table}, {seq_lens, batch * 4}, {cu_q, (batch + 1) * 4}};
+    for (const auto &x : indexes) {
+        if (overlaps(out, ob, x.p, x.bytes)) return fail(PTQ1_ERR_ALIAS, "out overlaps block_table, seq_lens or cu_q");
+        if (overlaps(ws, wn, x.p, x.bytes)) return fail(PTQ1_ERR_ALIAS, "ws overlaps an argument");
+    }
+    return hip_status(ptq1::launch_attn_chunk(plan, q, q_stride, q_dtype, cu_q, batch, n_q_rows, max_q, n_q_heads, *cache,
+                                              block_table, max_pages, seq_lens, max_len, static_cast<int32_t>(window),
+                                              static_cast<int32_t>(sinks), scale, out, static_cast<float *>(ws), stream),
+                      "ptq1_attn_chunk");
 }
 
 size_t ptq1_attn_prompt_workspace_bytes(int64_t batch, int64_t n_q_rows, int64_t max_k, int32_t n_q_heads,

@@ -1,0 +1,1057 @@
+// attn_chunk.hip -- attention of the last tokens of every sequence over the
+// paged cache that holds them already (ptq1_attn_chunk).
+//
+//   out_i = sum_j p_ij V_j / sum_j p_ij,  p_ij = exp2(t_ij - m_i),
+//   t_ij = scale log2(e) (q_i . K_j),     j over the keys that query i sees
+//
+// in one pass over the keys with a running maximum m_i.  Many rows are bounded
+// by the matrix cores, few by the cache's bytes.
+//
+// Rows.  As in attn_prompt.hip: the query rows of a kv head are its group's
+// heads of every token, a tile is 128 of them (32 a wave; of 256-wide heads a
+// pair of waves), and steps are 64 keys, in two LDS buffers, through 32x32x16
+// MFMA with one query row per lane.
+//
+// Layout.  K pages are token-major, V pages dimension-major, and both lie in
+// LDS as in memory, so both A operands are 16 contiguous bytes per lane and
+// nothing is transposed.  The rows of a score tile are assigned to tokens so
+// that the score registers of a lane are eight consecutive tokens: exactly the
+// k-slots of its V operand, so P needs no exchange.
+//
+// Pages.  A page holds whole runs of 16 tokens, of which a step has four.  A
+// wave instruction copies pieces of one run of K (its page is in a scalar), and
+// of V of all four (the lane picks its own).  The pages of a step are looked up
+// a step before they are needed, two before they are read.
+//
+// int8 caches.  16-bit pieces cannot come from memory, so a step's codes pass
+// through registers and become fp16 in LDS, exactly, once for all waves.  The
+// queries enter as fp16 too, scaled to their head's largest magnitude by a
+// power of two; K's step multiplies the scores, V's step the weights, which
+// then enter the second product in units of a power of two of their row.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "ptq1_attn.h"
+#include "ptq1_attn_tile.h"
+#include "ptq1_chunk.h"
+#include "ptq1_launch.h"
+
+namespace ptq1 {
+namespace {
+
+constexpr int BN = kChunkKeys;
+static_assert(kKeys == kChunkKeys, "a step is a tile of keys");
+constexpr int chunk_waves(int d) { return d == 256 ? 8 : 4; }
+
+template <typename C>
+struct ChunkOp {
+    typedef C type;
+};
+template <>
+struct ChunkOp<int8_t> {
+    typedef _Float16 type;
+};
+
+struct ChunkArgs {
+    const void *q;
+    int64_t qs;  // row stride in elements
+    const int32_t *cu, *lens, *table;
+    int64_t max_pages, batch, q_rows, max_q, max_len;
+    int32_t hq, hkv;
+    const void *k_pages, *v_pages;
+    const float *k_steps, *v_steps;
+    int64_t n_pages;
+    int32_t page_shift;
+    int32_t window, sinks;
+    float scale;
+    void *out;
+    int32_t wanted, cut;       // pieces of one kv head that fill the GPU; tiles may be cut
+    int32_t places, slot_rows; // of parts, of one kv head, and rows of one
+    int64_t rows_floats;
+    float *parts;
+};
+
+// The 16-byte piece p of row r of a tile in LDS lies at piece p ^ swizzle of
+// that row: 16 rows at one piece spread over all banks.  (V's rows are
+// dimensions, of 64 tokens: as K's of 64-wide heads.)
+template <int W>
+__device__ __forceinline__ int swizzle(int r)
+{
+    return W >= 128 ? r & 15 : (r >> 1) & 7;
+}
+template <int W>
+__device__ __forceinline__ int place(int r, int p)
+{
+    return r * W + ((p ^ swizzle<W>(r)) << 3);
+}
+// The token of row r of a score tile of 32: bits 2 and 3 change places.
+__device__ __forceinline__ int token_of_row(int r) { return (r & 19) | ((r & 4) << 1) | ((r & 8) >> 1); }
+
+// A sequence's rows and keys as the arguments give them.
+struct ChunkSeq {
+    int q0, lq, len;
+};
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkArgs &a, int64_t b)
+{
+    return {a.cu[b], a.cu[b + 1] - a.cu[b], a.lens[b]};
+}
+__device__ __forceinline__ bool refused(const ChunkArgs &a, const ChunkSeq &s)
+{
+    return s.q0 < 0 || s.lq > a.max_q || s.q0 + static_cast<int64_t>(s.lq) > a.q_rows || s.len < 0 || s.len > a.max_len;
+}
+// Tiles of the rows that exist.
+__device__ __forceinline__ int seq_tiles(const ChunkArgs &a, const ChunkSeq &s, int group)
+{
+    const int64_t first = s.q0 > 0 ? s.q0 : 0, end = s.q0 + static_cast<int64_t>(s.lq);
+    const int64_t n = (end < a.q_rows ? end : a.q_rows) - first;
+    return n > 0 ? static_cast<int>((n * group + kChunkRows - 1) / kChunkRows) : 0;
+}
+__device__ __forceinline__ int seq_steps(const ChunkArgs &a, const ChunkSeq &s, int group)
+{
+    return refused(a, s) ? 0 : steps_bound(s.len, a.window, a.sinks, group);
+}
+
+__device__ __forceinline__ int wave_total(int v)
+{
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+    return __builtin_amdgcn_readfirstlane(v);
+}
+// The sum of f(sequence) over the first n.
+template <class F>
+__device__ __forceinline__ int sum_over(const ChunkArgs &a, int64_t n, F f)
+{
+    int v = 0;
+    for (int64_t i = threadIdx.x & 63; i < n; i += 64) v += f(chunk_seq(a, i));
+    return wave_total(v);
+}
+
+// One tile of 128 query rows of one kv head, and the steps of one workgroup.
+struct ChunkTile {
+    int group, kh;
+    int64_t b;
+    int q0, off;             // the sequence's first row; keys before its first query
+    int rows, row0, end;     // its rows; this tile's first one and the one behind its last
+    ChunkSteps c;
+    int first, last;         // this workgroup's steps
+    int pieces, number;      // of the tile; the first piece's number among all of a kv head
+    int stride;              // between the numbers of its pieces
+};
+
+// False: nothing (more) to do.  The rows of a sequence that is refused become
+// NaN.  join: the tile of a workgroup of the join (tiles alone are numbered).
+template <typename QT, int D>
+__device__ __forceinline__ bool chunk_tile(const ChunkArgs &a, uint32_t block, bool join, ChunkTile &t)
+{
+    t.group = a.hq / a.hkv;
+    t.kh = static_cast<int>(block % static_cast<uint32_t>(a.hkv));
+    const int number = static_cast<int>(block / static_cast<uint32_t>(a.hkv));
+    int per = 1 << 30;
+    if (a.cut) {
+        const int total = sum_over(a, a.batch, [&](const ChunkSeq &s) { return seq_tiles(a, s, t.group) * seq_steps(a, s, t.group); });
+        per = chunk_piece(total, a.wanted);
+    }
+    const auto pieces = [&](const ChunkSeq &s) { return chunk_pieces(seq_steps(a, s, t.group), per); };
+    const auto numbers = [&](const ChunkSeq &s) { return seq_tiles(a, s, t.group) * pieces(s); };
+    int64_t b, at;
+    if (a.cut == 0 && a.batch > 64) {
+        if (!find_rows<kChunkRows>(number, a.cu, a.batch, a.q_rows, t.group, b, at)) return false;
+    } else {
+        const auto of = [&](int64_t i) {
+            const ChunkSeq s = chunk_seq(a, i);
+            return join ? seq_tiles(a, s, t.group) : numbers(s);
+        };
+        if (!(a.batch <= 64 ? find_tile<true>(number, a.batch, of, b, at) : find_tile_in_runs(number, a.batch, of, b, at)))
+            return false;
+    }
+    b = __builtin_amdgcn_readfirstlane(static_cast<int>(b));
+    int piece = 0, tile = __builtin_amdgcn_readfirstlane(static_cast<int>(at));
+    const ChunkSeq s = chunk_seq(a, b);
+    t.b = b;
+    t.stride = seq_tiles(a, s, t.group);
+    if (a.cut && !join) {
+        piece = tile / t.stride;
+        tile -= piece * t.stride;
+    }
+    if (refused(a, s)) {
+        const int64_t r = (s.q0 < 0 ? -static_cast<int64_t>(s.q0) * t.group : 0) + static_cast<int64_t>(tile) * kChunkRows + threadIdx.x;
+        const int64_t tok = s.q0 + r / t.group;
+        if (!join && piece == 0 && threadIdx.x < kChunkRows && tok < s.q0 + static_cast<int64_t>(s.lq) && tok < a.q_rows) {
+            QT *dst = static_cast<QT *>(a.out) + (tok * a.hq + t.kh * t.group + r % t.group) * D;
+            const float n = __builtin_nanf("");
+            for (int e = 0; e < D; e += 4) store4(dst + e, at_f32x4{n, n, n, n});
+        }
+        return false;
+    }
+    t.q0 = s.q0;
+    t.off = s.len - s.lq;
+    t.rows = s.lq * t.group;
+    // the last rows see the most keys: they start first
+    t.row0 = (t.stride - 1 - tile) * kChunkRows;
+    t.end = t.row0 + kChunkRows < t.rows ? t.row0 + kChunkRows : t.rows;
+    t.c = chunk_steps(t.row0 / t.group + t.off, (t.end - 1) / t.group + t.off, a.window, a.sinks);
+    t.pieces = chunk_pieces(t.c.steps, per);
+    if (piece >= t.pieces) return false;
+    t.first = piece * per;
+    t.last = t.c.steps - t.first > per ? t.first + per : t.c.steps;
+    t.number = number;
+    if (a.cut && t.pieces > 1) {
+        // find_tile<true> numbers the longest of each 64 sequences first: the
+        // pieces' places go by the order of the sequences
+        t.number = sum_over(a, b, numbers) + tile;
+        if (t.number + (t.pieces - 1) * t.stride >= a.places) return false;  // (offsets that decrease)
+        if (!join) t.number += piece * t.stride;
+    }
+    return true;
+}
+
+// The place of a row's part.
+__device__ __forceinline__ int64_t part_slot(const ChunkArgs &a, const ChunkTile &t, int number, int row)
+{
+    return (static_cast<int64_t>(number) * a.hkv + t.kh) * a.slot_rows + (row - t.row0);
+}
+
+// One lane's query row.
+struct ChunkRow {
+    bool is;
+    int tok, head;
+    SeenKeys seen;
+};
+__device__ __forceinline__ ChunkRow chunk_row(const ChunkArgs &a, const ChunkTile &t, int row)
+{
+    ChunkRow r;
+    r.is = row < t.rows;
+    const int at = r.is ? row : t.rows - 1;
+    r.tok = at / t.group;
+    r.head = t.kh * t.group + at % t.group;
+    r.seen = seen_keys(r.tok + t.off, a.window);
+    return r;
+}
+
+// Where the keys of a step are: a wave's lanes hold the pages of the step's
+// four runs of 16 tokens (lane % 4), looked up by `find` and checked by `use`,
+// which leaves them in scalars.  A run that no row of the tile sees (behind the
+// sequence, or between the first tokens and the windows, where pages may have
+// been given back) reads another's page; all of it is masked.
+struct ChunkPages {
+    const int32_t *table;
+    int page_shift, lo, reach, sunk;
+    uint32_t n_pages;
+    int32_t found = 0;
+    int32_t run[4];
+    bool bad = false;
+
+    __device__ __forceinline__ ChunkPages(const ChunkArgs &a, const ChunkTile &t)
+        : table(a.table + t.b * a.max_pages), page_shift(a.page_shift), lo(t.c.lo), reach(t.c.reach), sunk(t.c.sunk),
+          n_pages(static_cast<uint32_t>(a.n_pages))
+    {
+    }
+    __device__ __forceinline__ void find(int n0)
+    {
+        const int s = n0 + 16 * (threadIdx.x & 3);
+        const int tok = s < sunk ? s : min(max(s, lo), reach - 1);
+        found = table[tok >> page_shift];
+    }
+    __device__ __forceinline__ void use()
+    {
+        const bool is = static_cast<uint32_t>(found) < n_pages;
+        bad |= !is;
+        const int32_t pg = is ? found : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) run[i] = __builtin_amdgcn_readlane(pg, i);
+    }
+    __device__ __forceinline__ int32_t of(int i) const
+    {
+        const int32_t a = i & 1 ? run[1] : run[0], b = i & 1 ? run[3] : run[2];
+        return i & 2 ? b : a;
+    }
+};
+
+// A step's buffers in LDS; int8 caches: with the steps of its tokens (V's times
+// 2^-10: weights, up to 2^15, times them are then in fp32's range) and the
+// largest of V's.
+template <typename T>
+struct ChunkBuffer {
+    T *k, *v;
+    float *ks, *vs, *top;
+};
+
+// A lane's share of bringing a step's keys and values into LDS.
+template <typename C, int D>
+struct ChunkStaging {
+    static constexpr bool I8 = std::is_same<C, int8_t>::value;
+    typedef typename ChunkOp<C>::type T;
+    static constexpr int W = chunk_waves(D), NT = 64 * W;
+    static constexpr int NK = BN * D * static_cast<int>(sizeof(C)) / (16 * NT);  // 16-byte loads of a thread, for K and for V
+    const char *kp, *vp;   // of this kv head
+    const float *ksp, *vsp;
+    uint32_t page_bytes, page_cells;
+    int page_shift, mask;
+    at_u32x4 kr[I8 ? NK : 1], vr[I8 ? NK : 1];
+    float step = 0.0f;
+
+    __device__ __forceinline__ ChunkStaging(const ChunkArgs &a, int kh)
+        : page_shift(a.page_shift), mask((1 << a.page_shift) - 1)
+    {
+        page_cells = static_cast<uint32_t>(a.hkv) << page_shift;
+        page_bytes = page_cells * (D * static_cast<uint32_t>(sizeof(C)));
+        const int64_t first = (static_cast<int64_t>(kh) << page_shift) * (D * static_cast<int64_t>(sizeof(C)));
+        kp = static_cast<const char *>(a.k_pages) + first;
+        vp = static_cast<const char *>(a.v_pages) + first;
+        ksp = a.k_steps + (static_cast<int64_t>(kh) << page_shift);
+        vsp = a.v_steps + (static_cast<int64_t>(kh) << page_shift);
+    }
+
+    // 16-bit caches: straight into LDS
+    __device__ __forceinline__ void copy(const ChunkPages &p, int n0, const ChunkBuffer<T> &to) const
+    {
+        static_assert(!I8, "16 bits");
+        constexpr int P = D / 8, RK = 64 / P;  // pieces of a row of K, rows of an instruction
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            const int r0 = (i * W + wave) * RK, r = (r0 & 15) + lane / P;  // (a run's row: the swizzle goes by it)
+            const char *base = kp + static_cast<uint64_t>(page_bytes) * static_cast<uint32_t>(p.of(r0 >> 4)) +
+                               ((n0 + (r0 & ~15)) & mask) * (2 * D);
+            copy_to_lds(base, 16 * 2 * D, r * (2 * D) + 16 * ((lane % P) ^ swizzle<D>(r)), to.k + (i * W + wave) * 512);
+        }
+        // V: the piece of a lane is the same in every instruction
+        const int d0 = wave * 8 + (lane >> 3), piece = (lane & 7) ^ swizzle<BN>(d0);
+        const char *src = vp + static_cast<uint64_t>(page_bytes) * static_cast<uint32_t>(p.of(piece >> 1)) +
+                          2 * ((static_cast<uint32_t>(d0) << page_shift) + ((n0 + 8 * piece) & mask));
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src, (lds_void *)(to.v + (i * W + wave) * 512), 16, 0, 0);
+            src += static_cast<uint32_t>(2 * 8 * W) << page_shift;
+        }
+    }
+
+    // int8 caches: into registers ...
+    __device__ __forceinline__ void load(const ChunkPages &p, int n0)
+    {
+        static_assert(I8, "8 bits");
+        constexpr int L = D / 16;  // loads of a row of K
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            const int r0 = (i * W + wave) * (64 / L), r = (r0 & 15) + lane / L;
+            const char *base = kp + static_cast<uint64_t>(page_bytes) * static_cast<uint32_t>(p.of(r0 >> 4)) +
+                               ((n0 + (r0 & ~15)) & mask) * D;
+            kr[i] = *reinterpret_cast<const at_u32x4 *>(base + (r * D + 16 * (lane % L)));
+        }
+        const char *src = vp + static_cast<uint64_t>(page_bytes) * static_cast<uint32_t>(p.of(lane & 3)) +
+                          ((static_cast<uint32_t>(threadIdx.x >> 2) << page_shift) + ((n0 + 16 * (lane & 3)) & mask));
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            vr[i] = *reinterpret_cast<const at_u32x4 *>(src);
+            src += static_cast<uint32_t>(NT / 4) << page_shift;
+        }
+        if (wave < 2)
+            step = (wave == 0 ? ksp : vsp)[static_cast<uint64_t>(page_cells) * static_cast<uint32_t>(p.of(lane >> 4)) + ((n0 + lane) & mask)];
+    }
+    // ... and as fp16 into LDS
+    __device__ __forceinline__ void store(const ChunkBuffer<T> &to) const
+    {
+        constexpr int L = D / 16;
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            const int r = (i * W + wave) * (64 / L) + lane / L, p = 2 * (lane % L);
+            *reinterpret_cast<f16x8 *>(to.k + place<D>(r, p)) = codes_to_f16(kr[i][0], kr[i][1]);
+            *reinterpret_cast<f16x8 *>(to.k + place<D>(r, p + 1)) = codes_to_f16(kr[i][2], kr[i][3]);
+        }
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            const int d = i * (NT / 4) + static_cast<int>(threadIdx.x >> 2), p = 2 * (lane & 3);
+            *reinterpret_cast<f16x8 *>(to.v + place<BN>(d, p)) = codes_to_f16(vr[i][0], vr[i][1]);
+            *reinterpret_cast<f16x8 *>(to.v + place<BN>(d, p + 1)) = codes_to_f16(vr[i][2], vr[i][3]);
+        }
+        if (wave == 0) to.ks[lane] = step;
+        if (wave == 1) {
+            const float s = step * 0x1p-10f;
+            to.vs[lane] = s;
+            const float top = wave_max(s);
+            if (lane == 0) *to.top = top;
+        }
+    }
+};
+
+// A NaN or an infinity leaves a V tile in LDS (zeros in its place); true if there was one.
+template <typename T, int D>
+__device__ __forceinline__ bool clean_values(T *v)
+{
+    bool odd = false;
+    for (int i = threadIdx.x; i < BN * D / 8; i += 64 * chunk_waves(D)) {
+        at_u32x4 w = *reinterpret_cast<const at_u32x4 *>(v + 8 * i);
+        if (clear_non_finite<T>(w)) {
+            *reinterpret_cast<at_u32x4 *>(v + 8 * i) = w;
+            odd = true;
+        }
+    }
+    return odd;
+}
+
+// What was met on the way, for the end: keys among which a V tile had a NaN or
+// an infinity removed, and whether a page was not there.
+struct ChunkNotes {
+    int odd_from, odd_to, bad;
+};
+
+// The page of a key, -1 if there is none.
+__device__ __forceinline__ int64_t page_of_key(const ChunkArgs &a, const ChunkTile &t, int key)
+{
+    const int64_t pg = a.table[t.b * a.max_pages + (key >> a.page_shift)];
+    return pg >= 0 && pg < a.n_pages ? pg : -1;
+}
+
+// Adds to O^T, dimensions d0 + 32 i + ..., the NaNs and infinities among the
+// values that the row sees and that were left out of the products.
+template <typename T, int N>
+__device__ __forceinline__ void add_odd_values(const ChunkArgs &a, const ChunkTile &t, const ChunkRow &row,
+                                               const ChunkNotes &notes, int d, int d0, int half, at_f32x16 (&o)[N])
+{
+    const int64_t page = int64_t{1} << a.page_shift;
+    for (int j = notes.odd_from; j < notes.odd_to && j < t.c.reach; ++j) {
+        if (j >= t.c.sunk && j < t.c.lo) continue;
+        const int64_t pg = page_of_key(a, t, j);
+        if (pg < 0 || !(j < row.seen.hi && (j >= row.seen.lo || j < a.sinks))) continue;
+        const T *src = static_cast<const T *>(a.v_pages) + ((pg * a.hkv + t.kh) * d + d0 + 4 * half) * page + (j & (page - 1));
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float x = static_cast<float>(src[(32 * i + 8 * (e >> 2) + (e & 3)) * page]);
+                if (!(fabsf(x) <= 3.4028235e38f)) o[i][e] += x;
+            }
+    }
+}
+
+// The row sees a key whose page is not there.
+__device__ __forceinline__ bool sees_bad_page(const ChunkArgs &a, const ChunkTile &t, const ChunkRow &row)
+{
+    bool bad = false;
+    const int first = row.seen.lo >> a.page_shift, end = (row.seen.hi + (1 << a.page_shift) - 1) >> a.page_shift;
+    for (int i = 0; i < end && i < first; ++i)
+        if ((i << a.page_shift) < a.sinks) bad |= page_of_key(a, t, i << a.page_shift) < 0;
+        else break;
+    for (int i = first; i < end; ++i) bad |= page_of_key(a, t, i << a.page_shift) < 0;
+    return bad;
+}
+
+// The row's dimensions d0 + 32 i + 8 b + 4 half + e, finished: as they are, or
+// as one part of several (the mean over its keys, their reference and sum).
+template <typename QT, int N>
+__device__ __forceinline__ void store_rows(const ChunkArgs &a, const ChunkTile &t, const ChunkRow &row, int at, int d, int d0,
+                                           int half, const at_f32x16 (&o)[N], float m, float l)
+{
+    if (t.pieces == 1) {
+        QT *dst = static_cast<QT *>(a.out) + ((static_cast<int64_t>(t.q0) + row.tok) * a.hq + row.head) * d + d0 + 4 * half;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+                store4(dst + 32 * i + 2 * j, at_f32x4{o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]});
+        return;
+    }
+    const int64_t slot = part_slot(a, t, t.number, at);
+    float *dst = a.parts + slot * d + d0 + 4 * half;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+            store4(dst + 32 * i + 2 * j, at_f32x4{o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]});
+    if (half == 0 && d0 == 0) {
+        a.parts[a.rows_floats + slot * 2] = m;
+        a.parts[a.rows_floats + slot * 2 + 1] = l;
+    }
+}
+
+// A lane's row at the end: the mean over its keys, 1 / l times the sums of
+// products (int8 caches: and out of their units), with what was left aside on
+// the way.  A row that sees no key is zero; of a piece's keys a row may see
+// none.
+template <typename C, typename QT, int N>
+__device__ __forceinline__ void finish(const ChunkArgs &a, const ChunkTile &t, const ChunkRow &row, const ChunkNotes &notes,
+                                       int at, int d, int d0, int half, at_f32x16 (&o)[N], float m, float l, int unit)
+{
+    const bool none = row.seen.hi == 0 || (t.pieces > 1 && l == 0.0f);
+    float f = none ? 0.0f : 1.0f / l;
+    if (notes.bad != 0 && sees_bad_page(a, t, row)) l = f = __builtin_nanf("");
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        o[i] *= f;
+        if constexpr (std::is_same<C, int8_t>::value) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[i][j] = ldexpf(o[i][j], unit + 10);
+        }
+    }
+    if constexpr (!std::is_same<C, int8_t>::value)
+        if (notes.odd_from < notes.odd_to) add_odd_values<C, N>(a, t, row, notes, d, d0, half, o);
+    if (row.is) store_rows<QT, N>(a, t, row, at, d, d0, half, o, m, l);
+}
+
+// One lane's row as the products' B operand (k = 16 kk + 8 half + j) and the
+// factors that turn its sums into scores in units of log2: scores are sum * c
+// (int8: * the token's step * far).
+template <typename C, typename QT, int D>
+struct ChunkQuery {
+    static constexpr bool I8 = std::is_same<C, int8_t>::value;
+    typedef typename ChunkOp<C>::type T;
+    typedef typename Op16<T>::x8 x8;
+    static constexpr int KK = D / 16;
+    x8 f[KK];
+    float c, far = 1.0f;
+    __device__ __forceinline__ ChunkQuery(const ChunkArgs &a, const ChunkTile &t, const ChunkRow &row, int half)
+    {
+        typedef QT q8 __attribute__((ext_vector_type(8)));
+        const QT *qp = static_cast<const QT *>(a.q) + (static_cast<int64_t>(t.q0) + row.tok) * a.qs + static_cast<int64_t>(row.head) * D;
+        c = a.scale * kLog2e;
+        if constexpr (!I8) {
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) f[kk] = *reinterpret_cast<const x8 *>(qp + 16 * kk + 8 * half);
+        } else {
+            q8 raw[KK];
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) raw[kk] = *reinterpret_cast<const q8 *>(qp + 16 * kk + 8 * half);
+            uint32_t mx = 0;  // of the bit patterns: NaN and infinity last
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float x = static_cast<float>(raw[kk][j]);
+                    mx = max(mx, __builtin_bit_cast(uint32_t, x) & 0x7fffffffu);
+                }
+            mx = max(mx, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mx), 32, 64)));
+            // the largest magnitude in [2^14, 2^15): bf16 elements down to 2^-21
+            // of it enter exactly, smaller ones to 2^-39 of it
+            const int shift = 15 - __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, mx));
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[kk][j] = static_cast<_Float16>(ldexpf(static_cast<float>(raw[kk][j]), shift));
+            // sums are below 2^30; c comes first and a step (below 2^122) second,
+            // so c keeps what makes the first factor neither overflow nor lose
+            // bits, and `far` the rest of a power of two beyond that
+            const int all = __builtin_amdgcn_frexp_expf(c) - shift, here = min(max(all, -125), 80);
+            c = ldexpf(__builtin_amdgcn_frexp_mantf(c), here);
+            far = ldexpf(1.0f, min(max(all - here, -126), 127));
+            if (mx >= 0x7f800000u) c = __builtin_nanf("");  // a NaN or an infinity in the query
+        }
+    }
+};
+
+// The step's weights of KT * 32 keys from key n0 on, of one lane's row (score
+// register j of tile t: key n0 + 32 t + 16 (j / 8) + 8 half + j % 8).
+//
+// int8 caches: a weight times its value's step enters in units of 2^unit, in
+// which it is below 2^15.  In steps that every row sees whole, where the
+// largest step is at most one unit, that holds as it is; elsewhere the unit
+// goes by the products themselves, by at most 2^10 more than these need (so
+// that steps of about one size are not looked at again): what is lost is
+// below 2^-28 of the row's largest.
+template <typename C, int KT>
+struct ChunkSoftmax {
+    static constexpr bool I8 = std::is_same<C, int8_t>::value;
+    typedef typename ChunkOp<C>::type T;
+    typedef typename Op16<T>::x8 x8;
+    float m = -__builtin_inff(), l = 0.0f, l2 = 0.0f;  // m: the reference, in units of log2
+    bool large = false;
+    int unit = -112;
+
+    static __device__ __forceinline__ int key(int t, int j, int half) { return 32 * t + 16 * (j >> 3) + 8 * half + (j & 7); }
+
+    // the largest score of the lane's pair; hidden ones leave the scores
+    template <bool BORDER>
+    __device__ __forceinline__ float top(at_f32x16 (&s)[KT], const SeenKeys &seen, int sinks, int n0, int half, float c, float far,
+                                         const float *ks)
+    {
+        if constexpr (I8) {
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[t][j] = s[t][j] * c * ks[key(t, j, half)];
+            if (__ballot(far != 1.0f) != 0) {
+#pragma unroll
+                for (int t = 0; t < KT; ++t) s[t] *= far;
+            }
+        }
+        if constexpr (BORDER) {
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[t][j] = hidden(seen, sinks, n0 + key(t, j, half)) ? -__builtin_inff() : s[t][j];
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) top = fmaxf(top, s[t][j]);
+        top = lane_pair_max<32>(top);
+        return I8 ? top : top * c;
+    }
+    static __device__ __forceinline__ bool hidden(const SeenKeys &seen, int sinks, int key)
+    {
+        return (key >= seen.hi) | ((key < seen.lo) & (key >= sinks));
+    }
+
+    // The reference follows the largest score, by 8 at most behind it (weights
+    // up to 2^8 lose nothing): few steps after the first rescale.  units: o's.
+    template <int N>
+    __device__ __forceinline__ void raise(float top, at_f32x16 (&o)[N], int &units)
+    {
+        const float mt = reference<T>(top);
+        if (__ballot(mt > m + 8.0f) != 0) {
+            const float mn = fmaxf(m, mt);
+            float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+            l *= f;
+            l2 *= f;
+            if constexpr (I8) {
+                // the unit comes down with the weights, or a large step whose
+                // weight has become nothing would keep the resolution coarse
+                int down = static_cast<int>(__builtin_bit_cast(uint32_t, f) >> 23) - 126;  // f < 2^down
+                down = down > 0 ? 0 : down < -112 - units ? -112 - units : down;
+                f *= pow2(-down);
+                if (&units != &unit) unit = max(unit + down, -112);
+                units += down;
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) o[i] *= f;
+            m = mn;
+            large = large_scores(m);
+        }
+    }
+
+    // 16-bit caches
+    __device__ __forceinline__ void weights(at_f32x16 (&s)[KT], float c, x8 (&pf)[2 * KT])
+    {
+        const float ms = m == -__builtin_inff() ? 0.0f : m;
+        float mul = c;
+        if (large) {
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[t][j] *= c;
+            mul = 1.0f;
+        }
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                pf[2 * t + (j >> 3)][j & 7] = static_cast<T>(__builtin_amdgcn_exp2f(fmaf(s[t][j], mul, -ms)));
+#pragma unroll
+        for (int u = 0; u < 2 * KT; u += 2) {
+            l = add_weights<T>(pf[u], l);
+            l2 = add_weights<T>(pf[u + 1], l2);
+        }
+    }
+
+    // int8 caches: weights times steps, in units; rescale(f): the unit has become 1 / f of what it was
+    template <bool BORDER, class F>
+    __device__ __forceinline__ void products(at_f32x16 (&s)[KT], const SeenKeys &seen, int sinks, int n0, int half,
+                                             const float *vs, float vtop, x8 (&pf)[2 * KT], F rescale)
+    {
+        const float ms = m == -__builtin_inff() ? 0.0f : m;
+        float seen_top = vtop;
+        if constexpr (BORDER) seen_top = 0.0f;
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float p = __builtin_amdgcn_exp2f(s[t][j] - ms);
+                if ((j & 1) == 0) l += p;
+                else l2 += p;
+                float step = vs[key(t, j, half)];
+                if constexpr (BORDER) {
+                    step = hidden(seen, sinks, n0 + key(t, j, half)) ? 0.0f : step;
+                    seen_top = fmaxf(seen_top, step);
+                }
+                s[t][j] = p * step;
+            }
+        if (BORDER || __ballot(!(vtop <= pow2(unit))) != 0) {
+            float top = s[0][0];
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) top = fmaxf(top, s[t][j]);
+            top = lane_pair_max<32>(top);
+            if constexpr (BORDER) seen_top = lane_pair_max<32>(seen_top);
+            // 2^e above each
+            const int need = static_cast<int>(__builtin_bit_cast(uint32_t, top) >> 23) - 126 - 15;
+            const int step = static_cast<int>(__builtin_bit_cast(uint32_t, seen_top) >> 23) - 126;
+            const int next = min(max(need, min(step, need + 10)), 111);
+            if (next > unit) {
+                rescale(pow2(max(unit - next, -126)));
+                unit = next;
+            }
+        }
+        const float in_units = pow2(-unit);
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) pf[2 * t + (j >> 3)][j & 7] = static_cast<T>(s[t][j] * in_units);
+    }
+};
+
+template <typename C, typename QT, int D>
+__global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs a)
+{
+    typedef typename ChunkOp<C>::type T;
+    typedef typename Op16<T>::x8 x8;
+    constexpr bool I8 = std::is_same<C, int8_t>::value;
+    constexpr int KT = BN / 32, DT = D / 32, KK = D / 16;
+
+    // two buffers: separate objects, so that the copies into one need not have
+    // ended before the other is read
+    __shared__ __attribute__((aligned(16))) T kt0[BN * D], kt1[BN * D], vt0[BN * D], vt1[BN * D];
+    __shared__ float steps[I8 ? 4 * BN + 2 : 1];
+    __shared__ ChunkNotes notes;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 31, half = lane >> 5;
+    ChunkTile t;
+    if (!chunk_tile<QT, D>(a, blockIdx.x, false, t)) return;
+    const bool idle = t.row0 + 32 * wave >= t.rows;  // no row of this wave's is there
+    const int at = t.row0 + 32 * wave + col;
+    const ChunkRow row = chunk_row(a, t, at);
+    ChunkPages pages(a, t);
+    ChunkStaging<C, D> staging(a, t.kh);
+    const ChunkBuffer<T> b0{kt0, vt0, steps, steps + BN, steps + 4 * BN};
+    const ChunkBuffer<T> b1{kt1, vt1, steps + 2 * BN, steps + 3 * BN, steps + 4 * BN + 1};
+    if (t.first < t.last) pages.find(step_key(t.c, t.first));
+    const ChunkQuery<C, QT, D> q(a, t, row, half);
+    if (threadIdx.x == 0) notes = {1 << 30, 0, 0};
+
+    at_f32x16 o[DT];
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
+    ChunkSoftmax<C, KT> w;
+
+    auto step = [&](auto border, int i, const ChunkBuffer<T> &b, const ChunkBuffer<T> &next) __attribute__((always_inline)) {
+        constexpr bool BORDER = decltype(border)::value;  // some row may not see some key of the step
+        const int n0 = step_key(t.c, i);
+        if (i + 1 < t.last) {
+            pages.use();
+            if constexpr (I8)
+                staging.load(pages, step_key(t.c, i + 1));
+            else
+                staging.copy(pages, step_key(t.c, i + 1), next);
+            if (i + 2 < t.last) pages.find(step_key(t.c, i + 2));
+        }
+        x8 pf[2 * KT];
+        if (!idle) {
+            at_f32x16 s[KT];
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[k][j] = 0.0f;
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) {
+                    const x8 kf = *reinterpret_cast<const x8 *>(b.k + place<D>(32 * k + token_of_row(col), 2 * kk + half));
+                    s[k] = Op16<T>::mfma32(kf, q.f[kk], s[k]);
+                }
+            }
+            const float top = w.template top<BORDER>(s, row.seen, a.sinks, n0, half, q.c, q.far, b.ks);
+            w.raise(top, o, w.unit);
+            if constexpr (I8)
+                w.template products<BORDER>(s, row.seen, a.sinks, n0, half, b.vs, *b.top, pf, [&](float f) {
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) o[d] *= f;
+                });
+            else
+                w.weights(s, q.c, pf);
+        }
+        if constexpr (BORDER && !I8) {
+            // a zero weight would not keep a NaN or an infinity out of the rows
+            // that do not see it: such values leave the tile and are given to
+            // the rows that see them at the end
+            if (clean_values<T, D>(b.v)) {
+                atomicMin(&notes.odd_from, n0);
+                atomicMax(&notes.odd_to, n0 + BN);
+            }
+            __syncthreads();
+        }
+        if (!idle) {
+#pragma unroll
+            for (int u = 0; u < 2 * KT; ++u)
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    o[d] = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(b.v + place<BN>(32 * d + col, 2 * u + half)), pf[u], o[d]);
+        }
+        if constexpr (I8)
+            if (i + 1 < t.last) staging.store(next);
+        __syncthreads();
+    };
+
+    if (t.first < t.last) {
+        pages.use();
+        if constexpr (I8) {
+            staging.load(pages, step_key(t.c, t.first));
+            staging.store(b0);
+        } else
+            staging.copy(pages, step_key(t.c, t.first), b0);
+        if (t.first + 1 < t.last) pages.find(step_key(t.c, t.first + 1));
+    }
+    __syncthreads();
+    const auto turn = [&](int i, const ChunkBuffer<T> &b, const ChunkBuffer<T> &next) __attribute__((always_inline)) {
+        if (i >= t.c.all_from && i < t.c.all_to)
+            step(std::false_type{}, i, b, next);
+        else
+            step(std::true_type{}, i, b, next);
+    };
+    for (int i = t.first; i < t.last; i += 2) {
+        turn(i, b0, b1);
+        if (i + 1 >= t.last) break;
+        turn(i + 1, b1, b0);
+    }
+    if (__ballot(pages.bad) != 0 && lane == 0) notes.bad = 1;
+    __syncthreads();
+    if (idle) return;
+    const float l = lane_pair_sum<32>(w.l + w.l2);
+    finish<C, QT, DT>(a, t, row, notes, at, D, 0, half, o, w.m, l, w.unit);
+}
+
+// The same for 256-wide heads, whose O^T and queries for 32 rows take 192
+// registers of a lane: a pair of waves shares 32 rows.  Each makes the scores
+// of one half of a step's 64 keys and forms their weights, the pair exchanges
+// maxima and weights (int8 caches: and their units) through LDS, and each
+// multiplies all 64 keys' weights with one half of the dimensions.
+template <typename C, typename QT>
+__global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(ChunkArgs a)
+{
+    typedef typename ChunkOp<C>::type T;
+    typedef typename Op16<T>::x8 x8;
+    constexpr bool I8 = std::is_same<C, int8_t>::value;
+    constexpr int D = 256, DT = 4, KK = D / 16;
+    __shared__ __attribute__((aligned(16))) T kt0[BN * D], kt1[BN * D], vt0[BN * D], vt1[BN * D];
+    __shared__ x8 weights[4][4][64];   // [pair][k-step of 16 keys][lane]
+    __shared__ float tops[4][2][32];   // [pair][key half][row]
+    __shared__ int units[I8 ? 4 : 1][2][32];
+    __shared__ float steps[I8 ? 4 * BN + 2 : 1];
+    __shared__ ChunkNotes notes;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 31, half = lane >> 5;
+    const int pair = wave >> 1, part = wave & 1;
+    ChunkTile t;
+    if (!chunk_tile<QT, D>(a, blockIdx.x, false, t)) return;
+    const bool idle = t.row0 + 32 * pair >= t.rows;
+    const int at = t.row0 + 32 * pair + col;
+    const ChunkRow row = chunk_row(a, t, at);
+    ChunkPages pages(a, t);
+    ChunkStaging<C, D> staging(a, t.kh);
+    const ChunkBuffer<T> b0{kt0, vt0, steps, steps + BN, steps + 4 * BN};
+    const ChunkBuffer<T> b1{kt1, vt1, steps + 2 * BN, steps + 3 * BN, steps + 4 * BN + 1};
+    if (t.first < t.last) pages.find(step_key(t.c, t.first));
+    const ChunkQuery<C, QT, D> q(a, t, row, half);
+    if (threadIdx.x == 0) notes = {1 << 30, 0, 0};
+
+    at_f32x16 o[DT];  // dimensions 128 part + 32 i + ...
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
+    ChunkSoftmax<C, 1> w;  // l: of this wave's keys
+    int o_unit = -112;
+
+    auto step = [&](auto border, int i, const ChunkBuffer<T> &b, const ChunkBuffer<T> &next) __attribute__((always_inline)) {
+        constexpr bool BORDER = decltype(border)::value;
+        const int n0 = step_key(t.c, i), mine = n0 + 32 * part;
+        if (i + 1 < t.last) {
+            pages.use();
+            if constexpr (I8)
+                staging.load(pages, step_key(t.c, i + 1));
+            else
+                staging.copy(pages, step_key(t.c, i + 1), next);
+            if (i + 2 < t.last) pages.find(step_key(t.c, i + 2));
+        }
+        at_f32x16 s[1];
+        float top = 0.0f;
+        if (!idle) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s[0][j] = 0.0f;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+                s[0] = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(b.k + place<D>(32 * part + token_of_row(col), 2 * kk + half)), q.f[kk], s[0]);
+            top = w.template top<BORDER>(s, row.seen, a.sinks, mine, half, q.c, q.far, b.ks + 32 * part);
+            if (half == 0) tops[pair][part][col] = top;
+        }
+        barrier_lds();
+        if (!idle) {
+            top = fmaxf(top, tops[pair][part ^ 1][col]);
+            w.raise(top, o, o_unit);  // the same in both waves
+            x8 pf[2];
+            if constexpr (I8) {
+                w.template products<BORDER>(s, row.seen, a.sinks, mine, half, b.vs + 32 * part, *b.top, pf, [](float) {});
+                if (half == 0) units[pair][part][col] = w.unit;
+            } else
+                w.weights(s, q.c, pf);
+            weights[pair][2 * part][lane] = pf[0];
+            weights[pair][2 * part + 1][lane] = pf[1];
+        }
+        if constexpr (BORDER && !I8) {
+            if (clean_values<T, D>(b.v)) {
+                atomicMin(&notes.odd_from, n0);
+                atomicMax(&notes.odd_to, n0 + BN);
+            }
+        }
+        barrier_lds();
+        if (!idle) {
+            int behind[2] = {0, 0};  // of a half's unit behind o's
+            if constexpr (I8) {
+                const int u0 = units[pair][0][col], u1 = units[pair][1][col];
+                const int now = max(o_unit, max(u0, u1));
+                if (__ballot(now > o_unit) != 0) {
+                    const float f = pow2(max(o_unit - now, -126));
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) o[d] *= f;
+                    o_unit = now;
+                }
+                behind[0] = u0 - now;
+                behind[1] = u1 - now;
+            }
+            // ---- O^T of dimensions 128 part ..
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                x8 p = weights[pair][u][lane];
+                if constexpr (I8)
+                    if (__ballot(behind[u >> 1] != 0) != 0) p *= static_cast<T>(pow2(max(behind[u >> 1], -30)));
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    o[d] = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(b.v + place<BN>(128 * part + 32 * d + col, 2 * u + half)), p, o[d]);
+            }
+        }
+        if constexpr (I8)
+            if (i + 1 < t.last) staging.store(next);
+        barrier_copies();  // all have read, the next step is there
+    };
+
+    if (t.first < t.last) {
+        pages.use();
+        if constexpr (I8) {
+            staging.load(pages, step_key(t.c, t.first));
+            staging.store(b0);
+        } else
+            staging.copy(pages, step_key(t.c, t.first), b0);
+        if (t.first + 1 < t.last) pages.find(step_key(t.c, t.first + 1));
+    }
+    barrier_copies();
+    const auto turn = [&](int i, const ChunkBuffer<T> &b, const ChunkBuffer<T> &next) __attribute__((always_inline)) {
+        if (i >= t.c.all_from && i < t.c.all_to)
+            step(std::false_type{}, i, b, next);
+        else
+            step(std::true_type{}, i, b, next);
+    };
+    for (int i = t.first; i < t.last; i += 2) {
+        turn(i, b0, b1);
+        if (i + 1 >= t.last) break;
+        turn(i + 1, b1, b0);
+    }
+    if (__ballot(pages.bad) != 0 && lane == 0) notes.bad = 1;
+    // the pair's sums
+    float l = lane_pair_sum<32>(w.l + w.l2);
+    __syncthreads();
+    if (half == 0) tops[pair][part][col] = l;
+    __syncthreads();
+    if (idle) return;
+    l = tops[pair][0][col] + tops[pair][1][col];
+    finish<C, QT, DT>(a, t, row, notes, at, D, 128 * part, half, o, w.m, l, o_unit);
+}
+
+// Joins the parts of the tiles that were cut: D / 4 lanes per row, one row each
+// (blockIdx.y: the part of a tile's rows).
+constexpr int join_rows(int d) { return 256 / (d / 4); }
+
+template <typename QT, int D>
+__global__ void __launch_bounds__(256) k_chunk_join(ChunkArgs a)
+{
+    constexpr int LPR = D / 4;
+    ChunkTile t;
+    if (!chunk_tile<QT, D>(a, blockIdx.x, true, t) || t.pieces == 1) return;
+    const int x = threadIdx.x % LPR;
+    const int r = t.row0 + static_cast<int>(blockIdx.y * join_rows(D) + threadIdx.x / LPR);
+    if (r >= t.end) return;
+    const ChunkRow row = chunk_row(a, t, r);
+    const int64_t first = part_slot(a, t, t.number, r), stride = static_cast<int64_t>(t.stride) * a.hkv * a.slot_rows;
+    const float *ml = a.parts + a.rows_floats + first * 2, *src = a.parts + first * D + 4 * x;
+    float M = -__builtin_inff();
+    for (int i = x; i < t.pieces; i += LPR) M = fmaxf(M, ml[2 * i * stride]);
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) M = fmaxf(M, __shfl_xor(M, o, 64));
+    if (M == -__builtin_inff()) M = 0.0f;
+    float L = 0.0f;
+    for (int i = x; i < t.pieces; i += LPR) L += __builtin_amdgcn_exp2f(ml[2 * i * stride] - M) * ml[2 * i * stride + 1];
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) L += __shfl_xor(L, o, 64);
+    const float inv = row.seen.hi == 0 ? 0.0f : 1.0f / L;
+    at_f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int i = 0; i < t.pieces; ++i)
+        o += __builtin_amdgcn_exp2f(ml[2 * i * stride] - M) * ml[2 * i * stride + 1] * inv *
+             *reinterpret_cast<const at_f32x4 *>(src + i * stride * D);
+    store4(static_cast<QT *>(a.out) + ((static_cast<int64_t>(t.q0) + row.tok) * a.hq + row.head) * D + 4 * x, o);
+}
+
+template <typename C, typename QT, int D>
+hipError_t chunk_launch(const ChunkArgs &a, const ChunkPlan &p, hipStream_t s)
+{
+    const dim3 grid(static_cast<uint32_t>(p.numbers * a.hkv));
+    if constexpr (D == 256)
+        hipLaunchKernelGGL((k_attn_chunk_wide<C, QT>), grid, dim3(64 * chunk_waves(D)), 0, s, a);
+    else
+        hipLaunchKernelGGL((k_attn_chunk<C, QT, D>), grid, dim3(64 * chunk_waves(D)), 0, s, a);
+    if (p.cut)
+        hipLaunchKernelGGL((k_chunk_join<QT, D>), dim3(static_cast<uint32_t>(p.tiles * a.hkv), (p.slot_rows + join_rows(D) - 1) / join_rows(D)),
+                           dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename C, typename QT>
+hipError_t chunk_d(const ChunkArgs &a, const ChunkPlan &p, int d, hipStream_t s)
+{
+    return d == 64 ? chunk_launch<C, QT, 64>(a, p, s) : d == 128 ? chunk_launch<C, QT, 128>(a, p, s) : chunk_launch<C, QT, 256>(a, p, s);
+}
+
+}  // namespace
+
+// Bytes of parts above which nothing is cut.
+constexpr int64_t kMaxChunkParts = int64_t{1} << 28;
+
+ChunkPlan chunk_plan(int64_t batch, int64_t q_rows, int64_t max_q, int32_t hq, int32_t hkv, int32_t d, int64_t max_len,
+                     int64_t window, int64_t sinks)
+{
+    ChunkPlan p;
+    const int64_t group = hq / hkv, rows = max_q * group;
+    p.tiles = q_rows * group / kChunkRows + batch;
+    p.numbers = p.tiles;
+    p.slot_rows = static_cast<int32_t>(rows < kChunkRows ? rows : kChunkRows);
+    const int64_t slots = d == 256 ? 256 : 512;  // workgroups that the GPU holds
+    p.wanted = static_cast<int32_t>(slots / hkv > 1 ? slots / hkv : 1);
+    const int most = steps_bound(static_cast<int>(max_len), static_cast<int>(window), static_cast<int>(sinks), static_cast<int>(group));
+    const int64_t numbers = p.wanted + p.tiles, parts = numbers * hkv * p.slot_rows;
+    p.cut = most > kChunkMinSteps && p.tiles * hkv <= 8 * slots && parts * (d + 2) * 4 <= kMaxChunkParts;
+    if (p.cut) {
+        p.numbers = numbers;
+        p.rows_floats = static_cast<size_t>(parts) * d;
+        p.part_floats = p.rows_floats + static_cast<size_t>(parts) * 2;
+    }
+    return p;
+}
+
+hipError_t launch_attn_chunk(const ChunkPlan &p, const void *q, int64_t qs, int q_type, const int32_t *cu, int64_t batch,
+                             int64_t q_rows, int64_t max_q, int32_t hq, const ptq1_kv_cache &c, const int32_t *table,
+                             int64_t max_pages, const int32_t *lens, int64_t max_len, int32_t window, int32_t sinks,
+                             float scale, void *out, float *parts, hipStream_t s)
+{
+    const ChunkArgs a{q, qs, cu, lens, table, max_pages, batch, q_rows, max_q, max_len, hq, c.n_kv_heads, c.k_pages,
+                      c.v_pages, c.k_steps, c.v_steps, c.n_pages, __builtin_ctz(static_cast<unsigned>(c.page_size)),
+                      window, sinks, scale, out, p.wanted, p.cut, static_cast<int32_t>(p.numbers), p.slot_rows,
+                      static_cast<int64_t>(p.rows_floats), parts};
+    if (c.dtype == PTQ1_BF16) return chunk_d<__bf16, __bf16>(a, p, c.head_dim, s);
+    if (c.dtype == PTQ1_F16) return chunk_d<_Float16, _Float16>(a, p, c.head_dim, s);
+    return q_type == PTQ1_F16 ? chunk_d<int8_t, _Float16>(a, p, c.head_dim, s) : chunk_d<int8_t, __bf16>(a, p, c.head_dim, s);
+}
+
+}  // namespace ptq1

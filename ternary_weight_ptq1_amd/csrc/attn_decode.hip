@@ -150,25 +150,8 @@ __device__ __forceinline__ void split_terms(const float (&x)[8], typename Op16<T
     }
 }
 
-// 8 int8 codes (two dwords) as fp16, exact: the byte code + 128 put into the
-// mantissa of 1024 is 1152 + code.
-__device__ __forceinline__ f16x8 codes_to_f16(uint32_t a, uint32_t b)
-{
-    a ^= 0x80808080u;
-    b ^= 0x80808080u;
-    at_u32x4 w;
-    w[0] = __builtin_amdgcn_perm(0x64646464u, a, 0x04010400u);
-    w[1] = __builtin_amdgcn_perm(0x64646464u, a, 0x04030402u);
-    w[2] = __builtin_amdgcn_perm(0x64646464u, b, 0x04010400u);
-    w[3] = __builtin_amdgcn_perm(0x64646464u, b, 0x04030402u);
-    return __builtin_bit_cast(f16x8, w) - static_cast<_Float16>(1152.0f);
-}
-
 // The e of the power of two 2^e above a sum of weights (0 for 0, NaN and infinity).
 __device__ __forceinline__ int sum_exponent(float l) { return __builtin_amdgcn_frexp_expf(l); }
-
-// 2^e for e in [-126, 127]
-__device__ __forceinline__ float pow2(int e) { return __builtin_bit_cast(float, static_cast<uint32_t>(127 + e) << 23); }
 
 // C: cache element, QT: type of q and out, D: head_dim, NQ: 16-bit terms of
 // the queries (int8 caches: 8-bit digits), NP: 16-bit terms of the weights.

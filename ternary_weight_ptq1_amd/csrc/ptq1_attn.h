@@ -95,6 +95,23 @@ __device__ __forceinline__ void store4(_Float16 *p, at_f32x4 v)
     *reinterpret_cast<f16x4 *>(p) = __builtin_convertvector(v, f16x4);
 }
 
+// 8 int8 codes (two dwords) as fp16, exact: the byte code + 128 put into the
+// mantissa of 1024 is 1152 + code.
+__device__ __forceinline__ f16x8 codes_to_f16(uint32_t a, uint32_t b)
+{
+    a ^= 0x80808080u;
+    b ^= 0x80808080u;
+    at_u32x4 w;
+    w[0] = __builtin_amdgcn_perm(0x64646464u, a, 0x04010400u);
+    w[1] = __builtin_amdgcn_perm(0x64646464u, a, 0x04030402u);
+    w[2] = __builtin_amdgcn_perm(0x64646464u, b, 0x04010400u);
+    w[3] = __builtin_amdgcn_perm(0x64646464u, b, 0x04030402u);
+    return __builtin_bit_cast(f16x8, w) - static_cast<_Float16>(1152.0f);
+}
+
+// 2^e for e in [-126, 127]
+__device__ __forceinline__ float pow2(int e) { return __builtin_bit_cast(float, static_cast<uint32_t>(127 + e) << 23); }
+
 // The place of flat tile `flat` among the tiles of `batch` sequences, of which
 // sequence i has tiles_of(i): dense, so that none of the workgroups that the
 // engines take in turn is empty (with one tile index for all sequences, short

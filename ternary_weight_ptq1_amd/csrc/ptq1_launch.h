@@ -201,4 +201,23 @@ int64_t prompt_tiles(int64_t batch, int64_t q_rows, int32_t hq, int32_t hkv);
 hipError_t launch_attn_prompt(const PromptArgs &a, int dtype, int32_t d, const PromptPlan &plan, float *part,
                               hipStream_t s);
 
+// Attention of chunks over the cache.  Tiles of 128 query rows of a kv head
+// (`tiles` of one at most); where they may be cut along the keys, `numbers`
+// pieces of one at most, so that `wanted` of them fill the GPU, each with a place
+// for slot_rows rows of parts: the mean over the piece's keys [number][kv head]
+// [row][d], then their (reference, sum) pairs.
+struct ChunkPlan {
+    int64_t tiles = 0, numbers = 0;
+    int32_t wanted = 1, slot_rows = 0;
+    bool cut = false;
+    size_t rows_floats = 0, part_floats = 0;
+};
+ChunkPlan chunk_plan(int64_t batch, int64_t q_rows, int64_t max_q, int32_t hq, int32_t hkv, int32_t d, int64_t max_len,
+                     int64_t window, int64_t sinks);
+// window: 2^22 + 1 where there is none
+hipError_t launch_attn_chunk(const ChunkPlan &p, const void *q, int64_t qs, int q_type, const int32_t *cu, int64_t batch,
+                             int64_t q_rows, int64_t max_q, int32_t hq, const ptq1_kv_cache &c, const int32_t *table,
+                             int64_t max_pages, const int32_t *lens, int64_t max_len, int32_t window, int32_t sinks,
+                             float scale, void *out, float *parts, hipStream_t s);
+
 }  // namespace ptq1

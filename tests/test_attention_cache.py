@@ -259,3 +259,121 @@ def test_attn_decode_window_many_sequences(batch):
     sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
     got = P.ptq1_attn_decode_window(q, c, table, sl, 600, 3, max_len=9000)
     check_attention(q, c, table, [1] * batch, lens, got, WEIGHT_TERM[(BF16, BF16)], 600, 3)
+
+
+# ------------------------------------------------- chunks over the cache ----
+
+CHUNK_PAIRS = [(BF16, BF16), (F16, F16), (BF16, I8), (F16, I8)]
+# a weight enters rounded to the 16-bit type of the products (int8 caches: fp16, times its step)
+CHUNK_TERM = {(BF16, BF16): 2.0 ** -8, (F16, F16): 2.0 ** -11, (BF16, I8): 2.0 ** -11, (F16, I8): 2.0 ** -11}
+
+
+def chunk_state(seed, new, lens, hq, hkv, d, page, qt, ctype, window=0, sinks=0):
+    g = gen(seed)
+    table, pages = tables(g, lens, page)
+    c = filled_cache(g, pages, page, hkv, d, ctype)
+    keep_window(c, table, new, lens, window, sinks)
+    q = randn(g, sum(new), hq, d).to(qt)
+    return q, c, table, cumulated(new), torch.tensor(lens, dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("qt,ctype", CHUNK_PAIRS)
+@pytest.mark.parametrize("hq,hkv,d,page,new,lens,window,sinks", [
+    (1, 1, 64, 16, [1], [1], 0, 0),
+    (5, 1, 128, 16, [5], [77], 0, 0),
+    (6, 2, 256, 32, [3, 1], [129, 1], 0, 0),
+    (4, 2, 64, 16, [0, 33, 5, 1], [0, 33, 200, 64], 0, 0),
+    (40, 8, 128, 64, [33, 100], [33, 463], 0, 0),
+    (6, 1, 256, 256, [70, 65], [400, 65], 0, 0),
+    (33, 1, 128, 128, [9], [700], 0, 0),              # rows of a token in two tiles
+    (200, 1, 64, 32, [3], [90], 0, 0),                # a token's heads are more than a tile
+    (2, 2, 128, 16, [10, 7], [4, 7], 0, 0),           # more queries than tokens: the first ones see nothing
+    (8, 2, 64, 16, [20, 300], [500, 300], 50, 0),
+    (8, 2, 128, 16, [20, 300, 1], [500, 300, 999], 64, 5),
+    (6, 2, 256, 32, [130, 2], [930, 700], 100, 17),
+    (4, 4, 128, 64, [200], [1500], 1, 0),
+    (4, 4, 128, 64, [64], [700], 500, 130),
+    (4, 1, 64, 128, [150], [400], 10000, 10000),
+])
+def test_attn_chunk(qt, ctype, hq, hkv, d, page, new, lens, window, sinks):
+    s = chunk_state(hq + sum(lens), new, lens, hq, hkv, d, page, qt, ctype, window, sinks)
+    got = P.ptq1_attn_chunk(*s, window=window, sinks=sinks)
+    assert got.dtype == qt and got.shape == s[0].shape
+    check_attention(*s[:3], new, lens, got, CHUNK_TERM[(qt, ctype)], window, sinks)
+    # bounds change the split, not what is computed; the same call gives the same bits
+    tight = dict(max_q=max(new), max_len=max(lens))
+    once = P.ptq1_attn_chunk(*s, window=window, sinks=sinks, **tight)
+    check_attention(*s[:3], new, lens, once, CHUNK_TERM[(qt, ctype)], window, sinks)
+    assert torch.equal(once, P.ptq1_attn_chunk(*s, window=window, sinks=sinks, **tight))
+
+
+@pytest.mark.parametrize("qt,ctype", CHUNK_PAIRS)
+@pytest.mark.parametrize("hq,hkv,d,page,new,lens,window,sinks", [
+    (8, 2, 64, 16, [4, 1, 90], [9000, 30, 5000], 0, 0),
+    (5, 1, 128, 64, [6, 700], [20000, 700], 0, 0),
+    (8, 2, 128, 16, [8, 3], [7000, 12000], 4000, 4),
+    (6, 2, 256, 32, [5, 40], [6000, 3000], 0, 0),
+    (3, 1, 256, 64, [60], [9000], 5000, 100),
+])
+def test_attn_chunk_cut_along_the_keys(qt, ctype, hq, hkv, d, page, new, lens, window, sinks):
+    s = chunk_state(sum(lens), new, lens, hq, hkv, d, page, qt, ctype, window, sinks)
+    got = P.ptq1_attn_chunk(*s, window=window, sinks=sinks, max_q=max(new), max_len=max(lens))
+    assert P.workspace_bytes("attn_chunk", len(new), sum(new), max(new), hq, hkv, d, max(lens), window, sinks) > 0
+    check_attention(*s[:3], new, lens, got, CHUNK_TERM[(qt, ctype)], window, sinks)
+
+
+@pytest.mark.parametrize("batch", [65, 200, 1000])
+@pytest.mark.parametrize("high", [3, 40])
+def test_attn_chunk_many_sequences(batch, high):
+    rng = np.random.default_rng(batch)
+    new = [int(n) for n in rng.integers(0, high, batch)]
+    lens = [n + int(m) for n, m in zip(new, rng.integers(0, 500, batch))]
+    lens[7] = new[7] + 6000
+    s = chunk_state(batch, new, lens, 2, 1, 64, 64, BF16, BF16)
+    got = P.ptq1_attn_chunk(*s, max_q=max(new))
+    check_attention(*s[:3], new, lens, got, CHUNK_TERM[(BF16, BF16)])
+
+
+def test_attn_chunk_rows_apart_and_left_as_they_were():
+    """Queries that are parts of stacked rows; rows ahead of the first sequence and behind the last stay."""
+    g = gen(8)
+    new, lens = [20, 3], [150, 90]
+    table, pages = tables(g, lens, 16)
+    c = filled_cache(g, pages, 16, 2, 128, BF16)
+    rows = randn(g, 30, 12, 128).to(BF16)
+    q = rows[:, 2:10]
+    cu = cumulated(new, 4)
+    out = torch.full((30, 8, 128), 7.0, dtype=BF16, device=DEV)
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    assert P.ptq1_attn_chunk(q, c, table, cu, sl, out=out) is out
+    check_attention(q, c, table, new, lens, out, CHUNK_TERM[(BF16, BF16)], at=4)
+    assert bool((out[:4] == 7).all()) and bool((out[27:] == 7).all())
+
+
+@pytest.mark.parametrize("hq,d", [(4, 64), (4, 128), (4, 256)])
+@pytest.mark.parametrize("ctype", [BF16, I8])
+def test_attn_chunk_refused_sequences(hq, d, ctype):
+    """Lengths that are none, more queries than the bound, rows that are not there, pages that are not there."""
+    new, lens = [5, 6, 7, 8, 200, 9], [50, 60, 70, 80, 300, 9]
+    q, c, table, cu, sl = chunk_state(9, new, lens, hq, 2, d, 16, BF16, ctype)
+    page = table[4, 9].item()
+    sl[0], table[2, 1], table[4, 9] = -1, -3, c.n_pages  # tokens 16 .. 31 and 144 .. 159
+    got = P.ptq1_attn_chunk(q, c, table, cu, sl, max_q=200)
+    at = cu.tolist()
+    assert bool(got[at[0]:at[1]].isnan().all()) and bool(got[at[2]:at[3]].isnan().all())
+    # queries ahead of the page that is not there do not see it: positions 100 .. 143 of that sequence
+    assert bool(got[at[4] + 44:at[5]].isnan().all())
+    for b, m, n in ((1, 6, 60), (3, 8, 80), (5, 9, 9)):
+        check_attention(q, c, table[b:b + 1], [m], [n], got, CHUNK_TERM[(BF16, ctype)], at=at[b])
+    check_attention(q, c, table[4:5], [44], [144], got, CHUNK_TERM[(BF16, ctype)], at=at[4])
+    # a bound on the queries; with a window, the missing page is behind most of them
+    got = P.ptq1_attn_chunk(q, c, table, cu, sl, max_q=100, window=20)
+    assert bool(got[at[4]:at[5]].isnan().all())
+    table[4, 9] = page
+    table[4, 5] = -1  # tokens 80 .. 95: seen from positions 100 .. 114 (windows from 81 to 95 on)
+    got = P.ptq1_attn_chunk(q, c, table, cu, sl, max_q=200, window=20)
+    assert bool(got[at[4]:at[4] + 15].isnan().all()) and not bool(got[at[4] + 15:at[5]].isnan().any())
+    # rows past the tensor's end, and a length past its bound
+    short = P.ptq1_attn_chunk(q[:at[5] + 4], c, table, cu, sl, max_len=79, window=20)
+    assert bool(short[at[5]:].isnan().all()) and bool(short[at[3]:at[4]].isnan().all())
+    check_attention(q, c, table[1:2], [6], [60], short, CHUNK_TERM[(BF16, ctype)], 20, at=at[1])

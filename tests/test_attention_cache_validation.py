@@ -172,6 +172,140 @@ int main()
     assert out.returncode == 0, out.stdout + out.stderr
 
 
+def chunk(c=None, **other):
+    f = dict(q=at(0), qs=1024, qt=BF16, cu=at(4), batch=2, rows=40, max_q=30, hq=8, table=at(1), max_pages=100, lens=at(2),
+             max_len=6400, window=0, sinks=0, scale=0.1, out=at(3), ws=at(500), wsb=1 << 40)
+    f.update(other)
+    c = cache() if c is None else c
+    return err(P.lib().ptq1_attn_chunk(f["q"], f["qs"], f["qt"], f["cu"], f["batch"], f["rows"], f["max_q"], f["hq"],
+                                       C.byref(c), f["table"], f["max_pages"], f["lens"], f["max_len"], f["window"],
+                                       f["sinks"], f["scale"], f["out"], f["ws"], f["wsb"], None))
+
+
+@pytest.mark.parametrize("other,status,word", [
+    (dict(window=-1), SHAPE, "window"),
+    (dict(sinks=-1), SHAPE, "sinks"),
+    (dict(batch=-1), SHAPE, "batch"),
+    (dict(rows=-1), SHAPE, "n_q_rows"),
+    (dict(max_q=-1), SHAPE, "max_q"),
+    (dict(hq=7), SHAPE, "n_q_heads"),
+    (dict(scale=float("nan")), SHAPE, "scale"),
+    (dict(max_pages=-1), SHAPE, "max_pages"),
+    (dict(max_len=6401), SHAPE, "max_len"),
+    (dict(max_pages=1 << 20, max_len=(1 << 22) + 1), UNSUPPORTED, "max_len"),
+    (dict(qt=F32), UNSUPPORTED, "q_dtype"),
+    (dict(qt=F16), UNSUPPORTED, "q_dtype"),
+    (dict(rows=1 << 31), UNSUPPORTED, "rows"),
+    (dict(batch=1 << 23), UNSUPPORTED, "tiles"),
+    (dict(q=None), NULL, "q is"),
+    (dict(cu=None), NULL, "cu_q"),
+    (dict(table=None), NULL, "block_table"),
+    (dict(lens=at(2) + 2), ALIGN, "seq_lens"),
+    (dict(q=at(0) + 8), ALIGN, "q is not"),
+    (dict(qs=1004), SHAPE, "q: row stride"),
+    (dict(qs=1028), ALIGN, "q: row stride"),
+    (dict(out=None), NULL, "out is"),
+    (dict(out=at(0) + 1024), ALIAS, "out overlaps q"),
+    (dict(out=at(200)), ALIAS, "out overlaps the cache"),
+    (dict(out=at(4)), ALIAS, "cu_q"),
+    (dict(wsb=16), WORKSPACE, "ptq1_attn_chunk"),
+    (dict(ws=None), WORKSPACE, "ptq1_attn_chunk"),
+    (dict(ws=at(100)), ALIAS, "ws overlaps"),
+    (dict(ws=at(2)), ALIAS, "ws overlaps"),
+])
+def test_chunk_refused(other, status, word):
+    rc, msg = chunk(**other)
+    assert rc == status and word in msg, msg
+
+
+def test_chunk_cache_refused():
+    for other, status, word in ((dict(dtype=F32), UNSUPPORTED, "cache dtype"), (dict(page=8), UNSUPPORTED, "page_size"),
+                                (dict(d=80), UNSUPPORTED, "head_dim"), (dict(k_pages=None), NULL, "k_pages"),
+                                (dict(dtype=I8, k_steps=None), NULL, "k_steps")):
+        rc, msg = chunk(cache(**other))
+        assert rc == status and word in msg
+    assert chunk(batch=0)[0] == 0 and chunk(rows=0, q=None, out=None)[0] == 0
+
+
+def test_chunk_workspace():
+    size = lambda *a: P.workspace_bytes("attn_chunk", *a)  # noqa: E731
+    assert size(1, 5, 5, 40, 8, 128, 200, 0, 0) == 0                 # a few steps: nothing to cut
+    few, more = size(1, 5, 5, 40, 8, 128, 8000, 0, 0), size(1, 5, 500, 40, 8, 128, 8000, 0, 0)
+    assert 0 < few == more                                           # no sequence has more queries than there are
+    assert size(1, 5, 5, 40, 8, 128, 8000, 100, 4) == 0              # a small window: nothing to cut
+    assert size(1, 65536, 65536, 40, 8, 128, 65536, 0, 0) == 0       # the tiles fill the GPU
+    assert size(-1, 5, 5, 40, 8, 128, 200, 0, 0) == 0 and size(1, 5, 5, 40, 8, 128, 200, -1, 0) == 0
+
+
+def test_chunk_arithmetic(tmp_path):
+    """ptq1_chunk.h over positions, windows and sinks: a tile's steps hold every key that one of its rows sees, each in
+    one step; in the steps that every row is said to see whole, every row sees every key; no tile has more steps than the
+    bound; the pieces of all tiles fit their number."""
+    src = tmp_path / "c.cpp"
+    src.write_text("""
+#include <cstdio>
+#include <initializer_list>
+#include "ptq1_chunk.h"
+using namespace ptq1;
+int bad(const char *what, int a, int b, int w, int s) { std::printf("%s: %d %d %d %d\\n", what, a, b, w, s); return 1; }
+int main()
+{
+    const int windows[] = {1, 2, 15, 63, 64, 65, 100, 128, 200, 400, 5000}, sinks[] = {0, 1, 16, 63, 64, 65, 130, 500};
+    for (int first = -70; first < 420; first += first < 140 ? 3 : 17)
+        for (int rows : {1, 2, 5, 26, 64, 127, 128})
+            for (int w : windows)
+                for (int s : sinks) {
+                    const int last = first + rows - 1, len = imax(0, last + 1);
+                    const ChunkSteps c = chunk_steps(first, last, w, s);
+                    if (c.steps > steps_bound(len + 50, w, s, 128 / rows)) return bad("bound", first, rows, w, s);
+                    static int in[1000];
+                    for (int j = 0; j < 1000; ++j) in[j] = 0;
+                    int before = -1;
+                    for (int i = 0; i < c.steps; ++i) {
+                        const int n0 = step_key(c, i);
+                        if (n0 <= before || n0 >= c.reach) return bad("order", first, rows, w, s);
+                        before = n0;
+                        for (int j = n0; j < n0 + kChunkKeys; ++j) in[j] += 1;
+                        // the page of a run that is looked up holds a key that some row sees
+                        for (int q = 0; q < 4; ++q) {
+                            const int r = n0 + 16 * q, tok = r < c.sunk ? r : imin(imax(r, c.lo), c.reach - 1);
+                            bool some = false, near = false;
+                            for (int j = tok & ~15; j < (tok & ~15) + 16; ++j) some |= j < c.reach && (j >= c.lo || j < c.sunk);
+                            for (int j = r; j < r + 16; ++j) near |= j < c.reach && (j >= c.lo || j < c.sunk);
+                            if (tok < 0 || tok >= len || !some || (near && tok >> 4 != r >> 4)) return bad("page", first, rows, w, s);
+                        }
+                    }
+                    for (int p = first; p <= last; p += p + 1 == last ? 1 : 1 + (last - p) / 4) {
+                        const SeenKeys k = seen_keys(p, w);
+                        for (int j = 0; j < 900; ++j) {
+                            const bool sees = j <= p && (j > p - w || j < s);
+                            if (sees != (j < k.hi && (j >= k.lo || j < s))) return bad("seen", first, rows, w, s);
+                            if (sees && in[j] != 1) return bad("missing", p, j, w, s);
+                        }
+                        for (int i = imax(0, c.all_from); i < imin(c.steps, c.all_to); ++i)
+                            for (int j = step_key(c, i); j < step_key(c, i) + kChunkKeys; ++j)
+                                if (!(j <= p && j > p - w)) return bad("whole", p, j, w, s);
+                    }
+                }
+    // pieces: per * wanted covers the total, so the pieces of tiles with these steps are at most wanted + tiles
+    for (int wanted : {1, 7, 64, 512})
+        for (int tiles : {1, 3, 100})
+            for (int steps : {0, 1, 3, 4, 5, 63, 1000, 65536}) {
+                const int per = chunk_piece(tiles * steps, wanted);
+                if (tiles * chunk_pieces(steps, per) > wanted + tiles || per < kChunkMinSteps) return bad("pieces", wanted, tiles, steps, per);
+            }
+    const ChunkSteps c = chunk_steps((1 << 22) - 5, (1 << 22) - 1, (1 << 22) + 1, 1 << 22);
+    return c.steps == 65536 && c.lo == 0 ? 0 : bad("large", c.steps, c.lo, c.reach, c.gap);
+}
+""")
+    exe = tmp_path / "c"
+    csrc = os.path.join(os.path.dirname(P.__file__), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O2", "-fsanitize=undefined", "-fno-sanitize-recover", "-I", csrc, str(src), "-o",
+                    str(exe)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert out.returncode == 0, out.stdout + out.stderr
+
+
 # ------------------------------------------------------------- the binding ----
 
 def test_binding_write_norm(host_ok):
@@ -202,15 +336,33 @@ def test_binding_window(host_ok):
         P.ptq1_attn_decode_window(q, c, t, i32(1, 2), 10, out=z(2, 4, 128))
 
 
+def test_binding_chunk(host_ok):
+    c, t, cu = kv(), torch.zeros((2, 400), dtype=torch.int32), i32(0, 3, 5)
+    q = z(5, 8, 128)
+    for bad, match in (((z(5, 8, 64), c, t, cu, i32(3, 3)), "q must be"), ((q.float(), c, t, cu, i32(3, 3)), "q must be"),
+                       ((q, c, t[:1], cu, i32(3, 3)), "block_table"), ((q, c, t, cu[:0], i32()), "cu_q must hold"),
+                       ((q, c, t, cu.long(), i32(3, 3)), "cu_q must be"), ((q, c, t, cu, i32(3, 3, 3)), "seq_lens has"),
+                       ((z(5, 128, 8).transpose(1, 2), c, t, cu, i32(3, 3)), "heads of a row")):
+        with pytest.raises(ValueError, match=match):
+            P.ptq1_attn_chunk(*bad)
+    with pytest.raises(ValueError, match="ws has"):
+        P.ptq1_attn_chunk(q, c, t, cu, i32(3, 3), ws=torch.zeros(256, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="out has"):
+        P.ptq1_attn_chunk(q, c, t, cu, i32(3, 3), out=z(5, 4, 128))
+    with pytest.raises(TypeError, match="KvCache"):
+        P.ptq1_attn_chunk(q, c.k_pages, t, cu, i32(3, 3))
+
+
 def side_calls():
     """The calls of this file over host tensors."""
     c, t = kv(), torch.zeros((2, 400), dtype=torch.int32)
     q, k, s = z(3, 8, 128), z(3, 2, 128), torch.zeros(3, dtype=torch.int64)
     return {"kv_write_norm": lambda **o: P.ptq1_kv_write_norm(q, k, k, s, c, **o),
-            "attn_decode_window": lambda **o: P.ptq1_attn_decode_window(q[:2], c, t, i32(1, 2), 3000, **o)}
+            "attn_decode_window": lambda **o: P.ptq1_attn_decode_window(q[:2], c, t, i32(1, 2), 3000, **o),
+            "attn_chunk": lambda **o: P.ptq1_attn_chunk(q, c, t, i32(0, 1, 3), i32(1, 2), **o)}
 
 
-@pytest.mark.parametrize("name", ["kv_write_norm", "attn_decode_window"])
+@pytest.mark.parametrize("name", ["kv_write_norm", "attn_decode_window", "attn_chunk"])
 def test_side_stream_allocates_its_own_memory(monkeypatch, name):
     streams = Streams(monkeypatch)
     call = side_calls()[name]
