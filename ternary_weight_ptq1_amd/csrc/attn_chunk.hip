@@ -24,10 +24,10 @@
 // a step before they are needed, two before they are read.
 //
 // int8 caches.  16-bit pieces cannot come from memory, so a step's codes pass
-// through registers and become fp16 in LDS, exactly, once for all waves.  The
-// queries enter as fp16 too, scaled to their head's largest magnitude by a
-// power of two; K's step multiplies the scores, V's step the weights, which
-// then enter the second product in units of a power of two of their row.
+// through registers and become 16-bit operands in LDS, exactly, once for all
+// waves: K's in the queries' type, V's in fp16.  K's step, with the scale,
+// multiplies the scores; V's multiplies the weights, which then enter the second
+// product in units of a power of two of their row.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -42,14 +42,17 @@ namespace {
 
 constexpr int BN = kChunkKeys;
 static_assert(kKeys == kChunkKeys, "a step is a tile of keys");
+constexpr int kAhead = 4;  // K reads ahead of their products
 constexpr int chunk_waves(int d) { return d == 256 ? 8 : 4; }
 
+// The 16-bit type of the second product over a cache of C: int8 codes and the
+// weights that meet them are fp16.  (The first product is in the queries' type.)
 template <typename C>
-struct ChunkOp {
+struct WeightOf {
     typedef C type;
 };
 template <>
-struct ChunkOp<int8_t> {
+struct WeightOf<int8_t> {
     typedef _Float16 type;
 };
 
@@ -268,20 +271,43 @@ struct ChunkPages {
     }
 };
 
-// A step's buffers in LDS; int8 caches: with the steps of its tokens (V's times
-// 2^-10: weights, up to 2^15, times them are then in fp32's range) and the
-// largest of V's.
-template <typename T>
+// A step's buffers in LDS; int8 caches: with the steps of its tokens, K's times
+// scale and log2 e, V's in units of 2^*unit, which none exceeds.
+template <typename QT, typename T>
 struct ChunkBuffer {
-    T *k, *v;
-    float *ks, *vs, *top;
+    QT *k;
+    T *v;
+    float *ks, *vs;
+    int *unit;
 };
 
+// 8 int8 codes (two dwords) as bf16, exact.
+__device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t a, uint32_t b)
+{
+    at_u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = i < 2 ? a : b;
+        const float lo = static_cast<float>(static_cast<int8_t>(x >> (16 * (i & 1)))), hi = static_cast<float>(static_cast<int8_t>(x >> (16 * (i & 1) + 8)));
+        w[i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
+    }
+    return __builtin_bit_cast(bf16x8, w);
+}
+template <typename T>
+__device__ __forceinline__ typename Op16<T>::x8 codes_to(uint32_t a, uint32_t b)
+{
+    if constexpr (std::is_same<T, __bf16>::value)
+        return codes_to_bf16(a, b);
+    else
+        return codes_to_f16(a, b);
+}
+
 // A lane's share of bringing a step's keys and values into LDS.
-template <typename C, int D>
+template <typename C, typename QT, int D>
 struct ChunkStaging {
     static constexpr bool I8 = std::is_same<C, int8_t>::value;
-    typedef typename ChunkOp<C>::type T;
+    typedef typename WeightOf<C>::type T;
+    typedef ChunkBuffer<QT, T> Buffer;
     static constexpr int W = chunk_waves(D), NT = 64 * W;
     static constexpr int NK = BN * D * static_cast<int>(sizeof(C)) / (16 * NT);  // 16-byte loads of a thread, for K and for V
     const char *kp, *vp;   // of this kv head
@@ -289,11 +315,13 @@ struct ChunkStaging {
     uint32_t page_bytes, page_cells;
     int page_shift, mask;
     at_u32x4 kr[I8 ? NK : 1], vr[I8 ? NK : 1];
-    float step = 0.0f;
+    float step = 0.0f, c;
+    int lo, reach, sunk, unit = -126;
 
-    __device__ __forceinline__ ChunkStaging(const ChunkArgs &a, int kh)
-        : page_shift(a.page_shift), mask((1 << a.page_shift) - 1)
+    __device__ __forceinline__ ChunkStaging(const ChunkArgs &a, const ChunkTile &t)
+        : page_shift(a.page_shift), mask((1 << a.page_shift) - 1), c(a.scale * kLog2e), lo(t.c.lo), reach(t.c.reach), sunk(t.c.sunk)
     {
+        const int kh = t.kh;
         page_cells = static_cast<uint32_t>(a.hkv) << page_shift;
         page_bytes = page_cells * (D * static_cast<uint32_t>(sizeof(C)));
         const int64_t first = (static_cast<int64_t>(kh) << page_shift) * (D * static_cast<int64_t>(sizeof(C)));
@@ -304,7 +332,7 @@ struct ChunkStaging {
     }
 
     // 16-bit caches: straight into LDS
-    __device__ __forceinline__ void copy(const ChunkPages &p, int n0, const ChunkBuffer<T> &to) const
+    __device__ __forceinline__ void copy(const ChunkPages &p, int n0, const Buffer &to) const
     {
         static_assert(!I8, "16 bits");
         constexpr int P = D / 8, RK = 64 / P;  // pieces of a row of K, rows of an instruction
@@ -351,15 +379,16 @@ struct ChunkStaging {
             step = (wave == 0 ? ksp : vsp)[static_cast<uint64_t>(page_cells) * static_cast<uint32_t>(p.of(lane >> 4)) + ((n0 + lane) & mask)];
     }
     // ... and as fp16 into LDS
-    __device__ __forceinline__ void store(const ChunkBuffer<T> &to) const
+    __device__ __forceinline__ void store(int n0, const Buffer &to)
     {
         constexpr int L = D / 16;
         const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
             const int r = (i * W + wave) * (64 / L) + lane / L, p = 2 * (lane % L);
-            *reinterpret_cast<f16x8 *>(to.k + place<D>(r, p)) = codes_to_f16(kr[i][0], kr[i][1]);
-            *reinterpret_cast<f16x8 *>(to.k + place<D>(r, p + 1)) = codes_to_f16(kr[i][2], kr[i][3]);
+            typedef typename Op16<QT>::x8 k8;
+            *reinterpret_cast<k8 *>(to.k + place<D>(r, p)) = codes_to<QT>(kr[i][0], kr[i][1]);
+            *reinterpret_cast<k8 *>(to.k + place<D>(r, p + 1)) = codes_to<QT>(kr[i][2], kr[i][3]);
         }
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
@@ -367,12 +396,18 @@ struct ChunkStaging {
             *reinterpret_cast<f16x8 *>(to.v + place<BN>(d, p)) = codes_to_f16(vr[i][0], vr[i][1]);
             *reinterpret_cast<f16x8 *>(to.v + place<BN>(d, p + 1)) = codes_to_f16(vr[i][2], vr[i][3]);
         }
-        if (wave == 0) to.ks[lane] = step;
+        // (the product is finite, or it would make a NaN of a sum of zero)
+        if (wave == 0) to.ks[lane] = step != step ? step : fminf(step * c, 3.4028235e38f);
         if (wave == 1) {
-            const float s = step * 0x1p-10f;
-            to.vs[lane] = s;
-            const float top = wave_max(s);
-            if (lane == 0) *to.top = top;
+            // The unit: a power of two that no step exceeds among those that
+            // some row sees, the last one's as long as it is at most 2^12 more.
+            const int key = n0 + lane;
+            const bool some = (key < reach) & ((key >= lo) | (key < sunk));
+            const float top = wave_max(some ? step : 0.0f);
+            const int e = __builtin_amdgcn_readfirstlane(static_cast<int>(__builtin_bit_cast(uint32_t, top) >> 23) - 126);  // 2^e above
+            if (e > unit || e < unit - 12) unit = e > 125 ? unit : e + 2;
+            to.vs[lane] = ldexpf(step, -unit);
+            if (lane == 0) *to.unit = unit;
         }
     }
 };
@@ -483,7 +518,7 @@ __device__ __forceinline__ void finish(const ChunkArgs &a, const ChunkTile &t, c
         o[i] *= f;
         if constexpr (std::is_same<C, int8_t>::value) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[i][j] = ldexpf(o[i][j], unit + 10);
+            for (int j = 0; j < 16; ++j) o[i][j] = ldexpf(o[i][j], unit);
         }
     }
     if constexpr (!std::is_same<C, int8_t>::value)
@@ -491,96 +526,79 @@ __device__ __forceinline__ void finish(const ChunkArgs &a, const ChunkTile &t, c
     if (row.is) store_rows<QT, N>(a, t, row, at, d, d0, half, o, m, l);
 }
 
-// One lane's row as the products' B operand (k = 16 kk + 8 half + j) and the
-// factors that turn its sums into scores in units of log2: scores are sum * c
-// (int8: * the token's step * far).
-template <typename C, typename QT, int D>
+// One lane's row as the products' B operand (k = 16 kk + 8 half + j).
+template <typename QT, int D>
 struct ChunkQuery {
-    static constexpr bool I8 = std::is_same<C, int8_t>::value;
-    typedef typename ChunkOp<C>::type T;
-    typedef typename Op16<T>::x8 x8;
-    static constexpr int KK = D / 16;
-    x8 f[KK];
-    float c, far = 1.0f;
+    typename Op16<QT>::x8 f[D / 16];
     __device__ __forceinline__ ChunkQuery(const ChunkArgs &a, const ChunkTile &t, const ChunkRow &row, int half)
     {
-        typedef QT q8 __attribute__((ext_vector_type(8)));
         const QT *qp = static_cast<const QT *>(a.q) + (static_cast<int64_t>(t.q0) + row.tok) * a.qs + static_cast<int64_t>(row.head) * D;
-        c = a.scale * kLog2e;
-        if constexpr (!I8) {
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk) f[kk] = *reinterpret_cast<const x8 *>(qp + 16 * kk + 8 * half);
-        } else {
-            q8 raw[KK];
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk) raw[kk] = *reinterpret_cast<const q8 *>(qp + 16 * kk + 8 * half);
-            uint32_t mx = 0;  // of the bit patterns: NaN and infinity last
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float x = static_cast<float>(raw[kk][j]);
-                    mx = max(mx, __builtin_bit_cast(uint32_t, x) & 0x7fffffffu);
-                }
-            mx = max(mx, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mx), 32, 64)));
-            // the largest magnitude in [2^14, 2^15): bf16 elements down to 2^-21
-            // of it enter exactly, smaller ones to 2^-39 of it
-            const int shift = 15 - __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, mx));
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[kk][j] = static_cast<_Float16>(ldexpf(static_cast<float>(raw[kk][j]), shift));
-            // sums are below 2^30; c comes first and a step (below 2^122) second,
-            // so c keeps what makes the first factor neither overflow nor lose
-            // bits, and `far` the rest of a power of two beyond that
-            const int all = __builtin_amdgcn_frexp_expf(c) - shift, here = min(max(all, -125), 80);
-            c = ldexpf(__builtin_amdgcn_frexp_mantf(c), here);
-            far = ldexpf(1.0f, min(max(all - here, -126), 127));
-            if (mx >= 0x7f800000u) c = __builtin_nanf("");  // a NaN or an infinity in the query
-        }
+        for (int kk = 0; kk < D / 16; ++kk) f[kk] = *reinterpret_cast<const typename Op16<QT>::x8 *>(qp + 16 * kk + 8 * half);
     }
 };
 
-// The step's weights of KT * 32 keys from key n0 on, of one lane's row (score
+// Which keys of a step a row does not see.
+struct HiddenKeys {
+    int hi, lo, sinks;
+    bool gap;  // (of any row) first keys that are seen beside the window are among them
+    __device__ __forceinline__ HiddenKeys(const SeenKeys &seen, const ChunkTile &t, int n0)
+        : hi(seen.hi), lo(seen.lo), sinks(t.c.sunk), gap(n0 < t.c.sunk)
+    {
+    }
+    // (no branches in these: a value that one selects is lost by the compiler)
+    __device__ __forceinline__ bool beside_gap(int key) const { return (key >= hi) | ((key < lo) & (key >= sinks)); }
+    __device__ __forceinline__ bool without_gap(int key) const
+    {
+        return static_cast<uint32_t>(key - lo) >= static_cast<uint32_t>(hi - lo);
+    }
+};
+
+// The weights of KT * 32 keys from key n0 on, of one lane's row (score
 // register j of tile t: key n0 + 32 t + 16 (j / 8) + 8 half + j % 8).
 //
-// int8 caches: a weight times its value's step enters in units of 2^unit, in
-// which it is below 2^15.  In steps that every row sees whole, where the
-// largest step is at most one unit, that holds as it is; elsewhere the unit
-// goes by the products themselves, by at most 2^10 more than these need (so
-// that steps of about one size are not looked at again): what is lost is
-// below 2^-28 of the row's largest.
+// int8 caches: a weight times its value's step, in the step's unit, is p vs; o
+// is in units of 2^unit of its row.  Where the two units are the same in all
+// rows, that is all; elsewhere (the first steps, after the reference has moved,
+// where steps differ much, and on the border) the row's unit goes by the
+// products themselves, so that they are below 2^15, by at most 2^12 more than
+// they need: what is lost is below 2^-27 of the row's largest.
 template <typename C, int KT>
 struct ChunkSoftmax {
     static constexpr bool I8 = std::is_same<C, int8_t>::value;
-    typedef typename ChunkOp<C>::type T;
+    typedef typename WeightOf<C>::type T;
     typedef typename Op16<T>::x8 x8;
     float m = -__builtin_inff(), l = 0.0f, l2 = 0.0f;  // m: the reference, in units of log2
     bool large = false;
-    int unit = -112;
+    int unit = -126;
 
     static __device__ __forceinline__ int key(int t, int j, int half) { return 32 * t + 16 * (j >> 3) + 8 * half + (j & 7); }
 
     // the largest score of the lane's pair; hidden ones leave the scores
     template <bool BORDER>
-    __device__ __forceinline__ float top(at_f32x16 (&s)[KT], const SeenKeys &seen, int sinks, int n0, int half, float c, float far,
-                                         const float *ks)
+    __device__ __forceinline__ float top(at_f32x16 (&s)[KT], const HiddenKeys &hidden, int n0, int half, float c, const float *ks)
     {
         if constexpr (I8) {
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) s[t][j] = s[t][j] * c * ks[key(t, j, half)];
-            if (__ballot(far != 1.0f) != 0) {
-#pragma unroll
-                for (int t = 0; t < KT; ++t) s[t] *= far;
-            }
+                for (int j = 0; j < 16; ++j) {
+                    s[t][j] *= ks[key(t, j, half)];
+                    if ((j & 7) == 7) __builtin_amdgcn_sched_barrier(0);  // (or all steps are read up front)
+                }
         }
         if constexpr (BORDER) {
+            if (hidden.gap) {
 #pragma unroll
-            for (int t = 0; t < KT; ++t)
+                for (int t = 0; t < KT; ++t)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) s[t][j] = hidden(seen, sinks, n0 + key(t, j, half)) ? -__builtin_inff() : s[t][j];
+                    for (int j = 0; j < 16; ++j) s[t][j] = hidden.beside_gap(n0 + key(t, j, half)) ? -__builtin_inff() : s[t][j];
+            } else {
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) s[t][j] = hidden.without_gap(n0 + key(t, j, half)) ? -__builtin_inff() : s[t][j];
+            }
         }
         float top = s[0][0];
 #pragma unroll
@@ -589,10 +607,6 @@ struct ChunkSoftmax {
             for (int j = 0; j < 16; ++j) top = fmaxf(top, s[t][j]);
         top = lane_pair_max<32>(top);
         return I8 ? top : top * c;
-    }
-    static __device__ __forceinline__ bool hidden(const SeenKeys &seen, int sinks, int key)
-    {
-        return (key >= seen.hi) | ((key < seen.lo) & (key >= sinks));
     }
 
     // The reference follows the largest score, by 8 at most behind it (weights
@@ -607,13 +621,13 @@ struct ChunkSoftmax {
             l *= f;
             l2 *= f;
             if constexpr (I8) {
-                // the unit comes down with the weights, or a large step whose
+                // the units come down with the weights, or a large step whose
                 // weight has become nothing would keep the resolution coarse
                 int down = static_cast<int>(__builtin_bit_cast(uint32_t, f) >> 23) - 126;  // f < 2^down
-                down = down > 0 ? 0 : down < -112 - units ? -112 - units : down;
+                down = down > 0 ? 0 : down;
                 f *= pow2(-down);
-                if (&units != &unit) unit = max(unit + down, -112);
-                units += down;
+                if (&units != &unit) unit = max(unit + down, -300);
+                units = max(units + down, -300);
             }
 #pragma unroll
             for (int i = 0; i < N; ++i) o[i] *= f;
@@ -646,14 +660,12 @@ struct ChunkSoftmax {
         }
     }
 
-    // int8 caches: weights times steps, in units; rescale(f): the unit has become 1 / f of what it was
+    // int8 caches: weights times steps; rescale(f): o's unit has become 1 / f of what it was
     template <bool BORDER, class F>
-    __device__ __forceinline__ void products(at_f32x16 (&s)[KT], const SeenKeys &seen, int sinks, int n0, int half,
-                                             const float *vs, float vtop, x8 (&pf)[2 * KT], F rescale)
+    __device__ __forceinline__ void products(at_f32x16 (&s)[KT], const HiddenKeys &hidden, int n0, int half, const float *vs,
+                                             int of_steps, x8 (&pf)[2 * KT], F rescale)
     {
         const float ms = m == -__builtin_inff() ? 0.0f : m;
-        float seen_top = vtop;
-        if constexpr (BORDER) seen_top = 0.0f;
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -661,50 +673,78 @@ struct ChunkSoftmax {
                 const float p = __builtin_amdgcn_exp2f(s[t][j] - ms);
                 if ((j & 1) == 0) l += p;
                 else l2 += p;
-                float step = vs[key(t, j, half)];
-                if constexpr (BORDER) {
-                    step = hidden(seen, sinks, n0 + key(t, j, half)) ? 0.0f : step;
-                    seen_top = fmaxf(seen_top, step);
-                }
-                s[t][j] = p * step;
+                s[t][j] = p * vs[key(t, j, half)];
+                if ((j & 7) == 7) __builtin_amdgcn_sched_barrier(0);
             }
-        if (BORDER || __ballot(!(vtop <= pow2(unit))) != 0) {
+        if constexpr (BORDER) {
+            // a weight of nothing leaves a NaN as it is: of a step that the row does not see
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[t][j] = hidden.beside_gap(n0 + key(t, j, half)) ? 0.0f : s[t][j];
+        }
+        if (BORDER || __ballot(unit != of_steps) != 0) {
             float top = s[0][0];
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) top = fmaxf(top, s[t][j]);
             top = lane_pair_max<32>(top);
-            if constexpr (BORDER) seen_top = lane_pair_max<32>(seen_top);
-            // 2^e above each
-            const int need = static_cast<int>(__builtin_bit_cast(uint32_t, top) >> 23) - 126 - 15;
-            const int step = static_cast<int>(__builtin_bit_cast(uint32_t, seen_top) >> 23) - 126;
-            const int next = min(max(need, min(step, need + 10)), 111);
+            // (2^e above the largest)
+            const int need = static_cast<int>(__builtin_bit_cast(uint32_t, top) >> 23) - 126 - 15 + of_steps;
+            const int next = max(need, min(of_steps, need + 12));
             if (next > unit) {
-                rescale(pow2(max(unit - next, -126)));
+                rescale(ldexpf(1.0f, unit - next));
                 unit = next;
             }
+            const int by = of_steps - unit;
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[t][j] = ldexpf(s[t][j], by);
         }
-        const float in_units = pow2(-unit);
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) pf[2 * t + (j >> 3)][j & 7] = static_cast<T>(s[t][j] * in_units);
+            for (int j = 0; j < 16; ++j) pf[2 * t + (j >> 3)][j & 7] = static_cast<T>(s[t][j]);
     }
 };
+
+// The steps first .. last in pairs (a buffer each): in the inner loops those
+// whose keys every row sees, and the others.
+template <class F>
+__device__ __forceinline__ void run_steps(const ChunkTile &t, const F &step)
+{
+    int i = t.first;
+    const int whole = t.c.all_to < t.last ? t.c.all_to : t.last;
+    while (i < t.last) {
+        for (; i < t.last && (i < t.c.all_from || i + 2 > whole); i += 2) {
+            step(std::true_type{}, std::false_type{}, i);
+            if (i + 1 < t.last) step(std::true_type{}, std::true_type{}, i + 1);
+        }
+        for (; i + 2 <= whole; i += 2) {
+            step(std::false_type{}, std::false_type{}, i);
+            step(std::false_type{}, std::true_type{}, i + 1);
+        }
+    }
+}
 
 template <typename C, typename QT, int D>
 __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs a)
 {
-    typedef typename ChunkOp<C>::type T;
+    typedef typename WeightOf<C>::type T;
     typedef typename Op16<T>::x8 x8;
+    typedef ChunkBuffer<QT, T> Buffer;
     constexpr bool I8 = std::is_same<C, int8_t>::value;
     constexpr int KT = BN / 32, DT = D / 32, KK = D / 16;
 
     // two buffers: separate objects, so that the copies into one need not have
     // ended before the other is read
-    __shared__ __attribute__((aligned(16))) T kt0[BN * D], kt1[BN * D], vt0[BN * D], vt1[BN * D];
-    __shared__ float steps[I8 ? 4 * BN + 2 : 1];
+    __shared__ __attribute__((aligned(16))) QT kt0[BN * D], kt1[BN * D];
+    __shared__ __attribute__((aligned(16))) T vt0[BN * D], vt1[BN * D];
+    __shared__ float steps[I8 ? 4 * BN : 1];
+    __shared__ int step_units[2];
+    __shared__ SeenKeys seen_of[kChunkRows];  // (in registers it would be in the way of the inner steps)
     __shared__ ChunkNotes notes;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -712,14 +752,13 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
     ChunkTile t;
     if (!chunk_tile<QT, D>(a, blockIdx.x, false, t)) return;
     const bool idle = t.row0 + 32 * wave >= t.rows;  // no row of this wave's is there
-    const int at = t.row0 + 32 * wave + col;
-    const ChunkRow row = chunk_row(a, t, at);
     ChunkPages pages(a, t);
-    ChunkStaging<C, D> staging(a, t.kh);
-    const ChunkBuffer<T> b0{kt0, vt0, steps, steps + BN, steps + 4 * BN};
-    const ChunkBuffer<T> b1{kt1, vt1, steps + 2 * BN, steps + 3 * BN, steps + 4 * BN + 1};
+    ChunkStaging<C, QT, D> staging(a, t);
     if (t.first < t.last) pages.find(step_key(t.c, t.first));
-    const ChunkQuery<C, QT, D> q(a, t, row, half);
+    const float c = a.scale * kLog2e;
+    const ChunkRow first_row = chunk_row(a, t, t.row0 + 32 * wave + col);
+    seen_of[32 * wave + col] = first_row.seen;
+    const ChunkQuery<QT, D> q(a, t, first_row, half);
     if (threadIdx.x == 0) notes = {1 << 30, 0, 0};
 
     at_f32x16 o[DT];
@@ -729,8 +768,12 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
     ChunkSoftmax<C, KT> w;
 
-    auto step = [&](auto border, int i, const ChunkBuffer<T> &b, const ChunkBuffer<T> &next) __attribute__((always_inline)) {
+    // One step, while the next one's keys and values arrive in the other buffers.
+    auto step = [&](auto border, auto odd, int i) __attribute__((always_inline)) {
         constexpr bool BORDER = decltype(border)::value;  // some row may not see some key of the step
+        constexpr bool ODD = decltype(odd)::value;
+        const Buffer b{ODD ? kt1 : kt0, ODD ? vt1 : vt0, steps + (ODD ? 2 * BN : 0), steps + (ODD ? 3 * BN : BN), step_units + ODD};
+        const Buffer next{ODD ? kt0 : kt1, ODD ? vt0 : vt1, steps + (ODD ? 0 : 2 * BN), steps + (ODD ? BN : 3 * BN), step_units + !ODD};
         const int n0 = step_key(t.c, i);
         if (i + 1 < t.last) {
             pages.use();
@@ -738,8 +781,10 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
                 staging.load(pages, step_key(t.c, i + 1));
             else
                 staging.copy(pages, step_key(t.c, i + 1), next);
-            if (i + 2 < t.last) pages.find(step_key(t.c, i + 2));
         }
+        pages.find(step_key(t.c, min(i + 2, t.last - 1)));  // (in no branch, at whose end the compiler would wait for it)
+        SeenKeys seen{0, 0};
+        if constexpr (BORDER) seen = seen_of[32 * wave + col];
         x8 pf[2 * KT];
         if (!idle) {
             at_f32x16 s[KT];
@@ -749,19 +794,28 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
                 for (int j = 0; j < 16; ++j) s[k][j] = 0.0f;
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
-                    const x8 kf = *reinterpret_cast<const x8 *>(b.k + place<D>(32 * k + token_of_row(col), 2 * kk + half));
-                    s[k] = Op16<T>::mfma32(kf, q.f[kk], s[k]);
+                    typedef typename Op16<QT>::x8 k8;
+                    const k8 kf = *reinterpret_cast<const k8 *>(b.k + place<D>(32 * k + token_of_row(col), 2 * kk + half));
+                    s[k] = Op16<QT>::mfma32(kf, q.f[kk], s[k]);
                 }
             }
-            const float top = w.template top<BORDER>(s, row.seen, a.sinks, n0, half, q.c, q.far, b.ks);
-            w.raise(top, o, w.unit);
-            if constexpr (I8)
-                w.template products<BORDER>(s, row.seen, a.sinks, n0, half, b.vs, *b.top, pf, [&](float f) {
+            // the K reads run ahead of the products
+            __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+            for (int k = 0; k < KT * KK - kAhead; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x8, kAhead, 0);
+            w.raise(w.template top<BORDER>(s, HiddenKeys(seen, t, n0), n0, half, c, b.ks), o, w.unit);
+            if constexpr (I8) {
+                if constexpr (BORDER) asm volatile("" : "+v"(seen.lo), "+v"(seen.hi));  // (or the masks of 64 keys are kept)
+                w.template products<BORDER>(s, HiddenKeys(seen, t, n0), n0, half, b.vs, *b.unit, pf, [&](float f) {
 #pragma unroll
                     for (int d = 0; d < DT; ++d) o[d] *= f;
                 });
-            else
-                w.weights(s, q.c, pf);
+            } else
+                w.weights(s, c, pf);
         }
         if constexpr (BORDER && !I8) {
             // a zero weight would not keep a NaN or an infinity out of the rows
@@ -781,36 +835,30 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
                     o[d] = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(b.v + place<BN>(32 * d + col, 2 * u + half)), pf[u], o[d]);
         }
         if constexpr (I8)
-            if (i + 1 < t.last) staging.store(next);
+            if (i + 1 < t.last) staging.store(step_key(t.c, i + 1), next);
         __syncthreads();
     };
 
     if (t.first < t.last) {
+        const int n0 = step_key(t.c, t.first);
+        const Buffer b{kt0, vt0, steps, steps + BN, step_units};
         pages.use();
         if constexpr (I8) {
-            staging.load(pages, step_key(t.c, t.first));
-            staging.store(b0);
+            staging.load(pages, n0);
+            staging.store(n0, b);
         } else
-            staging.copy(pages, step_key(t.c, t.first), b0);
-        if (t.first + 1 < t.last) pages.find(step_key(t.c, t.first + 1));
+            staging.copy(pages, n0, b);
+        pages.find(step_key(t.c, min(t.first + 1, t.last - 1)));
     }
     __syncthreads();
-    const auto turn = [&](int i, const ChunkBuffer<T> &b, const ChunkBuffer<T> &next) __attribute__((always_inline)) {
-        if (i >= t.c.all_from && i < t.c.all_to)
-            step(std::false_type{}, i, b, next);
-        else
-            step(std::true_type{}, i, b, next);
-    };
-    for (int i = t.first; i < t.last; i += 2) {
-        turn(i, b0, b1);
-        if (i + 1 >= t.last) break;
-        turn(i + 1, b1, b0);
-    }
+    run_steps(t, step);
     if (__ballot(pages.bad) != 0 && lane == 0) notes.bad = 1;
     __syncthreads();
     if (idle) return;
-    const float l = lane_pair_sum<32>(w.l + w.l2);
-    finish<C, QT, DT>(a, t, row, notes, at, D, 0, half, o, w.m, l, w.unit);
+    // the row anew: kept through the loops it takes registers that the reads run ahead in
+    int again = t.row0 + 32 * wave + col;
+    asm volatile("" : "+v"(again));
+    finish<C, QT, DT>(a, t, chunk_row(a, t, again), notes, again, D, 0, half, o, w.m, lane_pair_sum<32>(w.l + w.l2), w.unit);
 }
 
 // The same for 256-wide heads, whose O^T and queries for 32 rows take 192
@@ -821,15 +869,19 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
 template <typename C, typename QT>
 __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(ChunkArgs a)
 {
-    typedef typename ChunkOp<C>::type T;
+    typedef typename WeightOf<C>::type T;
     typedef typename Op16<T>::x8 x8;
+    typedef ChunkBuffer<QT, T> Buffer;
     constexpr bool I8 = std::is_same<C, int8_t>::value;
     constexpr int D = 256, DT = 4, KK = D / 16;
-    __shared__ __attribute__((aligned(16))) T kt0[BN * D], kt1[BN * D], vt0[BN * D], vt1[BN * D];
+    __shared__ __attribute__((aligned(16))) QT kt0[BN * D], kt1[BN * D];
+    __shared__ __attribute__((aligned(16))) T vt0[BN * D], vt1[BN * D];
     __shared__ x8 weights[4][4][64];   // [pair][k-step of 16 keys][lane]
     __shared__ float tops[4][2][32];   // [pair][key half][row]
     __shared__ int units[I8 ? 4 : 1][2][32];
-    __shared__ float steps[I8 ? 4 * BN + 2 : 1];
+    __shared__ float steps[I8 ? 4 * BN : 1];
+    __shared__ int step_units[2];
+    __shared__ SeenKeys seen_of[kChunkRows];
     __shared__ ChunkNotes notes;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -838,14 +890,13 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
     ChunkTile t;
     if (!chunk_tile<QT, D>(a, blockIdx.x, false, t)) return;
     const bool idle = t.row0 + 32 * pair >= t.rows;
-    const int at = t.row0 + 32 * pair + col;
-    const ChunkRow row = chunk_row(a, t, at);
     ChunkPages pages(a, t);
-    ChunkStaging<C, D> staging(a, t.kh);
-    const ChunkBuffer<T> b0{kt0, vt0, steps, steps + BN, steps + 4 * BN};
-    const ChunkBuffer<T> b1{kt1, vt1, steps + 2 * BN, steps + 3 * BN, steps + 4 * BN + 1};
+    ChunkStaging<C, QT, D> staging(a, t);
     if (t.first < t.last) pages.find(step_key(t.c, t.first));
-    const ChunkQuery<C, QT, D> q(a, t, row, half);
+    const float c = a.scale * kLog2e;
+    const ChunkRow first_row = chunk_row(a, t, t.row0 + 32 * pair + col);
+    seen_of[32 * pair + col] = first_row.seen;
+    const ChunkQuery<QT, D> q(a, t, first_row, half);
     if (threadIdx.x == 0) notes = {1 << 30, 0, 0};
 
     at_f32x16 o[DT];  // dimensions 128 part + 32 i + ...
@@ -854,10 +905,13 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
     ChunkSoftmax<C, 1> w;  // l: of this wave's keys
-    int o_unit = -112;
+    int o_unit = -126;
 
-    auto step = [&](auto border, int i, const ChunkBuffer<T> &b, const ChunkBuffer<T> &next) __attribute__((always_inline)) {
+    auto step = [&](auto border, auto odd, int i) __attribute__((always_inline)) {
         constexpr bool BORDER = decltype(border)::value;
+        constexpr bool ODD = decltype(odd)::value;
+        const Buffer b{ODD ? kt1 : kt0, ODD ? vt1 : vt0, steps + (ODD ? 2 * BN : 0), steps + (ODD ? 3 * BN : BN), step_units + ODD};
+        const Buffer next{ODD ? kt0 : kt1, ODD ? vt0 : vt1, steps + (ODD ? 0 : 2 * BN), steps + (ODD ? BN : 3 * BN), step_units + !ODD};
         const int n0 = step_key(t.c, i), mine = n0 + 32 * part;
         if (i + 1 < t.last) {
             pages.use();
@@ -865,17 +919,28 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
                 staging.load(pages, step_key(t.c, i + 1));
             else
                 staging.copy(pages, step_key(t.c, i + 1), next);
-            if (i + 2 < t.last) pages.find(step_key(t.c, i + 2));
         }
+        pages.find(step_key(t.c, min(i + 2, t.last - 1)));
+        SeenKeys seen{0, 0};
+        if constexpr (BORDER) seen = seen_of[32 * pair + col];
         at_f32x16 s[1];
         float top = 0.0f;
         if (!idle) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) s[0][j] = 0.0f;
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
-                s[0] = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(b.k + place<D>(32 * part + token_of_row(col), 2 * kk + half)), q.f[kk], s[0]);
-            top = w.template top<BORDER>(s, row.seen, a.sinks, mine, half, q.c, q.far, b.ks + 32 * part);
+            for (int kk = 0; kk < KK; ++kk) {
+                typedef typename Op16<QT>::x8 k8;
+                s[0] = Op16<QT>::mfma32(*reinterpret_cast<const k8 *>(b.k + place<D>(32 * part + token_of_row(col), 2 * kk + half)), q.f[kk], s[0]);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+            for (int k = 0; k < KK - kAhead; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x8, kAhead, 0);
+            top = w.template top<BORDER>(s, HiddenKeys(seen, t, n0), mine, half, c, b.ks + 32 * part);
             if (half == 0) tops[pair][part][col] = top;
         }
         barrier_lds();
@@ -884,10 +949,11 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
             w.raise(top, o, o_unit);  // the same in both waves
             x8 pf[2];
             if constexpr (I8) {
-                w.template products<BORDER>(s, row.seen, a.sinks, mine, half, b.vs + 32 * part, *b.top, pf, [](float) {});
+                if constexpr (BORDER) asm volatile("" : "+v"(seen.lo), "+v"(seen.hi));
+                w.template products<BORDER>(s, HiddenKeys(seen, t, n0), mine, half, b.vs + 32 * part, *b.unit, pf, [](float) {});
                 if (half == 0) units[pair][part][col] = w.unit;
             } else
-                w.weights(s, q.c, pf);
+                w.weights(s, c, pf);
             weights[pair][2 * part][lane] = pf[0];
             weights[pair][2 * part + 1][lane] = pf[1];
         }
@@ -904,7 +970,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
                 const int u0 = units[pair][0][col], u1 = units[pair][1][col];
                 const int now = max(o_unit, max(u0, u1));
                 if (__ballot(now > o_unit) != 0) {
-                    const float f = pow2(max(o_unit - now, -126));
+                    const float f = ldexpf(1.0f, o_unit - now);
 #pragma unroll
                     for (int d = 0; d < DT; ++d) o[d] *= f;
                     o_unit = now;
@@ -917,38 +983,30 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
             for (int u = 0; u < 4; ++u) {
                 x8 p = weights[pair][u][lane];
                 if constexpr (I8)
-                    if (__ballot(behind[u >> 1] != 0) != 0) p *= static_cast<T>(pow2(max(behind[u >> 1], -30)));
+                    if (__ballot(behind[u >> 1] != 0) != 0) p *= static_cast<T>(ldexpf(1.0f, behind[u >> 1]));
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
                     o[d] = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(b.v + place<BN>(128 * part + 32 * d + col, 2 * u + half)), p, o[d]);
             }
         }
         if constexpr (I8)
-            if (i + 1 < t.last) staging.store(next);
+            if (i + 1 < t.last) staging.store(step_key(t.c, i + 1), next);
         barrier_copies();  // all have read, the next step is there
     };
 
     if (t.first < t.last) {
+        const int n0 = step_key(t.c, t.first);
+        const Buffer b{kt0, vt0, steps, steps + BN, step_units};
         pages.use();
         if constexpr (I8) {
-            staging.load(pages, step_key(t.c, t.first));
-            staging.store(b0);
+            staging.load(pages, n0);
+            staging.store(n0, b);
         } else
-            staging.copy(pages, step_key(t.c, t.first), b0);
-        if (t.first + 1 < t.last) pages.find(step_key(t.c, t.first + 1));
+            staging.copy(pages, n0, b);
+        pages.find(step_key(t.c, min(t.first + 1, t.last - 1)));
     }
     barrier_copies();
-    const auto turn = [&](int i, const ChunkBuffer<T> &b, const ChunkBuffer<T> &next) __attribute__((always_inline)) {
-        if (i >= t.c.all_from && i < t.c.all_to)
-            step(std::false_type{}, i, b, next);
-        else
-            step(std::true_type{}, i, b, next);
-    };
-    for (int i = t.first; i < t.last; i += 2) {
-        turn(i, b0, b1);
-        if (i + 1 >= t.last) break;
-        turn(i + 1, b1, b0);
-    }
+    run_steps(t, step);
     if (__ballot(pages.bad) != 0 && lane == 0) notes.bad = 1;
     // the pair's sums
     float l = lane_pair_sum<32>(w.l + w.l2);
@@ -957,7 +1015,9 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
     __syncthreads();
     if (idle) return;
     l = tops[pair][0][col] + tops[pair][1][col];
-    finish<C, QT, DT>(a, t, row, notes, at, D, 128 * part, half, o, w.m, l, o_unit);
+    int again = t.row0 + 32 * pair + col;
+    asm volatile("" : "+v"(again));
+    finish<C, QT, DT>(a, t, chunk_row(a, t, again), notes, again, D, 128 * part, half, o, w.m, l, o_unit);
 }
 
 // Joins the parts of the tiles that were cut: D / 4 lanes per row, one row each
