@@ -71,6 +71,7 @@ struct ChunkArgs {
     void *out;
     int32_t wanted, cut;       // pieces of one kv head that fill the GPU; tiles may be cut
     int32_t places, slot_rows; // of parts, of one kv head, and rows of one
+    float join_cost, piece_cost;  // in steps
     int64_t rows_floats;
     float *parts;
 };
@@ -83,10 +84,18 @@ __device__ __forceinline__ int swizzle(int r)
 {
     return W >= 128 ? r & 15 : (r >> 1) & 7;
 }
+// The byte offset of piece 0 of row r; piece p is at it ^ 16 p.
 template <int W>
-__device__ __forceinline__ int place(int r, int p)
+__device__ __forceinline__ int row_start(int r)
 {
-    return r * W + ((p ^ swizzle<W>(r)) << 3);
+    return r * (2 * W) + 16 * swizzle<W>(r);
+}
+// The value, which the compiler then makes anew where it is used: what every
+// step makes of a lane's place it would keep in registers through all of them.
+__device__ __forceinline__ int not_kept(int v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
 }
 // The token of row r of a score tile of 32: bits 2 and 3 change places.
 __device__ __forceinline__ int token_of_row(int r) { return (r & 19) | ((r & 4) << 1) | ((r & 8) >> 1); }
@@ -115,11 +124,33 @@ __device__ __forceinline__ int seq_steps(const ChunkArgs &a, const ChunkSeq &s, 
     return refused(a, s) ? 0 : steps_bound(s.len, a.window, a.sinks, group);
 }
 
-__device__ __forceinline__ int wave_total(int v)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp(int v)
 {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-    return __builtin_amdgcn_readfirstlane(v);
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);  // (0 where there is no such lane)
+}
+// The sum of the lanes up to and with this one's.
+__device__ __forceinline__ int lanes_to(int v)
+{
+    v += dpp<0x111, 0xF>(v);  // one lane down its row of 16, two ...
+    v += dpp<0x112, 0xF>(v);
+    v += dpp<0x114, 0xF>(v);
+    v += dpp<0x118, 0xF>(v);
+    v += dpp<0x142, 0xA>(v);  // the last of row 0 to row 1, of 2 to 3
+    v += dpp<0x143, 0xC>(v);  // of row 1 to rows 2 and 3
+    return v;
+}
+__device__ __forceinline__ int wave_total(int v) { return __builtin_amdgcn_readlane(lanes_to(v), 63); }
+// The largest, of numbers that are not negative.
+__device__ __forceinline__ int wave_largest(int v)
+{
+    v = max(v, dpp<0x111, 0xF>(v));
+    v = max(v, dpp<0x112, 0xF>(v));
+    v = max(v, dpp<0x114, 0xF>(v));
+    v = max(v, dpp<0x118, 0xF>(v));
+    v = max(v, dpp<0x142, 0xA>(v));
+    v = max(v, dpp<0x143, 0xC>(v));
+    return __builtin_amdgcn_readlane(v, 63);
 }
 // The sum of f(sequence) over the first n.
 template <class F>
@@ -130,89 +161,175 @@ __device__ __forceinline__ int sum_over(const ChunkArgs &a, int64_t n, F f)
     return wave_total(v);
 }
 
-// One tile of 128 query rows of one kv head, and the steps of one workgroup.
+// One tile of query rows of one kv head, and the steps of one workgroup.
 struct ChunkTile {
     int group, kh;
-    int64_t b;
+    int b;
     int q0, off;             // the sequence's first row; keys before its first query
     int rows, row0, end;     // its rows; this tile's first one and the one behind its last
     ChunkSteps c;
     int first, last;         // this workgroup's steps
-    int pieces, number;      // of the tile; the first piece's number among all of a kv head
-    int stride;              // between the numbers of its pieces
+    int pieces;              // of the tile
+    int place, stride;       // of the piece's part (join: of the first one's), and between them
 };
 
+// The numbers of the lanes before this one, and all lanes' together.
+__device__ __forceinline__ int lanes_before(int mine, int &total)
+{
+    const int sum = lanes_to(mine);
+    total = __builtin_amdgcn_readlane(sum, 63);
+    return sum - mine;
+}
+
+// Which tile and piece workgroup `number` of a kv head takes (join: which tile
+// of those that were cut), by the sequences' tiles and steps; false: none.
+//
+// Up to 64 sequences (a lane each): tiles are numbered from the longest
+// sequence on.  Where all are about equally long (0.6 of the longest on
+// average), whole rounds of tiles run uncut, and those behind them are cut in
+// the number that is estimated to end soonest: rounds of pieces, in steps, and
+// what a piece's rows and the join cost, in steps too.  Otherwise tiles are
+// only cut that are longer than an even share, into pieces of that: shorter
+// ones fill the gaps as they are.
+// More sequences: in their order, all cut, or none.
+struct ChunkPick {
+    ChunkSeq s;
+    int b, tiles, tile, piece, per, place, stride;
+};
+__device__ __forceinline__ bool pick_of_64(const ChunkArgs &a, int number, int group, bool join, ChunkPick &k)
+{
+    const int lane = threadIdx.x & 63, n = static_cast<int>(a.batch);
+    ChunkSeq s{0, 0, 0};
+    int tiles = 0, steps = 0;
+    if (lane < n) {
+        s = chunk_seq(a, lane);
+        tiles = seq_tiles(a, s, group);
+        steps = seq_steps(a, s, group);
+    }
+    int before = 0, all = 0;
+    for (int j = 0; j < n; ++j) {
+        const int t = __builtin_amdgcn_readlane(tiles, j), other = __builtin_amdgcn_readlane(steps, j);
+        all += t;
+        if (other > steps || (other == steps && j < lane)) before += t;
+    }
+    int whole = all, per = 1 << 30;
+    if (a.cut) {
+        const int total = wave_total(tiles * steps), longest = wave_largest(steps);
+        const int full = all / a.wanted * a.wanted, left = wave_total(max(0, min(tiles, before + tiles - full)) * steps);
+        if (10 * static_cast<int64_t>(total) < 6 * static_cast<int64_t>(all) * longest) {
+            whole = 0;
+            per = chunk_piece(total, a.wanted);
+        } else if (10 * static_cast<int64_t>(left) >= 6 * static_cast<int64_t>(all - full) * longest) {
+            const int n = chunk_cuts(all - full, longest, a.wanted, a.join_cost, a.piece_cost);
+            if (n > 1) {
+                whole = full;
+                per = imax(kChunkMinSteps, (longest + n - 1) / n);
+            }
+        }
+    }
+    const int rest = max(0, min(tiles, before + tiles - whole));  // its tiles that may be cut
+    k.per = per;
+    k.piece = 0;
+    int who;
+    if (!join && number < whole) {
+        k.per = 1 << 30;
+        who = __builtin_ctzll(__ballot(number >= before && number - before < tiles));
+        k.tile = number - __builtin_amdgcn_readlane(before, who);
+        k.place = 0;
+        k.stride = 0;
+    } else {
+        if (!join) number -= whole;
+        // (places for parts: of the tiles that are cut alone)
+        const int pieces = chunk_pieces(steps, per), numbers = rest * pieces;
+        int total, places;
+        const int place = lanes_before(pieces > 1 ? numbers : 0, places), from = lanes_before(join ? rest : numbers, total);
+        if (number >= total || places > a.places) return false;
+        who = __builtin_ctzll(__ballot(number >= from && number - from < (join ? rest : numbers)));
+        const int r = number - __builtin_amdgcn_readlane(from, who);
+        k.stride = __builtin_amdgcn_readlane(rest, who);
+        k.piece = join ? 0 : r / k.stride;
+        k.tile = __builtin_amdgcn_readlane(tiles, who) - k.stride + (join ? r : r - k.piece * k.stride);
+        k.place = __builtin_amdgcn_readlane(place, who) + r;
+    }
+    k.b = who;
+    k.s = {__builtin_amdgcn_readlane(s.q0, who), __builtin_amdgcn_readlane(s.lq, who), __builtin_amdgcn_readlane(s.len, who)};
+    k.tiles = __builtin_amdgcn_readlane(tiles, who);
+    return true;
+}
+__device__ __forceinline__ bool pick_of_many(const ChunkArgs &a, int number, int group, bool join, ChunkPick &k)
+{
+    k.per = 1 << 30;
+    if (a.cut)
+        k.per = chunk_piece(sum_over(a, a.batch, [&](const ChunkSeq &s) { return seq_tiles(a, s, group) * seq_steps(a, s, group); }),
+                            a.wanted);
+    const auto numbers = [&](const ChunkSeq &s) { return seq_tiles(a, s, group) * chunk_pieces(seq_steps(a, s, group), k.per); };
+    const auto of = [&](int64_t i) {
+        const ChunkSeq s = chunk_seq(a, i);
+        return join ? seq_tiles(a, s, group) : numbers(s);
+    };
+    int64_t b, at;
+    if (!(a.cut ? find_tile_in_runs(number, a.batch, of, b, at) : find_rows<kChunkRows>(number, a.cu, a.batch, a.q_rows, group, b, at)))
+        return false;
+    k.b = __builtin_amdgcn_readfirstlane(static_cast<int>(b));
+    k.tile = __builtin_amdgcn_readfirstlane(static_cast<int>(at));
+    k.s = chunk_seq(a, k.b);
+    k.tiles = k.stride = seq_tiles(a, k.s, group);
+    k.piece = k.place = 0;
+    const int pieces = chunk_pieces(seq_steps(a, k.s, group), k.per);
+    if (pieces > 1) {
+        const int before = sum_over(a, k.b, [&](const ChunkSeq &s) { return chunk_pieces(seq_steps(a, s, group), k.per) > 1 ? numbers(s) : 0; });
+        if (before + k.stride * pieces > a.places) return false;
+        k.place = before + k.tile;
+        if (!join) {
+            k.piece = k.tile / k.stride;
+            k.tile -= k.piece * k.stride;
+        }
+    }
+    return true;
+}
+
 // False: nothing (more) to do.  The rows of a sequence that is refused become
-// NaN.  join: the tile of a workgroup of the join (tiles alone are numbered).
+// NaN.
 template <typename QT, int D>
 __device__ __forceinline__ bool chunk_tile(const ChunkArgs &a, uint32_t block, bool join, ChunkTile &t)
 {
     t.group = a.hq / a.hkv;
     t.kh = static_cast<int>(block % static_cast<uint32_t>(a.hkv));
     const int number = static_cast<int>(block / static_cast<uint32_t>(a.hkv));
-    int per = 1 << 30;
-    if (a.cut) {
-        const int total = sum_over(a, a.batch, [&](const ChunkSeq &s) { return seq_tiles(a, s, t.group) * seq_steps(a, s, t.group); });
-        per = chunk_piece(total, a.wanted);
-    }
-    const auto pieces = [&](const ChunkSeq &s) { return chunk_pieces(seq_steps(a, s, t.group), per); };
-    const auto numbers = [&](const ChunkSeq &s) { return seq_tiles(a, s, t.group) * pieces(s); };
-    int64_t b, at;
-    if (a.cut == 0 && a.batch > 64) {
-        if (!find_rows<kChunkRows>(number, a.cu, a.batch, a.q_rows, t.group, b, at)) return false;
-    } else {
-        const auto of = [&](int64_t i) {
-            const ChunkSeq s = chunk_seq(a, i);
-            return join ? seq_tiles(a, s, t.group) : numbers(s);
-        };
-        if (!(a.batch <= 64 ? find_tile<true>(number, a.batch, of, b, at) : find_tile_in_runs(number, a.batch, of, b, at)))
-            return false;
-    }
-    b = __builtin_amdgcn_readfirstlane(static_cast<int>(b));
-    int piece = 0, tile = __builtin_amdgcn_readfirstlane(static_cast<int>(at));
-    const ChunkSeq s = chunk_seq(a, b);
-    t.b = b;
-    t.stride = seq_tiles(a, s, t.group);
-    if (a.cut && !join) {
-        piece = tile / t.stride;
-        tile -= piece * t.stride;
-    }
+    ChunkPick k;
+    if (!(a.batch <= 64 ? pick_of_64(a, number, t.group, join, k) : pick_of_many(a, number, t.group, join, k))) return false;
+    const ChunkSeq &s = k.s;
     if (refused(a, s)) {
-        const int64_t r = (s.q0 < 0 ? -static_cast<int64_t>(s.q0) * t.group : 0) + static_cast<int64_t>(tile) * kChunkRows + threadIdx.x;
+        const int64_t r = (s.q0 < 0 ? -static_cast<int64_t>(s.q0) * t.group : 0) + static_cast<int64_t>(k.tile) * kChunkRows + threadIdx.x;
         const int64_t tok = s.q0 + r / t.group;
-        if (!join && piece == 0 && threadIdx.x < kChunkRows && tok < s.q0 + static_cast<int64_t>(s.lq) && tok < a.q_rows) {
+        if (!join && k.piece == 0 && threadIdx.x < kChunkRows && tok < s.q0 + static_cast<int64_t>(s.lq) && tok < a.q_rows) {
             QT *dst = static_cast<QT *>(a.out) + (tok * a.hq + t.kh * t.group + r % t.group) * D;
             const float n = __builtin_nanf("");
             for (int e = 0; e < D; e += 4) store4(dst + e, at_f32x4{n, n, n, n});
         }
         return false;
     }
+    t.b = k.b;
     t.q0 = s.q0;
     t.off = s.len - s.lq;
     t.rows = s.lq * t.group;
     // the last rows see the most keys: they start first
-    t.row0 = (t.stride - 1 - tile) * kChunkRows;
+    t.row0 = (k.tiles - 1 - k.tile) * kChunkRows;
     t.end = t.row0 + kChunkRows < t.rows ? t.row0 + kChunkRows : t.rows;
     t.c = chunk_steps(t.row0 / t.group + t.off, (t.end - 1) / t.group + t.off, a.window, a.sinks);
-    t.pieces = chunk_pieces(t.c.steps, per);
-    if (piece >= t.pieces) return false;
-    t.first = piece * per;
-    t.last = t.c.steps - t.first > per ? t.first + per : t.c.steps;
-    t.number = number;
-    if (a.cut && t.pieces > 1) {
-        // find_tile<true> numbers the longest of each 64 sequences first: the
-        // pieces' places go by the order of the sequences
-        t.number = sum_over(a, b, numbers) + tile;
-        if (t.number + (t.pieces - 1) * t.stride >= a.places) return false;  // (offsets that decrease)
-        if (!join) t.number += piece * t.stride;
-    }
+    t.pieces = chunk_pieces(t.c.steps, k.per);
+    if (k.piece >= t.pieces) return false;
+    t.first = k.piece * k.per;
+    t.last = t.c.steps - t.first > k.per ? t.first + k.per : t.c.steps;
+    t.place = k.place;
+    t.stride = k.stride;
     return true;
 }
 
 // The place of a row's part.
-__device__ __forceinline__ int64_t part_slot(const ChunkArgs &a, const ChunkTile &t, int number, int row)
+__device__ __forceinline__ int64_t part_slot(const ChunkArgs &a, const ChunkTile &t, int row)
 {
-    return (static_cast<int64_t>(number) * a.hkv + t.kh) * a.slot_rows + (row - t.row0);
+    return (static_cast<int64_t>(t.place) * a.hkv + t.kh) * a.slot_rows + (row - t.row0);
 }
 
 // One lane's query row.
@@ -246,7 +363,7 @@ struct ChunkPages {
     bool bad = false;
 
     __device__ __forceinline__ ChunkPages(const ChunkArgs &a, const ChunkTile &t)
-        : table(a.table + t.b * a.max_pages), page_shift(a.page_shift), lo(t.c.lo), reach(t.c.reach), sunk(t.c.sunk),
+        : table(a.table + static_cast<int64_t>(t.b) * a.max_pages), page_shift(a.page_shift), lo(t.c.lo), reach(t.c.reach), sunk(t.c.sunk),
           n_pages(static_cast<uint32_t>(a.n_pages))
     {
     }
@@ -383,18 +500,20 @@ struct ChunkStaging {
     {
         constexpr int L = D / 16;
         const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int k_at = not_kept(row_start<D>(wave * (64 / L) + lane / L) ^ (32 * (lane % L)));
+        const int v_at = not_kept(row_start<BN>(static_cast<int>(threadIdx.x >> 2)) ^ (32 * (lane & 3)));
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
-            const int r = (i * W + wave) * (64 / L) + lane / L, p = 2 * (lane % L);
             typedef typename Op16<QT>::x8 k8;
-            *reinterpret_cast<k8 *>(to.k + place<D>(r, p)) = codes_to<QT>(kr[i][0], kr[i][1]);
-            *reinterpret_cast<k8 *>(to.k + place<D>(r, p + 1)) = codes_to<QT>(kr[i][2], kr[i][3]);
+            char *at = reinterpret_cast<char *>(to.k) + i * W * 64 * 32;  // (64 rows or 16 on: the swizzle is the same)
+            *reinterpret_cast<k8 *>(at + k_at) = codes_to<QT>(kr[i][0], kr[i][1]);
+            *reinterpret_cast<k8 *>(at + (k_at ^ 16)) = codes_to<QT>(kr[i][2], kr[i][3]);
         }
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
-            const int d = i * (NT / 4) + static_cast<int>(threadIdx.x >> 2), p = 2 * (lane & 3);
-            *reinterpret_cast<f16x8 *>(to.v + place<BN>(d, p)) = codes_to_f16(vr[i][0], vr[i][1]);
-            *reinterpret_cast<f16x8 *>(to.v + place<BN>(d, p + 1)) = codes_to_f16(vr[i][2], vr[i][3]);
+            char *at = reinterpret_cast<char *>(to.v) + i * (NT / 4) * (2 * BN);
+            *reinterpret_cast<f16x8 *>(at + v_at) = codes_to_f16(vr[i][0], vr[i][1]);
+            *reinterpret_cast<f16x8 *>(at + (v_at ^ 16)) = codes_to_f16(vr[i][2], vr[i][3]);
         }
         // (the product is finite, or it would make a NaN of a sum of zero)
         if (wave == 0) to.ks[lane] = step != step ? step : fminf(step * c, 3.4028235e38f);
@@ -436,7 +555,7 @@ struct ChunkNotes {
 // The page of a key, -1 if there is none.
 __device__ __forceinline__ int64_t page_of_key(const ChunkArgs &a, const ChunkTile &t, int key)
 {
-    const int64_t pg = a.table[t.b * a.max_pages + (key >> a.page_shift)];
+    const int64_t pg = a.table[static_cast<int64_t>(t.b) * a.max_pages + (key >> a.page_shift)];
     return pg >= 0 && pg < a.n_pages ? pg : -1;
 }
 
@@ -489,7 +608,7 @@ __device__ __forceinline__ void store_rows(const ChunkArgs &a, const ChunkTile &
                 store4(dst + 32 * i + 2 * j, at_f32x4{o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]});
         return;
     }
-    const int64_t slot = part_slot(a, t, t.number, at);
+    const int64_t slot = part_slot(a, t, at);
     float *dst = a.parts + slot * d + d0 + 4 * half;
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -749,8 +868,10 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 31, half = lane >> 5;
+    __shared__ ChunkTile tile_note;  // for the end: in registers it would be in the way meanwhile
     ChunkTile t;
     if (!chunk_tile<QT, D>(a, blockIdx.x, false, t)) return;
+    if (threadIdx.x == 0) tile_note = t;
     const bool idle = t.row0 + 32 * wave >= t.rows;  // no row of this wave's is there
     ChunkPages pages(a, t);
     ChunkStaging<C, QT, D> staging(a, t);
@@ -788,6 +909,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
         x8 pf[2 * KT];
         if (!idle) {
             at_f32x16 s[KT];
+            const int k_row = not_kept(row_start<D>(token_of_row(col)) ^ (16 * half));
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
 #pragma unroll
@@ -795,7 +917,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
                     typedef typename Op16<QT>::x8 k8;
-                    const k8 kf = *reinterpret_cast<const k8 *>(b.k + place<D>(32 * k + token_of_row(col), 2 * kk + half));
+                    const k8 kf = *reinterpret_cast<const k8 *>(reinterpret_cast<const char *>(b.k) + (k_row ^ (32 * kk)) + 32 * k * (2 * D));
                     s[k] = Op16<QT>::mfma32(kf, q.f[kk], s[k]);
                 }
             }
@@ -828,11 +950,12 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
             __syncthreads();
         }
         if (!idle) {
+            const int v_row = not_kept(row_start<BN>(col) ^ (16 * half));
 #pragma unroll
             for (int u = 0; u < 2 * KT; ++u)
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
-                    o[d] = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(b.v + place<BN>(32 * d + col, 2 * u + half)), pf[u], o[d]);
+                    o[d] = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(reinterpret_cast<const char *>(b.v) + (v_row ^ (32 * u)) + 32 * d * (2 * BN)), pf[u], o[d]);
         }
         if constexpr (I8)
             if (i + 1 < t.last) staging.store(step_key(t.c, i + 1), next);
@@ -855,10 +978,9 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
     if (__ballot(pages.bad) != 0 && lane == 0) notes.bad = 1;
     __syncthreads();
     if (idle) return;
-    // the row anew: kept through the loops it takes registers that the reads run ahead in
-    int again = t.row0 + 32 * wave + col;
-    asm volatile("" : "+v"(again));
-    finish<C, QT, DT>(a, t, chunk_row(a, t, again), notes, again, D, 0, half, o, w.m, lane_pair_sum<32>(w.l + w.l2), w.unit);
+    const ChunkTile end = tile_note;
+    const int at = end.row0 + 32 * wave + col;
+    finish<C, QT, DT>(a, end, chunk_row(a, end, at), notes, at, D, 0, half, o, w.m, lane_pair_sum<32>(w.l + w.l2), w.unit);
 }
 
 // The same for 256-wide heads, whose O^T and queries for 32 rows take 192
@@ -887,8 +1009,10 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 31, half = lane >> 5;
     const int pair = wave >> 1, part = wave & 1;
+    __shared__ ChunkTile tile_note;  // for the end: in registers it would be in the way meanwhile
     ChunkTile t;
     if (!chunk_tile<QT, D>(a, blockIdx.x, false, t)) return;
+    if (threadIdx.x == 0) tile_note = t;
     const bool idle = t.row0 + 32 * pair >= t.rows;
     ChunkPages pages(a, t);
     ChunkStaging<C, QT, D> staging(a, t);
@@ -928,10 +1052,11 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
         if (!idle) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) s[0][j] = 0.0f;
+            const int k_row = not_kept(row_start<D>(32 * part + token_of_row(col)) ^ (16 * half));
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
                 typedef typename Op16<QT>::x8 k8;
-                s[0] = Op16<QT>::mfma32(*reinterpret_cast<const k8 *>(b.k + place<D>(32 * part + token_of_row(col), 2 * kk + half)), q.f[kk], s[0]);
+                s[0] = Op16<QT>::mfma32(*reinterpret_cast<const k8 *>(reinterpret_cast<const char *>(b.k) + (k_row ^ (32 * kk))), q.f[kk], s[0]);
             }
             __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
 #pragma unroll
@@ -979,6 +1104,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
                 behind[1] = u1 - now;
             }
             // ---- O^T of dimensions 128 part ..
+            const int v_row = not_kept(row_start<BN>(128 * part + col) ^ (16 * half));
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 x8 p = weights[pair][u][lane];
@@ -986,7 +1112,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
                     if (__ballot(behind[u >> 1] != 0) != 0) p *= static_cast<T>(ldexpf(1.0f, behind[u >> 1]));
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
-                    o[d] = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(b.v + place<BN>(128 * part + 32 * d + col, 2 * u + half)), p, o[d]);
+                    o[d] = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(reinterpret_cast<const char *>(b.v) + (v_row ^ (32 * u)) + 32 * d * (2 * BN)), p, o[d]);
             }
         }
         if constexpr (I8)
@@ -1015,14 +1141,16 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
     __syncthreads();
     if (idle) return;
     l = tops[pair][0][col] + tops[pair][1][col];
-    int again = t.row0 + 32 * pair + col;
-    asm volatile("" : "+v"(again));
-    finish<C, QT, DT>(a, t, chunk_row(a, t, again), notes, again, D, 128 * part, half, o, w.m, l, o_unit);
+    const ChunkTile end = tile_note;
+    const int at = end.row0 + 32 * pair + col;
+    finish<C, QT, DT>(a, end, chunk_row(a, end, at), notes, at, D, 128 * part, half, o, w.m, l, o_unit);
 }
 
 // Joins the parts of the tiles that were cut: D / 4 lanes per row, one row each
-// (blockIdx.y: the part of a tile's rows).
+// at a time (blockIdx.y: which of a tile's rows).
 constexpr int join_rows(int d) { return 256 / (d / 4); }
+constexpr int64_t kJoinGroups = 2048;
+constexpr int kJoinAhead = 4;
 
 template <typename QT, int D>
 __global__ void __launch_bounds__(256) k_chunk_join(ChunkArgs a)
@@ -1031,27 +1159,40 @@ __global__ void __launch_bounds__(256) k_chunk_join(ChunkArgs a)
     ChunkTile t;
     if (!chunk_tile<QT, D>(a, blockIdx.x, true, t) || t.pieces == 1) return;
     const int x = threadIdx.x % LPR;
-    const int r = t.row0 + static_cast<int>(blockIdx.y * join_rows(D) + threadIdx.x / LPR);
-    if (r >= t.end) return;
-    const ChunkRow row = chunk_row(a, t, r);
-    const int64_t first = part_slot(a, t, t.number, r), stride = static_cast<int64_t>(t.stride) * a.hkv * a.slot_rows;
-    const float *ml = a.parts + a.rows_floats + first * 2, *src = a.parts + first * D + 4 * x;
-    float M = -__builtin_inff();
-    for (int i = x; i < t.pieces; i += LPR) M = fmaxf(M, ml[2 * i * stride]);
+    for (int r = t.row0 + static_cast<int>(blockIdx.y * join_rows(D) + threadIdx.x / LPR); r < t.end; r += gridDim.y * join_rows(D)) {
+        const ChunkRow row = chunk_row(a, t, r);
+        const int64_t first = part_slot(a, t, r), stride = static_cast<int64_t>(t.stride) * a.hkv * a.slot_rows;
+        const float2 *ml = reinterpret_cast<const float2 *>(a.parts + a.rows_floats) + first;
+        const float *src = a.parts + first * D + 4 * x;
+        // lane x has piece x's reference and sum (the first LPR of them), and
+        // every lane its elements of the first rows: one trip to memory
+        at_f32x4 ahead[kJoinAhead];
 #pragma unroll
-    for (int o = 1; o < LPR; o <<= 1) M = fmaxf(M, __shfl_xor(M, o, 64));
-    if (M == -__builtin_inff()) M = 0.0f;
-    float L = 0.0f;
-    for (int i = x; i < t.pieces; i += LPR) L += __builtin_amdgcn_exp2f(ml[2 * i * stride] - M) * ml[2 * i * stride + 1];
+        for (int i = 0; i < kJoinAhead; ++i) ahead[i] = *reinterpret_cast<const at_f32x4 *>(src + (i < t.pieces ? i : 0) * stride * D);
+        const float2 mine = x < t.pieces ? ml[x * stride] : float2{-__builtin_inff(), 0.0f};
+        float M = mine.x;
+        for (int i = x + LPR; i < t.pieces; i += LPR) M = fmaxf(M, ml[i * stride].x);
 #pragma unroll
-    for (int o = 1; o < LPR; o <<= 1) L += __shfl_xor(L, o, 64);
-    const float inv = row.seen.hi == 0 ? 0.0f : 1.0f / L;
-    at_f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int o = 1; o < LPR; o <<= 1) M = fmaxf(M, __shfl_xor(M, o, 64));
+        if (M == -__builtin_inff()) M = 0.0f;
+        const float weight = __builtin_amdgcn_exp2f(mine.x - M) * mine.y;
+        float L = weight;
+        for (int i = x + LPR; i < t.pieces; i += LPR) L += __builtin_amdgcn_exp2f(ml[i * stride].x - M) * ml[i * stride].y;
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) L += __shfl_xor(L, o, 64);
+        const float inv = row.seen.hi == 0 ? 0.0f : 1.0f / L;
+        const auto weight_of = [&](int i) {
+            return (i < LPR ? __shfl(weight, (threadIdx.x & 63 & ~(LPR - 1)) + i, 64)
+                            : __builtin_amdgcn_exp2f(ml[i * stride].x - M) * ml[i * stride].y) * inv;
+        };
+        at_f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kJoinAhead; ++i)
+            if (i < t.pieces) o += weight_of(i) * ahead[i];
 #pragma unroll 4
-    for (int i = 0; i < t.pieces; ++i)
-        o += __builtin_amdgcn_exp2f(ml[2 * i * stride] - M) * ml[2 * i * stride + 1] * inv *
-             *reinterpret_cast<const at_f32x4 *>(src + i * stride * D);
-    store4(static_cast<QT *>(a.out) + ((static_cast<int64_t>(t.q0) + row.tok) * a.hq + row.head) * D + 4 * x, o);
+        for (int i = kJoinAhead; i < t.pieces; ++i) o += weight_of(i) * *reinterpret_cast<const at_f32x4 *>(src + i * stride * D);
+        store4(static_cast<QT *>(a.out) + ((static_cast<int64_t>(t.q0) + row.tok) * a.hq + row.head) * D + 4 * x, o);
+    }
 }
 
 template <typename C, typename QT, int D>
@@ -1062,9 +1203,14 @@ hipError_t chunk_launch(const ChunkArgs &a, const ChunkPlan &p, hipStream_t s)
         hipLaunchKernelGGL((k_attn_chunk_wide<C, QT>), grid, dim3(64 * chunk_waves(D)), 0, s, a);
     else
         hipLaunchKernelGGL((k_attn_chunk<C, QT, D>), grid, dim3(64 * chunk_waves(D)), 0, s, a);
-    if (p.cut)
-        hipLaunchKernelGGL((k_chunk_join<QT, D>), dim3(static_cast<uint32_t>(p.tiles * a.hkv), (p.slot_rows + join_rows(D) - 1) / join_rows(D)),
+    if (p.cut) {
+        // a workgroup for some rows of a tile each; many tiles are mostly uncut,
+        // and their workgroups only find that out
+        const int64_t tiles = p.tiles * a.hkv, rows = (p.slot_rows + join_rows(D) - 1) / join_rows(D);
+        const int64_t each = kJoinGroups / tiles;
+        hipLaunchKernelGGL((k_chunk_join<QT, D>), dim3(static_cast<uint32_t>(tiles), static_cast<uint32_t>(each < 1 ? 1 : each < rows ? each : rows)),
                            dim3(256), 0, s, a);
+    }
     return hipGetLastError();
 }
 
@@ -1090,9 +1236,16 @@ ChunkPlan chunk_plan(int64_t batch, int64_t q_rows, int64_t max_q, int32_t hq, i
     const int64_t slots = d == 256 ? 256 : 512;  // workgroups that the GPU holds
     p.wanted = static_cast<int32_t>(slots / hkv > 1 ? slots / hkv : 1);
     const int most = steps_bound(static_cast<int>(max_len), static_cast<int>(window), static_cast<int>(sinks), static_cast<int>(group));
-    const int64_t numbers = p.wanted + p.tiles, parts = numbers * hkv * p.slot_rows;
-    p.cut = most > kChunkMinSteps && p.tiles * hkv <= 8 * slots && parts * (d + 2) * 4 <= kMaxChunkParts;
+    // pieces: of all tiles wanted + tiles at most, or twice wanted in the place of
+    // the last tiles; of those that are cut, which need a place, twice wanted
+    const int64_t numbers = 2 * p.wanted + p.tiles, places = 2 * p.wanted, parts = places * hkv * p.slot_rows;
+    p.cut = most > kChunkMinSteps && p.tiles * hkv <= 4 * slots && parts * (d + 2) * 4 <= kMaxChunkParts;
     if (p.cut) {
+        // a step's time with the GPU full, a piece's rows written and read in
+        // fp32 at half of HBM's rate (they come in bursts), and the join, in us
+        const double step = d == 256 ? 2.6 : d == 128 ? 1.9 : 1.1;
+        p.join_cost = static_cast<float>(6.0 / step);
+        p.piece_cost = static_cast<float>(static_cast<double>(hkv) * p.slot_rows * d * 4 * 2 / 2.5e6 / step);
         p.numbers = numbers;
         p.rows_floats = static_cast<size_t>(parts) * d;
         p.part_floats = p.rows_floats + static_cast<size_t>(parts) * 2;
@@ -1107,8 +1260,8 @@ hipError_t launch_attn_chunk(const ChunkPlan &p, const void *q, int64_t qs, int 
 {
     const ChunkArgs a{q, qs, cu, lens, table, max_pages, batch, q_rows, max_q, max_len, hq, c.n_kv_heads, c.k_pages,
                       c.v_pages, c.k_steps, c.v_steps, c.n_pages, __builtin_ctz(static_cast<unsigned>(c.page_size)),
-                      window, sinks, scale, out, p.wanted, p.cut, static_cast<int32_t>(p.numbers), p.slot_rows,
-                      static_cast<int64_t>(p.rows_floats), parts};
+                      window, sinks, scale, out, p.wanted, p.cut, 2 * p.wanted, p.slot_rows,
+                      p.join_cost, p.piece_cost, static_cast<int64_t>(p.rows_floats), parts};
     if (c.dtype == PTQ1_BF16) return chunk_d<__bf16, __bf16>(a, p, c.head_dim, s);
     if (c.dtype == PTQ1_F16) return chunk_d<_Float16, _Float16>(a, p, c.head_dim, s);
     return q_type == PTQ1_F16 ? chunk_d<int8_t, _Float16>(a, p, c.head_dim, s) : chunk_d<int8_t, __bf16>(a, p, c.head_dim, s);

@@ -28,15 +28,15 @@ constexpr SeenKeys seen_keys(int p, int window)
 // the keys step_key(i) .., real ones numbered through with `gap` steps between
 // the first tokens' and the windows' left out.
 struct ChunkSteps {
-    int lo = 0, reach = 0, sunk = 0;  // keys that some row sees: [lo, reach), and below sunk
-    int head = 0, gap = 0;            // from step `head` on, `gap` steps further
-    int steps = 0;
-    int all_from = 0, all_to = 0;     // every row sees every key of these steps
+    int lo, reach, sunk;   // keys that some row sees: [lo, reach), and below sunk
+    int head, gap;         // from step `head` on, `gap` steps further
+    int steps;
+    int all_from, all_to;  // every row sees every key of these steps
 };
 constexpr ChunkSteps chunk_steps(int first, int last, int window, int sinks)
 {
     constexpr int N = kChunkKeys;
-    ChunkSteps c;
+    ChunkSteps c{};
     c.lo = seen_keys(first, window).lo;
     c.reach = seen_keys(last, window).hi;
     c.sunk = imin(sinks, c.reach);
@@ -65,6 +65,25 @@ constexpr int steps_bound(int len, int window, int sinks, int group)
 // Steps of one piece where the tiles' steps are `total` in all and `wanted`
 // pieces fill the GPU.
 constexpr int chunk_piece(int total, int wanted) { return imax(kChunkMinSteps, (total + wanted - 1) / wanted); }
+
+// The number of pieces that `tiles` of `steps` each are cut in to end soonest
+// where `wanted` run side by side (join_cost, piece_cost: in steps): at most twice
+// as many pieces.
+constexpr int chunk_cuts(int tiles, int steps, int wanted, float join_cost, float piece_cost)
+{
+    int best = 1;
+    float least = 0.0f;
+    for (int n = 1; n == 1 || (tiles * n <= 2 * wanted && (steps + n - 1) / n >= kChunkMinSteps); n += n < 8 ? 1 : n / 4) {
+        const int rounds = (tiles * n + wanted - 1) / wanted;
+        const float cost = static_cast<float>(rounds * ((steps + n - 1) / n)) +
+                           (n > 1 ? join_cost + piece_cost * static_cast<float>(tiles * n) : 0.0f);
+        if (n == 1 || cost < least) {
+            least = cost;
+            best = n;
+        }
+    }
+    return best;
+}
 
 constexpr int chunk_pieces(int steps, int per) { return imax(1, (steps + per - 1) / per); }
 

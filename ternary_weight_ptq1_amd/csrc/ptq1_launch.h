@@ -203,12 +203,13 @@ hipError_t launch_attn_prompt(const PromptArgs &a, int dtype, int32_t d, const P
 
 // Attention of chunks over the cache.  Tiles of 128 query rows of a kv head
 // (`tiles` of one at most); where they may be cut along the keys, `numbers`
-// pieces of one at most, so that `wanted` of them fill the GPU, each with a place
-// for slot_rows rows of parts: the mean over the piece's keys [number][kv head]
-// [row][d], then their (reference, sum) pairs.
+// workgroups of one at most, so that `wanted` of them fill the GPU, and 2 wanted
+// places for slot_rows rows of parts: the mean over a piece's keys [place]
+// [kv head][row][d], then their (reference, sum) pairs.
 struct ChunkPlan {
     int64_t tiles = 0, numbers = 0;
     int32_t wanted = 1, slot_rows = 0;
+    float join_cost = 0.0f, piece_cost = 0.0f;  // in steps
     bool cut = false;
     size_t rows_floats = 0, part_floats = 0;
 };
