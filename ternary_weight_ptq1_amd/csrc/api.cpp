@@ -1306,7 +1306,8 @@ ptq1_status attn_decode(const char *name, const void *q, int32_t q_dtype, int64_
     if (window > max_len) window = max_len + 1;  // (all of them)
     if (sinks > max_len) sinks = max_len;
     const ptq1::DecodePlan plan = ptq1::decode_plan(batch, n_q_heads, cache->n_kv_heads, cache->head_dim,
-                                                    window > 0 ? ptq1::window_bound(max_len, window, sinks) : max_len);
+                                                    window > 0 ? ptq1::window_bound(max_len, window, sinks) : max_len,
+                                                    window > 0);
     const size_t need = round_up(plan.part_floats * 4, kWsAlign);
     PTQ1_TRY(check_ws(ws, ws_bytes, need, name));
     if (overlaps(out, qb, q, qb)) return fail(PTQ1_ERR_ALIAS, "out overlaps q");
@@ -1417,8 +1418,8 @@ size_t ptq1_attn_decode_window_workspace_bytes(int64_t batch, int32_t n_q_heads,
     if (window < 1 || sinks < 0 || !decode_sizes_ok(batch, n_q_heads, n_kv_heads, head_dim, max_len)) return 0;
     if (window > max_len) window = max_len + 1;
     if (sinks > max_len) sinks = max_len;
-    return ptq1_attn_decode_workspace_bytes(batch, n_q_heads, n_kv_heads, head_dim,
-                                            ptq1::window_bound(max_len, window, sinks));
+    return round_up(ptq1::decode_plan(batch, n_q_heads, n_kv_heads, head_dim, ptq1::window_bound(max_len, window, sinks),
+                                      true).part_floats * 4, kWsAlign);
 }
 
 ptq1_status ptq1_attn_decode_window(const void *q, int32_t q_dtype, int64_t batch, int32_t n_q_heads,

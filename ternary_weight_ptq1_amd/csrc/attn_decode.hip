@@ -726,7 +726,7 @@ hipError_t decode_types(const DecodePlan &p, const DecodeArgs &a, int q_type, in
 
 }  // namespace
 
-DecodePlan decode_plan(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_t max_len)
+DecodePlan decode_plan(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_t max_len, bool windowed)
 {
     DecodePlan p;
     const int64_t group = hq / hkv, hgroups = hkv * ((group + kDecHeads - 1) / kDecHeads);
@@ -741,6 +741,17 @@ DecodePlan decode_plan(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_
     // batches of short sequences are not cut (1024 of 512 tokens: 455 us with
     // the search for their pieces and the join's launch, 364 without)
     p.join = each > (batch + want - 1) / want;
+    if (windowed && p.join && each <= 8) {
+        // Windows are of one length, and mostly short: is the time of the steps
+        // that cutting saves (1.9 us each, 3.6 of 256-wide heads) more than it
+        // costs?  One sequence, 40 heads over 8 of 128: windows of 256, 700, 1024
+        // and 2000 tokens 11.9, 12.3, 12.1, 12.1 us cut and 8.0, 11.0, 14.3, 22.0
+        // uncut; 32 of 1024 and 2000 28.6, 45.4 and 22.6, 39.3; 200 of 700 over
+        // int8, 64-wide, 39.6 and 16.5.
+        const int64_t groups = batch * hgroups, slots = d == 256 ? 256 : 512;
+        const int64_t saved = each * ((groups + slots - 1) / slots) - (each * groups + slots - 1) / slots;
+        p.join = static_cast<double>(saved) * (d == 256 ? 3.6 : 1.9) > 6.0 + static_cast<double>(batch < 64 ? batch : 64) / 4;
+    }
     p.pieces = p.join && want + batch < each * batch ? want + batch : p.join ? each * batch : batch;
     if (p.join) {
         p.rows_floats = static_cast<size_t>(p.pieces) * hq * d;

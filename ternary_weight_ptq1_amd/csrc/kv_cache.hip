@@ -180,7 +180,7 @@ hipError_t launch_kv_write(const void *q, int64_t qs, const void *k, int64_t ks,
 {
     KvWriteArgs a{q,     k,     v,         qs,          ks,        vs,        tokens, hq,
                   c.n_kv_heads, positions, cos_sin, n_positions, rot, slots, q_out, c.k_pages, c.v_pages,
-                  c.k_steps, c.v_steps, c.n_pages * c.page_size, log2_of(c.page_size), 0, nullptr, nullptr, 0.0f};
+                  c.k_steps, c.v_steps, c.n_pages * c.page_size, log2_of(c.page_size), 0, nullptr, nullptr, 0.0f, 0, 0};
     return src == PTQ1_F32 ? write_q<false, float>(a, c.head_dim, c.dtype, q_type, s)
                            : src == PTQ1_F16 ? write_q<false, _Float16>(a, c.head_dim, c.dtype, q_type, s)
                                              : write_q<false, __bf16>(a, c.head_dim, c.dtype, q_type, s);

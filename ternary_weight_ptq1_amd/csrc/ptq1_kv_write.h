@@ -33,6 +33,8 @@ struct KvWriteArgs {
     uint32_t v_blocks;  // blocks of V tiles (first: they take longest); q and k rows follow
     const float *q_gain, *k_gain;  // of the norms, [D] or null: ones
     float eps;
+    uint32_t per_head;    // rows / heads is rows * per_head >> head_shift, for rows below 2^25
+    int32_t head_shift;
 };
 
 // Largest magnitude over the N-lane group (N = 16, 32 or 64) of |v|; NaN or
@@ -141,15 +143,22 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_write(KvWriteArgs a)
         const bool turns = e < a.rot, upper = e >= half;
         const int lo = upper ? e - half : e, other = upper ? lo : lo + half;
         at_f32x4 x[kRowsPer], y[kRowsPer], c[kRowsPer], sn[kRowsPer];
-        at_f32x4 gx[NORM ? kRowsPer : 1], gy[NORM ? kRowsPer : 1];  // gains of x and y
         int64_t token[kRowsPer];
         int h[kRowsPer], pos[kRowsPer];
         bool there[kRowsPer], placed[kRowsPer];
 #pragma unroll
         for (int u = 0; u < kRowsPer; ++u) {
             const uint32_t row = ((blockIdx.x - a.v_blocks) * kRowsPer + u) * RPB + sub;
-            token[u] = row / heads;
-            h[u] = static_cast<int>(row % heads);
+            if constexpr (NORM) {
+                // (of a 256-wide row a wave's lanes have one: its address is scalar)
+                const uint32_t r = LPR == kWave ? __builtin_amdgcn_readfirstlane(row) : row;
+                const uint32_t t = static_cast<uint32_t>((static_cast<uint64_t>(r) * a.per_head) >> a.head_shift);
+                token[u] = t;
+                h[u] = static_cast<int>(r - t * heads);
+            } else {
+                token[u] = row / heads;
+                h[u] = static_cast<int>(row % heads);
+            }
             there[u] = token[u] < a.tokens;
             if (!there[u]) continue;
             const S *src = h[u] < a.hq ? static_cast<const S *>(a.q) + token[u] * a.qs + static_cast<int64_t>(h[u]) * D
@@ -158,14 +167,6 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_write(KvWriteArgs a)
             if (turns) {
                 y[u] = load4(src + other);
                 pos[u] = a.positions[token[u]];
-            }
-            if constexpr (NORM) {
-                const float *gain = h[u] < a.hq ? a.q_gain : a.k_gain;
-                gx[u] = gy[u] = at_f32x4{1.0f, 1.0f, 1.0f, 1.0f};
-                if (gain != nullptr) {
-                    gx[u] = load4(gain + e);
-                    if (turns) gy[u] = load4(gain + other);
-                }
             }
         }
 #pragma unroll
@@ -188,8 +189,15 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_write(KvWriteArgs a)
                     f = 0x1p-70f;
                     a_row = __builtin_amdgcn_rsqf(group_sum<LPR>(squares4(x[u] * f)) * (1.0f / D));
                 }
-                x[u] = x[u] * f * a_row * gx[u];
-                if (turns) y[u] = y[u] * f * a_row * gy[u];
+                x[u] = x[u] * f * a_row;
+                if (turns) y[u] = y[u] * f * a_row;
+                // (a gain is in the caches: loaded ahead with the rows, it took
+                // registers that keep rows in flight, 114 us for 8191 tokens)
+                const float *gain = h[u] < a.hq ? a.q_gain : a.k_gain;
+                if (gain != nullptr) {
+                    x[u] *= load4(gain + e);
+                    if (turns) y[u] *= load4(gain + other);
+                }
             }
         }
 #pragma unroll
@@ -326,7 +334,11 @@ template <bool NORM, typename S, typename Q, typename C, int D>
 hipError_t write_launch(KvWriteArgs &a, hipStream_t s)
 {
     constexpr int RPB = kKvThreads / (D / 4) * kRowsPer;
-    const int64_t rows = a.tokens * (a.hq + a.hkv);
+    const int64_t heads = a.hq + a.hkv, rows = a.tokens * heads;
+    int log = 0;
+    while ((int64_t{1} << log) < heads) ++log;
+    a.head_shift = 25 + log;  // the product is off by less than 2^log rows of 2^25
+    a.per_head = static_cast<uint32_t>(((int64_t{1} << a.head_shift) + heads - 1) / heads);
     a.v_blocks = static_cast<uint32_t>((a.tokens + kVTok - 1) / kVTok * a.hkv * (D / kv_write_dims<C>(D)));
     hipLaunchKernelGGL((k_kv_write<S, Q, C, D, NORM>), dim3(a.v_blocks + static_cast<uint32_t>((rows + RPB - 1) / RPB)),
                        dim3(kKvThreads), 0, s, a);

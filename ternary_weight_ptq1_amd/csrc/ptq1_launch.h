@@ -168,7 +168,7 @@ struct DecodePlan {
     bool join = false;
     size_t rows_floats = 0, part_floats = 0;
 };
-DecodePlan decode_plan(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_t max_len);
+DecodePlan decode_plan(int64_t batch, int32_t hq, int32_t hkv, int32_t d, int64_t max_len, bool windowed = false);
 hipError_t launch_attn_decode(const DecodePlan &p, const void *q, int q_type, int64_t batch, int32_t hq,
                               const ptq1_kv_cache &c, const int32_t *table, int64_t max_pages, const int32_t *lens,
                               int64_t max_len, int32_t window, int32_t sinks, float scale, void *out, float *part,

@@ -23,7 +23,7 @@ def norm(c=None, **other):
 
 
 def window(c=None, **other):
-    f = dict(q=at(0), qt=BF16, batch=2, hq=8, table=at(1), max_pages=100, lens=at(2), max_len=6400, window=500, sinks=4,
+    f = dict(q=at(0), qt=BF16, batch=2, hq=8, table=at(1), max_pages=100, lens=at(2), max_len=6400, window=5000, sinks=4,
              scale=0.1, out=at(3), ws=at(500), wsb=1 << 40)
     f.update(other)
     c = cache() if c is None else c
