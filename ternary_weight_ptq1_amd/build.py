@@ -27,10 +27,11 @@ HIPCC_FLAGS = [
 
 # MFMA results in VGPRs: the GEMM scales every block's partial with VALU
 # FMAs, which cannot read accumulation registers directly.  The decode
-# attention is compiled without it (the pass that backs the option crashes on
-# its 256-wide kernels) and gets the same registers by the allocator's choice.
+# attention, and that of a few rows over the cache, are compiled without it (the
+# pass that backs the option crashes on their 256-wide kernels) and get the same
+# registers by the allocator's choice.
 VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-NO_VGPR_FORM = ("attn_decode.hip",)
+NO_VGPR_FORM = ("attn_decode.hip", "attn_chunk_few.hip")
 
 
 def hipcc() -> str:

@@ -32,49 +32,13 @@
 
 #include <type_traits>
 
-#include "ptq1_attn.h"
-#include "ptq1_attn_tile.h"
-#include "ptq1_chunk.h"
-#include "ptq1_launch.h"
+#include "ptq1_attn_chunk.h"
 
 namespace ptq1 {
 namespace {
 
-constexpr int BN = kChunkKeys;
-static_assert(kKeys == kChunkKeys, "a step is a tile of keys");
 constexpr int kAhead = 4;  // K reads ahead of their products
 constexpr int chunk_waves(int d) { return d == 256 ? 8 : 4; }
-
-// The 16-bit type of the second product over a cache of C: int8 codes and the
-// weights that meet them are fp16.  (The first product is in the queries' type.)
-template <typename C>
-struct WeightOf {
-    typedef C type;
-};
-template <>
-struct WeightOf<int8_t> {
-    typedef _Float16 type;
-};
-
-struct ChunkArgs {
-    const void *q;
-    int64_t qs;  // row stride in elements
-    const int32_t *cu, *lens, *table;
-    int64_t max_pages, batch, q_rows, max_q, max_len;
-    int32_t hq, hkv;
-    const void *k_pages, *v_pages;
-    const float *k_steps, *v_steps;
-    int64_t n_pages;
-    int32_t page_shift;
-    int32_t window, sinks;
-    float scale;
-    void *out;
-    int32_t wanted, cut;       // pieces of one kv head that fill the GPU; tiles may be cut
-    int32_t places, slot_rows; // of parts, of one kv head, and rows of one
-    float join_cost, piece_cost;  // in steps
-    int64_t rows_floats;
-    float *parts;
-};
 
 // The 16-byte piece p of row r of a tile in LDS lies at piece p ^ swizzle of
 // that row: 16 rows at one piece spread over all banks.  (V's rows are
@@ -97,297 +61,6 @@ __device__ __forceinline__ int not_kept(int v)
     asm volatile("" : "+v"(v));
     return v;
 }
-// The token of row r of a score tile of 32: bits 2 and 3 change places.
-__device__ __forceinline__ int token_of_row(int r) { return (r & 19) | ((r & 4) << 1) | ((r & 8) >> 1); }
-
-// A sequence's rows and keys as the arguments give them.
-struct ChunkSeq {
-    int q0, lq, len;
-};
-__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkArgs &a, int64_t b)
-{
-    return {a.cu[b], a.cu[b + 1] - a.cu[b], a.lens[b]};
-}
-__device__ __forceinline__ bool refused(const ChunkArgs &a, const ChunkSeq &s)
-{
-    return s.q0 < 0 || s.lq > a.max_q || s.q0 + static_cast<int64_t>(s.lq) > a.q_rows || s.len < 0 || s.len > a.max_len;
-}
-// Tiles of the rows that exist.
-__device__ __forceinline__ int seq_tiles(const ChunkArgs &a, const ChunkSeq &s, int group)
-{
-    const int64_t first = s.q0 > 0 ? s.q0 : 0, end = s.q0 + static_cast<int64_t>(s.lq);
-    const int64_t n = (end < a.q_rows ? end : a.q_rows) - first;
-    return n > 0 ? static_cast<int>((n * group + kChunkRows - 1) / kChunkRows) : 0;
-}
-__device__ __forceinline__ int seq_steps(const ChunkArgs &a, const ChunkSeq &s, int group)
-{
-    return refused(a, s) ? 0 : steps_bound(s.len, a.window, a.sinks, group);
-}
-
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp(int v)
-{
-    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);  // (0 where there is no such lane)
-}
-// The sum of the lanes up to and with this one's.
-__device__ __forceinline__ int lanes_to(int v)
-{
-    v += dpp<0x111, 0xF>(v);  // one lane down its row of 16, two ...
-    v += dpp<0x112, 0xF>(v);
-    v += dpp<0x114, 0xF>(v);
-    v += dpp<0x118, 0xF>(v);
-    v += dpp<0x142, 0xA>(v);  // the last of row 0 to row 1, of 2 to 3
-    v += dpp<0x143, 0xC>(v);  // of row 1 to rows 2 and 3
-    return v;
-}
-__device__ __forceinline__ int wave_total(int v) { return __builtin_amdgcn_readlane(lanes_to(v), 63); }
-// The largest, of numbers that are not negative.
-__device__ __forceinline__ int wave_largest(int v)
-{
-    v = max(v, dpp<0x111, 0xF>(v));
-    v = max(v, dpp<0x112, 0xF>(v));
-    v = max(v, dpp<0x114, 0xF>(v));
-    v = max(v, dpp<0x118, 0xF>(v));
-    v = max(v, dpp<0x142, 0xA>(v));
-    v = max(v, dpp<0x143, 0xC>(v));
-    return __builtin_amdgcn_readlane(v, 63);
-}
-// The sum of f(sequence) over the first n.
-template <class F>
-__device__ __forceinline__ int sum_over(const ChunkArgs &a, int64_t n, F f)
-{
-    int v = 0;
-    for (int64_t i = threadIdx.x & 63; i < n; i += 64) v += f(chunk_seq(a, i));
-    return wave_total(v);
-}
-
-// One tile of query rows of one kv head, and the steps of one workgroup.
-struct ChunkTile {
-    int group, kh;
-    int b;
-    int q0, off;             // the sequence's first row; keys before its first query
-    int rows, row0, end;     // its rows; this tile's first one and the one behind its last
-    ChunkSteps c;
-    int first, last;         // this workgroup's steps
-    int pieces;              // of the tile
-    int place, stride;       // of the piece's part (join: of the first one's), and between them
-};
-
-// The numbers of the lanes before this one, and all lanes' together.
-__device__ __forceinline__ int lanes_before(int mine, int &total)
-{
-    const int sum = lanes_to(mine);
-    total = __builtin_amdgcn_readlane(sum, 63);
-    return sum - mine;
-}
-
-// Which tile and piece workgroup `number` of a kv head takes (join: which tile
-// of those that were cut), by the sequences' tiles and steps; false: none.
-//
-// Up to 64 sequences (a lane each): tiles are numbered from the longest
-// sequence on.  Where all are about equally long (0.6 of the longest on
-// average), whole rounds of tiles run uncut, and those behind them are cut in
-// the number that is estimated to end soonest: rounds of pieces, in steps, and
-// what a piece's rows and the join cost, in steps too.  Otherwise tiles are
-// only cut that are longer than an even share, into pieces of that: shorter
-// ones fill the gaps as they are.
-// More sequences: in their order, all cut, or none.
-struct ChunkPick {
-    ChunkSeq s;
-    int b, tiles, tile, piece, per, place, stride;
-};
-__device__ __forceinline__ bool pick_of_64(const ChunkArgs &a, int number, int group, bool join, ChunkPick &k)
-{
-    const int lane = threadIdx.x & 63, n = static_cast<int>(a.batch);
-    ChunkSeq s{0, 0, 0};
-    int tiles = 0, steps = 0;
-    if (lane < n) {
-        s = chunk_seq(a, lane);
-        tiles = seq_tiles(a, s, group);
-        steps = seq_steps(a, s, group);
-    }
-    int before = 0, all = 0;
-    for (int j = 0; j < n; ++j) {
-        const int t = __builtin_amdgcn_readlane(tiles, j), other = __builtin_amdgcn_readlane(steps, j);
-        all += t;
-        if (other > steps || (other == steps && j < lane)) before += t;
-    }
-    int whole = all, per = 1 << 30;
-    if (a.cut) {
-        const int total = wave_total(tiles * steps), longest = wave_largest(steps);
-        const int full = all / a.wanted * a.wanted, left = wave_total(max(0, min(tiles, before + tiles - full)) * steps);
-        if (10 * static_cast<int64_t>(total) < 6 * static_cast<int64_t>(all) * longest) {
-            whole = 0;
-            per = chunk_piece(total, a.wanted);
-        } else if (10 * static_cast<int64_t>(left) >= 6 * static_cast<int64_t>(all - full) * longest) {
-            const int n = chunk_cuts(all - full, longest, a.wanted, a.join_cost, a.piece_cost);
-            if (n > 1) {
-                whole = full;
-                per = imax(kChunkMinSteps, (longest + n - 1) / n);
-            }
-        }
-    }
-    const int rest = max(0, min(tiles, before + tiles - whole));  // its tiles that may be cut
-    k.per = per;
-    k.piece = 0;
-    int who;
-    if (!join && number < whole) {
-        k.per = 1 << 30;
-        who = __builtin_ctzll(__ballot(number >= before && number - before < tiles));
-        k.tile = number - __builtin_amdgcn_readlane(before, who);
-        k.place = 0;
-        k.stride = 0;
-    } else {
-        if (!join) number -= whole;
-        // (places for parts: of the tiles that are cut alone)
-        const int pieces = chunk_pieces(steps, per), numbers = rest * pieces;
-        int total, places;
-        const int place = lanes_before(pieces > 1 ? numbers : 0, places), from = lanes_before(join ? rest : numbers, total);
-        if (number >= total || places > a.places) return false;
-        who = __builtin_ctzll(__ballot(number >= from && number - from < (join ? rest : numbers)));
-        const int r = number - __builtin_amdgcn_readlane(from, who);
-        k.stride = __builtin_amdgcn_readlane(rest, who);
-        k.piece = join ? 0 : r / k.stride;
-        k.tile = __builtin_amdgcn_readlane(tiles, who) - k.stride + (join ? r : r - k.piece * k.stride);
-        k.place = __builtin_amdgcn_readlane(place, who) + r;
-    }
-    k.b = who;
-    k.s = {__builtin_amdgcn_readlane(s.q0, who), __builtin_amdgcn_readlane(s.lq, who), __builtin_amdgcn_readlane(s.len, who)};
-    k.tiles = __builtin_amdgcn_readlane(tiles, who);
-    return true;
-}
-__device__ __forceinline__ bool pick_of_many(const ChunkArgs &a, int number, int group, bool join, ChunkPick &k)
-{
-    k.per = 1 << 30;
-    if (a.cut)
-        k.per = chunk_piece(sum_over(a, a.batch, [&](const ChunkSeq &s) { return seq_tiles(a, s, group) * seq_steps(a, s, group); }),
-                            a.wanted);
-    const auto numbers = [&](const ChunkSeq &s) { return seq_tiles(a, s, group) * chunk_pieces(seq_steps(a, s, group), k.per); };
-    const auto of = [&](int64_t i) {
-        const ChunkSeq s = chunk_seq(a, i);
-        return join ? seq_tiles(a, s, group) : numbers(s);
-    };
-    int64_t b, at;
-    if (!(a.cut ? find_tile_in_runs(number, a.batch, of, b, at) : find_rows<kChunkRows>(number, a.cu, a.batch, a.q_rows, group, b, at)))
-        return false;
-    k.b = __builtin_amdgcn_readfirstlane(static_cast<int>(b));
-    k.tile = __builtin_amdgcn_readfirstlane(static_cast<int>(at));
-    k.s = chunk_seq(a, k.b);
-    k.tiles = k.stride = seq_tiles(a, k.s, group);
-    k.piece = k.place = 0;
-    const int pieces = chunk_pieces(seq_steps(a, k.s, group), k.per);
-    if (pieces > 1) {
-        const int before = sum_over(a, k.b, [&](const ChunkSeq &s) { return chunk_pieces(seq_steps(a, s, group), k.per) > 1 ? numbers(s) : 0; });
-        if (before + k.stride * pieces > a.places) return false;
-        k.place = before + k.tile;
-        if (!join) {
-            k.piece = k.tile / k.stride;
-            k.tile -= k.piece * k.stride;
-        }
-    }
-    return true;
-}
-
-// False: nothing (more) to do.  The rows of a sequence that is refused become
-// NaN.
-template <typename QT, int D>
-__device__ __forceinline__ bool chunk_tile(const ChunkArgs &a, uint32_t block, bool join, ChunkTile &t)
-{
-    t.group = a.hq / a.hkv;
-    t.kh = static_cast<int>(block % static_cast<uint32_t>(a.hkv));
-    const int number = static_cast<int>(block / static_cast<uint32_t>(a.hkv));
-    ChunkPick k;
-    if (!(a.batch <= 64 ? pick_of_64(a, number, t.group, join, k) : pick_of_many(a, number, t.group, join, k))) return false;
-    const ChunkSeq &s = k.s;
-    if (refused(a, s)) {
-        const int64_t r = (s.q0 < 0 ? -static_cast<int64_t>(s.q0) * t.group : 0) + static_cast<int64_t>(k.tile) * kChunkRows + threadIdx.x;
-        const int64_t tok = s.q0 + r / t.group;
-        if (!join && k.piece == 0 && threadIdx.x < kChunkRows && tok < s.q0 + static_cast<int64_t>(s.lq) && tok < a.q_rows) {
-            QT *dst = static_cast<QT *>(a.out) + (tok * a.hq + t.kh * t.group + r % t.group) * D;
-            const float n = __builtin_nanf("");
-            for (int e = 0; e < D; e += 4) store4(dst + e, at_f32x4{n, n, n, n});
-        }
-        return false;
-    }
-    t.b = k.b;
-    t.q0 = s.q0;
-    t.off = s.len - s.lq;
-    t.rows = s.lq * t.group;
-    // the last rows see the most keys: they start first
-    t.row0 = (k.tiles - 1 - k.tile) * kChunkRows;
-    t.end = t.row0 + kChunkRows < t.rows ? t.row0 + kChunkRows : t.rows;
-    t.c = chunk_steps(t.row0 / t.group + t.off, (t.end - 1) / t.group + t.off, a.window, a.sinks);
-    t.pieces = chunk_pieces(t.c.steps, k.per);
-    if (k.piece >= t.pieces) return false;
-    t.first = k.piece * k.per;
-    t.last = t.c.steps - t.first > k.per ? t.first + k.per : t.c.steps;
-    t.place = k.place;
-    t.stride = k.stride;
-    return true;
-}
-
-// The place of a row's part.
-__device__ __forceinline__ int64_t part_slot(const ChunkArgs &a, const ChunkTile &t, int row)
-{
-    return (static_cast<int64_t>(t.place) * a.hkv + t.kh) * a.slot_rows + (row - t.row0);
-}
-
-// One lane's query row.
-struct ChunkRow {
-    bool is;
-    int tok, head;
-    SeenKeys seen;
-};
-__device__ __forceinline__ ChunkRow chunk_row(const ChunkArgs &a, const ChunkTile &t, int row)
-{
-    ChunkRow r;
-    r.is = row < t.rows;
-    const int at = r.is ? row : t.rows - 1;
-    r.tok = at / t.group;
-    r.head = t.kh * t.group + at % t.group;
-    r.seen = seen_keys(r.tok + t.off, a.window);
-    return r;
-}
-
-// Where the keys of a step are: a wave's lanes hold the pages of the step's
-// four runs of 16 tokens (lane % 4), looked up by `find` and checked by `use`,
-// which leaves them in scalars.  A run that no row of the tile sees (behind the
-// sequence, or between the first tokens and the windows, where pages may have
-// been given back) reads another's page; all of it is masked.
-struct ChunkPages {
-    const int32_t *table;
-    int page_shift, lo, reach, sunk;
-    uint32_t n_pages;
-    int32_t found = 0;
-    int32_t run[4];
-    bool bad = false;
-
-    __device__ __forceinline__ ChunkPages(const ChunkArgs &a, const ChunkTile &t)
-        : table(a.table + static_cast<int64_t>(t.b) * a.max_pages), page_shift(a.page_shift), lo(t.c.lo), reach(t.c.reach), sunk(t.c.sunk),
-          n_pages(static_cast<uint32_t>(a.n_pages))
-    {
-    }
-    __device__ __forceinline__ void find(int n0)
-    {
-        const int s = n0 + 16 * (threadIdx.x & 3);
-        const int tok = s < sunk ? s : min(max(s, lo), reach - 1);
-        found = table[tok >> page_shift];
-    }
-    __device__ __forceinline__ void use()
-    {
-        const bool is = static_cast<uint32_t>(found) < n_pages;
-        bad |= !is;
-        const int32_t pg = is ? found : 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) run[i] = __builtin_amdgcn_readlane(pg, i);
-    }
-    __device__ __forceinline__ int32_t of(int i) const
-    {
-        const int32_t a = i & 1 ? run[1] : run[0], b = i & 1 ? run[3] : run[2];
-        return i & 2 ? b : a;
-    }
-};
-
 // A step's buffers in LDS; int8 caches: with the steps of its tokens, K's times
 // scale and log2 e, V's in units of 2^*unit, which none exceeds.
 template <typename QT, typename T>
@@ -397,27 +70,6 @@ struct ChunkBuffer {
     float *ks, *vs;
     int *unit;
 };
-
-// 8 int8 codes (two dwords) as bf16, exact.
-__device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t a, uint32_t b)
-{
-    at_u32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t x = i < 2 ? a : b;
-        const float lo = static_cast<float>(static_cast<int8_t>(x >> (16 * (i & 1)))), hi = static_cast<float>(static_cast<int8_t>(x >> (16 * (i & 1) + 8)));
-        w[i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
-    }
-    return __builtin_bit_cast(bf16x8, w);
-}
-template <typename T>
-__device__ __forceinline__ typename Op16<T>::x8 codes_to(uint32_t a, uint32_t b)
-{
-    if constexpr (std::is_same<T, __bf16>::value)
-        return codes_to_bf16(a, b);
-    else
-        return codes_to_f16(a, b);
-}
 
 // A lane's share of bringing a step's keys and values into LDS.
 template <typename C, typename QT, int D>
@@ -508,23 +160,23 @@ struct ChunkStaging {
             char *at = reinterpret_cast<char *>(to.k) + i * W * 64 * 32;  // (64 rows or 16 on: the swizzle is the same)
             *reinterpret_cast<k8 *>(at + k_at) = codes_to<QT>(kr[i][0], kr[i][1]);
             *reinterpret_cast<k8 *>(at + (k_at ^ 16)) = codes_to<QT>(kr[i][2], kr[i][3]);
+            __builtin_amdgcn_sched_barrier(0);  // (or all codes are converted before the first are stored)
         }
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
             char *at = reinterpret_cast<char *>(to.v) + i * (NT / 4) * (2 * BN);
             *reinterpret_cast<f16x8 *>(at + v_at) = codes_to_f16(vr[i][0], vr[i][1]);
             *reinterpret_cast<f16x8 *>(at + (v_at ^ 16)) = codes_to_f16(vr[i][2], vr[i][3]);
+            __builtin_amdgcn_sched_barrier(0);
         }
         // (the product is finite, or it would make a NaN of a sum of zero)
         if (wave == 0) to.ks[lane] = step != step ? step : fminf(step * c, 3.4028235e38f);
         if (wave == 1) {
-            // The unit: a power of two that no step exceeds among those that
-            // some row sees, the last one's as long as it is at most 2^12 more.
             const int key = n0 + lane;
             const bool some = (key < reach) & ((key >= lo) | (key < sunk));
             const float top = wave_max(some ? step : 0.0f);
             const int e = __builtin_amdgcn_readfirstlane(static_cast<int>(__builtin_bit_cast(uint32_t, top) >> 23) - 126);  // 2^e above
-            if (e > unit || e < unit - 12) unit = e > 125 ? unit : e + 2;
+            unit = unit_of_steps(unit, e);
             to.vs[lane] = ldexpf(step, -unit);
             if (lane == 0) *to.unit = unit;
         }
@@ -544,53 +196,6 @@ __device__ __forceinline__ bool clean_values(T *v)
         }
     }
     return odd;
-}
-
-// What was met on the way, for the end: keys among which a V tile had a NaN or
-// an infinity removed, and whether a page was not there.
-struct ChunkNotes {
-    int odd_from, odd_to, bad;
-};
-
-// The page of a key, -1 if there is none.
-__device__ __forceinline__ int64_t page_of_key(const ChunkArgs &a, const ChunkTile &t, int key)
-{
-    const int64_t pg = a.table[static_cast<int64_t>(t.b) * a.max_pages + (key >> a.page_shift)];
-    return pg >= 0 && pg < a.n_pages ? pg : -1;
-}
-
-// Adds to O^T, dimensions d0 + 32 i + ..., the NaNs and infinities among the
-// values that the row sees and that were left out of the products.
-template <typename T, int N>
-__device__ __forceinline__ void add_odd_values(const ChunkArgs &a, const ChunkTile &t, const ChunkRow &row,
-                                               const ChunkNotes &notes, int d, int d0, int half, at_f32x16 (&o)[N])
-{
-    const int64_t page = int64_t{1} << a.page_shift;
-    for (int j = notes.odd_from; j < notes.odd_to && j < t.c.reach; ++j) {
-        if (j >= t.c.sunk && j < t.c.lo) continue;
-        const int64_t pg = page_of_key(a, t, j);
-        if (pg < 0 || !(j < row.seen.hi && (j >= row.seen.lo || j < a.sinks))) continue;
-        const T *src = static_cast<const T *>(a.v_pages) + ((pg * a.hkv + t.kh) * d + d0 + 4 * half) * page + (j & (page - 1));
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float x = static_cast<float>(src[(32 * i + 8 * (e >> 2) + (e & 3)) * page]);
-                if (!(fabsf(x) <= 3.4028235e38f)) o[i][e] += x;
-            }
-    }
-}
-
-// The row sees a key whose page is not there.
-__device__ __forceinline__ bool sees_bad_page(const ChunkArgs &a, const ChunkTile &t, const ChunkRow &row)
-{
-    bool bad = false;
-    const int first = row.seen.lo >> a.page_shift, end = (row.seen.hi + (1 << a.page_shift) - 1) >> a.page_shift;
-    for (int i = 0; i < end && i < first; ++i)
-        if ((i << a.page_shift) < a.sinks) bad |= page_of_key(a, t, i << a.page_shift) < 0;
-        else break;
-    for (int i = first; i < end; ++i) bad |= page_of_key(a, t, i << a.page_shift) < 0;
-    return bad;
 }
 
 // The row's dimensions d0 + 32 i + 8 b + 4 half + e, finished: as they are, or
@@ -644,190 +249,6 @@ __device__ __forceinline__ void finish(const ChunkArgs &a, const ChunkTile &t, c
         if (notes.odd_from < notes.odd_to) add_odd_values<C, N>(a, t, row, notes, d, d0, half, o);
     if (row.is) store_rows<QT, N>(a, t, row, at, d, d0, half, o, m, l);
 }
-
-// One lane's row as the products' B operand (k = 16 kk + 8 half + j).
-template <typename QT, int D>
-struct ChunkQuery {
-    typename Op16<QT>::x8 f[D / 16];
-    __device__ __forceinline__ ChunkQuery(const ChunkArgs &a, const ChunkTile &t, const ChunkRow &row, int half)
-    {
-        const QT *qp = static_cast<const QT *>(a.q) + (static_cast<int64_t>(t.q0) + row.tok) * a.qs + static_cast<int64_t>(row.head) * D;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) f[kk] = *reinterpret_cast<const typename Op16<QT>::x8 *>(qp + 16 * kk + 8 * half);
-    }
-};
-
-// Which keys of a step a row does not see.
-struct HiddenKeys {
-    int hi, lo, sinks;
-    bool gap;  // (of any row) first keys that are seen beside the window are among them
-    __device__ __forceinline__ HiddenKeys(const SeenKeys &seen, const ChunkTile &t, int n0)
-        : hi(seen.hi), lo(seen.lo), sinks(t.c.sunk), gap(n0 < t.c.sunk)
-    {
-    }
-    // (no branches in these: a value that one selects is lost by the compiler)
-    __device__ __forceinline__ bool beside_gap(int key) const { return (key >= hi) | ((key < lo) & (key >= sinks)); }
-    __device__ __forceinline__ bool without_gap(int key) const
-    {
-        return static_cast<uint32_t>(key - lo) >= static_cast<uint32_t>(hi - lo);
-    }
-};
-
-// The weights of KT * 32 keys from key n0 on, of one lane's row (score
-// register j of tile t: key n0 + 32 t + 16 (j / 8) + 8 half + j % 8).
-//
-// int8 caches: a weight times its value's step, in the step's unit, is p vs; o
-// is in units of 2^unit of its row.  Where the two units are the same in all
-// rows, that is all; elsewhere (the first steps, after the reference has moved,
-// where steps differ much, and on the border) the row's unit goes by the
-// products themselves, so that they are below 2^15, by at most 2^12 more than
-// they need: what is lost is below 2^-27 of the row's largest.
-template <typename C, int KT>
-struct ChunkSoftmax {
-    static constexpr bool I8 = std::is_same<C, int8_t>::value;
-    typedef typename WeightOf<C>::type T;
-    typedef typename Op16<T>::x8 x8;
-    float m = -__builtin_inff(), l = 0.0f, l2 = 0.0f;  // m: the reference, in units of log2
-    bool large = false;
-    int unit = -126;
-
-    static __device__ __forceinline__ int key(int t, int j, int half) { return 32 * t + 16 * (j >> 3) + 8 * half + (j & 7); }
-
-    // the largest score of the lane's pair; hidden ones leave the scores
-    template <bool BORDER>
-    __device__ __forceinline__ float top(at_f32x16 (&s)[KT], const HiddenKeys &hidden, int n0, int half, float c, const float *ks)
-    {
-        if constexpr (I8) {
-#pragma unroll
-            for (int t = 0; t < KT; ++t)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    s[t][j] *= ks[key(t, j, half)];
-                    if ((j & 7) == 7) __builtin_amdgcn_sched_barrier(0);  // (or all steps are read up front)
-                }
-        }
-        if constexpr (BORDER) {
-            if (hidden.gap) {
-#pragma unroll
-                for (int t = 0; t < KT; ++t)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) s[t][j] = hidden.beside_gap(n0 + key(t, j, half)) ? -__builtin_inff() : s[t][j];
-            } else {
-#pragma unroll
-                for (int t = 0; t < KT; ++t)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) s[t][j] = hidden.without_gap(n0 + key(t, j, half)) ? -__builtin_inff() : s[t][j];
-            }
-        }
-        float top = s[0][0];
-#pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) top = fmaxf(top, s[t][j]);
-        top = lane_pair_max<32>(top);
-        return I8 ? top : top * c;
-    }
-
-    // The reference follows the largest score, by 8 at most behind it (weights
-    // up to 2^8 lose nothing): few steps after the first rescale.  units: o's.
-    template <int N>
-    __device__ __forceinline__ void raise(float top, at_f32x16 (&o)[N], int &units)
-    {
-        const float mt = reference<T>(top);
-        if (__ballot(mt > m + 8.0f) != 0) {
-            const float mn = fmaxf(m, mt);
-            float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
-            l *= f;
-            l2 *= f;
-            if constexpr (I8) {
-                // the units come down with the weights, or a large step whose
-                // weight has become nothing would keep the resolution coarse
-                int down = static_cast<int>(__builtin_bit_cast(uint32_t, f) >> 23) - 126;  // f < 2^down
-                down = down > 0 ? 0 : down;
-                f *= pow2(-down);
-                if (&units != &unit) unit = max(unit + down, -300);
-                units = max(units + down, -300);
-            }
-#pragma unroll
-            for (int i = 0; i < N; ++i) o[i] *= f;
-            m = mn;
-            large = large_scores(m);
-        }
-    }
-
-    // 16-bit caches
-    __device__ __forceinline__ void weights(at_f32x16 (&s)[KT], float c, x8 (&pf)[2 * KT])
-    {
-        const float ms = m == -__builtin_inff() ? 0.0f : m;
-        float mul = c;
-        if (large) {
-#pragma unroll
-            for (int t = 0; t < KT; ++t)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) s[t][j] *= c;
-            mul = 1.0f;
-        }
-#pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                pf[2 * t + (j >> 3)][j & 7] = static_cast<T>(__builtin_amdgcn_exp2f(fmaf(s[t][j], mul, -ms)));
-#pragma unroll
-        for (int u = 0; u < 2 * KT; u += 2) {
-            l = add_weights<T>(pf[u], l);
-            l2 = add_weights<T>(pf[u + 1], l2);
-        }
-    }
-
-    // int8 caches: weights times steps; rescale(f): o's unit has become 1 / f of what it was
-    template <bool BORDER, class F>
-    __device__ __forceinline__ void products(at_f32x16 (&s)[KT], const HiddenKeys &hidden, int n0, int half, const float *vs,
-                                             int of_steps, x8 (&pf)[2 * KT], F rescale)
-    {
-        const float ms = m == -__builtin_inff() ? 0.0f : m;
-#pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float p = __builtin_amdgcn_exp2f(s[t][j] - ms);
-                if ((j & 1) == 0) l += p;
-                else l2 += p;
-                s[t][j] = p * vs[key(t, j, half)];
-                if ((j & 7) == 7) __builtin_amdgcn_sched_barrier(0);
-            }
-        if constexpr (BORDER) {
-            // a weight of nothing leaves a NaN as it is: of a step that the row does not see
-#pragma unroll
-            for (int t = 0; t < KT; ++t)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) s[t][j] = hidden.beside_gap(n0 + key(t, j, half)) ? 0.0f : s[t][j];
-        }
-        if (BORDER || __ballot(unit != of_steps) != 0) {
-            float top = s[0][0];
-#pragma unroll
-            for (int t = 0; t < KT; ++t)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) top = fmaxf(top, s[t][j]);
-            top = lane_pair_max<32>(top);
-            // (2^e above the largest)
-            const int need = static_cast<int>(__builtin_bit_cast(uint32_t, top) >> 23) - 126 - 15 + of_steps;
-            const int next = max(need, min(of_steps, need + 12));
-            if (next > unit) {
-                rescale(ldexpf(1.0f, unit - next));
-                unit = next;
-            }
-            const int by = of_steps - unit;
-#pragma unroll
-            for (int t = 0; t < KT; ++t)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) s[t][j] = ldexpf(s[t][j], by);
-        }
-#pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) pf[2 * t + (j >> 3)][j & 7] = static_cast<T>(s[t][j]);
-    }
-};
 
 // The steps first .. last in pairs (a buffer each): in the inner loops those
 // whose keys every row sees, and the others.
@@ -929,10 +350,10 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             }
             __builtin_amdgcn_sched_group_barrier(0x8, kAhead, 0);
-            w.raise(w.template top<BORDER>(s, HiddenKeys(seen, t, n0), n0, half, c, b.ks), o, w.unit);
+            w.raise(w.top(BORDER, s, HiddenKeys(seen, t, n0), n0, half, c, [&](int k, int j) { return b.ks[w.key(k, j, half)]; }), o, w.unit);
             if constexpr (I8) {
                 if constexpr (BORDER) asm volatile("" : "+v"(seen.lo), "+v"(seen.hi));  // (or the masks of 64 keys are kept)
-                w.template products<BORDER>(s, HiddenKeys(seen, t, n0), n0, half, b.vs, *b.unit, pf, [&](float f) {
+                w.products(BORDER, s, HiddenKeys(seen, t, n0), n0, half, [&](int k, int j) { return b.vs[w.key(k, j, half)]; }, *b.unit, pf, [&](float f) {
 #pragma unroll
                     for (int d = 0; d < DT; ++d) o[d] *= f;
                 });
@@ -1065,7 +486,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             }
             __builtin_amdgcn_sched_group_barrier(0x8, kAhead, 0);
-            top = w.template top<BORDER>(s, HiddenKeys(seen, t, n0), mine, half, c, b.ks + 32 * part);
+            top = w.top(BORDER, s, HiddenKeys(seen, t, n0), mine, half, c, [&](int, int j) { return b.ks[32 * part + w.key(0, j, half)]; });
             if (half == 0) tops[pair][part][col] = top;
         }
         barrier_lds();
@@ -1075,7 +496,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
             x8 pf[2];
             if constexpr (I8) {
                 if constexpr (BORDER) asm volatile("" : "+v"(seen.lo), "+v"(seen.hi));
-                w.template products<BORDER>(s, HiddenKeys(seen, t, n0), mine, half, b.vs + 32 * part, *b.unit, pf, [](float) {});
+                w.products(BORDER, s, HiddenKeys(seen, t, n0), mine, half, [&](int, int j) { return b.vs[32 * part + w.key(0, j, half)]; }, *b.unit, pf, [](float) {});
                 if (half == 0) units[pair][part][col] = w.unit;
             } else
                 w.weights(s, c, pf);
@@ -1146,29 +567,32 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
     finish<C, QT, DT>(a, end, chunk_row(a, end, at), notes, at, D, 128 * part, half, o, w.m, l, o_unit);
 }
 
-// Joins the parts of the tiles that were cut: D / 4 lanes per row, one row each
-// at a time (blockIdx.y: which of a tile's rows).
-constexpr int join_rows(int d) { return 256 / (d / 4); }
+// Joins the parts of the tiles that were cut: D / 4 lanes hold a row, and where
+// few tiles have many pieces, all groups of lanes share one row's (G > 1), each
+// taking every G-th (blockIdx.y: which of a tile's rows).
+constexpr int join_lanes(int d) { return d / 4; }
 constexpr int64_t kJoinGroups = 2048;
 constexpr int kJoinAhead = 4;
 
-template <typename QT, int D>
+template <typename QT, int D, bool MANY>
 __global__ void __launch_bounds__(256) k_chunk_join(ChunkArgs a)
 {
-    constexpr int LPR = D / 4;
+    constexpr int LPR = join_lanes(D), GROUPS = 256 / LPR, G = MANY ? GROUPS : 1, ROWS = GROUPS / G;
+    __shared__ at_f32x4 sums[MANY ? GROUPS : 1][LPR];
     ChunkTile t;
     if (!chunk_tile<QT, D>(a, blockIdx.x, true, t) || t.pieces == 1) return;
-    const int x = threadIdx.x % LPR;
-    for (int r = t.row0 + static_cast<int>(blockIdx.y * join_rows(D) + threadIdx.x / LPR); r < t.end; r += gridDim.y * join_rows(D)) {
+    const int x = threadIdx.x % LPR, g = threadIdx.x / LPR, part = MANY ? g : 0;
+    const int64_t stride = static_cast<int64_t>(t.stride) * a.hkv * a.slot_rows;
+    for (int r = t.row0 + static_cast<int>(blockIdx.y) * ROWS + (MANY ? 0 : g); r < t.end; r += gridDim.y * ROWS) {
         const ChunkRow row = chunk_row(a, t, r);
-        const int64_t first = part_slot(a, t, r), stride = static_cast<int64_t>(t.stride) * a.hkv * a.slot_rows;
+        const int64_t first = part_slot(a, t, r);
         const float2 *ml = reinterpret_cast<const float2 *>(a.parts + a.rows_floats) + first;
         const float *src = a.parts + first * D + 4 * x;
         // lane x has piece x's reference and sum (the first LPR of them), and
-        // every lane its elements of the first rows: one trip to memory
+        // every lane its elements of its first rows: one trip to memory
         at_f32x4 ahead[kJoinAhead];
 #pragma unroll
-        for (int i = 0; i < kJoinAhead; ++i) ahead[i] = *reinterpret_cast<const at_f32x4 *>(src + (i < t.pieces ? i : 0) * stride * D);
+        for (int i = 0; i < kJoinAhead; ++i) ahead[i] = *reinterpret_cast<const at_f32x4 *>(src + (part + i * G < t.pieces ? part + i * G : 0) * stride * D);
         const float2 mine = x < t.pieces ? ml[x * stride] : float2{-__builtin_inff(), 0.0f};
         float M = mine.x;
         for (int i = x + LPR; i < t.pieces; i += LPR) M = fmaxf(M, ml[i * stride].x);
@@ -1188,36 +612,53 @@ __global__ void __launch_bounds__(256) k_chunk_join(ChunkArgs a)
         at_f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < kJoinAhead; ++i)
-            if (i < t.pieces) o += weight_of(i) * ahead[i];
+            if (part + i * G < t.pieces) o += weight_of(part + i * G) * ahead[i];
 #pragma unroll 4
-        for (int i = kJoinAhead; i < t.pieces; ++i) o += weight_of(i) * *reinterpret_cast<const at_f32x4 *>(src + i * stride * D);
-        store4(static_cast<QT *>(a.out) + ((static_cast<int64_t>(t.q0) + row.tok) * a.hq + row.head) * D + 4 * x, o);
+        for (int i = part + kJoinAhead * G; i < t.pieces; i += G) o += weight_of(i) * *reinterpret_cast<const at_f32x4 *>(src + i * stride * D);
+        if constexpr (MANY) {
+            sums[g][x] = o;
+            __syncthreads();
+            if (g == 0) {
+#pragma unroll
+                for (int i = 1; i < GROUPS; ++i) o += sums[i][x];
+            }
+            __syncthreads();
+        }
+        if (!MANY || g == 0)
+            store4(static_cast<QT *>(a.out) + ((static_cast<int64_t>(t.q0) + row.tok) * a.hq + row.head) * D + 4 * x, o);
     }
 }
 
 template <typename C, typename QT, int D>
-hipError_t chunk_launch(const ChunkArgs &a, const ChunkPlan &p, hipStream_t s)
+hipError_t chunk_launch(const ChunkArgs &a, const ChunkPlan &p, int cache_type, int q_type, hipStream_t s)
 {
     const dim3 grid(static_cast<uint32_t>(p.numbers * a.hkv));
-    if constexpr (D == 256)
+    if (p.few) {
+        const hipError_t e = launch_chunk_few(a, cache_type, q_type, D, grid.x, s);
+        if (e != hipSuccess) return e;
+    } else if constexpr (D == 256)
         hipLaunchKernelGGL((k_attn_chunk_wide<C, QT>), grid, dim3(64 * chunk_waves(D)), 0, s, a);
     else
         hipLaunchKernelGGL((k_attn_chunk<C, QT, D>), grid, dim3(64 * chunk_waves(D)), 0, s, a);
     if (p.cut) {
         // a workgroup for some rows of a tile each; many tiles are mostly uncut,
         // and their workgroups only find that out
-        const int64_t tiles = p.tiles * a.hkv, rows = (p.slot_rows + join_rows(D) - 1) / join_rows(D);
-        const int64_t each = kJoinGroups / tiles;
-        hipLaunchKernelGGL((k_chunk_join<QT, D>), dim3(static_cast<uint32_t>(tiles), static_cast<uint32_t>(each < 1 ? 1 : each < rows ? each : rows)),
-                           dim3(256), 0, s, a);
+        const int64_t tiles = p.tiles * a.hkv, each = kJoinGroups / tiles;
+        const bool many = p.numbers >= 8 * p.tiles;
+        const int64_t at_once = many ? 1 : 256 / join_lanes(D), rows = (p.slot_rows + at_once - 1) / at_once;
+        const dim3 groups(static_cast<uint32_t>(tiles), static_cast<uint32_t>(each < 1 ? 1 : each < rows ? each : rows));
+        if (many)
+            hipLaunchKernelGGL((k_chunk_join<QT, D, true>), groups, dim3(256), 0, s, a);
+        else
+            hipLaunchKernelGGL((k_chunk_join<QT, D, false>), groups, dim3(256), 0, s, a);
     }
     return hipGetLastError();
 }
 
 template <typename C, typename QT>
-hipError_t chunk_d(const ChunkArgs &a, const ChunkPlan &p, int d, hipStream_t s)
+hipError_t chunk_d(const ChunkArgs &a, const ChunkPlan &p, int cache_type, int q_type, int d, hipStream_t s)
 {
-    return d == 64 ? chunk_launch<C, QT, 64>(a, p, s) : d == 128 ? chunk_launch<C, QT, 128>(a, p, s) : chunk_launch<C, QT, 256>(a, p, s);
+    return d == 64 ? chunk_launch<C, QT, 64>(a, p, cache_type, q_type, s) : d == 128 ? chunk_launch<C, QT, 128>(a, p, cache_type, q_type, s) : chunk_launch<C, QT, 256>(a, p, cache_type, q_type, s);
 }
 
 }  // namespace
@@ -1232,6 +673,7 @@ ChunkPlan chunk_plan(int64_t batch, int64_t q_rows, int64_t max_q, int32_t hq, i
     const int64_t group = hq / hkv, rows = max_q * group;
     p.tiles = q_rows * group / kChunkRows + batch;
     p.numbers = p.tiles;
+    p.few = rows <= kFewRows;
     p.slot_rows = static_cast<int32_t>(rows < kChunkRows ? rows : kChunkRows);
     const int64_t slots = d == 256 ? 256 : 512;  // workgroups that the GPU holds
     p.wanted = static_cast<int32_t>(slots / hkv > 1 ? slots / hkv : 1);
@@ -1246,7 +688,8 @@ ChunkPlan chunk_plan(int64_t batch, int64_t q_rows, int64_t max_q, int32_t hq, i
         const double step = d == 256 ? 2.6 : d == 128 ? 1.9 : 1.1;
         p.join_cost = static_cast<float>(6.0 / step);
         p.piece_cost = static_cast<float>(static_cast<double>(hkv) * p.slot_rows * d * 4 * 2 / 2.5e6 / step);
-        p.numbers = numbers;
+        const int64_t pieces = p.tiles * ((most + kChunkMinSteps - 1) / kChunkMinSteps);
+        p.numbers = pieces < numbers ? pieces : numbers;
         p.rows_floats = static_cast<size_t>(parts) * d;
         p.part_floats = p.rows_floats + static_cast<size_t>(parts) * 2;
     }
@@ -1258,13 +701,16 @@ hipError_t launch_attn_chunk(const ChunkPlan &p, const void *q, int64_t qs, int 
                              int64_t max_pages, const int32_t *lens, int64_t max_len, int32_t window, int32_t sinks,
                              float scale, void *out, float *parts, hipStream_t s)
 {
-    const ChunkArgs a{q, qs, cu, lens, table, max_pages, batch, q_rows, max_q, max_len, hq, c.n_kv_heads, c.k_pages,
+    int head_shift = 24;  // the product is off by less than 2^head_shift / 2^24 heads of 2^24
+    while ((1 << (head_shift - 24)) < c.n_kv_heads) ++head_shift;
+    const uint32_t per_head = static_cast<uint32_t>(((int64_t{1} << head_shift) + c.n_kv_heads - 1) / c.n_kv_heads);
+    const ChunkArgs a{q, qs, cu, lens, table, max_pages, batch, q_rows, max_q, max_len, hq, c.n_kv_heads, hq / c.n_kv_heads, per_head, head_shift, c.k_pages,
                       c.v_pages, c.k_steps, c.v_steps, c.n_pages, __builtin_ctz(static_cast<unsigned>(c.page_size)),
                       window, sinks, scale, out, p.wanted, p.cut, 2 * p.wanted, p.slot_rows,
                       p.join_cost, p.piece_cost, static_cast<int64_t>(p.rows_floats), parts};
-    if (c.dtype == PTQ1_BF16) return chunk_d<__bf16, __bf16>(a, p, c.head_dim, s);
-    if (c.dtype == PTQ1_F16) return chunk_d<_Float16, _Float16>(a, p, c.head_dim, s);
-    return q_type == PTQ1_F16 ? chunk_d<int8_t, _Float16>(a, p, c.head_dim, s) : chunk_d<int8_t, __bf16>(a, p, c.head_dim, s);
+    if (c.dtype == PTQ1_BF16) return chunk_d<__bf16, __bf16>(a, p, c.dtype, q_type, c.head_dim, s);
+    if (c.dtype == PTQ1_F16) return chunk_d<_Float16, _Float16>(a, p, c.dtype, q_type, c.head_dim, s);
+    return q_type == PTQ1_F16 ? chunk_d<int8_t, _Float16>(a, p, c.dtype, q_type, c.head_dim, s) : chunk_d<int8_t, __bf16>(a, p, c.dtype, q_type, c.head_dim, s);
 }
 
 }  // namespace ptq1

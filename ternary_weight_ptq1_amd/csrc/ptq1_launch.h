@@ -211,6 +211,7 @@ struct ChunkPlan {
     int32_t wanted = 1, slot_rows = 0;
     float join_cost = 0.0f, piece_cost = 0.0f;  // in steps
     bool cut = false;
+    bool few = false;  // no sequence has more than 32 rows of a kv head
     size_t rows_floats = 0, part_floats = 0;
 };
 ChunkPlan chunk_plan(int64_t batch, int64_t q_rows, int64_t max_q, int32_t hq, int32_t hkv, int32_t d, int64_t max_len,
