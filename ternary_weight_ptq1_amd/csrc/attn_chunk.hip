@@ -644,7 +644,7 @@ hipError_t chunk_launch(const ChunkArgs &a, const ChunkPlan &p, int cache_type, 
         // a workgroup for some rows of a tile each; many tiles are mostly uncut,
         // and their workgroups only find that out
         const int64_t tiles = p.tiles * a.hkv, each = kJoinGroups / tiles;
-        const bool many = p.numbers >= 8 * p.tiles;
+        const bool many = p.few && p.wanted >= 16 * p.tiles;
         const int64_t at_once = many ? 1 : 256 / join_lanes(D), rows = (p.slot_rows + at_once - 1) / at_once;
         const dim3 groups(static_cast<uint32_t>(tiles), static_cast<uint32_t>(each < 1 ? 1 : each < rows ? each : rows));
         if (many)
@@ -685,8 +685,8 @@ ChunkPlan chunk_plan(int64_t batch, int64_t q_rows, int64_t max_q, int32_t hq, i
     if (p.cut) {
         // a step's time with the GPU full, a piece's rows written and read in
         // fp32 at half of HBM's rate (they come in bursts), and the join, in us
-        const double step = d == 256 ? 2.6 : d == 128 ? 1.9 : 1.1;
-        p.join_cost = static_cast<float>(6.0 / step);
+        const double step = p.few ? (d == 256 ? 2.7 : 1.35) : d == 256 ? 2.6 : d == 128 ? 1.9 : 1.1;
+        p.join_cost = static_cast<float>((p.few ? 5.0 : 6.0) / step);
         p.piece_cost = static_cast<float>(static_cast<double>(hkv) * p.slot_rows * d * 4 * 2 / 2.5e6 / step);
         const int64_t pieces = p.tiles * ((most + kChunkMinSteps - 1) / kChunkMinSteps);
         p.numbers = pieces < numbers ? pieces : numbers;

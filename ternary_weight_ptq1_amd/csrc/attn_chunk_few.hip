@@ -7,6 +7,8 @@
 namespace ptq1 {
 namespace {
 
+constexpr int kFewWaves = 4;
+
 // Few rows of a sequence's (32 of a kv head at most): its keys' bytes bound it, as
 // they do the single tokens' attention, and as there K and V come straight from
 // memory into the operands' registers, a wave's next K requested as soon as the
@@ -15,13 +17,13 @@ namespace {
 // the end.  Tiles of 128 rows in LDS took 13.7 us for 5 queries behind 700 tokens
 // (40 heads over 8) and TALL for 32 sequences of 4000 to 8000 tokens with 4 to 8.
 template <typename C, typename QT, int D>
-__global__ void __launch_bounds__(256, D == 256 ? 1 : 2) k_attn_chunk_few(ChunkArgs a)
+__global__ void __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) k_attn_chunk_few(ChunkArgs a)
 {
     typedef typename WeightOf<C>::type T;
     typedef typename Op16<QT>::x8 k8;
     typedef typename Op16<T>::x8 x8;
     constexpr bool I8 = std::is_same<C, int8_t>::value;
-    constexpr int W = 4, DT = D / 32, KK = D / 16;
+    constexpr int W = kFewWaves, DT = D / 32, KK = D / 16;
     constexpr int NL = I8 ? D / 32 : D / 16;  // 16-byte loads of a lane, for K and for V
     __shared__ __attribute__((aligned(16))) float rows[W * kFewRows * (D + 4)];
     __shared__ float ms[W][kFewRows], ls[W][kFewRows];
@@ -251,11 +253,11 @@ template <typename C, typename QT>
 void few_launch(const ChunkArgs &a, int d, uint32_t groups, hipStream_t s)
 {
     if (d == 64)
-        hipLaunchKernelGGL((k_attn_chunk_few<C, QT, 64>), dim3(groups), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_attn_chunk_few<C, QT, 64>), dim3(groups), dim3(64 * kFewWaves), 0, s, a);
     else if (d == 128)
-        hipLaunchKernelGGL((k_attn_chunk_few<C, QT, 128>), dim3(groups), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_attn_chunk_few<C, QT, 128>), dim3(groups), dim3(64 * kFewWaves), 0, s, a);
     else
-        hipLaunchKernelGGL((k_attn_chunk_few<C, QT, 256>), dim3(groups), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_attn_chunk_few<C, QT, 256>), dim3(groups), dim3(64 * kFewWaves), 0, s, a);
 }
 
 }  // namespace

@@ -8,7 +8,7 @@ namespace ptq1 {
 
 constexpr int kChunkRows = 128;   // query rows of a tile
 constexpr int kChunkKeys = 64;    // keys of one step
-constexpr int kChunkMinSteps = 4; // steps of a piece, at least
+constexpr int kChunkMinSteps = 4; // steps of a piece, at least (1 or 2 where rows are few: 705 keys 20.0 and 16.4 us for 16.1)
 
 constexpr int imax(int a, int b) { return a > b ? a : b; }
 constexpr int imin(int a, int b) { return a < b ? a : b; }
@@ -72,13 +72,13 @@ constexpr int chunk_piece(int total, int wanted) { return imax(kChunkMinSteps, (
 constexpr int chunk_cuts(int tiles, int steps, int wanted, float join_cost, float piece_cost)
 {
     int best = 1;
-    float least = 0.0f;
+    float lowest = 0.0f;
     for (int n = 1; n == 1 || (tiles * n <= 2 * wanted && (steps + n - 1) / n >= kChunkMinSteps); n += n < 8 ? 1 : n / 4) {
         const int rounds = (tiles * n + wanted - 1) / wanted;
         const float cost = static_cast<float>(rounds * ((steps + n - 1) / n)) +
                            (n > 1 ? join_cost + piece_cost * static_cast<float>(tiles * n) : 0.0f);
-        if (n == 1 || cost < least) {
-            least = cost;
+        if (n == 1 || cost < lowest) {
+            lowest = cost;
             best = n;
         }
     }

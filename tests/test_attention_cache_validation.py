@@ -229,10 +229,10 @@ def test_chunk_cache_refused():
 
 def test_chunk_workspace():
     size = lambda *a: P.workspace_bytes("attn_chunk", *a)  # noqa: E731
-    assert size(1, 5, 5, 40, 8, 128, 200, 0, 0) == 0                 # a few steps: nothing to cut
+    assert size(1, 5, 5, 40, 8, 128, 100, 0, 0) == 0                 # a few steps: nothing to cut
     few, more = size(1, 5, 5, 40, 8, 128, 8000, 0, 0), size(1, 5, 500, 40, 8, 128, 8000, 0, 0)
     assert 0 < few == more                                           # no sequence has more queries than there are
-    assert size(1, 5, 5, 40, 8, 128, 8000, 100, 4) == 0              # a small window: nothing to cut
+    assert size(1, 50, 50, 40, 8, 128, 8000, 30, 4) == 0             # a small window: nothing to cut
     assert size(1, 65536, 65536, 40, 8, 128, 65536, 0, 0) == 0       # the tiles fill the GPU
     assert size(-1, 5, 5, 40, 8, 128, 200, 0, 0) == 0 and size(1, 5, 5, 40, 8, 128, 200, -1, 0) == 0
 
