@@ -183,19 +183,31 @@ struct ChunkStaging {
     }
 };
 
-// A NaN or an infinity leaves a V tile in LDS (zeros in its place); true if there was one.
+// A NaN or an infinity leaves a V tile in LDS (zeros in its place); true if there
+// was one.  Most tiles have none, which the largest magnitude among a thread's
+// values tells.
 template <typename T, int D>
 __device__ __forceinline__ bool clean_values(T *v)
 {
-    bool odd = false;
-    for (int i = threadIdx.x; i < BN * D / 8; i += 64 * chunk_waves(D)) {
-        at_u32x4 w = *reinterpret_cast<const at_u32x4 *>(v + 8 * i);
-        if (clear_non_finite<T>(w)) {
-            *reinterpret_cast<at_u32x4 *>(v + 8 * i) = w;
-            odd = true;
+    constexpr int NT = 64 * chunk_waves(D), N = BN * D / 8 / NT;
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    constexpr uint16_t kNone = std::is_same<T, __bf16>::value ? 0x7f80u : 0x7c00u;
+    at_u32x4 w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const at_u32x4 *>(v + 8 * (i * NT + threadIdx.x));
+    u16x2 most = {0, 0};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t x = w[i][j] & 0x7fff7fffu;
+            most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, x));
         }
-    }
-    return odd;
+    if (most[0] < kNone && most[1] < kNone) return false;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (clear_non_finite<T>(w[i])) *reinterpret_cast<at_u32x4 *>(v + 8 * (i * NT + threadIdx.x)) = w[i];
+    return true;
 }
 
 // The row's dimensions d0 + 32 i + 8 b + 4 half + e, finished: as they are, or
