@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
     for (int i = 0; i < DT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
-    ChunkSoftmax<C, KT> w;
+    ChunkSoftmax<C, KT, 1> w;
 
     // One step, while the next one's keys and values arrive in the other buffers.
     auto step = [&](auto border, auto odd, int i) __attribute__((always_inline)) {
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
         pages.find(step_key(t.c, min(i + 2, t.last - 1)));  // (in no branch, at whose end the compiler would wait for it)
         SeenKeys seen{0, 0};
         if constexpr (BORDER) seen = seen_of[32 * wave + col];
-        x8 pf[2 * KT];
+        x8 pf[1][2 * KT];
         if (!idle) {
             at_f32x16 s[KT];
             const int k_row = not_kept(row_start<D>(token_of_row(col)) ^ (16 * half));
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
             for (int u = 0; u < 2 * KT; ++u)
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
-                    o[d] = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(reinterpret_cast<const char *>(b.v) + (v_row ^ (32 * u)) + 32 * d * (2 * BN)), pf[u], o[d]);
+                    o[d] = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(reinterpret_cast<const char *>(b.v) + (v_row ^ (32 * u)) + 32 * d * (2 * BN)), pf[0][u], o[d]);
         }
         if constexpr (I8)
             if (i + 1 < t.last) staging.store(step_key(t.c, i + 1), next);
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
     for (int i = 0; i < DT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
-    ChunkSoftmax<C, 1> w;  // l: of this wave's keys
+    ChunkSoftmax<C, 1, 1> w;  // l: of this wave's keys
     int o_unit = -126;
 
     auto step = [&](auto border, auto odd, int i) __attribute__((always_inline)) {
@@ -505,15 +505,15 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
         if (!idle) {
             top = fmaxf(top, tops[pair][part ^ 1][col]);
             w.raise(top, o, o_unit);  // the same in both waves
-            x8 pf[2];
+            x8 pf[1][2];
             if constexpr (I8) {
                 if constexpr (BORDER) asm volatile("" : "+v"(seen.lo), "+v"(seen.hi));
                 w.products(BORDER, s, HiddenKeys(seen, t, n0), mine, half, [&](int, int j) { return b.vs[32 * part + w.key(0, j, half)]; }, *b.unit, pf, [](float) {});
                 if (half == 0) units[pair][part][col] = w.unit;
             } else
                 w.weights(s, c, pf);
-            weights[pair][2 * part][lane] = pf[0];
-            weights[pair][2 * part + 1][lane] = pf[1];
+            weights[pair][2 * part][lane] = pf[0][0];
+            weights[pair][2 * part + 1][lane] = pf[0][1];
         }
         if constexpr (BORDER && !I8) {
             if (clean_values<T, D>(b.v)) {

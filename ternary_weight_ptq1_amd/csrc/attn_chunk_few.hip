@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) k_attn_chunk
     for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[d][j] = 0.0f;
-    ChunkSoftmax<C, 1, I8> w;
+    ChunkSoftmax<C, 1, 2, I8> w;
     ChunkNotes notes{1 << 30, 0, 0};
     int steps_unit = -126;
 
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) k_attn_chunk
         }
         const HiddenKeys hidden(row.seen, t, n0);
         w.raise(w.top(border, s, hidden, n0, half, c, [](int, int) { return 1.0f; }), o, w.unit);
-        x8 pf[2];
+        x8 pf[2][2];  // [term][16 keys]
         if constexpr (I8) {
             float most = 0.0f;
 #pragma unroll
@@ -174,7 +174,8 @@ __global__ void __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) k_attn_chunk
                     if ((d & 1) == 1) __builtin_amdgcn_sched_barrier(0);
                 } else
                     vf = __builtin_bit_cast(x8, vr[2 * d + u]);
-                o[d] = Op16<T>::mfma32(vf, pf[u], o[d]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) o[d] = Op16<T>::mfma32(vf, pf[k][u], o[d]);
             }
         if (more) {
             load_v(key_of(i + W));

@@ -457,7 +457,10 @@ struct HiddenKeys {
 // they need: what is lost is below 2^-27 of the row's largest.
 //
 // RUN16: register j is key n0 + 32 t + 16 half + j instead.
-template <typename C, int KT, bool RUN16 = false>
+// TERMS: 16-bit terms that a weight (int8: times its step) enters as, the second
+// the rounding of what the first one leaves.  With one, the sum is that of the
+// rounded weights.
+template <typename C, int KT, int TERMS, bool RUN16 = false>
 struct ChunkSoftmax {
     static constexpr bool I8 = std::is_same<C, int8_t>::value;
     typedef typename WeightOf<C>::type T;
@@ -534,8 +537,23 @@ struct ChunkSoftmax {
         }
     }
 
+    // the terms of what is in s
+    __device__ __forceinline__ void terms(const at_f32x16 (&s)[KT], x8 (&pf)[TERMS][2 * KT])
+    {
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                float x = s[t][j];
+                if constexpr (TERMS > 1) asm volatile("" : "+v"(x));  // (one rounding of a product behind it for both terms)
+                const T first = static_cast<T>(x);
+                pf[0][2 * t + (j >> 3)][j & 7] = first;
+                if constexpr (TERMS > 1) pf[1][2 * t + (j >> 3)][j & 7] = static_cast<T>(x - static_cast<float>(first));
+            }
+    }
+
     // 16-bit caches
-    __device__ __forceinline__ void weights(at_f32x16 (&s)[KT], float c, x8 (&pf)[2 * KT])
+    __device__ __forceinline__ void weights(at_f32x16 (&s)[KT], float c, x8 (&pf)[TERMS][2 * KT])
     {
         const float ms = m == -__builtin_inff() ? 0.0f : m;
         float mul = c;
@@ -549,19 +567,27 @@ struct ChunkSoftmax {
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                pf[2 * t + (j >> 3)][j & 7] = static_cast<T>(__builtin_amdgcn_exp2f(fmaf(s[t][j], mul, -ms)));
+            for (int j = 0; j < 16; ++j) {
+                s[t][j] = __builtin_amdgcn_exp2f(fmaf(s[t][j], mul, -ms));
+                if constexpr (TERMS > 1) {
+                    if ((j & 1) == 0) l += s[t][j];
+                    else l2 += s[t][j];
+                }
+            }
+        terms(s, pf);
+        if constexpr (TERMS == 1) {
 #pragma unroll
-        for (int u = 0; u < 2 * KT; u += 2) {
-            l = add_weights<T>(pf[u], l);
-            l2 = add_weights<T>(pf[u + 1], l2);
+            for (int u = 0; u < 2 * KT; u += 2) {
+                l = add_weights<T>(pf[0][u], l);
+                l2 = add_weights<T>(pf[0][u + 1], l2);
+            }
         }
     }
 
     // int8 caches: weights times steps; rescale(f): o's unit has become 1 / f of what it was
     template <class S, class F>
     __device__ __forceinline__ void products(bool border, at_f32x16 (&s)[KT], const HiddenKeys &hidden, int n0, int half, S vs,
-                                             int of_steps, x8 (&pf)[2 * KT], F rescale)
+                                             int of_steps, x8 (&pf)[TERMS][2 * KT], F rescale)
     {
         const float ms = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll
@@ -601,10 +627,7 @@ struct ChunkSoftmax {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) s[t][j] = ldexpf(s[t][j], by);
         }
-#pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) pf[2 * t + (j >> 3)][j & 7] = static_cast<T>(s[t][j]);
+        terms(s, pf);
     }
 };
 
