@@ -48,12 +48,23 @@ __device__ __forceinline__ int swizzle(int r)
 {
     return W >= 128 ? r & 15 : (r >> 1) & 7;
 }
-// The byte offset of piece 0 of row r; piece p is at it ^ 16 p.
-template <int W>
-__device__ __forceinline__ int row_start(int r)
+// The byte offset of piece `half` of row r; piece 2 i + half is at it ^ kPair i.
+//
+// Of int8 caches a thread brings 16 codes, which are two pieces: the first
+// pieces of a row fill its first half and the second ones the other, and the
+// swizzle's bits are turned by one, so that 16 threads write 16 pieces on all
+// banks too.
+template <typename C, int W>
+__device__ __forceinline__ int row_of(int r, int half)
 {
-    return r * (2 * W) + 16 * swizzle<W>(r);
+    if constexpr (std::is_same<C, int8_t>::value) {
+        const int x = swizzle<W>(r);
+        return (r * (2 * W) + 16 * ((x >> 1) | (x & 1) * (W >= 128 ? 8 : 4))) ^ (W * half);
+    }
+    return (r * (2 * W) + 16 * swizzle<W>(r)) ^ (16 * half);
 }
+template <typename C>
+constexpr int kPair = std::is_same<C, int8_t>::value ? 16 : 32;
 // The value, which the compiler then makes anew where it is used: what every
 // step makes of a lane's place it would keep in registers through all of them.
 __device__ __forceinline__ int not_kept(int v)
@@ -152,21 +163,21 @@ struct ChunkStaging {
     {
         constexpr int L = D / 16;
         const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const int k_at = not_kept(row_start<D>(wave * (64 / L) + lane / L) ^ (32 * (lane % L)));
-        const int v_at = not_kept(row_start<BN>(static_cast<int>(threadIdx.x >> 2)) ^ (32 * (lane & 3)));
+        const int k_at = not_kept(row_of<C, D>(wave * (64 / L) + lane / L, 0) ^ (16 * (lane % L)));
+        const int v_at = not_kept(row_of<C, BN>(static_cast<int>(threadIdx.x >> 2), 0) ^ (16 * (lane & 3)));
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
             typedef typename Op16<QT>::x8 k8;
             char *at = reinterpret_cast<char *>(to.k) + i * W * 64 * 32;  // (64 rows or 16 on: the swizzle is the same)
             *reinterpret_cast<k8 *>(at + k_at) = codes_to<QT>(kr[i][0], kr[i][1]);
-            *reinterpret_cast<k8 *>(at + (k_at ^ 16)) = codes_to<QT>(kr[i][2], kr[i][3]);
+            *reinterpret_cast<k8 *>(at + (k_at ^ D)) = codes_to<QT>(kr[i][2], kr[i][3]);
             __builtin_amdgcn_sched_barrier(0);  // (or all codes are converted before the first are stored)
         }
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
             char *at = reinterpret_cast<char *>(to.v) + i * (NT / 4) * (2 * BN);
             *reinterpret_cast<f16x8 *>(at + v_at) = codes_to_f16(vr[i][0], vr[i][1]);
-            *reinterpret_cast<f16x8 *>(at + (v_at ^ 16)) = codes_to_f16(vr[i][2], vr[i][3]);
+            *reinterpret_cast<f16x8 *>(at + (v_at ^ BN)) = codes_to_f16(vr[i][2], vr[i][3]);
             __builtin_amdgcn_sched_barrier(0);
         }
         // (the product is finite, or it would make a NaN of a sum of zero)
@@ -342,7 +353,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
         x8 pf[1][2 * KT];
         if (!idle) {
             at_f32x16 s[KT];
-            const int k_row = not_kept(row_start<D>(token_of_row(col)) ^ (16 * half));
+            const int k_row = not_kept(row_of<C, D>(token_of_row(col), half));
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
 #pragma unroll
@@ -350,7 +361,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
                     typedef typename Op16<QT>::x8 k8;
-                    const k8 kf = *reinterpret_cast<const k8 *>(reinterpret_cast<const char *>(b.k) + (k_row ^ (32 * kk)) + 32 * k * (2 * D));
+                    const k8 kf = *reinterpret_cast<const k8 *>(reinterpret_cast<const char *>(b.k) + (k_row ^ (kPair<C> * kk)) + 32 * k * (2 * D));
                     s[k] = Op16<QT>::mfma32(kf, q.f[kk], s[k]);
                 }
             }
@@ -383,12 +394,12 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
             __syncthreads();
         }
         if (!idle) {
-            const int v_row = not_kept(row_start<BN>(col) ^ (16 * half));
+            const int v_row = not_kept(row_of<C, BN>(col, half));
 #pragma unroll
             for (int u = 0; u < 2 * KT; ++u)
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
-                    o[d] = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(reinterpret_cast<const char *>(b.v) + (v_row ^ (32 * u)) + 32 * d * (2 * BN)), pf[0][u], o[d]);
+                    o[d] = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(reinterpret_cast<const char *>(b.v) + (v_row ^ (kPair<C> * u)) + 32 * d * (2 * BN)), pf[0][u], o[d]);
         }
         if constexpr (I8)
             if (i + 1 < t.last) staging.store(step_key(t.c, i + 1), next);
@@ -485,11 +496,11 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
         if (!idle) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) s[0][j] = 0.0f;
-            const int k_row = not_kept(row_start<D>(32 * part + token_of_row(col)) ^ (16 * half));
+            const int k_row = not_kept(row_of<C, D>(32 * part + token_of_row(col), half));
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
                 typedef typename Op16<QT>::x8 k8;
-                s[0] = Op16<QT>::mfma32(*reinterpret_cast<const k8 *>(reinterpret_cast<const char *>(b.k) + (k_row ^ (32 * kk))), q.f[kk], s[0]);
+                s[0] = Op16<QT>::mfma32(*reinterpret_cast<const k8 *>(reinterpret_cast<const char *>(b.k) + (k_row ^ (kPair<C> * kk))), q.f[kk], s[0]);
             }
             __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
 #pragma unroll
@@ -537,7 +548,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
                 behind[1] = u1 - now;
             }
             // ---- O^T of dimensions 128 part ..
-            const int v_row = not_kept(row_start<BN>(128 * part + col) ^ (16 * half));
+            const int v_row = not_kept(row_of<C, BN>(128 * part + col, half));
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 x8 p = weights[pair][u][lane];
@@ -545,7 +556,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
                     if (__ballot(behind[u >> 1] != 0) != 0) p *= static_cast<T>(ldexpf(1.0f, behind[u >> 1]));
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
-                    o[d] = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(reinterpret_cast<const char *>(b.v) + (v_row ^ (32 * u)) + 32 * d * (2 * BN)), p, o[d]);
+                    o[d] = Op16<T>::mfma32(*reinterpret_cast<const x8 *>(reinterpret_cast<const char *>(b.v) + (v_row ^ (kPair<C> * u)) + 32 * d * (2 * BN)), p, o[d]);
             }
         }
         if constexpr (I8)

@@ -347,14 +347,18 @@ __device__ __forceinline__ int unit_of_steps(int unit, int e)
     return e > 125 || (e <= unit && e >= unit - 12) ? unit : e + 2;
 }
 
-// 8 int8 codes (two dwords) as bf16, exact.
+// 8 int8 codes (two dwords) as bf16, exact: bytes of code + 128 become fp32, of
+// which, less 128, the upper halves are bf16.
 __device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t a, uint32_t b)
 {
+    a ^= 0x80808080u;
+    b ^= 0x80808080u;
     at_u32x4 w;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t x = i < 2 ? a : b;
-        const float lo = static_cast<float>(static_cast<int8_t>(x >> (16 * (i & 1)))), hi = static_cast<float>(static_cast<int8_t>(x >> (16 * (i & 1) + 8)));
+        const float lo = static_cast<float>((x >> (16 * (i & 1))) & 0xffu) - 128.0f;
+        const float hi = static_cast<float>((x >> (16 * (i & 1) + 8)) & 0xffu) - 128.0f;
         w[i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
     }
     return __builtin_bit_cast(bf16x8, w);
