@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
     __shared__ float steps[I8 ? 4 * BN : 1];
     __shared__ int step_units[2];
     __shared__ SeenKeys seen_of[kChunkRows];  // (in registers it would be in the way of the inner steps)
+    __shared__ int lift_of[I8 ? kChunkRows : 1];
     __shared__ ChunkNotes notes;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -323,7 +324,9 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
     const float c = a.scale * kLog2e;
     const ChunkRow first_row = chunk_row(a, t, t.row0 + 32 * wave + col);
     seen_of[32 * wave + col] = first_row.seen;
-    const ChunkQuery<QT, D> q(a, t, first_row, half);
+    const ChunkQuery<QT, D, false, I8> q(a, t, first_row, half);
+    if constexpr (I8) lift_of[32 * wave + col] = q.lift;
+    const bool lifted = I8 && __ballot(q.lift != 0) != 0;
     if (threadIdx.x == 0) notes = {1 << 30, 0, 0};
 
     at_f32x16 o[DT];
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             }
             __builtin_amdgcn_sched_group_barrier(0x8, kAhead, 0);
-            w.raise(w.top(BORDER, s, HiddenKeys(seen, t, n0), n0, half, c, [&](int k, int j) { return b.ks[w.key(k, j, half)]; }), o, w.unit);
+            w.raise(w.top(BORDER, s, HiddenKeys(seen, t, n0), n0, half, c, [&](int k, int j) { return b.ks[w.key(k, j, half)]; }, lifted, [&] { return lift_of[32 * wave + col]; }), o, w.unit);
             if constexpr (I8) {
                 if constexpr (BORDER) asm volatile("" : "+v"(seen.lo), "+v"(seen.hi));  // (or the masks of 64 keys are kept)
                 w.products(BORDER, s, HiddenKeys(seen, t, n0), n0, half, [&](int k, int j) { return b.vs[w.key(k, j, half)]; }, *b.unit, pf, [&](float f) {
@@ -448,6 +451,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
     __shared__ float steps[I8 ? 4 * BN : 1];
     __shared__ int step_units[2];
     __shared__ SeenKeys seen_of[kChunkRows];
+    __shared__ int lift_of[I8 ? kChunkRows : 1];
     __shared__ ChunkNotes notes;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -464,7 +468,9 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
     const float c = a.scale * kLog2e;
     const ChunkRow first_row = chunk_row(a, t, t.row0 + 32 * pair + col);
     seen_of[32 * pair + col] = first_row.seen;
-    const ChunkQuery<QT, D> q(a, t, first_row, half);
+    const ChunkQuery<QT, D, false, I8> q(a, t, first_row, half);
+    if constexpr (I8) lift_of[32 * pair + col] = q.lift;
+    const bool lifted = I8 && __ballot(q.lift != 0) != 0;
     if (threadIdx.x == 0) notes = {1 << 30, 0, 0};
 
     at_f32x16 o[DT];  // dimensions 128 part + 32 i + ...
@@ -509,7 +515,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             }
             __builtin_amdgcn_sched_group_barrier(0x8, kAhead, 0);
-            top = w.top(BORDER, s, HiddenKeys(seen, t, n0), mine, half, c, [&](int, int j) { return b.ks[32 * part + w.key(0, j, half)]; });
+            top = w.top(BORDER, s, HiddenKeys(seen, t, n0), mine, half, c, [&](int, int j) { return b.ks[32 * part + w.key(0, j, half)]; }, lifted, [&] { return lift_of[32 * pair + col]; });
             if (half == 0) tops[pair][part][col] = top;
         }
         barrier_lds();

@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) k_attn_chunk
         if constexpr (I8) load_steps(a.v_steps, key_of(i), vsr);
         pages.find(key_of(min(i + W, n - 1)));
     }
-    const ChunkQuery<QT, D, I8> q(a, t, row, half);
+    const ChunkQuery<QT, D, I8, I8> q(a, t, row, half);
+    const bool lifted = I8 && __ballot(q.lift != 0) != 0;
     at_f32x16 o[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d)
@@ -121,11 +122,13 @@ __global__ void __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) k_attn_chunk
             s[0] = Op16<QT>::mfma32(kf, q.f[kk], s[0]);
         }
         if constexpr (I8) {
+            if (lifted) w.by_power(s, q.lift >> 1);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 const float k = ksr[j >> 2][j & 3];
                 s[0][j] *= k != k ? k : fminf(k * c, 3.4028235e38f);
             }
+            if (lifted) w.by_power(s, (q.lift + 1) >> 1);
         }
         if (more) {
             pages.use();
@@ -133,7 +136,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) k_attn_chunk
             if constexpr (I8) load_steps(a.k_steps, key_of(i + W), ksr);
         }
         const HiddenKeys hidden(row.seen, t, n0);
-        w.raise(w.top(border, s, hidden, n0, half, c, [](int, int) { return 1.0f; }), o, w.unit);
+        w.raise(w.top(border, s, hidden, n0, half, c, [](int, int) { return 1.0f; }, false, [] { return 0; }), o, w.unit);
         x8 pf[2][2];  // [term][16 keys]
         if constexpr (I8) {
             float most = 0.0f;

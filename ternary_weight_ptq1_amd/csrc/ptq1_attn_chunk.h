@@ -422,15 +422,42 @@ __device__ __forceinline__ bool sees_bad_page(const ChunkArgs &a, const ChunkTil
 // One lane's row as the products' B operand, k = 16 kk + 8 half + j (RUN16: 32
 // (kk / 2) + 16 half + 8 (kk % 2) + j, the order of 16 int8 codes that a lane
 // loads at once).
-template <typename QT, int D, bool RUN16 = false>
+//
+// int8 caches (LIFT): a score is the sum of query times code, times the key's
+// step.  bf16 queries below 2^-80 or above 2^80, whose sums could leave fp32's
+// range though the scores would not, enter divided by 2^lift, which brings the
+// row's largest to about one.
+template <typename QT, int D, bool RUN16 = false, bool LIFT = false>
 struct ChunkQuery {
     typename Op16<QT>::x8 f[D / 16];
+    int lift = 0;
     __device__ __forceinline__ ChunkQuery(const ChunkArgs &a, const ChunkTile &t, const ChunkRow &row, int half)
     {
         const QT *qp = static_cast<const QT *>(a.q) + (static_cast<int64_t>(t.q0) + row.tok) * a.qs + static_cast<int64_t>(row.head) * D;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
             f[kk] = *reinterpret_cast<const typename Op16<QT>::x8 *>(qp + (RUN16 ? 32 * (kk >> 1) + 16 * half + 8 * (kk & 1) : 16 * kk + 8 * half));
+        if constexpr (LIFT && std::is_same<QT, __bf16>::value) {
+            typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+            u16x2 most = {0, 0};
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t x = __builtin_bit_cast(at_u32x4, f[kk])[j] & 0x7fff7fffu;
+                    most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, x));
+                }
+            const float top = lane_pair_max<32>(__builtin_bit_cast(float, static_cast<uint32_t>(most[0] > most[1] ? most[0] : most[1]) << 16));
+            const int e = static_cast<int>(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
+            const bool far = (top > 0.0f) & (e < 128) & ((e > 80) | (e < -80));
+            lift = far ? e : 0;
+            if (__ballot(far) != 0) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[kk][j] = static_cast<QT>(ldexpf(static_cast<float>(f[kk][j]), -lift));
+            }
+        }
     }
 };
 
@@ -478,12 +505,22 @@ struct ChunkSoftmax {
         return RUN16 ? 32 * t + 16 * half + j : 32 * t + 16 * (j >> 3) + 8 * half + (j & 7);
     }
 
+    static __device__ __forceinline__ void by_power(at_f32x16 (&s)[KT], int e)
+    {
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s[t][j] = ldexpf(s[t][j], e);
+    }
+
     // the largest score of the lane's pair; on the border hidden ones leave the
-    // scores (int8 caches: ks(t, j) is the step of score register j of tile t)
-    template <class S>
-    __device__ __forceinline__ float top(bool border, at_f32x16 (&s)[KT], const HiddenKeys &hidden, int n0, int half, float c, S ks)
+    // scores (int8 caches: ks(t, j) is the step of score register j of tile t;
+    // lifted: of some row the queries are, lift() is the lane's)
+    template <class S, class L>
+    __device__ __forceinline__ float top(bool border, at_f32x16 (&s)[KT], const HiddenKeys &hidden, int n0, int half, float c, S ks, bool lifted, L lift)
     {
         if constexpr (I8) {
+            if (lifted) by_power(s, lift() >> 1);
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -491,6 +528,7 @@ struct ChunkSoftmax {
                     s[t][j] *= ks(t, j);
                     if (!RUN16 && (j & 7) == 7) __builtin_amdgcn_sched_barrier(0);  // (or all steps are read up front)
                 }
+            if (lifted) by_power(s, (lift() + 1) >> 1);
         }
         if (border) {
             if (hidden.gap) {

@@ -13,8 +13,9 @@ import pytest
 import torch
 
 import ternary_weight_ptq1_amd as P
-from test_attention import (BF16, DEV, F16, F32, I8, PAIRS, U, WEIGHT_TERM, attention_bounds, cache_values, check_rows,
-                            cumulated, filled_cache, gen, half_step, randn, rope_table, sequence, tables)
+from test_attention import (BF16, DEV, F16, F32, I8, PAIRS, U, WEIGHT_TERM, attention_bounds, busy, cache_values, check_rows,
+                            cumulated, filled_cache, gen, half_step, largest_values, ramp_sequence, randn, rope_table,
+                            sequence, tables, winners)
 
 pytestmark = pytest.mark.gpu
 NORM = 10 * U
@@ -166,7 +167,8 @@ def gathered(c, values, table, b, n):
     return x.transpose(0, 1).reshape(c.n_kv_heads, -1, c.head_dim)[:, :n]
 
 
-def check_attention(q, c, table, new, lens, got, term, window=0, sinks=0, scale=None, at=0):
+def check_attention(q, c, table, new, lens, got, term, window=0, sinks=0, scale=None, at=0, floor=0.0):
+    """floor: what a weight (int8: weight times step) may be off by beside its term, of the row's largest one."""
     hq, d = q.shape[1:]
     group = hq // c.n_kv_heads
     scale = d ** -0.5 if scale is None else scale
@@ -182,6 +184,11 @@ def check_attention(q, c, table, new, lens, got, term, window=0, sinks=0, scale=
                 rows = slice(h * group, (h + 1) * group)
                 qq = q[at + none:at + m, rows].double().reshape(-1, d)
                 want, tol = attention_bounds(qq, k[h], v[h], scale, term, mask.repeat_interleave(group, 0))
+                if floor:
+                    weights = torch.softmax((scale * (qq @ k[h].T.contiguous())).masked_fill(~mask.repeat_interleave(group, 0), -math.inf), 1)
+                    places = table[b, torch.arange(n, device=DEV) // c.page_size].long(), torch.arange(n, device=DEV) % c.page_size
+                    step = c.v_steps[places[0], h, places[1]].double() if c.dtype == I8 else torch.ones(n, dtype=torch.float64, device=DEV)
+                    tol = tol + floor * (weights * step).amax(1, keepdim=True) * (v[h].abs() / step[:, None]).sum(0)
                 tol = tol + half_step(want.abs() + tol, q.dtype)
                 err = (got[at + none:at + m, rows].double().reshape(-1, d) - want).abs()
                 assert bool((err <= tol).all()), f"b={b} h={h}: {(err / tol).nan_to_num(9e9).max().item():.3f} of the bound"
@@ -377,3 +384,343 @@ def test_attn_chunk_refused_sequences(hq, d, ctype):
     short = P.ptq1_attn_chunk(q[:at[5] + 4], c, table, cu, sl, max_len=79, window=20)
     assert bool(short[at[5]:].isnan().all()) and bool(short[at[3]:at[4]].isnan().all())
     check_attention(q, c, table[1:2], [6], [60], short, CHUNK_TERM[(BF16, ctype)], 20, at=at[1])
+
+
+# Where no sequence may have more than 32 rows of a kv head, a weight enters as two 16-bit terms: what the first leaves,
+# half a step of it at most, is rounded once more, by half a step of a value that is at most that (bf16: 2^-8 of a weight
+# leaves 2^-17, fp16: 2^-11 leaves 2^-23; int8: a weight times its step in fp32 first, 2^-24, and the step's unit is exact).
+FEW_TERM = {(BF16, BF16): 2.0 ** -17, (F16, F16): 2.0 ** -23, (BF16, I8): 2.0 ** -22, (F16, I8): 2.0 ** -22}
+
+
+@pytest.mark.parametrize("qt,ctype", CHUNK_PAIRS)
+@pytest.mark.parametrize("hq,hkv,d,page,new,lens,window,sinks", [
+    (1, 1, 64, 16, [32, 1, 0, 7], [40, 1, 9, 700], 0, 0),
+    (32, 1, 128, 64, [1, 1], [2, 333], 0, 0),
+    (6, 2, 256, 32, [10, 3], [200, 1000], 0, 0),
+    (15, 3, 128, 16, [6, 4, 6], [6, 3, 300], 0, 0),       # more queries than tokens
+    (8, 2, 128, 16, [8, 3, 1], [300, 5000, 65], 60, 5),
+    (4, 4, 64, 256, [9, 30], [5000, 31], 1000, 300),
+    (5, 1, 256, 64, [5], [7000], 0, 0),
+])
+def test_attn_chunk_few_rows(qt, ctype, hq, hkv, d, page, new, lens, window, sinks):
+    assert max(new) * hq // hkv <= 32
+    s = chunk_state(hq + sum(lens), new, lens, hq, hkv, d, page, qt, ctype, window, sinks)
+    got = P.ptq1_attn_chunk(*s, window=window, sinks=sinks, max_q=max(new))
+    check_attention(*s[:3], new, lens, got, FEW_TERM[(qt, ctype)], window, sinks)
+
+
+def chunk_term(qt, ctype, rows):
+    return (FEW_TERM if rows <= 32 else CHUNK_TERM)[(qt, ctype)]
+
+
+def set_token(c, table, b, j, k=None, v=None, heads=slice(None)):
+    """Token j of sequence b: K's dimension 1 and V's dimension 3 (int8 caches: their steps) become k and v."""
+    at, off = table[b, j // c.page_size].long(), j % c.page_size
+    for x, pages, steps in ((k, c.k_pages, c.k_steps), (v, c.v_pages, c.v_steps)):
+        if x is None:
+            continue
+        if steps is not None:
+            steps[at, heads, off] = x
+        elif pages is c.k_pages:
+            pages[at, heads, off, 1] = x
+        else:
+            pages[at, heads, 3, off] = x
+
+
+@pytest.mark.parametrize("qt,ctype", CHUNK_PAIRS)
+@pytest.mark.parametrize("hq,hkv,d,page,new,lens,window,sinks", [
+    (4, 2, 64, 16, [16, 5], [90, 33], 0, 0),
+    (8, 2, 128, 16, [8, 6], [700, 30], 100, 4),
+    (4, 2, 256, 64, [12, 7], [300, 65], 20, 0),
+    (4, 1, 128, 64, [8], [9000], 0, 0),
+    (4, 2, 64, 32, [150, 7], [400, 7], 0, 0),
+    (4, 2, 128, 16, [100, 9], [300, 200], 64, 3),
+    (2, 1, 256, 32, [80], [200], 0, 0),
+    (2, 1, 256, 16, [90, 30], [900, 70], 100, 17),
+    (2, 1, 64, 64, [130], [9000], 0, 0),
+    (2, 1, 128, 64, [70], [8000], 5000, 0),
+])
+def test_attn_chunk_non_finite(qt, ctype, hq, hkv, d, page, new, lens, window, sinks):
+    """NaN and infinities in keys and values: the entries that they enter are not finite, all others are
+    the rows without them.  Only kv head 0 holds them."""
+    state = chunk_state(sum(new) + d, new, lens, hq, hkv, d, page, qt, ctype, window, sinks)
+    q, c, table, cu, sl = state
+    args = dict(window=window, sinks=sinks, max_q=max(new))
+    group = hq // hkv
+    tensors = [t for t in (c.k_pages, c.v_pages, c.k_steps, c.v_steps) if t is not None]
+    before = [t.clone() for t in tensors]
+    clean = P.ptq1_attn_chunk(*state, **args)
+    term = chunk_term(qt, ctype, max(new) * group)
+    check_attention(q, c, table, new, lens, clean, term, window, sinks)
+    odd = torch.zeros(clean.shape, dtype=torch.bool, device=DEV)       # what must not be finite
+    either = torch.zeros(clean.shape, dtype=torch.bool, device=DEV)    # an infinite key's rows: a weight of zero, or NaN
+    at = 0
+    for b, (m, n) in enumerate(zip(new, lens)):
+        mask = window_mask(m, n, window, sinks)
+        places = [(n - 1, None, math.inf), (n - 1 - m // 2, None, math.nan), (n - 2, math.inf, None)]
+        if window:   # seen by the first queries alone
+            places += [(j, math.nan, None) for j in (n - m - window + m // 3 + 1,) if j >= sinks]
+        else:
+            places += [(n - 1 - m // 3, math.nan, None)]
+        if d == 256:  # several in one step, and two kinds in one token
+            places += [(n - 1 - m // 2, math.nan, None), (n - 3, None, -math.inf)]
+        for j, k, v in places:
+            set_token(c, table, b, j, k, v, slice(0, 1))
+            rows = mask[:, j]
+            if k is not None:
+                (odd if math.isnan(k) else either)[at:at + m, :group] |= rows[:, None, None]
+            else:
+                odd[at:at + m, :group, (slice(None) if ctype == I8 else slice(3, 4))] |= rows[:, None, None]
+        at += m
+    got = P.ptq1_attn_chunk(*state, **args)
+    odd &= ~either
+    assert bool(odd.any()) and bool((~odd & ~either).any())
+    assert not bool(got[odd].isfinite().any())
+    rest = ~odd & ~either
+    assert bool(got[rest].isfinite().all())
+    # (not the same bits: a row's reference may move because its neighbour's does)
+    for t, was in zip(tensors, before):
+        t.copy_(was)
+    check_attention(q, c, table, new, lens, torch.where(rest, got, clean), term, window, sinks)
+
+
+@pytest.mark.parametrize("qt,ctype", CHUNK_PAIRS)
+def test_attn_chunk_non_finite_queries(qt, ctype):
+    """A NaN takes its own row; beside it rows of the same tile stay."""
+    for new, lens in (([6], [100]), ([70], [300])):
+        state = chunk_state(77, new, lens, 4, 2, 128, 32, qt, ctype)
+        clean = P.ptq1_attn_chunk(*state, max_q=new[0])
+        state[0][3, 1, 5] = math.nan
+        state[0][4, 2, 6] = math.inf
+        got = P.ptq1_attn_chunk(*state, max_q=new[0])
+        assert bool(got[3, 1].isnan().all()) and not bool(got[4, 2].isfinite().all())
+        got[3, 1], got[4, 2] = clean[3, 1], clean[4, 2]
+        assert torch.equal(got, clean)
+
+
+def placed(k, v, page, ctype, steps=None):
+    """A cache whose pages hold k and v [n, heads, d] (int8: codes, with steps), in order, and its block table."""
+    n, h, d = k.shape
+    pages = -(-n // page)
+    c = P.ptq1_kv_cache(pages, page, h, d, ctype, DEV)
+    pad = torch.zeros((pages * page - n, h, d), dtype=k.dtype, device=DEV)
+    kk, vv = (torch.cat([x, pad]).view(pages, page, h, d) for x in (k, v))
+    c.k_pages.copy_(kk.transpose(1, 2))
+    c.v_pages.copy_(vv.permute(0, 2, 3, 1))
+    if ctype == I8:
+        c.k_steps.fill_(steps), c.v_steps.fill_(steps)
+    return c, torch.arange(pages, dtype=torch.int32, device=DEV).view(1, pages)
+
+
+@pytest.mark.parametrize("qt,ctype", CHUNK_PAIRS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("m,n", [(150, 150), (3, 9000), (60, 4000)])
+@pytest.mark.parametrize("size", [1e4, 1e6, 1e8, 1e12])
+def test_attn_chunk_large_scores_pick_one(qt, ctype, d, m, n, size):
+    """Scores of 10^4 to 10^12 and above: a softmax that picks one token, and no NaN or infinity on the way."""
+    q, c, table, cu, sl = chunk_state(n + d, [m], [n], 4, 2, d, 64, qt, ctype)
+    some = min(size, 1e3)
+    q, scale = (q.float() * some).to(qt), d ** -0.5 * size / some
+    got = P.ptq1_attn_chunk(q, c, table, cu, sl, scale=scale, max_q=m).double()
+    kc, vc = cache_values(c)
+    k, v = sequence(c, kc, table, 0, n), sequence(c, vc, table, 0, n)
+    assert bool((got.abs() <= v.abs().max() * 1.01).all())
+    counted = 0
+    for h in range(4):
+        want, ok = winners(q[:, h].double(), k[h // 2], v[h // 2], scale, window_mask(m, n, 0, 0))
+        counted += int(ok.sum())
+        # one weight, rounded to the products' type (int8: times its step), over the sum of the rounded ones (int8: of
+        # the unrounded ones)
+        tol = half_step(want, qt) + chunk_term(qt, ctype, 2 * m) * want.abs() + 4 * U * want.abs()
+        assert bool(((got[:, h] - want).abs()[ok] <= tol[ok]).all())
+    assert counted >= 4
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("power", [20, 23, 24, 25, 31])
+def test_attn_chunk_scores_around_powers_of_two(dtype, d, power):
+    """Exact scores that grow along the keys across a power of two (or minus it), where the size of the last place
+    changes: a row's mean stays within its values."""
+    g = gen(172 + power)
+    n = 200
+    v = randn(g, n, 2, d).to(dtype)
+    for sign in (1, -1):
+        q = torch.zeros((40, 2, d), device=DEV, dtype=dtype)
+        k = torch.zeros((n, 2, d), device=DEV, dtype=dtype)
+        half = 2.0 ** min(power // 2, 10)
+        q[..., 0], q[..., 1] = half, 1
+        k[..., 0] = sign * 2.0 ** min(power - math.log2(half), 15)
+        k[..., 1] = torch.arange(-n // 2, n // 2, device=DEV)[:, None] % 64 - 32 + torch.arange(n, device=DEV)[:, None] // 40 * 8
+        scale = math.log(2.0) * 2.0 ** (power - math.log2(half) - min(power - math.log2(half), 15))
+        c, table = placed(k, v, 64, dtype)
+        sl = torch.tensor([n], dtype=torch.int32, device=DEV)
+        for m in (1, 3, 40):
+            got = P.ptq1_attn_chunk(q[:m], c, table, cumulated([m]), sl, scale=scale, max_q=m).double()
+            assert bool(got.isfinite().all()) and bool((got.abs() <= 1.02 * v.abs().amax(0).double()).all())
+
+
+@pytest.mark.parametrize("qt,ctype", CHUNK_PAIRS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["first", "last", "up", "down"])
+@pytest.mark.parametrize("m", [3, 300])
+def test_attn_chunk_many_small_weights(qt, ctype, d, kind, m):
+    """A token that takes nearly the whole weight and has no value, beside thousands that have.  fp16 terms end at
+    2^-24 of a unit of which the largest weight has 2^7 at least (an error of 2^-32 of it), over int8 caches of which the
+    largest weight times step has 2^2 at least (2^-27).  The queries' own tokens weigh nothing."""
+    g = gen(91)
+    n, h = 2700, 4
+    s = torch.cat([ramp_sequence(kind, n), torch.full((m,), -100.0, dtype=torch.float64, device=DEV)])
+    q = torch.zeros((m, h, d), device=DEV, dtype=qt)
+    q[:, :, 0] = 1
+    k = torch.zeros((n + m, h, d), device=DEV, dtype=F32)
+    v = randn(g, n + m, h, d) + 2
+    k[:, :, 0] = s[:, None].float()
+    if ctype == I8:
+        k, v = (k * 2).round().clamp(-127, 127), (v * 20).round().clamp(-127, 127)
+    k, v = k.to(ctype), v.to(ctype)
+    if kind in ("first", "last"):
+        v[0 if kind == "first" else n - 1] = 0
+    c, table = placed(k, v, 64, ctype, 0.5)
+    scale = math.log(2.0)
+    got = P.ptq1_attn_chunk(q, c, table, cumulated([m]), torch.tensor([n + m], dtype=torch.int32, device=DEV), scale=scale, max_q=m)
+    step = 0.5 if ctype == I8 else 1.0
+    mask = window_mask(m, n + m, 0, 0)
+    for i in (0, h - 1):
+        qq, kk, vv = q[:, i].double(), k[:, i].double() * step, v[:, i].double() * step
+        want, tol = attention_bounds(qq, kk, vv, scale, chunk_term(qt, ctype, m), mask)
+        if ctype != BF16:
+            p = torch.softmax((scale * (qq @ kk.T.contiguous())).masked_fill(~mask, -math.inf), 1)
+            tol = tol + (2.0 ** -27 if ctype == I8 else 2.0 ** -32) * p.amax(1, keepdim=True) * vv.abs().sum(0)
+        tol = tol + half_step(want.abs() + tol, qt)
+        err = (got[:, i].double() - want).abs()
+        assert bool((err <= tol).all()), f"{(err / tol).max().item():.3f} of the bound"
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("m", [3, 300])
+def test_attn_chunk_rounded_weights_make_up_one(dtype, d, m):
+    """As for prompts: 500 weights that are rounded by 0.45 of a step, over one value that leaves half a step of room."""
+    n, step = 564, torch.finfo(dtype).eps
+    q = torch.zeros((m, 2, d), device=DEV, dtype=dtype)
+    k, v = (torch.zeros((n + m, 2, d), device=DEV, dtype=dtype) for _ in range(2))
+    q[..., 0], q[..., 1] = 1, 1
+    k[1:64, :, 0], k[n:, :, 0] = -100, -100
+    k[64:n, :, 0], k[64:n, :, 1] = 5, math.log2(1 + 0.45 * step)
+    v[64:n] = 1.98
+    c, table = placed(k, v, 32, dtype)
+    got = P.ptq1_attn_chunk(q, c, table, cumulated([m]), torch.tensor([n + m], dtype=torch.int32, device=DEV), scale=math.log(2.0),
+                            max_q=m)
+    w = torch.exp(math.log(2.0) * (q[0, 0].double() @ k[:, 0].double().T.contiguous()))
+    exact = (w / w.sum()) @ v[:, 0].double()
+    assert bool((exact - exact.to(dtype).double()).abs().max() < 0.4 * step)    # (far from a border of the rounding)
+    assert torch.equal(got, exact.to(dtype).expand(m, 2, d))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("m", [2, 300])
+@pytest.mark.parametrize("below", [22, 26, 30])
+def test_attn_chunk_small_weights_count_in_the_sum(dtype, m, below):
+    """One key of score 0 and value 0, then 65536 of weight 2^-22 to 2^-30 and one value (exact down to 2^-31 of the
+    largest in fp16); the queries' own tokens weigh nothing (2^-120)."""
+    n, d = 65537, 64
+    q = torch.zeros((m, 2, d), device=DEV, dtype=dtype)
+    k, v = (torch.zeros((n + m, 2, d), device=DEV, dtype=dtype) for _ in range(2))
+    q[..., 0], k[1:n, :, 0], v[1:n], k[n:, :, 0] = 1, -below, 1000, -120
+    c, table = placed(k, v, 256, dtype)
+    got = P.ptq1_attn_chunk(q, c, table, cumulated([m]), torch.tensor([n + m], dtype=torch.int32, device=DEV), scale=math.log(2.0),
+                            max_q=m).double()
+    total = 65536 * 2.0 ** -below
+    want = torch.tensor(1000 * total / (1 + total), dtype=torch.float64)
+    tol = want * (below * 2.0 ** -22 + 65536 * U)
+    assert bool(((got - want).abs() <= tol + half_step(want + tol, dtype)).all()), (got.flatten()[0].item(), want.item())
+
+
+@pytest.mark.parametrize("qt,size,step,scale", [
+    (BF16, 2.0 ** -121, 2.0 ** 121, 0.125),
+    (BF16, 2.0 ** -60, 2.0 ** 121, 2.0 ** -60),
+    (BF16, 2.0 ** -20, 2.0 ** 121, 2.0 ** -100),
+    (BF16, 2.0 ** 90, 2.0 ** -90, 0.1),
+    (BF16, 2.0 ** 121, 2.0 ** -110, 2.0 ** -11),
+    (BF16, 2.0 ** 121, 2.0 ** -100, 2.0 ** -21),
+    (BF16, 2.0 ** 100, 2.0 ** -45, 2.0 ** -57),
+    (BF16, 2.0 ** -115, 2.0 ** -2, 2.0 ** 116),
+    (F16, 2.0 ** 8, 2.0 ** 110, 2.0 ** -118),
+    (F16, 2.0 ** -8, 2.0 ** -100, 2.0 ** 108),
+])
+@pytest.mark.parametrize("new,lens", [([5, 3], [300, 70]), ([70, 40], [300, 70])])
+@pytest.mark.parametrize("d", [128, 256])
+def test_attn_chunk_large_and_small_steps(qt, size, step, scale, new, lens, d):
+    """int8 keys of any step, with queries and scales that make ordinary scores of them: no product on the way leaves
+    fp32's range.  (scale times step is a normal number.)  Some rows are nearly one token's, whose code may be zero: beside
+    its term a weight times step is off by 2^-27 of the row's largest, as in test_attn_chunk_many_small_weights."""
+    g = gen(110)
+    table, pages = tables(g, lens, 32)
+    c = filled_cache(g, pages, 32, 2, d, I8)
+    c.k_steps.mul_(50).clamp_(0.5, 1.0).mul_(step / 127)
+    c.k_pages[table[1, 1].item(), :, 3] = 0
+    q = (randn(g, sum(new), 8, d) * size).to(qt)
+    got = P.ptq1_attn_chunk(q, c, table, cumulated(new), torch.tensor(lens, dtype=torch.int32, device=DEV), scale=scale,
+                            max_q=max(new))
+    check_attention(q, c, table, new, lens, got, chunk_term(qt, I8, 4 * max(new)), scale=scale, floor=2.0 ** -27)
+
+
+@pytest.mark.parametrize("step", [2.0 ** 121, 2.0 ** 60, 2.0 ** -60, 2.0 ** -110])
+@pytest.mark.parametrize("new,lens", [([5, 3], [300, 70]), ([70, 40], [300, 70]), ([2, 1], [9000, 70])])
+@pytest.mark.parametrize("d", [128, 256])
+def test_attn_chunk_large_and_small_value_steps(step, new, lens, d):
+    """int8 values of any step, ordinary keys; one token's step is 2^10 times smaller than the others'."""
+    g = gen(113)
+    table, pages = tables(g, lens, 32)
+    c = filled_cache(g, pages, 32, 2, d, I8)
+    c.v_pages.copy_((c.v_pages.float() / 2).round())   # (the largest step's results stay below 2^128)
+    c.v_steps.mul_(50).clamp_(0.5, 1.0).mul_(step)
+    c.v_steps[table[0, 2].item(), :, 5] *= 2.0 ** -10
+    q = randn(g, sum(new), 8, d).to(BF16)
+    got = P.ptq1_attn_chunk(q, c, table, cumulated(new), torch.tensor(lens, dtype=torch.int32, device=DEV), max_q=max(new))
+    check_attention(q, c, table, new, lens, got, chunk_term(BF16, I8, 4 * max(new)), floor=2.0 ** -27)
+
+
+@pytest.mark.parametrize("qt", [BF16, F16])
+@pytest.mark.parametrize("m", [3, 100])
+def test_attn_chunk_unlike_value_steps(qt, m):
+    """Values whose steps differ by 2^40 between tokens, the large ones first, last, or in one page: every row keeps
+    the resolution that its own largest product allows (2^-27 of it, beside the terms')."""
+    g = gen(114)
+    n = 500
+    for kind in ("first", "last", "page"):
+        table, pages = tables(g, [n], 32)
+        c = filled_cache(g, pages, 32, 2, 128, I8)
+        rows = table[0].long()
+        c.v_steps[rows if kind != "page" else rows[5]] *= 2.0 ** 20
+        c.v_steps[rows[1:] if kind == "first" else rows[:-1] if kind == "last" else rows[6]] *= 2.0 ** -40
+        q = randn(g, m, 4, 128).to(qt)
+        got = P.ptq1_attn_chunk(q, c, table, cumulated([m]), torch.tensor([n], dtype=torch.int32, device=DEV), max_q=m)
+        kc, vc = cache_values(c)
+        mask = window_mask(m, n, 0, 0)
+        for h in range(4):
+            k, v = sequence(c, kc, table, 0, n)[h // 2], sequence(c, vc, table, 0, n)[h // 2]
+            want, tol = attention_bounds(q[:, h].double(), k, v, 128 ** -0.5, chunk_term(qt, I8, 2 * m), mask)
+            p = torch.softmax((128 ** -0.5 * (q[:, h].double() @ k.T.contiguous())).masked_fill(~mask, -math.inf), 1)
+            step = c.v_steps[rows[torch.arange(n, device=DEV) // 32], h // 2, torch.arange(n, device=DEV) % 32].double()
+            floor = 2.0 ** -27 * (p * step).amax(1, keepdim=True) * (v / step[:, None]).abs().sum(0)
+            tol = tol + floor
+            if qt == F16:  # (results past fp16 are infinite)
+                tol = torch.where(want.abs() > 6e4, math.inf, tol)
+            tol = tol + half_step(want.abs() + tol, qt)
+            err = (got[:, h].double() - want).abs()
+            assert bool(((err <= tol) | (tol == math.inf)).all()), f"{kind} {(err / tol).nan_to_num(9e9).max().item():.3f} of the bound"
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new,lens", [([300], [300]), ([3, 2], [9000, 700]), ([60, 9], [9000, 700])])
+def test_attn_chunk_largest_values(d, new, lens):
+    """bf16 values whose mean is in fp32's range and whose sum is not."""
+    g = gen(121)
+    table, pages = tables(g, lens, 32)
+    c = filled_cache(g, pages, 32, 2, d, BF16)
+    c.v_pages.copy_(largest_values(g, *c.v_pages.shape))
+    q = randn(g, sum(new), 4, d).to(BF16)
+    got = P.ptq1_attn_chunk(q, c, table, cumulated(new), torch.tensor(lens, dtype=torch.int32, device=DEV), max_q=max(new))
+    check_attention(q, c, table, new, lens, got, chunk_term(BF16, BF16, 2 * max(new)))
