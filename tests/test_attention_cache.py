@@ -724,3 +724,280 @@ def test_attn_chunk_largest_values(d, new, lens):
     q = randn(g, sum(new), 4, d).to(BF16)
     got = P.ptq1_attn_chunk(q, c, table, cumulated(new), torch.tensor(lens, dtype=torch.int32, device=DEV), max_q=max(new))
     check_attention(q, c, table, new, lens, got, chunk_term(BF16, BF16, 2 * max(new)))
+
+
+# ------------------------------------------------- together, as a layer has them ----
+
+def positions_of(new, lens):
+    return torch.cat([torch.arange(n - m, n, device=DEV) for m, n in zip(new, lens)])
+
+
+def slots_of(table, new, lens, page):
+    seq = torch.repeat_interleave(torch.arange(len(new), device=DEV), torch.tensor(new, device=DEV))
+    pos = positions_of(new, lens)
+    return table[seq, pos // page].long() * page + pos % page
+
+
+@pytest.mark.parametrize("qt,ctype", CHUNK_PAIRS)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 4)])
+def test_layer_half_by_chunks_then_tokens(qt, ctype, window, sinks):
+    """Prompts that arrive in chunks of unlike lengths (normed, rotated, written, attended), then single tokens: at
+    every step the plain layer over everything so far, and what the chunk call and the single tokens' call give for
+    the same token agree."""
+    g = gen(200)
+    hq, hkv, d, page = 8, 2, 128, 32
+    total = [410, 131]
+    table, pages = tables(g, total, page)
+    c = P.ptq1_kv_cache(pages, page, hkv, d, ctype, DEV)
+    rope = rope_table(512, d)
+    q_gain, k_gain = 1 + 0.2 * randn(g, d), 1 + 0.2 * randn(g, d)
+    lens = [0, 0]
+    for new in ([200, 3], [1, 64], [64, 1], [140, 60], [4, 2], [1, 1]):
+        lens = [a + b for a, b in zip(lens, new)]
+        n = sum(new)
+        x = randn(g, n, hq + 2 * hkv, d).to(qt)
+        pos = positions_of(new, lens).int()
+        q = P.ptq1_kv_write_norm(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], slots_of(table, new, lens, page), c,
+                                 q_gain=q_gain, k_gain=k_gain, positions=pos, cos_sin=rope, q_dtype=qt)
+        check_rows(q, *turned_norm(x[:, :hq], q_gain, 1e-6, pos, rope), qt)
+        sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        got = P.ptq1_attn_chunk(q, c, table, cumulated(new), sl, window=window, sinks=sinks)
+        check_attention(q, c, table, new, lens, got, CHUNK_TERM[(qt, ctype)], window, sinks, floor=2.0 ** -27)
+        # the last tokens, once more as single ones
+        last = torch.tensor(new, device=DEV).cumsum(0) - 1
+        one = (P.ptq1_attn_decode_window(q[last], c, table, sl, window, sinks) if window else
+               P.ptq1_attn_decode(q[last], c, table, sl))
+        check_attention(q[last], c, table, [1, 1], lens, one, WEIGHT_TERM[(qt, ctype)], window, sinks)
+        check_attention(q[last], c, table, [1, 1], lens, got[last], CHUNK_TERM[(qt, ctype)], window, sinks, floor=2.0 ** -27)
+    assert lens == total
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_chunks_and_whole_prompts_agree(dtype):
+    """A chunk that is a whole prompt, and one behind a context, against the prompt call on the rows read back."""
+    g = gen(201)
+    new, lens = [300, 90], [300, 700]
+    table, pages = tables(g, lens, 64)
+    c = filled_cache(g, pages, 64, 2, 128, dtype)
+    q = randn(g, sum(new), 8, 128).to(dtype)
+    cu, cu_k = cumulated(new), cumulated(lens)
+    k, v = P.ptq1_kv_read(c, table, cu_k, sum(lens), dtype=dtype)
+    got = P.ptq1_attn_chunk(q, c, table, cu, torch.tensor(lens, dtype=torch.int32, device=DEV))
+    want = P.ptq1_attn_prompt(q, k, v, cu, cu_k)
+    # (both round: twice the bound on either is two terms of the values' mean magnitude and two results)
+    tol = 2 * CHUNK_TERM[(dtype, dtype)] * 4 + 2 * half_step(want.double(), dtype)
+    assert bool(((got.double() - want.double()).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("ctype", [BF16, I8])
+def test_captured_chunk_step_replays_with_new_contents(ctype):
+    """Write with norms, chunk attention and windowed single tokens captured once and replayed with lengths, slots,
+    chunks and rows that the program puts into the same buffers, eager work in between; chunks shrink and grow, and a
+    sequence's chunk becomes empty."""
+    g = gen(202)
+    hq, hkv, d, page, width = 8, 2, 128, 32, 80
+    lens = [1500, 700]
+    table, pages = tables(g, [width * page] * 2, page)
+    c = filled_cache(g, pages, page, hkv, d, ctype)
+    rows = randn(g, 12, hq + 2 * hkv, d).to(BF16)
+    rope = rope_table(width * page, d)
+    slots = torch.zeros(12, dtype=torch.int64, device=DEV)
+    pos = torch.zeros(12, dtype=torch.int32, device=DEV)
+    cu, sl = cumulated([6, 6]), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    gain = 1 + 0.2 * randn(g, d)
+    sizes = dict(max_q=8, max_len=width * page)
+    need = P.workspace_bytes("attn_chunk", 2, 12, 8, hq, hkv, d, width * page, 1000, 4)
+    need_one = P.workspace_bytes("attn_decode_window", 2, hq, hkv, d, width * page, 600, 2)
+    assert need > 0
+    ws, ws_one = (torch.empty(n, dtype=torch.uint8, device=DEV) for n in (need, max(need_one, 16)))
+    q = torch.empty((12, hq, d), dtype=BF16, device=DEV)
+    out, one = torch.full_like(q, 7), torch.empty((2, hq, d), dtype=BF16, device=DEV)
+
+    def step():
+        P.ptq1_kv_write_norm(rows[:, :hq], rows[:, hq:hq + hkv], rows[:, hq + hkv:], slots, c, q_gain=gain, k_gain=gain,
+                             positions=pos, cos_sin=rope, out=q)
+        P.ptq1_attn_chunk(q, c, table, cu, sl, window=1000, sinks=4, out=out, ws=ws, **sizes)
+        P.ptq1_attn_decode_window(q[:2], c, table, sl, 600, 2, max_len=width * page, out=one, ws=ws_one)
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        step()
+    for new in ([6, 6], [4, 8], [8, 0], [1, 1], [7, 5]):
+        n = sum(new)
+        lens = [a + b for a, b in zip(lens, new)]
+        rows.copy_(randn(g, 12, hq + 2 * hkv, d))
+        slots.fill_(-1)
+        slots[:n] = slots_of(table, new, lens, page)
+        pos[:n] = positions_of(new, lens).int()
+        cu.copy_(cumulated(new))
+        sl.copy_(torch.tensor(lens, dtype=torch.int32))
+        out.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        first = out.clone(), one.clone(), q.clone()
+        step()
+        assert torch.equal(first[0], out) and torch.equal(first[1], one) and torch.equal(first[2], q)
+        check_attention(q[:n], c, table, new, lens, out, CHUNK_TERM[(BF16, ctype)], 1000, 4, floor=2.0 ** -27)
+        check_attention(q[:2], c, table, [1, 1], lens, one, WEIGHT_TERM[(BF16, ctype)], 600, 2)
+        assert bool((out[n:] == 7).all())
+
+
+def side_calls():
+    g = gen(203)
+    lens = [2100, 900]
+    table, pages = tables(g, lens, 32)
+    c = filled_cache(g, pages, 32, 2, 128, BF16)
+    q = randn(g, 100, 8, 128).to(BF16)
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    few, many = cumulated([5, 3]), cumulated([60, 40])
+    return [lambda **kw: P.ptq1_attn_chunk(q[:8], c, table, few, sl, max_q=5, **kw),
+            lambda **kw: P.ptq1_attn_chunk(q, c, table, many, sl, max_q=60, window=1500, sinks=3, **kw),
+            lambda **kw: P.ptq1_attn_decode_window(q[:2], c, table, sl, 1700, 3, **kw)]
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_window_and_chunk_calls_on_side_streams(which):
+    """On a stream of the caller's while its work is pending, beside pending work of the current one: scratch and
+    results are nobody else's."""
+    call = side_calls()[which]
+    want = call()
+    x = torch.full((4096, 4096), 1e-3, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            busy(x)
+        got = call(stream=side)
+        call(stream=side)                                                                      # dropped at once
+        taken = [torch.empty(1 << e, dtype=torch.uint8, device=DEV).fill_(255) for e in range(12, 21) for _ in range(3)]
+        busy(x)
+        torch.cuda.current_stream().synchronize()
+        side.synchronize()
+        assert torch.equal(got, want)
+        assert all(bool((t == 255).all()) for t in taken)
+
+
+def test_window_and_chunk_calls_on_two_streams():
+    """The same calls on two streams at once, with scratch of their own."""
+    calls = side_calls()
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(6):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append([call() for call in calls])
+    torch.cuda.synchronize()
+    for results in got:
+        assert all(torch.equal(a, b) for a, b in zip(results, want))
+
+
+@pytest.mark.parametrize("ctype", [BF16, I8])
+def test_new_calls_past_32_bit_offsets(ctype):
+    """Pages whose elements lie past 2^32: the write with norms, chunks of few and of many rows, windowed tokens."""
+    g = gen(204)
+    page, hkv, d, pages = 256, 8, 128, 16400
+    assert pages * page * hkv * d > 1 << 32
+    c = P.ptq1_kv_cache(pages, page, hkv, d, ctype, DEV)
+    table = torch.tensor([[16399, 3, 16397], [16398, 8200, 0]], dtype=torch.int32, device=DEV)
+    lens = [600, 515]
+    k, v = (randn(g, sum(lens), hkv, d).to(BF16) for _ in range(2))
+    P.ptq1_kv_write_norm(None, k, v, slots_of(table, lens, lens, page), c)
+    small = P.ptq1_kv_cache(6, page, hkv, d, ctype, DEV)     # the same pages, near its beginning
+    flat = table.flatten().long()
+    small.k_pages.copy_(c.k_pages[flat]), small.v_pages.copy_(c.v_pages[flat])
+    if ctype == I8:
+        small.k_steps.copy_(c.k_steps[flat]), small.v_steps.copy_(c.v_steps[flat])
+    near = torch.arange(6, dtype=torch.int32, device=DEV).view(2, 3)
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    y, e = turned_norm(k, None, 1e-6, None, None)
+    rows, _ = cache_values(small)
+    got = torch.cat([sequence(small, rows, near, b, n).transpose(0, 1) for b, n in enumerate(lens)])
+    check_rows(got, y, e, ctype)
+    for new in ([2, 1], [90, 40]):
+        q = randn(g, sum(new), 16, d).to(BF16)
+        far = P.ptq1_attn_chunk(q, c, table, cumulated(new), sl, max_q=max(new), window=400, sinks=3)
+        check_attention(q, small, near, new, lens, far, chunk_term(BF16, ctype, 2 * max(new)), 400, 3, floor=2.0 ** -27)
+    far = P.ptq1_attn_decode_window(q[:2], c, table, sl, 400, 3)
+    check_attention(q[:2], small, near, [1, 1], lens, far, WEIGHT_TERM[(BF16, ctype)], 400, 3)
+
+
+def test_attn_chunk_rows_far_apart():
+    """Query rows at the largest stride, their offsets past 2^32 bytes."""
+    g = gen(205)
+    n, stride = 200, 1 << 24
+    room = torch.empty((n, stride), dtype=BF16, device=DEV)
+    q = room.as_strided((n, 4, 128), (stride, 128, 1), 4096)
+    q.copy_(randn(g, *q.shape))
+    table, pages = tables(g, [n], 32)
+    c = filled_cache(g, pages, 32, 2, 128, BF16)
+    got = P.ptq1_attn_chunk(q, c, table, cumulated([n]), torch.tensor([n], dtype=torch.int32, device=DEV))
+    check_attention(q, c, table, [n], [n], got, CHUNK_TERM[(BF16, BF16)])
+
+
+def test_new_calls_with_nothing_to_do():
+    """No tokens, no sequences, no query rows; all lengths zero."""
+    c = filled_cache(gen(206), 4, 16, 2, 64, BF16)
+    none = torch.empty((0, 4, 64), dtype=BF16, device=DEV)
+    kv = torch.empty((0, 2, 64), dtype=BF16, device=DEV)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device=DEV)
+    assert P.ptq1_kv_write_norm(none, kv, kv, torch.empty(0, dtype=torch.int64, device=DEV), c, q_dtype=BF16).shape == none.shape
+    assert P.ptq1_attn_decode_window(none, c, i32(0, 4), i32(0), 5).shape == none.shape
+    assert P.ptq1_attn_chunk(none, c, i32(0, 4), i32(1), i32(0)).shape == none.shape
+    assert P.ptq1_attn_chunk(none, c, i32(2, 4), i32(3), torch.tensor([5, 0], dtype=torch.int32, device=DEV)).shape == none.shape
+    q = torch.ones((3, 4, 64), dtype=BF16, device=DEV)
+    assert bool((P.ptq1_attn_decode_window(q, c, i32(3, 4), i32(3), 5) == 0).all())
+    assert bool((P.ptq1_attn_chunk(q, c, i32(1, 4), cumulated([3]), i32(1)) == 0).all())
+    assert bool((P.ptq1_attn_chunk(q, c, i32(1, 4), cumulated([3]), i32(1), window=2, sinks=1) == 0).all())
+
+
+@pytest.mark.parametrize("qt,ctype", CHUNK_PAIRS)
+def test_window_and_chunk_share_pages(qt, ctype):
+    """Sequences that share the pages of a common beginning, one of them twice in the batch."""
+    g = gen(207)
+    table, pages = tables(g, [400], 32)
+    c = filled_cache(g, pages, 32, 2, 64, ctype)
+    table = table.expand(3, -1).contiguous()
+    new, lens = [7, 7, 40], [400, 400, 333]
+    q = randn(g, sum(new), 4, 64).to(qt)
+    q[7:14] = q[:7]
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    got = P.ptq1_attn_chunk(q, c, table, cumulated(new), sl, window=200, sinks=1)
+    check_attention(q, c, table, new, lens, got, CHUNK_TERM[(qt, ctype)], 200, 1)
+    assert torch.equal(got[:7], got[7:14])
+    one = P.ptq1_attn_decode_window(q[[0, 7, 20]], c, table, sl, 200, 1)
+    check_attention(q[[0, 7, 20]], c, table, [1] * 3, lens, one, WEIGHT_TERM[(qt, ctype)], 200, 1)
+    assert torch.equal(one[0], one[1])
+
+
+@pytest.mark.parametrize("qt,ctype", PAIRS)
+def test_attn_decode_window_non_finite(qt, ctype):
+    """NaN and infinities in tokens that are seen enter their heads' rows; those between the first tokens and the
+    window do not."""
+    g = gen(208)
+    lens, window, sinks = [700, 64], 90, 5
+    table, pages = tables(g, lens, 32)
+    c = filled_cache(g, pages, 32, 2, 128, ctype)
+    q = randn(g, 2, 8, 128).to(qt)
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    for j in (5, 300, 609):                          # beside the window and the first ones
+        set_token(c, table, 0, j, math.nan, math.inf)
+    got = P.ptq1_attn_decode_window(q, c, table, sl, window, sinks)
+    for t in (c.k_pages, c.v_pages, c.k_steps, c.v_steps):
+        if t is not None and t.dtype != torch.int8:
+            t.copy_(torch.where(t.isfinite(), t, 0))
+    check_attention(q, c, table, [1, 1], lens, got, WEIGHT_TERM[(qt, ctype)], window, sinks)
+    for j in (4, 610, 699):
+        was = [t.clone() for t in (c.k_pages, c.v_pages, c.k_steps, c.v_steps) if t is not None]
+        for k, v in ((math.nan, None), (None, math.nan), (None, math.inf)):
+            set_token(c, table, 0, j, k, v, slice(0, 1))
+            odd = P.ptq1_attn_decode_window(q, c, table, sl, window, sinks)
+            dims = slice(None) if k is not None or ctype == I8 else slice(3, 4)
+            assert not bool(odd[0, :4, dims].isfinite().any())
+            keep = torch.ones_like(odd, dtype=torch.bool)
+            keep[0, :4, dims] = False
+            assert torch.equal(odd[keep], got[keep])
+            for t, w in zip([t for t in (c.k_pages, c.v_pages, c.k_steps, c.v_steps) if t is not None], was):
+                t.copy_(w)
