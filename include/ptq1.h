@@ -455,9 +455,9 @@ ptq1_status ptq1_kv_write(const void *q, int64_t q_stride, const void *k, int64_
  *        ones.
  *   eps  2^-100 to 2^100.
  * Everything else as in ptq1_kv_write.  Finite rows of any magnitude are
- * normed (where the squares leave fp32's range, eps, which is then nothing
- * beside them, is left out).  A NaN in a head makes all of it NaN, an infinity
- * its own element NaN and the others, before the rotation, zero.
+ * normed, also where their squares leave fp32's range.  A NaN in a head makes
+ * all of it NaN, an infinity its own element NaN and the others, before the
+ * rotation, zero.
  * Errors: as ptq1_kv_write; SHAPE (eps). */
 ptq1_status ptq1_kv_write_norm(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                                int64_t v_stride, int32_t src_dtype, int64_t n_tokens, int32_t n_q_heads,

@@ -185,9 +185,9 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_write(KvWriteArgs a)
                 float f = 1.0f, a_row = __builtin_amdgcn_rsqf(sum * (1.0f / D) + a.eps);
                 if (!(sum <= 3.4028235e38f) && group_absmax<LPR>(absmax4(x[u])) <= 3.4028235e38f) {
                     // finite values whose squares are not: from 2^60 on, so that
-                    // 2^-70 of them has ordinary squares, beside which eps is nothing
+                    // 2^-70 of them has ordinary squares
                     f = 0x1p-70f;
-                    a_row = __builtin_amdgcn_rsqf(group_sum<LPR>(squares4(x[u] * f)) * (1.0f / D));
+                    a_row = __builtin_amdgcn_rsqf(group_sum<LPR>(squares4(x[u] * f)) * (1.0f / D) + a.eps * f * f);
                 }
                 x[u] = x[u] * f * a_row;
                 if (turns) y[u] = y[u] * f * a_row;

@@ -109,6 +109,44 @@ def test_kv_write_norm_magnitudes(d):
         check_rows(cache_values(c)[0][0].transpose(0, 1)[:len(sizes)], y, y.abs() * (NORM + lost), BF16)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("eps", [2.0 ** 100, 2.0 ** 90, 2.0 ** -100])
+def test_kv_write_norm_large_rows_and_eps(d, eps):
+    """Rows whose sum of squares is just below and just above fp32's largest, where eps may still count."""
+    g = gen(d + 1)
+    sizes = [2.0 ** e for e in (48, 50, 52, 56, 58, 59, 60, 61, 62, 63, 64, 65)]
+    x = ((1 + torch.rand((12, 2, d), generator=g, device=DEV, dtype=torch.float64)) *
+         torch.tensor(sizes, dtype=torch.float64, device=DEV)[:, None, None]).float()
+    c = P.ptq1_kv_cache(1, 16, 2, d, BF16, DEV)
+    out = P.ptq1_kv_write_norm(x, x, x, torch.arange(12, device=DEV), c, eps=eps)
+    y = normed(x, None, eps)
+    check_rows(out, y, y.abs() * NORM, F32)
+
+
+@pytest.mark.parametrize("ctype", [BF16, I8])
+def test_kv_write_norm_position_outside_the_table(ctype):
+    """Only the elements that would turn are NaN; an int8 row, which has one step, is NaN throughout."""
+    g = gen(141)
+    n, d, rot = 5, 128, 32
+    c = P.ptq1_kv_cache(1, 16, 1, d, ctype, DEV)
+    x = randn(g, n, 4, d)
+    pos = torch.tensor([0, -1, 3, 8, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
+    out = P.ptq1_kv_write_norm(x[:, :2], x[:, 2:3], x[:, 3:], torch.arange(n, device=DEV), c, positions=pos,
+                               cos_sin=rope_table(8, rot))
+    y = normed(x, None, 1e-6)
+    kc, vc = cache_values(c)
+    for t in range(n):
+        outside = not 0 <= pos[t].item() < 8
+        assert bool(out[t, :, :rot].isnan().all()) == outside
+        check_rows(out[t, :, rot:], y[t, :2, rot:], y[t, :2, rot:].abs() * NORM, F32)
+        if ctype == I8:
+            assert bool(kc[0, 0, t].isnan().all()) == outside and bool(kc[0, 0, t].isnan().any()) == outside
+        else:
+            assert bool(kc[0, 0, t, :rot].isnan().all()) == outside
+            check_rows(kc[0, 0, t, rot:], y[t, 2, rot:], y[t, 2, rot:].abs() * NORM, ctype)
+        assert bool(vc[0, 0, t].isfinite().all())
+
+
 def test_kv_write_norm_non_finite():
     """A NaN takes its head, an infinity makes its own element NaN and the others zero; other heads and V stay."""
     for ctype in (BF16, I8):
