@@ -173,15 +173,19 @@ __device__ __forceinline__ bool pick_of_64(const ChunkArgs &a, int number, int g
     int whole = all, per = 1 << 30;
     if (a.cut) {
         const int total = wave_total(tiles * steps), longest = wave_largest(steps);
-        const int full = all / a.wanted * a.wanted, left = wave_total(max(0, min(tiles, before + tiles - full)) * steps);
+        const int full = all / a.wanted * a.wanted, mine = max(0, min(tiles, before + tiles - full));
+        const int left = wave_total(mine * steps), last = wave_largest(mine > 0 ? steps : 0);
         if (10 * static_cast<int64_t>(total) < 6 * static_cast<int64_t>(all) * longest) {
             whole = 0;
             per = chunk_piece(total, a.wanted);
-        } else if (10 * static_cast<int64_t>(left) >= 6 * static_cast<int64_t>(all - full) * longest) {
-            const int n = chunk_cuts(all - full, longest, a.wanted, a.join_cost, a.piece_cost);
+        } else if (all > full && 10 * static_cast<int64_t>(left) >= 6 * static_cast<int64_t>(all - full) * last) {
+            // (a lane each: a loop over them took 10 us of a kernel's start)
+            const float cost = chunk_cost(chunk_cut_of(lane), all - full, last, a.wanted, a.join_cost, a.piece_cost);
+            const float least = -wave_max(cost < 0.0f ? -__builtin_inff() : -cost);
+            const int n = chunk_cut_of(__builtin_ctzll(__ballot(cost == least)));
             if (n > 1) {
                 whole = full;
-                per = imax(kChunkMinSteps, (longest + n - 1) / n);
+                per = imax(kChunkMinSteps, (last + n - 1) / n);
             }
         }
     }

@@ -66,24 +66,18 @@ constexpr int steps_bound(int len, int window, int sinks, int group)
 // pieces fill the GPU.
 constexpr int chunk_piece(int total, int wanted) { return imax(kChunkMinSteps, (total + wanted - 1) / wanted); }
 
-// The number of pieces that `tiles` of `steps` each are cut in to end soonest
-// where `wanted` run side by side (join_cost, piece_cost: in steps): at most twice
-// as many pieces.
-constexpr int chunk_cuts(int tiles, int steps, int wanted, float join_cost, float piece_cost)
+// What `tiles` of `steps` each, cut in n pieces, take where `wanted` run side by
+// side, in steps (join_cost and piece_cost too); negative: too many pieces (twice
+// `wanted` at most), or too short ones.
+constexpr float chunk_cost(int n, int tiles, int steps, int wanted, float join_cost, float piece_cost)
 {
-    int best = 1;
-    float lowest = 0.0f;
-    for (int n = 1; n == 1 || (tiles * n <= 2 * wanted && (steps + n - 1) / n >= kChunkMinSteps); n += n < 8 ? 1 : n / 4) {
-        const int rounds = (tiles * n + wanted - 1) / wanted;
-        const float cost = static_cast<float>(rounds * ((steps + n - 1) / n)) +
-                           (n > 1 ? join_cost + piece_cost * static_cast<float>(tiles * n) : 0.0f);
-        if (n == 1 || cost < lowest) {
-            lowest = cost;
-            best = n;
-        }
-    }
-    return best;
+    const int per = (steps + n - 1) / n;
+    if (n > 1 && (static_cast<int64_t>(tiles) * n > 2 * static_cast<int64_t>(wanted) || per < kChunkMinSteps)) return -1.0f;
+    return static_cast<float>((tiles * n + wanted - 1) / wanted * per) + (n > 1 ? join_cost + piece_cost * static_cast<float>(tiles * n) : 0.0f);
 }
+// The numbers of pieces that are considered, by lane: 1 to 15, then eight of
+// each power of two, up to 960.
+constexpr int chunk_cut_of(int lane) { return lane < 8 ? lane + 1 : (8 + (lane & 7)) << ((lane >> 3) - 1); }
 
 constexpr int chunk_pieces(int steps, int per) { return imax(1, (steps + per - 1) / per); }
 

@@ -294,6 +294,19 @@ int main()
                 const int per = chunk_piece(tiles * steps, wanted);
                 if (tiles * chunk_pieces(steps, per) > wanted + tiles || per < kChunkMinSteps) return bad("pieces", wanted, tiles, steps, per);
             }
+    // cuts: one piece is always allowed, more while they are long enough and find places
+    for (int lane = 0; lane < 64; ++lane) {
+        const int n = chunk_cut_of(lane);
+        if (n < 1 || n > 960 || (lane > 0 && n < chunk_cut_of(lane - 1)) || (lane < 15 && lane != 8 && n != lane + (lane < 8))) return bad("cut", lane, n, 0, 0);
+        for (int wanted : {1, 7, 64, 512})
+            for (int tiles : {1, 3, 100, 2048})
+                for (int steps : {1, 4, 5, 63, 1000, 65536}) {
+                    const float cost = chunk_cost(n, tiles, steps, wanted, 3.0f, 0.1f);
+                    const int per = imax(kChunkMinSteps, (steps + n - 1) / n);
+                    if (n == 1 ? !(cost > 0) : cost >= 0 && (tiles * chunk_pieces(steps, per) > 2 * wanted || (steps + n - 1) / n < kChunkMinSteps))
+                        return bad("cost", n, tiles, steps, wanted);
+                }
+    }
     const ChunkSteps c = chunk_steps((1 << 22) - 5, (1 << 22) - 1, (1 << 22) + 1, 1 << 22);
     return c.steps == 65536 && c.lo == 0 ? 0 : bad("large", c.steps, c.lo, c.reach, c.gap);
 }
