@@ -564,15 +564,20 @@ ptq1_status ptq1_attn_decode_window(const void *q, int32_t q_dtype, int64_t batc
  * What a query does not see does not enter its row, whatever it holds, and pages
  * that hold nothing that a query of their sequence sees are not read: their
  * entries of block_table may be anything.
- * bf16 or fp16 matrix cores, fp32 scores, maxima, sums and accumulators.  Over
- * 16-bit caches the weights enter the second product rounded to their type
- * (fp16: to 11 bits, down to 2^-32 of the row's largest), and their sum, in fp32, is that
- * of the rounded ones, as in ptq1_attn_prompt.  Over int8 caches the codes enter
- * exactly, as fp16, the queries as fp16 times a power of two of their head (bf16:
- * exact down to 2^-21 of the head's largest magnitude, then down to 2^-39 of
- * it), and weight times step rounded to fp16 (11 bits, down to 2^-28 of the
- * row's largest).  A NaN or an infinity in a query, or in a key or value that it
- * sees, makes the entries of out that it enters NaN or infinite.
+ * bf16 or fp16 matrix cores, fp32 scores, maxima, sums and accumulators.  K, V,
+ * queries and int8 codes enter exactly.  Weights enter the second product in
+ * the cache's 16-bit type, over int8 caches times their value's step in fp16:
+ *   where max_q * n_q_heads / n_kv_heads is at most 32 (few rows, where K and V
+ *        bound the call) as two terms, 16 (bf16) or 22 bits of a weight;
+ *   elsewhere as one, 8 (bf16) or 11 bits, and over 16-bit caches it is the
+ *        rounded weights that are summed, as in ptq1_attn_prompt.
+ * fp16 terms end at 2^-32 of the row's largest weight, over int8 caches at 2^-27
+ * of its largest weight times step.  Values up to the type's largest, and steps
+ * up to what ptq1_kv_write makes, do not overflow on the way to a row that is in
+ * range; over int8 caches log2(e) * scale * step has to be a normal number of
+ * fp32, or the keys' scores lose bits.  A NaN or an infinity in a query, or in a
+ * key or value that it sees, makes the entries of out that it enters NaN or
+ * infinite; an infinite key at a score of -infinity has weight zero instead.
  * Where the tiles of query rows alone would not fill the GPU, the keys are cut
  * into pieces that run side by side and are joined by a second launch, in a
  * fixed order, by the lengths on the device.

