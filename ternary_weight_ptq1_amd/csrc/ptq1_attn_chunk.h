@@ -354,20 +354,30 @@ __device__ __forceinline__ int unit_of_steps(int unit, int e)
     return e > 125 || (e <= unit && e >= unit - 12) ? unit : e + 2;
 }
 
-// 8 int8 codes (two dwords) as bf16, exact: bytes of code + 128 become fp32, of
-// which, less 128, the upper halves are bf16.
+// Byte B of x, signed, as fp32 (of a shift and a conversion the compiler makes
+// two instructions).
+template <int B>
+__device__ __forceinline__ float code_of(uint32_t x)
+{
+    float f;
+    if constexpr (B == 0)
+        asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0" : "=v"(f) : "v"(x));
+    else if constexpr (B == 1)
+        asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1" : "=v"(f) : "v"(x));
+    else if constexpr (B == 2)
+        asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2" : "=v"(f) : "v"(x));
+    else
+        asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3" : "=v"(f) : "v"(x));
+    return f;
+}
+// 8 int8 codes (two dwords) as bf16, exact: the upper halves of them as fp32.
 __device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t a, uint32_t b)
 {
-    a ^= 0x80808080u;
-    b ^= 0x80808080u;
-    at_u32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t x = i < 2 ? a : b;
-        const float lo = static_cast<float>((x >> (16 * (i & 1))) & 0xffu) - 128.0f;
-        const float hi = static_cast<float>((x >> (16 * (i & 1) + 8)) & 0xffu) - 128.0f;
-        w[i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
-    }
+    const auto pair = [](float lo, float hi) {
+        return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
+    };
+    const at_u32x4 w = {pair(code_of<0>(a), code_of<1>(a)), pair(code_of<2>(a), code_of<3>(a)), pair(code_of<0>(b), code_of<1>(b)),
+                        pair(code_of<2>(b), code_of<3>(b))};
     return __builtin_bit_cast(bf16x8, w);
 }
 template <typename T>
