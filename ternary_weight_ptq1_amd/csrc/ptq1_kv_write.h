@@ -13,7 +13,11 @@ namespace {
 
 constexpr int kKvThreads = 256;
 constexpr int kVTok = 64;  // tokens of one V tile (write): a wave's lanes
-constexpr int kRowsPer = 2;  // q and k rows a thread has in flight (write)
+// q and k rows a thread has in flight.  With norms, whose sums every row waits
+// for, more workgroups hide more than more rows: 8191 tokens of 24 + 4 + 4 heads of
+// 256 95 us with one, 101 with two, 151 with four.
+template <bool NORM>
+constexpr int kRowsPer = NORM ? 1 : 2;
 
 struct KvWriteArgs {
     const void *q, *k, *v;
@@ -134,6 +138,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_write(KvWriteArgs a)
     constexpr bool I8 = std::is_same<C, int8_t>::value;
     constexpr int LPR = D / 4;               // lanes per row
     constexpr int RPB = kKvThreads / LPR;    // rows per block and pass
+    constexpr int ROWS = kRowsPer<NORM>;
     const int sub = threadIdx.x / LPR, e = (threadIdx.x % LPR) * 4;
     const int64_t page = int64_t{1} << a.page_shift;
 
@@ -142,13 +147,13 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_write(KvWriteArgs a)
         const int half = a.rot >> 1;
         const bool turns = e < a.rot, upper = e >= half;
         const int lo = upper ? e - half : e, other = upper ? lo : lo + half;
-        at_f32x4 x[kRowsPer], y[kRowsPer], c[kRowsPer], sn[kRowsPer];
-        int64_t token[kRowsPer];
-        int h[kRowsPer], pos[kRowsPer];
-        bool there[kRowsPer], placed[kRowsPer];
+        at_f32x4 x[ROWS], y[ROWS], c[ROWS], sn[ROWS];
+        int64_t token[ROWS];
+        int h[ROWS], pos[ROWS];
+        bool there[ROWS], placed[ROWS];
 #pragma unroll
-        for (int u = 0; u < kRowsPer; ++u) {
-            const uint32_t row = ((blockIdx.x - a.v_blocks) * kRowsPer + u) * RPB + sub;
+        for (int u = 0; u < ROWS; ++u) {
+            const uint32_t row = ((blockIdx.x - a.v_blocks) * ROWS + u) * RPB + sub;
             if constexpr (NORM) {
                 // (of a 256-wide row a wave's lanes have one: its address is scalar)
                 const uint32_t r = LPR == kWave ? __builtin_amdgcn_readfirstlane(row) : row;
@@ -170,7 +175,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_write(KvWriteArgs a)
             }
         }
 #pragma unroll
-        for (int u = 0; u < kRowsPer; ++u) {
+        for (int u = 0; u < ROWS; ++u) {
             placed[u] = there[u] && turns && pos[u] >= 0 && pos[u] < a.n_positions;
             if (!placed[u]) continue;
             const float *cs = a.cos_sin + static_cast<int64_t>(pos[u]) * a.rot + lo;
@@ -179,7 +184,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_write(KvWriteArgs a)
         }
         if constexpr (NORM) {
 #pragma unroll
-            for (int u = 0; u < kRowsPer; ++u) {
+            for (int u = 0; u < ROWS; ++u) {
                 if (!there[u]) continue;  // (a row's lanes alike)
                 const float sum = group_sum<LPR>(squares4(x[u]));
                 float f = 1.0f, a_row = __builtin_amdgcn_rsqf(sum * (1.0f / D) + a.eps);
@@ -201,7 +206,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_write(KvWriteArgs a)
             }
         }
 #pragma unroll
-        for (int u = 0; u < kRowsPer; ++u) {
+        for (int u = 0; u < ROWS; ++u) {
             if (!there[u]) continue;
             if (placed[u]) {
 #pragma clang fp contract(off)
@@ -333,7 +338,7 @@ inline int log2_of(int32_t v) { return __builtin_ctz(static_cast<unsigned>(v)); 
 template <bool NORM, typename S, typename Q, typename C, int D>
 hipError_t write_launch(KvWriteArgs &a, hipStream_t s)
 {
-    constexpr int RPB = kKvThreads / (D / 4) * kRowsPer;
+    constexpr int RPB = kKvThreads / (D / 4) * kRowsPer<NORM>;
     const int64_t heads = a.hq + a.hkv, rows = a.tokens * heads;
     int log = 0;
     while ((int64_t{1} << log) < heads) ++log;
