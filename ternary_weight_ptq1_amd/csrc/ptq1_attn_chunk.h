@@ -516,6 +516,10 @@ struct ChunkSoftmax {
     float m = -__builtin_inff(), l = 0.0f, l2 = 0.0f;  // m: the reference, in units of log2
     bool large = false;
     int unit = -126;
+    // int8 caches: a step's scores are multiplied by their keys' steps and taken
+    // from the reference at once, base; `shift` further where it moves (and all
+    // of it where products are rounded first, base = 0)
+    float base = 0.0f, shift = 0.0f;
 
     static __device__ __forceinline__ int key(int t, int j, int half)
     {
@@ -530,19 +534,20 @@ struct ChunkSoftmax {
             for (int j = 0; j < 16; ++j) s[t][j] = ldexpf(s[t][j], e);
     }
 
-    // the largest score of the lane's pair; on the border hidden ones leave the
-    // scores (int8 caches: ks(t, j) is the step of score register j of tile t;
+    // the largest score of the lane's pair (int8 caches: less base); on the border
+    // hidden ones leave the scores (int8 caches: ks(t, j) is the step of score register j of tile t;
     // lifted: of some row the queries are, lift() is the lane's)
     template <class S, class L>
     __device__ __forceinline__ float top(bool border, at_f32x16 (&s)[KT], const HiddenKeys &hidden, int n0, int half, float c, S ks, bool lifted, L lift)
     {
         if constexpr (I8) {
+            base = large || lifted || m == -__builtin_inff() ? 0.0f : m;
             if (lifted) by_power(s, lift() >> 1);
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    s[t][j] *= ks(t, j);
+                    s[t][j] = fmaf(s[t][j], ks(t, j), -base);
                     if (!RUN16 && (j & 7) == 7) __builtin_amdgcn_sched_barrier(0);  // (or all steps are read up front)
                 }
             if (lifted) by_power(s, (lift() + 1) >> 1);
@@ -574,10 +579,11 @@ struct ChunkSoftmax {
     template <int N>
     __device__ __forceinline__ void raise(float top, at_f32x16 (&o)[N], int &units)
     {
-        const float mt = reference<T>(top);
-        if (__ballot(mt > m + 8.0f) != 0) {
-            const float mn = fmaxf(m, mt);
-            float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+        const float mt = reference<T>(top), was = I8 ? m - base : m;
+        if constexpr (I8) shift = was;
+        if (__ballot(mt > was + 8.0f) != 0) {
+            const float mn = fmaxf(was, mt);
+            float f = was == mn ? 1.0f : __builtin_amdgcn_exp2f(was - mn);
             l *= f;
             l2 *= f;
             if constexpr (I8) {
@@ -591,7 +597,8 @@ struct ChunkSoftmax {
             }
 #pragma unroll
             for (int i = 0; i < N; ++i) o[i] *= f;
-            m = mn;
+            if constexpr (I8) shift = mn;
+            m = I8 ? base + mn : mn;
             large = large_scores(m);
         }
     }
@@ -648,12 +655,18 @@ struct ChunkSoftmax {
     __device__ __forceinline__ void products(bool border, at_f32x16 (&s)[KT], const HiddenKeys &hidden, int n0, int half, S vs,
                                              int of_steps, x8 (&pf)[TERMS][2 * KT], F rescale)
     {
-        const float ms = m == -__builtin_inff() ? 0.0f : m;
+        if (shift == -__builtin_inff()) shift = 0.0f;
+        if (__ballot(shift != 0.0f) != 0) {
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[t][j] -= shift;
+        }
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const float p = __builtin_amdgcn_exp2f(s[t][j] - ms);
+                const float p = __builtin_amdgcn_exp2f(s[t][j]);
                 if ((j & 1) == 0) l += p;
                 else l2 += p;
                 s[t][j] = p * vs(t, j);
