@@ -30,14 +30,14 @@
 // product in units of a power of two of their row.
 //
 // Measured (matrix work differs by up to 10% from card to card; these are the
-// faster ones).  4096 tokens behind 28000 (40 heads over 8 of 128, bf16): 1510 to
-// 1570 us, 990 to 1030 TFLOP/s; matrix cores 51% busy, vector units 54%.  8 x 256 to
-// 512 tokens behind 6000 to 12000 over int8: 823 us, 730 TFLOP/s, the vector units (62%;
-// the codes of a step cost 200 of 700 instructions of a wave) and LDS (stores of
-// codes: on the layout of the 16-bit tiles they met two by two, 860 us).  4 x 350 to
-// 700 tokens behind 2000 to 4000, 256-wide heads, fp16: 235 us, 650 TFLOP/s, eight
+// faster ones).  4096 tokens behind 28000 (40 heads over 8 of 128, bf16): 1480 to
+// 1570 us, 990 to 1050 TFLOP/s; matrix cores 51% busy, vector units 54%.  8 x 256 to
+// 512 tokens behind 6000 to 12000 over int8: 755 us, 800 TFLOP/s, the vector units
+// (56%; the codes of a step cost 160 of 630 instructions of a wave) and LDS (stores
+// of codes: on the layout of the 16-bit tiles they met two by two, 3% more).  4 x 350
+// to 700 tokens behind 2000 to 4000, 256-wide heads, fp16: 233 us, 650 TFLOP/s, eight
 // waves in step through three barriers (matrix cores 29%).  3 x 1000 to 2000 tokens
-// in windows of 1024 (32 heads over 8 of 128): 133 us, 630 TFLOP/s: of a tile's 18
+// in windows of 1024 (32 heads over 8 of 128): 131 us, 640 TFLOP/s: of a tile's 18
 // steps three are on a border, and 158 tiles of a kv head run on 64 places.
 #include <hip/hip_runtime.h>
 

@@ -3,7 +3,7 @@
 // of ptq1_kv_write (ptq1_kv_write.h), whose q and k rows lie in the registers
 // of neighbouring lanes, so that a norm costs the exchanges of one sum and no
 // more memory traffic than its gains.  HBM bounds it: 8191 tokens of 24 + 4 + 4
-// heads of 256 (fp32 rows, bf16 queries and cache, 405 MB) take 103 us, 3.9 TB/s
+// heads of 256 (fp32 rows, bf16 queries and cache, 405 MB) take 96 us, 4.2 TB/s
 // (the same rows without norms 87 to 91); one token 3.5 us on the GPU.
 #include <hip/hip_runtime.h>
 
