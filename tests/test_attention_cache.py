@@ -1039,3 +1039,49 @@ def test_attn_decode_window_non_finite(qt, ctype):
             assert torch.equal(odd[keep], got[keep])
             for t, w in zip([t for t in (c.k_pages, c.v_pages, c.k_steps, c.v_steps) if t is not None], was):
                 t.copy_(w)
+
+
+@pytest.mark.parametrize("qt", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("m", [3, 150])
+@pytest.mark.parametrize("order", ["up", "down", "both"])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attn_chunk_scores_of_all_sizes(qt, d, m, order, sign):
+    """int8 keys whose steps run from 2^-10 to 2^40 along the sequence (or back, or both), queries of one: the reference
+    moves from small scores to those whose products are rounded first.  Rows stay within their values, and where one
+    score is far ahead it is that token's value."""
+    g = gen(220)
+    n = 900
+    table, pages = tables(g, [n], 32)
+    c = filled_cache(g, pages, 32, 1, d, I8)
+    c.k_pages.zero_()
+    rows, j = table[0].long(), torch.arange(n, device=DEV)
+    c.k_pages[rows[j // 32], 0, j % 32, 0] = sign * 100
+    e = torch.linspace(-10, 40, n, device=DEV)
+    e = {"up": e, "down": e.flip(0), "both": torch.cat([e[::2], e.flip(0)[::2]])[:n]}[order]
+    c.k_steps[rows[j // 32], 0, j % 32] = torch.exp2(e)
+    q = torch.zeros((m, 2, d), dtype=qt, device=DEV)
+    q[..., 0] = 1
+    got = P.ptq1_attn_chunk(q, c, table, cumulated([m]), torch.tensor([n], dtype=torch.int32, device=DEV), scale=0.5, max_q=m).double()
+    kc, vc = cache_values(c)
+    k, v = sequence(c, kc, table, 0, n)[0], sequence(c, vc, table, 0, n)[0]
+    assert bool((got.abs() <= v.abs().amax() * 1.01).all())
+    counted = 0
+    for h in range(2):
+        # a small score's error is its own, not that of the largest among the keys: those have no weight where it has
+        logits = (0.5 * (q[:, h].double() @ k.T.contiguous())).masked_fill(~window_mask(m, n, 0, 0), -math.inf)
+        best = logits.topk(2, 1)
+        ok = best.values[:, 0] - best.values[:, 1] > 100 + 64 * U * best.values[:, 0].abs()
+        want = v[best.indices[:, 0]]
+        tol = half_step(want, qt) + chunk_term(qt, I8, 2 * m) * want.abs() + 4 * U * want.abs()
+        assert bool(((got[:, h] - want).abs()[ok] <= tol[ok]).all())
+        counted += int(ok.sum())
+        small = best.values[:, 0].abs() < 1024
+        if bool(small.any()):
+            p = torch.softmax(logits[small], 1)
+            err = (got[small, h] - p @ v).abs()
+            # scores of up to 1024 and products of 2^-24 of them, four times, weights of one term
+            bound = (8 * 1024 * U + chunk_term(qt, I8, 2 * m) + 2 * n * U) * (p @ v.abs()) + 2.0 ** -27 * 127 * n * 0.03 * p.amax(1, keepdim=True)
+            assert bool((err <= bound + half_step((p @ v).abs() + bound, qt)).all())
+            counted += int(small.sum())
+    assert counted > 0
