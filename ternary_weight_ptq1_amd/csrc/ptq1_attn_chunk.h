@@ -518,7 +518,8 @@ struct ChunkSoftmax {
     int unit = -126;
     // int8 caches: a step's scores are multiplied by their keys' steps and taken
     // from the reference at once, base; `shift` further where it moves (and all
-    // of it where products are rounded first, base = 0)
+    // of it where products are rounded first, base = 0: in a row's first step,
+    // which has no reference yet, and among large or lifted scores)
     float base = 0.0f, shift = 0.0f;
 
     static __device__ __forceinline__ int key(int t, int j, int half)
@@ -582,7 +583,14 @@ struct ChunkSoftmax {
         const float mt = reference<T>(top), was = I8 ? m - base : m;
         if constexpr (I8) shift = was;
         if (__ballot(mt > was + 8.0f) != 0) {
-            const float mn = fmaxf(was, mt);
+            float mn = fmaxf(was, mt);
+            if constexpr (I8) {
+                // whole numbers, of which sums are exact: rounded here alone, a reference
+                // would be another for this step's keys than for the later ones'
+                m = base + ceilf(mn);
+                mn = m - base;
+            } else
+                m = mn;
             float f = was == mn ? 1.0f : __builtin_amdgcn_exp2f(was - mn);
             l *= f;
             l2 *= f;
@@ -598,7 +606,6 @@ struct ChunkSoftmax {
 #pragma unroll
             for (int i = 0; i < N; ++i) o[i] *= f;
             if constexpr (I8) shift = mn;
-            m = I8 ? base + mn : mn;
             large = large_scores(m);
         }
     }

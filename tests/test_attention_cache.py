@@ -1085,3 +1085,43 @@ def test_attn_chunk_scores_of_all_sizes(qt, d, m, order, sign):
             assert bool((err <= bound + half_step((p @ v).abs() + bound, qt)).all())
             counted += int(small.sum())
     assert counted > 0
+
+
+@pytest.mark.parametrize("qt", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("m", [3, 40])
+@pytest.mark.parametrize("power,sign", [(17, 1), (17, -1), (19, 1), (19, -1)])
+def test_attn_chunk_equal_int8_scores_weigh_the_same(qt, d, m, power, sign):
+    """int8 keys of one score, that of three halves of 2^power, over two runs of steps of values 1 and -1: whether the
+    reference moves in a step or has been where it is, its keys weigh the same.  The score, 101 codes times a step, lies
+    near the middle between two fp32 values, so that no rounded reference is the score less a round number.
+
+    Of a score less a reference near it fp32 leaves 2^-19 at most (both differ by less than 64), and a weight is
+    rounded by half a step of fp16: the weights of a run are within 2^-11 + 2^-17 of the other's."""
+    run = 128 if m <= 16 else 64                   # (few rows: four waves take 32 keys each in turn)
+    copies = 260 if m <= 16 else 1                 # so many sequences of few rows that none is cut: they share their pages
+    hkv, page = 8, 64
+    log2e = np.float32(math.log2(math.e))
+    scale = np.float32(math.log(2.0))
+    assert scale * log2e == 1.0                    # (scores in units of log2 are code times step)
+    grid = 2.0 ** (power - 23)
+    step = np.float32(1.5 * 2.0 ** power / 101)
+    while not 0.46 <= 101 * float(step) / grid % 1.0 <= 0.49:
+        step = np.nextafter(step, np.float32(math.inf))
+    before = np.float32(float(step) - sign * 20 / 101)   # a score that is lower by 20
+    n = 3 * run + m
+    codes, steps = torch.full((n,), 101.0 * sign), torch.full((n,), float(step))
+    steps[:run] = float(before)
+    codes[3 * run:], steps[3 * run:] = -127, 2.0 ** power / 40   # the queries' own tokens weigh nothing
+    k, v = (torch.zeros((n, hkv, d), dtype=I8, device=DEV) for _ in range(2))
+    k[..., 0] = codes.to(I8).to(DEV)[:, None]
+    v[run:2 * run], v[2 * run:3 * run] = 1, -1
+    c, table = placed(k, v, page, I8, 1.0)
+    at = torch.arange(n, device=DEV)
+    c.k_steps[table[0, at // page].long(), :, at % page] = steps.to(DEV)[:, None]
+    q = torch.zeros((copies * m, 2 * hkv, d), device=DEV, dtype=qt)
+    q[..., 0] = 1
+    sl = torch.full((copies,), n, dtype=torch.int32, device=DEV)
+    got = P.ptq1_attn_chunk(q, c, table.expand(copies, -1).contiguous(), cumulated([m] * copies), sl, scale=float(scale), max_q=m)
+    assert P.workspace_bytes("attn_chunk", copies, copies * m, m, 2 * hkv, hkv, d, c.n_pages * page, 0, 0) == 0
+    assert got.abs().max().item() <= 2.0 ** -11 + 2.0 ** -17, got.abs().max().item()
