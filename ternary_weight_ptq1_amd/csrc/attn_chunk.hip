@@ -205,31 +205,35 @@ struct ChunkStaging {
     }
 };
 
-// A NaN or an infinity leaves a V tile in LDS (zeros in its place); true if there
-// was one.  Most tiles have none, which the largest magnitude among a thread's
-// values tells.
+// NaNs and infinities leave a V tile in LDS (zeros in their place); one of a key
+// that some row sees is noted.  (Were those of other keys noted too, what lies
+// behind a sequence's end would decide the time: 84 us for 13 behind 161 and 130
+// keys, and with first tokens and a window's begin 2890 for 90.)  Most tiles have
+// none, which the largest magnitude among a thread's values tells.
 template <typename T, int D>
-__device__ __forceinline__ bool clean_values(T *v)
+__device__ __forceinline__ void clean_values(T *v, int n0, const ChunkSteps &seen, ChunkNotes *notes)
 {
     constexpr int NT = 64 * chunk_waves(D), N = BN * D / 8 / NT;
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    constexpr uint16_t kNone = std::is_same<T, __bf16>::value ? 0x7f80u : 0x7c00u;
     at_u32x4 w[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const at_u32x4 *>(v + 8 * (i * NT + threadIdx.x));
-    u16x2 most = {0, 0};
+    LargestHalf<T> most;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int i = 0; i < N; ++i) most.of(w[i]);
+    if (!most.non_finite()) return;
+    // (a thread's pieces are of the same eight keys, as in ChunkStaging)
+    const int piece = static_cast<int>(threadIdx.x & 7) ^ swizzle<BN>(static_cast<int>(threadIdx.x >> 3));
+    const at_u32x4 halves = seen_halves(n0 + 8 * piece, seen.lo, seen.reach, seen.sunk);
+    uint32_t gone = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t x = w[i][j] & 0x7fff7fffu;
-            most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, x));
-        }
-    if (most[0] < kNone && most[1] < kNone) return false;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int i = 0; i < N; ++i) {
+        const at_u32x4 was = w[i];
         if (clear_non_finite<T>(w[i])) *reinterpret_cast<at_u32x4 *>(v + 8 * (i * NT + threadIdx.x)) = w[i];
-    return true;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) gone |= (was[j] ^ w[i][j]) & halves[j];
+    }
+    if (gone == 0) return;
+    atomicOr(&notes->odd_steps, step_bit(n0));
 }
 
 // The row's dimensions d0 + 32 i + 8 b + 4 half + e, finished: as they are, or
@@ -280,7 +284,7 @@ __device__ __forceinline__ void finish(const ChunkArgs &a, const ChunkTile &t, c
         }
     }
     if constexpr (!std::is_same<C, int8_t>::value)
-        if (notes.odd_from < notes.odd_to) add_odd_values<C, N>(a, t, row, notes, d, d0, half, o);
+        if (notes.odd_steps != 0) add_odd_values<C, N>(a, t, row, notes, d, d0, half, o);
     if (row.is) store_rows<QT, N>(a, t, row, at, d, d0, half, o, m, l);
 }
 
@@ -338,7 +342,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
     const ChunkQuery<QT, D, false, I8> q(a, t, first_row, half);
     if constexpr (I8) lift_of[32 * wave + col] = q.lift;
     const bool lifted = I8 && __ballot(q.lift != 0) != 0;
-    if (threadIdx.x == 0) notes = {1 << 30, 0, 0};
+    if (threadIdx.x == 0) notes = {0, 0};
 
     at_f32x16 o[DT];
 #pragma unroll
@@ -401,10 +405,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(D), 2) k_attn_chunk(ChunkArgs
             // a zero weight would not keep a NaN or an infinity out of the rows
             // that do not see it: such values leave the tile and are given to
             // the rows that see them at the end
-            if (clean_values<T, D>(b.v)) {
-                atomicMin(&notes.odd_from, n0);
-                atomicMax(&notes.odd_to, n0 + BN);
-            }
+            clean_values<T, D>(b.v, n0, tile_note.c, &notes);
             __syncthreads();
         }
         if (!idle) {
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
     const ChunkQuery<QT, D, false, I8> q(a, t, first_row, half);
     if constexpr (I8) lift_of[32 * pair + col] = q.lift;
     const bool lifted = I8 && __ballot(q.lift != 0) != 0;
-    if (threadIdx.x == 0) notes = {1 << 30, 0, 0};
+    if (threadIdx.x == 0) notes = {0, 0};
 
     at_f32x16 o[DT];  // dimensions 128 part + 32 i + ...
 #pragma unroll
@@ -544,10 +545,7 @@ __global__ void __launch_bounds__(64 * chunk_waves(256), 2) k_attn_chunk_wide(Ch
             weights[pair][2 * part + 1][lane] = pf[0][1];
         }
         if constexpr (BORDER && !I8) {
-            if (clean_values<T, D>(b.v)) {
-                atomicMin(&notes.odd_from, n0);
-                atomicMax(&notes.odd_to, n0 + BN);
-            }
+            clean_values<T, D>(b.v, n0, tile_note.c, &notes);
         }
         barrier_lds();
         if (!idle) {

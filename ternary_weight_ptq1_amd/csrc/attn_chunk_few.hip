@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) k_attn_chunk
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[d][j] = 0.0f;
     ChunkSoftmax<C, 1, 2, I8> w;
-    ChunkNotes notes{1 << 30, 0, 0};
+    ChunkNotes notes{0, 0};
     int steps_unit = -126;
 
     for (; i < n; i += W) {
@@ -164,13 +164,18 @@ __global__ void __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) k_attn_chunk
             w.weights(s, c, pf);
         if (!I8 && border) {
             // (as in the tiles: what a row does not see must not meet its zero weight)
-            bool odd = false;
+            uint32_t odd = 0;
 #pragma unroll
-            for (int k = 0; k < NL; ++k) odd |= clear_non_finite<T>(vr[k]);
-            if (__ballot(odd) != 0) {
-                notes.odd_from = min(notes.odd_from, n0);
-                notes.odd_to = max(notes.odd_to, n0 + 32);
+            for (int u = 0; u < 2; ++u) {
+                const at_u32x4 seen = seen_halves(n0 + 16 * u + 8 * half, t.c.lo, t.c.reach, t.c.sunk);
+#pragma unroll
+                for (int k = u; k < NL; k += 2) {
+                    vr[k] &= seen;
+                    odd |= clear_non_finite<T>(vr[k]);
+                    asm volatile("" : "+v"(odd), "+v"(vr[k]));  // (one after the other: all at once need registers)
+                }
             }
+            if (__ballot(odd != 0) != 0) notes.odd_steps |= step_bit(n0);
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -195,7 +200,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) k_attn_chunk
     }
     const float l = lane_pair_sum<32>(w.l + w.l2);
     if constexpr (!I8)
-        if (notes.odd_from < notes.odd_to) add_odd_values<T, DT>(a, t, row, notes, D, 0, half, o);
+        if (notes.odd_steps != 0) add_odd_values<T, DT>(a, t, row, notes, D, 0, half, o);
 
     // ---- join the waves' rows: each row's weights of the waves first
     if (half == 0) {

@@ -325,6 +325,7 @@ struct ChunkPages {
         : table(a.table + static_cast<int64_t>(t.b) * a.max_pages), page_shift(a.page_shift), lo(t.c.lo), reach(t.c.reach), sunk(t.c.sunk),
           n_pages(static_cast<uint32_t>(a.n_pages))
     {
+        asm volatile("" : "+s"(n_pages));  // (kept, not loaded in every step)
     }
     __device__ __forceinline__ void find(int n0)
     {
@@ -389,11 +390,49 @@ __device__ __forceinline__ typename Op16<T>::x8 codes_to(uint32_t a, uint32_t b)
         return codes_to_f16(a, b);
 }
 
-// What was met on the way, for the end: keys among which a V tile had a NaN or
-// an infinity removed, and whether a page was not there.
+// What was met on the way, for the end: the steps (modulo 32) whose V tile had a
+// NaN or an infinity removed that some row sees, and whether a page was not there.
 struct ChunkNotes {
-    int odd_from, odd_to, bad;
+    uint32_t odd_steps;
+    int bad;
 };
+__device__ __forceinline__ uint32_t step_bit(int n0) { return 1u << ((n0 / kChunkKeys) & 31); }
+
+// The largest magnitude among 16-bit values, as bits: a NaN's or an infinity's if there is one.
+template <typename T>
+struct LargestHalf {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 most = {0, 0};
+    __device__ __forceinline__ void of(const at_u32x4 &w)
+    {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t x = w[j] & 0x7fff7fffu;
+            most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, x));
+        }
+    }
+    __device__ __forceinline__ bool non_finite() const
+    {
+        constexpr uint16_t kNone = std::is_same<T, __bf16>::value ? 0x7f80u : 0x7c00u;
+        return most[0] >= kNone || most[1] >= kNone;
+    }
+};
+
+// Of the eight keys from `key` on, in 16 bits each: ones for those that some row
+// of the tile sees.  The others hold anything (behind a sequence's end or ahead
+// of its windows what no token was written to), and are no row's concern.
+__device__ __forceinline__ at_u32x4 seen_halves(int key, int lo, int reach, int sunk)
+{
+    const auto below = [&](int end) { return (1 << min(max(end - key, 0), 8)) - 1; };  // a bit for each of the eight
+    const int some = below(reach) & (~below(lo) | below(sunk));
+    at_u32x4 m;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t a = __builtin_amdgcn_sbfe(some, 2 * j, 1), b = __builtin_amdgcn_sbfe(some, 2 * j + 1, 1);
+        m[j] = (a & 0xffffu) | (b & 0xffff0000u);
+    }
+    return m;
+}
 
 // The page of a key, -1 if there is none.
 __device__ __forceinline__ int64_t page_of_key(const ChunkArgs &a, const ChunkTile &t, int key)
@@ -409,18 +448,22 @@ __device__ __forceinline__ void add_odd_values(const ChunkArgs &a, const ChunkTi
                                                const ChunkNotes &notes, int d, int d0, int half, at_f32x16 (&o)[N])
 {
     const int64_t page = int64_t{1} << a.page_shift;
-    for (int j = notes.odd_from; j < notes.odd_to && j < t.c.reach; ++j) {
-        if (j >= t.c.sunk && j < t.c.lo) continue;
-        const int64_t pg = page_of_key(a, t, j);
-        if (pg < 0 || !(j < row.seen.hi && (j >= row.seen.lo || j < a.sinks))) continue;
-        const T *src = static_cast<const T *>(a.v_pages) + ((pg * a.hkv + t.kh) * d + d0 + 4 * half) * page + (j & (page - 1));
+    for (int step = t.first; step < t.last; ++step) {
+        const int n0 = step_key(t.c, step);
+        if ((notes.odd_steps & step_bit(n0)) == 0) continue;
+        for (int j = n0; j < n0 + kChunkKeys && j < t.c.reach; ++j) {
+            if (j >= t.c.sunk && j < t.c.lo) continue;
+            const int64_t pg = page_of_key(a, t, j);
+            if (pg < 0 || !(j < row.seen.hi && (j >= row.seen.lo || j < a.sinks))) continue;
+            const T *src = static_cast<const T *>(a.v_pages) + ((pg * a.hkv + t.kh) * d + d0 + 4 * half) * page + (j & (page - 1));
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+            for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float x = static_cast<float>(src[(32 * i + 8 * (e >> 2) + (e & 3)) * page]);
-                if (!(fabsf(x) <= 3.4028235e38f)) o[i][e] += x;
-            }
+                for (int e = 0; e < 16; ++e) {
+                    const float x = static_cast<float>(src[(32 * i + 8 * (e >> 2) + (e & 3)) * page]);
+                    if (!(fabsf(x) <= 3.4028235e38f)) o[i][e] += x;
+                }
+        }
     }
 }
 

@@ -68,18 +68,20 @@ __device__ __forceinline__ void copy_to_lds(const char *base, uint32_t bytes, ui
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)dst, 16, static_cast<int>(off), 0, 0, 0);
 }
 
-// Zeros in the place of NaNs and infinities (an exponent of all ones) among
-// eight values; true if there was one.
+// Zeros in the place of NaNs and infinities (an exponent of all ones, to which a
+// one in its last place carries into the sign's) among eight values; not zero if
+// there was one.  (No comparisons: their masks, of a lane's whole tile at once,
+// went through memory.)
 template <typename T>
-__device__ __forceinline__ bool clear_non_finite(at_u32x4 &w)
+__device__ __forceinline__ uint32_t clear_non_finite(at_u32x4 &w)
 {
-    constexpr uint32_t E = std::is_same<T, __bf16>::value ? 0x7f80u : 0x7c00u;
-    bool found = false;
+    constexpr uint32_t E = std::is_same<T, __bf16>::value ? 0x7f807f80u : 0x7c007c00u, kLast = E & ~(E << 1);
+    uint32_t found = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const bool lo = (w[i] & E) == E, hi = (w[i] & (E << 16)) == (E << 16);
-        w[i] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
-        found |= lo || hi;
+        const uint32_t hit = ((w[i] & E) + kLast) & 0x80008000u;
+        w[i] &= ~(hit | (hit - (hit >> 15)));
+        found |= hit;
     }
     return found;
 }
