@@ -840,6 +840,12 @@ def ptq1_kv_read(cache: KvCache, block_table: torch.Tensor, cu_seqlens: torch.Te
     return k, v
 
 
+def _bound(n: int) -> int:
+    """A bound of the caller's as the C calls take it: past 64 bits (where ctypes would keep the lowest ones) the largest
+    there is."""
+    return n if -1 << 63 <= n < 1 << 63 else (1 << 63) - 1 if n > 0 else -1
+
+
 def _attn_decode(q, cache, block_table, seq_lens, scale, max_len, out, ws, stream, seen):
     """Both calls of single tokens; seen: () or (window, sinks)."""
     kv = _kv(cache)
@@ -857,10 +863,11 @@ def _attn_decode(q, cache, block_table, seq_lens, scale, max_len, out, ws, strea
     max_pages = _table(block_table, batch, dv)
     if not _plain(seq_lens, torch.int32, batch, dv):
         _dev(seq_lens, "seq_lens", torch.int32, numel=batch, device=dv)
-    if max_len is None:
-        max_len = max_pages * kv.page_size
+    max_len = max_pages * kv.page_size if max_len is None else _bound(max_len)
     handle = _current_handle(dv)
     if seen:
+        if (seen[0] | seen[1]) >> 63:  # (cheaper than two calls)
+            seen = _bound(seen[0]), _bound(seen[1])
         name, call, size = "ptq1_attn_decode_window", lib().ptq1_attn_decode_window, lib().ptq1_attn_decode_window_workspace_bytes
     else:
         name, call, size = "ptq1_attn_decode", lib().ptq1_attn_decode, lib().ptq1_attn_decode_workspace_bytes
@@ -934,10 +941,10 @@ def ptq1_attn_chunk(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, 
     max_pages = _table(block_table, batch, dv)
     if not _plain(seq_lens, torch.int32, batch, dv):
         _dev(seq_lens, "seq_lens", torch.int32, numel=batch, device=dv)
-    if max_q is None:
-        max_q = rows
-    if max_len is None:
-        max_len = max_pages * kv.page_size
+    max_q = rows if max_q is None else max_q
+    max_len = max_pages * kv.page_size if max_len is None else max_len
+    if (max_q | max_len | window | sinks) >> 63:
+        max_q, max_len, window, sinks = map(_bound, (max_q, max_len, window, sinks))
     handle = _current_handle(dv)
     wsb = lib().ptq1_attn_chunk_workspace_bytes(batch, rows, max_q, hq, kv.n_kv_heads, d, max_len, window, sinks)
     if ws is None:
@@ -1026,7 +1033,7 @@ def workspace_bytes(kind: str, *shape) -> int:
           "attn_decode_window": "ptq1_attn_decode_window_workspace_bytes",
           "attn_chunk": "ptq1_attn_chunk_workspace_bytes",
           "attn_prompt": "ptq1_attn_prompt_workspace_bytes"}[kind]
-    return int(getattr(lib(), fn)(*shape))
+    return int(getattr(lib(), fn)(*map(_bound, shape)))
 
 
 # -------------------------------------------------------------- profiling ----

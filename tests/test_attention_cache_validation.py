@@ -395,3 +395,32 @@ def test_stream_of_another_device_refused(monkeypatch):
     for call in side_calls().values():
         with pytest.raises(ValueError, match="the stream is on cuda:1"):
             call(stream=streams.side)
+
+
+@pytest.mark.parametrize("far", [1 << 63, (1 << 64) + 1, 1 << 200])
+def test_bounds_past_64_bits(monkeypatch, far):
+    """Windows, first tokens and bounds of any size are as given, not their lowest 64 bits."""
+    real, calls = P.lib(), []
+
+    class Seen:
+        def __getattr__(self, name):
+            if name.endswith("_bytes"):
+                return getattr(real, name)
+            return lambda *a: calls.append(a) or 0
+
+    monkeypatch.setattr(P, "_on_device", lambda t: True)
+    monkeypatch.setattr(P, "_current_handle", lambda device: 0)
+    monkeypatch.setattr(P, "lib", lambda: Seen())
+    c, t, q = kv(), torch.zeros((2, 400), dtype=torch.int32), z(3, 8, 128)
+    most = (1 << 63) - 1
+    P.ptq1_attn_decode_window(q[:2], c, t, i32(1, 2), far, far)
+    P.ptq1_attn_decode_window(q[:2], c, t, i32(1, 2), -far, 0, max_len=far)
+    P.ptq1_attn_decode(q[:2], c, t, i32(1, 2), max_len=far)
+    P.ptq1_attn_chunk(q, c, t, i32(0, 1, 3), i32(1, 2), window=far, sinks=far, max_q=far, max_len=-far)
+    assert calls[0][8:11] == (6400, most, most)
+    assert calls[1][8] == most and calls[1][9] < 0
+    assert calls[2][8] == most
+    assert calls[3][6] == most and calls[3][12] < 0 and calls[3][13:15] == (most, most)
+    for kind, shape in (("attn_decode_window", (1, 8, 2, 128, 100000)), ("attn_chunk", (1, 8, 8, 8, 2, 128, 100000))):
+        need = P.workspace_bytes(kind, *shape, 100000, 100000)
+        assert need > 0 and P.workspace_bytes(kind, *shape, far, far) == need
