@@ -1166,3 +1166,31 @@ def test_attn_chunk_takes_no_longer_over_what_no_query_sees(dtype, hq, hkv, d, p
     assert torch.equal(call(), want)
     taken = time_of(call)
     assert taken < 2 * clean, f"{taken:.1f} us for {clean:.1f}"
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new,lens", [([300, 90], [300, 700]), ([9, 1], [9, 500])])
+def test_chunks_and_whole_prompts_agree_row_by_row(dtype, d, new, lens):
+    """The chunk call and the prompt call on the rows read back: either is off from 64 bits by its own row's bound and half
+    a step, so the two differ by both at most."""
+    g = gen(301)
+    table, pages = tables(g, lens, 64)
+    c = filled_cache(g, pages, 64, 2, d, dtype)
+    q = randn(g, sum(new), 8, d).to(dtype)
+    cu, cu_k = cumulated(new), cumulated(lens)
+    k, v = P.ptq1_kv_read(c, table, cu_k, sum(lens), dtype=dtype)
+    got = P.ptq1_attn_chunk(q, c, table, cu, torch.tensor(lens, dtype=torch.int32, device=DEV), max_q=max(new)).double()
+    prompt = P.ptq1_attn_prompt(q, k, v, cu, cu_k).double()
+    at_q = at_k = 0
+    for m, n in zip(new, lens):
+        for h in range(8):
+            rows, keys = slice(at_q, at_q + m), slice(at_k, at_k + n)
+            qq, kk, vv = q[rows, h].double(), k[keys, h // 4].double(), v[keys, h // 4].double()
+            mask = window_mask(m, n, 0, 0)
+            bounds = [attention_bounds(qq, kk, vv, d ** -0.5, term, mask) for term in
+                      (chunk_term(dtype, dtype, 4 * max(new)), CHUNK_TERM[(dtype, dtype)])]
+            tol = sum(t + half_step(want.abs() + t, dtype) for want, t in bounds)
+            err = (got[rows, h] - prompt[rows, h]).abs()
+            assert bool((err <= tol).all()), f"{(err / tol).max().item():.3f} of the bound"
+        at_q, at_k = at_q + m, at_k + n
