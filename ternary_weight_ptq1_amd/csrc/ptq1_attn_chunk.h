@@ -628,10 +628,10 @@ struct ChunkSoftmax {
         if (__ballot(mt > was + 8.0f) != 0) {
             float mn = fmaxf(was, mt);
             if constexpr (I8) {
-                // whole numbers, of which sums are exact: rounded here alone, a reference
-                // would be another for this step's keys than for the later ones'
-                m = base + ceilf(mn);
-                mn = m - base;
+                // whole numbers, of which sums are exact (below 2^24): rounded here alone,
+                // a reference would be another for this step's keys than for the later ones'
+                mn = ceilf(mn);
+                m = base + mn;
             } else
                 m = mn;
             float f = was == mn ? 1.0f : __builtin_amdgcn_exp2f(was - mn);

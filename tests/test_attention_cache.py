@@ -1194,3 +1194,47 @@ def test_chunks_and_whole_prompts_agree_row_by_row(dtype, d, new, lens):
             err = (got[rows, h] - prompt[rows, h]).abs()
             assert bool((err <= tol).all()), f"{(err / tol).max().item():.3f} of the bound"
         at_q, at_k = at_q + m, at_k + n
+
+
+@pytest.mark.parametrize("qt", [BF16, F16])
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("m", [3, 40])
+@pytest.mark.parametrize("before", [2.0, -1e3, 134.5, 2.0 ** 18 + 6.5, -2.0 ** 18 + 6.5, 9e5])
+@pytest.mark.parametrize("power", [24, 31, 42])
+@pytest.mark.parametrize("twice", [False, True])
+def test_attn_chunk_int8_scores_that_leap(qt, d, m, before, power, twice):
+    """int8 keys whose scores leap within one step from `before` at most to 2^power and more (in units of log2), where
+    one is far ahead of the others (twice: it comes again two steps later).  Rows are that key's value.  Its score, 127
+    times its step, lies in the middle between two fp32 values, and so does what is left of it above (or below) some of
+    the references that the scores before have, 7 less than them."""
+    g = gen(320 + power)
+    run = 128 if m <= 16 else 64
+    n, hkv, page = 4 * run + m, 2, 64
+    steps = torch.rand(n, generator=g, device=DEV).double()
+    steps[:run] = abs(before) / 64 * (0.9 + 0.1 * steps[:run] if before > 0 else 1 + 0.1 * steps[:run])
+    steps[run // 2] = abs(before) / 64
+    steps[run:] = 2.0 ** power / 127 * (1 + 0.5 * steps[run:])
+    first, again = run + 37, 3 * run + 11
+    half = 2.0 ** (power - 24)                       # of the score's last place
+    lead = int(1.875 * 2.0 ** power / 127 / half) // 4 * 4 + (1 if before > 0 else 3)
+    steps[[first, again] if twice else [first]] = half * lead
+    assert 127 * lead % 4 == (3 if before > 0 else 1) and lead < 1 << 24
+    codes = torch.full((n,), 127, device=DEV)
+    codes[:run] = 64 if before > 0 else -64
+    codes[4 * run:], steps[4 * run:] = -127, 2.0 ** power / 64   # the queries' own tokens
+    k = torch.zeros((n, hkv, d), dtype=I8, device=DEV)
+    v = torch.randint(-127, 128, (n, hkv, d), generator=g, device=DEV).to(I8)
+    if twice:
+        v[again] = v[first]
+    k[..., 0] = codes.to(I8)[:, None]
+    c, table = placed(k, v, page, I8, 1.0)
+    at = torch.arange(n, device=DEV)
+    c.k_steps[table[0, at // page].long(), :, at % page] = steps.float()[:, None]
+    q = torch.zeros((m, 2 * hkv, d), device=DEV, dtype=qt)
+    q[..., 0] = 1
+    scale = float(np.float32(math.log(2.0)))         # (log2(e) times it is one in fp32)
+    got = P.ptq1_attn_chunk(q, c, table, cumulated([m]), torch.tensor([n], dtype=torch.int32, device=DEV), scale=scale, max_q=m)
+    want = v[first].double().repeat_interleave(2, 0)
+    # (the others' scores are lower by a fifth: they weigh nothing)
+    tol = chunk_term(qt, I8, 2 * m) * want.abs() + 4 * U * want.abs()
+    assert bool(((got.double() - want).abs() <= tol + half_step(want.abs() + tol, qt)).all())
