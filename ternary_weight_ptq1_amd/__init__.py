@@ -919,8 +919,10 @@ def ptq1_attn_chunk(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, 
     bf16 over an int8 cache; rows may lie apart) are the last of sequence b's seq_lens[b] (int32) tokens, whose pages are
     block_table[b] (int32 [batch, max_pages]).  Causal; window > 0: over the last `window` tokens (the query's own among
     them) and the first `sinks` alone; pages that no query sees are not read.  scale: 1 / sqrt(head_dim) by default;
-    max_q, max_len: bounds on the sequences' queries and tokens (all rows, the table's by default).  ws: optional scratch
-    of at least workspace_bytes("attn_chunk", batch, n_q_rows, max_q, n_q_heads, n_kv_heads, head_dim, max_len, window,
+    max_q, max_len: bounds on the sequences' queries and tokens (all rows, the table's by default); where max_q * n_q_heads
+    / n_kv_heads is at most 32 a kernel for few rows runs, whose weights have 16 bits and more (of many rows' 8 in bf16, 11
+    in fp16), so give max_q where a batch has few queries a sequence.  ws: optional scratch of at least
+    workspace_bytes("attn_chunk", batch, n_q_rows, max_q, n_q_heads, n_kv_heads, head_dim, max_len, window,
     sinks) bytes."""
     kv = _kv(cache)
     dv = kv.device

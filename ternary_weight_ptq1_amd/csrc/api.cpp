@@ -1189,8 +1189,9 @@ ptq1_status check_lengths(int64_t max_pages, int64_t max_len, int32_t page_size)
     return ok();
 }
 
-// Rows and tiles of the chunk attention, with a piece more for each of 512
-// workgroups where tiles are cut.
+// Rows and tiles of the chunk attention.  (Cut tiles add 2 * wanted workgroups of
+// a kv head, 2048 at most of all together, and only 2048 tiles or fewer are cut:
+// no grid that is cut comes near the limit.)
 bool chunk_sizes_ok(int64_t batch, int64_t q_rows, int32_t hq, int32_t hkv)
 {
     if (batch < 0 || batch > kMaxRows32 || hkv < 1 || hkv > 1024 || hq < 1 || hq > kMaxHeads) return false;

@@ -31,8 +31,8 @@
 //
 // Measured (matrix work differs by up to 10% from card to card; these are the
 // faster ones).  4096 tokens behind 28000 (40 heads over 8 of 128, bf16): 1480 to
-// 1570 us, 990 to 1050 TFLOP/s; matrix cores 51% busy, vector units 54%.  8 x 256 to
-// 512 tokens behind 6000 to 12000 over int8: 755 us, 800 TFLOP/s, the vector units
+// 1580 us, 980 to 1050 TFLOP/s; matrix cores 51% busy, vector units 54%.  8 x 256 to
+// 512 tokens behind 6000 to 12000 over int8: 766 to 780 us, 780 TFLOP/s, the vector units
 // (56%; the codes of a step cost 160 of 630 instructions of a wave) and LDS (stores
 // of codes: on the layout of the 16-bit tiles they met two by two, 3% more).  4 x 350
 // to 700 tokens behind 2000 to 4000, 256-wide heads, fp16: 233 us, 650 TFLOP/s, eight
@@ -169,7 +169,7 @@ struct ChunkStaging {
         if (wave < 2)
             step = (wave == 0 ? ksp : vsp)[static_cast<uint64_t>(page_cells) * static_cast<uint32_t>(p.of(lane >> 4)) + ((n0 + lane) & mask)];
     }
-    // ... and as fp16 into LDS
+    // ... and as 16-bit operands into LDS: K's in the queries' type, V's in fp16
     __device__ __forceinline__ void store(int n0, const Buffer &to)
     {
         constexpr int L = D / 16;
@@ -713,7 +713,9 @@ ChunkPlan chunk_plan(int64_t batch, int64_t q_rows, int64_t max_q, int32_t hq, i
     p.numbers = p.tiles;
     p.few = rows <= kFewRows;
     p.slot_rows = static_cast<int32_t>(rows < kChunkRows ? rows : kChunkRows);
-    const int64_t slots = d == 256 ? 256 : 512;  // workgroups that the GPU holds
+    // workgroups that the GPU holds (of 64-wide heads over 16-bit caches it holds
+    // 768, three a CU: their last rounds are judged by a smaller GPU than it is)
+    const int64_t slots = d == 256 ? 256 : 512;
     p.wanted = static_cast<int32_t>(slots / hkv > 1 ? slots / hkv : 1);
     const int most = steps_bound(static_cast<int>(max_len), static_cast<int>(window), static_cast<int>(sinks), static_cast<int>(group));
     // pieces: of all tiles wanted + tiles at most, or twice wanted in the place of

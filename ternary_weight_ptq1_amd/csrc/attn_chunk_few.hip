@@ -23,6 +23,11 @@ constexpr int kFewWaves = 4;
 // sequences of 4000 to 8000 tokens with 4 to 8 (32 heads over 8): 157 us, and 13.5
 // for the join, of 810 MB (5.2 TB/s); the tiles took 160.  Measured and not kept:
 // eight waves (17.7 against 15.8 us behind 700 tokens, both launches).
+//
+// 256-wide heads hold one wave a SIMD and have 11 to 21 registers spilled, some of
+// them read back in every step: 32 sequences of 4000 to 8000 tokens with 3 to 5
+// (24 heads over 4) take 225 us for 800 MB (3.6 TB/s), over int8 160 for 407.
+// 128-wide heads over int8, 32 sequences as above: 143 us for 419 MB (2.9 TB/s).
 template <typename C, typename QT, int D>
 __global__ void __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) k_attn_chunk_few(ChunkArgs a)
 {

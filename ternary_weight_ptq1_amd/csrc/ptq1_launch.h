@@ -216,7 +216,7 @@ struct ChunkPlan {
 };
 ChunkPlan chunk_plan(int64_t batch, int64_t q_rows, int64_t max_q, int32_t hq, int32_t hkv, int32_t d, int64_t max_len,
                      int64_t window, int64_t sinks);
-// window: 2^22 + 1 where there is none
+// window: max_len + 1 where there is none
 hipError_t launch_attn_chunk(const ChunkPlan &p, const void *q, int64_t qs, int q_type, const int32_t *cu, int64_t batch,
                              int64_t q_rows, int64_t max_q, int32_t hq, const ptq1_kv_cache &c, const int32_t *table,
                              int64_t max_pages, const int32_t *lens, int64_t max_len, int32_t window, int32_t sinks,
